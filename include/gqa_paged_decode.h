@@ -331,7 +331,8 @@ int gqa_sparse_paged_decode(const void* q, const void* k_cache, const void* v_ca
  * its copies in flight and returned early, so that call's outputs are not
  * valid), bit 4 = bad page id, bit 8 = bad kv_indptr, bit 16 = an arrival or
  * range counter could not be claimed, bit 32 = an in-kernel merge gave up
- * waiting for a sequence's pieces (that sequence's outputs are not valid).
+ * waiting for a sequence's pieces (that sequence's outputs are not valid),
+ * bit 64 = a prompt pass's sequences hold more tokens than its bound.
  * 0 means no error.
  */
 int gqa_paged_decode_device_error(int* flags);
@@ -395,6 +396,162 @@ int gqa_paged_decode_test_wait_limit_ns(uint64_t ns);
 int gqa_paged_decode_noalloc(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_indptr,
                              const int32_t* kv_indices, float sm_scale, void* out, float* lse, int batch,
                              struct CUstream_st* stream);
+
+/*
+ * ---- Operators around the decode: what a serving step runs before and after it.
+ *
+ * Rotary positions. For a token at position p (any int32; negative turns
+ * back) and pair i < rot_dim / 2 of the window [rot_offset, rot_offset +
+ * rot_dim) of a head, with a = p * inv_freq[i] radians:
+ *   y1 = scale * (x1 cos a - x2 sin a),  y2 = scale * (x2 cos a + x1 sin a),
+ * (x1, x2) being elements (i, i + rot_dim / 2) of the window (GQA_ROPE_HALF)
+ * or (2 i, 2 i + 1) (GQA_ROPE_INTERLEAVED). The angle is formed in 64-bit
+ * integer arithmetic, so it does not lose precision at far positions; the
+ * rotation is in fp32 and rounded once. positions: [num_tokens] int32;
+ * inv_freq: [rot_dim / 2] double, both in device memory.
+ */
+#define GQA_ROPE_HALF 0
+#define GQA_ROPE_INTERLEAVED 1
+#define GQA_TYPE_BF16 0
+#define GQA_TYPE_F16 1
+#define GQA_TYPE_F32 2
+#define GQA_CACHE_BF16 0
+#define GQA_CACHE_FP8 1
+
+#define GQA_ROPE_SCALING_NONE 0     /* base^(-2 i / rot_dim) */
+#define GQA_ROPE_SCALING_LINEAR 1   /* all of them divided by factor (positions interpolated) */
+#define GQA_ROPE_SCALING_BASE 2     /* base grown to base * factor^(rot_dim / (rot_dim - 2)) */
+#define GQA_ROPE_SCALING_BY_PARTS 3 /* pairs that make at least fast_turns turns over original_positions are kept,
+                                       those below slow_turns are divided by factor, a linear ramp between */
+
+/*
+ * Frequencies on the host (no GPU needed): fills inv_freq[rot_dim / 2] (host
+ * memory) in radians a position, and *scale (may be NULL) with the factor that
+ * goes with them: 0.1 ln(factor) + 1 by parts, else 1. factor >= 1 (unused
+ * without scaling); original_positions, slow_turns < fast_turns are used by
+ * parts only (customary: 1 and 32).
+ */
+int gqa_rope_inv_freq(int rot_dim, double base, int scaling, double factor, double original_positions,
+                      double slow_turns, double fast_turns, double* inv_freq, float* scale);
+
+/*
+ * Rotates x [num_tokens][num_heads][head_dim] (GQA_TYPE_*; token and head
+ * strides in elements, a head's values contiguous) into out, laid out by its
+ * own strides; elements outside the window are copied. out may be x itself
+ * with the same strides, and must not overlap it otherwise; its rows must not
+ * overlap one another. inverse != 0 turns by -a: it undoes a rotation (with
+ * scale 1 / scale), and is the gradient of one (with the same scale).
+ * num_heads and head_dim up to 1024. Addresses need the type's alignment only;
+ * 16-byte aligned rows and windows are fastest. num_tokens == 0 returns 0
+ * without launching.
+ */
+int gqa_rope(const void* x, const int32_t* positions, const double* inv_freq, float scale, void* out, int num_tokens,
+             int num_heads, int head_dim, int rot_offset, int rot_dim, int layout, int inverse, int dtype,
+             int64_t x_token_stride, int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride,
+             struct CUstream_st* stream);
+
+/*
+ * One pass over a step's new tokens before the decode: rotates q [n][32][128]
+ * into q_out (contiguous) and k_new [n][4][128], and stores the K and V rows in
+ * pages slots[r] of the caches as gqa_paged_kv_append does (slots outside
+ * [0, num_pages) store nothing; their query row is still written). All bf16;
+ * q_stride, k_stride and v_stride are token strides in elements (multiples of
+ * 8, heads contiguous), so q, k_new and v_new may be views of one fused row.
+ * inv_freq NULL: no rotation (positions, scale, rot_offset, rot_dim and layout
+ * are not read). q and q_out may both be NULL: keys and values only. q_out may
+ * be q when q is contiguous. cache_format GQA_CACHE_BF16: caches as in
+ * gqa_paged_kv_append; GQA_CACHE_FP8: rows of 528 bytes as in
+ * gqa_paged_decode_fp8, a head's scale being the smallest power of two that
+ * keeps its largest finite value within 448 (1 for a head of zeros, at least
+ * 2^-126), its codes e4m3(value / scale), nearest even, of the fp32 values;
+ * infinities become +-448 * scale and NaN the NaN code. Pointers 16-byte
+ * aligned. Valid slots should be distinct. Asynchronous; num_tokens == 0
+ * returns 0 without launching.
+ */
+int gqa_rope_kv_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                       const int32_t* slots, const double* inv_freq, float scale, int rot_offset, int rot_dim,
+                       int layout, void* q_out, void* k_cache, void* v_cache, int cache_format, int num_tokens,
+                       int num_pages, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       struct CUstream_st* stream);
+
+/* gqa_paged_kv_append into an FP8 cache (the quantisation of gqa_rope_kv_append, no rotation). */
+int gqa_paged_kv_append_fp8(const void* k_new, const void* v_new, const int32_t* slots, void* k_cache, void* v_cache,
+                            int num_tokens, int num_pages, struct CUstream_st* stream);
+
+/*
+ * Reads an FP8 cache back: for r < num_tokens, row r of k_out and v_out
+ * ([num_tokens][4][128] bf16) is code * scale of page indices[r], rounded to
+ * bf16; a page outside [0, num_pages) gives zeros. Pages may repeat. With
+ * indices = kv_indices this expands a whole batch in page-table order.
+ */
+int gqa_paged_kv_read_fp8(const void* k_cache, const void* v_cache, const int32_t* indices, void* k_out, void* v_out,
+                          int num_tokens, int num_pages, struct CUstream_st* stream);
+
+/*
+ * Latent-cache append: row slots[r] of kv_cache ([num_slots][576] bf16, that
+ * is num_blocks * page_size rows) becomes latent[r] (512 values) followed by
+ * k_rope[r] (64 values), turned by positions[r] unless inv_freq ([32]) is
+ * NULL. Token strides in elements (latent: a multiple of 8, 16-byte aligned;
+ * k_rope: even, 4-byte aligned). Slots outside [0, num_slots) store nothing.
+ */
+int gqa_mla_kv_append(const void* latent, const void* k_rope, const int32_t* positions, const int32_t* slots,
+                      const double* inv_freq, float scale, int layout, void* kv_cache, int num_tokens, int num_slots,
+                      int64_t latent_stride, int64_t rope_stride, struct CUstream_st* stream);
+
+/*
+ * Latent attention, absorbed form: the projections on either side of
+ * gqa_mla_decode. w_kv [num_heads][256][512] bf16 is the up-projection of the
+ * latent row c: head h's key is w_kv[h][0:128] c and its value w_kv[h][128:256] c.
+ *
+ * gqa_mla_absorb_q: q [n][num_heads][192] (128 values that meet the expanded
+ * key, then 64 rotary ones; token and head strides in elements, multiples of
+ * 8) to q_out [n][num_heads][576] (contiguous): q[0:128] w_kv[h][0:128], then
+ * the rotary values, turned by positions[n] unless inv_freq ([32]) is NULL.
+ *
+ * gqa_mla_expand_out: o_latent [n][num_heads][512] (the decode's output) to
+ * out [n][num_heads][128] = w_kv[h][128:256] o_latent.
+ *
+ * bf16, fp32 accumulation, 16-byte aligned; num_heads <= 1024, n <= 2^20.
+ */
+int gqa_mla_absorb_q(const void* q, const void* w_kv, const int32_t* positions, const double* inv_freq, float scale,
+                     int layout, void* q_out, int num_tokens, int num_heads, int64_t q_token_stride,
+                     int64_t q_head_stride, struct CUstream_st* stream);
+int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int num_tokens, int num_heads,
+                       struct CUstream_st* stream);
+
+/*
+ * Latent attention, expanded form (prompts and prompt chunks): ragged queries
+ * over the paged latent cache, with per-head keys and values expanded from it.
+ * Sequence b owns query rows [cu_seqlens_q[b], cu_seqlens_q[b + 1]) of q
+ * ([total_q][num_heads][192] bf16, rotary part already turned; strides in
+ * elements, multiples of 8) and the n = cache_seqlens[b] cached tokens its
+ * block table lists (as in gqa_mla_decode; the new tokens are among them). With
+ * k_t = [w_kv[h][0:128] c_t ; rotary key of t] and v_t = w_kv[h][128:256] c_t,
+ *   out[i][h] = sum_t softmax(softmax_scale * q[i][h] . k_t) v_t     (bf16)
+ *   lse[h][i] = log sum_t exp(...)   (natural log, fp32, [num_heads][total_q]; may be NULL)
+ * over t < n and, if causal, t <= n - nq + (i - cu_seqlens_q[b]), nq being the
+ * sequence's query count. A row that sees no token gives out = 0 and lse =
+ * -inf. A token whose block lies outside [0, num_blocks) is left out; lengths
+ * are clamped as in gqa_mla_decode. A token whose latent row is not all finite
+ * makes the rows that see it NaN, and no others. Rows past cu_seqlens_q[batch] are left as
+ * they were. The expanded keys and values are fp16 (scaled by a power of two
+ * where the values need it); everything else accumulates in fp32. lse carries
+ * that rounding of the keys: about 2^-12 of a score's size.
+ *
+ * max_kv_tokens bounds the sum of the lengths on the host (it sizes the
+ * workspace); sequences past it see no token and set bit 64 of the device error
+ * word. A cu_seqlens_q that decreases or leaves [0, total_q] sets bit 8.
+ * workspace: gqa_mla_prefill_ws_size(batch, num_heads, max_kv_tokens) bytes of
+ * device memory (0: arguments out of range), 256-byte aligned, one per call in
+ * flight; its contents need no initialisation. Asynchronous; batch == 0 or
+ * total_q == 0 returns 0 without launching.
+ */
+size_t gqa_mla_prefill_ws_size(int batch, int num_heads, int64_t max_kv_tokens);
+int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const int32_t* block_table,
+                    const int32_t* cache_seqlens, const int32_t* cu_seqlens_q, float softmax_scale, int causal,
+                    void* out, float* lse, int batch, int total_q, int num_heads, int page_size, int num_blocks,
+                    int page_table_width, int64_t max_kv_tokens, int64_t q_token_stride, int64_t q_head_stride,
+                    void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

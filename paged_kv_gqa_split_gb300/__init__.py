@@ -9,7 +9,18 @@ is the selected-token variant over a block table of any page size,
 ``run_fp8`` reads an FP8 (e4m3, per-128 fp32 scale) cache, ``mla_run`` is
 the dense MLA decode over one 576-value latent KV head, and
 ``kv_append`` stores new tokens' K/V rows into the page pool.
+
+What a serving step runs around them (``serving``): ``rope_inv_freq`` and
+``rope`` (rotary positions), ``rope_kv_append`` (Q and K turned, K and V stored
+in a bf16 or FP8 cache), ``kv_append_fp8``, ``kv_read_fp8`` and
+``mla_kv_append`` (the caches' write and read), and latent attention's
+``mla_absorb_q``, ``mla_expand_out``, ``mla_absorbed_run`` (new tokens) and
+``mla_prefill`` (prompts).
 """
 from ._lib import GqaError, kv_append, mla_run, run, run_checked, run_fp8, sparse_run  # noqa: F401
+from .serving import (kv_append_fp8, kv_read_fp8, mla_absorb_q, mla_absorbed_run, mla_expand_out,  # noqa: F401
+                      mla_kv_append, mla_prefill, rope, rope_inv_freq, rope_kv_append)
 
-__all__ = ["GqaError", "kv_append", "mla_run", "run", "run_checked", "run_fp8", "sparse_run"]
+__all__ = ["GqaError", "kv_append", "kv_append_fp8", "kv_read_fp8", "mla_absorb_q", "mla_absorbed_run",
+           "mla_expand_out", "mla_kv_append", "mla_prefill", "mla_run", "rope", "rope_inv_freq", "rope_kv_append", "run",
+           "run_checked", "run_fp8", "sparse_run"]

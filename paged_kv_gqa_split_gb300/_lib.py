@@ -29,6 +29,7 @@ GQA_ERR_UNSUPPORTED_DEVICE = -4
 NUM_QO_HEADS, NUM_KV_HEADS, HEAD_DIM, PAGE_SIZE = 32, 4, 128, 1
 
 _vp = ctypes.c_void_p
+_d = ctypes.c_double
 _SIGNATURES = {
     "gqa_paged_decode": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, ctypes.c_int, _vp]),
     "gqa_paged_decode_ws_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64]),
@@ -52,6 +53,21 @@ _SIGNATURES = {
     "gqa_paged_decode_last_launch_count": (ctypes.c_int, []),
     "gqa_paged_decode_test_fail_allocs": (ctypes.c_int, [ctypes.c_int]),
     "gqa_paged_decode_test_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
+    "gqa_rope_inv_freq": (ctypes.c_int, [ctypes.c_int, _d, ctypes.c_int, _d, _d, _d, _d, _vp,
+                                         ctypes.POINTER(ctypes.c_float)]),
+    "gqa_rope": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_float, _vp] + [ctypes.c_int] * 8 + [ctypes.c_int64] * 4 + [_vp]),
+    "gqa_rope_kv_append": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float] + [ctypes.c_int] * 3 + [_vp] * 3 +
+                           [ctypes.c_int] * 3 + [ctypes.c_int64] * 3 + [_vp]),
+    "gqa_paged_kv_append_fp8": (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 2 + [_vp]),
+    "gqa_paged_kv_read_fp8": (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 2 + [_vp]),
+    "gqa_mla_kv_append": (ctypes.c_int, [_vp] * 5 + [ctypes.c_float, ctypes.c_int, _vp] + [ctypes.c_int] * 2 +
+                          [ctypes.c_int64] * 2 + [_vp]),
+    "gqa_mla_absorb_q": (ctypes.c_int, [_vp] * 4 + [ctypes.c_float, ctypes.c_int, _vp] + [ctypes.c_int] * 2 +
+                         [ctypes.c_int64] * 2 + [_vp]),
+    "gqa_mla_expand_out": (ctypes.c_int, [_vp] * 3 + [ctypes.c_int] * 2 + [_vp]),
+    "gqa_mla_prefill_ws_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64]),
+    "gqa_mla_prefill": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float, ctypes.c_int, _vp, _vp] + [ctypes.c_int] * 6 +
+                        [ctypes.c_int64] * 3 + [_vp, ctypes.c_size_t, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None

@@ -19,6 +19,7 @@ constexpr int kErrBadPage = 4;       // a kv_indices entry outside [0, num_pages
 constexpr int kErrBadIndptr = 8;     // kv_indptr not starting at 0 / decreasing
 constexpr int kErrTicket = 16;       // a split sequence's arrival ticket did not settle
 constexpr int kErrMergeWait = 32;    // an in-kernel merge waited too long for a sequence's pieces
+constexpr int kErrKvBound = 64;      // a prompt pass's sequences hold more tokens than the caller's bound
 
 struct DecodeParams {
   const void* q;
@@ -205,8 +206,105 @@ cudaError_t launch_validate(const int* indptr, const int* indices, int batch, in
                             cudaStream_t stream);
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, const int* slots, void* k_cache, void* v_cache,
                              int n, int num_pages, int sm_count, cudaStream_t stream);
+// ------------------------------------------- serving operators around decode
+// Element types of gqa_rope (GQA_TYPE_* of the public header).
+enum : int { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };
+
+struct RopeParams {  // gqa_rope.cu; strides in elements
+  const void* x;
+  void* out;
+  const int* positions;    // [num_tokens]
+  const double* inv_freq;  // [rot_dim / 2]
+  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  float scale;
+  int num_tokens, num_heads, head_dim, rot_offset, rot_dim, layout, inverse;
+  int copy_rest;           // copy the elements outside the window (0: in place)
+  int tokens_per_block;
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, int sm_count, cudaStream_t stream);
+
+struct AppendParams {  // gqa_rope_append.cu; token strides in elements
+  const void* q;  // [n][32][128] or NULL
+  const void* k;  // [n][4][128]
+  const void* v;
+  const int* positions;
+  const int* slots;
+  const double* inv_freq;  // NULL: no rotation
+  void* q_out;             // [n][32][128] contiguous
+  void* k_cache;
+  void* v_cache;
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  int num_tokens, num_pages, rot_offset, rot_dim, layout, fp8;
+  int splits;  // warps a token
+};
+cudaError_t launch_rope_append(AppendParams p, int sm_count, cudaStream_t stream);
+cudaError_t launch_kv_read_fp8(const void* k_cache, const void* v_cache, const int* indices, void* k_out, void* v_out,
+                               int n, int num_pages, int sm_count, cudaStream_t stream);
+
+struct MlaAppendParams {  // gqa_rope_append.cu
+  const void* latent;  // [n][512]
+  const void* k_rope;  // [n][64]
+  const int* positions;
+  const int* slots;
+  const double* inv_freq;  // [32] or NULL
+  void* kv_cache;          // [num_slots][576]
+  int64_t latent_stride, rope_stride;
+  float scale;
+  int num_tokens, num_slots, layout;
+};
+cudaError_t launch_mla_append(const MlaAppendParams& p, int sm_count, cudaStream_t stream);
+
+struct MlaProjParams {  // gqa_mla_proj.cu
+  const void* x;  // absorb_q: q [n][h][192]; expand_out: o_lat [n][h][512]
+  const void* w;  // [h][256][512]
+  const int* positions;
+  const double* inv_freq;  // [32] or NULL (absorb_q)
+  void* out;               // [n][h][out_width] contiguous
+  int64_t x_token_stride, x_head_stride;
+  float scale;
+  int num_tokens, num_heads, out_width, layout;
+};
+cudaError_t launch_mla_absorb_q(const MlaProjParams& p, cudaStream_t stream);
+cudaError_t launch_mla_expand_out(const MlaProjParams& p, cudaStream_t stream);
+
+// Latent attention's prompt pass (gqa_mla_prefill.cu).
+struct MlaPrefillParams {
+  const void* q;             // [total_q][h][192]
+  const void* w;             // [h][256][512]
+  const void* kv;            // [num_blocks * page_size][576]
+  const int* block_table;    // [batch][width]
+  const int* cache_seqlens;  // [batch]
+  const int* cu_q;           // [batch + 1]
+  void* out;                 // [total_q][h][128]
+  float* lse;                // [h][total_q] or NULL
+  int64_t q_token_stride, q_head_stride;
+  float scale_log2;
+  int batch, total_q, num_heads, page_size, num_blocks, width, causal;
+  int cap;        // packed key rows the workspace holds, a multiple of 128
+  int heads_per_pass;
+  // workspace
+  int* kv_len;    // [batch] keys of each sequence that are read
+  int* kv_start;  // [batch + 1] first packed row (multiples of 128)
+  int* q_start;   // [batch][2] first query row and query count, cut to [0, total_q)
+  int* qt_start;  // [batch + 1] first query tile
+  unsigned* amax;      // [4] largest finite |value| bits: latent, rotary key, key weights, value weights
+  unsigned* valid;     // [cap / 32] packed rows that hold a token of the pool
+  unsigned* bad;       // [cap / 32] packed rows whose latent is not all finite
+  void* lat;           // [cap][512] bf16
+  void* kr;            // [cap][64] rotary keys: bf16 from the gather, fp16 (scaled) after the expansion
+  void* kn;            // [heads_per_pass][cap][128] fp16 keys (scaled)
+  void* vv;            // [heads_per_pass][cap][128] fp16 values (scaled)
+  int* err;
+  int head0, heads;    // heads of this pass
+};
+// Bytes of the workspace; with base != NULL also points the params' fields into it.
+size_t mla_prefill_workspace(MlaPrefillParams* p, char* base);
+cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream);
+
 cudaError_t read_and_clear_device_error(int* out);
 cudaError_t device_error_word(int** ptr);  // device address of the error word (current device)
+int current_device_sms(int* sm_count);      // GQA_OK and the SM count when the current device is supported
 
 // Raises a kernel's dynamic shared-memory limit to `bytes` once per device
 // (`done` is the kernel's own flag table, zero-initialised static storage).

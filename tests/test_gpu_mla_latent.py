@@ -1,0 +1,351 @@
+"""GPU parity of latent attention's projections (absorbed form) and prompt pass (expanded form)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.serving as sv
+import paged_kv_gqa_split_gb300 as pkg
+from paged_kv_gqa_split_gb300 import _lib
+from paged_kv_gqa_split_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+U = 2.0 ** -23  # a step of the fp32 accumulation (rounded or cut)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library(cuda_device):
+    build()
+    _lib.load()
+
+
+def weights(h, seed, std=512 ** -0.5):
+    return (torch.randn(h, 256, 512, generator=torch.Generator().manual_seed(seed)) * std).to(BF)
+
+
+# ------------------------------------------------------------------- projections
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 33, 63, 64, 65, 130, 300])
+@pytest.mark.parametrize("h", [1, 3, 16])
+def test_projections(n, h):
+    g = torch.Generator().manual_seed(n * 100 + h)
+    w = weights(h, n)
+    q, o = torch.randn(n, h, 192, generator=g).to(BF), torch.randn(n, h, 512, generator=g).to(BF)
+    got = pkg.mla_absorb_q(q.cuda(), w.cuda())
+    want = sv.mla_absorb_q_oracle(q, w)
+    size = np.einsum("nhd,hdl->nhl", np.abs(sv.f64(q))[..., :128], np.abs(sv.f64(w))[:, :128])
+    d = 128 * U * size
+    assert np.all(np.abs(sv.f64(got)[..., :512] - want) <= 2.0 ** -8 * (np.abs(want) + d) + d)
+    assert torch.equal(got[..., 512:].cpu(), q[..., 128:])
+    got = pkg.mla_expand_out(o.cuda(), w.cuda())
+    want = sv.mla_expand_out_oracle(o, w)
+    d = 512 * U * np.einsum("nhl,hdl->nhd", np.abs(sv.f64(o)), np.abs(sv.f64(w))[:, 128:])
+    assert np.all(np.abs(sv.f64(got) - want) <= 2.0 ** -8 * (np.abs(want) + d) + d)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n", [1, 20, 70])
+def test_absorb_rotates_and_takes_strides(layout, n):
+    g = torch.Generator().manual_seed(n)
+    h = 5
+    w, pos = weights(h, 3).cuda(), torch.randint(0, 1 << 20, (n,), generator=g, dtype=torch.int32).cuda()
+    freq = pkg.rope_inv_freq(64)[0]
+    q = torch.randn(n, h + 2, 200, generator=g).to(BF).cuda()[:, 1:1 + h, :192]
+    got = pkg.mla_absorb_q(q, w, pos, freq, 1.1, layout)
+    assert torch.equal(got[..., :512], pkg.mla_absorb_q(q.contiguous(), w)[..., :512])
+    want = sv.rope_oracle(q[..., 128:], pos, freq, 1.1, 0, layout)
+    d = 2.0 ** -21 * 1.1 * sv.rope_pair_size(q[..., 128:], 64, 0, layout)
+    assert np.all(np.abs(sv.f64(got[..., 512:]) - want) <= 2.0 ** -8 * (np.abs(want) + d) + d)
+    head_major = q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(pkg.mla_absorb_q(head_major, w, pos, freq, 1.1, layout), got)
+    buf = torch.zeros_like(got)
+    assert pkg.mla_absorb_q(q, w, pos, freq, 1.1, layout, out=buf) is buf and torch.equal(buf, got)
+
+
+def test_projections_not_finite_and_empty():
+    n, h = 18, 2
+    w = weights(h, 4).cuda()
+    q = torch.randn(n, h, 192, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    clean = pkg.mla_absorb_q(q, w)
+    q[4, 1, 3] = float("nan")
+    got = pkg.mla_absorb_q(q, w)
+    touched = torch.zeros(n, h, dtype=torch.bool)
+    touched[4, 1] = True
+    assert torch.equal(got[~touched], clean[~touched]) and torch.isnan(got[4, 1, :512]).all()
+    assert pkg.mla_absorb_q(q[:0], w).shape == (0, h, 576)
+    assert pkg.mla_expand_out(torch.zeros(0, h, 512, dtype=BF, device="cuda"), w).shape == (0, h, 128)
+
+
+# -------------------------------------------------------------------- prompt pass
+def case(lens, h, page, seed, std=1.0, extra=3, bad_blocks=0, width=None, w_std=512 ** -0.5):
+    """Paged latent rows, every slot that no sequence owns being NaN."""
+    g = torch.Generator().manual_seed(seed)
+    width = width or max(1, max(-(-n // page) for _, n in lens))
+    used = sum(-(-min(n, width * page) // page) for _, n in lens)
+    blocks = used + extra
+    cache = torch.full((blocks, page, 1, 576), float("nan"))
+    table = torch.full((len(lens), width), -7, dtype=torch.int32)
+    ids, at = torch.randperm(blocks, generator=g), 0
+    for b, (_, n) in enumerate(lens):
+        k = -(-min(n, width * page) // page)
+        table[b, :k] = ids[at:at + k].to(torch.int32)
+        for j in range(k):
+            fill = min(page, n - j * page)
+            cache[table[b, j], :fill, 0] = torch.randn(fill, 576, generator=g) * std
+        at += k
+    for i in range(bad_blocks):  # entries outside the pool: their tokens are left out
+        b = i % len(lens)
+        if lens[b][1]:
+            table[b, (3 * i) % max(1, -(-min(lens[b][1], width * page) // page))] = [blocks, -1, 2 ** 31 - 1][i % 3]
+    cu = [0]
+    for nq, _ in lens:
+        cu.append(cu[-1] + nq)
+    q = torch.randn(cu[-1], h, 192, generator=g) * std
+    return dict(q=q.to(BF), w_kv=weights(h, seed, w_std), kv_cache=cache.to(BF), block_table=table,
+                cache_seqlens=torch.tensor([n for _, n in lens], dtype=torch.int32),
+                cu_seqlens_q=torch.tensor(cu, dtype=torch.int32))
+
+
+def on_gpu(c):
+    return {k: v.cuda() for k, v in c.items()}
+
+
+def check(out, lse, c, scale, causal):
+    o, l, ob, lb = sv.mla_prefill_oracle(c["q"], c["w_kv"], c["kv_cache"], c["block_table"], c["cache_seqlens"],
+                                         c["cu_seqlens_q"], scale, causal)
+    done = ~np.isnan(l[0])
+    got, gl = sv.f64(out), sv.f64(lse)
+    err = np.abs(got - o)[done] - ob[done]
+    assert np.all(err <= 0), f"out {err.max()} over its bound"
+    empty = np.isneginf(l)
+    assert np.array_equal(np.isneginf(gl)[:, done], empty[:, done])
+    assert np.all(got.transpose(1, 0, 2)[empty] == 0)
+    fin = np.isfinite(l)
+    err = np.abs(gl[fin] - l[fin]) - lb[fin]
+    assert np.all(err <= 0), f"lse {err.max()} over its bound"
+
+
+RAGGED = [(130, 130), (1, 1), (0, 0), (47, 300), (0, 50), (129, 128 + 129), (2, 700)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("h,page", [(1, 1), (3, 64), (2, 7), (16, 16)])
+def test_prefill_ragged(h, page, causal):
+    lens = RAGGED if h < 16 else RAGGED[:4]
+    c = case(lens, h, page, 10 * h + page)
+    g = on_gpu(c)
+    out, lse = pkg.mla_prefill(**g, causal=causal)
+    check(out, lse, c, 192 ** -0.5, causal)
+    tight = sum(n for _, n in lens)
+    out2, lse2 = pkg.mla_prefill(**g, causal=causal, max_kv_tokens=tight)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert pkg.mla_prefill(**g, causal=causal, with_lse=False)[1] is None
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 385, 640])
+def test_prefill_lengths(n):
+    for lens in ([(n, n)], [(1, n)], [(n, n + 129)]):
+        c = case(lens, 2, 16, n)
+        out, lse = pkg.mla_prefill(**on_gpu(c))
+        check(out, lse, c, 192 ** -0.5, True)
+
+
+def test_prefill_rows_that_see_nothing():
+    """More queries than cached tokens (their first rows see none), lengths of 0, blocks outside the pool."""
+    c = case([(70, 3), (5, 0), (40, 40), (300, 200)], 3, 8, 5, bad_blocks=5)
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+    c["block_table"][2] = -1
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+    assert torch.all(torch.isneginf(lse[:, 75:115]))
+
+
+def test_prefill_lengths_past_the_table_and_negative():
+    c = case([(20, 100), (9, 30)], 2, 16, 8, width=4)  # 64 tokens of room
+    c["cache_seqlens"][1] = -5
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+
+
+def test_prefill_rows_behind_the_last_sequence_stay():
+    c = case([(30, 30), (10, 90)], 2, 16, 9)
+    g = on_gpu(c)
+    g["q"] = torch.cat([g["q"], torch.full((25, 2, 192), float("nan"), dtype=BF, device="cuda")])
+    out = torch.full((65, 2, 128), 5.0, dtype=BF, device="cuda")
+    lse = torch.full((2, 65), 5.0, device="cuda")
+    pkg.mla_prefill(**g, out=out, lse=lse)
+    assert torch.all(out[40:] == 5.0) and torch.all(lse[:, 40:] == 5.0)
+    check(out[:40], lse[:, :40], c, 192 ** -0.5, True)
+
+
+@pytest.mark.parametrize("std,w_std,scale", [(64.0, 1.0, 1e-5), (2.0 ** -30, 2.0 ** -20, 2.0 ** 70), (2.0 ** 40, 2.0 ** 30, 2.0 ** -120)])
+def test_prefill_sizes_of_values(std, w_std, scale):
+    """Values past fp16's range either way: the bounds scale with the values (powers of two change nothing)."""
+    c = case([(40, 90)], 2, 16, 12, std=std, w_std=w_std)
+    out, lse = pkg.mla_prefill(**on_gpu(c), softmax_scale=scale)
+    if std == 64.0:
+        check(out, lse, c, scale, True)
+        return
+    # bring the same numbers back to ordinary size by powers of two: the outputs have to agree to their roundings
+    d = dict(c, q=c["q"] / std, kv_cache=c["kv_cache"] / std, w_kv=(c["w_kv"].float() / w_std * 2.0 ** -5).to(BF))
+    rows = torch.arange(576) >= 512
+    k = std * w_std * 32  # expanded keys are this much larger than d's, rotary ones std: keep only the former
+    c["kv_cache"][..., rows] = 0
+    d["kv_cache"][..., rows] = 0
+    out, lse = pkg.mla_prefill(**on_gpu(c), softmax_scale=scale)
+    o2, l2 = pkg.mla_prefill(**on_gpu(d), softmax_scale=scale * std * k)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert torch.equal((out.double() / k).to(BF), o2.double().to(BF))
+    assert torch.allclose(lse, l2, rtol=0, atol=1e-5)
+
+
+def test_prefill_large_scores_and_not_finite_values():
+    c = case([(50, 50), (40, 260)], 2, 16, 13, std=6.0)  # scores of many hundreds: one weight takes it all
+    g = on_gpu(c)
+    out, lse = pkg.mla_prefill(**g, softmax_scale=1.0)
+    check(out, lse, c, 1.0, True)
+    clean = out.clone()
+    # a token of sequence 1 that is not finite reaches that sequence's rows that see it, and no others
+    g["kv_cache"][g["block_table"][1, 15].long(), 3] = float("inf")
+    out, _ = pkg.mla_prefill(**g, softmax_scale=1.0)
+    sees = torch.arange(90) >= 50 + (15 * 16 + 3 - 220)
+    assert torch.equal(out[~sees], clean[~sees]) and torch.isnan(out[sees]).all()
+    q = g["q"].clone()
+    q[7, 1, 100] = float("nan")
+    g = on_gpu(c)
+    g["q"] = q
+    out, lse = pkg.mla_prefill(**g, softmax_scale=1.0)
+    hit = torch.zeros(90, 2, dtype=torch.bool)
+    hit[7, 1] = True
+    assert torch.equal(out[~hit], clean[~hit]) and torch.isnan(out[7, 1]).all() and torch.isnan(lse[1, 7])
+
+
+def test_prefill_strides():
+    c = case([(90, 150), (33, 33)], 3, 16, 14)
+    g = on_gpu(c)
+    want = pkg.mla_prefill(**g)[0]
+    wide = torch.zeros(123, 5, 208, dtype=BF, device="cuda")
+    wide[:, 1:4, 8:200] = g["q"]
+    g["q"] = wide[:, 1:4, 8:200]
+    assert torch.equal(pkg.mla_prefill(**g)[0], want)
+    g["q"] = c["q"].transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    assert torch.equal(pkg.mla_prefill(**g)[0], want)
+
+
+def test_prefill_bound_too_small_is_reported():
+    c = case([(20, 100), (30, 500), (10, 40)], 2, 16, 15)
+    g = on_gpu(c)
+    _lib.gqa_paged_decode_device_error()
+    out, lse = pkg.mla_prefill(**g, max_kv_tokens=120)
+    assert _lib.gqa_paged_decode_device_error() == 64
+    assert torch.all(torch.isneginf(lse[:, 20:50])) and torch.all(out[20:50] == 0)
+    whole = pkg.mla_prefill(**g)[0]
+    assert torch.equal(out[:20], whole[:20])
+
+
+def test_prefill_malformed_offsets_are_reported_and_stay_in_range():
+    c = case([(20, 20), (30, 30)], 1, 16, 16)
+    g = on_gpu(c)
+    for cu in ([0, 40, 20], [-3, 20, 50], [0, 20, 90]):
+        g["cu_seqlens_q"] = torch.tensor(cu, dtype=torch.int32).cuda()
+        guard = torch.full((150, 1, 128), 5.0, dtype=BF, device="cuda")
+        pkg.mla_prefill(**g, out=guard[50:100])
+        assert _lib.gqa_paged_decode_device_error() == 8
+        assert torch.all(guard[:50] == 5.0) and torch.all(guard[100:] == 5.0)
+
+
+def test_prefill_many_sequences():
+    """More sequences than one chunk of the plan's prefix sums (1024)."""
+    g = torch.Generator().manual_seed(17)
+    lens = [(int(a), int(a) + int(b)) for a, b in zip(torch.randint(0, 4, (1500,), generator=g),
+                                                     torch.randint(0, 5, (1500,), generator=g))]
+    c = case(lens, 1, 4, 17)
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+
+
+def test_prefill_passes_over_the_heads_agree():
+    """A bound on the tokens that makes the heads take several passes gives the same values."""
+    c = case([(60, 200)], 5, 16, 18)
+    g = on_gpu(c)
+    want, wl = pkg.mla_prefill(**g)
+    big = 2_000_000  # 512 bytes a token and head: two heads a pass
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    out, lse = pkg.mla_prefill(**g, max_kv_tokens=big)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_prefill_repeats_and_streams_and_graph():
+    c = case([(150, 400), (64, 64)], 4, 32, 19)
+    g = on_gpu(c)
+    want, wl = pkg.mla_prefill(**g)
+    for _ in range(3):
+        out, lse = pkg.mla_prefill(**g)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):  # two calls at once, each with its own workspace
+        for s in streams:
+            got.append(pkg.mla_prefill(**g, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) and torch.equal(l, wl) for o, l in got)
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkg.mla_prefill(**g, out=out, with_lse=False)
+    g["q"].copy_(g["q"].flip(0))
+    expect = pkg.mla_prefill(**g)[0]
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, expect)
+
+
+def test_prefill_refusals():
+    g = on_gpu(case([(5, 9)], 2, 16, 20))
+    for change in (dict(q=g["q"].float()), dict(q=g["q"][:, :1]), dict(w_kv=g["w_kv"][:, :200]), dict(kv_cache=g["kv_cache"][:, :, 0]),
+                   dict(block_table=g["block_table"].long()), dict(cache_seqlens=g["cache_seqlens"].repeat(2)),
+                   dict(cu_seqlens_q=g["cu_seqlens_q"][:1]), dict(out=torch.empty(5, 2, 64, dtype=BF, device="cuda")),
+                   dict(lse=torch.empty(5, 2, device="cuda")), dict(max_kv_tokens=-1), dict(max_kv_tokens=1 << 40)):
+        with pytest.raises(ValueError):
+            pkg.mla_prefill(**dict(g, **change))
+    with pytest.raises(pkg.GqaError):
+        pkg.mla_prefill(**g, softmax_scale=float("nan"))
+    with pytest.raises(pkg.GqaError):
+        pkg.mla_prefill(**g, workspace=torch.empty(100, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------- used together
+def test_prompt_then_steps():
+    """A serving run: a prompt's latents written and attended (expanded), then steps of one token (absorbed). Each
+    output against the float64 definition on what the cache holds."""
+    g = torch.Generator().manual_seed(30)
+    h, page, n, steps = 16, 32, 90, 3
+    w, freq = weights(h, 31), pkg.rope_inv_freq(64)[0]
+    cache = torch.full((8, page, 1, 576), float("nan"), dtype=BF, device="cuda")
+    table = torch.tensor([[5, 2, 7, 0]], dtype=torch.int32)
+    slot = torch.tensor([int(table[0, t // page]) * page + t % page for t in range(n + steps)], dtype=torch.int32).cuda()
+    rows = torch.randn(n + steps, 576, generator=g).to(BF).cuda()
+    q = torch.randn(n + steps, h, 192, generator=g).to(BF).cuda()
+    pos = torch.arange(n + steps, dtype=torch.int32).cuda()
+    pkg.mla_kv_append(rows[:n, :512], rows[:n, 512:], slot[:n], cache, pos[:n], freq)
+    turned = pkg.rope(q, pos, freq, rot_offset=128, layout="interleaved")
+    one = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    out, lse = pkg.mla_prefill(turned[:n], w.cuda(), cache, table.cuda(), one([n]), one([0, n]))
+    c = dict(q=turned[:n].cpu(), w_kv=w, kv_cache=cache.cpu(), block_table=table, cache_seqlens=one([n]).cpu(),
+             cu_seqlens_q=one([0, n]).cpu())
+    check(out, lse, c, 192 ** -0.5, True)
+    for i in range(n, n + steps):
+        pkg.mla_kv_append(rows[i:i + 1, :512], rows[i:i + 1, 512:], slot[i:i + 1], cache, pos[i:i + 1], freq)
+        o, l = pkg.mla_absorbed_run(q[None, i:i + 1], w.cuda(), cache, table.cuda(), one([i + 1]), pos[i:i + 1], freq)
+        ref, lref, _, _ = sv.mla_prefill_oracle(turned[i:i + 1].cpu(), w, cache.cpu(), table, [i + 1], [0, 1], 192 ** -0.5)
+        assert np.all(np.abs(sv.f64(o)[0, 0] - ref[0]) <= 2e-2 + 2e-2 * np.abs(ref[0]))
+        assert np.abs(sv.f64(l)[0, :, 0] - lref[:, 0]).max() <= 2e-2
+        e, _ = pkg.mla_prefill(turned[i:i + 1], w.cuda(), cache, table.cuda(), one([i + 1]), one([0, 1]))
+        assert np.abs(sv.f64(e)[0] - sv.f64(o)[0, 0]).max() <= 2e-2  # the two forms agree
+    assert _lib.gqa_paged_decode_device_error() == 0
