@@ -297,7 +297,12 @@ struct MlaPrefillParams {
   void* vv;            // [heads_per_pass][cap][128] fp16 values (scaled)
   int* err;
   int head0, heads;    // heads of this pass
+  int head_group;      // heads whose CTAs run together
 };
+// A 2D tensor map over rows of `width` values (`pitch` bytes apart, 128-byte swizzle), read as boxes of
+// box_w x box_rows. False if the driver call is missing or refuses.
+bool tc_encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows,
+                  int64_t pitch, int box_w, int box_rows);
 // Bytes of the workspace; with base != NULL also points the params' fields into it.
 size_t mla_prefill_workspace(MlaPrefillParams* p, char* base);
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream);

@@ -23,22 +23,26 @@
 // (paged rows to packed rows, 128-aligned per sequence and zero-filled, and the
 // maxima), the expansion, the attention. Tensor-core bound.
 #include <cuda_bf16.h>
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
 #include "gqa_kernels.h"
 #include "gqa_ptx.cuh"
+#include "gqa_tc.cuh"
 
 namespace gqa {
 namespace {
 
-constexpr int kLat = 512, kNope = 128, kRope = 64, kHeadV = 128, kRow = kLat + kRope, kDqk = kNope + kRope;
+constexpr int kLat = 512, kNope = 128, kRope = 64, kHeadV = 128, kRow = kLat + kRope;
 constexpr int kAlign = 128;    // packed rows of a sequence start at a multiple of this
-constexpr int kQTile = 64;    // query rows a CTA takes
+constexpr int kQTile = 256;   // query rows a CTA takes
 constexpr int64_t kExpandBytes = int64_t{1} << 30;  // expanded keys and values of one pass over the heads
+constexpr int64_t kGroupBytes = int64_t{64} << 20;  // and of the heads whose CTAs run together (half of L2)
 
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
@@ -289,164 +293,370 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_expand_kernel(const MlaPr
 }
 
 // -------------------------------------------------------------- attention
-// 64 query rows of one head a CTA, 16 a warp; tiles of 64 keys, two in flight.
-constexpr int kKTile = 64;
-constexpr int kQBytes = kQTile * kDqk * 2, kKBytes = kKTile * kDqk * 2, kVBytes = kKTile * kHeadV * 2;
-constexpr int kAttnSmem = kQBytes + 2 * (kKBytes + kVBytes) + kQTile * 4;
-__global__ void __launch_bounds__(128) gqa_mla_prefill_attn_kernel(const MlaPrefillParams p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t sb = smem_addr(smem);
-  float* rowfac = reinterpret_cast<float*>(smem + kQBytes + 2 * (kKBytes + kVBytes));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qt = blockIdx.x, hp = blockIdx.y, h = p.head0 + hp;
-  if (qt >= __ldg(p.qt_start + p.batch)) return;
+// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
+// keys in tiles of 128. Per tile and key tile, S = Q K^T (M = 128 rows, N = 128
+// keys, 12 MMAs of K = 16) lands in tensor memory, a thread per row turns it
+// into fp16 probabilities that overwrite it there, and O += P V (8 MMAs, P read
+// from tensor memory) accumulates beside it. The two tiles alternate: while one
+// is in its softmax, the tensor core does the other's O and next S.
+//
+// Roles: two softmax warpgroups (one per tile), an MMA thread, a copy thread.
+// Shared memory: the queries (2 x 48 KB, fp16, 128-byte swizzle) and a ring of
+// eight 16 KB units of 128 keys x 64 values: three per key tile (two of the
+// expanded key, one rotary), two per value tile, so the next keys load while
+// the current values are in use. Tensor memory: S at columns 0 and 128 (P over
+// its first 64), O at 256 and 384.
+//
+// The running maximum moves only when a row's scores pass it by 2^8, so O is
+// seldom rescaled; probabilities are held times 2^7, at most 2^15, which keeps
+// small ones fp16 normals. Every wait is bounded: on a timeout the CTA flags
+// the device error word and leaves after draining its copies and MMAs.
+constexpr int kKTile = 128, kUnit = kKTile * 128, kRing = 8;
+constexpr int kQTileBytes = 3 * kUnit;
+constexpr int kAtWarps = 10, kAtThreads = kAtWarps * 32, kMmaWarp = 8, kCopyWarp = 9;
+constexpr float kShift = 7.f, kMoveBy = 8.f;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kAtRing = 2 * kQTileBytes, kAtBars = kAtRing + kRing * kUnit;
+enum : int { B_FULL = 0, B_EMPTY = B_FULL + kRing, B_Q = B_EMPTY + kRing, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2,
+             B_DONE = B_O + 2, B_COUNT };
+constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
+constexpr int kAtSmem = kAtAbort + 4 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
+static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
+
+struct AttnMaps {  // boxes of 64 values x 128 rows
+  CUtensorMap kn, vv, kr;
+};
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Bounded wait that ignores the abort flag (draining before exit).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitNs) break;
+}
+
+// Whole warp: lane 0 waits (bounded), every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = tc_wait(bar, parity, abort_s, err, bit, kWaitNs) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Bits c of a word whose key 32 k + c (of the key tile at t0) is at most lim.
+__device__ __forceinline__ unsigned upto(int lim, int t0, int k) {
+  const int c = lim - t0 - 32 * k;
+  return c < 0 ? 0u : (c >= 31 ? 0xffffffffu : (2u << c) - 1u);
+}
+
+__global__ void __launch_bounds__(kAtThreads, 1)
+    gqa_mla_prefill_attn_kernel(const MlaPrefillParams p, const __grid_constant__ AttnMaps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  // CTAs in order: groups of heads whose keys and values stay in L2 together,
+  // within a group the last query tiles (the most keys, if causal) first
+  const int tiles = __ldg(p.qt_start + p.batch);
+  const int64_t rank = blockIdx.x;
+  if (rank >= static_cast<int64_t>(tiles) * p.heads) return;
+  const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
+  const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
+  const int gh = min(p.head_group, p.heads - group * p.head_group);
+  const int qt = tiles - 1 - in_group / gh, hp = group * p.head_group + in_group % gh, h = p.head0 + hp;
+
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kAtAbort);
+  auto bar = [&](int i) { return base + kAtBars + 8u * static_cast<uint32_t>(i); };
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), (i >= B_Q && i < B_S) || (i >= B_P && i < B_O) ? 4u : 1u);
+    *abort_s = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) tc_alloc(base + kAtSlot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kAtSlot);
+
   const int b = find_seq(p.qt_start, p.batch, qt);
   const int nq = __ldg(p.q_start + 2 * b + 1), i0 = (qt - __ldg(p.qt_start + b)) * kQTile;
   const int64_t q0 = __ldg(p.q_start + 2 * b);
   const int n = __ldg(p.kv_len + b), kv0 = __ldg(p.kv_start + b);
-  // the sequence's own length places the queries (n may be cut by the table or the bound)
-  const int seq_n = n;
-  const int last = p.causal ? min(n, seq_n - nq + min(i0 + kQTile, nq)) : n;  // keys any row of the tile sees
-  const int ntiles = last > 0 ? (last + kKTile - 1) / kKTile : 0;
+  int* err = p.err;
+  // key tiles of each query tile: up to the last key that its last row sees
+  int nt[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const int last_row = min(i0 + 128 * (a + 1), nq) - 1;
+    int keys = last_row < i0 + 128 * a ? 0 : (p.causal ? min(n, n - nq + last_row + 1) : n);
+    keys = max(keys, 0);
+    nt[a] = (keys + kKTile - 1) / kKTile;
+  }
+  const int total = max(nt[0], nt[1]);
 
-  // queries to fp16, each row brought to a largest value in [2^10, 2^11)
-  for (int r = warp * 16; r < warp * 16 + 16; ++r) {
-    uint32_t v[3];
-    unsigned top = 0;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      v[j] = i0 + r < nq ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                   (q0 + i0 + r) * p.q_token_stride + h * p.q_head_stride) +
-                                 32 * j + lane)
-                         : 0u;
-      top = finite_bits2(v[j], top);
+  if (warp == kCopyWarp) {
+    if (lane == 0 && total > 0) {
+      const int y0 = hp * p.cap + kv0;
+      int u = 0;
+      bool good = true;
+      for (int j = 0; j < total && good; ++j)
+        for (int k = 0; k < 5 && good; ++k, ++u) {
+          const int s = u % kRing;
+          if (u >= kRing && !tc_wait(bar(B_EMPTY + s), ((u / kRing) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kWaitNs)) {
+            good = false;
+            break;
+          }
+          const uint32_t full = bar(B_FULL + s), dst = base + kAtRing + s * kUnit;
+          mbar_arrive_expect_tx(full, kUnit);
+          if (k == 2)
+            tma_load_2d(dst, &maps.kr, 0, kv0 + j * kKTile, full);
+          else if (k < 2)
+            tma_load_2d(dst, &maps.kn, 64 * k, y0 + j * kKTile, full);
+          else
+            tma_load_2d(dst, &maps.vv, 64 * (k - 3), y0 + j * kKTile, full);
+        }
+      for (int i = u > kRing ? u - kRing : 0; i < u; ++i) drain_wait(bar(B_FULL + i % kRing), (i / kRing) & 1);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
-    if (lane == 0) rowfac[r] = pow2(max(e, -126));
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && total > 0) {
+      constexpr uint32_t idesc_s = tc_idesc_f16(128, kKTile, false, false);
+      constexpr uint32_t idesc_o = tc_idesc_f16(128, kHeadV, false, true);
+      constexpr uint32_t idesc_o2 = tc_idesc_f16(128, kHeadV / 2, false, true);
+      int landed = 0;  // units known to have landed
+      auto need = [&](int units) -> bool {
+        for (; landed < units; ++landed)
+          if (!tc_wait(bar(B_FULL + landed % kRing), (landed / kRing) & 1, abort_s, err, kErrTimeoutFull, kWaitNs)) return false;
+        return true;
+      };
+      auto unit = [&](int u) { return base + kAtRing + (u % kRing) * kUnit; };
+      auto scores = [&](int a, int j) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const float f = pow2(min(-e, 127));
-      const uint32_t h2 = pack_f16(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw128(sb + j * (kQTile * 128), r, lane >> 2) + (lane & 3) * 4), "r"(h2)
-                   : "memory");
+        for (int r = 0; r < 3; ++r) {
+          const uint64_t dq = tc_sdesc(base + a * kQTileBytes + r * kUnit, 16, 1024, kSwizzle128B);
+          const uint64_t dk = tc_sdesc(unit(5 * j + r), 16, 1024, kSwizzle128B);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(tmem + 128 * a, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_s, (r | kk) ? 1u : 0u);
+        }
+        tc_commit(bar(B_S + a));
+      };
+      auto values = [&](int a, int j) {
+        // V as B: N = 128 values over two units (LBO), K = keys in 8-row groups (SBO)
+        const uint32_t v0 = unit(5 * j + 3), v1 = unit(5 * j + 4);
+        const uint32_t o = tmem + 256 + 128 * a, pr = tmem + 128 * a;
+        if (v1 == v0 + kUnit) {
+          const uint64_t dv = tc_sdesc(v0, kUnit, 1024, kSwizzle128B);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_tmem_a(o, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, (j | kk) ? 1u : 0u);
+        } else {  // the pair wraps around the ring's end
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint64_t dv = tc_sdesc(half ? v1 : v0, kUnit, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_tmem_a(o + 64 * half, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o2, (j | kk) ? 1u : 0u);
+          }
+        }
+      };
+      auto release = [&](int u, int count) {
+        for (int i = 0; i < count; ++i) tc_commit(bar(B_EMPTY + (u + i) % kRing));
+      };
+      bool good = need(3);
+      for (int a = 0; a < 2 && good; ++a) {
+        if (nt[a] == 0) continue;
+        good = tc_wait(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull, kWaitNs);
+        if (!good) break;
+        tc_fence_after();
+        scores(a, 0);
+      }
+      if (good) release(0, 3);
+      for (int j = 0; j < total && good; ++j) {
+        for (int a = 0; a < 2 && good; ++a) {
+          if (j >= nt[a]) continue;
+          good = tc_wait(bar(B_P + a), j & 1, abort_s, err, kErrTimeoutFull, kWaitNs) && need(5 * j + 5);
+          if (!good) break;
+          tc_fence_after();
+          values(a, j);
+          const bool last_user = a == 1 || j >= nt[1];
+          if (last_user) release(5 * j + 3, 2);
+          if (j + 1 < nt[a]) {
+            good = need(5 * (j + 1) + 3);
+            if (!good) break;
+            scores(a, j + 1);
+          } else {
+            tc_commit(bar(B_O + a));
+          }
+          if (j + 1 < total && (a == 1 || j + 1 >= nt[1])) release(5 * (j + 1), 3);
+        }
+        // tile 0 has no tile j, but tile 1 does (or the reverse): the release above ran with the last active one
+      }
+      tc_commit(bar(B_DONE));  // every MMA done before tensor memory is freed
+      drain_wait(bar(B_DONE), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------- a softmax warpgroup: tile a, row 32 wq + lane
+    const int a = warp >> 2, wq = warp & 3;
+    const uint32_t quarter = static_cast<uint32_t>(32 * wq) << 16;
+    const uint32_t s_col = tmem + quarter + 128 * a, o_col = tmem + quarter + 256 + 128 * a;
+    const int row0 = i0 + 128 * a + 32 * wq;  // query row (of the sequence) of lane 0
+    const int i = row0 + lane;
+    float row_fac = 1.f;
+    if (nt[a] > 0) {  // the warp's 32 queries to fp16, each brought to a largest value in [2^10, 2^11)
+      const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + h * p.q_head_stride;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        uint32_t v[8][3];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            v[r][k] = row0 + r0 + r < nq ? __ldg(reinterpret_cast<const uint32_t*>(qp + (q0 + row0 + r0 + r) * p.q_token_stride) +
+                                                 32 * k + lane)
+                                         : 0u;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const unsigned top = __reduce_max_sync(0xffffffffu, finite_bits2(v[r][0], finite_bits2(v[r][1], finite_bits2(v[r][2], 0u))));
+          const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
+          if (lane == r0 + r) row_fac = pow2(e);
+          const float f = sign * pow2(-e);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t h2 = pack_f16(__uint_as_float(v[r][k] << 16) * f, __uint_as_float(v[r][k] & 0xffff0000u) * f);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw128(base + a * kQTileBytes + k * kUnit, 32 * wq + r0 + r, lane >> 2) +
+                                                        (lane & 3) * 4),
+                         "r"(h2)
+                         : "memory");
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q + a));
+    }
+    int ek, ev;
+    kv_exponents(p.amax, ek, ev);
+    const float sc = fmaxf(row_fac * fabsf(p.scale_log2) * pow2(ek), 1e-37f);  // > 0: -inf * sc stays -inf
+    const int lim = p.causal ? n - nq + i : INT_MAX;          // last key this row sees
+    const int lim0 = p.causal ? n - nq + row0 : INT_MAX;      // and the warp's first row
+    float m = -INFINITY;
+    uint64_t l2 = 0;
+    bool good = true;
+    for (int j = 0; j < nt[a] && good; ++j) {
+      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(p.valid) + (kv0 >> 7) + j);
+      good = warp_wait(bar(B_S + a), j & 1, abort_s, err, kErrTimeoutFull);
+      if (!good) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_ld32(s_col + 32 * c, s + 32 * c);
+      tc_wait_ld();
+      const int t0 = j * kKTile;
+      if ((vw.x & vw.y & vw.z & vw.w) != 0xffffffffu || t0 + kKTile - 1 > lim0) {
+        const unsigned w[4] = {vw.x & upto(lim, t0, 0), vw.y & upto(lim, t0, 1), vw.z & upto(lim, t0, 2), vw.w & upto(lim, t0, 3)};
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (((w[c >> 5] >> (c & 31)) & 1u) == 0) s[c] = 0xff800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const bool move = top > m + kMoveBy;
+      if (__any_sync(0xffffffffu, move)) {
+        const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2(m - top));
+        if (move) m = top;
+        float lo, hi;
+        unpack2(l2, lo, hi);
+        l2 = pack2(lo * alpha, hi * alpha);
+        if (j > 0) {  // the commit that signalled S also covers the previous tile's O
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tc_ld16(o_col + 16 * c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tc_st16(o_col + 16 * c, o);
+          }
+        }
+      }
+      const float off = m == -INFINITY ? 0.f : kShift - m;
+      const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float x0, x1;
+          unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), sc2, off2), x0, x1);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          l2 = add2(l2, pack2(x0, x1));
+          pk[k] = pack_f16(x0, x1);
+        }
+        tc_st16(s_col + 16 * c, pk);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_P + a));
+    }
+    if (nt[a] > 0 && good) good = warp_wait(bar(B_O + a), 0, abort_s, err, kErrTimeoutFull);
+    tc_fence_after();
+    if (good) {
+      float l, hi;
+      unpack2(l2, l, hi);
+      l += hi;
+      const bool none = l == 0.f;  // the row sees no token
+      const float inv = pow2(ev) / l;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (nt[a] > 0) {
+          tc_ld32(o_col + 32 * c, o);
+          tc_wait_ld();
+        }
+        if (i < nq)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+            out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
+          }
+      }
+      if (p.lse != nullptr && i < nq)
+        p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] = none ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
     }
   }
-  const __half* kn = static_cast<const __half*>(p.kn) + (static_cast<int64_t>(hp) * p.cap + kv0) * 128;
-  const __half* vv = static_cast<const __half*>(p.vv) + (static_cast<int64_t>(hp) * p.cap + kv0) * 128;
-  const __half* kr = static_cast<const __half*>(p.kr) + static_cast<int64_t>(kv0) * kRope;
-  auto load = [&](int j) {
-    const uint32_t ks = sb + kQBytes + (j & 1) * (kKBytes + kVBytes), vs = ks + kKBytes;
-    for (int i = tid; i < kKTile * 16; i += 128) {
-      const int r = i >> 4, c = i & 15;
-      const int64_t t = static_cast<int64_t>(j) * kKTile + r;
-      cp_async_16(sw128(ks + (c >> 3) * (kKTile * 128), r, c & 7), kn + t * 128 + c * 8, 16u);
-      cp_async_16(sw128(vs + (c >> 3) * (kKTile * 128), r, c & 7), vv + t * 128 + c * 8, 16u);
-    }
-    for (int i = tid; i < kKTile * 8; i += 128) {
-      const int r = i >> 3, c = i & 7;
-      cp_async_16(sw128(ks + 2 * (kKTile * 128), r, c), kr + (static_cast<int64_t>(j) * kKTile + r) * kRope + c * 8, 16u);
-    }
-  };
-  float o[16][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  tc_fence_before();
   __syncthreads();
-  int ek, ev;
-  kv_exponents(p.amax, ek, ev);
-  float sc[2];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) sc[half] = rowfac[warp * 16 + (lane >> 2) + 8 * half] * p.scale_log2 * pow2(ek);
-  if (ntiles > 0) load(0);
-  cp_async_commit();
-  for (int j = 0; j < ntiles; ++j) {
-    if (j + 1 < ntiles) load(j + 1);
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    const uint32_t ks = sb + kQBytes + (j & 1) * (kKBytes + kVBytes), vs = ks + kKBytes;
-    float s[8][4] = {};
-#pragma unroll
-    for (int kk = 0; kk < 12; ++kk) {
-      uint32_t a0, a1, a2, a3;
-      ldsm_x4(sw128(sb + (kk >> 2) * (kQTile * 128), warp * 16 + (lane & 15), 2 * (kk & 3) + (lane >> 4)), a0, a1, a2, a3);
-#pragma unroll
-      for (int nj = 0; nj < 8; nj += 2) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(sw128(ks + (kk >> 2) * (kKTile * 128), nj * 8 + ((lane >> 4) << 3) + (lane & 7), 2 * (kk & 3) + ((lane >> 3) & 1)),
-                b0, b1, b2, b3);
-        mma_f16_16816(s[nj], a0, a1, a2, a3, b0, b1);
-        mma_f16_16816(s[nj + 1], a0, a1, a2, a3, b2, b3);
-      }
-    }
-    const unsigned v0 = __ldg(p.valid + (kv0 >> 5) + 2 * j), v1 = __ldg(p.valid + (kv0 >> 5) + 2 * j + 1);
-    float mx[2] = {m[0], m[1]};
-#pragma unroll
-    for (int nj = 0; nj < 8; ++nj)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = nj * 8 + 2 * (lane & 3) + (e & 1), half = e >> 1;
-        const int t = j * kKTile + col, i = i0 + warp * 16 + (lane >> 2) + 8 * half;
-        const bool ok = (((col < 32 ? v0 : v1) >> (col & 31)) & 1u) != 0 && (!p.causal || t <= seq_n - nq + i);
-        s[nj][e] = ok ? s[nj][e] * sc[half] : -INFINITY;
-        mx[half] = fmaxf(mx[half], s[nj][e]);
-      }
-    float fix[2], base[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-      mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
-      fix[half] = mx[half] == -INFINITY ? 1.f : ex2(m[half] - mx[half]);
-      // probabilities are held times 2^14, so that small ones stay fp16 normals
-      base[half] = mx[half] == -INFINITY ? 0.f : 14.f - mx[half];
-      m[half] = mx[half];
-      l[half] *= fix[half];
-    }
-#pragma unroll
-    for (int nd = 0; nd < 16; ++nd) {
-      o[nd][0] *= fix[0];
-      o[nd][1] *= fix[0];
-      o[nd][2] *= fix[1];
-      o[nd][3] *= fix[1];
-    }
-#pragma unroll
-    for (int nj = 0; nj < 8; ++nj)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[nj][e] = ex2(s[nj][e] + base[e >> 1]);
-        l[e >> 1] += s[nj][e];
-      }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t a0 = pack_f16(s[2 * kk][0], s[2 * kk][1]), a1 = pack_f16(s[2 * kk][2], s[2 * kk][3]);
-      const uint32_t a2 = pack_f16(s[2 * kk + 1][0], s[2 * kk + 1][1]), a3 = pack_f16(s[2 * kk + 1][2], s[2 * kk + 1][3]);
-#pragma unroll
-      for (int nd = 0; nd < 16; nd += 2) {
-        uint32_t b0, b1, b2, b3;
-        const int c = nd + (lane >> 4);
-        ldsm_x4_trans(sw128(vs + (c >> 3) * (kKTile * 128), kk * 16 + (lane & 15), c & 7), b0, b1, b2, b3);
-        mma_f16_16816(o[nd], a0, a1, a2, a3, b0, b1);
-        mma_f16_16816(o[nd + 1], a0, a1, a2, a3, b2, b3);
-      }
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-    l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-    const int i = i0 + warp * 16 + (lane >> 2) + 8 * half;
-    if (i >= nq) continue;
-    const bool none = l[half] == 0.f;  // the row sees no token
-    const float inv = pow2(ev) / l[half];
-    __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV;
-#pragma unroll
-    for (int nd = 0; nd < 16; ++nd)
-      *reinterpret_cast<uint32_t*>(row + nd * 8 + 2 * (lane & 3)) =
-          none ? 0u : pack_bf16(o[nd][2 * half] * inv, o[nd][2 * half + 1] * inv);
-    if (p.lse != nullptr && (lane & 3) == 0)
-      p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] =
-          none ? -INFINITY : (m[half] - 14.f + log2f(l[half])) * 0.6931471805599453f;
-  }
+  if (warp == 0) tc_dealloc(tmem, 512);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -485,14 +695,22 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
   static std::atomic<int> ex_done[kMaxDevices], at_done[kMaxDevices];
   cudaError_t e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), 3 * kExStage);
   if (e != cudaSuccess) return e;
-  e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel), kAttnSmem);
+  e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel), kAtSmem);
   if (e != cudaSuccess) return e;
-  const int q_tiles = p.total_q / kQTile + p.batch;
+  const int64_t q_tiles = p.total_q / kQTile + p.batch;
+  const int64_t group = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
   for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass) {
     p.head0 = h0;
     p.heads = p.num_heads - h0 < p.heads_per_pass ? p.num_heads - h0 : p.heads_per_pass;
+    p.head_group = static_cast<int>(group < 1 ? 1 : (group > p.heads ? p.heads : group));
+    AttnMaps maps;
+    const int64_t rows = static_cast<int64_t>(p.heads) * p.cap;
+    if (!tc_encode_2d(&maps.kn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kn, kNope, rows, kNope * 2, 64, kKTile) ||
+        !tc_encode_2d(&maps.vv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.vv, kHeadV, rows, kHeadV * 2, 64, kKTile) ||
+        !tc_encode_2d(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kr, kRope, p.cap, kRope * 2, 64, kKTile))
+      return cudaErrorInvalidValue;
     gqa_mla_prefill_expand_kernel<<<dim3(p.cap / kExBM, 2 * p.heads + 1), 256, 3 * kExStage, stream>>>(p);
-    gqa_mla_prefill_attn_kernel<<<dim3(q_tiles, p.heads), 128, kAttnSmem, stream>>>(p);
+    gqa_mla_prefill_attn_kernel<<<static_cast<unsigned>(q_tiles * p.heads), kAtThreads, kAtSmem, stream>>>(p, maps);
   }
   return cudaGetLastError();
 }

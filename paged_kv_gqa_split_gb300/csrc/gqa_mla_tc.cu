@@ -658,15 +658,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
 
 // Rows of 576 bf16 (1152 B apart), read as boxes of 64 values x box_rows rows, 128-byte swizzle.
 bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int box_rows) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
-  if (fn == nullptr || rows < 1) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDqk), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(kDqk) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tc_encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, kDqk, rows, kDqk * 2, 64, box_rows);
 }
 
 int box_rows_for(int page_size) { return page_size % 64 == 0 ? 64 : 32; }
@@ -691,6 +683,19 @@ cudaError_t launch_tc(const MlaParams& p, const MlaTcMaps& maps, int ctas, cudaS
 }
 
 }  // namespace
+
+bool tc_encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows,
+                  int64_t pitch, int box_w, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (fn == nullptr || rows < 1) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_w), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool mla_tc_supported(int page_size) { return page_size > 0 && page_size % 32 == 0; }
 
