@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kLat = 512, kNope = 128, kRope = 64, kHeadV = 128, kRow = kLat + kRope;
 constexpr int kAlign = 128;    // packed rows of a sequence start at a multiple of this
-constexpr int kQTile = 256;   // query rows a CTA takes
+constexpr int kQTile = 512;   // query rows a pair of CTAs takes
 constexpr int64_t kExpandBytes = int64_t{1} << 30;  // expanded keys and values of one pass over the heads
 constexpr int64_t kGroupBytes = int64_t{64} << 20;  // and of the heads whose CTAs run together (half of L2)
 
@@ -293,37 +293,49 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_expand_kernel(const MlaPr
 }
 
 // -------------------------------------------------------------- attention
-// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
-// keys in tiles of 128. Per tile and key tile, S = Q K^T (M = 128 rows, N = 128
-// keys, 12 MMAs of K = 16) lands in tensor memory, a thread per row turns it
-// into fp16 probabilities that overwrite it there, and O += P V (8 MMAs, P read
-// from tensor memory) accumulates beside it. The two tiles alternate: while one
-// is in its softmax, the tensor core does the other's O and next S.
+// A pair of CTAs takes 512 query rows of one head as two tiles of 256 (128 rows
+// a CTA each) and walks the keys in tiles of 128. Per tile and key tile, S = Q K^T
+// (M = 256, N = 128 keys, 12 MMAs of K = 16) lands in tensor memory, a thread per
+// row turns it into fp16 probabilities that overwrite it there, and O += P V (8
+// MMAs, P read from tensor memory) accumulates beside it. The two tiles alternate:
+// while one is in its softmax, the tensor cores do the other's O and next S.
 //
-// Roles: two softmax warpgroups (one per tile), an MMA thread, a copy thread.
-// Shared memory: the queries (2 x 48 KB, fp16, 128-byte swizzle) and a ring of
-// eight 16 KB units of 128 keys x 64 values: three per key tile (two of the
-// expanded key, one rotary), two per value tile, so the next keys load while
-// the current values are in use. Tensor memory: S at columns 0 and 128 (P over
-// its first 64), O at 256 and 384.
+// Why pairs: the queries take 96 KB of a CTA's shared memory, and V and the next K
+// are in use at once (80 KB at 128 keys). One CTA alone has room for 1.6 key tiles
+// in flight, and its MMAs waited for loads half of the time (measured: 5300 clocks
+// a key tile against 2560 of MMAs). A pair keeps half of each key and value tile
+// in each CTA, which gives a ring of three tiles, and halves the L2 reads.
+//
+// Roles in each CTA: two softmax warpgroups (one per tile), an MMA warp (the even
+// CTA's issues for both), a copy warp. Shared memory: the queries (2 x 48 KB, fp16,
+// 128-byte swizzle), three slots of half a key tile (64 keys x 192) and three of
+// half a value tile (128 keys x 64 values). Tensor memory: S at columns 0 and 128
+// (P over its first 64), O at 256 and 384.
 //
 // The running maximum moves only when a row's scores pass it by 2^8, so O is
 // seldom rescaled; probabilities are held times 2^7, at most 2^15, which keeps
 // small ones fp16 normals. Every wait is bounded: on a timeout the CTA flags
 // the device error word and leaves after draining its copies and MMAs.
-constexpr int kKTile = 128, kUnit = kKTile * 128, kRing = 8;
-constexpr int kQTileBytes = 3 * kUnit;
-constexpr int kAtWarps = 10, kAtThreads = kAtWarps * 32, kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kKTile = 128, kSlots = 3;
+constexpr int kQRegion = 128 * 128, kQTileBytes = 3 * kQRegion;  // 128 rows x 64 values; a CTA's half of a query tile
+constexpr int kKRegion = 64 * 128, kKSlot = 3 * kKRegion;        // 64 keys x 64 values
+constexpr int kVSlot = kKTile * 128;                             // 128 keys x 64 values
+constexpr int kAtThreads = 384, kMmaWarp = 0, kCopyWarp = 1, kSoftWarp = 4;  // warps 2 and 3 only allot registers
+// 168 registers a thread at launch (384 x 168 of the SM's 65536); the split below is no more
+constexpr int kSoftRegs = 208, kRoleRegs = 88;
+static_assert(256 * kSoftRegs + 128 * kRoleRegs <= kAtThreads * 168, "register split");
 constexpr float kShift = 7.f, kMoveBy = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kAtRing = 2 * kQTileBytes, kAtBars = kAtRing + kRing * kUnit;
-enum : int { B_FULL = 0, B_EMPTY = B_FULL + kRing, B_Q = B_EMPTY + kRing, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2,
-             B_DONE = B_O + 2, B_COUNT };
+constexpr int kAtK = 2 * kQTileBytes, kAtV = kAtK + kSlots * kKSlot, kAtBars = kAtV + kSlots * kVSlot;
+// Barriers. The even CTA's: K and V landed (both halves' bytes), queries and P written (4 warps of each CTA).
+// Both CTAs' (MMA commits): K and V slots free, S and O written, all done.
+enum : int { B_KFULL = 0, B_VFULL = B_KFULL + kSlots, B_Q = B_VFULL + kSlots, B_P = B_Q + 2, B_KFREE = B_P + 2,
+             B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_DONE = B_O + 2, B_COUNT };
 constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
 constexpr int kAtSmem = kAtAbort + 4 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
 static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
 
-struct AttnMaps {  // boxes of 64 values x 128 rows
+struct AttnMaps {  // boxes of 64 values x 64 rows (keys) and x 128 rows (values)
   CUtensorMap kn, vv, kr;
 };
 
@@ -353,11 +365,13 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kWaitNs) break;
 }
 
-// Whole warp: lane 0 waits (bounded), every lane gets the same answer.
+// Whole warp: every lane waits (bounded; no lane runs apart from the others), every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = tc_wait(bar, parity, abort_s, err, bit, kWaitNs) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs));
+}
+// The same for a barrier that both CTAs' threads arrive on.
+__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs) && mbar_try_wait_cluster(bar, parity));
 }
 
 // Bits c of a word whose key 32 k + c (of the key tile at t0) is at most lim.
@@ -372,7 +386,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // CTAs in order: groups of heads whose keys and values stay in L2 together,
   // within a group the last query tiles (the most keys, if causal) first
   const int tiles = __ldg(p.qt_start + p.batch);
-  const int64_t rank = blockIdx.x;
+  const uint32_t half = cluster_rank();  // which 128 rows of a tile, which half of the keys and values
+  const int64_t rank = blockIdx.x >> 1;
   if (rank >= static_cast<int64_t>(tiles) * p.heads) return;
   const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
   const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
@@ -386,14 +401,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kAtAbort);
   auto bar = [&](int i) { return base + kAtBars + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), (i >= B_Q && i < B_S) || (i >= B_P && i < B_O) ? 4u : 1u);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q && i < B_KFREE ? 8u : 1u);
     *abort_s = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 0) tc_alloc(base + kAtSlot, 512);
+  if (warp == 0) tc2_alloc(base + kAtSlot, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the barriers and the tensor memory of both CTAs are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kAtSlot);
 
@@ -402,125 +418,131 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int64_t q0 = __ldg(p.q_start + 2 * b);
   const int n = __ldg(p.kv_len + b), kv0 = __ldg(p.kv_start + b);
   int* err = p.err;
-  // key tiles of each query tile: up to the last key that its last row sees
+  // key tiles of each query tile (the same in both CTAs): up to the last key that its last row sees
   int nt[2];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    const int last_row = min(i0 + 128 * (a + 1), nq) - 1;
-    int keys = last_row < i0 + 128 * a ? 0 : (p.causal ? min(n, n - nq + last_row + 1) : n);
+    const int last_row = min(i0 + 256 * (a + 1), nq) - 1;
+    int keys = last_row < i0 + 256 * a ? 0 : (p.causal ? min(n, n - nq + last_row + 1) : n);
     keys = max(keys, 0);
     nt[a] = (keys + kKTile - 1) / kKTile;
   }
   const int total = max(nt[0], nt[1]);
 
-  if (warp == kCopyWarp) {
-    if (lane == 0 && total > 0) {
-      const int y0 = hp * p.cap + kv0;
-      int u = 0;
-      bool good = true;
-      for (int j = 0; j < total && good; ++j)
-        for (int k = 0; k < 5 && good; ++k, ++u) {
-          const int s = u % kRing;
-          if (u >= kRing && !tc_wait(bar(B_EMPTY + s), ((u / kRing) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kWaitNs)) {
-            good = false;
-            break;
-          }
-          const uint32_t full = bar(B_FULL + s), dst = base + kAtRing + s * kUnit;
-          mbar_arrive_expect_tx(full, kUnit);
-          if (k == 2)
-            tma_load_2d(dst, &maps.kr, 0, kv0 + j * kKTile, full);
-          else if (k < 2)
-            tma_load_2d(dst, &maps.kn, 64 * k, y0 + j * kKTile, full);
-          else
-            tma_load_2d(dst, &maps.vv, 64 * (k - 3), y0 + j * kKTile, full);
+  if (warp < kSoftWarp) {
+    setmaxnreg_dec<kRoleRegs>();
+    if (warp == kCopyWarp && lane == 0) {
+      const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
+      const uint32_t kfull = cluster_addr(bar(B_KFULL), 0), vfull = cluster_addr(bar(B_VFULL), 0);
+      int j = 0, s = 0;
+      uint32_t ph = 1;  // parity of the slot's previous release
+      for (; j < total; ++j) {
+        const uint32_t kd = base + kAtK + s * kKSlot, vd = base + kAtV + s * kVSlot;
+        if (j >= kSlots && !tc_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty, kWaitNs)) break;
+        if (half == 0) mbar_arrive_expect_tx(bar(B_KFULL + s), 2 * kKSlot);
+        tma2_load_2d(kd, &maps.kn, 0, y0 + j * kKTile, kfull + 8 * s);
+        tma2_load_2d(kd + kKRegion, &maps.kn, 64, y0 + j * kKTile, kfull + 8 * s);
+        tma2_load_2d(kd + 2 * kKRegion, &maps.kr, 0, r0 + j * kKTile, kfull + 8 * s);
+        if (j >= kSlots && !tc_wait(bar(B_VFREE + s), ph, abort_s, err, kErrTimeoutEmpty, kWaitNs)) break;
+        if (half == 0) mbar_arrive_expect_tx(bar(B_VFULL + s), 2 * kVSlot);
+        tma2_load_2d(vd, &maps.vv, 64 * half, v0 + j * kKTile, vfull + 8 * s);
+        if (++s == kSlots) {
+          s = 0;
+          ph ^= 1;
         }
-      for (int i = u > kRing ? u - kRing : 0; i < u; ++i) drain_wait(bar(B_FULL + i % kRing), (i / kRing) & 1);
+      }
+      if (half == 0)  // no copy may still be writing either CTA's shared memory when the pair leaves
+        for (int i = max(0, j - kSlots); i < j; ++i) {
+          drain_wait(bar(B_KFULL + i % kSlots), (i / kSlots) & 1);
+          drain_wait(bar(B_VFULL + i % kSlots), (i / kSlots) & 1);
+        }
     }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    if (lane == 0 && total > 0) {
-      constexpr uint32_t idesc_s = tc_idesc_f16(128, kKTile, false, false);
-      constexpr uint32_t idesc_o = tc_idesc_f16(128, kHeadV, false, true);
-      constexpr uint32_t idesc_o2 = tc_idesc_f16(128, kHeadV / 2, false, true);
-      int landed = 0;  // units known to have landed
-      auto need = [&](int units) -> bool {
-        for (; landed < units; ++landed)
-          if (!tc_wait(bar(B_FULL + landed % kRing), (landed / kRing) & 1, abort_s, err, kErrTimeoutFull, kWaitNs)) return false;
-        return true;
-      };
-      auto unit = [&](int u) { return base + kAtRing + (u % kRing) * kUnit; };
-      auto scores = [&](int a, int j) {
-#pragma unroll
-        for (int r = 0; r < 3; ++r) {
-          const uint64_t dq = tc_sdesc(base + a * kQTileBytes + r * kUnit, 16, 1024, kSwizzle128B);
-          const uint64_t dk = tc_sdesc(unit(5 * j + r), 16, 1024, kSwizzle128B);
+    if (warp == kMmaWarp && half == 0 && total > 0) {
+      // the whole warp walks the tiles (warp-uniform operands), one elected lane issues
+      constexpr uint32_t idesc_s = tc_idesc_f16(256, kKTile, false, false);
+      constexpr uint32_t idesc_o = tc_idesc_f16(256, kHeadV, false, true);
+      const uint64_t dq0 = tc_sdesc(base, 16, 1024, kSwizzle128B);
+      const uint64_t dk0 = tc_sdesc(base + kAtK, 16, 1024, kSwizzle128B);
+      // V as B: N = 64 values a CTA (one swizzle atom), K = keys in 8-row groups (SBO)
+      const uint64_t dv0 = tc_sdesc(base + kAtV, kVSlot, 1024, kSwizzle128B);
+      auto scores = [&](int a, uint64_t dk) {
+        uint64_t dq = dq0 + a * (kQTileBytes >> 4);
+#pragma unroll 1
+        for (uint32_t r = 0; r < 3; ++r) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(tmem + 128 * a, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_s, (r | kk) ? 1u : 0u);
+            tc2_mma_warp(tmem + 128 * a, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_s, kk ? 1u : r);
+          dq += kQRegion >> 4;
+          dk += kKRegion >> 4;
         }
-        tc_commit(bar(B_S + a));
+        tc2_commit_warp(bar(B_S + a));
       };
-      auto values = [&](int a, int j) {
-        // V as B: N = 128 values over two units (LBO), K = keys in 8-row groups (SBO)
-        const uint32_t v0 = unit(5 * j + 3), v1 = unit(5 * j + 4);
-        const uint32_t o = tmem + 256 + 128 * a, pr = tmem + 128 * a;
-        if (v1 == v0 + kUnit) {
-          const uint64_t dv = tc_sdesc(v0, kUnit, 1024, kSwizzle128B);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_tmem_a(o, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, (j | kk) ? 1u : 0u);
-        } else {  // the pair wraps around the ring's end
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint64_t dv = tc_sdesc(half ? v1 : v0, kUnit, 1024, kSwizzle128B);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_tmem_a(o + 64 * half, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o2, (j | kk) ? 1u : 0u);
-          }
-        }
-      };
-      auto release = [&](int u, int count) {
-        for (int i = 0; i < count; ++i) tc_commit(bar(B_EMPTY + (u + i) % kRing));
-      };
-      bool good = need(3);
-      for (int a = 0; a < 2 && good; ++a) {
-        if (nt[a] == 0) continue;
-        good = tc_wait(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull, kWaitNs);
-        if (!good) break;
+      // slots and parities of V(j) and K(j + 1)
+      int vs = 0, ks = 0;
+      uint32_t vp = 0, kp = 0;
+      const int nt0 = nt[0], nt1 = nt[1];
+      bool good = warp_wait(bar(B_KFULL), 0, abort_s, err, kErrTimeoutFull);
+#pragma unroll 1
+      for (int a = 0; a < 2; ++a) {
+        if (!good || (a == 0 ? nt0 : nt1) == 0) continue;
+        good = warp_wait_pair(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull);
+        if (!good) continue;
         tc_fence_after();
-        scores(a, 0);
+        scores(a, dk0);
       }
-      if (good) release(0, 3);
+      if (good) tc2_commit_warp(bar(B_KFREE));
+#pragma unroll 1
       for (int j = 0; j < total && good; ++j) {
-        for (int a = 0; a < 2 && good; ++a) {
-          if (j >= nt[a]) continue;
-          good = tc_wait(bar(B_P + a), j & 1, abort_s, err, kErrTimeoutFull, kWaitNs) && need(5 * j + 5);
-          if (!good) break;
-          tc_fence_after();
-          values(a, j);
-          const bool last_user = a == 1 || j >= nt[1];
-          if (last_user) release(5 * j + 3, 2);
-          if (j + 1 < nt[a]) {
-            good = need(5 * (j + 1) + 3);
-            if (!good) break;
-            scores(a, j + 1);
-          } else {
-            tc_commit(bar(B_O + a));
-          }
-          if (j + 1 < total && (a == 1 || j + 1 >= nt[1])) release(5 * (j + 1), 3);
+        if (++ks == kSlots) {
+          ks = 0;
+          kp ^= 1;
         }
-        // tile 0 has no tile j, but tile 1 does (or the reverse): the release above ran with the last active one
+        const uint64_t dk = dk0 + ks * (kKSlot >> 4);
+#pragma unroll 1
+        for (int a = 0; a < 2; ++a) {
+          const int mine = a == 0 ? nt0 : nt1;
+          if (!good || j >= mine) continue;
+          good = warp_wait(bar(B_VFULL + vs), vp, abort_s, err, kErrTimeoutFull) &&
+                 warp_wait(bar(B_P + a), j & 1, abort_s, err, kErrTimeoutFull);
+          if (!good) continue;
+          tc_fence_after();
+          uint64_t dv = dv0 + vs * (kVSlot >> 4);
+          uint32_t pr = tmem + 128 * a;
+#pragma unroll 1
+          for (uint32_t k4 = 0; k4 < 2; ++k4) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc2_mma_tmem_a_warp(tmem + 256 + 128 * a, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : (j | k4));
+            dv += (4 * 2048) >> 4;
+            pr += 32;
+          }
+          if (a == 1 || j >= nt1) tc2_commit_warp(bar(B_VFREE + vs));  // no other tile reads these values
+          if (j + 1 < mine) {
+            good = warp_wait(bar(B_KFULL + ks), kp, abort_s, err, kErrTimeoutFull);
+            if (!good) continue;
+            scores(a, dk);
+            if (a == 1 || j + 1 >= nt1) tc2_commit_warp(bar(B_KFREE + ks));
+          } else {
+            tc2_commit_warp(bar(B_O + a));
+          }
+        }
+        if (++vs == kSlots) {
+          vs = 0;
+          vp ^= 1;
+        }
       }
-      tc_commit(bar(B_DONE));  // every MMA done before tensor memory is freed
-      drain_wait(bar(B_DONE), 0);
+      tc2_commit_warp(bar(B_DONE));  // every MMA done before tensor memory is freed
+      if (lane == 0) drain_wait(bar(B_DONE), 0);
     }
     __syncwarp();
   } else {
     // ------------------------------------- a softmax warpgroup: tile a, row 32 wq + lane
-    const int a = warp >> 2, wq = warp & 3;
+    setmaxnreg_inc<kSoftRegs>();
+    const int a = (warp - kSoftWarp) >> 2, wq = warp & 3;
     const uint32_t quarter = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t s_col = tmem + quarter + 128 * a, o_col = tmem + quarter + 256 + 128 * a;
-    const int row0 = i0 + 128 * a + 32 * wq;  // query row (of the sequence) of lane 0
+    const int row0 = i0 + 256 * a + 128 * half + 32 * wq;  // query row (of the sequence) of lane 0
+    const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + a), 0);
     const int i = row0 + lane;
     float row_fac = 1.f;
     if (nt[a] > 0) {  // the warp's 32 queries to fp16, each brought to a largest value in [2^10, 2^11)
@@ -545,7 +567,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const uint32_t h2 = pack_f16(__uint_as_float(v[r][k] << 16) * f, __uint_as_float(v[r][k] & 0xffff0000u) * f);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw128(base + a * kQTileBytes + k * kUnit, 32 * wq + r0 + r, lane >> 2) +
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw128(base + a * kQTileBytes + k * kQRegion, 32 * wq + r0 + r, lane >> 2) +
                                                         (lane & 3) * 4),
                          "r"(h2)
                          : "memory");
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_Q + a));
+      if (lane == 0) mbar_arrive_cluster(q_bar);
     }
     int ek, ev;
     kv_exponents(p.amax, ek, ev);
@@ -622,7 +644,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P + a));
+      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar);
     }
     if (nt[a] > 0 && good) good = warp_wait(bar(B_O + a), 0, abort_s, err, kErrTimeoutFull);
     tc_fence_after();
@@ -656,7 +678,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tc_dealloc(tmem, 512);
+  cluster_sync();  // the other CTA's arrivals, MMAs and copies are done too
+  if (warp == 0) tc2_dealloc(tmem, 512);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -705,12 +728,24 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
     p.head_group = static_cast<int>(group < 1 ? 1 : (group > p.heads ? p.heads : group));
     AttnMaps maps;
     const int64_t rows = static_cast<int64_t>(p.heads) * p.cap;
-    if (!tc_encode_2d(&maps.kn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kn, kNope, rows, kNope * 2, 64, kKTile) ||
+    if (!tc_encode_2d(&maps.kn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kn, kNope, rows, kNope * 2, 64, kKTile / 2) ||
         !tc_encode_2d(&maps.vv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.vv, kHeadV, rows, kHeadV * 2, 64, kKTile) ||
-        !tc_encode_2d(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kr, kRope, p.cap, kRope * 2, 64, kKTile))
+        !tc_encode_2d(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kr, kRope, p.cap, kRope * 2, 64, kKTile / 2))
       return cudaErrorInvalidValue;
     gqa_mla_prefill_expand_kernel<<<dim3(p.cap / kExBM, 2 * p.heads + 1), 256, 3 * kExStage, stream>>>(p);
-    gqa_mla_prefill_attn_kernel<<<static_cast<unsigned>(q_tiles * p.heads), kAtThreads, kAtSmem, stream>>>(p, maps);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * q_tiles * p.heads));
+    cfg.blockDim = dim3(kAtThreads);
+    cfg.dynamicSmemBytes = kAtSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gqa_mla_prefill_attn_kernel, p, maps);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
