@@ -302,12 +302,16 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_expand_kernel(const MlaPr
 //
 // Why pairs: the queries take 96 KB of a CTA's shared memory, and V and the next K
 // are in use at once (80 KB at 128 keys). One CTA alone has room for 1.6 key tiles
-// in flight, and its MMAs waited for loads half of the time (measured: 5300 clocks
-// a key tile against 2560 of MMAs). A pair keeps half of each key and value tile
-// in each CTA, which gives a ring of three tiles, and halves the L2 reads.
+// in flight, and its MMAs waited for loads (measured: 3900 to 4000 clocks a key tile of
+// both query tiles, against 2560 of MMAs). A pair keeps half of each key and value tile
+// in each CTA, which gives a ring of three tiles, and halves the L2 reads: 2810 clocks,
+// the tensor cores busy for 91 % of them.
 //
-// Roles in each CTA: two softmax warpgroups (one per tile), an MMA warp (the even
-// CTA's issues for both), a copy warp. Shared memory: the queries (2 x 48 KB, fp16,
+// Roles in each CTA: two softmax warpgroups and two MMA warps (one of each per tile;
+// the even CTA's issue for both CTAs, in turns), a copy warp. Issuing an MMA takes
+// nearly as long as its 64 clocks, so with one MMA warp for both tiles its waits and
+// commits stood between the MMAs (1690 clocks a step of 1280); without turns the two
+// tiles fall into step and the tensor cores idle during their softmax. Shared memory: the queries (2 x 48 KB, fp16,
 // 128-byte swizzle), three slots of half a key tile (64 keys x 192) and three of
 // half a value tile (128 keys x 64 values). Tensor memory: S at columns 0 and 128
 // (P over its first 64), O at 256 and 384.
@@ -320,17 +324,18 @@ constexpr int kKTile = 128, kSlots = 3;
 constexpr int kQRegion = 128 * 128, kQTileBytes = 3 * kQRegion;  // 128 rows x 64 values; a CTA's half of a query tile
 constexpr int kKRegion = 64 * 128, kKSlot = 3 * kKRegion;        // 64 keys x 64 values
 constexpr int kVSlot = kKTile * 128;                             // 128 keys x 64 values
-constexpr int kAtThreads = 384, kMmaWarp = 0, kCopyWarp = 1, kSoftWarp = 4;  // warps 2 and 3 only allot registers
+constexpr int kAtThreads = 384, kCopyWarp = 2, kSoftWarp = 4;  // MMA warps 0 and 1; warp 3 only allots registers
 // 168 registers a thread at launch (384 x 168 of the SM's 65536); the split below is no more
-constexpr int kSoftRegs = 208, kRoleRegs = 88;
+constexpr int kSoftRegs = 216, kRoleRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kRoleRegs <= kAtThreads * 168, "register split");
 constexpr float kShift = 7.f, kMoveBy = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kAtK = 2 * kQTileBytes, kAtV = kAtK + kSlots * kKSlot, kAtBars = kAtV + kSlots * kVSlot;
-// Barriers. The even CTA's: K and V landed (both halves' bytes), queries and P written (4 warps of each CTA).
-// Both CTAs' (MMA commits): K and V slots free, S and O written, all done.
-enum : int { B_KFULL = 0, B_VFULL = B_KFULL + kSlots, B_Q = B_VFULL + kSlots, B_P = B_Q + 2, B_KFREE = B_P + 2,
-             B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_DONE = B_O + 2, B_COUNT };
+// Barriers. The even CTA's: K and V landed (both halves' bytes), queries and the halves of P written (4 warps of
+// each CTA). Both CTAs' (MMA commits): K and V slots free (of both tiles), S and O written, all done.
+enum : int { B_KFULL = 0, B_VFULL = B_KFULL + kSlots, B_Q = B_VFULL + kSlots, B_P = B_Q + 2, B_KFREE = B_P + 4,
+             B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_DONE = B_O + 2,
+             B_TURN = B_DONE + 1, B_COUNT = B_TURN + 2 };  // and whose turn it is to issue
 constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
 constexpr int kAtSmem = kAtAbort + 4 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
 static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
@@ -355,6 +360,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Two scores to probabilities 2^(s sc + off): packed fp16, and their sum added to l.
+__device__ __forceinline__ uint32_t exp_pair(uint32_t s0, uint32_t s1, uint64_t sc2, uint64_t off2, uint64_t& l) {
+  float x0, x1;
+  unpack2(fma2(pack2(__uint_as_float(s0), __uint_as_float(s1)), sc2, off2), x0, x1);
+  x0 = ex2(x0);
+  x1 = ex2(x1);
+  l = add2(l, pack2(x0, x1));
+  return pack_f16(x0, x1);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -401,7 +422,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kAtAbort);
   auto bar = [&](int i) { return base + kAtBars + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q && i < B_KFREE ? 8u : 1u);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q && i < B_KFREE ? 8u : ((i >= B_KFREE && i < B_S) || i == B_DONE ? 2u : 1u));
     *abort_s = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -457,81 +478,71 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           drain_wait(bar(B_VFULL + i % kSlots), (i / kSlots) & 1);
         }
     }
-    if (warp == kMmaWarp && half == 0 && total > 0) {
-      // the whole warp walks the tiles (warp-uniform operands), one elected lane issues
+    if (warp < 2 && half == 0 && total > 0) {
+      // tile a: the whole warp walks the keys (warp-uniform operands), one elected lane issues
+      const int a = warp, mine = a == 0 ? nt[0] : nt[1];
       constexpr uint32_t idesc_s = tc_idesc_f16(256, kKTile, false, false);
       constexpr uint32_t idesc_o = tc_idesc_f16(256, kHeadV, false, true);
-      const uint64_t dq0 = tc_sdesc(base, 16, 1024, kSwizzle128B);
+      const uint64_t dq0 = tc_sdesc(base + a * kQTileBytes, 16, 1024, kSwizzle128B);
       const uint64_t dk0 = tc_sdesc(base + kAtK, 16, 1024, kSwizzle128B);
       // V as B: N = 64 values a CTA (one swizzle atom), K = keys in 8-row groups (SBO)
       const uint64_t dv0 = tc_sdesc(base + kAtV, kVSlot, 1024, kSwizzle128B);
-      auto scores = [&](int a, uint64_t dk) {
-        uint64_t dq = dq0 + a * (kQTileBytes >> 4);
+      const uint32_t s_col = tmem + 128 * a, o_col = tmem + 256 + 128 * a;
+      int s = 0;  // slot and parity of tile j
+      uint32_t ph = 0;
+      bool good = true;
 #pragma unroll 1
-        for (uint32_t r = 0; r < 3; ++r) {
+      for (int j = 0; j <= total; ++j) {
+        // O += P(j - 1) V(j - 1), then S(j) = Q K(j), in turn with the other tile's warp. Slots of keys that this
+        // tile does not see are freed as they land, not sooner: an arrival for the slot's next use would count for
+        // this one.
+        const int vs = s == 0 ? kSlots - 1 : s - 1;
+        const uint32_t vp = s == 0 ? ph ^ 1u : ph;
+        const bool pv = j > 0 && j <= mine, qk = j < mine;
+        if (j > 0) good = warp_wait(bar(B_VFULL + vs), vp, abort_s, err, kErrTimeoutFull);
+        if (j < total) good = good && warp_wait(bar(B_KFULL + s), ph, abort_s, err, kErrTimeoutFull);
+        if (j == 0 && qk) good = good && warp_wait_pair(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull);
+        if (a == 1 || j > 0) good = good && warp_wait(bar(B_TURN + a), (a == 1 ? j : j - 1) & 1, abort_s, err, kErrTimeoutFull);
+        if (pv) good = good && warp_wait(bar(B_P + 2 * a), (j - 1) & 1, abort_s, err, kErrTimeoutFull);
+        if (!good) break;
+        tc_fence_after();
+        if (pv) {
+          const uint64_t dv = dv0 + vs * (kVSlot >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc2_mma_warp(tmem + 128 * a, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_s, kk ? 1u : r);
-          dq += kQRegion >> 4;
-          dk += kKRegion >> 4;
-        }
-        tc2_commit_warp(bar(B_S + a));
-      };
-      // slots and parities of V(j) and K(j + 1)
-      int vs = 0, ks = 0;
-      uint32_t vp = 0, kp = 0;
-      const int nt0 = nt[0], nt1 = nt[1];
-      bool good = warp_wait(bar(B_KFULL), 0, abort_s, err, kErrTimeoutFull);
-#pragma unroll 1
-      for (int a = 0; a < 2; ++a) {
-        if (!good || (a == 0 ? nt0 : nt1) == 0) continue;
-        good = warp_wait_pair(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull);
-        if (!good) continue;
-        tc_fence_after();
-        scores(a, dk0);
-      }
-      if (good) tc2_commit_warp(bar(B_KFREE));
-#pragma unroll 1
-      for (int j = 0; j < total && good; ++j) {
-        if (++ks == kSlots) {
-          ks = 0;
-          kp ^= 1;
-        }
-        const uint64_t dk = dk0 + ks * (kKSlot >> 4);
-#pragma unroll 1
-        for (int a = 0; a < 2; ++a) {
-          const int mine = a == 0 ? nt0 : nt1;
-          if (!good || j >= mine) continue;
-          good = warp_wait(bar(B_VFULL + vs), vp, abort_s, err, kErrTimeoutFull) &&
-                 warp_wait(bar(B_P + a), j & 1, abort_s, err, kErrTimeoutFull);
-          if (!good) continue;
+            tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : j - 1);
+          good = warp_wait(bar(B_P + 2 * a + 1), (j - 1) & 1, abort_s, err, kErrTimeoutFull);
+          if (!good) break;
           tc_fence_after();
-          uint64_t dv = dv0 + vs * (kVSlot >> 4);
-          uint32_t pr = tmem + 128 * a;
-#pragma unroll 1
-          for (uint32_t k4 = 0; k4 < 2; ++k4) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc2_mma_tmem_a_warp(tmem + 256 + 128 * a, pr + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : (j | k4));
-            dv += (4 * 2048) >> 4;
-            pr += 32;
-          }
-          if (a == 1 || j >= nt1) tc2_commit_warp(bar(B_VFREE + vs));  // no other tile reads these values
-          if (j + 1 < mine) {
-            good = warp_wait(bar(B_KFULL + ks), kp, abort_s, err, kErrTimeoutFull);
-            if (!good) continue;
-            scores(a, dk);
-            if (a == 1 || j + 1 >= nt1) tc2_commit_warp(bar(B_KFREE + ks));
-          } else {
-            tc2_commit_warp(bar(B_O + a));
-          }
+          for (int kk = 4; kk < 8; ++kk)
+            tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1u);
         }
-        if (++vs == kSlots) {
-          vs = 0;
-          vp ^= 1;
+        const uint64_t dk = dk0 + s * (kKSlot >> 4);
+        auto scores = [&](int r) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc2_mma_warp(s_col, dq0 + ((r * kQRegion + kk * 32) >> 4), dk + ((r * kKRegion + kk * 32) >> 4), idesc_s,
+                         (r | kk) ? 1u : 0u);
+        };
+        if (qk) scores(0);
+        if (lane == 0) mbar_arrive(bar(B_TURN + 1 - a));  // early: the rest is issued before the other warp gets going
+        __syncwarp();
+        if (qk) {
+          scores(1);
+          scores(2);
+          tc2_commit_warp(bar(B_S + a));
+        }
+        if (j > 0) tc2_commit_warp(bar(B_VFREE + vs));
+        if (pv && j == mine) tc2_commit_warp(bar(B_O + a));
+        if (j < total) tc2_commit_warp(bar(B_KFREE + s));
+        if (++s == kSlots) {
+          s = 0;
+          ph ^= 1;
         }
       }
       tc2_commit_warp(bar(B_DONE));  // every MMA done before tensor memory is freed
+      __syncwarp();
       if (lane == 0) drain_wait(bar(B_DONE), 0);
     }
     __syncwarp();
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t quarter = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t s_col = tmem + quarter + 128 * a, o_col = tmem + quarter + 256 + 128 * a;
     const int row0 = i0 + 256 * a + 128 * half + 32 * wq;  // query row (of the sequence) of lane 0
-    const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + a), 0);
+    const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + 2 * a), 0);
     const int i = row0 + lane;
     float row_fac = 1.f;
     if (nt[a] > 0) {  // the warp's 32 queries to fp16, each brought to a largest value in [2^10, 2^11)
@@ -602,12 +613,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         for (int c = 0; c < 128; ++c)
           if (((w[c >> 5] >> (c & 31)) & 1u) == 0) s[c] = 0xff800000u;  // -inf
       }
+      // Optimistic: the first half's probabilities are formed with the running maximum as it stands, beside the search
+      // for this tile's; only if a row passed it by 2^8 (the first tile, and seldom after) are they formed again.
+      const uint64_t sc2 = pack2(sc, sc);
+      uint64_t off2 = pack2(kShift - m, kShift - m), l_new = 0;
+      uint32_t pk[32];
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      for (int k = 0; k < 32; ++k) {
+        pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
+        mx[k & 3] = max3(mx[k & 3], max3(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1]), __uint_as_float(s[4 * k + 2])),
+                         __uint_as_float(s[4 * k + 3]));
+      }
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
       const bool move = top > m + kMoveBy;
-      if (__any_sync(0xffffffffu, move)) {
+      if (__any_sync(0xffffffffu, move || m == -INFINITY)) {
         const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2(m - top));
         if (move) m = top;
         float lo, hi;
@@ -624,27 +644,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             tc_st16(o_col + 16 * c, o);
           }
         }
-      }
-      const float off = m == -INFINITY ? 0.f : kShift - m;
-      const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+        const float off = m == -INFINITY ? 0.f : kShift - m;
+        off2 = pack2(off, off);
+        l_new = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x0, x1;
-          unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), sc2, off2), x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          l2 = add2(l2, pack2(x0, x1));
-          pk[k] = pack_f16(x0, x1);
-        }
-        tc_st16(s_col + 16 * c, pk);
+        for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
       }
+      tc_st32(s_col, pk);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar);
+      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 0);  // half of the keys: the MMAs may start on it
+#pragma unroll
+      for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[64 + 2 * k], s[64 + 2 * k + 1], sc2, off2, l_new);
+      l2 = add2(l2, l_new);
+      tc_st32(s_col + 32, pk);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 1);
     }
     if (nt[a] > 0 && good) good = warp_wait(bar(B_O + a), 0, abort_s, err, kErrTimeoutFull);
     tc_fence_after();
