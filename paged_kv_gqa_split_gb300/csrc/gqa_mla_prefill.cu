@@ -214,82 +214,209 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 
 __device__ __forceinline__ uint32_t sw128(uint32_t base, int r, int c) { return base + r * 128 + ((c ^ (r & 7)) << 4); }
 
+// ------------------------------------------------------------------ waits
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Bounded wait that ignores the abort flag (draining before exit).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitNs) break;
+}
+
+// Whole warp: every lane waits (bounded; no lane runs apart from the others), every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs));
+}
+// The same for a barrier that both CTAs' threads arrive on.
+__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs) && mbar_try_wait_cluster(bar, parity));
+}
+
 // -------------------------------------------------------------- expansion
-// [128 packed rows x 512] x W[h]^T [512 x 128 columns] on mma.sync; column
-// block 0 gives the head's keys, 1 its values. Block column 2 of head 0 turns
-// the rotary keys into scaled fp16.
-constexpr int kExBM = 128, kExStage = (kExBM + 128) * 128;
-__global__ void __launch_bounds__(256) gqa_mla_prefill_expand_kernel(const MlaPrefillParams p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t sb = smem_addr(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp >> 2, wn = warp & 3;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kExBM;
-  if (m0 >= __ldg(p.kv_start + p.batch)) return;
-  const int part = blockIdx.y & 1, hp = blockIdx.y >> 1;
-  int ek, ev;
-  kv_exponents(p.amax, ek, ev);
-  if (hp >= p.heads) {  // the last block column: rotary keys, once (the first pass over the heads)
-    if (part != 0 || p.head0 != 0) return;
-    uint32_t* kr = static_cast<uint32_t*>(p.kr) + m0 * (kRope / 2);
-    const float f = pow2(-ek);
-    for (int i = tid; i < kExBM * kRope / 2; i += 256) {
-      const uint32_t v = kr[i];
-      kr[i] = pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
-    }
-    return;
+// Keys and values of `heads_each` heads for 256 packed rows, by a pair of CTAs: D [256
+// rows x 256 columns] = rows [256 x 512] W[h]^T, columns 0..127 the head's keys and
+// 128..255 its values (32 MMAs of M = 256, N = 256, K = 16, 128 clocks each). A CTA keeps
+// its 128 rows of the latents in shared memory (128 KB) for all its heads and streams its
+// half of the weights (the even CTA the key rows, the odd one the value rows) through four
+// slots of 64 of the 512 values. The accumulators of two heads fill tensor memory, so a
+// head's epilogue (scale, round to fp16, through shared memory and a tensor copy out) runs
+// beside the next head's MMAs. Bound by the MMAs where there are many rows; the weights are
+// read from L2 at 32 bytes a clock and SM.
+//
+// Roles in each CTA: an MMA warp (the even CTA's issues for both), a copy warp, a warp that
+// turns the rotary keys into scaled fp16 (once, with the first heads), four epilogue warps.
+constexpr int kExThreads = 256, kExSlots = 4, kExRegion = 128 * 128;
+constexpr int kExB = 8 * kExRegion, kExOut = kExB + kExSlots * kExRegion, kExBars = kExOut + 2 * kExRegion;
+enum : int { E_A = 0, E_BFULL = E_A + 8, E_BFREE = E_BFULL + kExSlots, E_DFULL = E_BFREE + kExSlots, E_DFREE = E_DFULL + 2,
+             E_DONE = E_DFREE + 2, E_COUNT };
+constexpr int kExSlot = kExBars + E_COUNT * 8, kExAbort = kExSlot + 4, kExSmem = kExAbort + 4 + 1024;
+static_assert(kExSmem <= 227 * 1024, "expansion exceeds shared memory");
+
+struct ExpandMaps {  // boxes of 64 values x 128 rows
+  CUtensorMap lat, w, kn, vv;
+};
+
+__global__ void __launch_bounds__(kExThreads, 1)
+    gqa_mla_prefill_expand_kernel(const MlaPrefillParams p, const __grid_constant__ ExpandMaps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  const int total = __ldg(p.kv_start + p.batch);
+  if (static_cast<int>(blockIdx.x >> 1) * 256 >= total) return;
+  const uint32_t half = cluster_rank();
+  const int m0 = static_cast<int>(blockIdx.x) * 128;  // this CTA's packed rows (may lie past the last one)
+  const int h0 = blockIdx.y * p.heads_each, nh = min(p.heads_each, p.heads - h0);
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kExAbort);
+  auto bar = [&](int i) { return base + kExBars + 8u * static_cast<uint32_t>(i); };
+  if (tid == 0) {
+    for (int i = 0; i < E_COUNT; ++i) mbar_init(bar(i), i >= E_DFREE && i < E_DONE ? 8u : 1u);
+    *abort_s = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
   }
-  const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.lat) + m0 * kLat;
-  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.w) + (static_cast<int64_t>(p.head0 + hp) * 256 + part * 128) * kLat;
-  auto load = [&](int ck) {
-    const uint32_t as = sb + (ck % 3) * kExStage, bs = as + kExBM * 128;
-    for (int i = tid; i < 128 * 8; i += 256) {
-      const int r = i >> 3, c = i & 7;
-      cp_async_16(sw128(as, r, c), a + static_cast<int64_t>(r) * kLat + ck * 64 + c * 8, 16u);
-      cp_async_16(sw128(bs, r, c), b + static_cast<int64_t>(r) * kLat + ck * 64 + c * 8, 16u);
+  if (warp == 3) tc2_alloc(base + kExSlot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the barriers and the tensor memory of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kExSlot);
+  int* err = p.err;
+
+  if (warp == 0) {
+    if (half == 0) {
+      constexpr uint32_t idesc = tc_idesc_bf16(256, 256, false, false);
+      const uint64_t da0 = tc_sdesc(base, 16, 1024, kSwizzle128B), db0 = tc_sdesc(base + kExB, 16, 1024, kSwizzle128B);
+      bool good = true;
+      int s = 0;
+      uint32_t ph = 0;
+#pragma unroll 1
+      for (int h = 0; h < nh && good; ++h) {
+        const uint32_t d = tmem + 256 * (h & 1);
+        if (h >= 2) good = warp_wait(bar(E_DFREE + (h & 1)), ((h >> 1) - 1) & 1, abort_s, err, kErrTimeoutEmpty);
+        tc_fence_after();
+#pragma unroll 1
+        for (uint32_t c = 0; c < 8 && good; ++c) {
+          if (h == 0) good = warp_wait(bar(E_A + c), 0, abort_s, err, kErrTimeoutFull);
+          good = good && warp_wait(bar(E_BFULL + s), ph, abort_s, err, kErrTimeoutFull);
+          if (!good) break;
+          const uint64_t da = da0 + c * (kExRegion >> 4), db = db0 + s * (kExRegion >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc2_mma_warp(d, da + ((kk * 32) >> 4), db + ((kk * 32) >> 4), idesc, kk ? 1u : c);
+          tc2_commit_warp(bar(E_BFREE + s));
+          if (++s == kExSlots) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (good) tc2_commit_warp(bar(E_DFULL + (h & 1)));
+      }
+      tc2_commit_warp(bar(E_DONE));
+      __syncwarp();
+      if (lane == 0) drain_wait(bar(E_DONE), 0);
     }
-  };
-  float acc[4][4][4] = {};
-  load(0);
-  cp_async_commit();
-  load(1);
-  cp_async_commit();
-  for (int ck = 0; ck < 8; ++ck) {
-    cp_async_wait<1>();
-    __syncthreads();
-    if (ck + 2 < 8) load(ck + 2);
-    cp_async_commit();
-    const uint32_t as = sb + (ck % 3) * kExStage, bs = as + kExBM * 128;
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t a_full = cluster_addr(bar(E_A), 0), b_full = cluster_addr(bar(E_BFULL), 0);
+      int u = 0;
+      bool good = true;
+      for (int h = 0; h < nh && good; ++h)
+        for (int c = 0; c < 8; ++c, ++u) {
+          const int s = u % kExSlots;
+          if (h == 0) {
+            if (half == 0) mbar_arrive_expect_tx(bar(E_A + c), 2 * kExRegion);
+            tma2_load_2d(base + c * kExRegion, &maps.lat, 64 * c, m0, a_full + 8 * c);
+          }
+          if (u >= kExSlots && !tc_wait(bar(E_BFREE + s), ((u / kExSlots) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kWaitNs)) {
+            good = false;
+            break;
+          }
+          if (half == 0) mbar_arrive_expect_tx(bar(E_BFULL + s), 2 * kExRegion);
+          tma2_load_2d(base + kExB + s * kExRegion, &maps.w, 64 * c, (p.head0 + h0 + h) * 256 + 128 * half, b_full + 8 * s);
+        }
+      if (half == 0) {  // no copy may still be writing either CTA's shared memory when the pair leaves
+        for (int i = u > kExSlots ? u - kExSlots : 0; i < u; ++i) drain_wait(bar(E_BFULL + i % kExSlots), (i / kExSlots) & 1);
+        for (int c = 0; c < min(u, 8); ++c) drain_wait(bar(E_A + c), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    if (p.head0 == 0 && blockIdx.y == 0 && m0 < total) {
+      int ek, ev;
+      kv_exponents(p.amax, ek, ev);
+      const float f = pow2(-ek);
+      uint4* kr = reinterpret_cast<uint4*>(p.kr) + static_cast<int64_t>(m0) * (kRope / 8);
+#pragma unroll 4
+      for (int i = lane; i < 128 * kRope / 8; i += 32) {
+        const uint4 v = kr[i];
+        auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+        kr[i] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+      }
+    }
+  } else if (warp >= 4) {
+    const int wq = warp & 3, row = 32 * wq + lane;
+    const bool out = m0 < total;
+    const bool bad = out && ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+    int ek, ev;
+    kv_exponents(p.amax, ek, ev);
+    const uint32_t dfree = cluster_addr(bar(E_DFREE), 0);
+    bool good = true;
+    int buf = 0;
+#pragma unroll 1
+    for (int h = 0; h < nh && good; ++h) {
+      good = warp_wait(bar(E_DFULL + (h & 1)), (h >> 1) & 1, abort_s, err, kErrTimeoutFull);
+      // the four warps agree, so that none is left at the barrier below
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+          : "=r"(buf)
+          : "r"(good ? 1 : 0)
+          : "memory");
+      good = buf != 0;
+      if (!good) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * (h & 1);
+#pragma unroll 1
+      for (int r = 0; r < 4; ++r) {  // 64 columns: keys 0..63, 64..127, values 0..63, 64..127
+        uint32_t v[64];
+        tc_ld32(d + 64 * r, v);
+        tc_ld32(d + 64 * r + 32, v + 32);
+        tc_wait_ld();
+        if (r == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(dfree + 8 * (h & 1));
+        }
+        const float f = pow2(r < 2 ? -ek : -ev);
+        const uint32_t dst = base + kExOut + (r & 1) * kExRegion;
+        if (warp == 4 && lane == 0) bulk_wait_read<1>();  // this buffer's last copy out has read it
+        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t af[4][4];
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[4];
 #pragma unroll
-      for (int mi = 0; mi < 4; ++mi)
-        ldsm_x4(sw128(as, (wm * 4 + mi) * 16 + (lane & 15), 2 * kk + (lane >> 4)), af[mi][0], af[mi][1], af[mi][2], af[mi][3]);
-#pragma unroll
-      for (int nj = 0; nj < 4; nj += 2) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(sw128(bs, wn * 32 + nj * 8 + ((lane >> 4) << 3) + (lane & 7), 2 * kk + ((lane >> 3) & 1)), b0, b1, b2, b3);
-#pragma unroll
-        for (int mi = 0; mi < 4; ++mi) {
-          mma_bf16_16816(acc[mi][nj], af[mi][0], af[mi][1], af[mi][2], af[mi][3], b0, b1);
-          mma_bf16_16816(acc[mi][nj + 1], af[mi][0], af[mi][1], af[mi][2], af[mi][3], b2, b3);
+          for (int e = 0; e < 4; ++e)
+            o[e] = bad ? (r < 2 ? 0x7fff7fffu : 0u)
+                       : pack_f16(__uint_as_float(v[8 * c + 2 * e]) * f, __uint_as_float(v[8 * c + 2 * e + 1]) * f);
+          st_shared_u4(sw128(dst, row, c), o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == 4 && lane == 0) {
+          if (out) tma_store_2d(r < 2 ? &maps.kn : &maps.vv, 64 * (r & 1), (h0 + h) * p.cap + m0, dst);
+          bulk_commit();
         }
       }
     }
+    if (warp == 4 && lane == 0) bulk_wait_read<0>();
+    __syncwarp();
   }
-  const float f = pow2(part == 0 ? -ek : -ev);
-  __half* o = static_cast<__half*>(part == 0 ? p.kn : p.vv) + (static_cast<int64_t>(hp) * p.cap + m0) * 128;
-#pragma unroll
-  for (int mi = 0; mi < 4; ++mi)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = (wm * 4 + mi) * 16 + (lane >> 2) + 8 * half;
-      const bool bad = ((__ldg(p.bad + (m0 >> 5) + (r >> 5)) >> (r & 31)) & 1u) != 0;
-#pragma unroll
-      for (int nj = 0; nj < 4; ++nj)
-        *reinterpret_cast<uint32_t*>(o + r * 128 + wn * 32 + nj * 8 + 2 * (lane & 3)) =
-            bad ? (part == 0 ? 0x7fff7fffu : 0u) : pack_f16(acc[mi][nj][2 * half] * f, acc[mi][nj][2 * half + 1] * f);
-    }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's arrivals, MMAs and copies are done too
+  if (warp == 3) tc2_dealloc(tmem, 512);
 }
 
 // -------------------------------------------------------------- attention
@@ -329,7 +456,6 @@ constexpr int kAtThreads = 384, kCopyWarp = 2, kSoftWarp = 4;  // MMA warps 0 an
 constexpr int kSoftRegs = 216, kRoleRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kRoleRegs <= kAtThreads * 168, "register split");
 constexpr float kShift = 7.f, kMoveBy = 8.f;
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kAtK = 2 * kQTileBytes, kAtV = kAtK + kSlots * kKSlot, kAtBars = kAtV + kSlots * kVSlot;
 // Barriers. The even CTA's: K and V landed (both halves' bytes), queries and the halves of P written (4 warps of
 // each CTA). Both CTAs' (MMA commits): K and V slots free (of both tiles), S and O written, all done.
@@ -377,22 +503,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// Bounded wait that ignores the abort flag (draining before exit).
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (global_timer_ns() - t0 > kWaitNs) break;
-}
-
-// Whole warp: every lane waits (bounded; no lane runs apart from the others), every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs));
-}
-// The same for a barrier that both CTAs' threads arrive on.
-__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs) && mbar_try_wait_cluster(bar, parity));
 }
 
 // Bits c of a word whose key 32 k + c (of the key tile at t0) is at most lim.
@@ -730,39 +840,76 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
   return at;
 }
 
+namespace {
+
+// Kernel over pairs of CTAs.
+template <typename... Args>
+cudaError_t launch_pairs(void (*fn)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// Heads a pair of the expansion takes: the count that ends first, a head being 4096 clocks of MMAs and a pair's start
+// (its latents and first weights) about as much.
+int expand_heads_each(int tiles, int heads, int pairs) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int each = 1; each <= heads; ++each) {
+    const int64_t waves = (static_cast<int64_t>(tiles) * ((heads + each - 1) / each) + pairs - 1) / pairs;
+    const int64_t cost = waves * (each + 1);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = each;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream) {
   gqa_mla_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p);
   gqa_mla_prefill_gather_kernel<<<sm_count * 8, 256, 0, stream>>>(p);
   static std::atomic<int> ex_done[kMaxDevices], at_done[kMaxDevices];
-  cudaError_t e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), 3 * kExStage);
+  cudaError_t e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), kExSmem);
   if (e != cudaSuccess) return e;
   e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel), kAtSmem);
   if (e != cudaSuccess) return e;
   const int64_t q_tiles = p.total_q / kQTile + p.batch;
   const int64_t group = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
+  const int tiles = (p.cap + 255) / 256;
   for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass) {
     p.head0 = h0;
     p.heads = p.num_heads - h0 < p.heads_per_pass ? p.num_heads - h0 : p.heads_per_pass;
     p.head_group = static_cast<int>(group < 1 ? 1 : (group > p.heads ? p.heads : group));
-    AttnMaps maps;
+    p.heads_each = expand_heads_each(tiles, p.heads, sm_count / 2);
+    ExpandMaps ex;
+    AttnMaps at;
     const int64_t rows = static_cast<int64_t>(p.heads) * p.cap;
-    if (!tc_encode_2d(&maps.kn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kn, kNope, rows, kNope * 2, 64, kKTile / 2) ||
-        !tc_encode_2d(&maps.vv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.vv, kHeadV, rows, kHeadV * 2, 64, kKTile) ||
-        !tc_encode_2d(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kr, kRope, p.cap, kRope * 2, 64, kKTile / 2))
+    constexpr CUtensorMapDataType kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kF = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (!tc_encode_2d(&ex.lat, kBf, p.lat, kLat, p.cap, kLat * 2, 64, 128) ||
+        !tc_encode_2d(&ex.w, kBf, p.w, kLat, static_cast<int64_t>(p.num_heads) * (kNope + kHeadV), kLat * 2, 64, 128) ||
+        !tc_encode_2d(&ex.kn, kF, p.kn, kNope, rows, kNope * 2, 64, 128) ||
+        !tc_encode_2d(&ex.vv, kF, p.vv, kHeadV, rows, kHeadV * 2, 64, 128) ||
+        !tc_encode_2d(&at.kn, kF, p.kn, kNope, rows, kNope * 2, 64, kKTile / 2) ||
+        !tc_encode_2d(&at.kr, kF, p.kr, kRope, p.cap, kRope * 2, 64, kKTile / 2))
       return cudaErrorInvalidValue;
-    gqa_mla_prefill_expand_kernel<<<dim3(p.cap / kExBM, 2 * p.heads + 1), 256, 3 * kExStage, stream>>>(p);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * q_tiles * p.heads));
-    cfg.blockDim = dim3(kAtThreads);
-    cfg.dynamicSmemBytes = kAtSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gqa_mla_prefill_attn_kernel, p, maps);
+    at.vv = ex.vv;  // the same boxes
+    const dim3 grid(2 * tiles, (p.heads + p.heads_each - 1) / p.heads_each);
+    e = launch_pairs(gqa_mla_prefill_expand_kernel, grid, kExThreads, kExSmem, stream, p, ex);
+    if (e != cudaSuccess) return e;
+    e = launch_pairs(gqa_mla_prefill_attn_kernel, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,
+                     stream, p, at);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
