@@ -42,65 +42,71 @@ constexpr int kLat = 512, kNope = 128, kRope = 64, kHeadV = 128, kRow = kLat + k
 constexpr int kAlign = 128;    // packed rows of a sequence start at a multiple of this
 constexpr int kQTile = 512;   // query rows a pair of CTAs takes
 constexpr int64_t kExpandBytes = int64_t{1} << 30;  // expanded keys and values of one pass over the heads
-constexpr int64_t kGroupBytes = int64_t{64} << 20;  // and of the heads whose CTAs run together (half of L2)
+constexpr int64_t kGroupBytes = int64_t{96} << 20;  // and of the heads whose CTAs run together (they stay in L2)
 
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
-// sums run over chunks of 1024 sequences.
+// sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps').
 __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPrefillParams p) {
-  __shared__ int64_t sk[1024];
-  __shared__ int sq[1024];
-  __shared__ int64_t base_k;
-  __shared__ int base_q;
-  const int tid = threadIdx.x;
+  __shared__ int64_t sk[32];
+  __shared__ int sq[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
   if (tid < 4) p.amax[tid] = 0;
-  if (tid == 0) {
-    base_k = 0;
-    base_q = 0;
-  }
+  int64_t base_k = 0;
+  int base_q = 0;
   const int64_t table = static_cast<int64_t>(p.width) * p.page_size;
   for (int b0 = 0; b0 < p.batch; b0 += 1024) {
     const int b = b0 + tid;
-    int len = 0, tiles = 0, qs = 0;
+    int len = 0, tiles = 0;
     if (b < p.batch) {
       // a malformed cu_q never makes a row out of range: entries are clamped to
       // [0, total_q], and a decreasing pair counts as an empty sequence
-      qs = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-      const int qe = min(max(__ldg(p.cu_q + b + 1), 0), p.total_q);
-      if (__ldg(p.cu_q + b + 1) < __ldg(p.cu_q + b) || __ldg(p.cu_q + b) < 0 || __ldg(p.cu_q + b + 1) > p.total_q)
-        atomicOr(p.err, kErrBadIndptr);
+      const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), n = __ldg(p.cache_seqlens + b);
+      const int qs = min(max(c0, 0), p.total_q), qe = min(max(c1, 0), p.total_q);
+      if (c1 < c0 || c0 < 0 || c1 > p.total_q) atomicOr(p.err, kErrBadIndptr);
       const int nq = max(qe - qs, 0);
       tiles = (nq + kQTile - 1) / kQTile;
-      if (nq > 0) len = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.cache_seqlens + b), 0)), table));
+      if (nq > 0) len = static_cast<int>(min(static_cast<int64_t>(max(n, 0)), table));
       p.q_start[2 * b] = qs;
       p.q_start[2 * b + 1] = nq;
     }
-    sk[tid] = (static_cast<int64_t>(len) + kAlign - 1) / kAlign * kAlign;
-    sq[tid] = tiles;
+    const int64_t rows = (static_cast<int64_t>(len) + kAlign - 1) / kAlign * kAlign;
+    int64_t k = rows;
+    int q = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t vk = __shfl_up_sync(0xffffffffu, k, o);
+      const int vq = __shfl_up_sync(0xffffffffu, q, o);
+      if (lane >= o) {
+        k += vk;
+        q += vq;
+      }
+    }
+    if (lane == 31) {
+      sk[warp] = k;
+      sq[warp] = q;
+    }
     __syncthreads();
-    for (int o = 1; o < 1024; o <<= 1) {
-      const int64_t vk = tid >= o ? sk[tid - o] : 0;
-      const int vq = tid >= o ? sq[tid - o] : 0;
-      __syncthreads();
-      sk[tid] += vk;
-      sq[tid] += vq;
-      __syncthreads();
+    int64_t before_k = base_k;
+    int before_q = base_q;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) {
+        before_k += sk[w];
+        before_q += sq[w];
+      }
+      base_k += sk[w];
+      base_q += sq[w];
     }
     if (b < p.batch) {
-      const int64_t end = base_k + sk[tid];
-      const int64_t start = end - (static_cast<int64_t>(len) + kAlign - 1) / kAlign * kAlign;
+      const int64_t end = before_k + k;
       if (end > p.cap) {  // more tokens than the caller's bound: these sequences see no key
         atomicOr(p.err, kErrKvBound);
         len = 0;
       }
       p.kv_len[b] = len;
-      p.kv_start[b] = static_cast<int>(min(start, static_cast<int64_t>(p.cap)));
-      p.qt_start[b] = base_q + sq[tid] - tiles;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      base_k += sk[1023];
-      base_q += sq[1023];
+      p.kv_start[b] = static_cast<int>(min(end - rows, static_cast<int64_t>(p.cap)));
+      p.qt_start[b] = before_q + q - tiles;
     }
     __syncthreads();
   }
@@ -115,7 +121,7 @@ __device__ __forceinline__ int find_seq(const int* start, int batch, int x) {
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(start + mid) <= x) lo = mid; else hi = mid;
+    if (__ldcg(start + mid) <= x) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -138,58 +144,62 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
 }
 
 // ----------------------------------------------------------------- gather
-// A warp per packed row (rows [0, cap) in turn, 32 rows a block), then a warp
-// per weight row.
+// A block per 32 packed rows, four rows a warp with all their loads in flight; before that, and before the
+// plan's results are needed, a warp per weight row for the maxima.
 __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPrefillParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int total = __ldg(p.kv_start + p.batch);
-  const int groups = total / 32;  // 32 packed rows share a word of valid bits and a sequence
   unsigned top_c = 0, top_r = 0, top_k = 0, top_v = 0;
-  __shared__ unsigned bad_s;
-  for (int g = blockIdx.x; g < groups; g += gridDim.x) {
-    if (threadIdx.x == 0) bad_s = 0;
-    __syncthreads();
-    // the last sequence that starts at or before the row (empty ones start where the next does)
-    const int b = find_seq(p.kv_start, p.batch, 32 * g);
-    const int t0 = 32 * g - __ldg(p.kv_start + b), n = __ldg(p.kv_len + b);
-    if (warp == 0) {
-      const int t = t0 + lane;
-      bool ok = false;
-      if (t < n) {
-        const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.width + t / p.page_size);
-        ok = blk >= 0 && blk < p.num_blocks;
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) p.valid[g] = m;
-    }
-    for (int i = warp; i < 32; i += 8) {
-      const int t = t0 + i;
-      const uint4* src = nullptr;
-      if (t < n) {
-        const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.width + t / p.page_size);
-        if (blk >= 0 && blk < p.num_blocks)
-          src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv) +
-                                               (static_cast<int64_t>(blk) * p.page_size + t % p.page_size) * kRow);
-      }
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      const uint4 a = src ? __ldg(src + lane) : zero, c = src ? __ldg(src + 32 + lane) : zero;
-      const uint4 r = src && lane < 8 ? __ldg(src + 64 + lane) : zero;
-      uint4* lat = reinterpret_cast<uint4*>(p.lat) + static_cast<int64_t>(32 * g + i) * (kLat / 8);
-      lat[lane] = a;
-      lat[32 + lane] = c;
-      if (lane < 8) reinterpret_cast<uint4*>(p.kr)[static_cast<int64_t>(32 * g + i) * (kRope / 8) + lane] = r;
-      top_c = finite_bits(c, finite_bits(a, top_c));
-      top_r = finite_bits(r, top_r);
-      if (__any_sync(0xffffffffu, not_finite(a) || not_finite(c)) && lane == 0) atomicOr(&bad_s, 1u << i);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) p.bad[g] = bad_s;
-  }
+  __shared__ unsigned bad_s[8];
+  pdl_launch_dependents();
   const int wrows = p.num_heads * (kNope + kHeadV);
+#pragma unroll 4
   for (int r = blockIdx.x * 8 + warp; r < wrows; r += gridDim.x * 8) {
     const uint4* src = reinterpret_cast<const uint4*>(p.w) + static_cast<int64_t>(r) * (kLat / 8);
     const unsigned t = finite_bits(__ldg(src + 32 + lane), finite_bits(__ldg(src + lane), 0));
     if ((r & 255) < kNope) top_k = max(top_k, t); else top_v = max(top_v, t);
+  }
+  pdl_wait();
+  const int groups = __ldg(p.kv_start + p.batch) / 32;  // 32 packed rows share a word of valid bits and a sequence
+  for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+    // the last sequence that starts at or before the row (empty ones start where the next does)
+    const int b = find_seq(p.kv_start, p.batch, 32 * g);
+    const int t0 = 32 * g - __ldg(p.kv_start + b), n = __ldg(p.kv_len + b);
+    // lane l looks up row l's slot
+    int64_t slot = -1;
+    if (t0 + lane < n) {
+      const int t = t0 + lane, blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.width + t / p.page_size);
+      if (blk >= 0 && blk < p.num_blocks) slot = static_cast<int64_t>(blk) * p.page_size + t % p.page_size;
+    }
+    const unsigned ok = __ballot_sync(0xffffffffu, slot >= 0);
+    uint4 v[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t from = __shfl_sync(0xffffffffu, slot, 4 * warp + i);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv) + from * kRow);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      v[i][0] = from >= 0 ? __ldg(src + lane) : zero;
+      v[i][1] = from >= 0 ? __ldg(src + 32 + lane) : zero;
+      v[i][2] = from >= 0 && lane < 8 ? __ldg(src + 64 + lane) : zero;
+    }
+    unsigned bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = 32 * g + 4 * warp + i;
+      uint4* lat = reinterpret_cast<uint4*>(p.lat) + row * (kLat / 8);
+      lat[lane] = v[i][0];
+      lat[32 + lane] = v[i][1];
+      if (lane < 8) reinterpret_cast<uint4*>(p.kr)[row * (kRope / 8) + lane] = v[i][2];
+      top_c = finite_bits(v[i][1], finite_bits(v[i][0], top_c));
+      top_r = finite_bits(v[i][2], top_r);
+      if (__any_sync(0xffffffffu, not_finite(v[i][0]) || not_finite(v[i][1]))) bad |= 1u << (4 * warp + i);
+    }
+    if (lane == 0) bad_s[warp] = bad;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      p.valid[g] = ok;
+      p.bad[g] = bad_s[0] | bad_s[1] | bad_s[2] | bad_s[3] | bad_s[4] | bad_s[5] | bad_s[6] | bad_s[7];
+    }
+    __syncthreads();
   }
   const unsigned top[4] = {top_c, top_r, top_k, top_v};
 #pragma unroll
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
 // |c . w| <= 512 max|c| max|w| < 2^(Ec + 1 + Ew + 1 + 9), to be below 2^15.
 __device__ __forceinline__ int exponent_of(unsigned bits) { return static_cast<int>(bits >> 23) - 127; }
 __device__ __forceinline__ void kv_exponents(const unsigned* amax, int& ek, int& ev) {
-  const unsigned c = __ldg(amax), r = __ldg(amax + 1), wk = __ldg(amax + 2), wv = __ldg(amax + 3);
+  const unsigned c = __ldcg(amax), r = __ldcg(amax + 1), wk = __ldcg(amax + 2), wv = __ldcg(amax + 3);
   ek = r != 0 ? exponent_of(r) + 1 - 15 : -126;
   if (c != 0 && wk != 0) ek = max(ek, exponent_of(c) + exponent_of(wk) + 11 - 15);
   ev = c != 0 && wv != 0 ? exponent_of(c) + exponent_of(wv) + 11 - 15 : 0;
@@ -245,8 +255,9 @@ __device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, vo
 // read from L2 at 32 bytes a clock and SM.
 //
 // Roles in each CTA: an MMA warp (the even CTA's issues for both), a copy warp, a warp that
-// turns the rotary keys into scaled fp16 (once, with the first heads), four epilogue warps.
-constexpr int kExThreads = 256, kExSlots = 4, kExRegion = 128 * 128;
+// turns the rotary keys into scaled fp16 (once, with the first heads), two epilogue
+// warpgroups (keys and values; one for both took 5700 clocks a head).
+constexpr int kExThreads = 384, kExSlots = 4, kExRegion = 128 * 128;
 constexpr int kExB = 8 * kExRegion, kExOut = kExB + kExSlots * kExRegion, kExBars = kExOut + 2 * kExRegion;
 enum : int { E_A = 0, E_BFULL = E_A + 8, E_BFREE = E_BFULL + kExSlots, E_DFULL = E_BFREE + kExSlots, E_DFREE = E_DFULL + 2,
              E_DONE = E_DFREE + 2, E_COUNT };
@@ -260,6 +271,8 @@ struct ExpandMaps {  // boxes of 64 values x 128 rows
 __global__ void __launch_bounds__(kExThreads, 1)
     gqa_mla_prefill_expand_kernel(const MlaPrefillParams p, const __grid_constant__ ExpandMaps maps) {
   extern __shared__ uint8_t smem_raw[];
+  pdl_wait();
+  pdl_launch_dependents();  // after the wait: what the next kernel reads before its own is then complete
   const int total = __ldg(p.kv_start + p.batch);
   if (static_cast<int>(blockIdx.x >> 1) * 256 >= total) return;
   const uint32_t half = cluster_rank();
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kExAbort);
   auto bar = [&](int i) { return base + kExBars + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < E_COUNT; ++i) mbar_init(bar(i), i >= E_DFREE && i < E_DONE ? 8u : 1u);
+    for (int i = 0; i < E_COUNT; ++i) mbar_init(bar(i), i >= E_DFREE && i < E_DONE ? 16u : 1u);
     *abort_s = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -357,60 +370,58 @@ __global__ void __launch_bounds__(kExThreads, 1)
       }
     }
   } else if (warp >= 4) {
+    const int part = (warp >> 2) - 1;  // 0: keys, 1: values
     const int wq = warp & 3, row = 32 * wq + lane;
-    const bool out = m0 < total;
+    const bool out = m0 < total, first = wq == 0 && lane == 0;
     const bool bad = out && ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
     int ek, ev;
     kv_exponents(p.amax, ek, ev);
+    const float f = pow2(part == 0 ? -ek : -ev);
+    const uint32_t of_bad = part == 0 ? 0x7fff7fffu : 0u;
     const uint32_t dfree = cluster_addr(bar(E_DFREE), 0);
-    bool good = true;
-    int buf = 0;
+    const uint32_t dst = base + kExOut + part * kExRegion;
 #pragma unroll 1
-    for (int h = 0; h < nh && good; ++h) {
-      good = warp_wait(bar(E_DFULL + (h & 1)), (h >> 1) & 1, abort_s, err, kErrTimeoutFull);
-      // the four warps agree, so that none is left at the barrier below
+    for (int h = 0; h < nh; ++h) {
+      const bool good = warp_wait(bar(E_DFULL + (h & 1)), (h >> 1) & 1, abort_s, err, kErrTimeoutFull);
+      int all;  // the four warps agree, so that none is left at the barriers below
       asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-          : "=r"(buf)
-          : "r"(good ? 1 : 0)
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+          : "=r"(all)
+          : "r"(good ? 1 : 0), "r"(1 + part)
           : "memory");
-      good = buf != 0;
-      if (!good) break;
+      if (!all) break;
       tc_fence_after();
-      const uint32_t d = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * (h & 1);
+      const uint32_t d = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * (h & 1) + 128 * part;
 #pragma unroll 1
-      for (int r = 0; r < 4; ++r) {  // 64 columns: keys 0..63, 64..127, values 0..63, 64..127
+      for (int r = 0; r < 2; ++r) {  // 64 columns
         uint32_t v[64];
         tc_ld32(d + 64 * r, v);
         tc_ld32(d + 64 * r + 32, v + 32);
         tc_wait_ld();
-        if (r == 3) {
+        if (r == 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(dfree + 8 * (h & 1));
         }
-        const float f = pow2(r < 2 ? -ek : -ev);
-        const uint32_t dst = base + kExOut + (r & 1) * kExRegion;
-        if (warp == 4 && lane == 0) bulk_wait_read<1>();  // this buffer's last copy out has read it
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (first) bulk_wait_read<0>();  // the last copy out has read the buffer
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = bad ? (r < 2 ? 0x7fff7fffu : 0u)
-                       : pack_f16(__uint_as_float(v[8 * c + 2 * e]) * f, __uint_as_float(v[8 * c + 2 * e + 1]) * f);
+            o[e] = bad ? of_bad : pack_f16(__uint_as_float(v[8 * c + 2 * e]) * f, __uint_as_float(v[8 * c + 2 * e + 1]) * f);
           st_shared_u4(sw128(dst, row, c), o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (warp == 4 && lane == 0) {
-          if (out) tma_store_2d(r < 2 ? &maps.kn : &maps.vv, 64 * (r & 1), (h0 + h) * p.cap + m0, dst);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+        if (first && out) {
+          tma_store_2d(part == 0 ? &maps.kn : &maps.vv, 64 * r, (h0 + h) * p.cap + m0, dst);
           bulk_commit();
         }
       }
     }
-    if (warp == 4 && lane == 0) bulk_wait_read<0>();
+    if (first) bulk_wait_read<0>();
     __syncwarp();
   }
   tc_fence_before();
@@ -516,10 +527,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // CTAs in order: groups of heads whose keys and values stay in L2 together,
   // within a group the last query tiles (the most keys, if causal) first
-  const int tiles = __ldg(p.qt_start + p.batch);
+  // What the plan and the gather wrote is complete when this kernel may start (the expansion lets it start after its
+  // own wait); only the copies of keys and values wait for the expansion. Read past L1, which an earlier call's
+  // values of the same workspace may still be in.
+  const int tiles = __ldcg(p.qt_start + p.batch);
   const uint32_t half = cluster_rank();  // which 128 rows of a tile, which half of the keys and values
   const int64_t rank = blockIdx.x >> 1;
-  if (rank >= static_cast<int64_t>(tiles) * p.heads) return;
+  if (rank >= static_cast<int64_t>(tiles) * p.heads) {
+    pdl_wait();
+    return;
+  }
   const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
   const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
   const int gh = min(p.head_group, p.heads - group * p.head_group);
@@ -545,9 +562,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kAtSlot);
 
   const int b = find_seq(p.qt_start, p.batch, qt);
-  const int nq = __ldg(p.q_start + 2 * b + 1), i0 = (qt - __ldg(p.qt_start + b)) * kQTile;
-  const int64_t q0 = __ldg(p.q_start + 2 * b);
-  const int n = __ldg(p.kv_len + b), kv0 = __ldg(p.kv_start + b);
+  const int2 qs = __ldcg(reinterpret_cast<const int2*>(p.q_start) + b);
+  const int n = __ldcg(p.kv_len + b), kv0 = __ldcg(p.kv_start + b), i0 = (qt - __ldcg(p.qt_start + b)) * kQTile;
+  const int nq = qs.y;
+  const int64_t q0 = qs.x;
   int* err = p.err;
   // key tiles of each query tile (the same in both CTAs): up to the last key that its last row sees
   int nt[2];
@@ -562,6 +580,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   if (warp < kSoftWarp) {
     setmaxnreg_dec<kRoleRegs>();
+    if (warp == kCopyWarp) pdl_wait();
     if (warp == kCopyWarp && lane == 0) {
       const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
       const uint32_t kfull = cluster_addr(bar(B_KFULL), 0), vfull = cluster_addr(bar(B_VFULL), 0);
@@ -666,35 +685,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + 2 * a), 0);
     const int i = row0 + lane;
     float row_fac = 1.f;
-    if (nt[a] > 0) {  // the warp's 32 queries to fp16, each brought to a largest value in [2^10, 2^11)
-      const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
-      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + h * p.q_head_stride;
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += 8) {
-        uint32_t v[8][3];
+    if (nt[a] > 0) {  // this row's query to fp16, its largest value in [2^10, 2^11)
+      uint4 v[24];
+      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (q0 + i) * p.q_token_stride +
+                                                       h * p.q_head_stride);
+      unsigned top = 0;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+      for (int k = 0; k < 24; ++k) v[k] = i < nq ? __ldg(qp + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
-            v[r][k] = row0 + r0 + r < nq ? __ldg(reinterpret_cast<const uint32_t*>(qp + (q0 + row0 + r0 + r) * p.q_token_stride) +
-                                                 32 * k + lane)
-                                         : 0u;
+      for (int k = 0; k < 24; ++k) top = finite_bits(v[k], top);
+      const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
+      row_fac = pow2(e);
+      const float f = p.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
+      auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const unsigned top = __reduce_max_sync(0xffffffffu, finite_bits2(v[r][0], finite_bits2(v[r][1], finite_bits2(v[r][2], 0u))));
-          const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
-          if (lane == r0 + r) row_fac = pow2(e);
-          const float f = sign * pow2(-e);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t h2 = pack_f16(__uint_as_float(v[r][k] << 16) * f, __uint_as_float(v[r][k] & 0xffff0000u) * f);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw128(base + a * kQTileBytes + k * kQRegion, 32 * wq + r0 + r, lane >> 2) +
-                                                        (lane & 3) * 4),
-                         "r"(h2)
-                         : "memory");
-          }
-        }
-      }
+      for (int k = 0; k < 24; ++k)
+        st_shared_u4(sw128(base + a * kQTileBytes + (k >> 3) * kQRegion, 32 * wq + lane, k & 7), half2(v[k].x), half2(v[k].y),
+                     half2(v[k].z), half2(v[k].w));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(q_bar);
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     uint64_t l2 = 0;
     bool good = true;
     for (int j = 0; j < nt[a] && good; ++j) {
-      const uint4 vw = __ldg(reinterpret_cast<const uint4*>(p.valid) + (kv0 >> 7) + j);
+      const uint4 vw = __ldcg(reinterpret_cast<const uint4*>(p.valid) + (kv0 >> 7) + j);
       good = warp_wait(bar(B_S + a), j & 1, abort_s, err, kErrTimeoutFull);
       if (!good) break;
       tc_fence_after();
@@ -842,20 +849,23 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
 
 namespace {
 
-// Kernel over pairs of CTAs.
+// Kernel that may start while the one before it ends (it waits for that one itself), over clusters of `cluster` CTAs.
 template <typename... Args>
-cudaError_t launch_pairs(void (*fn)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+cudaError_t launch_next(void (*fn)(Args...), int cluster, dim3 grid, int threads, int smem, cudaStream_t stream,
+                        Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
@@ -879,19 +889,23 @@ int expand_heads_each(int tiles, int heads, int pairs) {
 
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream) {
   gqa_mla_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p);
-  gqa_mla_prefill_gather_kernel<<<sm_count * 8, 256, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_next(gqa_mla_prefill_gather_kernel, 1, dim3(sm_count * 8), 256, 0, stream, p);
+  if (e != cudaSuccess) return e;
   static std::atomic<int> ex_done[kMaxDevices], at_done[kMaxDevices];
-  cudaError_t e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), kExSmem);
+  e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), kExSmem);
   if (e != cudaSuccess) return e;
   e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel), kAtSmem);
   if (e != cudaSuccess) return e;
   const int64_t q_tiles = p.total_q / kQTile + p.batch;
-  const int64_t group = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
+  const int64_t fit = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
   const int tiles = (p.cap + 255) / 256;
   for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass) {
     p.head0 = h0;
     p.heads = p.num_heads - h0 < p.heads_per_pass ? p.num_heads - h0 : p.heads_per_pass;
-    p.head_group = static_cast<int>(group < 1 ? 1 : (group > p.heads ? p.heads : group));
+    const int groups = static_cast<int>(fit < 1 ? p.heads : (p.heads + fit - 1) / fit);
+    p.head_group = (p.heads + groups - 1) / groups;
     p.heads_each = expand_heads_each(tiles, p.heads, sm_count / 2);
     ExpandMaps ex;
     AttnMaps at;
@@ -906,9 +920,9 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
       return cudaErrorInvalidValue;
     at.vv = ex.vv;  // the same boxes
     const dim3 grid(2 * tiles, (p.heads + p.heads_each - 1) / p.heads_each);
-    e = launch_pairs(gqa_mla_prefill_expand_kernel, grid, kExThreads, kExSmem, stream, p, ex);
+    e = launch_next(gqa_mla_prefill_expand_kernel, 2, grid, kExThreads, kExSmem, stream, p, ex);
     if (e != cudaSuccess) return e;
-    e = launch_pairs(gqa_mla_prefill_attn_kernel, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,
+    e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,
                      stream, p, at);
     if (e != cudaSuccess) return e;
   }
