@@ -278,6 +278,11 @@ __global__ void __launch_bounds__(kExThreads, 1)
   const uint32_t half = cluster_rank();
   const int m0 = static_cast<int>(blockIdx.x) * 128;  // this CTA's packed rows (may lie past the last one)
   const int h0 = blockIdx.y * p.heads_each, nh = min(p.heads_each, p.heads - h0);
+  // pairs start at different heads, so that they do not all read the same weights at once
+  auto head = [&](int h) {
+    const int r = h + static_cast<int>(blockIdx.x >> 1) % nh;
+    return h0 + (r < nh ? r : r - nh);
+  };
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -332,28 +337,31 @@ __global__ void __launch_bounds__(kExThreads, 1)
       if (lane == 0) drain_wait(bar(E_DONE), 0);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t a_full = cluster_addr(bar(E_A), 0), b_full = cluster_addr(bar(E_BFULL), 0);
-      int u = 0;
-      bool good = true;
-      for (int h = 0; h < nh && good; ++h)
-        for (int c = 0; c < 8; ++c, ++u) {
-          const int s = u % kExSlots;
-          if (h == 0) {
-            if (half == 0) mbar_arrive_expect_tx(bar(E_A + c), 2 * kExRegion);
-            tma2_load_2d(base + c * kExRegion, &maps.lat, 64 * c, m0, a_full + 8 * c);
-          }
-          if (u >= kExSlots && !tc_wait(bar(E_BFREE + s), ((u / kExSlots) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kWaitNs)) {
-            good = false;
-            break;
-          }
-          if (half == 0) mbar_arrive_expect_tx(bar(E_BFULL + s), 2 * kExRegion);
-          tma2_load_2d(base + kExB + s * kExRegion, &maps.w, 64 * c, (p.head0 + h0 + h) * 256 + 128 * half, b_full + 8 * s);
+    const uint32_t a_full = cluster_addr(bar(E_A), 0), b_full = cluster_addr(bar(E_BFULL), 0);
+    const uint32_t expect = half == 0 ? 2 * kExRegion : 0;
+    const int y0 = p.head0 * 256 + 128 * half;
+    int s = 0, u = 0;
+    uint32_t ph = 1;  // parity of the slot's previous release
+    bool good = true;
+#pragma unroll 1
+    for (int h = 0; h < nh && good; ++h) {
+      const int y = y0 + head(h) * 256;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c, ++u) {
+        if (h == 0)
+          tma2_load_2d_warp(base + c * kExRegion, &maps.lat, 64 * c, m0, bar(E_A + c), expect, a_full + 8 * c);
+        if (u >= kExSlots) good = warp_wait(bar(E_BFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
+        if (!good) break;
+        tma2_load_2d_warp(base + kExB + s * kExRegion, &maps.w, 64 * c, y, bar(E_BFULL + s), expect, b_full + 8 * s);
+        if (++s == kExSlots) {
+          s = 0;
+          ph ^= 1;
         }
-      if (half == 0) {  // no copy may still be writing either CTA's shared memory when the pair leaves
-        for (int i = u > kExSlots ? u - kExSlots : 0; i < u; ++i) drain_wait(bar(E_BFULL + i % kExSlots), (i / kExSlots) & 1);
-        for (int c = 0; c < min(u, 8); ++c) drain_wait(bar(E_A + c), 0);
       }
+    }
+    if (half == 0 && lane == 0) {  // no copy may still be writing either CTA's shared memory when the pair leaves
+      for (int i = u > kExSlots ? u - kExSlots : 0; i < u; ++i) drain_wait(bar(E_BFULL + i % kExSlots), (i / kExSlots) & 1);
+      for (int c = 0; c < min(u, 8); ++c) drain_wait(bar(E_A + c), 0);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         fence_proxy_async_smem();
         asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
         if (first && out) {
-          tma_store_2d(part == 0 ? &maps.kn : &maps.vv, 64 * r, (h0 + h) * p.cap + m0, dst);
+          tma_store_2d(part == 0 ? &maps.kn : &maps.vv, 64 * r, head(h) * p.cap + m0, dst);
           bulk_commit();
         }
       }
@@ -580,32 +588,33 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   if (warp < kSoftWarp) {
     setmaxnreg_dec<kRoleRegs>();
-    if (warp == kCopyWarp) pdl_wait();
-    if (warp == kCopyWarp && lane == 0) {
+    if (warp == kCopyWarp) {
+      pdl_wait();
       const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
       const uint32_t kfull = cluster_addr(bar(B_KFULL), 0), vfull = cluster_addr(bar(B_VFULL), 0);
+      const uint32_t k_bytes = half == 0 ? 2 * kKSlot : 0, v_bytes = half == 0 ? 2 * kVSlot : 0;
       int j = 0, s = 0;
       uint32_t ph = 1;  // parity of the slot's previous release
+#pragma unroll 1
       for (; j < total; ++j) {
         const uint32_t kd = base + kAtK + s * kKSlot, vd = base + kAtV + s * kVSlot;
-        if (j >= kSlots && !tc_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty, kWaitNs)) break;
-        if (half == 0) mbar_arrive_expect_tx(bar(B_KFULL + s), 2 * kKSlot);
-        tma2_load_2d(kd, &maps.kn, 0, y0 + j * kKTile, kfull + 8 * s);
-        tma2_load_2d(kd + kKRegion, &maps.kn, 64, y0 + j * kKTile, kfull + 8 * s);
-        tma2_load_2d(kd + 2 * kKRegion, &maps.kr, 0, r0 + j * kKTile, kfull + 8 * s);
-        if (j >= kSlots && !tc_wait(bar(B_VFREE + s), ph, abort_s, err, kErrTimeoutEmpty, kWaitNs)) break;
-        if (half == 0) mbar_arrive_expect_tx(bar(B_VFULL + s), 2 * kVSlot);
-        tma2_load_2d(vd, &maps.vv, 64 * half, v0 + j * kKTile, vfull + 8 * s);
+        if (j >= kSlots && !warp_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty)) break;
+        tma2_load_2d_warp(kd, &maps.kn, 0, y0 + j * kKTile, bar(B_KFULL + s), k_bytes, kfull + 8 * s);
+        tma2_load_2d_warp(kd + kKRegion, &maps.kn, 64, y0 + j * kKTile, 0, 0, kfull + 8 * s);
+        tma2_load_2d_warp(kd + 2 * kKRegion, &maps.kr, 0, r0 + j * kKTile, 0, 0, kfull + 8 * s);
+        if (j >= kSlots && !warp_wait(bar(B_VFREE + s), ph, abort_s, err, kErrTimeoutEmpty)) break;
+        tma2_load_2d_warp(vd, &maps.vv, 64 * half, v0 + j * kKTile, bar(B_VFULL + s), v_bytes, vfull + 8 * s);
         if (++s == kSlots) {
           s = 0;
           ph ^= 1;
         }
       }
-      if (half == 0)  // no copy may still be writing either CTA's shared memory when the pair leaves
+      if (half == 0 && lane == 0)  // no copy may still be writing either CTA's shared memory when the pair leaves
         for (int i = max(0, j - kSlots); i < j; ++i) {
           drain_wait(bar(B_KFULL + i % kSlots), (i / kSlots) & 1);
           drain_wait(bar(B_VFULL + i % kSlots), (i / kSlots) & 1);
         }
+      __syncwarp();
     }
     if (warp < 2 && half == 0 && total > 0) {
       // tile a: the whole warp walks the keys (warp-uniform operands), one elected lane issues

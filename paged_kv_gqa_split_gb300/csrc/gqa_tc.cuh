@@ -227,12 +227,16 @@ __device__ __forceinline__ void tc2_commit_warp(uint32_t bar) {
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
       : "memory");
 }
-// 2D tensor copy into this CTA's shared memory, counted on an mbarrier of either CTA (a cluster_addr).
-__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+// Whole warp: one elected lane announces `expect` bytes (0: none) on its own barrier `bar`, then copies a 2D box into
+// this CTA's shared memory, counted on `full`, an mbarrier of either CTA (a cluster_addr).
+__device__ __forceinline__ void tma2_load_2d_warp(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                  uint32_t expect, uint32_t full) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "{\n\t.reg .pred e, q;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.and.u32 q, %1, 0, e;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%3, {%4, %5}], [%6];\n\t}" ::
+          "r"(bar),
+      "r"(expect), "r"(dst), "l"(map), "r"(x), "r"(y), "r"(full)
       : "memory");
 }
 
