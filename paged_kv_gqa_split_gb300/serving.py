@@ -28,16 +28,17 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 def _check(device, dtype, contiguous, **tensors):
     """Each tensor (None is skipped): on the GPU `device`, of `dtype` (None: any) and, if asked, contiguous."""
+    index = device.index
     for name, t in tensors.items():
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} is on {t.device}: the CUDA library has no CPU path; move inputs to the GPU")
-        if t.device != device:
+        if t.get_device() != index or index is None:  # a CPU tensor's is -1
+            if not t.is_cuda:
+                raise ValueError(f"{name} is on {t.device}: the CUDA library has no CPU path; move inputs to the GPU")
             raise ValueError(f"all tensors must be on {device}; {name} is on {t.device}")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}")
         if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -63,23 +64,28 @@ def _rotation(device, n, positions, inv_freq, pairs=None):
         raise ValueError("a rotation needs positions")
     _check(device, torch.int32, True, positions=positions)
     _check(device, torch.float64, True, inv_freq=inv_freq)
-    if positions.shape != (n,):
+    if positions.dim() != 1 or positions.shape[0] != n:
         raise ValueError(f"positions must be [{n}]")
     if inv_freq.dim() != 1 or inv_freq.shape[0] < 1 or (pairs is not None and inv_freq.shape[0] != pairs):
         raise ValueError(f"inv_freq must be [{'pairs' if pairs is None else pairs}]")
     return positions.data_ptr(), inv_freq.data_ptr()
 
 
+_entries = {}  # C entry points already looked up
+
+
 def _call(name, device, stream, made, *args):
     """Calls the C entry on `stream` (default: the device's current stream) and raises on an error code;
     `made`: tensors allocated here, kept from reuse until another stream is done with them."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load(), name)
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() without building a Stream
     else:
         handle = stream.cuda_stream
         for t in made:
             t.record_stream(stream)
-    fn = getattr(load(), name)
     if device.index == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
@@ -91,10 +97,10 @@ def _call(name, device, stream, made, *args):
 
 def _token_stride(name, t, heads, dim):
     """Token stride of t [n, heads, dim] whose heads lie one after another."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or stride[2] != 1 or stride[1] != dim:
         raise ValueError(f"{name} must be [N, {heads}, {dim}] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 # ------------------------------------------------------------------ rotary
@@ -137,11 +143,11 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, scale
         _check(dev, x.dtype, False, out=out)
         if out.shape != x.shape:
             raise ValueError("out must have x's shape")
-    if (x.stride(2) != 1 or out.stride(2) != 1) and dim > 1:
+    (xt, xh, xe), (ot, oh, oe) = x.stride(), out.stride()
+    if (xe != 1 or oe != 1) and dim > 1:
         raise ValueError("a head's values must be contiguous")
     _call("gqa_rope", dev, stream, made, x.data_ptr(), pos, freq, scale, out.data_ptr(), n, heads, dim, rot_offset,
-          2 * inv_freq.shape[0], _layout(layout), 1 if inverse else 0, _TYPES[x.dtype], x.stride(0), x.stride(1),
-          out.stride(0), out.stride(1))
+          2 * inv_freq.shape[0], _layout(layout), 1 if inverse else 0, _TYPES[x.dtype], xt, xh, ot, oh)
     return out
 
 
