@@ -12,8 +12,10 @@
 // of a decode step the head's weights (128 KB) are the larger operand, so the
 // bound is the bytes of weights and rows; mma.sync keeps up with HBM there
 // (2 * tokens FLOP per weight byte). A CTA takes a head, BN output columns and
-// BM tokens and streams K in chunks of 64 through a cp.async ring; the columns
-// are split so that even 16 heads fill the GPU.
+// BM tokens (16, 64 or 128, so that up to 128 tokens read the weights once) and
+// streams K in chunks of 64 through a cp.async ring, absorb_q's two chunks at
+// once. The results go through shared memory to 16-byte stores: a fragment's own
+// are 4 bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,10 +41,55 @@ struct ProjTile {
   static constexpr int kABytes = BM * kBK * 2, kBBytes = BN * kBK * 2;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kSmem = STAGES * kStage;
+  static_assert(kSmem >= BM * BN * 2, "the results are staged in the ring");
 };
 
 // 16-byte chunk c of row r of a tile of 128-byte rows, XOR-swizzled.
 __device__ __forceinline__ uint32_t sw(uint32_t base, int r, int c) { return base + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// The 64 rotary values of tokens [m0, m1), head h: a thread takes four pairs of a token (a CTA of its own: at the end
+// of one of the products they took longer than the product).
+__device__ __forceinline__ void rotary_tail(const MlaProjParams& p, int m0, int m1, int h, int threads) {
+  __shared__ unsigned long long turns[kRope / 2];
+  if (p.inv_freq != nullptr) {
+    if (threadIdx.x < kRope / 2) turns[threadIdx.x] = rope_turn(__ldg(p.inv_freq + threadIdx.x));
+    __syncthreads();
+  }
+  const bool half = p.layout != kRopeInterleaved;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < (m1 - m0) * 8; i += threads) {
+    const int m = m0 + (i >> 3), j = (i & 7) * 4;  // pairs j .. j + 3
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + m * p.x_token_stride + h * p.x_head_stride + kNope;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (static_cast<int64_t>(m) * p.num_heads + h) * p.out_width + kLat;
+    // two words of two values each: half layout the pairs' first and their second elements, else two pairs each
+    const int e1 = half ? j : 2 * j, e2 = half ? j + kRope / 2 : 2 * j + 4;
+    uint2 a = *reinterpret_cast<const uint2*>(x + e1), b = *reinterpret_cast<const uint2*>(x + e2);
+    if (p.inv_freq != nullptr) {
+      const int pos = __ldg(p.positions + m);
+      float v[8] = {__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
+                    __uint_as_float(a.y & 0xffff0000u), __uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                    __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 c = rope_cos_sin(pos, turns[j + k], p.scale);
+        const float x1 = half ? v[k] : v[2 * k], x2 = half ? v[4 + k] : v[2 * k + 1];
+        const float y1 = x1 * c.x - x2 * c.y, y2 = x2 * c.x + x1 * c.y;
+        if (half) {
+          y[k] = y1;
+          y[4 + k] = y2;
+        } else {
+          y[2 * k] = y1;
+          y[2 * k + 1] = y2;
+        }
+      }
+      a = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      b = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    }
+    *reinterpret_cast<uint2*>(o + e1) = a;
+    *reinterpret_cast<uint2*>(o + e2) = b;
+  }
+}
 
 template <int WM, int WN, int MI, int NI, int STAGES, bool BT>
 __global__ void __launch_bounds__(WM* WN * 32) gqa_mla_proj_kernel(const MlaProjParams p) {
@@ -52,6 +99,10 @@ __global__ void __launch_bounds__(WM* WN * 32) gqa_mla_proj_kernel(const MlaProj
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp / WN, wn = warp % WN;
   const int n0 = blockIdx.x * T::BN, h = blockIdx.y, m0 = blockIdx.z * T::BM;
+  if (BT && n0 >= kLat) {
+    rotary_tail(p, m0, min(m0 + T::BM, p.num_tokens), h, T::kThreads);
+    return;
+  }
   constexpr int K = BT ? kNope : kLat;
   constexpr int kChunks = K / kBK;
   const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.x) + h * p.x_head_stride;
@@ -115,37 +166,31 @@ __global__ void __launch_bounds__(WM* WN * 32) gqa_mla_proj_kernel(const MlaProj
       }
     }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring becomes the staging of the results: BM rows, BN / 64 blocks of 128 bytes a row
 
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-  const int64_t row = static_cast<int64_t>(p.num_heads) * p.out_width;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int m = m0 + (wm * MI + mi) * 16 + (lane >> 2) + 8 * half;
-      if (m >= p.num_tokens) continue;
-      __nv_bfloat16* o = out + m * row + h * p.out_width + n0 + wn * NI * 8 + 2 * (lane & 3);
+      const int r = (wm * MI + mi) * 16 + (lane >> 2) + 8 * half;
 #pragma unroll
-      for (int nj = 0; nj < NI; ++nj)
-        *reinterpret_cast<uint32_t*>(o + nj * 8) = pack_bf16(acc[mi][nj][2 * half], acc[mi][nj][2 * half + 1]);
-    }
-  if (BT && blockIdx.x == 0) {  // the rotary tail of this CTA's tokens
-    for (int i = tid; i < T::BM * (kRope / 2); i += T::kThreads) {
-      const int m = m0 + i / (kRope / 2), j = i % (kRope / 2);
-      if (m >= p.num_tokens) break;
-      const int e1 = p.layout == kRopeInterleaved ? 2 * j : j, e2 = p.layout == kRopeInterleaved ? e1 + 1 : j + kRope / 2;
-      const __nv_bfloat16* x = a + m * p.x_token_stride + kNope;
-      float x1 = __bfloat162float(x[e1]), x2 = __bfloat162float(x[e2]);
-      if (p.inv_freq != nullptr) {
-        const float2 c = rope_cos_sin(__ldg(p.positions + m), rope_turn(__ldg(p.inv_freq + j)), p.scale);
-        const float y1 = x1 * c.x - x2 * c.y;
-        x2 = x2 * c.x + x1 * c.y;
-        x1 = y1;
+      for (int nj = 0; nj < NI; ++nj) {
+        const int c = wn * NI + nj;  // 16-byte chunk of the row
+        const uint32_t at = sw(sb + (c >> 3) * (T::BM * 128), r, c & 7) + 4 * (lane & 3);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pack_bf16(acc[mi][nj][2 * half], acc[mi][nj][2 * half + 1]))
+                     : "memory");
       }
-      __nv_bfloat16* o = out + m * row + h * p.out_width + kLat;
-      o[e1] = __float2bfloat16_rn(x1);
-      o[e2] = __float2bfloat16_rn(x2);
     }
+  __syncthreads();
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + h * p.out_width;
+  const int64_t row = static_cast<int64_t>(p.num_heads) * p.out_width;
+  for (int i = tid; i < T::BM * (T::BN / 8); i += T::kThreads) {
+    const int r = i / (T::BN / 8), c = i % (T::BN / 8), m = m0 + r;
+    if (m >= p.num_tokens) break;
+    uint4 v;
+    ld_shared_u4(sw(sb + (c >> 3) * (T::BM * 128), r, c & 7), v.x, v.y, v.z, v.w);
+    *reinterpret_cast<uint4*>(out + m * row + n0 + c * 8) = v;
   }
 }
 
@@ -156,7 +201,7 @@ cudaError_t launch(const MlaProjParams& p, cudaStream_t stream) {
   const void* fn = reinterpret_cast<const void*>(gqa_mla_proj_kernel<WM, WN, MI, NI, STAGES, BT>);
   const cudaError_t e = set_smem_limit_once(configured, fn, T::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((BT ? kLat : kHeadV) / T::BN, p.num_heads, (p.num_tokens + T::BM - 1) / T::BM);
+  const dim3 grid((BT ? kLat / T::BN + 1 : kHeadV / T::BN), p.num_heads, (p.num_tokens + T::BM - 1) / T::BM);
   gqa_mla_proj_kernel<WM, WN, MI, NI, STAGES, BT><<<grid, T::kThreads, T::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -164,11 +209,15 @@ cudaError_t launch(const MlaProjParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_mla_absorb_q(const MlaProjParams& p, cudaStream_t stream) {
-  return p.num_tokens <= 16 ? launch<1, 4, 1, 2, 2, true>(p, stream) : launch<2, 4, 2, 4, 2, true>(p, stream);
+  if (p.num_tokens <= 16) return launch<1, 4, 1, 2, 3, true>(p, stream);   // 16 x 64
+  if (p.num_tokens <= 64) return launch<2, 4, 2, 2, 3, true>(p, stream);   // 64 x 64
+  return launch<4, 2, 2, 4, 3, true>(p, stream);                           // 128 x 64
 }
 
 cudaError_t launch_mla_expand_out(const MlaProjParams& p, cudaStream_t stream) {
-  return p.num_tokens <= 16 ? launch<1, 4, 1, 2, 4, false>(p, stream) : launch<2, 4, 2, 2, 3, false>(p, stream);
+  if (p.num_tokens <= 16) return launch<1, 4, 1, 2, 6, false>(p, stream);  // 16 x 64
+  if (p.num_tokens <= 64) return launch<2, 4, 2, 2, 5, false>(p, stream);  // 64 x 64
+  return launch<4, 2, 2, 4, 4, false>(p, stream);                          // 128 x 64
 }
 
 }  // namespace gqa

@@ -10,12 +10,14 @@
 // Infinities saturate to +-448 * scale and NaN stays NaN; neither enters the
 // scale, so the other values of the head keep their precision.
 //
-// All of it is bounded by HBM. Append: a warp takes `rows` of one token's 40
-// head rows (32 Q, 4 K, 4 V); a row is 128 values, four consecutive ones per
-// lane. A lane's four (cos, sin) pairs are formed once and serve every Q and K
-// row the warp handles; partners come from another lane by shuffle when the
-// pairs' distance is a whole number of lanes, else through a row staged in
-// shared memory. K before quantisation stays fp32 (not rounded to bf16 first).
+// All of it is bounded by HBM. Append: a token's 40 head rows (32 Q, 4 K, 4 V) are
+// ten batches of four; a warp takes all of them, or with few tokens a share, with the
+// next batch's loads in flight. A row is 128 values, four consecutive ones per lane. A
+// lane's four (cos, sin) pairs are formed once and serve every Q and K row the warp
+// handles (the frequencies' 64-bit arithmetic once per CTA: the part has few FP64
+// lanes); partners come from another lane by shuffle when the pairs' distance is a
+// whole number of lanes, else through a row staged in shared memory. K before
+// quantisation stays fp32 (not rounded to bf16 first).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,12 +32,13 @@ namespace gqa {
 namespace {
 
 constexpr int kAppendWarps = 8;
-constexpr int kRowsPerToken = kQoHeads + 2 * kKvHeads;  // 40
+constexpr int kBatch = 4;                                          // rows: a batch is all of Q, K or V
+constexpr int kBatches = (kQoHeads + 2 * kKvHeads) / kBatch;       // 10: eight of Q, then K, then V
+static_assert(kKvHeads == kBatch && kQoHeads % kBatch == 0, "batches of four rows");
 constexpr int kF8Codes = kKvHeads * kHeadDim;           // 512
 constexpr int kF8Row = kF8Codes + 4 * kKvHeads;         // 528
 
-__device__ __forceinline__ float4 load_row4(const __nv_bfloat16* row, int lane) {
-  const uint2 v = __ldcs(reinterpret_cast<const uint2*>(row) + lane);
+__device__ __forceinline__ float4 unpack_row4(uint2 v) {
   return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                      __uint_as_float(v.y & 0xffff0000u));
 }
@@ -52,7 +55,7 @@ __device__ __forceinline__ int partner_of(int e, int pairs) {  // window element
 }
 
 template <int LAYOUT>
-__device__ __forceinline__ LaneTurn lane_turn(const AppendParams& p, int pos, int lane) {
+__device__ __forceinline__ LaneTurn lane_turn(const AppendParams& p, const unsigned long long* turns, int pos, int lane) {
   LaneTurn t;
   const int pairs = p.rot_dim >> 1;
 #pragma unroll
@@ -63,7 +66,7 @@ __device__ __forceinline__ LaneTurn lane_turn(const AppendParams& p, int pos, in
     if (e >= 0 && e < p.rot_dim) {
       const int i = LAYOUT == kRopeInterleaved ? e >> 1 : (e < pairs ? e : e - pairs);
       const bool second = LAYOUT == kRopeInterleaved ? (e & 1) != 0 : e >= pairs;
-      const float2 v = rope_cos_sin(pos, rope_turn(__ldg(p.inv_freq + i)), p.scale);
+      const float2 v = rope_cos_sin(pos, turns[i], p.scale);
       t.c[j] = v.x;
       t.s[j] = second ? v.y : -v.y;
     }
@@ -131,42 +134,69 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 template <int LAYOUT, bool SHUFFLE, bool FP8>
 __global__ void __launch_bounds__(kAppendWarps * 32) gqa_rope_append_kernel(const AppendParams p) {
   __shared__ float stage[SHUFFLE ? 1 : kAppendWarps][SHUFFLE ? 4 : kHeadDim];
+  __shared__ unsigned long long turns[kHeadDim / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (p.inv_freq != nullptr) {
+    if (threadIdx.x < p.rot_dim / 2) turns[threadIdx.x] = rope_turn(__ldg(p.inv_freq + threadIdx.x));
+    __syncthreads();
+  }
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp;
   const int n = static_cast<int>(w / p.splits);
   const int part = static_cast<int>(w - static_cast<int64_t>(n) * p.splits);
   if (n >= p.num_tokens) return;
-  const int first_row = p.q != nullptr ? 0 : kQoHeads;
-  const int rows = kRowsPerToken - first_row;
-  const int r0 = first_row + part * rows / p.splits, r1 = first_row + (part + 1) * rows / p.splits;
+  const int first = p.q != nullptr ? 0 : kBatches - 2;  // no queries: the batches of K and V
   const int slot = __ldg(p.slots + n);
-  const bool stored = slot >= 0 && slot < p.num_pages;
-  const bool turned = p.inv_freq != nullptr && r0 < kQoHeads + kKvHeads;
+  const int count = slot >= 0 && slot < p.num_pages ? kBatches : kBatches - 2;  // not stored: the queries only
+  const int b0 = first + part * (kBatches - first) / p.splits;
+  const int b1 = min(first + (part + 1) * (kBatches - first) / p.splits, count);
+  if (b0 >= b1) return;
+
+  auto load = [&](int b, uint2 (&v)[kBatch]) {
+    const void* from = b < kBatches - 2 ? p.q : (b == kBatches - 2 ? p.k : p.v);
+    const int64_t stride = b < kBatches - 2 ? p.q_stride : (b == kBatches - 2 ? p.k_stride : p.v_stride);
+    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(from) + n * stride +
+                                                      (b < kBatches - 2 ? b * kBatch * kHeadDim : 0)) + lane;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v[i] = __ldcs(src + i * (kHeadDim / 4));
+  };
+  uint2 next[kBatch];
+  load(b0, next);
+  const bool turned = p.inv_freq != nullptr && b0 < kBatches - 1;
   LaneTurn t;
-  if (turned) t = lane_turn<LAYOUT>(p, __ldg(p.positions + n), lane);
+  if (turned) t = lane_turn<LAYOUT>(p, turns, __ldg(p.positions + n), lane);
   float* row = stage[SHUFFLE ? 0 : warp];
-  for (int r = r0; r < r1; ++r) {
-    const bool is_q = r < kQoHeads, is_k = !is_q && r < kQoHeads + kKvHeads;
-    if (!is_q && !stored) break;
-    const int h = is_q ? r : (is_k ? r - kQoHeads : r - kQoHeads - kKvHeads);
-    const __nv_bfloat16* src =
-        static_cast<const __nv_bfloat16*>(is_q ? p.q : (is_k ? p.k : p.v)) +
-        n * (is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride)) + h * kHeadDim;
-    float4 x = load_row4(src, lane);
-    if (turned && (is_q || is_k)) x = turn_row<LAYOUT, SHUFFLE>(p, x, t, lane, row);
+  for (int b = b0; b < b1; ++b) {
+    uint2 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v[i] = next[i];
+    if (b + 1 < b1) load(b + 1, next);
+    const bool is_q = b < kBatches - 2, is_k = b == kBatches - 2;
+    float4 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      x[i] = unpack_row4(v[i]);
+      if (turned && (is_q || is_k)) x[i] = turn_row<LAYOUT, SHUFFLE>(p, x[i], t, lane, row);
+    }
     if (is_q || !FP8) {
-      __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.q_out) + (static_cast<int64_t>(n) * kQoHeads + h) * kHeadDim
+      __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.q_out) + (static_cast<int64_t>(n) * kQoHeads + b * kBatch) * kHeadDim
                                 : static_cast<__nv_bfloat16*>(is_k ? p.k_cache : p.v_cache) +
-                                      (static_cast<int64_t>(slot) * kKvHeads + h) * kHeadDim;
-      reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+                                      static_cast<int64_t>(slot) * (kKvHeads * kHeadDim);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        reinterpret_cast<uint2*>(dst + i * kHeadDim)[lane] = make_uint2(pack_bf16(x[i].x, x[i].y), pack_bf16(x[i].z, x[i].w));
     } else {
-      const unsigned top = __reduce_max_sync(
-          0xffffffffu, max(max(finite_abs(x.x), finite_abs(x.y)), max(finite_abs(x.z), finite_abs(x.w))));
-      const unsigned f = scale_field(top);
-      const float inv = __uint_as_float((254u - f) << 23);
       uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + static_cast<int64_t>(slot) * kF8Row;
-      reinterpret_cast<uint32_t*>(dst + h * kHeadDim)[lane] = e4m3x4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      if (lane == 0) reinterpret_cast<float*>(dst + kF8Codes)[h] = __uint_as_float(f << 23);
+      unsigned f[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        f[i] = scale_field(__reduce_max_sync(
+            0xffffffffu, max(max(finite_abs(x[i].x), finite_abs(x[i].y)), max(finite_abs(x[i].z), finite_abs(x[i].w)))));
+        const float inv = __uint_as_float((254u - f[i]) << 23);
+        reinterpret_cast<uint32_t*>(dst + i * kHeadDim)[lane] =
+            e4m3x4(x[i].x * inv, x[i].y * inv, x[i].z * inv, x[i].w * inv);
+      }
+      if (lane == 0)
+        *reinterpret_cast<uint4*>(dst + kF8Codes) = make_uint4(f[0] << 23, f[1] << 23, f[2] << 23, f[3] << 23);
     }
   }
 }
@@ -181,38 +211,60 @@ cudaError_t launch_append(const AppendParams& p, int grid, cudaStream_t stream) 
 }
 
 // ------------------------------------------------------------ FP8 read back
-// One warp per token and cache half: lane l reads the 16 codes [16 l, 16 l + 16)
-// (head l / 8) and writes their 16 bf16 values.
+// A warp takes four tokens, their eight rows' loads in flight together. Lane l reads
+// the codes [8 l, 8 l + 8) of each half of a row (heads 0 and 1, 2 and 3) and writes
+// their eight bf16 values: both sides contiguous over the warp.
+constexpr int kReadTokens = 4;
+__device__ __forceinline__ uint4 dequantise8(uint2 codes, float scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t h2 = cvt_e4m3x2_f16x2((j < 2 ? codes.x : codes.y) >> (16 * (j & 1)));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    o[j] = pack_bf16(v.x * scale, v.y * scale);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 __global__ void __launch_bounds__(256) gqa_kv_read_fp8_kernel(const uint8_t* __restrict__ k_cache,
                                                               const uint8_t* __restrict__ v_cache,
                                                               const int* __restrict__ indices, uint4* __restrict__ k_out,
                                                               uint4* __restrict__ v_out, int n, int num_pages) {
   const int lane = threadIdx.x & 31;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < n; i += stride) {
-    const int page = __ldg(indices + i);
-    const bool ok = page >= 0 && page < num_pages;
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kReadTokens;
+  if (i0 >= n) return;
+  int page = -1;
+  if (lane < kReadTokens && i0 + lane < n) {
+    page = __ldg(indices + i0 + lane);
+    if (page >= num_pages) page = -1;
+  }
+  uint2 codes[2 * kReadTokens][2];
+  float scale[2 * kReadTokens][2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint4 codes = make_uint4(0, 0, 0, 0);
-      float scale = 0.f;
-      if (ok) {
-        const uint8_t* row = (c == 0 ? k_cache : v_cache) + static_cast<int64_t>(page) * kF8Row;
-        codes = __ldg(reinterpret_cast<const uint4*>(row) + lane);
-        scale = __ldg(reinterpret_cast<const float*>(row + kF8Codes) + (lane >> 3));
-      }
-      const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
-      uint32_t o[8];
+  for (int t = 0; t < kReadTokens; ++t) {
+    const int pg = __shfl_sync(0xffffffffu, page, t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t h2 = cvt_e4m3x2_f16x2(in[j >> 1] >> (16 * (j & 1)));
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        o[j] = ok ? pack_bf16(v.x * scale, v.y * scale) : 0u;
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        codes[2 * t + c][h] = make_uint2(0, 0);
+        scale[2 * t + c][h] = 0.f;
+        if (pg >= 0) {
+          const uint8_t* row = (c == 0 ? k_cache : v_cache) + static_cast<int64_t>(pg) * kF8Row;
+          codes[2 * t + c][h] = __ldg(reinterpret_cast<const uint2*>(row) + 32 * h + lane);
+          scale[2 * t + c][h] = __ldg(reinterpret_cast<const float*>(row + kF8Codes) + 2 * h + (lane >> 4));
+        }
       }
-      uint4* dst = (c == 0 ? k_out : v_out) + i * (kF8Codes / 8) + 2 * lane;
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
+  }
+#pragma unroll
+  for (int t = 0; t < kReadTokens; ++t) {
+    if (i0 + t >= n) break;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ((c == 0 ? k_out : v_out) + (i0 + t) * (kF8Codes / 8))[32 * h + lane] =
+            dequantise8(codes[2 * t + c][h], scale[2 * t + c][h]);
   }
 }
 
@@ -248,8 +300,13 @@ __global__ void __launch_bounds__(256) gqa_mla_append_kernel(const MlaAppendPara
 }  // namespace
 
 cudaError_t launch_rope_append(AppendParams p, int sm_count, cudaStream_t stream) {
-  (void)sm_count;
-  p.splits = 4;
+  // a warp a token, or with few tokens more warps each: ten (a batch each), five or two, while a wave of 64 warps an
+  // SM holds them
+  const int64_t wave = static_cast<int64_t>(sm_count) * 64;
+  const int batches = p.q != nullptr ? kBatches : 2;
+  p.splits = 1;
+  for (int s : {10, 5, 2})
+    if (p.splits == 1 && s <= batches && p.num_tokens * static_cast<int64_t>(s) <= wave) p.splits = s;
   const int64_t warps = static_cast<int64_t>(p.num_tokens) * p.splits;
   const int grid = static_cast<int>((warps + kAppendWarps - 1) / kAppendWarps);
   const int pairs = p.rot_dim >> 1;
@@ -262,9 +319,8 @@ cudaError_t launch_rope_append(AppendParams p, int sm_count, cudaStream_t stream
 
 cudaError_t launch_kv_read_fp8(const void* k_cache, const void* v_cache, const int* indices, void* k_out, void* v_out,
                                int n, int num_pages, int sm_count, cudaStream_t stream) {
-  int grid = (n + 7) / 8;
-  const int cap = sm_count * 8;
-  if (grid > cap) grid = cap;
+  (void)sm_count;
+  const int grid = (n + 8 * kReadTokens - 1) / (8 * kReadTokens);
   gqa_kv_read_fp8_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint8_t*>(k_cache),
                                                    static_cast<const uint8_t*>(v_cache), indices,
                                                    static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), n, num_pages);
