@@ -219,8 +219,7 @@ struct RopeParams {  // gqa_rope.cu; strides in elements
   float scale;
   int num_tokens, num_heads, head_dim, rot_offset, rot_dim, layout, inverse;
   int copy_rest;           // copy the elements outside the window (0: in place)
-  int tokens_per_block;
-  uint32_t head_magic;     // ceil(2^32 / num_heads), 0 for one head
+  int heads_each;          // heads a thread walks
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, int sm_count, cudaStream_t stream);
 

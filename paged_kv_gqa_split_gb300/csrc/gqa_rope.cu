@@ -7,16 +7,16 @@
 // (2 i, 2 i + 1) (interleaved). Elements outside the window are copied.
 // `inverse` turns by -a, which undoes a rotation and is also its gradient.
 //
-// Bounded by HBM: every element is read and written once, and an angle costs
-// one sincos shared by all heads of its token. A CTA takes a few tokens: it fills
-// a table of their (cos, sin) pairs in shared memory (the frequencies' 64-bit
-// arithmetic once per CTA: the part has few FP64 lanes), then its threads walk the
-// (token, head) rows, a thread always at the same vector of a head, four rows'
-// loads in flight. With 16-byte vectors (bf16 / fp16: 8 elements) a half-layout
-// item holds the vectors of both partners, so a rotation never crosses threads and
-// in-place calls are safe. Windows, strides or addresses that do not fit 16-byte
-// vectors take the one-element form. Rotation is in fp32; the one rounding is the
-// store to the tensor's type.
+// Bounded by HBM: every element is read and written once. A thread stays at one
+// vector of a head and one token and walks that token's heads (or, with few tokens,
+// a share of them), a few rows' loads in flight; it forms its pairs' (cos, sin) once
+// for all of them, while the first rows load. The frequencies' 64-bit arithmetic runs
+// once per CTA: the part has few FP64 lanes. (With a table of all pairs' (cos, sin) in
+// shared memory the two barriers and the table's latency held HBM at 50 %.) With 16-byte
+// vectors (bf16 / fp16: 8 elements) a half-layout item holds the vectors of both
+// partners, so a rotation never crosses threads and in-place calls are safe. Windows,
+// strides or addresses that do not fit 16-byte vectors take the one-element form.
+// Rotation is in fp32; the one rounding is the store to the tensor's type.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,7 +65,7 @@ struct Item {
     if (turn && LAYOUT == kRopeHalf) b = *reinterpret_cast<const VecT*>(x + e + pairs);
     if (turn && LAYOUT == kRopeInterleaved && V == 1) b = *reinterpret_cast<const VecT*>(x + e + 1);
   }
-  __device__ __forceinline__ void finish(T* y, int e, int pairs, bool turn, const float2* cs) {
+  __device__ __forceinline__ void finish(T* y, int e, int pairs, bool turn, const float2 (&cs)[LAYOUT == kRopeHalf ? V : (V + 1) / 2]) {
     if (!turn) {
       *reinterpret_cast<VecT*>(y + e) = a;
     } else if (LAYOUT == kRopeHalf || V == 1) {
@@ -93,22 +93,21 @@ struct Item {
 
 template <typename T, int V, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) gqa_rope_kernel(const RopeParams p) {
-  extern __shared__ float2 cs[];  // [tokens_per_block][r / 2], then the frequencies [r / 2]
-  const int pairs = p.rot_dim >> 1;
-  const int n0 = blockIdx.x * p.tokens_per_block;
-  const int nt = min(p.tokens_per_block, p.num_tokens - n0);
-
+  extern __shared__ unsigned long long turns[];  // [r / 2]
   // Items of a head: the window's (pairs of vectors, vectors or pairs), then the vectors outside it unless in place.
-  constexpr int kTurned = LAYOUT == kRopeHalf ? V : (V == 1 ? 1 : V / 2);  // pairs an item turns
+  constexpr int kTurned = LAYOUT == kRopeHalf ? V : (V + 1) / 2;  // pairs an item turns
+  constexpr int U = LAYOUT == kRopeHalf ? 2 : 4;                  // rows in flight
+  const int pairs = p.rot_dim >> 1;
   const int turn_items = pairs / kTurned;
   const int per_head = turn_items + (p.copy_rest ? (p.head_dim - p.rot_dim) / V : 0);
-  const int rows = nt * p.num_heads;
-  const bool wide = per_head > kRopeThreads;  // a head holds more items than threads: one row at a time
-  const int rows_at_once = wide ? 1 : kRopeThreads / per_head;
+  const bool wide = per_head > kRopeThreads;  // a head holds more items than threads
+  const int tokens = wide ? 1 : kRopeThreads / per_head;
   const int y = wide ? 0 : threadIdx.x / per_head;
-  const int k0 = threadIdx.x - y * per_head;
-  const uint32_t magic = p.head_magic;
-  constexpr int U = 4;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * tokens + y;
+  const int h0 = blockIdx.y * p.heads_each, h1 = min(h0 + p.heads_each, p.num_heads);
+  const bool active = y < tokens && n < p.num_tokens;
+  const T* x = static_cast<const T*>(p.x) + n * p.x_token_stride;
+  T* out = static_cast<T*>(p.out) + n * p.out_token_stride;
   Item<T, V, LAYOUT> it[U];
   int e = 0;
   bool turn = false;
@@ -117,55 +116,58 @@ __global__ void __launch_bounds__(kRopeThreads) gqa_rope_kernel(const RopeParams
     e = turn ? p.rot_offset + k * kTurned * (LAYOUT == kRopeHalf ? 1 : 2) : (k - turn_items) * V;
     if (!turn && e >= p.rot_offset) e += p.rot_dim;
   };
-  auto token = [&](int row) { return magic != 0 ? static_cast<int>(__umulhi(row, magic)) : row; };  // row / num_heads
-  auto load = [&](int r) {
+  auto load = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = r + u * rows_at_once;
-      if (row >= rows) break;
-      const int t = token(row), h = row - t * p.num_heads;
-      it[u].load(static_cast<const T*>(p.x) + (n0 + t) * p.x_token_stride + h * p.x_head_stride, e, pairs, turn);
-    }
+    for (int u = 0; u < U; ++u)
+      if (h + u < h1) it[u].load(x + (h + u) * p.x_head_stride, e, pairs, turn);
   };
-  const bool active = y < rows_at_once;
-  place(k0);
-  if (active) load(y);  // in flight while the table is filled
-
-  unsigned long long* turns = reinterpret_cast<unsigned long long*>(cs + p.tokens_per_block * pairs);
-  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) turns[i] = rope_turn(__ldg(p.inv_freq + i));
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs * nt; i += kRopeThreads) {
-    const int t = i / pairs;
-    float2 v = rope_cos_sin(__ldg(p.positions + n0 + t), turns[i - t * pairs], p.scale);
-    if (p.inverse) v.y = -v.y;
-    cs[i] = v;
+  int k = threadIdx.x - y * per_head;
+  int pos = 0;
+  if (active) {
+    place(k);
+    load(h0);
+    pos = __ldg(p.positions + n);
   }
+  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) turns[i] = rope_turn(__ldg(p.inv_freq + i));
   __syncthreads();
   if (!active) return;
 
-  for (int k = k0; k < per_head; k += kRopeThreads) {
-    if (k != k0) {
-      place(k);
-      load(y);
-    }
-    const float2* mine = cs + (turn ? k * kTurned : 0);
-    for (int r = y; r < rows; r += U * rows_at_once) {
+  for (;;) {
+    float2 cs[kTurned];
+    if (turn) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = r + u * rows_at_once;
-        if (row >= rows) break;
-        const int t = token(row), h = row - t * p.num_heads;
-        it[u].finish(static_cast<T*>(p.out) + (n0 + t) * p.out_token_stride + h * p.out_head_stride, e, pairs, turn,
-                     mine + t * pairs);
+      for (int j = 0; j < kTurned; ++j) {
+        cs[j] = rope_cos_sin(pos, turns[k * kTurned + j], p.scale);
+        if (p.inverse) cs[j].y = -cs[j].y;
       }
-      load(r + U * rows_at_once);
     }
-    if (!wide) break;
+    for (int h = h0; h < h1; h += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u < h1) it[u].finish(out + (h + u) * p.out_head_stride, e, pairs, turn, cs);
+      if (h + U < h1) load(h + U);
+    }
+    k += kRopeThreads;
+    if (!wide || k >= per_head) break;
+    place(k);
+    load(h0);
   }
 }
 
 template <typename T, int V>
-cudaError_t launch(const RopeParams& p, int grid, int smem, cudaStream_t stream) {
+cudaError_t launch(RopeParams p, int sm_count, cudaStream_t stream) {
+  const int pairs = p.rot_dim / 2;
+  const int turned = p.layout == kRopeHalf ? V : (V + 1) / 2;
+  const int per_head = pairs / turned + (p.copy_rest ? (p.head_dim - p.rot_dim) / V : 0);
+  const int tokens = per_head > kRopeThreads ? 1 : kRopeThreads / per_head;
+  const int64_t blocks = (static_cast<int64_t>(p.num_tokens) + tokens - 1) / tokens;
+  // all heads of a token a thread, or, where that leaves fewer than 8 CTAs an SM, a share of them
+  const int64_t want = 8 * static_cast<int64_t>(sm_count);
+  int64_t splits = blocks >= want ? 1 : (want + blocks - 1) / blocks;
+  if (splits > p.num_heads) splits = p.num_heads;
+  p.heads_each = static_cast<int>((p.num_heads + splits - 1) / splits);
+  const dim3 grid(static_cast<unsigned>(blocks), (p.num_heads + p.heads_each - 1) / p.heads_each);
+  const int smem = pairs * static_cast<int>(sizeof(unsigned long long));
   if (p.layout == kRopeHalf)
     gqa_rope_kernel<T, V, kRopeHalf><<<grid, kRopeThreads, smem, stream>>>(p);
   else
@@ -176,20 +178,12 @@ cudaError_t launch(const RopeParams& p, int grid, int smem, cudaStream_t stream)
 template <typename T>
 cudaError_t launch_type(RopeParams p, int sm_count, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(T);
-  const int pairs = p.rot_dim / 2;
   const int64_t strides = p.x_token_stride | p.x_head_stride | p.out_token_stride | p.out_head_stride;
   const bool addr = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out)) & 15) == 0;
-  const int window = p.layout == kRopeHalf ? pairs : p.rot_dim;
+  const int window = p.layout == kRopeHalf ? p.rot_dim / 2 : p.rot_dim;
   const bool vec = addr && (strides | p.rot_offset | window | (p.head_dim - p.rot_dim)) % V == 0;
   p.copy_rest = p.x != p.out || p.x_token_stride != p.out_token_stride || p.x_head_stride != p.out_head_stride;
-  // one token a CTA until the CTAs fill the GPU 16 times over, then up to 8 share a table
-  const int most = p.num_tokens / (16 * sm_count);
-  p.tokens_per_block = most < 1 ? 1 : (most > 8 ? 8 : most);
-  const int smem = (p.tokens_per_block + 1) * pairs * static_cast<int>(sizeof(float2));
-  const int grid = (p.num_tokens + p.tokens_per_block - 1) / p.tokens_per_block;
-  // row / heads as the upper half of row * magic: exact below 2^32 / heads rows (a CTA has at most 8 * heads)
-  p.head_magic = p.num_heads > 1 ? static_cast<uint32_t>(((1ull << 32) + p.num_heads - 1) / p.num_heads) : 0;
-  return vec ? launch<T, V>(p, grid, smem, stream) : launch<T, 1>(p, grid, smem, stream);
+  return vec ? launch<T, V>(p, sm_count, stream) : launch<T, 1>(p, sm_count, stream);
 }
 
 }  // namespace
