@@ -298,7 +298,6 @@ struct MlaPrefillParams {
   int* err;
   int head0, heads;    // heads of this pass
   int head_group;      // heads whose CTAs run together
-  int heads_each;      // heads a pair of the expansion takes
 };
 // A 2D tensor map over rows of `width` values (`pitch` bytes apart, 128-byte swizzle), read as boxes of
 // box_w x box_rows. False if the driver call is missing or refuses.

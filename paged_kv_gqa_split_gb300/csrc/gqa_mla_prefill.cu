@@ -244,23 +244,27 @@ __device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, vo
 }
 
 // -------------------------------------------------------------- expansion
-// Keys and values of `heads_each` heads for 256 packed rows, by a pair of CTAs: D [256
-// rows x 256 columns] = rows [256 x 512] W[h]^T, columns 0..127 the head's keys and
-// 128..255 its values (32 MMAs of M = 256, N = 256, K = 16, 128 clocks each). A CTA keeps
-// its 128 rows of the latents in shared memory (128 KB) for all its heads and streams its
+// Keys and values of one head for 256 packed rows are a unit: D [256 rows x 256 columns] =
+// rows [256 x 512] W[h]^T, columns 0..127 the head's keys and 128..255 its values (32 MMAs
+// of M = 256, N = 256, K = 16, 128 clocks each), by a pair of CTAs. Every pair takes an
+// equal run of the units (all heads of a row tile, then the next tile). A CTA keeps its 128
+// rows of the latents in shared memory (128 KB) for all heads of the tile and streams its
 // half of the weights (the even CTA the key rows, the odd one the value rows) through four
-// slots of 64 of the 512 values. The accumulators of two heads fill tensor memory, so a
-// head's epilogue (scale, round to fp16, through shared memory and a tensor copy out) runs
-// beside the next head's MMAs. Bound by the MMAs where there are many rows; the weights are
-// read from L2 at 32 bytes a clock and SM.
+// slots of 64 of the 512 values; the next tile's rows replace the old ones region by region
+// behind the MMAs. The accumulators of two units fill tensor memory, so a unit's epilogue
+// (scale, round to fp16, through shared memory and a tensor copy out) runs beside the next
+// unit's MMAs. Bound by the MMAs and, a fifth over them, the traffic of the copies out
+// (without them 32 heads of 16384 rows took 77 us instead of 97).
 //
 // Roles in each CTA: an MMA warp (the even CTA's issues for both), a copy warp, a warp that
-// turns the rotary keys into scaled fp16 (once, with the first heads), two epilogue
+// turns the rotary keys into scaled fp16 (once, with the first head), two epilogue
 // warpgroups (keys and values; one for both took 5700 clocks a head).
 constexpr int kExThreads = 384, kExSlots = 4, kExRegion = 128 * 128;
 constexpr int kExB = 8 * kExRegion, kExOut = kExB + kExSlots * kExRegion, kExBars = kExOut + 2 * kExRegion;
-enum : int { E_A = 0, E_BFULL = E_A + 8, E_BFREE = E_BFULL + kExSlots, E_DFULL = E_BFREE + kExSlots, E_DFREE = E_DFULL + 2,
-             E_DONE = E_DFREE + 2, E_COUNT };
+// Barriers. The even CTA's: regions of A and slots of B landed (both halves' bytes), accumulators read (8 warps of each
+// CTA). Both CTAs' (MMA commits): regions and slots free, accumulators written, all done.
+enum : int { E_A = 0, E_BFULL = E_A + 8, E_DFREE = E_BFULL + kExSlots, E_AFREE = E_DFREE + 2, E_BFREE = E_AFREE + 8,
+             E_DFULL = E_BFREE + kExSlots, E_DONE = E_DFULL + 2, E_COUNT = E_DONE + 1 };
 constexpr int kExSlot = kExBars + E_COUNT * 8, kExAbort = kExSlot + 4, kExSmem = kExAbort + 4 + 1024;
 static_assert(kExSmem <= 227 * 1024, "expansion exceeds shared memory");
 
@@ -274,15 +278,19 @@ __global__ void __launch_bounds__(kExThreads, 1)
   pdl_wait();
   pdl_launch_dependents();  // after the wait: what the next kernel reads before its own is then complete
   const int total = __ldg(p.kv_start + p.batch);
-  if (static_cast<int>(blockIdx.x >> 1) * 256 >= total) return;
+  const int64_t all = static_cast<int64_t>((total + 255) / 256) * p.heads;
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const int u0 = static_cast<int>(all * pair / pairs), u1 = static_cast<int>(all * (pair + 1) / pairs);
+  if (u0 >= u1) return;
   const uint32_t half = cluster_rank();
-  const int m0 = static_cast<int>(blockIdx.x) * 128;  // this CTA's packed rows (may lie past the last one)
-  const int h0 = blockIdx.y * p.heads_each, nh = min(p.heads_each, p.heads - h0);
-  // pairs start at different heads, so that they do not all read the same weights at once
-  auto head = [&](int h) {
-    const int r = h + static_cast<int>(blockIdx.x >> 1) % nh;
-    return h0 + (r < nh ? r : r - nh);
+  // unit u: tile u / heads; the heads of a tile start at another one in each tile, so that pairs do not read the same
+  // weights at once
+  auto tile_of = [&](int u) { return u / p.heads; };
+  auto head_of = [&](int u) {
+    const int t = u / p.heads, r = u - t * p.heads + t % p.heads;
+    return r < p.heads ? r : r - p.heads;
   };
+  auto first_of_tile = [&](int u) { return u == u0 || u % p.heads == 0; };
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kExAbort);
   auto bar = [&](int i) { return base + kExBars + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < E_COUNT; ++i) mbar_init(bar(i), i >= E_DFREE && i < E_DONE ? 16u : 1u);
+    for (int i = 0; i < E_COUNT; ++i) mbar_init(bar(i), i >= E_DFREE && i < E_AFREE ? 16u : 1u);
     *abort_s = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -309,15 +317,18 @@ __global__ void __launch_bounds__(kExThreads, 1)
       const uint64_t da0 = tc_sdesc(base, 16, 1024, kSwizzle128B), db0 = tc_sdesc(base + kExB, 16, 1024, kSwizzle128B);
       bool good = true;
       int s = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, aph = 1;  // parities of the slot and of the tile's regions
 #pragma unroll 1
-      for (int h = 0; h < nh && good; ++h) {
-        const uint32_t d = tmem + 256 * (h & 1);
-        if (h >= 2) good = warp_wait(bar(E_DFREE + (h & 1)), ((h >> 1) - 1) & 1, abort_s, err, kErrTimeoutEmpty);
+      for (int u = u0; u < u1 && good; ++u) {
+        const int i = u - u0;
+        const bool first = first_of_tile(u), last = u + 1 == u1 || (u + 1) % p.heads == 0;
+        if (first) aph ^= 1;
+        const uint32_t d = tmem + 256 * (i & 1);
+        if (i >= 2) good = warp_wait(bar(E_DFREE + (i & 1)), ((i >> 1) - 1) & 1, abort_s, err, kErrTimeoutEmpty);
         tc_fence_after();
 #pragma unroll 1
         for (uint32_t c = 0; c < 8 && good; ++c) {
-          if (h == 0) good = warp_wait(bar(E_A + c), 0, abort_s, err, kErrTimeoutFull);
+          if (first) good = warp_wait(bar(E_A + c), aph, abort_s, err, kErrTimeoutFull);
           good = good && warp_wait(bar(E_BFULL + s), ph, abort_s, err, kErrTimeoutFull);
           if (!good) break;
           const uint64_t da = da0 + c * (kExRegion >> 4), db = db0 + s * (kExRegion >> 4);
@@ -325,12 +336,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             tc2_mma_warp(d, da + ((kk * 32) >> 4), db + ((kk * 32) >> 4), idesc, kk ? 1u : c);
           tc2_commit_warp(bar(E_BFREE + s));
+          if (last) tc2_commit_warp(bar(E_AFREE + c));
           if (++s == kExSlots) {
             s = 0;
             ph ^= 1;
           }
         }
-        if (good) tc2_commit_warp(bar(E_DFULL + (h & 1)));
+        if (good) tc2_commit_warp(bar(E_DFULL + (i & 1)));
       }
       tc2_commit_warp(bar(E_DONE));
       __syncwarp();
@@ -339,18 +351,23 @@ __global__ void __launch_bounds__(kExThreads, 1)
   } else if (warp == 1) {
     const uint32_t a_full = cluster_addr(bar(E_A), 0), b_full = cluster_addr(bar(E_BFULL), 0);
     const uint32_t expect = half == 0 ? 2 * kExRegion : 0;
-    const int y0 = p.head0 * 256 + 128 * half;
-    int s = 0, u = 0;
+    int s = 0, n = 0, tiles = 0, a_regions = 0;
     uint32_t ph = 1;  // parity of the slot's previous release
     bool good = true;
 #pragma unroll 1
-    for (int h = 0; h < nh && good; ++h) {
-      const int y = y0 + head(h) * 256;
+    for (int u = u0; u < u1 && good; ++u) {
+      const int y = (p.head0 + head_of(u)) * 256 + 128 * half, m0 = tile_of(u) * 256 + 128 * half;
+      const bool first = first_of_tile(u);
+      if (first) ++tiles;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c, ++u) {
-        if (h == 0)
+      for (int c = 0; c < 8; ++c, ++n) {
+        if (first) {
+          if (tiles > 1) good = warp_wait(bar(E_AFREE + c), tiles & 1, abort_s, err, kErrTimeoutEmpty);
+          if (!good) break;
+          a_regions = c + 1;
           tma2_load_2d_warp(base + c * kExRegion, &maps.lat, 64 * c, m0, bar(E_A + c), expect, a_full + 8 * c);
-        if (u >= kExSlots) good = warp_wait(bar(E_BFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
+        }
+        if (n >= kExSlots) good = warp_wait(bar(E_BFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
         if (!good) break;
         tma2_load_2d_warp(base + kExB + s * kExRegion, &maps.w, 64 * c, y, bar(E_BFULL + s), expect, b_full + 8 * s);
         if (++s == kExSlots) {
@@ -360,15 +377,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
       }
     }
     if (half == 0 && lane == 0) {  // no copy may still be writing either CTA's shared memory when the pair leaves
-      for (int i = u > kExSlots ? u - kExSlots : 0; i < u; ++i) drain_wait(bar(E_BFULL + i % kExSlots), (i / kExSlots) & 1);
-      for (int c = 0; c < min(u, 8); ++c) drain_wait(bar(E_A + c), 0);
+      for (int i = n > kExSlots ? n - kExSlots : 0; i < n; ++i) drain_wait(bar(E_BFULL + i % kExSlots), (i / kExSlots) & 1);
+      for (int c = 0; c < a_regions; ++c) drain_wait(bar(E_A + c), (tiles - 1) & 1);
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (p.head0 == 0 && blockIdx.y == 0 && m0 < total) {
-      int ek, ev;
-      kv_exponents(p.amax, ek, ev);
-      const float f = pow2(-ek);
+    int ek, ev;
+    kv_exponents(p.amax, ek, ev);
+    const float f = pow2(-ek);
+    for (int u = u0; u < u1 && p.head0 == 0; ++u) {
+      const int m0 = tile_of(u) * 256 + 128 * half;
+      if (u % p.heads != 0 || m0 >= total) continue;  // once a tile, whichever pair has its first unit
       uint4* kr = reinterpret_cast<uint4*>(p.kr) + static_cast<int64_t>(m0) * (kRope / 8);
 #pragma unroll 4
       for (int i = lane; i < 128 * kRope / 8; i += 32) {
@@ -380,26 +399,29 @@ __global__ void __launch_bounds__(kExThreads, 1)
   } else if (warp >= 4) {
     const int part = (warp >> 2) - 1;  // 0: keys, 1: values
     const int wq = warp & 3, row = 32 * wq + lane;
-    const bool out = m0 < total, first = wq == 0 && lane == 0;
-    const bool bad = out && ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+    const bool issuer = wq == 0 && lane == 0;
     int ek, ev;
     kv_exponents(p.amax, ek, ev);
     const float f = pow2(part == 0 ? -ek : -ev);
     const uint32_t of_bad = part == 0 ? 0x7fff7fffu : 0u;
     const uint32_t dfree = cluster_addr(bar(E_DFREE), 0);
     const uint32_t dst = base + kExOut + part * kExRegion;
+    bool bad = false;
 #pragma unroll 1
-    for (int h = 0; h < nh; ++h) {
-      const bool good = warp_wait(bar(E_DFULL + (h & 1)), (h >> 1) & 1, abort_s, err, kErrTimeoutFull);
-      int all;  // the four warps agree, so that none is left at the barriers below
+    for (int u = u0; u < u1; ++u) {
+      const int i = u - u0, m0 = tile_of(u) * 256 + 128 * half;  // this CTA's packed rows (may lie past the last one)
+      const bool out = m0 < total;
+      if (first_of_tile(u)) bad = out && ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+      const bool good = warp_wait(bar(E_DFULL + (i & 1)), (i >> 1) & 1, abort_s, err, kErrTimeoutFull);
+      int every;  // the four warps agree, so that none is left at the barriers below
       asm volatile(
           "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-          : "=r"(all)
+          : "=r"(every)
           : "r"(good ? 1 : 0), "r"(1 + part)
           : "memory");
-      if (!all) break;
+      if (!every) break;
       tc_fence_after();
-      const uint32_t d = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * (h & 1) + 128 * part;
+      const uint32_t d = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * (i & 1) + 128 * part;
 #pragma unroll 1
       for (int r = 0; r < 2; ++r) {  // 64 columns
         uint32_t v[64];
@@ -409,9 +431,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
         if (r == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(dfree + 8 * (h & 1));
+          if (lane == 0) mbar_arrive_cluster_relaxed(dfree + 8 * (i & 1));
         }
-        if (first) bulk_wait_read<0>();  // the last copy out has read the buffer
+        if (issuer) bulk_wait_read<0>();  // the last copy out has read the buffer
         asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -423,13 +445,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
         fence_proxy_async_smem();
         asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-        if (first && out) {
-          tma_store_2d(part == 0 ? &maps.kn : &maps.vv, 64 * r, head(h) * p.cap + m0, dst);
+        if (issuer && out) {
+          tma_store_2d(part == 0 ? &maps.kn : &maps.vv, 64 * r, head_of(u) * p.cap + m0, dst);
           bulk_commit();
         }
       }
     }
-    if (first) bulk_wait_read<0>();
+    if (issuer) bulk_wait_read<0>();
     __syncwarp();
   }
   tc_fence_before();
@@ -878,22 +900,6 @@ cudaError_t launch_next(void (*fn)(Args...), int cluster, dim3 grid, int threads
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// Heads a pair of the expansion takes: the count that ends first, a head being 4096 clocks of MMAs and a pair's start
-// (its latents and first weights) about as much.
-int expand_heads_each(int tiles, int heads, int pairs) {
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int each = 1; each <= heads; ++each) {
-    const int64_t waves = (static_cast<int64_t>(tiles) * ((heads + each - 1) / each) + pairs - 1) / pairs;
-    const int64_t cost = waves * (each + 1);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = each;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream) {
@@ -909,13 +915,11 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
   if (e != cudaSuccess) return e;
   const int64_t q_tiles = p.total_q / kQTile + p.batch;
   const int64_t fit = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
-  const int tiles = (p.cap + 255) / 256;
   for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass) {
     p.head0 = h0;
     p.heads = p.num_heads - h0 < p.heads_per_pass ? p.num_heads - h0 : p.heads_per_pass;
     const int groups = static_cast<int>(fit < 1 ? p.heads : (p.heads + fit - 1) / fit);
     p.head_group = (p.heads + groups - 1) / groups;
-    p.heads_each = expand_heads_each(tiles, p.heads, sm_count / 2);
     ExpandMaps ex;
     AttnMaps at;
     const int64_t rows = static_cast<int64_t>(p.heads) * p.cap;
@@ -928,8 +932,7 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
         !tc_encode_2d(&at.kr, kF, p.kr, kRope, p.cap, kRope * 2, 64, kKTile / 2))
       return cudaErrorInvalidValue;
     at.vv = ex.vv;  // the same boxes
-    const dim3 grid(2 * tiles, (p.heads + p.heads_each - 1) / p.heads_each);
-    e = launch_next(gqa_mla_prefill_expand_kernel, 2, grid, kExThreads, kExSmem, stream, p, ex);
+    e = launch_next(gqa_mla_prefill_expand_kernel, 2, dim3(sm_count / 2 * 2), kExThreads, kExSmem, stream, p, ex);
     if (e != cudaSuccess) return e;
     e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,
                      stream, p, at);

@@ -152,6 +152,14 @@ def test_prefill_lengths(n):
         check(out, lse, c, 192 ** -0.5, True)
 
 
+@pytest.mark.parametrize("lens,h", [([(70, 10000)], 3), ([(40, 5000), (600, 2600), (1, 4000)], 5), ([(3, 700)] * 40, 1)])
+def test_prefill_long_and_many(lens, h):
+    """More units of the expansion than pairs of CTAs: runs that cross row tiles, and tiles shared by two pairs."""
+    c = case(lens, h, 64, h)
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+
+
 def test_prefill_rows_that_see_nothing():
     """More queries than cached tokens (their first rows see none), lengths of 0, blocks outside the pool."""
     c = case([(70, 3), (5, 0), (40, 40), (300, 200)], 3, 8, 5, bad_blocks=5)
