@@ -299,8 +299,11 @@ struct MlaPrefillParams {
   int head0, heads;    // heads of this pass
   int head_group;      // heads whose CTAs run together
 };
-// A 2D tensor map over rows of `width` values (`pitch` bytes apart, 128-byte swizzle), read as boxes of
-// box_w x box_rows. False if the driver call is missing or refuses.
+// A tensor map of 2 or 3 dimensions (sizes and boxes from the contiguous one on, `pitch` bytes between steps of the
+// others, 128-byte swizzle). False if the driver call is missing or refuses.
+bool tc_encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const int64_t* size,
+               const int64_t* pitch, const int* box);
+// Rows of `width` values, `pitch` bytes apart, as boxes of box_w x box_rows.
 bool tc_encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows,
                   int64_t pitch, int box_w, int box_rows);
 // Bytes of the workspace; with base != NULL also points the params' fields into it.

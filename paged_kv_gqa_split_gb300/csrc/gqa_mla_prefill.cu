@@ -502,13 +502,13 @@ constexpr int kAtK = 2 * kQTileBytes, kAtV = kAtK + kSlots * kKSlot, kAtBars = k
 // each CTA). Both CTAs' (MMA commits): K and V slots free (of both tiles), S and O written, all done.
 enum : int { B_KFULL = 0, B_VFULL = B_KFULL + kSlots, B_Q = B_VFULL + kSlots, B_P = B_Q + 2, B_KFREE = B_P + 4,
              B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_DONE = B_O + 2,
-             B_TURN = B_DONE + 1, B_COUNT = B_TURN + 2 };  // and whose turn it is to issue
+             B_TURN = B_DONE + 1, B_QRAW = B_TURN + 2, B_COUNT = B_QRAW + 2 };  // whose turn to issue; bf16 queries landed
 constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
 constexpr int kAtSmem = kAtAbort + 4 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
 static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
 
-struct AttnMaps {  // boxes of 64 values x 64 rows (keys) and x 128 rows (values)
-  CUtensorMap kn, vv, kr;
+struct AttnMaps {  // boxes of 64 values x 64 rows (keys) and x 128 rows (values, queries of one head)
+  CUtensorMap kn, vv, kr, q;
 };
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -611,6 +611,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (warp < kSoftWarp) {
     setmaxnreg_dec<kRoleRegs>();
     if (warp == kCopyWarp) {
+#pragma unroll 1
+      for (int a = 0; a < 2; ++a) {
+        if (nt[a] == 0) continue;
+#pragma unroll 1
+        for (int r = 0; r < 3; ++r)
+          tma_load_3d_warp(base + a * kQTileBytes + r * kQRegion, &maps.q, 64 * r, h, static_cast<int>(q0) + i0 + 256 * a + 128 * half,
+                           bar(B_QRAW + a), r == 0 ? kQTileBytes : 0);
+      }
       pdl_wait();
       const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
       const uint32_t kfull = cluster_addr(bar(B_KFULL), 0), vfull = cluster_addr(bar(B_VFULL), 0);
@@ -631,7 +639,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ph ^= 1;
         }
       }
-      if (half == 0 && lane == 0)  // no copy may still be writing either CTA's shared memory when the pair leaves
+      // no copy may still be writing either CTA's shared memory when the pair leaves
+      if (lane == 0)
+        for (int a = 0; a < 2; ++a)
+          if (nt[a] > 0) drain_wait(bar(B_QRAW + a), 0);
+      if (half == 0 && lane == 0)
         for (int i = max(0, j - kSlots); i < j; ++i) {
           drain_wait(bar(B_KFULL + i % kSlots), (i / kSlots) & 1);
           drain_wait(bar(B_VFULL + i % kSlots), (i / kSlots) & 1);
@@ -716,23 +728,32 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + 2 * a), 0);
     const int i = row0 + lane;
     float row_fac = 1.f;
-    if (nt[a] > 0) {  // this row's query to fp16, its largest value in [2^10, 2^11)
-      uint4 v[24];
-      const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (q0 + i) * p.q_token_stride +
-                                                       h * p.q_head_stride);
+    if (nt[a] > 0) {
+      // this row's query, copied in as bf16, to fp16 with its largest value in [2^10, 2^11). Small loops: straight-line
+      // code for the whole row took 6 to 8 us a CTA, most of it instruction fetch. Rows past the sequence's queries hold
+      // whatever follows them; their results are not stored.
+      const bool landed = warp_wait(bar(B_QRAW + a), 0, abort_s, err, kErrTimeoutFull);
+      const uint32_t q_row = base + a * kQTileBytes;
       unsigned top = 0;
-#pragma unroll
-      for (int k = 0; k < 24; ++k) v[k] = i < nq ? __ldg(qp + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < 24; ++k) top = finite_bits(v[k], top);
-      const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
-      row_fac = pow2(e);
-      const float f = p.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
-      auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
-#pragma unroll
-      for (int k = 0; k < 24; ++k)
-        st_shared_u4(sw128(base + a * kQTileBytes + (k >> 3) * kQRegion, 32 * wq + lane, k & 7), half2(v[k].x), half2(v[k].y),
-                     half2(v[k].z), half2(v[k].w));
+      if (landed) {
+#pragma unroll 4
+        for (int k = 0; k < 24; ++k) {
+          uint4 v;
+          ld_shared_u4(sw128(q_row + (k >> 3) * kQRegion, 32 * wq + lane, k & 7), v.x, v.y, v.z, v.w);
+          top = finite_bits(v, top);
+        }
+        const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
+        row_fac = pow2(e);
+        const float f = p.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
+        auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+#pragma unroll 2
+        for (int k = 0; k < 24; ++k) {
+          const uint32_t at = sw128(q_row + (k >> 3) * kQRegion, 32 * wq + lane, k & 7);
+          uint4 v;
+          ld_shared_u4(at, v.x, v.y, v.z, v.w);
+          st_shared_u4(at, half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(q_bar);
@@ -932,6 +953,9 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
         !tc_encode_2d(&at.kr, kF, p.kr, kRope, p.cap, kRope * 2, 64, kKTile / 2))
       return cudaErrorInvalidValue;
     at.vv = ex.vv;  // the same boxes
+    const int64_t q_size[3] = {kNope + kRope, p.num_heads, p.total_q}, q_pitch[2] = {2 * p.q_head_stride, 2 * p.q_token_stride};
+    const int q_box[3] = {64, 1, 128};
+    if (!tc_encode(&at.q, kBf, p.q, 3, q_size, q_pitch, q_box)) return cudaErrorInvalidValue;
     e = launch_next(gqa_mla_prefill_expand_kernel, 2, dim3(sm_count / 2 * 2), kExThreads, kExSmem, stream, p, ex);
     if (e != cudaSuccess) return e;
     e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,

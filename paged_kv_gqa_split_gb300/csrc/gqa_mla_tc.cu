@@ -684,17 +684,28 @@ cudaError_t launch_tc(const MlaParams& p, const MlaTcMaps& maps, int ctas, cudaS
 
 }  // namespace
 
+bool tc_encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const int64_t* size,
+               const int64_t* pitch, const int* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
+  if (fn == nullptr || rank < 2 || rank > 3) return false;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t boxes[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    if (size[i] < 1) return false;
+    dims[i] = static_cast<cuuint64_t>(size[i]);
+    boxes[i] = static_cast<cuuint32_t>(box[i]);
+    if (i > 0) strides[i - 1] = static_cast<cuuint64_t>(pitch[i - 1]);
+  }
+  return fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows,
                   int64_t pitch, int box_w, int box_rows) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
-  if (fn == nullptr || rows < 1) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_w), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const int64_t size[2] = {width, rows};
+  const int box[2] = {box_w, box_rows};
+  return tc_encode(map, type, base, 2, size, &pitch, box);
 }
 
 bool mla_tc_supported(int page_size) { return page_size > 0 && page_size % 32 == 0; }
