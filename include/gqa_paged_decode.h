@@ -408,7 +408,10 @@ int gqa_paged_decode_noalloc(const void* q, const void* k_cache, const void* v_c
  * or (2 i, 2 i + 1) (GQA_ROPE_INTERLEAVED). The angle is formed in 64-bit
  * integer arithmetic, so it does not lose precision at far positions; the
  * rotation is in fp32 and rounded once. positions: [num_tokens] int32;
- * inv_freq: [rot_dim / 2] double, both in device memory.
+ * inv_freq: [rot_dim / 2] finite doubles, both in device memory.
+ *
+ * The calls of this section are asynchronous on `stream`, allocate nothing and
+ * keep nothing between calls; they can be captured into a graph.
  */
 #define GQA_ROPE_HALF 0
 #define GQA_ROPE_INTERLEAVED 1
@@ -465,8 +468,8 @@ int gqa_rope(const void* x, const int32_t* positions, const double* inv_freq, fl
  * keeps its largest finite value within 448 (1 for a head of zeros, at least
  * 2^-126), its codes e4m3(value / scale), nearest even, of the fp32 values;
  * infinities become +-448 * scale and NaN the NaN code. Pointers 16-byte
- * aligned. Valid slots should be distinct. Asynchronous; num_tokens == 0
- * returns 0 without launching.
+ * aligned. Valid slots should be distinct: a page that two rows name may end up
+ * with parts of both. Asynchronous; num_tokens == 0 returns 0 without launching.
  */
 int gqa_rope_kv_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
                        const int32_t* slots, const double* inv_freq, float scale, int rot_offset, int rot_dim,

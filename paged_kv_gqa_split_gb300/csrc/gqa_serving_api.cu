@@ -14,6 +14,7 @@
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kMaxHeads = 1024;
 
@@ -290,7 +291,7 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
   if (q == nullptr || w_kv == nullptr || kv_cache == nullptr || block_table == nullptr || cache_seqlens == nullptr ||
       cu_seqlens_q == nullptr || out == nullptr)
     return GQA_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(softmax_scale)) return GQA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(softmax_scale * kLog2e)) return GQA_ERR_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(w_kv, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(cache_seqlens, 4) || !aligned(cu_seqlens_q, 4) ||
       !stride_ok(q_token_stride, 192, 8) || !stride_ok(q_head_stride, 192, 8))
@@ -306,7 +307,7 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
   p.lse = lse;
   p.q_token_stride = q_token_stride;
   p.q_head_stride = q_head_stride;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = softmax_scale * kLog2e;
   p.batch = batch;
   p.total_q = total_q;
   p.num_heads = num_heads;

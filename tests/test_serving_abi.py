@@ -111,7 +111,7 @@ def test_prefill_refusals(lib):
     assert lib.gqa_mla_prefill(*dict(ok, total=0, q=None).values()) == 0
     _refused(lib.gqa_mla_prefill, ok, [
         dict(batch=-1), dict(total=-1), dict(q=None), dict(w=None), dict(kv=None), dict(table=None), dict(lens=None),
-        dict(cu=None), dict(out=None), dict(scale=math.nan), dict(heads=0), dict(heads=1025), dict(page=0), dict(blocks=0),
+        dict(cu=None), dict(out=None), dict(scale=math.nan), dict(scale=3e38), dict(heads=0), dict(heads=1025), dict(page=0), dict(blocks=0),
         dict(width=0), dict(max_kv=-1), dict(max_kv=1 << 31), dict(blocks=1 << 26, page=64), dict(width=1 << 26, page=64),
         dict(q=A + 8), dict(w=A + 8), dict(kv=A + 2), dict(out=A + 8), dict(lse=A + 2), dict(table=A + 1), dict(qt=191),
         dict(qt=580), dict(qh=100)])
