@@ -201,11 +201,20 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
     }
     __syncthreads();
   }
+  // a maximum of integers: the order of the atomics does not matter; one a block (one a warp took 10 us)
+  __shared__ unsigned top_s[4][8];
   const unsigned top[4] = {top_c, top_r, top_k, top_v};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {  // a maximum of integers: the order of the atomics does not matter
+  for (int i = 0; i < 4; ++i) {
     const unsigned m = __reduce_max_sync(0xffffffffu, top[i]);
-    if (lane == 0 && m != 0) atomicMax(p.amax + i, m);
+    if (lane == 0) top_s[i][warp] = m;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    unsigned m = top_s[lane >> 3][lane & 7];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((lane & 7) == 0 && m != 0) atomicMax(p.amax + (lane >> 3), m);
   }
 }
 
