@@ -19,9 +19,11 @@
 // and, a weight of 0 times 0 being 0, no others.
 // Scores, softmax statistics and outputs accumulate in fp32.
 //
-// Steps, each a kernel: the plan (prefix sums over the sequences), the gather
-// (paged rows to packed rows, 128-aligned per sequence and zero-filled, and the
-// maxima), the expansion, the attention. Tensor-core bound.
+// Steps, each a kernel that starts while the one before it ends: the plan (prefix
+// sums over the sequences), the gather (paged rows to packed rows, 128-aligned per
+// sequence and zero-filled, and the maxima), the expansion, the attention. Bound by
+// the tensor cores: 8192 tokens x 16 heads 263 us in all (1440 TFLOP/s, 77 % of the
+// measured cuBLAS bf16 rate); five short prompts 33 us, the chain's latency.
 #include <cuda_bf16.h>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -262,8 +264,8 @@ __device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, vo
 // slots of 64 of the 512 values; the next tile's rows replace the old ones region by region
 // behind the MMAs. The accumulators of two units fill tensor memory, so a unit's epilogue
 // (scale, round to fp16, through shared memory and a tensor copy out) runs beside the next
-// unit's MMAs. Bound by the MMAs and, a fifth over them, the traffic of the copies out
-// (without them 32 heads of 16384 rows took 77 us instead of 97).
+// unit's MMAs. Bound by the MMAs and, a fifth over them, the traffic of the copies out:
+// 32 heads of 16384 rows take 94 us (1460 TFLOP/s), without the copies out 77.
 //
 // Roles in each CTA: an MMA warp (the even CTA's issues for both), a copy warp, a warp that
 // turns the rotary keys into scaled fp16 (once, with the first head), two epilogue
@@ -497,6 +499,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // seldom rescaled; probabilities are held times 2^7, at most 2^15, which keeps
 // small ones fp16 normals. Every wait is bounded: on a timeout the CTA flags
 // the device error word and leaves after draining its copies and MMAs.
+//
+// Measured: 8192 causal tokens x 16 heads 208 us (1650 TFLOP/s), 1024 tokens behind
+// 16384 x 32 heads 193 us (1720 TFLOP/s, on 64 of the 76 pairs).
 constexpr int kKTile = 128, kSlots = 3;
 constexpr int kQRegion = 128 * 128, kQTileBytes = 3 * kQRegion;  // 128 rows x 64 values; a CTA's half of a query tile
 constexpr int kKRegion = 64 * 128, kKSlot = 3 * kKRegion;        // 64 keys x 64 values

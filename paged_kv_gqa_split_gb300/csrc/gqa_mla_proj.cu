@@ -15,7 +15,9 @@
 // BM tokens (16, 64 or 128, so that up to 128 tokens read the weights once) and
 // streams K in chunks of 64 through a cp.async ring, absorb_q's two chunks at
 // once. The results go through shared memory to 16-byte stores: a fragment's own
-// are 4 bytes.
+// are 4 bytes. Measured, 128 tokens x 128 heads: absorb_q 14.5 us (42 MB), expand_out
+// 11.4 us (38 MB); 4 tokens x 16 heads: absorb_q 4.3 us. One wave of CTAs: its
+// latency, not bytes, is what is left.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
