@@ -18,6 +18,11 @@ import torch
 from ._lib import (FP8_ROW_BYTES, GQA_OK, GqaError, HEAD_DIM, MLA_D_QK, MLA_D_V, NUM_KV_HEADS, NUM_QO_HEADS, load,
                    mla_run)
 
+try:  # the allocation that compiled PyTorch programs call: no dispatch (3 us of a 14 us call on the GPU's host)
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 CACHE_BF16, CACHE_FP8 = 0, 1
@@ -26,70 +31,93 @@ MLA_D_HEAD = MLA_NOPE + MLA_ROPE  # query and expanded key values a head
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _check(device, dtype, contiguous, **tensors):
-    """Each tensor (None is skipped): on the GPU `device`, of `dtype` (None: any) and, if asked, contiguous."""
-    index = device.index
+def _ready(index, t, dtype):
+    """Whether t is a contiguous tensor of `dtype` on GPU `index`: the common case, in few steps."""
+    return isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.is_contiguous()
+
+
+def _check(index, dtype, contiguous, **tensors):
+    """Raises for the first tensor (None is skipped) that is not on GPU `index` (a CPU tensor's is -1), of `dtype`
+    (None: any) and, if asked, contiguous."""
     for name, t in tensors.items():
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != index or index is None:  # a CPU tensor's is -1
-            if not t.is_cuda:
-                raise ValueError(f"{name} is on {t.device}: the CUDA library has no CPU path; move inputs to the GPU")
-            raise ValueError(f"all tensors must be on {device}; {name} is on {t.device}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}: the CUDA library has no CPU path; move inputs to the GPU")
+        if t.get_device() != index:
+            raise ValueError(f"all tensors must be on cuda:{index}; {name} is on {t.device}")
         if dtype is not None and t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}")
         if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
 
-def _device(name, t):
+def _index(name, t):
+    """The GPU of t, the tensor that sets the call's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    return t.device
+    index = t.get_device()
+    if index < 0:
+        _check(index, None, False, **{name: t})
+    return index
+
+
+def _new(index, shape, dtype):
+    """An uninitialised contiguous tensor on GPU `index`."""
+    if _empty_strided_cuda is None or index != torch._C._cuda_getDevice():
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    stride, step = [], 1
+    for size in reversed(shape):
+        stride.insert(0, step)
+        step *= max(size, 1)
+    return _empty_strided_cuda(shape, tuple(stride), dtype)
 
 
 def _layout(layout):
-    if layout not in ROPE_LAYOUTS:
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    return ROPE_LAYOUTS[layout]
+    return code
 
 
-def _rotation(device, n, positions, inv_freq, pairs=None):
-    """(positions pointer, inv_freq pointer); inv_freq None: no rotation."""
+def _rotation(index, n, positions, inv_freq, pairs=None):
+    """(positions pointer, inv_freq pointer, pairs); inv_freq None: no rotation."""
     if inv_freq is None:
-        return None, None
+        return None, None, 0
     if positions is None:
         raise ValueError("a rotation needs positions")
-    _check(device, torch.int32, True, positions=positions)
-    _check(device, torch.float64, True, inv_freq=inv_freq)
+    if not _ready(index, positions, torch.int32) or not _ready(index, inv_freq, torch.float64):
+        _check(index, torch.int32, True, positions=positions)
+        _check(index, torch.float64, True, inv_freq=inv_freq)
     if positions.dim() != 1 or positions.shape[0] != n:
         raise ValueError(f"positions must be [{n}]")
-    if inv_freq.dim() != 1 or inv_freq.shape[0] < 1 or (pairs is not None and inv_freq.shape[0] != pairs):
+    have = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
+    if have < 1 or (pairs is not None and have != pairs):
         raise ValueError(f"inv_freq must be [{'pairs' if pairs is None else pairs}]")
-    return positions.data_ptr(), inv_freq.data_ptr()
+    return positions.data_ptr(), inv_freq.data_ptr(), have
 
 
 _entries = {}  # C entry points already looked up
 
 
-def _call(name, device, stream, made, *args):
-    """Calls the C entry on `stream` (default: the device's current stream) and raises on an error code;
+def _call(name, index, stream, made, *args):
+    """Calls the C entry on `stream` (default: GPU `index`'s current stream) and raises on an error code;
     `made`: tensors allocated here, kept from reuse until another stream is done with them."""
     fn = _entries.get(name)
     if fn is None:
         fn = _entries[name] = getattr(load(), name)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)  # current_stream() without building a Stream
+        handle = torch._C._cuda_getCurrentRawStream(index)  # current_stream() without building a Stream
     else:
         handle = stream.cuda_stream
         for t in made:
             t.record_stream(stream)
-    if device.index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
     if rc != GQA_OK:
         raise GqaError(rc, name)
@@ -127,27 +155,27 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, scale
     """Rotary positions on x [N, heads, dim] (bf16, fp16 or fp32; any token and head strides): the window of
     2 * len(inv_freq) values from rot_offset is turned, the rest copied. out: a tensor like x, possibly x itself
     (default: a new contiguous one). inverse turns back, and is the gradient."""
-    dev = _device("x", x)
-    _check(dev, None, False, x=x)
-    if x.dim() != 3 or x.dtype not in _TYPES:
+    index = _index("x", x)
+    code = _TYPES.get(x.dtype)
+    if code is None or x.dim() != 3:
         raise ValueError("x must be [N, heads, dim] in bfloat16, float16 or float32")
     n, heads, dim = x.shape
     if inv_freq is None:
         raise ValueError("rope needs inv_freq")
-    pos, freq = _rotation(dev, n, positions, inv_freq)
+    pos, freq, pairs = _rotation(index, n, positions, inv_freq)
     made = ()
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=x.dtype, device=dev)
+        out = _new(index, (n, heads, dim), x.dtype)
         made = (out,)
     else:
-        _check(dev, x.dtype, False, out=out)
+        _check(index, x.dtype, False, out=out)
         if out.shape != x.shape:
             raise ValueError("out must have x's shape")
     (xt, xh, xe), (ot, oh, oe) = x.stride(), out.stride()
     if (xe != 1 or oe != 1) and dim > 1:
         raise ValueError("a head's values must be contiguous")
-    _call("gqa_rope", dev, stream, made, x.data_ptr(), pos, freq, scale, out.data_ptr(), n, heads, dim, rot_offset,
-          2 * inv_freq.shape[0], _layout(layout), 1 if inverse else 0, _TYPES[x.dtype], xt, xh, ot, oh)
+    _call("gqa_rope", index, stream, made, x.data_ptr(), pos, freq, scale, out.data_ptr(), n, heads, dim, rot_offset,
+          2 * pairs, _layout(layout), 1 if inverse else 0, code, xt, xh, ot, oh)
     return out
 
 
@@ -173,31 +201,31 @@ def rope_kv_append(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.
     """One pass over a step's new tokens: q [N, 32, 128] and k_new [N, 4, 128] turned by their positions (inv_freq
     None: not turned), k_new and v_new stored in pages slots[r] of bf16 caches [P, 1, 4, 128] or FP8 caches [P, 528]
     (quantised). q, k_new and v_new may be views of one fused row. Returns the turned q (None without q)."""
-    dev = _device("k_cache", k_cache)
-    _check(dev, torch.bfloat16, False, q=q, k_new=k_new, v_new=v_new, q_out=q_out)
-    _check(dev, None, True, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
-    _check(dev, torch.int32, True, slots=slots)
+    index = _index("k_cache", k_cache)
+    _check(index, torch.bfloat16, False, q=q, k_new=k_new, v_new=v_new, q_out=q_out)
+    _check(index, None, True, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    if not _ready(index, slots, torch.int32):
+        _check(index, torch.int32, True, slots=slots)
     fmt, pages = _cache_format(k_cache, v_cache)
     if slots.dim() != 1:
         raise ValueError("slots must be [N]")
     n = slots.shape[0]
     ks, vs = _token_stride("k_new", k_new, NUM_KV_HEADS, HEAD_DIM), _token_stride("v_new", v_new, NUM_KV_HEADS, HEAD_DIM)
-    qs, made = 0, ()
+    qs, q_ptr, out_ptr, made = 0, None, None, ()
     if q is not None:
         qs = _token_stride("q", q, NUM_QO_HEADS, HEAD_DIM)
         if q_out is None:
-            q_out = torch.empty((n, NUM_QO_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            q_out = _new(index, (n, NUM_QO_HEADS, HEAD_DIM), torch.bfloat16)
             made = (q_out,)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k_new.shape[0] != n or v_new.shape[0] != n or (q is not None and (q.shape[0] != n or q_out.shape != q.shape)):
         raise ValueError("q, k_new, v_new and q_out must have one row per slot")
-    pos, freq = _rotation(dev, n, positions, inv_freq)
-    _call("gqa_rope_kv_append", dev, stream, made, q.data_ptr() if q is not None else None, k_new.data_ptr(),
-          v_new.data_ptr(), pos, slots.data_ptr(), freq, scale, rot_offset,
-          2 * inv_freq.shape[0] if inv_freq is not None else 0, _layout(layout),
-          q_out.data_ptr() if q_out is not None else None, k_cache.data_ptr(), v_cache.data_ptr(), fmt, n, pages, qs,
-          ks, vs)
+    pos, freq, pairs = _rotation(index, n, positions, inv_freq)
+    _call("gqa_rope_kv_append", index, stream, made, q_ptr, k_new.data_ptr(), v_new.data_ptr(), pos, slots.data_ptr(),
+          freq, scale, rot_offset, 2 * pairs, _layout(layout), out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), fmt, n,
+          pages, qs, ks, vs)
     return q_out
 
 
@@ -215,24 +243,27 @@ def kv_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, indices: torch.Ten
                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The rows of pages indices[r] of FP8 caches [P, 528] as bfloat16 ([N, 4, 128] each); zeros for a page outside
     [0, P)."""
-    dev = _device("k_cache", k_cache)
-    _check(dev, torch.uint8, True, k_cache=k_cache, v_cache=v_cache)
-    _check(dev, torch.int32, True, indices=indices)
-    _, pages = _cache_format(k_cache, v_cache)
+    index = _index("k_cache", k_cache)
+    if not (_ready(index, k_cache, torch.uint8) and _ready(index, v_cache, torch.uint8) and
+            _ready(index, indices, torch.int32)):
+        _check(index, torch.uint8, True, k_cache=k_cache, v_cache=v_cache)
+        _check(index, torch.int32, True, indices=indices)
+    pages = _cache_format(k_cache, v_cache)[1]
     if indices.dim() != 1:
         raise ValueError("indices must be [N]")
-    shape, made = (indices.shape[0], NUM_KV_HEADS, HEAD_DIM), []
-    _check(dev, torch.bfloat16, True, k_out=k_out, v_out=v_out)
+    n = indices.shape[0]
+    shape, made = (n, NUM_KV_HEADS, HEAD_DIM), []
+    _check(index, torch.bfloat16, True, k_out=k_out, v_out=v_out)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = _new(index, shape, torch.bfloat16)
         made.append(k_out)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = _new(index, shape, torch.bfloat16)
         made.append(v_out)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out and v_out must be {shape}")
-    _call("gqa_paged_kv_read_fp8", dev, stream, made, k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
-          k_out.data_ptr(), v_out.data_ptr(), shape[0], pages)
+    _call("gqa_paged_kv_read_fp8", index, stream, made, k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), n, pages)
     return k_out, v_out
 
 
@@ -248,34 +279,37 @@ def mla_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, slots: torch.Tenso
                   stream: Optional[torch.cuda.Stream] = None) -> None:
     """Store latent [N, 512] and the (turned) rotary key k_rope [N, 64] in slots[r] = block * page_size + offset of
     kv_cache [num_blocks, page_size, 1, 576] (in place); other slots are skipped."""
-    dev = _device("kv_cache", kv_cache)
-    _check(dev, torch.bfloat16, True, kv_cache=kv_cache)
-    _check(dev, torch.bfloat16, False, latent=latent, k_rope=k_rope)
-    _check(dev, torch.int32, True, slots=slots)
+    index = _index("kv_cache", kv_cache)
+    _check(index, torch.bfloat16, True, kv_cache=kv_cache)
+    _check(index, torch.bfloat16, False, latent=latent, k_rope=k_rope)
+    _check(index, torch.int32, True, slots=slots)
     blocks, page = _latent_cache(kv_cache)
     n = slots.shape[0] if slots.dim() == 1 else -1
     for name, t, d in (("latent", latent, MLA_D_V), ("k_rope", k_rope, MLA_ROPE)):
         if t.dim() != 2 or t.shape != (n, d) or t.stride(1) != 1:
             raise ValueError(f"{name} must be [N, {d}] with contiguous rows, one per slot")
-    pos, freq = _rotation(dev, n, positions, inv_freq, MLA_ROPE // 2)
-    _call("gqa_mla_kv_append", dev, stream, (), latent.data_ptr(), k_rope.data_ptr(), pos, slots.data_ptr(), freq, scale,
+    pos, freq, _ = _rotation(index, n, positions, inv_freq, MLA_ROPE // 2)
+    _call("gqa_mla_kv_append", index, stream, (), latent.data_ptr(), k_rope.data_ptr(), pos, slots.data_ptr(), freq, scale,
           _layout(layout), kv_cache.data_ptr(), n, blocks * page, latent.stride(0) if n > 1 else MLA_D_V,
           k_rope.stride(0) if n > 1 else MLA_ROPE)
 
 
 # --------------------------------------------------------- latent attention
-def _weights(w_kv, heads, dev):
-    _check(dev, torch.bfloat16, True, w_kv=w_kv)
+def _weights(w_kv, heads, index):
+    if not _ready(index, w_kv, torch.bfloat16):
+        _check(index, torch.bfloat16, True, w_kv=w_kv)
     if w_kv.shape != (heads, MLA_NOPE + MLA_HEAD_V, MLA_D_V):
         raise ValueError(f"w_kv must be [{heads}, {MLA_NOPE + MLA_HEAD_V}, {MLA_D_V}]")
     return w_kv.data_ptr()
 
 
 def _query(q):
-    if q.dim() != 3 or q.shape[2] != MLA_D_HEAD or q.stride(2) != 1:
-        raise ValueError(f"q must be [N, heads, {MLA_D_HEAD}] with contiguous heads")
+    """(N, heads, token stride, head stride) of q [N, heads, 192]."""
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != MLA_D_HEAD or q.stride(2) != 1:
+        raise ValueError(f"q must be bfloat16 [N, heads, {MLA_D_HEAD}] with contiguous heads")
     n, h, d = q.shape
-    return n, h, q.stride(0) if n > 1 else h * d, q.stride(1) if h > 1 else d
+    ts, hs, _ = q.stride()
+    return n, h, ts if n > 1 else h * d, hs if h > 1 else d
 
 
 def mla_absorb_q(q: torch.Tensor, w_kv: torch.Tensor, positions: Optional[torch.Tensor] = None,
@@ -283,20 +317,19 @@ def mla_absorb_q(q: torch.Tensor, w_kv: torch.Tensor, positions: Optional[torch.
                  out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """q [N, heads, 192] to the latent decode's queries [N, heads, 576]: q[..., :128] w_kv[h, :128], then the 64 rotary
     values (turned by positions if inv_freq [32] is given). w_kv: [heads, 256, 512]."""
-    dev = _device("q", q)
-    _check(dev, torch.bfloat16, False, q=q)
+    index = _index("q", q)
     n, h, ts, hs = _query(q)
-    w = _weights(w_kv, h, dev)
-    pos, freq = _rotation(dev, n, positions, inv_freq, MLA_ROPE // 2)
+    w = _weights(w_kv, h, index)
+    pos, freq, _ = _rotation(index, n, positions, inv_freq, MLA_ROPE // 2)
     made = ()
     if out is None:
-        out = torch.empty((n, h, MLA_D_QK), dtype=torch.bfloat16, device=dev)
+        out = _new(index, (n, h, MLA_D_QK), torch.bfloat16)
         made = (out,)
     else:
-        _check(dev, torch.bfloat16, True, out=out)
+        _check(index, torch.bfloat16, True, out=out)
         if out.shape != (n, h, MLA_D_QK):
             raise ValueError(f"out must be {(n, h, MLA_D_QK)}")
-    _call("gqa_mla_absorb_q", dev, stream, made, q.data_ptr(), w, pos, freq, scale, _layout(layout), out.data_ptr(), n, h,
+    _call("gqa_mla_absorb_q", index, stream, made, q.data_ptr(), w, pos, freq, scale, _layout(layout), out.data_ptr(), n, h,
           ts, hs)
     return out
 
@@ -304,21 +337,22 @@ def mla_absorb_q(q: torch.Tensor, w_kv: torch.Tensor, positions: Optional[torch.
 def mla_expand_out(o_latent: torch.Tensor, w_kv: torch.Tensor, out: Optional[torch.Tensor] = None,
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The latent decode's output [N, heads, 512] to the heads' values [N, heads, 128]: w_kv[h, 128:] o_latent."""
-    dev = _device("o_latent", o_latent)
-    _check(dev, torch.bfloat16, True, o_latent=o_latent)
+    index = _index("o_latent", o_latent)
+    if not _ready(index, o_latent, torch.bfloat16):
+        _check(index, torch.bfloat16, True, o_latent=o_latent)
     if o_latent.dim() != 3 or o_latent.shape[2] != MLA_D_V:
         raise ValueError(f"o_latent must be [N, heads, {MLA_D_V}]")
     n, h, _ = o_latent.shape
-    w = _weights(w_kv, h, dev)
+    w = _weights(w_kv, h, index)
     made = ()
     if out is None:
-        out = torch.empty((n, h, MLA_HEAD_V), dtype=torch.bfloat16, device=dev)
+        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16)
         made = (out,)
     else:
-        _check(dev, torch.bfloat16, True, out=out)
+        _check(index, torch.bfloat16, True, out=out)
         if out.shape != (n, h, MLA_HEAD_V):
             raise ValueError(f"out must be {(n, h, MLA_HEAD_V)}")
-    _call("gqa_mla_expand_out", dev, stream, made, o_latent.data_ptr(), w, out.data_ptr(), n, h)
+    _call("gqa_mla_expand_out", index, stream, made, o_latent.data_ptr(), w, out.data_ptr(), n, h)
     return out
 
 
@@ -353,12 +387,14 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
     cache_seqlens [B] list, the new ones among them. max_kv_tokens: a bound on the sum of cache_seqlens, which sizes
     the workspace (default: what the block table can list). Returns (out [total, heads, 128] bf16, lse [heads, total]
     fp32 natural log, or None)."""
-    dev = _device("q", q)
-    _check(dev, torch.bfloat16, False, q=q)
-    _check(dev, torch.bfloat16, True, kv_cache=kv_cache, out=out)
-    _check(dev, torch.int32, True, block_table=block_table, cache_seqlens=cache_seqlens, cu_seqlens_q=cu_seqlens_q)
+    index = _index("q", q)
     n, h, ts, hs = _query(q)
-    w = _weights(w_kv, h, dev)
+    w = _weights(w_kv, h, index)
+    if not (_ready(index, kv_cache, torch.bfloat16) and _ready(index, block_table, torch.int32) and
+            _ready(index, cache_seqlens, torch.int32) and _ready(index, cu_seqlens_q, torch.int32)):
+        _check(index, torch.bfloat16, True, kv_cache=kv_cache)
+        _check(index, torch.int32, True, block_table=block_table, cache_seqlens=cache_seqlens, cu_seqlens_q=cu_seqlens_q)
+    _check(index, torch.bfloat16, True, out=out)
     blocks, page = _latent_cache(kv_cache)
     if block_table.dim() != 2 or cache_seqlens.shape != (block_table.shape[0],) or \
             cu_seqlens_q.shape != (block_table.shape[0] + 1,):
@@ -370,16 +406,16 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         softmax_scale = 1.0 / math.sqrt(MLA_D_HEAD)
     made = []
     if out is None:
-        out = torch.empty((n, h, MLA_HEAD_V), dtype=torch.bfloat16, device=dev)
+        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16)
         made.append(out)
     elif out.shape != (n, h, MLA_HEAD_V):
         raise ValueError(f"out must be {(n, h, MLA_HEAD_V)}")
     if lse is not None:
-        _check(dev, torch.float32, True, lse=lse)
+        _check(index, torch.float32, True, lse=lse)
         if lse.shape != (h, n):
             raise ValueError(f"lse must be {(h, n)}")
     elif with_lse:
-        lse = torch.empty((h, n), dtype=torch.float32, device=dev)
+        lse = _new(index, (h, n), torch.float32)
         made.append(lse)
     if b == 0 or n == 0:
         return out, lse
@@ -387,11 +423,11 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         size = load().gqa_mla_prefill_ws_size(b, h, max_kv_tokens)
         if size == 0:
             raise ValueError(f"batch {b}, heads {h} and max_kv_tokens {max_kv_tokens} are out of range")
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        workspace = _new(index, (size,), torch.uint8)
         made.append(workspace)
     else:
-        _check(dev, None, True, workspace=workspace)
-    _call("gqa_mla_prefill", dev, stream, made, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
+        _check(index, None, True, workspace=workspace)
+    _call("gqa_mla_prefill", index, stream, made, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
           cache_seqlens.data_ptr(), cu_seqlens_q.data_ptr(), softmax_scale, 1 if causal else 0, out.data_ptr(),
           lse.data_ptr() if lse is not None else None, b, n, h, page, blocks, width, max_kv_tokens, ts, hs,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
