@@ -264,6 +264,7 @@ struct MlaProjParams {  // gqa_mla_proj.cu
   int64_t x_token_stride, x_head_stride;
   float scale;
   int num_tokens, num_heads, out_width, layout;
+  int* err;
 };
 cudaError_t launch_mla_absorb_q(const MlaProjParams& p, cudaStream_t stream);
 cudaError_t launch_mla_expand_out(const MlaProjParams& p, cudaStream_t stream);

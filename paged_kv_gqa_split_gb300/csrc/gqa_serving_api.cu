@@ -242,6 +242,7 @@ int gqa_mla_absorb_q(const void* q, const void* w_kv, const int32_t* positions, 
   p.num_heads = num_heads;
   p.out_width = 576;
   p.layout = inv_freq != nullptr ? layout : GQA_ROPE_HALF;
+  if (gqa::device_error_word(&p.err) != cudaSuccess) return GQA_ERR_LAUNCH;
   return launched(gqa::launch_mla_absorb_q(p, stream));
 }
 
@@ -265,6 +266,7 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
   p.num_tokens = num_tokens;
   p.num_heads = num_heads;
   p.out_width = 128;
+  if (gqa::device_error_word(&p.err) != cudaSuccess) return GQA_ERR_LAUNCH;
   return launched(gqa::launch_mla_expand_out(p, stream));
 }
 

@@ -31,6 +31,11 @@ MLA_D_HEAD = MLA_NOPE + MLA_ROPE  # query and expanded key values a head
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _on(index, t, dtype):
+    """Whether t is a tensor of `dtype` on GPU `index`."""
+    return isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype
+
+
 def _ready(index, t, dtype):
     """Whether t is a contiguous tensor of `dtype` on GPU `index`: the common case, in few steps."""
     return isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.is_contiguous()
@@ -201,10 +206,12 @@ def rope_kv_append(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.
     """One pass over a step's new tokens: q [N, 32, 128] and k_new [N, 4, 128] turned by their positions (inv_freq
     None: not turned), k_new and v_new stored in pages slots[r] of bf16 caches [P, 1, 4, 128] or FP8 caches [P, 528]
     (quantised). q, k_new and v_new may be views of one fused row. Returns the turned q (None without q)."""
-    index = _index("k_cache", k_cache)
-    _check(index, torch.bfloat16, False, q=q, k_new=k_new, v_new=v_new, q_out=q_out)
-    _check(index, None, True, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
-    if not _ready(index, slots, torch.int32):
+    index, bf = _index("k_cache", k_cache), torch.bfloat16
+    if not (_on(index, k_new, bf) and _on(index, v_new, bf) and (q is None or _on(index, q, bf)) and
+            (q_out is None or _ready(index, q_out, bf)) and k_cache.is_contiguous() and
+            _ready(index, v_cache, k_cache.dtype) and _ready(index, slots, torch.int32)):
+        _check(index, bf, False, q=q, k_new=k_new, v_new=v_new, q_out=q_out)
+        _check(index, None, True, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
         _check(index, torch.int32, True, slots=slots)
     fmt, pages = _cache_format(k_cache, v_cache)
     if slots.dim() != 1:
