@@ -537,9 +537,10 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
  * -inf. A token whose block lies outside [0, num_blocks) is left out; lengths
  * are clamped as in gqa_mla_decode. A token whose latent row is not all finite
  * makes the rows that see it NaN, and no others. Rows past cu_seqlens_q[batch] are left as
- * they were. The expanded keys and values are fp16 (scaled by a power of two
- * where the values need it); everything else accumulates in fp32. lse carries
- * that rounding of the keys: about 2^-12 of a score's size.
+ * they were. The expanded keys and values are fp16, scaled by a power of two per
+ * sequence (values below about 2^-29 of 512 * max|latent| * max|w_kv| lose bits);
+ * everything else accumulates in fp32. lse carries that rounding of the keys:
+ * about 2^-12 of a score's size.
  *
  * max_kv_tokens bounds the sum of the lengths on the host (it sizes the
  * workspace); sequences past it see no token and set bit 64 of the device error

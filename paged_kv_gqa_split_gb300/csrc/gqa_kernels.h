@@ -289,7 +289,7 @@ struct MlaPrefillParams {
   int* kv_start;  // [batch + 1] first packed row (multiples of 128)
   int* q_start;   // [batch][2] first query row and query count, cut to [0, total_q)
   int* qt_start;  // [batch + 1] first query tile
-  unsigned* amax;      // [4] largest finite |value| bits: latent, rotary key, key weights, value weights
+  unsigned* amax;      // largest finite |value| bits: key weights, value weights, then [batch][2] latent, rotary key
   unsigned* valid;     // [cap / 32] packed rows that hold a token of the pool
   unsigned* bad;       // [cap / 32] packed rows whose latent is not all finite
   void* lat;           // [cap][512] bf16

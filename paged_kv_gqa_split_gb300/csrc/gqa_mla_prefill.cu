@@ -12,8 +12,8 @@
 // bits against bf16's 8: with bf16 the output was 1.6 x further from the 64-bit
 // result than one rounding of it, with fp16 1.01 x). fp16's range is kept by
 // powers of two, which change nothing else: a query row is brought to a largest
-// value in [2^10, 2^11); keys and values have one exponent each, from the bound
-// 512 * max|c| * max|W| (and the rotary keys). The maxima are taken over finite
+// value in [2^10, 2^11); keys and values of a sequence have one exponent each, from the
+// bound 512 * max|c| * max|W| (and the rotary keys). The maxima are taken over finite
 // values, so an infinity stays with its row: a token whose latent is not all
 // finite gets NaN keys and zero values, which makes the rows that see it NaN
 // and, a weight of 0 times 0 being 0, no others.
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
   __shared__ int sq[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
-  if (tid < 4) p.amax[tid] = 0;
+  if (tid < 2) p.amax[tid] = 0;
   int64_t base_k = 0;
   int base_q = 0;
   const int64_t table = static_cast<int64_t>(p.width) * p.page_size;
@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
       if (nq > 0) len = static_cast<int>(min(static_cast<int64_t>(max(n, 0)), table));
       p.q_start[2 * b] = qs;
       p.q_start[2 * b + 1] = nq;
+      p.amax[2 + 2 * b] = p.amax[3 + 2 * b] = 0;
     }
     const int64_t rows = (static_cast<int64_t>(len) + kAlign - 1) / kAlign * kAlign;
     int64_t k = rows;
@@ -150,8 +151,8 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
 // plan's results are needed, a warp per weight row for the maxima.
 __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPrefillParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned top_c = 0, top_r = 0, top_k = 0, top_v = 0;
-  __shared__ unsigned bad_s[8];
+  unsigned top_k = 0, top_v = 0;
+  __shared__ unsigned group_s[3][8];  // of each warp: rows not finite, largest latent, largest rotary key
   pdl_launch_dependents();
   const int wrows = p.num_heads * (kNope + kHeadV);
 #pragma unroll 4
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
       v[i][1] = from >= 0 ? __ldg(src + 32 + lane) : zero;
       v[i][2] = from >= 0 && lane < 8 ? __ldg(src + 64 + lane) : zero;
     }
-    unsigned bad = 0;
+    unsigned bad = 0, top_c = 0, top_r = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t row = 32 * g + 4 * warp + i;
@@ -195,36 +196,51 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
       top_r = finite_bits(v[i][2], top_r);
       if (__any_sync(0xffffffffu, not_finite(v[i][0]) || not_finite(v[i][1]))) bad |= 1u << (4 * warp + i);
     }
-    if (lane == 0) bad_s[warp] = bad;
+    top_c = __reduce_max_sync(0xffffffffu, top_c);
+    top_r = __reduce_max_sync(0xffffffffu, top_r);
+    if (lane == 0) {
+      group_s[0][warp] = bad;
+      group_s[1][warp] = top_c;
+      group_s[2][warp] = top_r;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      p.valid[g] = ok;
-      p.bad[g] = bad_s[0] | bad_s[1] | bad_s[2] | bad_s[3] | bad_s[4] | bad_s[5] | bad_s[6] | bad_s[7];
+    if (warp == 0) {  // lanes 0..7, 8..15 and 16..23 combine the three
+      unsigned m = lane < 24 ? group_s[lane >> 3][lane & 7] : 0;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const unsigned other = __shfl_xor_sync(0xffffffffu, m, o);
+        m = lane < 8 ? m | other : max(m, other);
+      }
+      if (lane == 0) {
+        p.valid[g] = ok;
+        p.bad[g] = m;
+      }
+      // a maximum of integers: the order of the atomics does not matter
+      if ((lane == 8 || lane == 16) && m != 0) atomicMax(p.amax + 2 + 2 * b + (lane >> 4), m);
     }
     __syncthreads();
   }
-  // a maximum of integers: the order of the atomics does not matter; one a block (one a warp took 10 us)
-  __shared__ unsigned top_s[4][8];
-  const unsigned top[4] = {top_c, top_r, top_k, top_v};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned m = __reduce_max_sync(0xffffffffu, top[i]);
-    if (lane == 0) top_s[i][warp] = m;
+  __shared__ unsigned top_s[2][8];
+  top_k = __reduce_max_sync(0xffffffffu, top_k);
+  top_v = __reduce_max_sync(0xffffffffu, top_v);
+  if (lane == 0) {
+    top_s[0][warp] = top_k;
+    top_s[1][warp] = top_v;
   }
   __syncthreads();
-  if (warp == 0) {
-    unsigned m = top_s[lane >> 3][lane & 7];
+  if (warp == 0) {  // one atomic a block (one a warp took 10 us)
+    unsigned m = lane < 16 ? top_s[lane >> 3][lane & 7] : 0;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((lane & 7) == 0 && m != 0) atomicMax(p.amax + (lane >> 3), m);
+    if ((lane == 0 || lane == 8) && m != 0) atomicMax(p.amax + (lane >> 3), m);
   }
 }
 
-// Exponents that bring keys and values into fp16 (value * 2^-e):
+// Exponents that bring a sequence's keys and values into fp16 (value * 2^-e):
 // |c . w| <= 512 max|c| max|w| < 2^(Ec + 1 + Ew + 1 + 9), to be below 2^15.
 __device__ __forceinline__ int exponent_of(unsigned bits) { return static_cast<int>(bits >> 23) - 127; }
-__device__ __forceinline__ void kv_exponents(const unsigned* amax, int& ek, int& ev) {
-  const unsigned c = __ldcg(amax), r = __ldcg(amax + 1), wk = __ldcg(amax + 2), wv = __ldcg(amax + 3);
+__device__ __forceinline__ void kv_exponents(const unsigned* amax, int b, int& ek, int& ev) {
+  const unsigned wk = __ldcg(amax), wv = __ldcg(amax + 1), c = __ldcg(amax + 2 + 2 * b), r = __ldcg(amax + 3 + 2 * b);
   ek = r != 0 ? exponent_of(r) + 1 - 15 : -126;
   if (c != 0 && wk != 0) ek = max(ek, exponent_of(c) + exponent_of(wk) + 11 - 15);
   ev = c != 0 && wv != 0 ? exponent_of(c) + exponent_of(wv) + 11 - 15 : 0;
@@ -393,12 +409,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    int ek, ev;
-    kv_exponents(p.amax, ek, ev);
-    const float f = pow2(-ek);
     for (int u = u0; u < u1 && p.head0 == 0; ++u) {
       const int m0 = tile_of(u) * 256 + 128 * half;
       if (u % p.heads != 0 || m0 >= total) continue;  // once a tile, whichever pair has its first unit
+      int ek, ev;
+      kv_exponents(p.amax, find_seq(p.kv_start, p.batch, m0), ek, ev);  // 128 rows are one sequence's
+      const float f = pow2(-ek);
       uint4* kr = reinterpret_cast<uint4*>(p.kr) + static_cast<int64_t>(m0) * (kRope / 8);
 #pragma unroll 4
       for (int i = lane; i < 128 * kRope / 8; i += 32) {
@@ -411,9 +427,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const int part = (warp >> 2) - 1;  // 0: keys, 1: values
     const int wq = warp & 3, row = 32 * wq + lane;
     const bool issuer = wq == 0 && lane == 0;
-    int ek, ev;
-    kv_exponents(p.amax, ek, ev);
-    const float f = pow2(part == 0 ? -ek : -ev);
+    float f = 1.f;
     const uint32_t of_bad = part == 0 ? 0x7fff7fffu : 0u;
     const uint32_t dfree = cluster_addr(bar(E_DFREE), 0);
     const uint32_t dst = base + kExOut + part * kExRegion;
@@ -422,7 +436,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
     for (int u = u0; u < u1; ++u) {
       const int i = u - u0, m0 = tile_of(u) * 256 + 128 * half;  // this CTA's packed rows (may lie past the last one)
       const bool out = m0 < total;
-      if (first_of_tile(u)) bad = out && ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+      if (first_of_tile(u) && out) {  // 128 rows are one sequence's
+        int ek, ev;
+        kv_exponents(p.amax, find_seq(p.kv_start, p.batch, m0), ek, ev);
+        f = pow2(part == 0 ? -ek : -ev);
+        bad = ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+      }
       const bool good = warp_wait(bar(E_DFULL + (i & 1)), (i >> 1) & 1, abort_s, err, kErrTimeoutFull);
       int every;  // the four warps agree, so that none is left at the barriers below
       asm volatile(
@@ -773,7 +792,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (lane == 0) mbar_arrive_cluster(q_bar);
     }
     int ek, ev;
-    kv_exponents(p.amax, ek, ev);
+    kv_exponents(p.amax, b, ek, ev);
     const float sc = fmaxf(row_fac * fabsf(p.scale_log2) * pow2(ek), 1e-37f);  // > 0: -inf * sc stays -inf
     const int lim = p.causal ? n - nq + i : INT_MAX;          // last key this row sees
     const int lim0 = p.causal ? n - nq + row0 : INT_MAX;      // and the warp's first row
@@ -903,7 +922,7 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
   p->kv_start = reinterpret_cast<int*>(take((B + 1) * 4));
   p->q_start = reinterpret_cast<int*>(take(B * 8));
   p->qt_start = reinterpret_cast<int*>(take((B + 1) * 4));
-  p->amax = reinterpret_cast<unsigned*>(take(16));
+  p->amax = reinterpret_cast<unsigned*>(take((2 + 2 * B) * 4));
   p->valid = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
   p->bad = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
   p->lat = take(cap * kLat * 2);

@@ -5,7 +5,8 @@ Rotary positions (``rope_inv_freq``, ``rope``), the cache's write and read
 latent attention's projections and prompt pass (``mla_absorb_q``,
 ``mla_expand_out``, ``mla_absorbed_run``, ``mla_prefill``). As in ``_lib``:
 argument checks and marshalling only, no CPU path; a call runs on the current
-stream of its tensors' device unless ``stream`` is given.
+stream of its tensors' device unless ``stream`` is given (what the call
+allocates then belongs to that stream).
 """
 from __future__ import annotations
 
@@ -69,8 +70,11 @@ def _index(name, t):
     return index
 
 
-def _new(index, shape, dtype):
-    """An uninitialised contiguous tensor on GPU `index`."""
+def _new(index, shape, dtype, stream):
+    """An uninitialised contiguous tensor on GPU `index`, in the memory of the stream that the call runs on."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
     if _empty_strided_cuda is None or index != torch._C._cuda_getDevice():
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
     stride, step = [], 1
@@ -107,18 +111,13 @@ def _rotation(index, n, positions, inv_freq, pairs=None):
 _entries = {}  # C entry points already looked up
 
 
-def _call(name, index, stream, made, *args):
-    """Calls the C entry on `stream` (default: GPU `index`'s current stream) and raises on an error code;
-    `made`: tensors allocated here, kept from reuse until another stream is done with them."""
+def _call(name, index, stream, *args):
+    """Calls the C entry on `stream` (default: GPU `index`'s current stream) and raises on an error code."""
     fn = _entries.get(name)
     if fn is None:
         fn = _entries[name] = getattr(load(), name)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)  # current_stream() without building a Stream
-    else:
-        handle = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
+    # the current stream's handle, without building a Stream
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
@@ -168,10 +167,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, scale
     if inv_freq is None:
         raise ValueError("rope needs inv_freq")
     pos, freq, pairs = _rotation(index, n, positions, inv_freq)
-    made = ()
     if out is None:
-        out = _new(index, (n, heads, dim), x.dtype)
-        made = (out,)
+        out = _new(index, (n, heads, dim), x.dtype, stream)
     else:
         _check(index, x.dtype, False, out=out)
         if out.shape != x.shape:
@@ -179,7 +176,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, scale
     (xt, xh, xe), (ot, oh, oe) = x.stride(), out.stride()
     if (xe != 1 or oe != 1) and dim > 1:
         raise ValueError("a head's values must be contiguous")
-    _call("gqa_rope", index, stream, made, x.data_ptr(), pos, freq, scale, out.data_ptr(), n, heads, dim, rot_offset,
+    _call("gqa_rope", index, stream, x.data_ptr(), pos, freq, scale, out.data_ptr(), n, heads, dim, rot_offset,
           2 * pairs, _layout(layout), 1 if inverse else 0, code, xt, xh, ot, oh)
     return out
 
@@ -218,19 +215,18 @@ def rope_kv_append(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.
         raise ValueError("slots must be [N]")
     n = slots.shape[0]
     ks, vs = _token_stride("k_new", k_new, NUM_KV_HEADS, HEAD_DIM), _token_stride("v_new", v_new, NUM_KV_HEADS, HEAD_DIM)
-    qs, q_ptr, out_ptr, made = 0, None, None, ()
+    qs, q_ptr, out_ptr = 0, None, None
     if q is not None:
         qs = _token_stride("q", q, NUM_QO_HEADS, HEAD_DIM)
         if q_out is None:
-            q_out = _new(index, (n, NUM_QO_HEADS, HEAD_DIM), torch.bfloat16)
-            made = (q_out,)
+            q_out = _new(index, (n, NUM_QO_HEADS, HEAD_DIM), torch.bfloat16, stream)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k_new.shape[0] != n or v_new.shape[0] != n or (q is not None and (q.shape[0] != n or q_out.shape != q.shape)):
         raise ValueError("q, k_new, v_new and q_out must have one row per slot")
     pos, freq, pairs = _rotation(index, n, positions, inv_freq)
-    _call("gqa_rope_kv_append", index, stream, made, q_ptr, k_new.data_ptr(), v_new.data_ptr(), pos, slots.data_ptr(),
+    _call("gqa_rope_kv_append", index, stream, q_ptr, k_new.data_ptr(), v_new.data_ptr(), pos, slots.data_ptr(),
           freq, scale, rot_offset, 2 * pairs, _layout(layout), out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), fmt, n,
           pages, qs, ks, vs)
     return q_out
@@ -259,17 +255,15 @@ def kv_read_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, indices: torch.Ten
     if indices.dim() != 1:
         raise ValueError("indices must be [N]")
     n = indices.shape[0]
-    shape, made = (n, NUM_KV_HEADS, HEAD_DIM), []
+    shape = (n, NUM_KV_HEADS, HEAD_DIM)
     _check(index, torch.bfloat16, True, k_out=k_out, v_out=v_out)
     if k_out is None:
-        k_out = _new(index, shape, torch.bfloat16)
-        made.append(k_out)
+        k_out = _new(index, shape, torch.bfloat16, stream)
     if v_out is None:
-        v_out = _new(index, shape, torch.bfloat16)
-        made.append(v_out)
+        v_out = _new(index, shape, torch.bfloat16, stream)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out and v_out must be {shape}")
-    _call("gqa_paged_kv_read_fp8", index, stream, made, k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
+    _call("gqa_paged_kv_read_fp8", index, stream, k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
           k_out.data_ptr(), v_out.data_ptr(), n, pages)
     return k_out, v_out
 
@@ -296,7 +290,7 @@ def mla_kv_append(latent: torch.Tensor, k_rope: torch.Tensor, slots: torch.Tenso
         if t.dim() != 2 or t.shape != (n, d) or t.stride(1) != 1:
             raise ValueError(f"{name} must be [N, {d}] with contiguous rows, one per slot")
     pos, freq, _ = _rotation(index, n, positions, inv_freq, MLA_ROPE // 2)
-    _call("gqa_mla_kv_append", index, stream, (), latent.data_ptr(), k_rope.data_ptr(), pos, slots.data_ptr(), freq, scale,
+    _call("gqa_mla_kv_append", index, stream, latent.data_ptr(), k_rope.data_ptr(), pos, slots.data_ptr(), freq, scale,
           _layout(layout), kv_cache.data_ptr(), n, blocks * page, latent.stride(0) if n > 1 else MLA_D_V,
           k_rope.stride(0) if n > 1 else MLA_ROPE)
 
@@ -328,15 +322,13 @@ def mla_absorb_q(q: torch.Tensor, w_kv: torch.Tensor, positions: Optional[torch.
     n, h, ts, hs = _query(q)
     w = _weights(w_kv, h, index)
     pos, freq, _ = _rotation(index, n, positions, inv_freq, MLA_ROPE // 2)
-    made = ()
     if out is None:
-        out = _new(index, (n, h, MLA_D_QK), torch.bfloat16)
-        made = (out,)
+        out = _new(index, (n, h, MLA_D_QK), torch.bfloat16, stream)
     else:
         _check(index, torch.bfloat16, True, out=out)
         if out.shape != (n, h, MLA_D_QK):
             raise ValueError(f"out must be {(n, h, MLA_D_QK)}")
-    _call("gqa_mla_absorb_q", index, stream, made, q.data_ptr(), w, pos, freq, scale, _layout(layout), out.data_ptr(), n, h,
+    _call("gqa_mla_absorb_q", index, stream, q.data_ptr(), w, pos, freq, scale, _layout(layout), out.data_ptr(), n, h,
           ts, hs)
     return out
 
@@ -351,15 +343,13 @@ def mla_expand_out(o_latent: torch.Tensor, w_kv: torch.Tensor, out: Optional[tor
         raise ValueError(f"o_latent must be [N, heads, {MLA_D_V}]")
     n, h, _ = o_latent.shape
     w = _weights(w_kv, h, index)
-    made = ()
     if out is None:
-        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16)
-        made = (out,)
+        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16, stream)
     else:
         _check(index, torch.bfloat16, True, out=out)
         if out.shape != (n, h, MLA_HEAD_V):
             raise ValueError(f"out must be {(n, h, MLA_HEAD_V)}")
-    _call("gqa_mla_expand_out", index, stream, made, o_latent.data_ptr(), w, out.data_ptr(), n, h)
+    _call("gqa_mla_expand_out", index, stream, o_latent.data_ptr(), w, out.data_ptr(), n, h)
     return out
 
 
@@ -411,10 +401,8 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         max_kv_tokens = b * width * page
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(MLA_D_HEAD)
-    made = []
     if out is None:
-        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16)
-        made.append(out)
+        out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16, stream)
     elif out.shape != (n, h, MLA_HEAD_V):
         raise ValueError(f"out must be {(n, h, MLA_HEAD_V)}")
     if lse is not None:
@@ -422,19 +410,17 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         if lse.shape != (h, n):
             raise ValueError(f"lse must be {(h, n)}")
     elif with_lse:
-        lse = _new(index, (h, n), torch.float32)
-        made.append(lse)
+        lse = _new(index, (h, n), torch.float32, stream)
     if b == 0 or n == 0:
         return out, lse
     if workspace is None:
         size = load().gqa_mla_prefill_ws_size(b, h, max_kv_tokens)
         if size == 0:
             raise ValueError(f"batch {b}, heads {h} and max_kv_tokens {max_kv_tokens} are out of range")
-        workspace = _new(index, (size,), torch.uint8)
-        made.append(workspace)
+        workspace = _new(index, (size,), torch.uint8, stream)
     else:
         _check(index, None, True, workspace=workspace)
-    _call("gqa_mla_prefill", index, stream, made, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
+    _call("gqa_mla_prefill", index, stream, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
           cache_seqlens.data_ptr(), cu_seqlens_q.data_ptr(), softmax_scale, 1 if causal else 0, out.data_ptr(),
           lse.data_ptr() if lse is not None else None, b, n, h, page, blocks, width, max_kv_tokens, ts, hs,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())

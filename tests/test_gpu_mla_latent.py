@@ -210,6 +210,18 @@ def test_prefill_sizes_of_values(std, w_std, scale):
     assert torch.allclose(lse, l2, rtol=0, atol=1e-5)
 
 
+def test_prefill_a_sequence_of_huge_values_leaves_the_others():
+    """Finite values near the type's largest in one sequence: the others' outputs are bit for bit what they were."""
+    c = case([(50, 200), (30, 30), (129, 300)], 2, 16, 21)
+    g = on_gpu(c)
+    out, lse = pkg.mla_prefill(**g)
+    g["kv_cache"][g["block_table"][1, 0].long(), 5] *= 2.0 ** 100
+    got, gl = pkg.mla_prefill(**g)
+    keep = torch.ones(209, dtype=torch.bool)
+    keep[50:80] = False
+    assert torch.equal(got[keep], out[keep]) and torch.equal(gl[:, keep], lse[:, keep])
+
+
 def test_prefill_large_scores_and_not_finite_values():
     c = case([(50, 50), (40, 260)], 2, 16, 13, std=6.0)  # scores of many hundreds: one weight takes it all
     g = on_gpu(c)
