@@ -290,6 +290,7 @@ struct MlaPrefillParams {
   int* q_start;   // [batch][2] first query row and query count, cut to [0, total_q)
   int* qt_start;  // [batch + 1] first query tile
   unsigned* amax;      // largest finite |value| bits: key weights, value weights, then [batch][2] latent, rotary key
+  int* units;          // [num_heads] units of the attention taken so far, a counter a pass
   unsigned* valid;     // [cap / 32] packed rows that hold a token of the pool
   unsigned* bad;       // [cap / 32] packed rows whose latent is not all finite
   void* lat;           // [cap][512] bf16
@@ -297,7 +298,7 @@ struct MlaPrefillParams {
   void* kn;            // [heads_per_pass][cap][128] fp16 keys (scaled)
   void* vv;            // [heads_per_pass][cap][128] fp16 values (scaled)
   int* err;
-  int head0, heads;    // heads of this pass
+  int pass, head0, heads;  // this pass over the heads, and its heads
   int head_group;      // heads whose CTAs run together
 };
 // A tensor map of 2 or 3 dimensions (sizes and boxes from the contiguous one on, `pitch` bytes between steps of the

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   if (tid < 2) p.amax[tid] = 0;
+  for (int i = tid; i < p.num_heads; i += 1024) p.units[i] = 0;
   int64_t base_k = 0;
   int base_q = 0;
   const int64_t table = static_cast<int64_t>(p.width) * p.page_size;
@@ -254,6 +255,10 @@ __device__ __forceinline__ uint32_t sw128(uint32_t base, int r, int c) { return 
 // ------------------------------------------------------------------ waits
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// The value that all lanes hold, so that the compiler knows it to be one: operands of MMAs then need no move from a
+// lane's register (the attention's key tiles took a tenth longer with them in a loop over units).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
 // Bounded wait that ignores the abort flag (draining before exit).
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -262,12 +267,14 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Whole warp: every lane waits (bounded; no lane runs apart from the others), every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit,
+                                          uint64_t limit = kWaitNs) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, limit));
 }
 // The same for a barrier that both CTAs' threads arrive on.
-__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit) {
-  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, kWaitNs) && mbar_try_wait_cluster(bar, parity));
+__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit,
+                                               uint64_t limit = kWaitNs) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_s, err, bit, limit) && mbar_try_wait_cluster(bar, parity));
 }
 
 // -------------------------------------------------------------- expansion
@@ -505,6 +512,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // in each CTA, which gives a ring of three tiles, and halves the L2 reads: 2810 clocks,
 // the tensor cores busy for 91 % of them.
 //
+// The pairs are persistent: a unit is the 512 query rows of one head; a pair begins with the unit of its own number
+// and takes the next ones from a counter (heads in groups, the query tiles of the most keys first), a few key tiles
+// before it needs them. What a unit costs beside its key tiles is then the copy and turning of its queries, the first
+// scores and the last output: 7 us, where a pair launched per unit took 13 to 15. The barriers' phases, the rings and
+// the turns simply run on from unit to unit.
+//
 // Roles in each CTA: two softmax warpgroups and two MMA warps (one of each per tile;
 // the even CTA's issue for both CTAs, in turns), a copy warp. Issuing an MMA takes
 // nearly as long as its 64 clocks, so with one MMA warp for both tiles its waits and
@@ -532,12 +545,22 @@ static_assert(256 * kSoftRegs + 128 * kRoleRegs <= kAtThreads * 168, "register s
 constexpr float kShift = 7.f, kMoveBy = 8.f;
 constexpr int kAtK = 2 * kQTileBytes, kAtV = kAtK + kSlots * kKSlot, kAtBars = kAtV + kSlots * kVSlot;
 // Barriers. The even CTA's: K and V landed (both halves' bytes), queries and the halves of P written (4 warps of
-// each CTA). Both CTAs' (MMA commits): K and V slots free (of both tiles), S and O written, all done.
+// each CTA), whose turn it is to issue, a unit's number read by the other CTA. Both CTAs': K and V
+// slots free (a commit of each MMA warp), S and O written, queries read (MMA commits), all done; bf16 queries landed;
+// unit published, unit taken (every warp with a role); the odd CTA's: the unit's number has come.
 enum : int { B_KFULL = 0, B_VFULL = B_KFULL + kSlots, B_Q = B_VFULL + kSlots, B_P = B_Q + 2, B_KFREE = B_P + 4,
-             B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_DONE = B_O + 2,
-             B_TURN = B_DONE + 1, B_QRAW = B_TURN + 2, B_COUNT = B_QRAW + 2 };  // whose turn to issue; bf16 queries landed
+             B_VFREE = B_KFREE + kSlots, B_S = B_VFREE + kSlots, B_O = B_S + 2, B_QFREE = B_O + 2, B_DONE = B_QFREE + 2,
+             B_TURN = B_DONE + 1, B_QRAW = B_TURN + 2, B_UFULL = B_QRAW + 2, B_UFREE = B_UFULL + 2, B_MFULL = B_UFREE + 2,
+             B_MFREE = B_MFULL + 2, B_COUNT = B_MFREE + 2 };
+__device__ __forceinline__ uint32_t attn_bar_count(int i, uint32_t half) {
+  if (i >= B_Q && i < B_KFREE) return 8;
+  if ((i >= B_KFREE && i < B_S) || i == B_DONE) return 2;
+  if (i >= B_UFREE && i < B_MFULL) return half == 0 ? 10 : 8;  // softmax and, in the even CTA, MMA warps
+  return 1;
+}
 constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
-constexpr int kAtSmem = kAtAbort + 4 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
+constexpr int kAtUnits = (kAtAbort + 4 + 15) / 16 * 16, kAtMail = kAtUnits + 2 * 48;  // two units of 12 words, two numbers
+constexpr int kAtSmem = kAtMail + 8 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
 static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
 
 struct AttnMaps {  // boxes of 64 values x 64 rows (keys) and x 128 rows (values, queries of one head)
@@ -585,26 +608,21 @@ __device__ __forceinline__ unsigned upto(int lim, int t0, int k) {
   return c < 0 ? 0u : (c >= 31 ? 0xffffffffu : (2u << c) - 1u);
 }
 
+// A word into the shared memory of a CTA of the cluster, counted by that CTA's mbarrier.
+__device__ __forceinline__ void st_async(uint32_t addr, int value, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];" ::"r"(addr), "r"(value), "r"(bar)
+               : "memory");
+}
+
+// Words of a unit in shared memory: whether there is one, head of the pass, first query row of the sequence, its
+// queries, their first row among all, its keys, their first packed row, key tiles of the two query tiles, exponents.
+enum : int { U_OK = 0, U_HEAD, U_ROW, U_NQ, U_Q0, U_KEYS, U_KV0, U_NT0, U_NT1, U_EK, U_EV };
+constexpr uint64_t kUnitWaitNs = 10 * kWaitNs;  // a unit may last longer than any wait inside it
+
 __global__ void __launch_bounds__(kAtThreads, 1)
     gqa_mla_prefill_attn_kernel(const MlaPrefillParams p, const __grid_constant__ AttnMaps maps) {
   extern __shared__ uint8_t smem_raw[];
-  // CTAs in order: groups of heads whose keys and values stay in L2 together,
-  // within a group the last query tiles (the most keys, if causal) first
-  // What the plan and the gather wrote is complete when this kernel may start (the expansion lets it start after its
-  // own wait); only the copies of keys and values wait for the expansion. Read past L1, which an earlier call's
-  // values of the same workspace may still be in.
-  const int tiles = __ldcg(p.qt_start + p.batch);
   const uint32_t half = cluster_rank();  // which 128 rows of a tile, which half of the keys and values
-  const int64_t rank = blockIdx.x >> 1;
-  if (rank >= static_cast<int64_t>(tiles) * p.heads) {
-    pdl_wait();
-    return;
-  }
-  const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
-  const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
-  const int gh = min(p.head_group, p.heads - group * p.head_group);
-  const int qt = tiles - 1 - in_group / gh, hp = group * p.head_group + in_group % gh, h = p.head0 + hp;
-
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -612,7 +630,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + kAtAbort);
   auto bar = [&](int i) { return base + kAtBars + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q && i < B_KFREE ? 8u : ((i >= B_KFREE && i < B_S) || i == B_DONE ? 2u : 1u));
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), attn_bar_count(i, half));
     *abort_s = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -623,128 +641,231 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   cluster_sync();  // the barriers and the tensor memory of both CTAs are ready
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + kAtSlot);
-
-  const int b = find_seq(p.qt_start, p.batch, qt);
-  const int2 qs = __ldcg(reinterpret_cast<const int2*>(p.q_start) + b);
-  const int n = __ldcg(p.kv_len + b), kv0 = __ldcg(p.kv_start + b), i0 = (qt - __ldcg(p.qt_start + b)) * kQTile;
-  const int nq = qs.y;
-  const int64_t q0 = qs.x;
   int* err = p.err;
-  // key tiles of each query tile (the same in both CTAs): up to the last key that its last row sees
-  int nt[2];
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    const int last_row = min(i0 + 256 * (a + 1), nq) - 1;
-    int keys = last_row < i0 + 256 * a ? 0 : (p.causal ? min(n, n - nq + last_row + 1) : n);
-    keys = max(keys, 0);
-    nt[a] = (keys + kKTile - 1) / kKTile;
-  }
-  const int total = max(nt[0], nt[1]);
+
+  // Waits for unit number `it` of this pair, for a warp with a role; false at the end (or on a timeout). A role reads a
+  // unit's words where it needs them (in registers they spilled) and leaves the unit when it has read the last.
+  auto unit_word = [&](int it, int w) { return reinterpret_cast<const volatile int*>(sm + kAtUnits + 48 * (it & 1))[w]; };
+  auto enter_unit = [&](int it) -> bool {
+    return warp_wait(bar(B_UFULL + (it & 1)), (it >> 1) & 1, abort_s, err, kErrTimeoutFull, kUnitWaitNs) &&
+           unit_word(it, U_OK) != 0;
+  };
+  auto leave_unit = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B_UFREE + (it & 1)));
+  };
 
   if (warp < kSoftWarp) {
     setmaxnreg_dec<kRoleRegs>();
     if (warp == kCopyWarp) {
-#pragma unroll 1
-      for (int a = 0; a < 2; ++a) {
-        if (nt[a] == 0) continue;
-#pragma unroll 1
-        for (int r = 0; r < 3; ++r)
-          tma_load_3d_warp(base + a * kQTileBytes + r * kQRegion, &maps.q, 64 * r, h, static_cast<int>(q0) + i0 + 256 * a + 128 * half,
-                           bar(B_QRAW + a), r == 0 ? kQTileBytes : 0);
-      }
-      pdl_wait();
-      const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
+      // What the plan and the gather wrote is complete when this kernel may start (the expansion lets it start after its
+      // own wait); only the copies of keys and values wait for the expansion. Read past L1, which an earlier call's
+      // values of the same workspace may still be in.
+      const int tiles = __ldcg(p.qt_start + p.batch), pairs = gridDim.x >> 1;
+      const int start = lane + 1 < p.batch ? __ldcg(p.qt_start + lane + 1) : INT_MAX;  // of the first 32 after sequence 0
       const uint32_t kfull = cluster_addr(bar(B_KFULL), 0), vfull = cluster_addr(bar(B_VFULL), 0);
       const uint32_t k_bytes = half == 0 ? 2 * kKSlot : 0, v_bytes = half == 0 ? 2 * kVSlot : 0;
-      int j = 0, s = 0;
-      uint32_t ph = 1;  // parity of the slot's previous release
+      int s = 0, keys = 0, values = 0;  // slot, counts of copies begun
+      uint32_t ph = 1;                  // parity of the slot's previous release
+      int queries[2] = {0, 0};          // loads of each tile's queries
+      int rank = blockIdx.x >> 1, next = 0;
+      bool good = true;
 #pragma unroll 1
-      for (; j < total; ++j) {
-        const uint32_t kd = base + kAtK + s * kKSlot, vd = base + kAtV + s * kVSlot;
-        if (j >= kSlots && !warp_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty)) break;
-        tma2_load_2d_warp(kd, &maps.kn, 0, y0 + j * kKTile, bar(B_KFULL + s), k_bytes, kfull + 8 * s);
-        tma2_load_2d_warp(kd + kKRegion, &maps.kn, 64, y0 + j * kKTile, 0, 0, kfull + 8 * s);
-        tma2_load_2d_warp(kd + 2 * kKRegion, &maps.kr, 0, r0 + j * kKTile, 0, 0, kfull + 8 * s);
-        if (j >= kSlots && !warp_wait(bar(B_VFREE + s), ph, abort_s, err, kErrTimeoutEmpty)) break;
-        tma2_load_2d_warp(vd, &maps.vv, 64 * half, v0 + j * kKTile, bar(B_VFULL + s), v_bytes, vfull + 8 * s);
-        if (++s == kSlots) {
-          s = 0;
-          ph ^= 1;
+      for (int it = 0;; ++it) {
+        const int us = it & 1;
+        if (it > 0) {  // the even CTA took the unit's number, the odd one gets it
+          const uint32_t mail = base + kAtMail + 4 * us;
+          if (half == 0) {
+            rank = pairs + __shfl_sync(0xffffffffu, next, 0);
+            if (it > 2) {
+              good = warp_wait_pair(bar(B_MFREE + us), ((it - 3) >> 1) & 1, abort_s, err, kErrTimeoutEmpty, kUnitWaitNs);
+              if (!good) break;
+            }
+            if (lane == 0) st_async(cluster_addr(mail, 1), rank, cluster_addr(bar(B_MFULL + us), 1));
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(bar(B_MFULL + us), 4);
+            good = warp_wait(bar(B_MFULL + us), ((it - 1) >> 1) & 1, abort_s, err, kErrTimeoutFull, kUnitWaitNs);
+            if (!good) break;
+            rank = *reinterpret_cast<volatile int*>(sm + kAtMail + 4 * us);
+          }
+          __syncwarp();
         }
+        const bool ok = rank < static_cast<int64_t>(tiles) * p.heads;
+        int hp = 0, b = 0, i0 = 0, n = 0, kv0 = 0, ek = 0, ev = 0, nt[2] = {0, 0};
+        int2 qs = {0, 0};
+        if (ok) {
+          // in order: groups of heads whose keys and values stay in L2 together, within a group the last query tiles
+          // (the most keys, if causal) first
+          const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
+          const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
+          const int gh = min(p.head_group, p.heads - group * p.head_group);
+          const int qt = tiles - 1 - in_group / gh;
+          hp = group * p.head_group + in_group % gh;
+          // the last sequence that starts at this tile or before it
+          b = __popc(__ballot_sync(0xffffffffu, start <= qt));
+          for (int k = 33; b == k - 1 && k < p.batch; k += 32)
+            b += __popc(__ballot_sync(0xffffffffu, k + lane < p.batch && __ldcg(p.qt_start + min(k + lane, p.batch)) <= qt));
+          qs = __ldcg(reinterpret_cast<const int2*>(p.q_start) + b);
+          n = __ldcg(p.kv_len + b);
+          kv0 = __ldcg(p.kv_start + b);
+          i0 = (qt - __ldcg(p.qt_start + b)) * kQTile;
+          kv_exponents(p.amax, b, ek, ev);
+          // key tiles of each query tile (the same in both CTAs): up to the last key that its last row sees
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const int last_row = min(i0 + 256 * (a + 1), qs.y) - 1;
+            int see = last_row < i0 + 256 * a ? 0 : (p.causal ? min(n, n - qs.y + last_row + 1) : n);
+            nt[a] = (max(see, 0) + kKTile - 1) / kKTile;
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          if (!good || nt[a] == 0) continue;
+          if (queries[a] > 0) good = warp_wait(bar(B_QFREE + a), (queries[a] - 1) & 1, abort_s, err, kErrTimeoutEmpty);
+          if (!good) continue;
+          ++queries[a];
+#pragma unroll 1
+          for (int r = 0; r < 3; ++r)
+            tma_load_3d_warp(base + a * kQTileBytes + r * kQRegion, &maps.q, 64 * r, p.head0 + hp,
+                             qs.x + i0 + 256 * a + 128 * half, bar(B_QRAW + a), r == 0 ? kQTileBytes : 0);
+        }
+        if (!good) break;
+        if (it >= 2 && !warp_wait(bar(B_UFREE + us), ((it >> 1) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kUnitWaitNs)) break;
+        if (lane == 0) {
+          volatile int* w = reinterpret_cast<volatile int*>(sm + kAtUnits + 48 * us);
+          w[U_OK] = ok ? 1 : 0;
+          w[U_HEAD] = hp;
+          w[U_EK] = ek;
+          w[U_EV] = ev;
+          w[U_ROW] = i0;
+          w[U_NQ] = qs.y;
+          w[U_Q0] = qs.x;
+          w[U_KEYS] = n;
+          w[U_KV0] = kv0;
+          w[U_NT0] = nt[0];
+          w[U_NT1] = nt[1];
+          mbar_arrive(bar(B_UFULL + us));
+        }
+        __syncwarp();
+        if (!ok) break;
+        if (it == 0) pdl_wait();
+        const int total = max(nt[0], nt[1]), ask_at = max(total - 6, 0);
+        const int y0 = hp * p.cap + kv0 + 64 * half, r0 = kv0 + 64 * half, v0 = hp * p.cap + kv0;
+#pragma unroll 1
+        for (int j = 0; j < total && good; ++j) {
+          // the next unit is taken a few key tiles before the end of this one, not sooner: another pair may be free
+          if (j == ask_at && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
+          __syncwarp();
+          const uint32_t kd = base + kAtK + s * kKSlot, vd = base + kAtV + s * kVSlot;
+          if (keys >= kSlots) good = warp_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
+          if (!good) break;
+          tma2_load_2d_warp(kd, &maps.kn, 0, y0 + j * kKTile, bar(B_KFULL + s), k_bytes, kfull + 8 * s);
+          tma2_load_2d_warp(kd + kKRegion, &maps.kn, 64, y0 + j * kKTile, 0, 0, kfull + 8 * s);
+          tma2_load_2d_warp(kd + 2 * kKRegion, &maps.kr, 0, r0 + j * kKTile, 0, 0, kfull + 8 * s);
+          ++keys;
+          if (values >= kSlots) good = warp_wait(bar(B_VFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
+          if (!good) break;
+          tma2_load_2d_warp(vd, &maps.vv, 64 * half, v0 + j * kKTile, bar(B_VFULL + s), v_bytes, vfull + 8 * s);
+          ++values;
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!good) break;
+        if (total == 0 && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
+        if (it > 0 && half == 1 && lane == 0) mbar_arrive_cluster(cluster_addr(bar(B_MFREE + us), 0));
+        __syncwarp();
       }
+      if (keys == 0) pdl_wait();
       // no copy may still be writing either CTA's shared memory when the pair leaves
       if (lane == 0)
         for (int a = 0; a < 2; ++a)
-          if (nt[a] > 0) drain_wait(bar(B_QRAW + a), 0);
+          if (queries[a] > 0) drain_wait(bar(B_QRAW + a), (queries[a] - 1) & 1);
       if (half == 0 && lane == 0)
-        for (int i = max(0, j - kSlots); i < j; ++i) {
-          drain_wait(bar(B_KFULL + i % kSlots), (i / kSlots) & 1);
-          drain_wait(bar(B_VFULL + i % kSlots), (i / kSlots) & 1);
+        for (int k = 0; k < kSlots; ++k) {
+          const int i = keys - 1 - k, v = values - 1 - k;
+          if (i >= 0) drain_wait(bar(B_KFULL + i % kSlots), (i / kSlots) & 1);
+          if (v >= 0) drain_wait(bar(B_VFULL + v % kSlots), (v / kSlots) & 1);
         }
       __syncwarp();
-    }
-    if (warp < 2 && half == 0 && total > 0) {
+    } else if (warp < 2 && half == 0) {
       // tile a: the whole warp walks the keys (warp-uniform operands), one elected lane issues
-      const int a = warp, mine = a == 0 ? nt[0] : nt[1];
+      const int a = static_cast<int>(uniform(warp));
+      const uint32_t ub = uniform(base), ut = uniform(tmem);
       constexpr uint32_t idesc_s = tc_idesc_f16(256, kKTile, false, false);
       constexpr uint32_t idesc_o = tc_idesc_f16(256, kHeadV, false, true);
-      const uint64_t dq0 = tc_sdesc(base + a * kQTileBytes, 16, 1024, kSwizzle128B);
-      const uint64_t dk0 = tc_sdesc(base + kAtK, 16, 1024, kSwizzle128B);
+      const uint64_t dq0 = tc_sdesc(ub + a * kQTileBytes, 16, 1024, kSwizzle128B);
+      const uint64_t dk0 = tc_sdesc(ub + kAtK, 16, 1024, kSwizzle128B);
       // V as B: N = 64 values a CTA (one swizzle atom), K = keys in 8-row groups (SBO)
-      const uint64_t dv0 = tc_sdesc(base + kAtV, kVSlot, 1024, kSwizzle128B);
-      const uint32_t s_col = tmem + 128 * a, o_col = tmem + 256 + 128 * a;
+      const uint64_t dv0 = tc_sdesc(ub + kAtV, kVSlot, 1024, kSwizzle128B);
+      const uint32_t s_col = ut + 128 * a, o_col = ut + 256 + 128 * a;
+      auto bar = [&](int i) { return ub + kAtBars + 8u * static_cast<uint32_t>(i); };
       int s = 0;  // slot and parity of tile j
-      uint32_t ph = 0;
+      uint32_t ph = 0, np = 0, nq = 0, turn = 0;  // counts of P read, queries taken, turns had
       bool good = true;
 #pragma unroll 1
-      for (int j = 0; j <= total; ++j) {
-        // O += P(j - 1) V(j - 1), then S(j) = Q K(j), in turn with the other tile's warp. Slots of keys that this
-        // tile does not see are freed as they land, not sooner: an arrival for the slot's next use would count for
-        // this one.
-        const int vs = s == 0 ? kSlots - 1 : s - 1;
-        const uint32_t vp = s == 0 ? ph ^ 1u : ph;
-        const bool pv = j > 0 && j <= mine, qk = j < mine;
-        if (j > 0) good = warp_wait(bar(B_VFULL + vs), vp, abort_s, err, kErrTimeoutFull);
-        if (j < total) good = good && warp_wait(bar(B_KFULL + s), ph, abort_s, err, kErrTimeoutFull);
-        if (j == 0 && qk) good = good && warp_wait_pair(bar(B_Q + a), 0, abort_s, err, kErrTimeoutFull);
-        if (a == 1 || j > 0) good = good && warp_wait(bar(B_TURN + a), (a == 1 ? j : j - 1) & 1, abort_s, err, kErrTimeoutFull);
-        if (pv) good = good && warp_wait(bar(B_P + 2 * a), (j - 1) & 1, abort_s, err, kErrTimeoutFull);
-        if (!good) break;
-        tc_fence_after();
-        if (pv) {
-          const uint64_t dv = dv0 + vs * (kVSlot >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : j - 1);
-          good = warp_wait(bar(B_P + 2 * a + 1), (j - 1) & 1, abort_s, err, kErrTimeoutFull);
+      for (int it = 0; good && enter_unit(it); ++it) {
+        const int mine = static_cast<int>(uniform(unit_word(it, U_NT0 + a)));
+        const int total = max(mine, static_cast<int>(uniform(unit_word(it, U_NT0 + 1 - a))));
+        leave_unit(it);
+        if (total == 0) continue;
+#pragma unroll 1
+        for (int j = 0; j <= total; ++j, ++turn) {
+          // O += P(j - 1) V(j - 1), then S(j) = Q K(j), in turn with the other tile's warp. Slots of keys that this
+          // tile does not see are freed as they land, not sooner: an arrival for the slot's next use would count for
+          // this one.
+          const int vs = s == 0 ? kSlots - 1 : s - 1;
+          const uint32_t vp = s == 0 ? ph ^ 1u : ph;
+          const bool pv = j > 0 && j <= mine, qk = j < mine;
+          if (j > 0) good = warp_wait(bar(B_VFULL + vs), vp, abort_s, err, kErrTimeoutFull);
+          if (j < total) good = good && warp_wait(bar(B_KFULL + s), ph, abort_s, err, kErrTimeoutFull);
+          if (j == 0 && qk) good = good && warp_wait_pair(bar(B_Q + a), nq & 1, abort_s, err, kErrTimeoutFull);
+          if (a == 1 || turn > 0)
+            good = good && warp_wait(bar(B_TURN + a), (a == 1 ? turn : turn - 1) & 1, abort_s, err, kErrTimeoutFull);
+          if (pv) good = good && warp_wait(bar(B_P + 2 * a), np & 1, abort_s, err, kErrTimeoutFull);
           if (!good) break;
           tc_fence_after();
+          if (pv) {
+            const uint64_t dv = dv0 + vs * (kVSlot >> 4);
 #pragma unroll
-          for (int kk = 4; kk < 8; ++kk)
-            tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1u);
-        }
-        const uint64_t dk = dk0 + s * (kKSlot >> 4);
-        auto scores = [&](int r) {
+            for (int kk = 0; kk < 4; ++kk)
+              tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : j - 1);
+            good = warp_wait(bar(B_P + 2 * a + 1), np & 1, abort_s, err, kErrTimeoutFull);
+            if (!good) break;
+            ++np;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc2_mma_warp(s_col, dq0 + ((r * kQRegion + kk * 32) >> 4), dk + ((r * kKRegion + kk * 32) >> 4), idesc_s,
-                         (r | kk) ? 1u : 0u);
-        };
-        if (qk) scores(0);
-        if (lane == 0) mbar_arrive(bar(B_TURN + 1 - a));  // early: the rest is issued before the other warp gets going
-        __syncwarp();
-        if (qk) {
-          scores(1);
-          scores(2);
-          tc2_commit_warp(bar(B_S + a));
+            for (int kk = 4; kk < 8; ++kk)
+              tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1u);
+          }
+          const uint64_t dk = dk0 + s * (kKSlot >> 4);
+          auto scores = [&](int r) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc2_mma_warp(s_col, dq0 + ((r * kQRegion + kk * 32) >> 4), dk + ((r * kKRegion + kk * 32) >> 4), idesc_s,
+                           (r | kk) ? 1u : 0u);
+          };
+          if (qk) scores(0);
+          if (lane == 0) mbar_arrive(bar(B_TURN + 1 - a));  // early: the rest is issued before the other warp gets going
+          __syncwarp();
+          if (qk) {
+            scores(1);
+            scores(2);
+            tc2_commit_warp(bar(B_S + a));
+            if (j == mine - 1) tc2_commit_warp(bar(B_QFREE + a));
+          }
+          if (j > 0) tc2_commit_warp(bar(B_VFREE + vs));
+          if (pv && j == mine) tc2_commit_warp(bar(B_O + a));
+          if (j < total) {
+            tc2_commit_warp(bar(B_KFREE + s));
+            if (++s == kSlots) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
         }
-        if (j > 0) tc2_commit_warp(bar(B_VFREE + vs));
-        if (pv && j == mine) tc2_commit_warp(bar(B_O + a));
-        if (j < total) tc2_commit_warp(bar(B_KFREE + s));
-        if (++s == kSlots) {
-          s = 0;
-          ph ^= 1;
-        }
+        if (mine > 0) ++nq;
       }
       tc2_commit_warp(bar(B_DONE));  // every MMA done before tensor memory is freed
       __syncwarp();
@@ -757,18 +878,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int a = (warp - kSoftWarp) >> 2, wq = warp & 3;
     const uint32_t quarter = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t s_col = tmem + quarter + 128 * a, o_col = tmem + quarter + 256 + 128 * a;
-    const int row0 = i0 + 256 * a + 128 * half + 32 * wq;  // query row (of the sequence) of lane 0
     const uint32_t q_bar = cluster_addr(bar(B_Q + a), 0), p_bar = cluster_addr(bar(B_P + 2 * a), 0);
-    const int i = row0 + lane;
-    float row_fac = 1.f;
-    if (nt[a] > 0) {
-      // this row's query, copied in as bf16, to fp16 with its largest value in [2^10, 2^11). Small loops: straight-line
-      // code for the whole row took 6 to 8 us a CTA, most of it instruction fetch. Rows past the sequence's queries hold
-      // whatever follows them; their results are not stored.
-      const bool landed = warp_wait(bar(B_QRAW + a), 0, abort_s, err, kErrTimeoutFull);
-      const uint32_t q_row = base + a * kQTileBytes;
-      unsigned top = 0;
-      if (landed) {
+    uint32_t scored = 0, turned = 0;  // counts of S read and of queries turned
+    bool good = true;
+#pragma unroll 1
+    for (int it = 0; good && enter_unit(it); ++it) {
+      const int nt = unit_word(it, U_NT0 + a);
+      float row_fac = 1.f;
+      if (nt > 0) {
+        // this row's query, copied in as bf16, to fp16 with its largest value in [2^10, 2^11). Small loops: straight-line
+        // code for the whole row took 6 to 8 us a CTA, most of it instruction fetch. Rows past the sequence's queries hold
+        // whatever follows them; their results are not stored.
+        good = warp_wait(bar(B_QRAW + a), turned & 1, abort_s, err, kErrTimeoutFull);
+        if (!good) break;
+        const uint32_t q_row = base + a * kQTileBytes;
+        unsigned top = 0;
 #pragma unroll 4
         for (int k = 0; k < 24; ++k) {
           uint4 v;
@@ -786,114 +910,123 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ld_shared_u4(at, v.x, v.y, v.z, v.w);
           st_shared_u4(at, half2(v.x), half2(v.y), half2(v.z), half2(v.w));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(q_bar);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(q_bar);
-    }
-    int ek, ev;
-    kv_exponents(p.amax, b, ek, ev);
-    const float sc = fmaxf(row_fac * fabsf(p.scale_log2) * pow2(ek), 1e-37f);  // > 0: -inf * sc stays -inf
-    const int lim = p.causal ? n - nq + i : INT_MAX;          // last key this row sees
-    const int lim0 = p.causal ? n - nq + row0 : INT_MAX;      // and the warp's first row
-    float m = -INFINITY;
-    uint64_t l2 = 0;
-    bool good = true;
-    for (int j = 0; j < nt[a] && good; ++j) {
-      const uint4 vw = __ldcg(reinterpret_cast<const uint4*>(p.valid) + (kv0 >> 7) + j);
-      good = warp_wait(bar(B_S + a), j & 1, abort_s, err, kErrTimeoutFull);
-      if (!good) break;
+      const float sc = fmaxf(row_fac * fabsf(p.scale_log2) * pow2(unit_word(it, U_EK)), 1e-37f);  // > 0: -inf * sc stays -inf
+      // the last key that the warp's first row and this row see
+      const int row0 = unit_word(it, U_ROW) + 256 * a + 128 * half + 32 * wq;
+      const int lim0 = p.causal ? unit_word(it, U_KEYS) - unit_word(it, U_NQ) + row0 : INT_MAX;
+      const int lim = p.causal ? lim0 + lane : INT_MAX;
+      const uint4* valid = reinterpret_cast<const uint4*>(p.valid) + (unit_word(it, U_KV0) >> 7);
+      float m = -INFINITY;
+      uint64_t l2 = 0;
+      for (int j = 0; j < nt && good; ++j) {
+        const uint4 vw = __ldcg(valid + j);
+        good = warp_wait(bar(B_S + a), scored & 1, abort_s, err, kErrTimeoutFull);
+        if (!good) break;
+        ++scored;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_ld32(s_col + 32 * c, s + 32 * c);
+        tc_wait_ld();
+        const int t0 = j * kKTile;
+        if ((vw.x & vw.y & vw.z & vw.w) != 0xffffffffu || t0 + kKTile - 1 > lim0) {
+          const unsigned w[4] = {vw.x & upto(lim, t0, 0), vw.y & upto(lim, t0, 1), vw.z & upto(lim, t0, 2), vw.w & upto(lim, t0, 3)};
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (((w[c >> 5] >> (c & 31)) & 1u) == 0) s[c] = 0xff800000u;  // -inf
+        }
+        // Optimistic: the first half's probabilities are formed with the running maximum as it stands, beside the search
+        // for this tile's; only if a row passed it by 2^8 (the first tile, and seldom after) are they formed again.
+        const uint64_t sc2 = pack2(sc, sc);
+        uint64_t off2 = pack2(kShift - m, kShift - m), l_new = 0;
+        uint32_t pk[32];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
+          mx[k & 3] = max3(mx[k & 3], max3(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1]), __uint_as_float(s[4 * k + 2])),
+                           __uint_as_float(s[4 * k + 3]));
+        }
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
+        const bool move = top > m + kMoveBy;
+        if (__any_sync(0xffffffffu, move || m == -INFINITY)) {
+          const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2(m - top));
+          if (move) m = top;
+          float lo, hi;
+          unpack2(l2, lo, hi);
+          l2 = pack2(lo * alpha, hi * alpha);
+          if (j > 0) {  // the commit that signalled S also covers the previous tile's O
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tc_ld16(o_col + 16 * c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tc_st16(o_col + 16 * c, o);
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : kShift - m;
+          off2 = pack2(off, off);
+          l_new = 0;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
+        }
+        tc_st32(s_col, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 0);  // half of the keys: the MMAs may start on it
+#pragma unroll
+        for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[64 + 2 * k], s[64 + 2 * k + 1], sc2, off2, l_new);
+        l2 = add2(l2, l_new);
+        tc_st32(s_col + 32, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 1);
+      }
+      if (nt > 0 && good) good = warp_wait(bar(B_O + a), turned++ & 1, abort_s, err, kErrTimeoutFull);
       tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc_ld32(s_col + 32 * c, s + 32 * c);
-      tc_wait_ld();
-      const int t0 = j * kKTile;
-      if ((vw.x & vw.y & vw.z & vw.w) != 0xffffffffu || t0 + kKTile - 1 > lim0) {
-        const unsigned w[4] = {vw.x & upto(lim, t0, 0), vw.y & upto(lim, t0, 1), vw.z & upto(lim, t0, 2), vw.w & upto(lim, t0, 3)};
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (((w[c >> 5] >> (c & 31)) & 1u) == 0) s[c] = 0xff800000u;  // -inf
-      }
-      // Optimistic: the first half's probabilities are formed with the running maximum as it stands, beside the search
-      // for this tile's; only if a row passed it by 2^8 (the first tile, and seldom after) are they formed again.
-      const uint64_t sc2 = pack2(sc, sc);
-      uint64_t off2 = pack2(kShift - m, kShift - m), l_new = 0;
-      uint32_t pk[32];
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
-        mx[k & 3] = max3(mx[k & 3], max3(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1]), __uint_as_float(s[4 * k + 2])),
-                         __uint_as_float(s[4 * k + 3]));
-      }
-      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
-      const bool move = top > m + kMoveBy;
-      if (__any_sync(0xffffffffu, move || m == -INFINITY)) {
-        const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2(m - top));
-        if (move) m = top;
-        float lo, hi;
-        unpack2(l2, lo, hi);
-        l2 = pack2(lo * alpha, hi * alpha);
-        if (j > 0) {  // the commit that signalled S also covers the previous tile's O
+      if (good) {  // (the MMAs of the next unit's O follow this warp's next P)
+        float l, hi;
+        unpack2(l2, l, hi);
+        l += hi;
+        const bool none = l == 0.f;  // the row sees no token
+        const float inv = pow2(unit_word(it, U_EV)) / l;
+        const int i = unit_word(it, U_ROW) + 256 * a + 128 * half + 32 * wq + lane, nq = unit_word(it, U_NQ);
+        const int64_t q0 = unit_word(it, U_Q0);
+        const int h = p.head0 + unit_word(it, U_HEAD);
+        leave_unit(it);
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV);
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tc_ld16(o_col + 16 * c, o);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tc_ld32(o_col + 32 * c, o);
             tc_wait_ld();
+          } else {  // (undefined values would be kept from unit to unit, and spilled)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tc_st16(o_col + 16 * c, o);
+            for (int k = 0; k < 32; ++k) o[k] = 0;
           }
+          if (i < nq)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t r[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+              out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
+            }
         }
-        const float off = m == -INFINITY ? 0.f : kShift - m;
-        off2 = pack2(off, off);
-        l_new = 0;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[2 * k], s[2 * k + 1], sc2, off2, l_new);
+        if (p.lse != nullptr && i < nq)
+          p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] = none ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
       }
-      tc_st32(s_col, pk);
-      tc_wait_st();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 0);  // half of the keys: the MMAs may start on it
-#pragma unroll
-      for (int k = 0; k < 32; ++k) pk[k] = exp_pair(s[64 + 2 * k], s[64 + 2 * k + 1], sc2, off2, l_new);
-      l2 = add2(l2, l_new);
-      tc_st32(s_col + 32, pk);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * 1);
-    }
-    if (nt[a] > 0 && good) good = warp_wait(bar(B_O + a), 0, abort_s, err, kErrTimeoutFull);
-    tc_fence_after();
-    if (good) {
-      float l, hi;
-      unpack2(l2, l, hi);
-      l += hi;
-      const bool none = l == 0.f;  // the row sees no token
-      const float inv = pow2(ev) / l;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (nt[a] > 0) {
-          tc_ld32(o_col + 32 * c, o);
-          tc_wait_ld();
-        }
-        if (i < nq)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-            out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
-          }
-      }
-      if (p.lse != nullptr && i < nq)
-        p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] = none ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
     }
   }
   tc_fence_before();
@@ -923,6 +1056,7 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
   p->q_start = reinterpret_cast<int*>(take(B * 8));
   p->qt_start = reinterpret_cast<int*>(take((B + 1) * 4));
   p->amax = reinterpret_cast<unsigned*>(take((2 + 2 * B) * 4));
+  p->units = reinterpret_cast<int*>(take(static_cast<size_t>(p->num_heads) * 4));
   p->valid = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
   p->bad = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
   p->lat = take(cap * kLat * 2);
@@ -969,7 +1103,8 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
   if (e != cudaSuccess) return e;
   const int64_t q_tiles = p.total_q / kQTile + p.batch;
   const int64_t fit = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
-  for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass) {
+  p.pass = 0;
+  for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass, ++p.pass) {
     p.head0 = h0;
     p.heads = p.num_heads - h0 < p.heads_per_pass ? p.num_heads - h0 : p.heads_per_pass;
     const int groups = static_cast<int>(fit < 1 ? p.heads : (p.heads + fit - 1) / fit);
@@ -991,8 +1126,9 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
     if (!tc_encode(&at.q, kBf, p.q, 3, q_size, q_pitch, q_box)) return cudaErrorInvalidValue;
     e = launch_next(gqa_mla_prefill_expand_kernel, 2, dim3(sm_count / 2 * 2), kExThreads, kExSmem, stream, p, ex);
     if (e != cudaSuccess) return e;
-    e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * q_tiles * p.heads)), kAtThreads, kAtSmem,
-                     stream, p, at);
+    const int64_t units = q_tiles * p.heads, pairs = sm_count / 2;
+    e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * (units < pairs ? units : pairs))), kAtThreads,
+                    kAtSmem, stream, p, at);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

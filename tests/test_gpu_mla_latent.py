@@ -160,6 +160,21 @@ def test_prefill_long_and_many(lens, h):
     check(out, lse, c, 192 ** -0.5, True)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_several_units_a_pair(causal):
+    """More units of the attention than pairs of CTAs, some without keys (in one query tile or both), long behind short."""
+    lens = [(1, 1), (600, 100), (520, 0), (513, 700), (0, 40), (3, 900), (257, 257), (512, 129), (700, 30), (1, 128),
+            (1030, 0), (1030, 1030), (40, 5), (256, 256), (2, 2)]
+    c = case(lens, 16, 32, 24)
+    g = on_gpu(c)
+    out, lse = pkg.mla_prefill(**g, causal=causal)
+    check(out, lse, c, 192 ** -0.5, causal)
+    for _ in range(20):  # which pair takes a unit changes nothing
+        out2, lse2 = pkg.mla_prefill(**g, causal=causal)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
 def test_prefill_rows_that_see_nothing():
     """More queries than cached tokens (their first rows see none), lengths of 0, blocks outside the pool."""
     c = case([(70, 3), (5, 0), (40, 40), (300, 200)], 3, 8, 5, bad_blocks=5)
