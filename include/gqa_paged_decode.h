@@ -541,6 +541,8 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
  * sequence (values below about 2^-29 of 512 * max|latent| * max|w_kv| lose bits);
  * everything else accumulates in fp32. lse carries that rounding of the keys:
  * about 2^-12 of a score's size.
+ * With few queries and many tokens a row's sums are split and joined in an order
+ * that the call's sizes and lengths determine: a call repeated gives the same bits.
  *
  * max_kv_tokens bounds the sum of the lengths on the host (it sizes the
  * workspace); sequences past it see no token and set bit 64 of the device error

@@ -291,6 +291,9 @@ struct MlaPrefillParams {
   int* qt_start;  // [batch + 1] first query tile
   unsigned* amax;      // largest finite |value| bits: key weights, value weights, then [batch][2] latent, rotary key
   int* units;          // [num_heads] units of the attention taken so far, a counter a pass
+  int* steps;          // [256] first step of each query tile (see kSplitTiles), [255] the most steps of one; then
+                       // [256] the steps of each, the most first
+  float* part;         // outputs and statistics of pieces; both NULL below kSplitRows packed rows
   unsigned* valid;     // [cap / 32] packed rows that hold a token of the pool
   unsigned* bad;       // [cap / 32] packed rows whose latent is not all finite
   void* lat;           // [cap][512] bf16
@@ -300,6 +303,7 @@ struct MlaPrefillParams {
   int* err;
   int pass, head0, heads;  // this pass over the heads, and its heads
   int head_group;      // heads whose CTAs run together
+  int split;           // units may be split over their keys
 };
 // A tensor map of 2 or 3 dimensions (sizes and boxes from the contiguous one on, `pitch` bytes between steps of the
 // others, 128-byte swizzle). False if the driver call is missing or refuses.

@@ -21,8 +21,9 @@
 //
 // Steps, each a kernel that starts while the one before it ends: the plan (prefix
 // sums over the sequences), the gather (paged rows to packed rows, 128-aligned per
-// sequence and zero-filled, and the maxima), the expansion, the attention. Bound by
-// the tensor cores: 8192 tokens x 16 heads 263 us in all (1440 TFLOP/s, 77 % of the
+// sequence and zero-filled, and the maxima), the expansion, the attention, and a join
+// where that was split. Bound by
+// the tensor cores: 8192 tokens x 16 heads 252 us in all (1500 TFLOP/s, 80 % of the
 // measured cuBLAS bf16 rate); five short prompts 33 us, the chain's latency.
 #include <cuda_bf16.h>
 #include <cuda.h>
@@ -46,6 +47,13 @@ constexpr int kQTile = 512;   // query rows a pair of CTAs takes
 constexpr int64_t kExpandBytes = int64_t{1} << 30;  // expanded keys and values of one pass over the heads
 constexpr int64_t kGroupBytes = int64_t{96} << 20;  // and of the heads whose CTAs run together (they stay in L2)
 
+// Splitting the attention's units over their keys (see there): at most this many units (query tiles x heads) and pairs
+// of CTAs, from this many packed rows on; steps (key tiles' time) that a unit, and joining one, cost besides; the least
+// piece.
+constexpr int kSplitTiles = 152, kSplitPairs = 76, kSplitRows = 2048;
+constexpr int kUnitSteps = 5, kJoinSteps = 16, kPieceSteps = 12;
+constexpr int kPartFloats = 32 * (kHeadV + 2);  // a warp's piece: 32 rows of output, then their maxima and sums
+
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
 // sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps').
@@ -55,7 +63,6 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   if (tid < 2) p.amax[tid] = 0;
-  for (int i = tid; i < p.num_heads; i += 1024) p.units[i] = 0;
   int64_t base_k = 0;
   int base_q = 0;
   const int64_t table = static_cast<int64_t>(p.width) * p.page_size;
@@ -130,6 +137,40 @@ __device__ __forceinline__ int find_seq(const int* start, int batch, int x) {
   return lo;
 }
 
+// Whether to split, by steps: the time of the pass without it and an even share of a pair. An eighth off, because with
+// every pair busy the clock falls by as much (1024 tokens behind 16384 x 32 heads, 64 units: 186 us whole, on 64 pairs at
+// 1.87 GHz; 186 us and the join split over 76, at 1.75 GHz). 4096 tokens x 4 heads: 60 us split, 70 whole; x 16 heads,
+// where it is not: 118 and 94.
+__host__ __device__ __forceinline__ bool split_pays(int64_t whole, int64_t even) {
+  return (even < kPieceSteps ? kPieceSteps : even) + kJoinSteps < whole - whole / 8;
+}
+// The split of a pass's units over the pairs. Without it the end is the longest unit's or, with more units than pairs, the
+// pairs-th and the next one's (units are taken the longest first). Every pair takes an equal run of the steps of all
+// units, and so at most one piece that begins inside a unit and one that ends inside one. Unit u of the steps
+// [first, first + steps) is in pieces 0, 1, ... of pairs pair0, pair0 + 1, ...; its first kUnitSteps stand for no keys.
+struct Split {
+  int64_t per_head, run;  // steps of a head, of a pair (0: units are not split)
+  __device__ __forceinline__ Split(const MlaPrefillParams& p, int tiles, int pairs) {
+    per_head = run = 0;
+    if (!p.split || static_cast<int64_t>(tiles) * p.heads > kSplitTiles) return;
+    per_head = __ldcg(p.steps + tiles);
+    const int64_t most = __ldcg(p.steps + 255), even = (per_head * p.heads + pairs - 1) / pairs;
+    run = max(even, static_cast<int64_t>(kPieceSteps));
+    const int64_t second = tiles * p.heads <= pairs ? 0 : 2 * static_cast<int64_t>(__ldcg(p.steps + 256 + (pairs - 1) / p.heads));
+    const int64_t whole = max(most, second);
+    if (!split_pays(whole, even)) run = 0;
+  }
+  __device__ __forceinline__ int pieces(int64_t first, int steps, int& pair0) const {
+    pair0 = static_cast<int>(first / run);
+    if (steps <= kUnitSteps) return 1;
+    if ((pair0 + 1) * run - first <= kUnitSteps) ++pair0;
+    return static_cast<int>((first + steps - 1) / run) - pair0 + 1;
+  }
+  __device__ __forceinline__ int slot(int64_t first, int pair0, int piece) const {  // two for each pair
+    return 2 * (pair0 + piece) + (piece == 0 && first > pair0 * run ? 1 : 0);
+  }
+};
+
 __device__ __forceinline__ unsigned finite_bits2(uint32_t two, unsigned top) {  // larger finite |bf16| of a pair, as fp32 bits
   const unsigned lo = (two << 16) & 0x7fffffffu, hi = two & 0x7fff0000u;
   if (lo < 0x7f800000u) top = max(top, lo);
@@ -155,6 +196,8 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
   unsigned top_k = 0, top_v = 0;
   __shared__ unsigned group_s[3][8];  // of each warp: rows not finite, largest latent, largest rotary key
   pdl_launch_dependents();
+  if (blockIdx.x == gridDim.x - 1)
+    for (int i = threadIdx.x; i < p.num_heads; i += 256) p.units[i] = 0;
   const int wrows = p.num_heads * (kNope + kHeadV);
 #pragma unroll 4
   for (int r = blockIdx.x * 8 + warp; r < wrows; r += gridDim.x * 8) {
@@ -220,6 +263,50 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
       if ((lane == 8 || lane == 16) && m != 0) atomicMax(p.amax + 2 + 2 * b + (lane >> 4), m);
     }
     __syncthreads();
+  }
+  if (p.split && blockIdx.x == gridDim.x - 1) {
+    // first step of each query tile: a step a key tile that its last row sees, and those that a unit costs besides
+    __shared__ int steps_s[256];
+    steps_s[threadIdx.x] = 0;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < p.batch) {  // at most kSplitTiles sequences; malformed offsets may make more tiles
+      const int b = threadIdx.x, nq = __ldg(p.q_start + 2 * b + 1), n = __ldg(p.kv_len + b), t0 = __ldg(p.qt_start + b);
+      for (int i = 0; i * kQTile < nq && t0 + i < 256; ++i) {
+        const int see = p.causal ? min(n, n - nq + min(kQTile * (i + 1), nq)) : n;
+        steps_s[t0 + i] = (max(see, 0) + kAlign - 1) / kAlign + kUnitSteps;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int v[8], sum = 0, most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = steps_s[8 * lane + i];
+        most = max(most, v[i]);
+        sum += v[i];
+      }
+      int at = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+      }
+      at -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (8 * lane + i < 255) p.steps[8 * lane + i] = at;
+        at += v[i];
+      }
+      most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(most));
+      if (lane == 0) p.steps[255] = most;
+    }
+    // query tiles, the longest first
+    const int mine = steps_s[threadIdx.x];
+    int longer = 0;
+#pragma unroll 8
+    for (int i = 0; i < kSplitTiles; ++i)
+      longer += steps_s[i] > mine || (steps_s[i] == mine && i < static_cast<int>(threadIdx.x));
+    if (mine > 0) p.steps[256 + longer] = mine;
   }
   __shared__ unsigned top_s[2][8];
   top_k = __reduce_max_sync(0xffffffffu, top_k);
@@ -509,14 +596,21 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // are in use at once (80 KB at 128 keys). One CTA alone has room for 1.6 key tiles
 // in flight, and its MMAs waited for loads (measured: 3900 to 4000 clocks a key tile of
 // both query tiles, against 2560 of MMAs). A pair keeps half of each key and value tile
-// in each CTA, which gives a ring of three tiles, and halves the L2 reads: 2810 clocks,
-// the tensor cores busy for 91 % of them.
+// in each CTA, which gives a ring of three tiles, and halves the L2 reads: 2520 to 2600
+// clocks once caches and clock have settled, all of them MMAs (the clock then holds
+// 1.75 to 1.87 GHz of 2.07: the power is what is left to save).
 //
 // The pairs are persistent: a unit is the 512 query rows of one head; a pair begins with the unit of its own number
 // and takes the next ones from a counter (heads in groups, the query tiles of the most keys first), a few key tiles
 // before it needs them. What a unit costs beside its key tiles is then the copy and turning of its queries, the first
 // scores and the last output: 7 us, where a pair launched per unit took 13 to 15. The barriers' phases, the rings and
 // the turns simply run on from unit to unit.
+//
+// With few units (a chunk of a prompt behind a long prefix, few heads) pairs would be idle: then each takes an equal run
+// of the key tiles of all units (as the plan's lengths make them), writes outputs and statistics of the pieces of units
+// that others have a part of in fp32, and a kernel behind it joins them. 200 tokens behind 16384 x 16 heads: 123 us
+// instead of 228 in all, 1024 behind 32768 x 16 heads 305 instead of 456, 256 behind 131072 x 1 head 189 instead of
+// 1346. The pass that may split has a kernel of its own: a key tile takes 2 % longer in it.
 //
 // Roles in each CTA: two softmax warpgroups and two MMA warps (one of each per tile;
 // the even CTA's issue for both CTAs, in turns), a copy warp. Issuing an MMA takes
@@ -532,7 +626,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // small ones fp16 normals. Every wait is bounded: on a timeout the CTA flags
 // the device error word and leaves after draining its copies and MMAs.
 //
-// Measured: 8192 causal tokens x 16 heads 208 us (1650 TFLOP/s), 1024 tokens behind
+// Measured: 8192 causal tokens x 16 heads 197 us (1740 TFLOP/s), 1024 tokens behind
 // 16384 x 32 heads 193 us (1720 TFLOP/s, on 64 of the 76 pairs).
 constexpr int kKTile = 128, kSlots = 3;
 constexpr int kQRegion = 128 * 128, kQTileBytes = 3 * kQRegion;  // 128 rows x 64 values; a CTA's half of a query tile
@@ -614,11 +708,17 @@ __device__ __forceinline__ void st_async(uint32_t addr, int value, uint32_t bar)
                : "memory");
 }
 
+__device__ __forceinline__ float natural_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+}
+
 // Words of a unit in shared memory: whether there is one, head of the pass, first query row of the sequence, its
-// queries, their first row among all, its keys, their first packed row, key tiles of the two query tiles, exponents.
-enum : int { U_OK = 0, U_HEAD, U_ROW, U_NQ, U_Q0, U_KEYS, U_KV0, U_NT0, U_NT1, U_EK, U_EV };
+// queries, their first row among all, its keys (from the piece's first on), that one's packed row, key tiles of the two
+// query tiles, exponents; where a piece's rows go, -1: the unit is in one piece.
+enum : int { U_OK = 0, U_HEAD, U_ROW, U_NQ, U_Q0, U_KEYS, U_KV0, U_NT0, U_NT1, U_EK, U_EV, U_SLOT };
 constexpr uint64_t kUnitWaitNs = 10 * kWaitNs;  // a unit may last longer than any wait inside it
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kAtThreads, 1)
     gqa_mla_prefill_attn_kernel(const MlaPrefillParams p, const __grid_constant__ AttnMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -668,12 +768,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       int s = 0, keys = 0, values = 0;  // slot, counts of copies begun
       uint32_t ph = 1;                  // parity of the slot's previous release
       int queries[2] = {0, 0};          // loads of each tile's queries
-      int rank = blockIdx.x >> 1, next = 0;
+      const int pair = blockIdx.x >> 1;
+      int rank = pair, next = 0;
       bool good = true;
+      const Split cut(p, tiles, pairs);
+      const bool split = kSplit && cut.run > 0;
+      int64_t x = cut.run * pair;
+      const int64_t x_end = min(x + cut.run, cut.per_head * p.heads);
 #pragma unroll 1
       for (int it = 0;; ++it) {
         const int us = it & 1;
-        if (it > 0) {  // the even CTA took the unit's number, the odd one gets it
+        if (it > 0 && !split) {  // the even CTA took the unit's number, the odd one gets it
           const uint32_t mail = base + kAtMail + 4 * us;
           if (half == 0) {
             rank = pairs + __shfl_sync(0xffffffffu, next, 0);
@@ -690,17 +795,42 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           __syncwarp();
         }
-        const bool ok = rank < static_cast<int64_t>(tiles) * p.heads;
+        bool ok = false;
         int hp = 0, b = 0, i0 = 0, n = 0, kv0 = 0, ek = 0, ev = 0, nt[2] = {0, 0};
+        int qt = 0, k0 = 0, k1 = INT_MAX, slot = -1;
         int2 qs = {0, 0};
+        if (!split) {
+          ok = rank < static_cast<int64_t>(tiles) * p.heads;
+          if (ok) {
+            // in order: groups of heads whose keys and values stay in L2 together, within a group the last query tiles
+            // (the most keys, if causal) first
+            const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
+            const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
+            const int gh = min(p.head_group, p.heads - group * p.head_group);
+            qt = tiles - 1 - in_group / gh;
+            hp = group * p.head_group + in_group % gh;
+          }
+        }
+        while (split && !ok && x < x_end) {
+          hp = static_cast<int>(x / cut.per_head);
+          const int at = static_cast<int>(x - hp * cut.per_head);
+          qt = 0;
+#pragma unroll
+          for (int i = 0; i < kSplitTiles / 32 + 1; ++i) {
+            const int t = 32 * i + lane + 1;
+            qt += __popc(__ballot_sync(0xffffffffu, t < tiles && __ldcg(p.steps + min(t, tiles)) <= at));
+          }
+          const int u0 = __ldcg(p.steps + qt), steps = __ldcg(p.steps + qt + 1) - u0;
+          const int64_t first = hp * cut.per_head + u0;
+          const int begin = at - u0, end = static_cast<int>(min(x_end - first, static_cast<int64_t>(steps)));
+          k0 = max(begin - kUnitSteps, 0);
+          k1 = max(end - kUnitSteps, 0);
+          ok = k1 > k0 || (steps == kUnitSteps && begin == 0);
+          x = first + end;
+          int pair0;
+          slot = cut.pieces(first, steps, pair0) > 1 ? cut.slot(first, pair0, pair - pair0) : -1;
+        }
         if (ok) {
-          // in order: groups of heads whose keys and values stay in L2 together, within a group the last query tiles
-          // (the most keys, if causal) first
-          const int group = static_cast<int>(rank / (static_cast<int64_t>(tiles) * p.head_group));
-          const int in_group = static_cast<int>(rank - static_cast<int64_t>(group) * tiles * p.head_group);
-          const int gh = min(p.head_group, p.heads - group * p.head_group);
-          const int qt = tiles - 1 - in_group / gh;
-          hp = group * p.head_group + in_group % gh;
           // the last sequence that starts at this tile or before it
           b = __popc(__ballot_sync(0xffffffffu, start <= qt));
           for (int k = 33; b == k - 1 && k < p.batch; k += 32)
@@ -715,8 +845,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           for (int a = 0; a < 2; ++a) {
             const int last_row = min(i0 + 256 * (a + 1), qs.y) - 1;
             int see = last_row < i0 + 256 * a ? 0 : (p.causal ? min(n, n - qs.y + last_row + 1) : n);
-            nt[a] = (max(see, 0) + kKTile - 1) / kKTile;
+            nt[a] = max(min((max(see, 0) + kKTile - 1) / kKTile, k1) - k0, 0);
           }
+          n -= kKTile * k0;
+          kv0 += kKTile * k0;
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
@@ -744,6 +876,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           w[U_KV0] = kv0;
           w[U_NT0] = nt[0];
           w[U_NT1] = nt[1];
+          w[U_SLOT] = slot;
           mbar_arrive(bar(B_UFULL + us));
         }
         __syncwarp();
@@ -754,7 +887,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll 1
         for (int j = 0; j < total && good; ++j) {
           // the next unit is taken a few key tiles before the end of this one, not sooner: another pair may be free
-          if (j == ask_at && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
+          if (j == ask_at && !split && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
           __syncwarp();
           const uint32_t kd = base + kAtK + s * kKSlot, vd = base + kAtV + s * kVSlot;
           if (keys >= kSlots) good = warp_wait(bar(B_KFREE + s), ph, abort_s, err, kErrTimeoutEmpty);
@@ -773,8 +906,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         }
         if (!good) break;
-        if (total == 0 && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
-        if (it > 0 && half == 1 && lane == 0) mbar_arrive_cluster(cluster_addr(bar(B_MFREE + us), 0));
+        if (total == 0 && !split && half == 0 && lane == 0) next = atomicAdd(p.units + p.pass, 1);
+        if (it > 0 && !split && half == 1 && lane == 0) mbar_arrive_cluster(cluster_addr(bar(B_MFREE + us), 0));
         __syncwarp();
       }
       if (keys == 0) pdl_wait();
@@ -996,35 +1129,60 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         float l, hi;
         unpack2(l2, l, hi);
         l += hi;
-        const bool none = l == 0.f;  // the row sees no token
-        const float inv = pow2(unit_word(it, U_EV)) / l;
+        const int slot = kSplit ? unit_word(it, U_SLOT) : -1;
+        const float scale = pow2(unit_word(it, U_EV));
         const int i = unit_word(it, U_ROW) + 256 * a + 128 * half + 32 * wq + lane, nq = unit_word(it, U_NQ);
         const int64_t q0 = unit_word(it, U_Q0);
         const int h = p.head0 + unit_word(it, U_HEAD);
         leave_unit(it);
-        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV);
+        if (slot >= 0) {
+          // a piece: this warp's rows as 32 groups of four columns, a lane's row each, then the rows' (m, l)
+          int w = 8 * half + 4 * a + wq, ln = lane;
+          asm volatile("" : "+r"(w), "+r"(ln));  // (else their products are formed before the loop over units, and spilled)
+          float4* to = reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(slot) * 16 + w) * kPartFloats) + ln;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (nt > 0) {
-            tc_ld32(o_col + 32 * c, o);
-            tc_wait_ld();
-          } else {  // (undefined values would be kept from unit to unit, and spilled)
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            if (nt > 0) {
+              tc_ld16(o_col + 16 * c, o);
+              tc_wait_ld();
+            } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
-          }
-          if (i < nq)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t r[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-              out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
+              for (int k = 0; k < 16; ++k) o[k] = 0;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              to[32 * (4 * c + k)] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+          reinterpret_cast<float2*>(to - ln + kHeadV / 4 * 32)[ln] = make_float2(m, l);
+        } else {
+          const bool none = l == 0.f;  // the row sees no token
+          const float inv = scale / l;
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((q0 + i) * p.num_heads + h) * kHeadV);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            if (nt > 0) {
+              tc_ld32(o_col + 32 * c, o);
+              tc_wait_ld();
+            } else {  // (undefined values would be kept from unit to unit, and spilled)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0;
+            }
+            if (i < nq)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
+              }
+          }
         }
-        if (p.lse != nullptr && i < nq)
-          p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] = none ? -INFINITY : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        if (slot < 0 && p.lse != nullptr && i < nq)
+          p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i] = natural_lse(m, l);
       }
       tc_fence_before();
     }
@@ -1033,6 +1191,75 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __syncthreads();
   cluster_sync();  // the other CTA's arrivals, MMAs and copies are done too
   if (warp == 0) tc2_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the units that were split: a warp per 32 rows and kJoinCols columns, a lane a row, the pieces in order.
+// Bound by reading them, out of L2: 512 bytes a row and piece (8192 tokens x 4 heads in all: 107 us with 8 columns a warp,
+// 100 with 16 or 32).
+constexpr int kJoinThreads = 256, kJoinCols = 16;
+__global__ void __launch_bounds__(kJoinThreads) gqa_mla_prefill_join_kernel(const MlaPrefillParams p, int pairs) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int tiles = __ldcg(p.qt_start + p.batch);
+  const Split cut(p, tiles, pairs);
+  if (cut.run == 0) return;
+  const int tasks = tiles * p.heads * 16 * (kHeadV / kJoinCols), warps = gridDim.x * (kJoinThreads / 32);
+  for (int task = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); task < tasks; task += warps) {
+    const int c = task % (kHeadV / kJoinCols), rows = task / (kHeadV / kJoinCols) % 16, unit = task / (kHeadV / kJoinCols) / 16;
+    const int hp = unit / tiles, qt = unit - hp * tiles;
+    const int u0 = __ldcg(p.steps + qt), steps = __ldcg(p.steps + qt + 1) - u0;
+    const int64_t first = hp * cut.per_head + u0;
+    int pair0;
+    const int pieces = cut.pieces(first, steps, pair0);
+    if (pieces == 1) continue;
+    const int b = find_seq(p.qt_start, p.batch, qt);
+    const int2 qs = __ldcg(reinterpret_cast<const int2*>(p.q_start) + b);
+    const int row0 = (qt - __ldcg(p.qt_start + b)) * kQTile + 256 * ((rows >> 2) & 1) + 128 * (rows >> 3) + 32 * (rows & 3);
+    if (row0 >= qs.y) continue;
+    auto part = [&](int k) { return p.part + (static_cast<int64_t>(cut.slot(first, pair0, k)) * 16 + rows) * kPartFloats; };
+    auto stats = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + 32 * kHeadV) + lane); };
+    float m = -INFINITY, l = 0.f, o[kJoinCols];
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float2 ml = stats(k);
+      if (ml.y != 0.f) m = fmaxf(m, ml.x);  // a sum of 0: the row sees none of the piece's keys
+    }
+#pragma unroll
+    for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float2 ml = stats(k);
+      float4 v[kJoinCols / 4];
+#pragma unroll
+      for (int e = 0; e < kJoinCols / 4; ++e)
+        v[e] = __ldcg(reinterpret_cast<const float4*>(part(k)) + 32 * (kJoinCols / 4 * c + e) + lane);
+      if (ml.y == 0.f) continue;
+      const float f = ex2(ml.x - m);
+      l += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < kJoinCols / 4; ++e) {
+        o[4 * e] += f * v[e].x;
+        o[4 * e + 1] += f * v[e].y;
+        o[4 * e + 2] += f * v[e].z;
+        o[4 * e + 3] += f * v[e].w;
+      }
+    }
+    int ek, ev;
+    kv_exponents(p.amax, b, ek, ev);
+    const float inv = pow2(ev) / l;
+    const int i = row0 + lane, h = p.head0 + hp;
+    if (i >= qs.y) continue;
+    const int64_t row = static_cast<int64_t>(qs.x) + i;
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (row * p.num_heads + h) * kHeadV);
+#pragma unroll
+    for (int k = 0; k < kJoinCols / 8; ++k) {
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = l == 0.f ? 0u : pack_bf16(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+      out[kJoinCols / 8 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    if (c == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(h) * p.total_q + row] = natural_lse(m, l);
+  }
 }
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1063,6 +1290,10 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
   p->kr = take(cap * kRope * 2);
   p->kn = take(cap * kNope * 2 * hp);
   p->vv = take(cap * kHeadV * 2 * hp);
+  if (cap >= kSplitRows) {
+    p->steps = reinterpret_cast<int*>(take(512 * 4));
+    p->part = reinterpret_cast<float*>(take(static_cast<size_t>(2 * kSplitPairs) * 16 * kPartFloats * 4));
+  }
   return at;
 }
 
@@ -1091,17 +1322,31 @@ cudaError_t launch_next(void (*fn)(Args...), int cluster, dim3 grid, int threads
 }  // namespace
 
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream) {
+  const int64_t q_tiles = (p.total_q + int64_t{kQTile - 1} * p.batch) / kQTile;  // at most
+  const int all_pairs = sm_count / 2;
+  // Whether sequences of the average lengths would be split (the plan's lengths then decide): a pass that may split but
+  // does not takes 6 us longer (its own attention kernel 2 to 3, an empty join 3, the steps 1).
+  auto may_split = [&](int heads) {
+    const int64_t units = q_tiles * heads, n = p.cap / p.batch, nq = p.total_q / p.batch;
+    const int64_t most = n / kAlign + kUnitSteps;
+    const int64_t mean = most - (p.causal && nq > kQTile ? (nq - kQTile) / (2 * kAlign) : 0);
+    return p.part != nullptr && units <= kSplitTiles && mean > 0 &&
+           split_pays(units <= all_pairs || most > 2 * mean ? most : 2 * mean, (units * mean + all_pairs - 1) / all_pairs);
+  };
+  const int tail = p.num_heads % p.heads_per_pass;
+  p.split = may_split(p.num_heads < p.heads_per_pass ? p.num_heads : p.heads_per_pass) || (tail != 0 && may_split(tail));
   gqa_mla_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_next(gqa_mla_prefill_gather_kernel, 1, dim3(sm_count * 8), 256, 0, stream, p);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> ex_done[kMaxDevices], at_done[kMaxDevices];
+  static std::atomic<int> ex_done[kMaxDevices], at_done[kMaxDevices], sp_done[kMaxDevices];
   e = set_smem_limit_once(ex_done, reinterpret_cast<const void*>(gqa_mla_prefill_expand_kernel), kExSmem);
   if (e != cudaSuccess) return e;
-  e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel), kAtSmem);
+  e = set_smem_limit_once(at_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel<false>), kAtSmem);
   if (e != cudaSuccess) return e;
-  const int64_t q_tiles = p.total_q / kQTile + p.batch;
+  e = set_smem_limit_once(sp_done, reinterpret_cast<const void*>(gqa_mla_prefill_attn_kernel<true>), kAtSmem);
+  if (e != cudaSuccess) return e;
   const int64_t fit = kGroupBytes / (static_cast<int64_t>(p.cap) * (kNope + kHeadV) * 2);
   p.pass = 0;
   for (int h0 = 0; h0 < p.num_heads; h0 += p.heads_per_pass, ++p.pass) {
@@ -1126,9 +1371,20 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
     if (!tc_encode(&at.q, kBf, p.q, 3, q_size, q_pitch, q_box)) return cudaErrorInvalidValue;
     e = launch_next(gqa_mla_prefill_expand_kernel, 2, dim3(sm_count / 2 * 2), kExThreads, kExSmem, stream, p, ex);
     if (e != cudaSuccess) return e;
-    const int64_t units = q_tiles * p.heads, pairs = sm_count / 2;
-    e = launch_next(gqa_mla_prefill_attn_kernel, 2, dim3(static_cast<unsigned>(2 * (units < pairs ? units : pairs))), kAtThreads,
-                    kAtSmem, stream, p, at);
+    const int64_t units = q_tiles * p.heads;
+    int64_t pairs = all_pairs;
+    p.split = may_split(p.heads);
+    if (p.split) {
+      pairs = pairs < kSplitPairs ? pairs : kSplitPairs;
+      const dim3 grid(static_cast<unsigned>(2 * pairs));
+      e = launch_next(gqa_mla_prefill_attn_kernel<true>, 2, grid, kAtThreads, kAtSmem, stream, p, at);
+      if (e != cudaSuccess) return e;
+      e = launch_next(gqa_mla_prefill_join_kernel, 1, dim3(sm_count * 4), kJoinThreads, 0, stream, p,
+                      static_cast<int>(pairs));
+    } else {
+      const dim3 grid(static_cast<unsigned>(2 * (units < pairs ? units : pairs)));
+      e = launch_next(gqa_mla_prefill_attn_kernel<false>, 2, grid, kAtThreads, kAtSmem, stream, p, at);
+    }
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

@@ -175,6 +175,56 @@ def test_prefill_several_units_a_pair(causal):
     assert _lib.gqa_paged_decode_device_error() == 0
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,h", [([(200, 6000)], 1), ([(1, 20000), (2, 129), (700, 1200)], 2), ([(520, 4000)] * 2, 20),
+                                    ([(1, 9000), (600, 8100), (0, 0), (520, 0), (300, 40), (513, 9000)], 2)])
+def test_prefill_units_split_over_the_keys(lens, h, causal):
+    """Few units with many keys: pieces of a unit in several pairs of CTAs, joined by whichever is last."""
+    c = case(lens, h, 64, 25 + h)
+    g = on_gpu(c)
+    out, lse = pkg.mla_prefill(**g, causal=causal)
+    check(out, lse, c, 192 ** -0.5, causal)
+    for _ in range(20):
+        out2, lse2 = pkg.mla_prefill(**g, causal=causal)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [pkg.mla_prefill(**g, causal=causal, stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, o) and torch.equal(lse, l) for o, l in got)
+    out3 = torch.zeros_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkg.mla_prefill(**g, causal=causal, out=out3, with_lse=False)
+    for _ in range(2):
+        out3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, out3)
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+def test_prefill_split_in_several_passes():
+    """The pieces of one pass over the heads are joined before the next pass writes its own."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    c = case([(60, 9000)], 5, 64, 34)
+    out, lse = pkg.mla_prefill(**on_gpu(c), max_kv_tokens=2_000_000)  # two heads a pass
+    check(out, lse, c, 192 ** -0.5, True)
+
+
+def test_prefill_split_rows_not_finite():
+    """A token that is not finite, late in a long sequence: rows that see it are NaN, the others as without it."""
+    c = case([(200, 6000)], 2, 64, 33)
+    blk = int(c["block_table"][0, 5900 // 64])
+    c["kv_cache"][blk, 5900 % 64, 0, :512] = 0
+    want, _ = pkg.mla_prefill(**on_gpu(c))
+    c["kv_cache"][blk, 5900 % 64, 0, :512] = float("inf")
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    assert torch.equal(out[:100], want[:100])  # row i sees the tokens up to 5800 + i
+    assert out[100:].isnan().all() and lse[:, 100:].isnan().all() and lse[:, :100].isfinite().all()
+
+
 def test_prefill_rows_that_see_nothing():
     """More queries than cached tokens (their first rows see none), lengths of 0, blocks outside the pool."""
     c = case([(70, 3), (5, 0), (40, 40), (300, 200)], 3, 8, 5, bad_blocks=5)
