@@ -283,6 +283,7 @@ struct MlaPrefillParams {
   float scale_log2;
   int batch, total_q, num_heads, page_size, num_blocks, width, causal;
   int cap;        // packed key rows the workspace holds, a multiple of 128
+  int q_tiles;    // query tiles that total_q rows of batch sequences make at most
   int heads_per_pass;
   // workspace
   int* kv_len;    // [batch] keys of each sequence that are read

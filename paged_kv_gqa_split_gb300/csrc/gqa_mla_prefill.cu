@@ -56,15 +56,16 @@ constexpr int kPartFloats = 32 * (kHeadV + 2);  // a warp's piece: 32 rows of ou
 
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
-// sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps').
+// sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps'). Only
+// malformed offsets, whose sequences share rows, have more query tiles than p.q_tiles;
+// those past it are left out.
 __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPrefillParams p) {
   __shared__ int64_t sk[32];
   __shared__ int sq[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   if (tid < 2) p.amax[tid] = 0;
-  int64_t base_k = 0;
-  int base_q = 0;
+  int64_t base_k = 0, base_q = 0;
   const int64_t table = static_cast<int64_t>(p.width) * p.page_size;
   for (int b0 = 0; b0 < p.batch; b0 += 1024) {
     const int b = b0 + tid;
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
     }
     __syncthreads();
     int64_t before_k = base_k;
-    int before_q = base_q;
+    int64_t before_q = base_q;
     for (int w = 0; w < 32; ++w) {
       if (w < warp) {
         before_k += sk[w];
@@ -117,13 +118,13 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
       }
       p.kv_len[b] = len;
       p.kv_start[b] = static_cast<int>(min(end - rows, static_cast<int64_t>(p.cap)));
-      p.qt_start[b] = before_q + q - tiles;
+      p.qt_start[b] = static_cast<int>(min(before_q + q - tiles, static_cast<int64_t>(p.q_tiles)));
     }
     __syncthreads();
   }
   if (tid == 0) {
     p.kv_start[p.batch] = static_cast<int>(min(base_k, static_cast<int64_t>(p.cap)));
-    p.qt_start[p.batch] = base_q;
+    p.qt_start[p.batch] = static_cast<int>(min(base_q, static_cast<int64_t>(p.q_tiles)));
   }
 }
 
@@ -1323,6 +1324,7 @@ cudaError_t launch_next(void (*fn)(Args...), int cluster, dim3 grid, int threads
 
 cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t stream) {
   const int64_t q_tiles = (p.total_q + int64_t{kQTile - 1} * p.batch) / kQTile;  // at most
+  p.q_tiles = static_cast<int>(q_tiles);
   const int all_pairs = sm_count / 2;
   // Whether sequences of the average lengths would be split (the plan's lengths then decide): a pass that may split but
   // does not takes 6 us longer (its own attention kernel 2 to 3, an empty join 3, the steps 1).

@@ -342,6 +342,22 @@ def test_prefill_malformed_offsets_are_reported_and_stay_in_range():
         assert torch.all(guard[:50] == 5.0) and torch.all(guard[100:] == 5.0)
 
 
+@pytest.mark.parametrize("n,h", [(300, 3), (9000, 2)])
+def test_prefill_malformed_offsets_that_share_rows(n, h):
+    """More query tiles than the rows make: reported, nothing outside the rows written, and the next call is right."""
+    c = case([(2048, n), (0, 0), (0, n), (0, 0)], h, 64, 23)
+    g = on_gpu(c)
+    g["cu_seqlens_q"] = torch.tensor([0, 2048, 0, 2048, 0], dtype=torch.int32, device="cuda")
+    buf = torch.full((2048 + 64, h, 128), 5.0, dtype=BF, device="cuda")
+    pkg.mla_prefill(**g, out=buf[32:-32])
+    assert _lib.gqa_paged_decode_device_error() == 8
+    assert (buf[:32] == 5).all() and (buf[-32:] == 5).all()
+    c = case([(70, n)], h, 64, 24)
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    check(out, lse, c, 192 ** -0.5, True)
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
 def test_prefill_many_sequences():
     """More sequences than one chunk of the plan's prefix sums (1024)."""
     g = torch.Generator().manual_seed(17)
