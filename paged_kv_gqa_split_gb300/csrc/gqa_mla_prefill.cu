@@ -56,7 +56,9 @@ constexpr int kPartFloats = 32 * (kHeadV + 2);  // a warp's piece: 32 rows of ou
 
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
-// sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps'). Only
+// sums run over chunks of 1024 sequences (a warp's by shuffles, then the warps'). What this and
+// the later kernels write into the workspace is read with __ldcg throughout: the readers start
+// before the writers end, and the non-coherent load is for words that no one writes meanwhile. Only
 // malformed offsets, whose sequences share rows, have more query tiles than p.q_tiles;
 // those past it are left out.
 __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPrefillParams p) {
@@ -207,11 +209,11 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
     if ((r & 255) < kNope) top_k = max(top_k, t); else top_v = max(top_v, t);
   }
   pdl_wait();
-  const int groups = __ldg(p.kv_start + p.batch) / 32;  // 32 packed rows share a word of valid bits and a sequence
+  const int groups = __ldcg(p.kv_start + p.batch) / 32;  // 32 packed rows share a word of valid bits and a sequence
   for (int g = blockIdx.x; g < groups; g += gridDim.x) {
     // the last sequence that starts at or before the row (empty ones start where the next does)
     const int b = find_seq(p.kv_start, p.batch, 32 * g);
-    const int t0 = 32 * g - __ldg(p.kv_start + b), n = __ldg(p.kv_len + b);
+    const int t0 = 32 * g - __ldcg(p.kv_start + b), n = __ldcg(p.kv_len + b);
     // lane l looks up row l's slot
     int64_t slot = -1;
     if (t0 + lane < n) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
     steps_s[threadIdx.x] = 0;
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < p.batch) {  // at most kSplitTiles sequences; malformed offsets may make more tiles
-      const int b = threadIdx.x, nq = __ldg(p.q_start + 2 * b + 1), n = __ldg(p.kv_len + b), t0 = __ldg(p.qt_start + b);
+      const int b = threadIdx.x, nq = __ldcg(p.q_start + 2 * b + 1), n = __ldcg(p.kv_len + b), t0 = __ldcg(p.qt_start + b);
       for (int i = 0; i * kQTile < nq && t0 + i < 256; ++i) {
         const int see = p.causal ? min(n, n - nq + min(kQTile * (i + 1), nq)) : n;
         steps_s[t0 + i] = (max(see, 0) + kAlign - 1) / kAlign + kUnitSteps;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   pdl_wait();
   pdl_launch_dependents();  // after the wait: what the next kernel reads before its own is then complete
-  const int total = __ldg(p.kv_start + p.batch);
+  const int total = __ldcg(p.kv_start + p.batch);
   const int64_t all = static_cast<int64_t>((total + 255) / 256) * p.heads;
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   const int u0 = static_cast<int>(all * pair / pairs), u1 = static_cast<int>(all * (pair + 1) / pairs);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         int ek, ev;
         kv_exponents(p.amax, find_seq(p.kv_start, p.batch, m0), ek, ev);
         f = pow2(part == 0 ? -ek : -ev);
-        bad = ((__ldg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
+        bad = ((__ldcg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
       }
       const bool good = warp_wait(bar(E_DFULL + (i & 1)), (i >> 1) & 1, abort_s, err, kErrTimeoutFull);
       int every;  // the four warps agree, so that none is left at the barriers below
