@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kMlaMergeThreads) gqa_mla_merge_kernel(const M
   const int B = p.batch;
   const int j = blockIdx.x / G, row0 = (blockIdx.x - j * G) * kMlaRows;
   const bool boundary = j + 1 < p.plan.tier1_ctas + p.plan.tier2_ctas;
-  const int T = __ldg(p.kv_indptr + B);
-  pdl_wait();
+  pdl_wait();  // the decode lets this grid start before the scan's words (kv_indptr, bounds) are complete
+  const int T = __ldcg(p.kv_indptr + B);
   const int4 rec0 = boundary ? __ldcg(p.split_rec + j) : make_int4(0, 0, 0, 0);
   const int4 rec1 = boundary ? __ldcg(p.split_rec + (p.plan.tier1_ctas + p.plan.tier2_ctas) + j)
                              : make_int4(0, 0, 0, 0);

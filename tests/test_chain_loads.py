@@ -35,3 +35,10 @@ def test_prompt_pass_reads_its_workspace_past_l1():
     fields.remove("err")
     for arg in noncoherent(source("gqa_mla_prefill.cu")):
         assert not any(re.search(rf"\bp\.{f}\b", arg) for f in fields), arg
+
+
+def test_latent_merge_reads_the_token_count_behind_its_wait():
+    """The decode triggers its dependents before its own wait, so the merge may start while the scan still runs."""
+    body = source("gqa_mla.cu").split("gqa_mla_merge_kernel(const MlaParams p) {")[1]
+    before = body[:body.index("pdl_wait();")]
+    assert "p.kv_indptr" not in before and "p.bounds" not in before
