@@ -32,15 +32,24 @@ enum : int {
   F_QREG = 32,   // Q fragments were prefetched into registers when the tile was issued
 };
 
+// An entry of kv_indptr: the caller's (constant while the kernel runs, the non-coherent load), or WRITTEN by an
+// earlier kernel of the chain, which may still run when this one starts: then a plain load behind pdl_wait (and not
+// __ldcg: the latent decode looks its ranges up so often that reading them past L1 made it 2 to 5 % slower).
+template <bool WRITTEN>
+__device__ __forceinline__ int load_index(const int* p) {
+  return WRITTEN ? *p : __ldg(p);
+}
+
 // Largest b in [0, batch) with indptr[b] <= t (needs indptr[0] <= t < indptr[batch]).
 // Warp-cooperative 32-ary search: each round samples 32 evenly spaced entries.
 // Returns -1 if indptr[0] > t (malformed table).
-__device__ __forceinline__ int warp_find_seq(const int* __restrict__ indptr, int batch, int t, int lane) {
+template <bool WRITTEN = false>
+__device__ __forceinline__ int warp_find_seq(const int* indptr, int batch, int t, int lane) {
   int lo = 0, hi = batch;
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int pos = lo + lane * step;
-    const int val = pos < hi ? __ldg(indptr + pos) : INT32_MAX;
+    const int val = pos < hi ? load_index<WRITTEN>(indptr + pos) : INT32_MAX;
     const unsigned m = __ballot_sync(0xffffffffu, val <= t);
     if (m == 0) return -1;
     const int k = 31 - __clz(m);
@@ -49,16 +58,17 @@ __device__ __forceinline__ int warp_find_seq(const int* __restrict__ indptr, int
     lo = nlo;
   }
   const int pos = lo + lane;
-  const int val = pos < hi ? __ldg(indptr + pos) : INT32_MAX;
+  const int val = pos < hi ? load_index<WRITTEN>(indptr + pos) : INT32_MAX;
   const unsigned m = __ballot_sync(0xffffffffu, val <= t);
   if (m == 0) return -1;
   return lo + 31 - __clz(m);
 }
 
 // kv_indptr[base + lane], or INT32_MAX past the end.
-__device__ __forceinline__ int load_indptr_window(const int* __restrict__ indptr, int batch, int base, int lane) {
+template <bool WRITTEN = false>
+__device__ __forceinline__ int load_indptr_window(const int* indptr, int batch, int base, int lane) {
   const int pos = base + lane;
-  return pos <= batch ? __ldg(indptr + pos) : INT32_MAX;
+  return pos <= batch ? load_index<WRITTEN>(indptr + pos) : INT32_MAX;
 }
 
 // First round of warp_find_window for the whole table, which needs no token

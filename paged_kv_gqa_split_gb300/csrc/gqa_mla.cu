@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_scan_kernel(const int* __restric
 constexpr int kMlaFillThreads = 256;
 constexpr int kMlaFillPer = 4;
 constexpr int kMlaFillChunk = kMlaFillThreads * kMlaFillPer;
-__global__ void __launch_bounds__(kMlaFillThreads) gqa_mla_fill_kernel(const int* __restrict__ indptr,
+__global__ void __launch_bounds__(kMlaFillThreads) gqa_mla_fill_kernel(const int* indptr,
                                                                       const int* __restrict__ block_table,
                                                                       int chunks, int width, int page_size,
                                                                       int num_blocks, int* __restrict__ slots) {
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMlaFillThreads) gqa_mla_fill_kernel(const int
   pdl_wait();  // indptr comes from the scan kernel
   const int b = blockIdx.x / chunks;
   const int t0 = (blockIdx.x - b * chunks) * kMlaFillChunk + threadIdx.x;
-  const int base = __ldg(indptr + b), n = __ldg(indptr + b + 1) - base;
+  const int base = indptr[b], n = indptr[b + 1] - base;
   if (t0 - static_cast<int>(threadIdx.x) >= n) return;
   const int* row = block_table + static_cast<int64_t>(b) * width;
   int page[kMlaFillPer];
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
   const uint8_t* __restrict__ kv = static_cast<const uint8_t*>(p.kv);
   const __nv_bfloat16* __restrict__ qg = static_cast<const __nv_bfloat16*>(p.q);
   const int B = p.batch;
-  const int T = __ldg(p.kv_indptr + B);
+  const int T = __ldcg(p.kv_indptr + B);
   const int HG = p.rows / kMlaRows;
   MlaSmemPlan* splan = reinterpret_cast<MlaSmemPlan*>(smem + L::kPlanOff + w * 32);
   int64_t u0, u1;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
             m = __ballot_sync(0xffffffffu, win <= tt);
             if (m != 0xffffffffu) break;
             wb += 31;
-            win = load_indptr_window(p.kv_indptr, B, wb, lane);
+            win = load_indptr_window<true>(p.kv_indptr, B, wb, lane);
           }
           if (m == 0) {
             if (lane == 0) atomicOr(p.err, kErrBadIndptr);
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
 #pragma unroll
       for (int cc = 0; cc < kMlaIdsRing / 32; ++cc) request_ids(ib + 32 * cc + lane);
       cp_async_commit();
-      wb = warp_find_seq(p.kv_indptr, B, tt, lane);
-      if (wb >= 0) win = load_indptr_window(p.kv_indptr, B, wb, lane);
+      wb = warp_find_seq<true>(p.kv_indptr, B, tt, lane);
+      if (wb >= 0) win = load_indptr_window<true>(p.kv_indptr, B, wb, lane);
       cp_async_wait<0>();
       __syncwarp();
       if (wb < 0) {
@@ -569,12 +569,12 @@ __global__ void __launch_bounds__(kMlaMergeThreads) gqa_mla_merge_kernel(const M
   const int j = blockIdx.x / G, row0 = (blockIdx.x - j * G) * kMlaRows;
   const bool boundary = j + 1 < p.plan.tier1_ctas + p.plan.tier2_ctas;
   pdl_wait();  // the decode lets this grid start before the scan's words (kv_indptr, bounds) are complete
-  const int T = __ldcg(p.kv_indptr + B);
+  const int T = p.kv_indptr[B];
   const int4 rec0 = boundary ? __ldcg(p.split_rec + j) : make_int4(0, 0, 0, 0);
   const int4 rec1 = boundary ? __ldcg(p.split_rec + (p.plan.tier1_ctas + p.plan.tier2_ctas) + j)
                              : make_int4(0, 0, 0, 0);
   for (int b = blockIdx.x; b < B; b += gridDim.x) {  // empty sequences: O = 0, LSE = -inf
-    if (__ldg(p.kv_indptr + b) == __ldg(p.kv_indptr + b + 1)) {
+    if (p.kv_indptr[b] == p.kv_indptr[b + 1]) {
       uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(b) * p.rows * kMlaDv);
       for (int i = tid; i < p.rows * kMlaDv * 2 / 16; i += kMlaMergeThreads) ob[i] = make_uint4(0, 0, 0, 0);
       if (p.lse != nullptr)

@@ -117,14 +117,14 @@ struct TcWalker {
   bool seg_open, ok;
   SplitInfo p_si;
 
-  __device__ int64_t begin_of(int64_t c) const { return bounds != nullptr ? __ldg(bounds + c) : pl.begin(c); }
+  __device__ int64_t begin_of(int64_t c) const { return bounds != nullptr ? bounds[c] : pl.begin(c); }
   // CTA whose range holds unit u: with bounds, the last c with bounds[c] <= u (ranges may be empty)
   __device__ int64_t cta_of(int64_t u) const {
     if (bounds == nullptr) return pl.cta_of(u);
     int lo = 0, hi = pl.P1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(bounds + mid) <= u) lo = mid; else hi = mid;
+      if (bounds[mid] <= u) lo = mid; else hi = mid;
     }
     return lo;
   }
@@ -135,8 +135,8 @@ struct TcWalker {
     B = batch;
     T = total;
     pl = plan;
-    u0 = cuts != nullptr ? __ldg(cuts + cta) : plan.begin(cta);
-    u1 = cuts != nullptr ? __ldg(cuts + cta + 1) : plan.end(cta);
+    u0 = cuts != nullptr ? cuts[cta] : plan.begin(cta);
+    u1 = cuts != nullptr ? cuts[cta + 1] : plan.end(cta);
     u_next = u0;
     hg = tt = t_stop = p_lo = p_hi = p_flags = pb = wb = win = 0;
     seg_open = false;
@@ -153,7 +153,7 @@ struct TcWalker {
             m = __ballot_sync(0xffffffffu, win <= tt);
             if (m != 0xffffffffu) break;
             wb += 31;
-            win = load_indptr_window(indptr, B, wb, lane);
+            win = load_indptr_window<true>(indptr, B, wb, lane);
           }
           if (m == 0) {
             if (lane == 0) atomicOr(err, kErrBadIndptr);
@@ -191,13 +191,13 @@ struct TcWalker {
       u_next = static_cast<int64_t>(hg) * T + t_stop;
       seg_open = true;
       p_hi = tt;
-      wb = warp_find_seq(indptr, B, tt, lane);
+      wb = warp_find_seq<true>(indptr, B, tt, lane);
       if (wb < 0) {
         if (lane == 0) atomicOr(err, kErrBadIndptr);
         ok = false;
         break;
       }
-      win = load_indptr_window(indptr, B, wb, lane);
+      win = load_indptr_window<true>(indptr, B, wb, lane);
     }
     return false;
   }
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kSlotOff);
 
-  const int T = __ldg(p.kv_indptr + p.batch);
+  const int T = p.kv_indptr[p.batch];
   const int HG = p.rows / R;
   const Plan pl = make_plan(static_cast<int64_t>(T) * HG, p.plan);
   TcWalker wk;

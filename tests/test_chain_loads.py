@@ -2,7 +2,8 @@
 
 The non-coherent load (__ldg) may be served from a cache line, or moved to a place, from before the words were
 written, so it is for a call's inputs alone. Words of the workspace that an earlier kernel of the chain writes are
-read with __ldcg, and behind the wait unless the kernel ahead has passed that wait itself.
+read with __ldcg or a plain load, and behind the wait unless the kernel ahead has passed that wait itself (then only
+with __ldcg).
 """
 import os
 import re
@@ -42,3 +43,13 @@ def test_latent_merge_reads_the_token_count_behind_its_wait():
     body = source("gqa_mla.cu").split("gqa_mla_merge_kernel(const MlaParams p) {")[1]
     before = body[:body.index("pdl_wait();")]
     assert "p.kv_indptr" not in before and "p.bounds" not in before
+
+
+def test_latent_decode_reads_the_scan_with_coherent_loads():
+    """kv_indptr and the ranges are the scan's words: no non-coherent load of them, by name or through a helper."""
+    for name in ("gqa_mla.cu", "gqa_mla_tc.cu"):
+        text = source(name)
+        for arg in noncoherent(text):
+            assert not re.search(r"\b(kv_indptr|indptr|bounds|cuts|cost_ptr|slots)\b", arg), (name, arg)
+        assert not re.search(r"\b(warp_find_seq|load_indptr_window|warp_find_window)\(", text)
+        assert not re.search(r"const int\* __restrict__ indptr", text)
