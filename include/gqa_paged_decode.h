@@ -537,9 +537,11 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
  * -inf. A token whose block lies outside [0, num_blocks) is left out; lengths
  * are clamped as in gqa_mla_decode. A token whose latent row is not all finite
  * makes the rows that see it NaN, and no others. Rows past cu_seqlens_q[batch] are left as
- * they were. The expanded keys and values are fp16, scaled by a power of two per
- * sequence (values below about 2^-29 of 512 * max|latent| * max|w_kv| lose bits);
- * everything else accumulates in fp32. lse carries that rounding of the keys:
+ * they were. The expanded keys and values are fp16, scaled by powers of two, one
+ * per sequence or, where its tokens differ by more than 2^8, one per token: a
+ * token's values below about 2^-29 of 512 * max|its latent| * max|w_kv| lose bits
+ * (2^-21 where the sequence has one), and no token's size costs another's.
+ * Everything else accumulates in fp32. lse carries that rounding of the keys:
  * about 2^-12 of a score's size.
  * With few queries and many tokens a row's sums are split and joined in an order
  * that the call's sizes and lengths determine: a call repeated gives the same bits.

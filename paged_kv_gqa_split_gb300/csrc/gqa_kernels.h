@@ -290,13 +290,16 @@ struct MlaPrefillParams {
   int* kv_start;  // [batch + 1] first packed row (multiples of 128)
   int* q_start;   // [batch][2] first query row and query count, cut to [0, total_q)
   int* qt_start;  // [batch + 1] first query tile
-  unsigned* amax;      // largest finite |value| bits: key weights, value weights, then [batch][2] latent, rotary key
+  unsigned* amax;      // largest finite |value| bits: key weights, value weights; from [4] on [batch][4] latent, rotary key, and
+                       // those of the token with the smallest ones above 0, inverted
   int* units;          // [num_heads] units of the attention taken so far, a counter a pass
   int* steps;          // [256] first step of each query tile (see kSplitTiles), [255] the most steps of one; then
                        // [256] the steps of each, the most first
   float* part;         // outputs and statistics of pieces; both NULL below kSplitRows packed rows
   unsigned* valid;     // [cap / 32] packed rows that hold a token of the pool
   unsigned* bad;       // [cap / 32] packed rows whose latent is not all finite
+  uint2* row_top;      // [cap] largest finite |value| bits of a row: latent, rotary key
+  float2* row_scale;   // [cap] in sequences whose rows have their own exponents: factor of the scores, exponent of the values
   void* lat;           // [cap][512] bf16
   void* kr;            // [cap][64] rotary keys: bf16 from the gather, fp16 (scaled) after the expansion
   void* kn;            // [heads_per_pass][cap][128] fp16 keys (scaled)

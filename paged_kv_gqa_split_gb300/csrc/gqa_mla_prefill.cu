@@ -13,9 +13,12 @@
 // result than one rounding of it, with fp16 1.01 x). fp16's range is kept by
 // powers of two, which change nothing else: a query row is brought to a largest
 // value in [2^10, 2^11); keys and values of a sequence have one exponent each, from the
-// bound 512 * max|c| * max|W| (and the rotary keys). The maxima are taken over finite
-// values, so an infinity stays with its row: a token whose latent is not all
-// finite gets NaN keys and zero values, which makes the rows that see it NaN
+// bound 512 * max|c| * max|W| (and the rotary keys). A sequence whose tokens' own maxima
+// lie more than 2^8 apart is "wide": there each token has exponents of its own, so that a
+// huge one costs no bits of the others (rows that do not see it, or give it no weight, are
+// what they are without it), and the attention has a second, slower loop for it. The maxima
+// are taken over finite values, so an infinity stays with its row: a token whose latent is
+// not all finite gets NaN keys and zero values, which makes the rows that see it NaN
 // and, a weight of 0 times 0 being 0, no others.
 // Scores, softmax statistics and outputs accumulate in fp32.
 //
@@ -52,7 +55,8 @@ constexpr int64_t kGroupBytes = int64_t{96} << 20;  // and of the heads whose CT
 // piece.
 constexpr int kSplitTiles = 152, kSplitPairs = 76, kSplitRows = 2048;
 constexpr int kUnitSteps = 5, kJoinSteps = 16, kPieceSteps = 12;
-constexpr int kPartFloats = 32 * (kHeadV + 2);  // a warp's piece: 32 rows of output, then their maxima and sums
+constexpr int kPartFloats = 32 * (kHeadV + 4);  // a warp's piece: 32 rows of output, then their maxima, sums and output units
+constexpr unsigned kWindow = 8;  // binades that the tokens of a sequence with one exponent may be apart
 
 // ------------------------------------------------------------------- plan
 // One block: lengths clamped to the table, packed starts, query tiles. Prefix
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(1024) gqa_mla_prefill_plan_kernel(const MlaPre
       if (nq > 0) len = static_cast<int>(min(static_cast<int64_t>(max(n, 0)), table));
       p.q_start[2 * b] = qs;
       p.q_start[2 * b + 1] = nq;
-      p.amax[2 + 2 * b] = p.amax[3 + 2 * b] = 0;
+      *reinterpret_cast<uint4*>(p.amax + 4 + 4 * b) = make_uint4(0, 0, 0, 0);
     }
     const int64_t rows = (static_cast<int64_t>(len) + kAlign - 1) / kAlign * kAlign;
     int64_t k = rows;
@@ -197,7 +201,8 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
 __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPrefillParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned top_k = 0, top_v = 0;
-  __shared__ unsigned group_s[3][8];  // of each warp: rows not finite, largest latent, largest rotary key
+  // of each warp: rows not finite; largest latent and rotary key of its rows; the smallest row's, inverted
+  __shared__ unsigned group_s[5][8];
   pdl_launch_dependents();
   if (blockIdx.x == gridDim.x - 1)
     for (int i = threadIdx.x; i < p.num_heads; i += 256) p.units[i] = 0;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
       v[i][1] = from >= 0 ? __ldg(src + 32 + lane) : zero;
       v[i][2] = from >= 0 && lane < 8 ? __ldg(src + 64 + lane) : zero;
     }
-    unsigned bad = 0, top_c = 0, top_r = 0;
+    unsigned bad = 0, top_c = 0, top_r = 0, low_c = 0, low_r = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t row = 32 * g + 4 * warp + i;
@@ -239,20 +244,25 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
       lat[lane] = v[i][0];
       lat[32 + lane] = v[i][1];
       if (lane < 8) reinterpret_cast<uint4*>(p.kr)[row * (kRope / 8) + lane] = v[i][2];
-      top_c = finite_bits(v[i][1], finite_bits(v[i][0], top_c));
-      top_r = finite_bits(v[i][2], top_r);
+      const unsigned c = __reduce_max_sync(0xffffffffu, finite_bits(v[i][1], finite_bits(v[i][0], 0)));
+      const unsigned r = __reduce_max_sync(0xffffffffu, finite_bits(v[i][2], 0));
+      if (lane == 0) p.row_top[row] = make_uint2(c, r);
+      top_c = max(top_c, c);
+      top_r = max(top_r, r);
+      if (c != 0) low_c = max(low_c, ~c);
+      if (r != 0) low_r = max(low_r, ~r);
       if (__any_sync(0xffffffffu, not_finite(v[i][0]) || not_finite(v[i][1]))) bad |= 1u << (4 * warp + i);
     }
-    top_c = __reduce_max_sync(0xffffffffu, top_c);
-    top_r = __reduce_max_sync(0xffffffffu, top_r);
     if (lane == 0) {
       group_s[0][warp] = bad;
       group_s[1][warp] = top_c;
       group_s[2][warp] = top_r;
+      group_s[3][warp] = low_c;
+      group_s[4][warp] = low_r;
     }
     __syncthreads();
-    if (warp == 0) {  // lanes 0..7, 8..15 and 16..23 combine the three
-      unsigned m = lane < 24 ? group_s[lane >> 3][lane & 7] : 0;
+    if (warp == 0) {  // eight lanes combine each of the first four
+      unsigned m = group_s[lane >> 3][lane & 7];
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) {
         const unsigned other = __shfl_xor_sync(0xffffffffu, m, o);
@@ -263,7 +273,10 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
         p.bad[g] = m;
       }
       // a maximum of integers: the order of the atomics does not matter
-      if ((lane == 8 || lane == 16) && m != 0) atomicMax(p.amax + 2 + 2 * b + (lane >> 4), m);
+      if (lane != 0 && (lane & 7) == 0 && m != 0) atomicMax(p.amax + 3 + 4 * b + (lane >> 3), m);
+    } else if (warp == 1) {
+      const unsigned m = __reduce_max_sync(0xffffffffu, lane < 8 ? group_s[4][lane] : 0);
+      if (lane == 0 && m != 0) atomicMax(p.amax + 7 + 4 * b, m);
     }
     __syncthreads();
   }
@@ -327,16 +340,35 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
   }
 }
 
-// Exponents that bring a sequence's keys and values into fp16 (value * 2^-e):
+// Exponents that bring keys and values into fp16 (value * 2^-e), from the largest latent c and rotary key r:
 // |c . w| <= 512 max|c| max|w| < 2^(Ec + 1 + Ew + 1 + 9), to be below 2^15.
 __device__ __forceinline__ int exponent_of(unsigned bits) { return static_cast<int>(bits >> 23) - 127; }
-__device__ __forceinline__ void kv_exponents(const unsigned* amax, int b, int& ek, int& ev) {
-  const unsigned wk = __ldcg(amax), wv = __ldcg(amax + 1), c = __ldcg(amax + 2 + 2 * b), r = __ldcg(amax + 3 + 2 * b);
+__device__ __forceinline__ void exponents(const unsigned* amax, unsigned c, unsigned r, int& ek, int& ev) {
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(amax));
+  const unsigned wk = w.x, wv = w.y;
   ek = r != 0 ? exponent_of(r) + 1 - 15 : -126;
   if (c != 0 && wk != 0) ek = max(ek, exponent_of(c) + exponent_of(wk) + 11 - 15);
   ev = c != 0 && wv != 0 ? exponent_of(c) + exponent_of(wv) + 11 - 15 : 0;
   ek = min(max(ek, -126), 126);
   ev = min(max(ev, -126), 126);
+}
+// A sequence's, and whether its tokens have their own instead.
+__device__ __forceinline__ bool kv_exponents(const unsigned* amax, int b, int& ek, int& ev) {
+  const uint4 t = __ldcg(reinterpret_cast<const uint4*>(amax + 4 + 4 * b));
+  exponents(amax, t.x, t.y, ek, ev);
+  return (t.x != 0 && (t.x >> 23) - (~t.z >> 23) > kWindow) || (t.y != 0 && (t.y >> 23) - (~t.w >> 23) > kWindow);
+}
+// Those of a packed row of sequence b; a row of zeros has the sequence's.
+__device__ __forceinline__ bool row_exponents(const MlaPrefillParams& p, int b, int64_t row, int& ek, int& ev) {
+  const bool wide = kv_exponents(p.amax, b, ek, ev);
+  if (wide) {
+    const uint2 top = __ldcg(p.row_top + row);
+    int rk, rv;
+    exponents(p.amax, top.x, top.y, rk, rv);
+    if ((top.x | top.y) != 0) ek = rk;
+    if (top.x != 0) ev = rv;
+  }
+  return wide;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
 
@@ -510,14 +542,26 @@ __global__ void __launch_bounds__(kExThreads, 1)
       const int m0 = tile_of(u) * 256 + 128 * half;
       if (u % p.heads != 0 || m0 >= total) continue;  // once a tile, whichever pair has its first unit
       int ek, ev;
-      kv_exponents(p.amax, find_seq(p.kv_start, p.batch, m0), ek, ev);  // 128 rows are one sequence's
+      const int b = find_seq(p.kv_start, p.batch, m0);  // 128 rows are one sequence's
+      const bool wide = kv_exponents(p.amax, b, ek, ev);
       const float f = pow2(-ek);
       uint4* kr = reinterpret_cast<uint4*>(p.kr) + static_cast<int64_t>(m0) * (kRope / 8);
-#pragma unroll 4
-      for (int i = lane; i < 128 * kRope / 8; i += 32) {
-        const uint4 v = kr[i];
+      auto scaled = [](uint4 v, float f) {
         auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
-        kr[i] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+        return make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+      };
+      if (!wide) {
+#pragma unroll 4
+        for (int i = lane; i < 128 * kRope / 8; i += 32) kr[i] = scaled(kr[i], f);
+        continue;
+      }
+      for (int i = lane; i < 128; i += 32) {
+        int rk, rv;
+        row_exponents(p, b, m0 + i, rk, rv);
+        // factors of the row's scores (0 below 2^-126) and, in base 2, of its values; none for values that are all 0
+        p.row_scale[m0 + i] = make_float2(rk - ek < -126 ? 0.f : pow2(rk - ek),
+                                          __ldcg(p.row_top + m0 + i).x != 0 ? static_cast<float>(rv - ev) : -INFINITY);
+        for (int c = 0; c < kRope / 8; ++c) kr[i * (kRope / 8) + c] = scaled(kr[i * (kRope / 8) + c], pow2(-rk));
       }
     }
   } else if (warp >= 4) {
@@ -535,7 +579,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
       const bool out = m0 < total;
       if (first_of_tile(u) && out) {  // 128 rows are one sequence's
         int ek, ev;
-        kv_exponents(p.amax, find_seq(p.kv_start, p.batch, m0), ek, ev);
+        row_exponents(p, find_seq(p.kv_start, p.batch, m0), m0 + row, ek, ev);
         f = pow2(part == 0 ? -ek : -ev);
         bad = ((__ldcg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
       }
@@ -626,7 +670,14 @@ __global__ void __launch_bounds__(kExThreads, 1)
 //
 // The running maximum moves only when a row's scores pass it by 2^8, so O is
 // seldom rescaled; probabilities are held times 2^7, at most 2^15, which keeps
-// small ones fp16 normals. Every wait is bounded: on a timeout the CTA flags
+// small ones fp16 normals.
+//
+// A wide sequence's keys and values have an exponent a token. Scores are then scaled by column, and the weights of O are
+// 2^(score + value exponent) against a running maximum of their own (the sum keeps the scores'): a second exponential a
+// score and two passes over the tile. 8192 tokens x 16 heads, one of them 2^60 times as large: 764 us in all (239
+// without it).
+//
+// Every wait is bounded: on a timeout the CTA flags
 // the device error word and leaves after draining its copies and MMAs.
 //
 // Measured: 8192 causal tokens x 16 heads 197 us (1740 TFLOP/s), 1024 tokens behind
@@ -656,7 +707,7 @@ __device__ __forceinline__ uint32_t attn_bar_count(int i, uint32_t half) {
   return 1;
 }
 constexpr int kAtSlot = kAtBars + B_COUNT * 8, kAtAbort = kAtSlot + 4;
-constexpr int kAtUnits = (kAtAbort + 4 + 15) / 16 * 16, kAtMail = kAtUnits + 2 * 48;  // two units of 12 words, two numbers
+constexpr int kAtUnits = (kAtAbort + 4 + 15) / 16 * 16, kAtMail = kAtUnits + 2 * 64;  // two units of 13 words, two numbers
 constexpr int kAtSmem = kAtMail + 8 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
 static_assert(kAtSmem <= 227 * 1024, "prompt attention exceeds shared memory");
 
@@ -717,8 +768,8 @@ __device__ __forceinline__ float natural_lse(float m, float l) {
 
 // Words of a unit in shared memory: whether there is one, head of the pass, first query row of the sequence, its
 // queries, their first row among all, its keys (from the piece's first on), that one's packed row, key tiles of the two
-// query tiles, exponents; where a piece's rows go, -1: the unit is in one piece.
-enum : int { U_OK = 0, U_HEAD, U_ROW, U_NQ, U_Q0, U_KEYS, U_KV0, U_NT0, U_NT1, U_EK, U_EV, U_SLOT };
+// query tiles, exponents; where a piece's rows go, -1: the unit is in one piece; whether tokens have their own exponents.
+enum : int { U_OK = 0, U_HEAD, U_ROW, U_NQ, U_Q0, U_KEYS, U_KV0, U_NT0, U_NT1, U_EK, U_EV, U_SLOT, U_WIDE };
 constexpr uint64_t kUnitWaitNs = 10 * kWaitNs;  // a unit may last longer than any wait inside it
 
 template <bool kSplit>
@@ -748,7 +799,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   // Waits for unit number `it` of this pair, for a warp with a role; false at the end (or on a timeout). A role reads a
   // unit's words where it needs them (in registers they spilled) and leaves the unit when it has read the last.
-  auto unit_word = [&](int it, int w) { return reinterpret_cast<const volatile int*>(sm + kAtUnits + 48 * (it & 1))[w]; };
+  auto unit_word = [&](int it, int w) { return reinterpret_cast<const volatile int*>(sm + kAtUnits + 64 * (it & 1))[w]; };
   auto enter_unit = [&](int it) -> bool {
     return warp_wait(bar(B_UFULL + (it & 1)), (it >> 1) & 1, abort_s, err, kErrTimeoutFull, kUnitWaitNs) &&
            unit_word(it, U_OK) != 0;
@@ -798,7 +849,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           __syncwarp();
         }
-        bool ok = false;
+        bool ok = false, wide = false;
         int hp = 0, b = 0, i0 = 0, n = 0, kv0 = 0, ek = 0, ev = 0, nt[2] = {0, 0};
         int qt = 0, k0 = 0, k1 = INT_MAX, slot = -1;
         int2 qs = {0, 0};
@@ -842,7 +893,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           n = __ldcg(p.kv_len + b);
           kv0 = __ldcg(p.kv_start + b);
           i0 = (qt - __ldcg(p.qt_start + b)) * kQTile;
-          kv_exponents(p.amax, b, ek, ev);
+          wide = kv_exponents(p.amax, b, ek, ev);
           // key tiles of each query tile (the same in both CTAs): up to the last key that its last row sees
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
@@ -867,7 +918,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (!good) break;
         if (it >= 2 && !warp_wait(bar(B_UFREE + us), ((it >> 1) - 1) & 1, abort_s, err, kErrTimeoutEmpty, kUnitWaitNs)) break;
         if (lane == 0) {
-          volatile int* w = reinterpret_cast<volatile int*>(sm + kAtUnits + 48 * us);
+          volatile int* w = reinterpret_cast<volatile int*>(sm + kAtUnits + 64 * us);
           w[U_OK] = ok ? 1 : 0;
           w[U_HEAD] = hp;
           w[U_EK] = ek;
@@ -880,6 +931,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           w[U_NT0] = nt[0];
           w[U_NT1] = nt[1];
           w[U_SLOT] = slot;
+          w[U_WIDE] = wide ? 1 : 0;
           mbar_arrive(bar(B_UFULL + us));
         }
         __syncwarp();
@@ -1056,9 +1108,85 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int lim0 = p.causal ? unit_word(it, U_KEYS) - unit_word(it, U_NQ) + row0 : INT_MAX;
       const int lim = p.causal ? lim0 + lane : INT_MAX;
       const uint4* valid = reinterpret_cast<const uint4*>(p.valid) + (unit_word(it, U_KV0) >> 7);
-      float m = -INFINITY;
+      float m = -INFINITY, m_out = -INFINITY;  // O's unit, where it is not the maximum
       uint64_t l2 = 0;
-      for (int j = 0; j < nt && good; ++j) {
+      const bool wide = unit_word(it, U_WIDE) != 0;
+      if (wide) {
+        const float2* scales = p.row_scale + unit_word(it, U_KV0);
+        float l = 0.f;
+        pdl_wait();  // the expansion's row scales
+#pragma unroll 1
+        for (int j = 0; j < nt && good; ++j) {
+          const int t0 = j * kKTile;
+          const uint4 vw = __ldcg(valid + j);
+          good = warp_wait(bar(B_S + a), scored & 1, abort_s, err, kErrTimeoutFull);
+          if (!good) break;
+          ++scored;
+          tc_fence_after();
+          // columns [32 c, 32 c + 32): scores in base 2, and the exponents of their values
+          auto columns = [&](int c, auto&& each) {
+            uint32_t s[32];
+            tc_ld32(s_col + 32 * c, s);
+            tc_wait_ld();
+            const unsigned w = (c == 0 ? vw.x : c == 1 ? vw.y : c == 2 ? vw.z : vw.w) & upto(lim, t0, c);
+            const float4* fg = reinterpret_cast<const float4*>(scales + t0 + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float4 v = __ldcg(fg + k);
+              each(2 * k, ((w >> (2 * k)) & 1u) != 0 ? __uint_as_float(s[2 * k]) * v.x * sc : -INFINITY, v.y);
+              each(2 * k + 1, ((w >> (2 * k + 1)) & 1u) != 0 ? __uint_as_float(s[2 * k + 1]) * v.z * sc : -INFINITY, v.w);
+            }
+          };
+          float top = -INFINITY, top_out = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
+            columns(c, [&](int, float x, float g) {
+              top = fmaxf(top, x);
+              top_out = fmaxf(top_out, x + g);
+            });
+          if (top > m + kMoveBy) {
+            l = m == -INFINITY ? 0.f : l * ex2(m - top);
+            m = top;
+          }
+          const bool move = top_out > m_out + kMoveBy;
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = !move ? 1.f : (m_out == -INFINITY ? 0.f : ex2(m_out - top_out));
+            if (move) m_out = top_out;
+            if (j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tc_ld16(o_col + 16 * c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tc_st16(o_col + 16 * c, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : kShift - m, off_out = m_out == -INFINITY ? 0.f : kShift - m_out;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            float last = 0.f;
+            columns(c, [&](int k, float x, float g) {
+              l += ex2(x + off);
+              const float y = ex2(x + g + off_out);
+              if (k & 1) pk[k >> 1] = pack_f16(last, y);
+              last = y;
+            });
+            tc_st16(s_col + 16 * c, pk);  // over scores that have been read
+            if (c & 1) {
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8 * (c >> 1));
+            }
+          }
+        }
+        l2 = pack2(l, 0.f);
+      }
+      for (int j = 0; j < nt && good && !wide; ++j) {
         const uint4 vw = __ldcg(valid + j);
         good = warp_wait(bar(B_S + a), scored & 1, abort_s, err, kErrTimeoutFull);
         if (!good) break;
@@ -1133,13 +1261,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         unpack2(l2, l, hi);
         l += hi;
         const int slot = kSplit ? unit_word(it, U_SLOT) : -1;
-        const float scale = pow2(unit_word(it, U_EV));
+        float scale = pow2(unit_word(it, U_EV)), scale2 = 1.f;
+        if (wide) scale = scale2 = ex2(0.5f * (static_cast<float>(unit_word(it, U_EV)) + (m_out - m)));  // in two: see the range
+        else m_out = m;
         const int i = unit_word(it, U_ROW) + 256 * a + 128 * half + 32 * wq + lane, nq = unit_word(it, U_NQ);
         const int64_t q0 = unit_word(it, U_Q0);
         const int h = p.head0 + unit_word(it, U_HEAD);
         leave_unit(it);
         if (slot >= 0) {
-          // a piece: this warp's rows as 32 groups of four columns, a lane's row each, then the rows' (m, l)
+          // a piece: this warp's rows as 32 groups of four columns, a lane's row each, then the rows' (m, l, O's unit)
           int w = 8 * half + 4 * a + wq, ln = lane;
           asm volatile("" : "+r"(w), "+r"(ln));  // (else their products are formed before the loop over units, and spilled)
           float4* to = reinterpret_cast<float4*>(p.part + (static_cast<int64_t>(slot) * 16 + w) * kPartFloats) + ln;
@@ -1158,7 +1288,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               to[32 * (4 * c + k)] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
-          reinterpret_cast<float2*>(to - ln + kHeadV / 4 * 32)[ln] = make_float2(m, l);
+          to[32 * (kHeadV / 4)] = make_float4(m, l, m_out, 0.f);
         } else {
           const bool none = l == 0.f;  // the row sees no token
           const float inv = scale / l;
@@ -1179,7 +1309,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 uint32_t r[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                  r[e] = none ? 0u : pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv * scale2,
+                                               __uint_as_float(o[8 * k + 2 * e + 1]) * inv * scale2);
                 out[4 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
               }
           }
@@ -1220,25 +1351,28 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_mla_prefill_join_kernel(cons
     const int row0 = (qt - __ldcg(p.qt_start + b)) * kQTile + 256 * ((rows >> 2) & 1) + 128 * (rows >> 3) + 32 * (rows & 3);
     if (row0 >= qs.y) continue;
     auto part = [&](int k) { return p.part + (static_cast<int64_t>(cut.slot(first, pair0, k)) * 16 + rows) * kPartFloats; };
-    auto stats = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + 32 * kHeadV) + lane); };
-    float m = -INFINITY, l = 0.f, o[kJoinCols];
+    auto stats = [&](int k) { return __ldcg(reinterpret_cast<const float4*>(part(k) + 32 * kHeadV) + lane); };
+    float m = -INFINITY, m_out = -INFINITY, l = 0.f, o[kJoinCols];
 #pragma unroll 4
     for (int k = 0; k < pieces; ++k) {
-      const float2 ml = stats(k);
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);  // a sum of 0: the row sees none of the piece's keys
+      const float4 ml = stats(k);
+      if (ml.y == 0.f) continue;  // the row sees none of the piece's keys
+      m = fmaxf(m, ml.x);
+      m_out = fmaxf(m_out, ml.z);
     }
+    const float ref = m_out == -INFINITY ? 0.f : m_out;
 #pragma unroll
     for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < pieces; ++k) {
-      const float2 ml = stats(k);
+      const float4 ml = stats(k);
       float4 v[kJoinCols / 4];
 #pragma unroll
       for (int e = 0; e < kJoinCols / 4; ++e)
         v[e] = __ldcg(reinterpret_cast<const float4*>(part(k)) + 32 * (kJoinCols / 4 * c + e) + lane);
       if (ml.y == 0.f) continue;
-      const float f = ex2(ml.x - m);
-      l += f * ml.y;
+      const float f = ex2(ml.z - ref);
+      l += ex2(ml.x - m) * ml.y;
 #pragma unroll
       for (int e = 0; e < kJoinCols / 4; ++e) {
         o[4 * e] += f * v[e].x;
@@ -1248,8 +1382,10 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_mla_prefill_join_kernel(cons
       }
     }
     int ek, ev;
-    kv_exponents(p.amax, b, ek, ev);
-    const float inv = pow2(ev) / l;
+    const bool wide = kv_exponents(p.amax, b, ek, ev);
+    float scale = pow2(ev), scale2 = 1.f;
+    if (wide) scale = scale2 = ex2(0.5f * (static_cast<float>(ev) + (m_out - m)));
+    const float inv = scale / l;
     const int i = row0 + lane, h = p.head0 + hp;
     if (i >= qs.y) continue;
     const int64_t row = static_cast<int64_t>(qs.x) + i;
@@ -1258,7 +1394,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_mla_prefill_join_kernel(cons
     for (int k = 0; k < kJoinCols / 8; ++k) {
       uint32_t r[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = l == 0.f ? 0u : pack_bf16(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+      for (int e = 0; e < 4; ++e) r[e] = l == 0.f ? 0u : pack_bf16(o[8 * k + 2 * e] * inv * scale2, o[8 * k + 2 * e + 1] * inv * scale2);
       out[kJoinCols / 8 * c + k] = make_uint4(r[0], r[1], r[2], r[3]);
     }
     if (c == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(h) * p.total_q + row] = natural_lse(m, l);
@@ -1285,10 +1421,12 @@ size_t mla_prefill_workspace(MlaPrefillParams* p, char* base) {
   p->kv_start = reinterpret_cast<int*>(take((B + 1) * 4));
   p->q_start = reinterpret_cast<int*>(take(B * 8));
   p->qt_start = reinterpret_cast<int*>(take((B + 1) * 4));
-  p->amax = reinterpret_cast<unsigned*>(take((2 + 2 * B) * 4));
+  p->amax = reinterpret_cast<unsigned*>(take((4 + 4 * B) * 4));
   p->units = reinterpret_cast<int*>(take(static_cast<size_t>(p->num_heads) * 4));
   p->valid = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
   p->bad = reinterpret_cast<unsigned*>(take(cap / 32 * 4));
+  p->row_top = reinterpret_cast<uint2*>(take(cap * 8));
+  p->row_scale = reinterpret_cast<float2*>(take(cap * 8));
   p->lat = take(cap * kLat * 2);
   p->kr = take(cap * kRope * 2);
   p->kn = take(cap * kNope * 2 * hp);

@@ -450,3 +450,97 @@ def test_prompt_then_steps():
         e, _ = pkg.mla_prefill(turned[i:i + 1], w.cuda(), cache, table.cuda(), one([i + 1]), one([0, 1]))
         assert np.abs(sv.f64(e)[0] - sv.f64(o)[0, 0]).max() <= 2e-2  # the two forms agree
     assert _lib.gqa_paged_decode_device_error() == 0
+
+
+# -------------------------------------------------- tokens of very different size
+def one_huge(n, nq, h, at, factor, seed):
+    """A sequence with one token `factor` times as large, one of zeros, and the same without the huge one (its page,
+    of a single token, is outside the pool there)."""
+    c = case([(nq, n)], h, 1, seed)
+    block = int(c["block_table"][0, at])
+    c["kv_cache"][block] = (c["kv_cache"][block].double() * factor).to(BF)
+    c["kv_cache"][int(c["block_table"][0, n // 3])] = 0
+    without = dict(c, block_table=c["block_table"].clone())
+    without["block_table"][0, at] = -1
+    return c, without
+
+
+def check_huge(out, lse, c, without, at, causal):
+    """Rows that do not see the token or give it no weight are the definition's without it; rows that give it all of
+    theirs are its value: half a step of bf16 (2^-8), one of fp16 each for value and weight (2^-10 together), and the
+    accumulation of the value (512 steps of 2^-23 of its products, 2^-14)."""
+    nq, n = c["q"].shape[0], int(c["cache_seqlens"][0])
+    o, l, ob, lb = sv.mla_prefill_oracle(without["q"], without["w_kv"], without["kv_cache"], without["block_table"],
+                                         without["cache_seqlens"], without["cu_seqlens_q"], 192 ** -0.5, causal)
+    row = sv.f64(c["kv_cache"][int(c["block_table"][0, at]), 0, 0])
+    full, mag = sv.f64(c["w_kv"]) @ row[:512], np.abs(sv.f64(c["w_kv"])) @ np.abs(row[:512])
+    key = np.concatenate([full[:, :128], np.broadcast_to(row[512:], (full.shape[0], 64))], 1)
+    score = 192 ** -0.5 * np.einsum("nhd,hd->nh", sv.f64(c["q"]), key)
+    sees = np.ones(nq, bool) if not causal else np.arange(nq) >= at - (n - nq)
+    takes = sees[:, None] & (score > 0)
+    assert np.all(np.abs(score) > 1e4)  # nothing between all and no weight (the others' scores are a few units)
+    got, gl = sv.f64(out), sv.f64(lse).T
+    err = np.abs(got - o) - ob
+    assert np.all(err[~takes] <= 0), f"out {err[~takes].max()} over its bound"
+    err = np.abs(gl - l.T) - lb.T
+    assert np.all(err[~takes] <= 0), f"lse {err[~takes].max()} over its bound"
+    v = np.broadcast_to(full[:, 128:], got.shape)
+    tol = (2.0 ** -8 + 2.0 ** -10) * np.abs(v) + 2.0 ** -13 * mag[:, 128:]
+    assert np.all((np.abs(got - v) <= tol)[takes]) and takes.any() == sees.any()
+    assert np.all(np.abs(gl - score)[takes] <= 2.0 ** -10 * 192 ** -0.5 * np.einsum(
+        "nhd,hd->nh", np.abs(sv.f64(c["q"])), np.concatenate([mag[:, :128], np.abs(key[:, 128:])], 1))[takes])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,nq,h,at,factor", [
+    (200, 200, 2, 150, 2.0 ** 60), (300, 300, 3, 299, 2.0 ** 100), (700, 530, 1, 640, 2.0 ** 40), (130, 1, 2, 5, 2.0 ** 60),
+    (600, 600, 2, 0, 2.0 ** 60), (6000, 200, 2, 5900, 2.0 ** 60), (6000, 200, 2, 100, 2.0 ** 80)])
+def test_prefill_one_huge_token(n, nq, h, at, factor, causal):
+    """A finite token far larger than the others, late, early, and where units are split over their keys."""
+    c, without = one_huge(n, nq, h, at, factor, n + h)
+    out, lse = pkg.mla_prefill(**on_gpu(c), causal=causal)
+    check_huge(out, lse, c, without, at, causal)
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+def test_prefill_small_tokens_before_ordinary_ones():
+    """Rows that see only tokens 2^-60 times the later ones' size keep full precision: their scores are 0, so a row is
+    the mean of the values it sees. Bounds as in check_huge, and n steps of 2^-23 for the sum."""
+    c = case([(200, 200)], 2, 1, 41)
+    small = c["block_table"][0, :40].long()
+    c["kv_cache"][small] = (c["kv_cache"][small].double() * 2.0 ** -60).to(BF)
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    rows, w = sv.f64(c["kv_cache"][small])[:, 0, 0, :512], sv.f64(c["w_kv"])[:, 128:]
+    v, mag = np.einsum("tl,hdl->thd", rows, w), np.einsum("tl,hdl->thd", np.abs(rows), np.abs(w))
+    count = np.arange(1, 41)[:, None, None]
+    want, size, mags = (np.cumsum(x, 0) / count for x in (v, np.abs(v), mag))
+    tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size + 2.0 ** -13 * mags
+    assert np.all(np.abs(sv.f64(out)[:40] - want) <= tol)
+    check(out[40:], lse[:, 40:], dict(c, q=c["q"][40:], cu_seqlens_q=torch.tensor([0, 160], dtype=torch.int32)),
+          192 ** -0.5, True)
+
+
+def test_prefill_one_huge_token_in_several_passes_and_beside_others():
+    """Passes over the heads read the same row exponents; sequences without such a token keep their bits."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    c = case([(50, 90), (300, 300), (33, 700)], 5, 1, 42)
+    plain, _ = pkg.mla_prefill(**on_gpu(c))
+    block = int(c["block_table"][1, 250])
+    c["kv_cache"][block] = (c["kv_cache"][block].double() * 2.0 ** 70).to(BF)
+    want, wl = pkg.mla_prefill(**on_gpu(c))
+    out, lse = pkg.mla_prefill(**on_gpu(c), max_kv_tokens=2_000_000)  # two heads a pass
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    assert torch.equal(out[:50], plain[:50]) and torch.equal(out[350:], plain[350:])
+
+
+def test_prefill_not_finite_and_huge_tokens_together():
+    """Rows before either are as without both; rows that see the one that is not finite are NaN."""
+    c = case([(200, 200)], 2, 1, 43)
+    want, _ = pkg.mla_prefill(**on_gpu(c))
+    for t, x in ((120, 2.0 ** 60), (160, float("inf"))):
+        c["kv_cache"][int(c["block_table"][0, t])] *= x
+    out, lse = pkg.mla_prefill(**on_gpu(c))
+    oracle = sv.mla_prefill_oracle(c["q"][:120], c["w_kv"], c["kv_cache"], c["block_table"], [120], [0, 120], 192 ** -0.5)
+    assert np.all(np.abs(sv.f64(out)[:120] - oracle[0]) <= oracle[2])
+    assert out[:160].isfinite().all() and out[160:].isnan().all() and lse[:, 160:].isnan().all()
