@@ -406,7 +406,7 @@ int gqa_paged_decode_noalloc(const void* q, const void* k_cache, const void* v_c
  *   y1 = scale * (x1 cos a - x2 sin a),  y2 = scale * (x2 cos a + x1 sin a),
  * (x1, x2) being elements (i, i + rot_dim / 2) of the window (GQA_ROPE_HALF)
  * or (2 i, 2 i + 1) (GQA_ROPE_INTERLEAVED). The angle is formed in 64-bit
- * integer arithmetic, so it does not lose precision at far positions; the
+ * integer arithmetic and is within 2^-23 radians at every 32-bit position; the
  * rotation is in fp32 and rounded once. positions: [num_tokens] int32;
  * inv_freq: [rot_dim / 2] finite doubles, both in device memory.
  *

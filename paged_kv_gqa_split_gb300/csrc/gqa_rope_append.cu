@@ -277,6 +277,7 @@ template <int LAYOUT>
 __global__ void __launch_bounds__(256) gqa_mla_append_kernel(const MlaAppendParams p) {
   const int lane = threadIdx.x & 31;
   const int stride = gridDim.x * (blockDim.x >> 5);
+  const unsigned long long turn = p.inv_freq != nullptr ? rope_turn(__ldg(p.inv_freq + lane)) : 0;  // of the lane's pair
   for (int n = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); n < p.num_tokens; n += stride) {
     const int slot = __ldg(p.slots + n);
     if (slot < 0 || slot >= p.num_slots) continue;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(256) gqa_mla_append_kernel(const MlaAppendPara
     const int e1 = LAYOUT == kRopeInterleaved ? 2 * lane : lane, e2 = LAYOUT == kRopeInterleaved ? e1 + 1 : lane + 32;
     float x1 = __bfloat162float(rope[e1]), x2 = __bfloat162float(rope[e2]);
     if (p.inv_freq != nullptr) {
-      const float2 c = rope_cos_sin(__ldg(p.positions + n), rope_turn(__ldg(p.inv_freq + lane)), p.scale);
+      const float2 c = rope_cos_sin(__ldg(p.positions + n), turn, p.scale);
       const float y1 = x1 * c.x - x2 * c.y;
       x2 = x2 * c.x + x1 * c.y;
       x1 = y1;

@@ -4,6 +4,8 @@ Bound: the angle's fraction of a turn is cut to 2^-33 and its float to 2^-25 of 
 is within 2 ulp, and scale, product and sum round once each: below 2^-21 of scale * (|x1| + |x2|) together. The store adds
 half a step of the type.
 """
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -147,3 +149,32 @@ def test_rope_refusals():
                 lambda: pkg.rope(x, pos, freq, out=x[:, :1].expand(4, 2, 64))):
         with pytest.raises(pkg.GqaError):
             bad()
+
+
+def turns(p, f):
+    """The fraction of a turn of the angle p * f (f a double), in [-1/2, 1/2], from rational arithmetic."""
+    def atan_inverse(x, one):
+        total, term, n = 0, one // x, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term, n = term // (x * x), n + 2
+        return total
+    one = 1 << 400
+    pi = Fraction(4 * (4 * atan_inverse(5, one) - atan_inverse(239, one)), one)
+    t = Fraction(p) * Fraction(f) / (2 * pi)
+    return float(t - round(t))
+
+
+def test_angles_of_far_positions():
+    """(1, 0) turned gives (cos, sin) of the angle itself: off by 2^-25 of a half turn (the float), 2^-32 of a turn (the
+    fixed-point fraction) and sincospif's 2 ulp of 2^-24, together below 2^-22. The angle is rational arithmetic's: a
+    double's product loses as much as this bound."""
+    freq = [1.0, 0.9, 3.7, 6.1, 500000.0 ** (-4 / 256), 1 / 3, 1e-4, 100.25, -0.7, 2.0 ** 70 / 3, 1e-12, 2.0 ** 116]
+    r = len(freq)
+    pos = [2 ** 31 - 1, -2 ** 31 + 1, 10 ** 9 + 7, -123456789, 1, 0]
+    x = torch.zeros(len(pos), 1, 2 * r, device="cuda")
+    x[..., :r] = 1.0
+    got = sv.f64(pkg.rope(x, torch.tensor(pos, dtype=torch.int32).cuda(), torch.tensor(freq, dtype=torch.float64).cuda()))
+    angle = 2 * np.pi * np.array([[turns(p, f) for f in freq] for p in pos])
+    assert np.abs(got[:, 0, :r] - np.cos(angle)).max() <= 2.0 ** -22
+    assert np.abs(got[:, 0, r:] - np.sin(angle)).max() <= 2.0 ** -22
