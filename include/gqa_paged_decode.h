@@ -536,8 +536,9 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
  * sequence's query count. A row that sees no token gives out = 0 and lse =
  * -inf. A token whose block lies outside [0, num_blocks) is left out; lengths
  * are clamped as in gqa_mla_decode. A token whose latent row is not all finite
- * makes the rows that see it NaN, and no others. Rows past cu_seqlens_q[batch] are left as
- * they were. The expanded keys and values are fp16, scaled by powers of two, one
+ * makes the rows that see it NaN, and no others. Rows of no sequence (before cu_seqlens_q[0],
+ * from cu_seqlens_q[batch] on) are left as they were; gqa_mla_prefill_fill with GQA_FILL_OUT
+ * makes them 0 in out, with GQA_FILL_LSE -inf in lse. The expanded keys and values are fp16, scaled by powers of two, one
  * per sequence or, where its tokens differ by more than 2^8, one per token: a
  * token's values below about 2^-29 of 512 * max|its latent| * max|w_kv| lose bits
  * (2^-21 where the sequence has one), and no token's size costs another's.
@@ -560,6 +561,13 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
                     void* out, float* lse, int batch, int total_q, int num_heads, int page_size, int num_blocks,
                     int page_table_width, int64_t max_kv_tokens, int64_t q_token_stride, int64_t q_head_stride,
                     void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+#define GQA_FILL_OUT 1
+#define GQA_FILL_LSE 2
+int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, const int32_t* block_table,
+                         const int32_t* cache_seqlens, const int32_t* cu_seqlens_q, float softmax_scale, int causal,
+                         int fill, void* out, float* lse, int batch, int total_q, int num_heads, int page_size,
+                         int num_blocks, int page_table_width, int64_t max_kv_tokens, int64_t q_token_stride,
+                         int64_t q_head_stride, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

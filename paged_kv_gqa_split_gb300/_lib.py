@@ -68,6 +68,8 @@ _SIGNATURES = {
     "gqa_mla_prefill_ws_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64]),
     "gqa_mla_prefill": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float, ctypes.c_int, _vp, _vp] + [ctypes.c_int] * 6 +
                         [ctypes.c_int64] * 3 + [_vp, ctypes.c_size_t, _vp]),
+    "gqa_mla_prefill_fill": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float] + [ctypes.c_int] * 2 + [_vp, _vp] +
+                             [ctypes.c_int] * 6 + [ctypes.c_int64] * 3 + [_vp, ctypes.c_size_t, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None

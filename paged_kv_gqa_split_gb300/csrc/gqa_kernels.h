@@ -282,6 +282,7 @@ struct MlaPrefillParams {
   int64_t q_token_stride, q_head_stride;
   float scale_log2;
   int batch, total_q, num_heads, page_size, num_blocks, width, causal;
+  int fill;       // rows of no sequence: 1: out becomes 0, 2: lse becomes -inf, 0: they stay
   int cap;        // packed key rows the workspace holds, a multiple of 128
   int q_tiles;    // query tiles that total_q rows of batch sequences make at most
   int heads_per_pass;

@@ -195,6 +195,23 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
   return not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
 }
 
+// Query rows of no sequence, before the first one's and behind the last one's: out 0 and lse -inf, as asked. Runs ahead
+// of the attention, which overwrites what malformed offsets make overlap.
+__device__ __forceinline__ void fill_rows(const MlaPrefillParams& p) {
+  const int q0 = min(max(__ldg(p.cu_q), 0), p.total_q), q1 = min(max(__ldg(p.cu_q + p.batch), 0), p.total_q);
+  const int64_t rows = static_cast<int64_t>(q0) + (p.total_q - q1), step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int per_row = p.num_heads * (kHeadV / 8);
+  for (int64_t i = t0; i < rows * per_row && (p.fill & 1) != 0; i += step) {
+    const int64_t r = i / per_row, row = r < q0 ? r : q1 + (r - q0);
+    reinterpret_cast<uint4*>(p.out)[row * per_row + (i - r * per_row)] = make_uint4(0, 0, 0, 0);
+  }
+  for (int64_t i = t0; i < rows * p.num_heads && (p.fill & 2) != 0; i += step) {
+    const int64_t h = i / rows, r = i - h * rows;
+    p.lse[h * p.total_q + (r < q0 ? r : q1 + (r - q0))] = -INFINITY;
+  }
+}
+
 // ----------------------------------------------------------------- gather
 // A block per 32 packed rows, four rows a warp with all their loads in flight; before that, and before the
 // plan's results are needed, a warp per weight row for the maxima.
@@ -204,6 +221,7 @@ __global__ void __launch_bounds__(256) gqa_mla_prefill_gather_kernel(const MlaPr
   // of each warp: rows not finite; largest latent and rotary key of its rows; the smallest row's, inverted
   __shared__ unsigned group_s[5][8];
   pdl_launch_dependents();
+  if (p.fill != 0) fill_rows(p);
   if (blockIdx.x == gridDim.x - 1)
     for (int i = threadIdx.x; i < p.num_heads; i += 256) p.units[i] = 0;
   const int wrows = p.num_heads * (kNope + kHeadV);

@@ -284,6 +284,16 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
                     float* lse, int batch, int total_q, int num_heads, int page_size, int num_blocks, int page_table_width,
                     int64_t max_kv_tokens, int64_t q_token_stride, int64_t q_head_stride, void* workspace,
                     size_t workspace_bytes, struct CUstream_st* stream) {
+  return gqa_mla_prefill_fill(q, w_kv, kv_cache, block_table, cache_seqlens, cu_seqlens_q, softmax_scale, causal, 0, out,
+                              lse, batch, total_q, num_heads, page_size, num_blocks, page_table_width, max_kv_tokens,
+                              q_token_stride, q_head_stride, workspace, workspace_bytes, stream);
+}
+
+int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, const int32_t* block_table,
+                         const int32_t* cache_seqlens, const int32_t* cu_seqlens_q, float softmax_scale, int causal,
+                         int fill, void* out, float* lse, int batch, int total_q, int num_heads, int page_size,
+                         int num_blocks, int page_table_width, int64_t max_kv_tokens, int64_t q_token_stride,
+                         int64_t q_head_stride, void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
   if (batch < 0 || total_q < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (batch == 0 || total_q == 0) return GQA_OK;
   if (!prefill_sizes_ok(batch, num_heads, max_kv_tokens) || total_q > (1 << 26)) return GQA_ERR_INVALID_ARGUMENT;
@@ -292,6 +302,8 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
     return GQA_ERR_INVALID_ARGUMENT;
   if (q == nullptr || w_kv == nullptr || kv_cache == nullptr || block_table == nullptr || cache_seqlens == nullptr ||
       cu_seqlens_q == nullptr || out == nullptr)
+    return GQA_ERR_INVALID_ARGUMENT;
+  if (fill < 0 || fill > (GQA_FILL_OUT | GQA_FILL_LSE) || ((fill & GQA_FILL_LSE) != 0 && lse == nullptr))
     return GQA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(softmax_scale * kLog2e)) return GQA_ERR_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(w_kv, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
@@ -317,6 +329,7 @@ int gqa_mla_prefill(const void* q, const void* w_kv, const void* kv_cache, const
   p.num_blocks = num_blocks;
   p.width = page_table_width;
   p.causal = causal != 0;
+  p.fill = fill;
   p.cap = static_cast<int>(prefill_rows(batch, max_kv_tokens));
   if (workspace == nullptr || !aligned(workspace, 256) ||
       workspace_bytes < gqa::mla_prefill_workspace(&p, static_cast<char*>(workspace)))

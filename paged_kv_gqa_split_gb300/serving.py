@@ -27,6 +27,7 @@ except ImportError:
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 CACHE_BF16, CACHE_FP8 = 0, 1
+FILL_OUT, FILL_LSE = 1, 2
 MLA_NOPE, MLA_ROPE, MLA_HEAD_V = 128, 64, 128
 MLA_D_HEAD = MLA_NOPE + MLA_ROPE  # query and expanded key values a head
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -382,7 +383,8 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
     """Latent attention for prompts and prompt chunks, expanded form: packed queries q [total, heads, 192] (sequence
     b's rows from cu_seqlens_q[b] on, rotary part turned) over the cached tokens that block_table [B, width] and
     cache_seqlens [B] list, the new ones among them. max_kv_tokens: a bound on the sum of cache_seqlens, which sizes
-    the workspace (default: what the block table can list). Returns (out [total, heads, 128] bf16, lse [heads, total]
+    the workspace (default: what the block table can list). Rows of no sequence are 0 (lse -inf) in outputs that the call
+    allocates, and left as they were in given ones. Returns (out [total, heads, 128] bf16, lse [heads, total]
     fp32 natural log, or None)."""
     index = _index("q", q)
     n, h, ts, hs = _query(q)
@@ -401,7 +403,9 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         max_kv_tokens = b * width * page
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(MLA_D_HEAD)
+    fill = 0  # outputs of the call's own have no rows left as they were
     if out is None:
+        fill |= FILL_OUT
         out = _new(index, (n, h, MLA_HEAD_V), torch.bfloat16, stream)
     elif out.shape != (n, h, MLA_HEAD_V):
         raise ValueError(f"out must be {(n, h, MLA_HEAD_V)}")
@@ -410,8 +414,14 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         if lse.shape != (h, n):
             raise ValueError(f"lse must be {(h, n)}")
     elif with_lse:
+        fill |= FILL_LSE
         lse = _new(index, (h, n), torch.float32, stream)
     if b == 0 or n == 0:
+        with torch.cuda.stream(stream):
+            if fill & FILL_OUT:
+                out.zero_()
+            if fill & FILL_LSE:
+                lse.fill_(-math.inf)
         return out, lse
     if workspace is None:
         size = load().gqa_mla_prefill_ws_size(b, h, max_kv_tokens)
@@ -420,8 +430,8 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
         workspace = _new(index, (size,), torch.uint8, stream)
     else:
         _check(index, None, True, workspace=workspace)
-    _call("gqa_mla_prefill", index, stream, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
-          cache_seqlens.data_ptr(), cu_seqlens_q.data_ptr(), softmax_scale, 1 if causal else 0, out.data_ptr(),
+    _call("gqa_mla_prefill_fill", index, stream, q.data_ptr(), w, kv_cache.data_ptr(), block_table.data_ptr(),
+          cache_seqlens.data_ptr(), cu_seqlens_q.data_ptr(), softmax_scale, 1 if causal else 0, fill, out.data_ptr(),
           lse.data_ptr() if lse is not None else None, b, n, h, page, blocks, width, max_kv_tokens, ts, hs,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse

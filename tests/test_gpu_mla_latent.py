@@ -544,3 +544,46 @@ def test_prefill_not_finite_and_huge_tokens_together():
     oracle = sv.mla_prefill_oracle(c["q"][:120], c["w_kv"], c["kv_cache"], c["block_table"], [120], [0, 120], 192 ** -0.5)
     assert np.all(np.abs(sv.f64(out)[:120] - oracle[0]) <= oracle[2])
     assert out[:160].isfinite().all() and out[160:].isnan().all() and lse[:, 160:].isnan().all()
+
+
+# ------------------------------------------------------------ rows of no sequence
+def poisoned(*shapes):
+    """Leaves NaN in the memory that tensors of these shapes are likely to get next."""
+    held = [torch.full(s, float("nan"), dtype=t, device="cuda") for s, t in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("before,behind", [(0, 25), (7, 0), (5, 130)])
+def test_prefill_own_outputs_have_no_rows_left_over(before, behind):
+    c = case([(30, 30), (0, 0), (10, 90)], 2, 16, 9)
+    g = on_gpu(c)
+    pad = lambda n: torch.full((n, 2, 192), float("nan"), dtype=BF, device="cuda")  # noqa: E731
+    g["q"] = torch.cat([pad(before), g["q"], pad(behind)])
+    g["cu_seqlens_q"] += before
+    n, rows = before + 40 + behind, slice(before, before + 40)
+    poisoned(((n, 2, 128), BF), ((2, n), torch.float32))
+    out, lse = pkg.mla_prefill(**g)
+    check(out[rows], lse[:, rows], c, 192 ** -0.5, True)
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[rows] = False
+    assert (out[rest] == 0).all() and torch.isneginf(lse[:, rest]).all()
+    kept = torch.full_like(out, 5.0)  # a given output keeps its rows, the call's own lse does not
+    _, lse = pkg.mla_prefill(**g, out=kept)
+    assert (kept[rest] == 5).all() and torch.equal(kept[rows], out[rows]) and torch.isneginf(lse[:, rest]).all()
+    kept = torch.full_like(lse, 5.0)
+    out2, _ = pkg.mla_prefill(**g, lse=kept)
+    assert (kept[:, rest] == 5).all() and torch.equal(out2, out)
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+def test_prefill_own_outputs_of_no_sequences():
+    g = on_gpu(case([(5, 9)], 2, 16, 20))
+    g |= dict(block_table=g["block_table"][:0], cache_seqlens=g["cache_seqlens"][:0], cu_seqlens_q=g["cu_seqlens_q"][:1])
+    for stream in (None, torch.cuda.Stream()):
+        poisoned(((5, 2, 128), BF), ((2, 5), torch.float32))
+        out, lse = pkg.mla_prefill(**g, stream=stream)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and torch.isneginf(lse).all()
+    out = torch.full((5, 2, 128), 5.0, dtype=BF, device="cuda")
+    assert (pkg.mla_prefill(**g, out=out, with_lse=False)[0] == 5).all()

@@ -127,6 +127,14 @@ def test_prefill_refusals(lib):
     assert lib.gqa_mla_prefill_ws_size(1, 128, 1 << 20) < (8 << 30)
 
 
+def test_prefill_fill_refusals(lib):
+    ok = dict(q=A, w=A, kv=A, table=A, lens=A, cu=A, scale=0.1, causal=1, fill=3, out=A, lse=A, batch=2, total=7, heads=3,
+              page=16, blocks=9, width=4, max_kv=100, qt=576, qh=192, ws=A, ws_bytes=1 << 40, stream=None)
+    assert lib.gqa_mla_prefill_fill(*dict(ok, batch=0).values()) == 0
+    _refused(lib.gqa_mla_prefill_fill, ok, [dict(fill=-1), dict(fill=4), dict(fill=2, lse=None), dict(q=None), dict(width=0)])
+    assert lib.gqa_mla_prefill_fill(*dict(ok, ws=None).values()) == _lib.GQA_ERR_WORKSPACE
+
+
 def test_cpu_tensors_raise(lib):
     bf = torch.bfloat16
     i = torch.zeros(2, dtype=torch.int32)
