@@ -43,11 +43,15 @@ def _ready(index, t, dtype):
     return isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.is_contiguous()
 
 
+_OPTIONAL = {"q", "q_out", "out", "lse", "k_out", "v_out"}  # arguments that may be None where _check sees them
+_INT_MAX = 2 ** 31 - 1
+
+
 def _check(index, dtype, contiguous, **tensors):
-    """Raises for the first tensor (None is skipped) that is not on GPU `index` (a CPU tensor's is -1), of `dtype`
-    (None: any) and, if asked, contiguous."""
+    """Raises for the first tensor (None only where it is optional) that is not on GPU `index` (a CPU tensor's is -1),
+    of `dtype` (None: any) and, if asked, contiguous."""
     for name, t in tensors.items():
-        if t is None:
+        if t is None and name in _OPTIONAL:
             continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -92,10 +96,12 @@ def _layout(layout):
     return code
 
 
-def _rotation(index, n, positions, inv_freq, pairs=None):
+def _rotation(index, n, positions, inv_freq, pairs=None, rot_offset=0):
     """(positions pointer, inv_freq pointer, pairs); inv_freq None: no rotation."""
     if inv_freq is None:
         return None, None, 0
+    if not 0 <= rot_offset <= _INT_MAX:  # a C int would drop the upper bits
+        raise ValueError("rot_offset must not be negative or past the head")
     if positions is None:
         raise ValueError("a rotation needs positions")
     if not _ready(index, positions, torch.int32) or not _ready(index, inv_freq, torch.float64):
@@ -167,7 +173,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, scale
     n, heads, dim = x.shape
     if inv_freq is None:
         raise ValueError("rope needs inv_freq")
-    pos, freq, pairs = _rotation(index, n, positions, inv_freq)
+    pos, freq, pairs = _rotation(index, n, positions, inv_freq, rot_offset=rot_offset)
     if out is None:
         out = _new(index, (n, heads, dim), x.dtype, stream)
     else:
@@ -226,7 +232,7 @@ def rope_kv_append(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.
         raise ValueError("q_out needs q")
     if k_new.shape[0] != n or v_new.shape[0] != n or (q is not None and (q.shape[0] != n or q_out.shape != q.shape)):
         raise ValueError("q, k_new, v_new and q_out must have one row per slot")
-    pos, freq, pairs = _rotation(index, n, positions, inv_freq)
+    pos, freq, pairs = _rotation(index, n, positions, inv_freq, rot_offset=rot_offset)
     _call("gqa_rope_kv_append", index, stream, q_ptr, k_new.data_ptr(), v_new.data_ptr(), pos, slots.data_ptr(),
           freq, scale, rot_offset, 2 * pairs, _layout(layout), out_ptr, k_cache.data_ptr(), v_cache.data_ptr(), fmt, n,
           pages, qs, ks, vs)
@@ -237,6 +243,7 @@ def kv_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
                   v_cache: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Quantise each new token's K/V rows [N, 4, 128] into page slots[r] of FP8 caches [P, 528] (in place); slots
     outside [0, P) are skipped."""
+    _check(_index("k_cache", k_cache), None, False, v_cache=v_cache)
     if _cache_format(k_cache, v_cache)[0] != CACHE_FP8:
         raise ValueError("kv_append_fp8 needs FP8 caches; kv_append stores bfloat16 ones")
     rope_kv_append(None, k_new, v_new, slots, k_cache, v_cache, stream=stream)
@@ -401,6 +408,8 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
     b, width = block_table.shape
     if max_kv_tokens is None:
         max_kv_tokens = b * width * page
+    if not 0 <= max_kv_tokens <= _INT_MAX:
+        raise ValueError(f"max_kv_tokens {max_kv_tokens} is out of range")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(MLA_D_HEAD)
     fill = 0  # outputs of the call's own have no rows left as they were

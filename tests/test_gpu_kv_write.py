@@ -277,3 +277,36 @@ def test_latent_append(layout, n, rotate):
     others = torch.ones(blocks * page, dtype=torch.bool)
     others[at] = False
     assert torch.all(flat[others] == 2.0)
+
+
+def test_missing_tensors_and_offsets_past_an_int_are_refused():
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    k, q = torch.zeros(3, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 32, 128, dtype=torch.bfloat16, device="cuda")
+    c, bc = torch.zeros(8, 528, dtype=torch.uint8, device="cuda"), torch.zeros(8, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    lat, row = torch.zeros(4, 16, 1, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 576, dtype=torch.bfloat16, device="cuda")
+    w, freq = torch.zeros(2, 256, 512, dtype=torch.bfloat16, device="cuda"), pkg.rope_inv_freq(64)[0]
+    ql, cu = torch.zeros(3, 2, 192, dtype=torch.bfloat16, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    calls = [(pkg.rope, dict(x=q, positions=i, inv_freq=freq), ["x"]),
+             (pkg.rope_kv_append, dict(q=q, k_new=k, v_new=k, slots=i, k_cache=bc, v_cache=bc),
+              ["k_new", "v_new", "slots", "k_cache", "v_cache"]),
+             (pkg.kv_append_fp8, dict(k_new=k, v_new=k, slots=i, k_cache=c, v_cache=c),
+              ["k_new", "v_new", "slots", "k_cache", "v_cache"]),
+             (pkg.kv_read_fp8, dict(k_cache=c, v_cache=c, indices=i), ["k_cache", "v_cache", "indices"]),
+             (pkg.mla_kv_append, dict(latent=row[:, :512], k_rope=row[:, 512:], slots=i, kv_cache=lat),
+              ["latent", "k_rope", "slots", "kv_cache"]),
+             (pkg.mla_absorb_q, dict(q=ql, w_kv=w), ["q", "w_kv"]),
+             (pkg.mla_expand_out, dict(o_latent=ql.new_zeros(3, 2, 512), w_kv=w), ["o_latent", "w_kv"]),
+             (pkg.mla_prefill, dict(q=ql, w_kv=w, kv_cache=lat, block_table=i[None], cache_seqlens=i[:1], cu_seqlens_q=cu),
+              ["q", "w_kv", "kv_cache", "block_table", "cache_seqlens", "cu_seqlens_q"])]
+    for fn, args, required in calls:
+        fn(**args)
+        for name in required:
+            with pytest.raises(TypeError, match=name):
+                fn(**dict(args, **{name: None}))
+    for offset in (-1, 2 ** 31, 2 ** 32):
+        with pytest.raises(ValueError):
+            pkg.rope(q, i, freq, rot_offset=offset)
+        with pytest.raises(ValueError):
+            pkg.rope_kv_append(q, k, k, i, bc, bc, i, freq, rot_offset=offset)
+    with pytest.raises(ValueError):
+        pkg.mla_prefill(ql, w, lat, i[None], i[:1], cu, max_kv_tokens=1 << 64)
