@@ -349,12 +349,13 @@ int gqa_paged_decode_device_error(int* flags);
  *
  * gqa_paged_decode_test_wait_limit_ns(ns): the give-up limit, in
  * nanoseconds, of the bounded waits of the decode kernels: the mbarrier waits
- * of the TMA-gather variant (gather = 1 in gqa_paged_decode_set_tuning) and,
- * in the one-wave mode, a warp's wait for the pieces of a sequence it merges.
+ * of the TMA-gather variant (gather = 1 in gqa_paged_decode_set_tuning), those
+ * of the latent projections above 16 tokens and, in the one-wave mode, a
+ * warp's wait for the pieces of a sequence it merges.
  * 0 restores the default of 2 s. A wait that runs out sets bit 1, 2 or 32 of
- * the device error word; a TMA-variant CTA returns after its copies in flight
- * have landed (that drain keeps the 2 s limit), a merging warp skips that
- * merge. A call made with a tiny limit therefore completes, with outputs that
+ * the device error word; a TMA-variant or projection CTA returns after its
+ * copies and MMAs in flight have ended (that drain keeps the 2 s limit), a
+ * merging warp skips that merge. A call made with a tiny limit therefore completes, with outputs that
  * are not valid.
  */
 int gqa_paged_decode_test_fail_allocs(int count);

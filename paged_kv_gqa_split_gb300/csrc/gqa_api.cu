@@ -378,12 +378,13 @@ int decode_in_scratch(const void* q, const void* k_cache, const void* v_cache, c
              false, 0, nullptr, true);
 }
 
-int current_device_sms(int* sm_count) {
+int current_device_sms(int* sm_count, unsigned long long* wait_limit_ns) {
   std::lock_guard<std::mutex> lock(g_mu);
   int dev = 0;
   DeviceState* st = nullptr;
   const int rc = current_device(&dev, &st);
   if (rc == GQA_OK) *sm_count = st->sm_count;
+  if (wait_limit_ns != nullptr) *wait_limit_ns = g_wait_limit_ns > 0 ? g_wait_limit_ns : kDefaultWaitLimitNs;
   return rc;
 }
 

@@ -265,6 +265,7 @@ struct MlaProjParams {  // gqa_mla_proj.cu
   float scale;
   int num_tokens, num_heads, out_width, layout;
   int* err;
+  unsigned long long wait_limit_ns;  // give-up limit of the tensor-memory kernel's waits
 };
 cudaError_t launch_mla_absorb_q(const MlaProjParams& p, cudaStream_t stream);
 cudaError_t launch_mla_expand_out(const MlaProjParams& p, cudaStream_t stream);
@@ -323,7 +324,8 @@ cudaError_t launch_mla_prefill(MlaPrefillParams p, int sm_count, cudaStream_t st
 
 cudaError_t read_and_clear_device_error(int* out);
 cudaError_t device_error_word(int** ptr);  // device address of the error word (current device)
-int current_device_sms(int* sm_count);      // GQA_OK and the SM count when the current device is supported
+// GQA_OK, the SM count and the give-up limit of bounded waits when the current device is supported
+int current_device_sms(int* sm_count, unsigned long long* wait_limit_ns = nullptr);
 
 // Raises a kernel's dynamic shared-memory limit to `bytes` once per device
 // (`done` is the kernel's own flag table, zero-initialised static storage).

@@ -236,7 +236,7 @@ struct ProjMaps {
   CUtensorMap x, w, out;  // boxes of 64 values x 1 head x 128 tokens; of 64 x 128 (64) weight rows
 };
 
-constexpr uint64_t kProjWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = kDefaultWaitLimitNs;
 
 template <bool ABSORB>
 __global__ void __launch_bounds__(128) gqa_mla_proj_tc_kernel(const MlaProjParams p, const __grid_constant__ ProjMaps maps) {
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(128) gqa_mla_proj_tc_kernel(const MlaProjParam
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + T::kSlot);
   auto wait = [&](uint32_t bar, uint32_t parity, int bit) {
-    return __all_sync(0xffffffffu, tc_wait(bar, parity, &abort_s, p.err, bit, kProjWaitNs));
+    return __all_sync(0xffffffffu, tc_wait_limited(bar, parity, &abort_s, p.err, bit, p.wait_limit_ns));
   };
 
   int c = 0;
@@ -301,13 +301,7 @@ __global__ void __launch_bounds__(128) gqa_mla_proj_tc_kernel(const MlaProjParam
     __syncwarp();
   }
   // every warp takes its 32 rows of the result
-  const bool good = wait(done, 0, kErrTimeoutFull);
-  if (abort_s && warp == 1 && lane == 0) {  // no copy may still be writing shared memory when the CTA leaves
-    const uint64_t t0 = global_timer_ns();
-    for (int i = c > T::kStages ? c - T::kStages : 0; i < c; ++i)
-      while (!mbar_try_wait(full(i % T::kStages), (i / T::kStages) & 1) && global_timer_ns() - t0 < kProjWaitNs) {
-      }
-  }
+  const bool good = wait(done, 0, kErrTimeoutFull) && (warp > 1 || c == T::kChunks);
   __syncwarp();
   tc_fence_after();
   if (__syncthreads_and(good && !abort_s)) {  // the operands have been read: their place takes the results
@@ -334,7 +328,19 @@ __global__ void __launch_bounds__(128) gqa_mla_proj_tc_kernel(const MlaProjParam
       bulk_commit();
       bulk_wait_read<0>();
     }
+  } else if (warp < 2 && lane == 0) {
+    // gave up: no copy may still be writing shared memory, and no MMA reading it or writing tensor memory, when the CTA
+    // leaves (bounded, and deaf to the abort flag)
+    const uint64_t t0 = global_timer_ns();
+    auto drain = [&](uint32_t bar, uint32_t parity) {
+      while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kDrainNs) {
+      }
+    };
+    if (warp == 0) drain(done, 0);
+    else
+      for (int i = c > T::kStages ? c - T::kStages : 0; i < c; ++i) drain(full(i % T::kStages), (i / T::kStages) & 1);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tc_dealloc(tmem, T::kCols);

@@ -227,9 +227,9 @@ int gqa_mla_absorb_q(const void* q, const void* w_kv, const int32_t* positions, 
       !stride_ok(q_head_stride, 192, 8))
     return GQA_ERR_INVALID_ARGUMENT;
   int sms = 0;
-  const int rc = gqa::current_device_sms(&sms);
-  if (rc != GQA_OK) return rc;
   gqa::MlaProjParams p{};
+  const int rc = gqa::current_device_sms(&sms, &p.wait_limit_ns);
+  if (rc != GQA_OK) return rc;
   p.x = q;
   p.w = w_kv;
   p.positions = positions;
@@ -255,9 +255,9 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
     return GQA_ERR_INVALID_ARGUMENT;
   if (!aligned(o_latent, 16) || !aligned(w_kv, 16) || !aligned(out, 16)) return GQA_ERR_INVALID_ARGUMENT;
   int sms = 0;
-  const int rc = gqa::current_device_sms(&sms);
-  if (rc != GQA_OK) return rc;
   gqa::MlaProjParams p{};
+  const int rc = gqa::current_device_sms(&sms, &p.wait_limit_ns);
+  if (rc != GQA_OK) return rc;
   p.x = o_latent;
   p.w = w_kv;
   p.out = out;

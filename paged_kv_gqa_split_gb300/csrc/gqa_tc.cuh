@@ -286,4 +286,20 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
+// The same with a limit that may be below what one try_wait suspends the thread for (the test hook's): such a limit
+// spins on the non-blocking test.
+__device__ __forceinline__ bool tc_wait_limited(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err,
+                                                int err_bit, uint64_t limit_ns) {
+  if (limit_ns >= 1000000ull) return tc_wait(bar, parity, abort_s, err, err_bit, limit_ns);
+  for (const uint64_t t0 = global_timer_ns();;) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if (*abort_s) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      atomicOr(err, err_bit);
+      *abort_s = 1;
+      return false;
+    }
+  }
+}
+
 }  // namespace gqa
