@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
     constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, R, false, false);
     constexpr uint32_t idesc_o = tc_idesc_bf16(128, R, true, false);
     int n = 0, j = 0, piece = -1;
-    int pj = -1, p_first = 0, p_piece = 0;  // the tile whose P.V is pending
+    int pj = -1, p_first = 0, p_piece = 0, p_end = 0;  // the tile whose P.V is pending, and its first row past the end
     bool good = true;
     auto take_unit = [&](int& s) -> bool {
       s = n % kRing;
@@ -393,6 +393,14 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
       for (int u = 0; u < kVUnits; ++u) {
         int s;
         if (!take_unit(s)) return false;
+        if (p_end % BR != 0) {
+          // rows of the last box past the piece's tokens: slots that may hold anything, and their weight of 0 times an
+          // infinity or NaN is NaN
+          for (int i = lane; i < (BR - p_end % BR) * 16; i += 32)
+            st_shared_v4(base + s * kUnitBytes + (i & 1) * kRegionBytes + (p_end + (i >> 4)) * 128 + ((i >> 1) & 7) * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         // V^T block u: M = 128 dims over the unit's two regions (LBO), K = tokens in 8-row groups (SBO);
         // the whole warp forms the (uniform) descriptors, one elected lane issues
         const uint64_t dv = tc_sdesc(base + s * kUnitBytes, kRegionBytes, 1024, kSwizzle128B);
@@ -449,6 +457,7 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
       pj = j;
       p_first = (tl.flags & F_QLOAD) ? 1 : 0;
       p_piece = piece;
+      p_end = (tl.t_loc & (kTile - 1)) + tl.cnt;
       ++j;
     }
     if (good && pj >= 0) issue_pv();

@@ -226,3 +226,34 @@ def test_mla_batch_past_grid(kernel, h_q):
     empty = [b for b, n in enumerate(lens) if n == 0]
     assert np.all(o[empty] == 0.0) and np.all(np.isneginf(l[empty]))
     check(w, o, l)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kernel", [0, 1, 3])
+@pytest.mark.parametrize("lens,h_q,s_q,ps", [
+    ([1, 0, 17, 64, 65, 300, 127, 129, 100], 32, 1, 64), ([2000, 5, 700, 31, 33], 64, 1, 32), ([900, 33, 0, 130], 16, 2, 128),
+    ([6001, 40], 16, 1, 96), ([9999], 128, 1, 64)])
+def test_slots_past_the_lengths_hold_anything(lens, h_q, s_q, ps, kernel, value):
+    """The rest of a sequence's last page, and blocks of no sequence, do not reach the results: bit for bit what zeros
+    there give."""
+    assert _lib.gqa_mla_set_tuning(kernel) == 0
+    g = torch.Generator().manual_seed(len(lens) + ps)
+    used = [-(-n // ps) for n in lens]
+    blocks, width = sum(used) + 3, max(used) + 1
+    ids, table, at = torch.randperm(blocks, generator=g), torch.full((len(lens), width), -1, dtype=torch.int32), 0
+    cache = torch.zeros(blocks, ps, 1, 576)
+    own = torch.zeros(blocks, ps, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for j in range(used[b]):
+            table[b, j] = ids[at + j]
+            fill = min(ps, n - j * ps)
+            cache[ids[at + j], :fill, 0] = torch.randn(fill, 576, generator=g)
+            own[ids[at + j], :fill] = True
+        at += used[b]
+    q = torch.randn(len(lens), s_q, h_q, 576, generator=g).to(torch.bfloat16).cuda()
+    args = (table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 576 ** -0.5)
+    want, wl_ = _lib.mla_run(q, cache.to(torch.bfloat16).cuda(), *args)
+    cache[~own] = value
+    out, lse = _lib.mla_run(q, cache.to(torch.bfloat16).cuda(), *args)
+    assert torch.equal(out, want) and torch.equal(lse, wl_) and out.isfinite().all()
+    assert _lib.gqa_paged_decode_device_error() == 0
