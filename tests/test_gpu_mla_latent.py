@@ -587,3 +587,69 @@ def test_prefill_own_outputs_of_no_sequences():
         assert (out == 0).all() and torch.isneginf(lse).all()
     out = torch.full((5, 2, 128), 5.0, dtype=BF, device="cuda")
     assert (pkg.mla_prefill(**g, out=out, with_lse=False)[0] == 5).all()
+
+
+# ------------------------------------------------------- the absorbed form's batch
+@pytest.mark.parametrize("s_q,h,page", [(1, 32, 64), (3, 16, 32), (2, 64, 16), (4, 4, 1)])
+def test_absorbed_run_of_a_batch(s_q, h, page):
+    """Several sequences and new tokens: out and lse rows in their places, against the definition (tolerances as for
+    one token above: queries, weights and latent outputs are rounded to bf16 on the way) and the three calls it makes."""
+    lens = [(s_q, 40), (s_q, 700), (s_q, 1), (s_q, 129)]
+    c = case(lens, h, page, 50 + h)
+    g, n = on_gpu(c), len(lens) * s_q
+    freq, pos = pkg.rope_inv_freq(64)[0], torch.randint(0, 5000, (n,), dtype=torch.int32, generator=torch.Generator().manual_seed(s_q)).cuda()
+    args = (g["w_kv"], g["kv_cache"], g["block_table"], g["cache_seqlens"], pos, freq, 1.1)
+    out, lse = pkg.mla_absorbed_run(g["q"].view(len(lens), s_q, h, 192), *args)
+    assert out.shape == (len(lens), s_q, h, 128) and lse.shape == (len(lens), h, s_q)
+    turned = pkg.rope(g["q"], pos, freq, 1.1, 128, "interleaved").cpu()
+    o, l, _, _ = sv.mla_prefill_oracle(turned, c["w_kv"], c["kv_cache"], c["block_table"], c["cache_seqlens"],
+                                       c["cu_seqlens_q"], 192 ** -0.5, causal=False)
+    got = sv.f64(out).reshape(n, h, 128)
+    assert np.all(np.abs(got - o) <= 2e-2 + 2e-2 * np.abs(o))
+    assert np.abs(sv.f64(lse).transpose(1, 0, 2).reshape(h, n) - l).max() <= 2e-2
+    lat = pkg.mla_absorb_q(g["q"], g["w_kv"], pos, freq, 1.1)
+    o_lat, lse2 = pkg.mla_run(lat.view(len(lens), s_q, h, 576), g["kv_cache"], g["block_table"], g["cache_seqlens"], 192 ** -0.5)
+    assert torch.equal(lse, lse2)
+    assert torch.equal(out.view(n, h, 128), pkg.mla_expand_out(o_lat.view(n, h, 512), g["w_kv"]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out2, lse2 = pkg.mla_absorbed_run(g["q"].view(len(lens), s_q, h, 192), *args, stream=side)
+    side.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert pkg.mla_absorbed_run(g["q"].view(len(lens), s_q, h, 192), *args, with_lse=False)[1] is None
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_projections_in_streams_and_a_graph(n):
+    """Both forms of the projections (up to 16 tokens and above) in two streams at once and captured; out= given."""
+    g, h = torch.Generator().manual_seed(n), 5
+    w = weights(h, n).cuda()
+    q, o = torch.randn(n, h, 192, generator=g).to(BF).cuda(), torch.randn(n, h, 512, generator=g).to(BF).cuda()
+    pos, freq = torch.arange(n, dtype=torch.int32).cuda(), pkg.rope_inv_freq(64)[0]
+    calls = [lambda **k: pkg.mla_absorb_q(q, w, pos, freq, **k), lambda **k: pkg.mla_expand_out(o, w, **k)]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [f(stream=s) for _ in range(4) for s in streams for f in calls]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
+    outs = [torch.zeros_like(x) for x in want]
+    assert all(f(out=x) is x and torch.equal(x, y) for f, x, y in zip(calls, outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for f, x in zip(calls, outs):
+            f(out=x)
+    q.copy_(q.flip(0))
+    o.copy_(o.flip(0))
+    want = [f() for f in calls]
+    for _ in range(2):
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    for bad in (torch.empty(n, h, 64, dtype=BF, device="cuda"), torch.empty(n, h, 128, device="cuda"),
+                torch.empty(n, 128, h, dtype=BF, device="cuda").transpose(1, 2)):
+        with pytest.raises(ValueError):
+            pkg.mla_expand_out(o, w, out=bad)

@@ -178,3 +178,24 @@ def test_angles_of_far_positions():
     angle = 2 * np.pi * np.array([[turns(p, f) for f in freq] for p in pos])
     assert np.abs(got[:, 0, :r] - np.cos(angle)).max() <= 2.0 ** -22
     assert np.abs(got[:, 0, r:] - np.sin(angle)).max() <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,heads,dim,offset,rot", [(3, 5, 1023, 1, 1022), (2, 3, 1024, 301, 600), (5, 1, 1024, 0, 1024),
+                                                    (1, 7, 900, 0, 30), (4, 2, 515, 0, 514)])
+def test_heads_of_more_items_than_threads(n, heads, dim, offset, rot, layout, dtype):
+    """One element an item (rows that start off a 16-byte boundary): a thread takes several items of a head, in place
+    and out of place."""
+    x, pos, freq = make(n, heads, dim + 3, rot, dtype, 7 * dim + n)
+    x = x[..., 1:1 + dim]
+    got = pkg.rope(x, pos, freq, 1.25, offset, layout)
+    close(got, x, pos, freq, 1.25, offset, layout)
+    back = pkg.rope(got, pos, freq, 1.0, offset, layout, inverse=True)
+    close(back, got, pos, freq, 1.0, offset, layout, inverse=True)
+    same = x.clone()
+    wide = torch.full((n, heads, dim + 3), 9.0, dtype=dtype, device="cuda")
+    wide[..., 1:1 + dim] = same
+    pkg.rope(wide[..., 1:1 + dim], pos, freq, 1.25, offset, layout, out=wide[..., 1:1 + dim])
+    assert torch.equal(wide[..., 1:1 + dim], got)
+    assert (wide[..., 0] == 9).all() and (wide[..., 1 + dim:] == 9).all()
