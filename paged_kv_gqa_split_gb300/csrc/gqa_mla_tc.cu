@@ -114,6 +114,7 @@ struct TcWalker {
   Plan pl;
   int64_t u0, u1, u_next;
   int hg, tt, t_stop, p_lo, p_hi, p_flags, pb, wb, win;
+  int seq_len;  // tokens of the piece's sequence
   bool seg_open, ok;
   SplitInfo p_si;
 
@@ -139,6 +140,7 @@ struct TcWalker {
     u1 = cuts != nullptr ? cuts[cta + 1] : plan.end(cta);
     u_next = u0;
     hg = tt = t_stop = p_lo = p_hi = p_flags = pb = wb = win = 0;
+    seq_len = 0;
     seg_open = false;
     ok = true;
     p_si = SplitInfo{1, 0, 0};
@@ -165,6 +167,7 @@ struct TcWalker {
           p_lo = __shfl_sync(0xffffffffu, win, k);
           const int seq_hi = __shfl_sync(0xffffffffu, win, k + 1);
           p_hi = min(seq_hi, t_stop);
+          seq_len = seq_hi - p_lo;
           const int64_t base_u = static_cast<int64_t>(hg) * T;
           p_flags = F_QLOAD | ((tt == p_lo && p_hi == seq_hi) ? F_FINAL : 0) | ((base_u + tt != u0) ? F_SLOT1 : 0);
           const int64_t c_first = cta_of(base_u + p_lo), c_last = cta_of(base_u + seq_hi - 1);
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
     constexpr uint32_t idesc_s = tc_idesc_bf16(kTile, R, false, false);
     constexpr uint32_t idesc_o = tc_idesc_bf16(128, R, true, false);
     int n = 0, j = 0, piece = -1;
-    int pj = -1, p_first = 0, p_piece = 0, p_end = 0;  // the tile whose P.V is pending, and its first row past the end
+    int pj = -1, p_first = 0, p_piece = 0, p_end = 0;  // the tile whose P.V is pending, and, in a sequence's last box, the first row past the piece (else 0)
     bool good = true;
     auto take_unit = [&](int& s) -> bool {
       s = n % kRing;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
         int s;
         if (!take_unit(s)) return false;
         if (p_end % BR != 0) {
-          // rows of the last box past the piece's tokens: slots that may hold anything, and their weight of 0 times an
+          // rows of the last box past the sequence's tokens: slots that may hold anything, and their weight of 0 times an
           // infinity or NaN is NaN
           for (int i = lane; i < (BR - p_end % BR) * 16; i += 32)
             st_shared_v4(base + s * kUnitBytes + (i & 1) * kRegionBytes + (p_end + (i >> 4)) * 128 + ((i >> 1) & 7) * 16, 0, 0, 0, 0);
@@ -457,7 +460,8 @@ __global__ void __launch_bounds__(TcCfg<R>::kThreads, 1)
       pj = j;
       p_first = (tl.flags & F_QLOAD) ? 1 : 0;
       p_piece = piece;
-      p_end = (tl.t_loc & (kTile - 1)) + tl.cnt;
+      p_end = tl.t_loc + tl.cnt;
+      p_end = (p_end + BR - 1) / BR * BR > wk.seq_len ? (tl.t_loc & (kTile - 1)) + tl.cnt : 0;
       ++j;
     }
     if (good && pj >= 0) issue_pv();
