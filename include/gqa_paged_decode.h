@@ -258,12 +258,22 @@ int gqa_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache
  * num_blocks * page_size and batch * page_table_width * page_size must be
  * below 2^31. Asynchronous on `stream`; batch == 0 returns 0 without
  * launching. Uses the library-owned workspace (CSR offsets, one slot per
- * cached token, fp32 partials). Returns GQA_OK, GQA_ERR_INVALID_ARGUMENT,
+ * cached token, fp32 partials), so calls on different streams must be ordered,
+ * and a graph that captured one is not replayed after a call that needed a
+ * larger workspace. gqa_mla_decode_ws takes the caller's instead:
+ * gqa_mla_decode_ws_size bytes (0: arguments out of range, or no supported
+ * device) under the present tuning, 256-byte aligned, one per call in flight,
+ * not initialised; too small a one is GQA_ERR_WORKSPACE. Returns GQA_OK, GQA_ERR_INVALID_ARGUMENT,
  * GQA_ERR_WORKSPACE, GQA_ERR_LAUNCH or GQA_ERR_UNSUPPORTED_DEVICE.
  */
 int gqa_mla_decode(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* cache_seqlens,
                    float softmax_scale, void* out, float* lse, int batch, int s_q, int h_q, int page_size,
                    int num_blocks, int page_table_width, struct CUstream_st* stream);
+size_t gqa_mla_decode_ws_size(int batch, int s_q, int h_q, int page_size, int num_blocks, int page_table_width);
+int gqa_mla_decode_ws(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* cache_seqlens,
+                      float softmax_scale, void* out, float* lse, int batch, int s_q, int h_q, int page_size,
+                      int num_blocks, int page_table_width, struct CUstream_st* stream, void* workspace,
+                      size_t workspace_bytes);
 
 /*
  * Kernel choice of gqa_mla_decode for tests and benchmarks (process-wide):

@@ -48,6 +48,9 @@ _SIGNATURES = {
     "gqa_sparse_paged_decode": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float, _vp, _vp] + [ctypes.c_int] * 6 + [_vp]),
     "gqa_paged_decode_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, ctypes.c_int, _vp]),
     "gqa_mla_decode": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp] + [ctypes.c_int] * 6 + [_vp]),
+    "gqa_mla_decode_ws_size": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "gqa_mla_decode_ws": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp] + [ctypes.c_int] * 6 +
+                          [_vp, _vp, ctypes.c_size_t]),
     "gqa_mla_set_tuning": (ctypes.c_int, [ctypes.c_int]),
     "gqa_paged_decode_set_merge_mode": (ctypes.c_int, [ctypes.c_int]),
     "gqa_paged_decode_last_launch_count": (ctypes.c_int, []),
@@ -461,10 +464,13 @@ def gqa_mla_decode(q, kv_cache, block_table, cache_seqlens, softmax_scale, out, 
 def mla_run(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
             softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, with_lse: bool = True,
-            stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+            stream: Optional[torch.cuda.Stream] = None,
+            workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Dense MLA paged decode on the GPU (flash_mla_with_kvcache's dense path,
     one latent KV head of 576 values, d_v = 512). Returns (out [B, s_q, h_q, 512]
-    bf16, lse [B, h_q, s_q] fp32 natural log, or None)."""
+    bf16, lse [B, h_q, s_q] fp32 natural log, or None). workspace: a call of its
+    own streams or graphs passes one of mla_workspace_size bytes; without, the
+    library's is used, which calls ordered on one stream share."""
     tensors = {"q": q, "kv_cache": kv_cache, "block_table": block_table, "cache_seqlens": cache_seqlens}
     for name, t in tensors.items():
         if not isinstance(t, torch.Tensor):
@@ -496,10 +502,26 @@ def mla_run(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, 
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     with torch.cuda.device(q.device):
-        rc = gqa_mla_decode(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
-                            float(softmax_scale), out.data_ptr(), lse.data_ptr() if lse is not None else None, bsz,
-                            s_q, h_q, int(kv_cache.shape[1]), int(kv_cache.shape[0]), int(block_table.shape[1]),
-                            stream.cuda_stream)
+        args = (q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), cache_seqlens.data_ptr(),
+                float(softmax_scale), out.data_ptr(), lse.data_ptr() if lse is not None else None, bsz,
+                s_q, h_q, int(kv_cache.shape[1]), int(kv_cache.shape[0]), int(block_table.shape[1]),
+                stream.cuda_stream)
+        if workspace is None:
+            rc, where = gqa_mla_decode(*args), "gqa_mla_decode"
+        else:
+            if workspace.device != q.device or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous and on q's device")
+            rc = load().gqa_mla_decode_ws(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            where = "gqa_mla_decode_ws"
     if rc != GQA_OK:
-        raise GqaError(rc, "gqa_mla_decode")
+        raise GqaError(rc, where)
     return out, lse
+
+
+def mla_workspace_size(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor) -> int:
+    """Bytes of a workspace for mla_run on these tensors (shapes only are read)."""
+    with torch.cuda.device(q.device):
+        size = load().gqa_mla_decode_ws_size(*q.shape[:3], kv_cache.shape[1], kv_cache.shape[0], block_table.shape[1])
+    if size == 0 and q.shape[0] > 0:
+        raise ValueError("q, kv_cache and block_table are out of range")
+    return size

@@ -364,6 +364,136 @@ int run(const void* q, const void* k, const void* v, const int32_t* indptr, cons
   return GQA_OK;
 }
 
+bool mla_sizes_ok(int batch, int s_q, int h_q, int page_size, int num_blocks, int page_table_width) {
+  if (batch <= 0 || s_q <= 0 || h_q <= 0 || page_size <= 0 || num_blocks <= 0 || page_table_width <= 0) return false;
+  const int64_t rows = static_cast<int64_t>(s_q) * h_q;
+  if (rows % 16 != 0 || rows > (1 << 20) || static_cast<int64_t>(num_blocks) * page_size > INT32_MAX) return false;
+  const int64_t width = static_cast<int64_t>(page_table_width) * page_size;
+  if (width > INT32_MAX) return false;
+  const int64_t max_tokens = batch * width;  // bound on sum(seqlens)
+  return max_tokens <= INT32_MAX && max_tokens * (rows / 16) <= (int64_t{1} << 40);
+}
+
+gqa::PlanConfig mla_plan(const DeviceState& st, const Tuning& t, int kind) {
+  gqa::PlanConfig cfg;
+  cfg.tier1_ctas = t.num_ctas > 0 ? t.num_ctas : st.sm_count * gqa::mla_ctas_per_sm(kind);  // one wave
+  // one tier unless the tuning asks for tier 2: the MLA merge walks a sequence's pieces in turn
+  cfg.tier2_ctas = t.tier2_ctas > 0 ? t.tier2_ctas : 0;
+  cfg.min_units = t.min_units > 0 ? t.min_units : kDefaultMinUnits;
+  cfg.tier2_permille = t.tier2_permille;
+  cfg.tier2_min_units = t.tier2_min_units;
+  return cfg;
+}
+
+// Offsets of the latent decode's workspace (CSR offsets at 0), and its bytes.
+struct MlaSpace {
+  size_t slots, po, pl, rec, cost, bounds, need;
+  bool balanced;
+};
+MlaSpace mla_space(const gqa::PlanConfig& cfg, int kind, int piece_rows, int batch, int page_table_width, int page_size) {
+  const int64_t max_tokens = static_cast<int64_t>(batch) * page_table_width * page_size;
+  const size_t ctas = static_cast<size_t>(cfg.tier1_ctas) + cfg.tier2_ctas, pr = static_cast<size_t>(piece_rows);
+  MlaSpace at{};
+  at.slots = round256(static_cast<size_t>(batch + 1) * 4);
+  at.po = at.slots + round256(static_cast<size_t>(max_tokens) * 4);
+  at.pl = at.po + round256(2 * ctas * pr * 512 * sizeof(float));
+  at.rec = at.pl + round256(2 * ctas * pr * sizeof(float));
+  // the tensor-memory kernel with one tier: CTA ranges balanced by the scan for the cost of pieces
+  // (the scan's 32-bit cost prefix must hold every token plus the piece cost of every sequence)
+  at.balanced = kind == gqa::kMlaKernelTensorMemory && cfg.tier2_ctas == 0 &&
+                max_tokens + static_cast<int64_t>(batch) * kMlaTcPieceCost <= INT32_MAX;
+  at.cost = at.rec + round256(2 * ctas * 16);
+  at.bounds = at.cost + round256(static_cast<size_t>(batch + 1) * 4);
+  at.need = at.bounds + round256((ctas + 1) * sizeof(int64_t));
+  return at;
+}
+
+// gqa_mla_decode on the library's workspace (own) or the caller's.
+int mla_decode(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* cache_seqlens,
+               float softmax_scale, void* out, float* lse, int batch, int s_q, int h_q, int page_size, int num_blocks,
+               int page_table_width, cudaStream_t stream, bool own, void* user_ws, size_t user_ws_bytes) {
+  if (batch < 0) return GQA_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return GQA_OK;
+  if (!mla_sizes_ok(batch, s_q, h_q, page_size, num_blocks, page_table_width)) return GQA_ERR_INVALID_ARGUMENT;
+  const int64_t rows = static_cast<int64_t>(s_q) * h_q;
+  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || cache_seqlens == nullptr || out == nullptr)
+    return GQA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(softmax_scale)) return GQA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||
+      !aligned(cache_seqlens, 4) || (lse != nullptr && !aligned(lse, 4)))
+    return GQA_ERR_INVALID_ARGUMENT;
+
+  DeviceState* st = nullptr;
+  int dev = 0;
+  gqa::PlanConfig cfg;
+  void* ws = user_ws;
+  MlaSpace at;
+  gqa::MlaParams mp{};
+  mp.q = q;
+  mp.kv = kv_cache;
+  mp.batch = batch;
+  mp.rows = static_cast<int>(rows);
+  mp.block_table = block_table;
+  mp.width = page_table_width;
+  mp.page_size = page_size;
+  mp.num_blocks = num_blocks;
+  int mla_kind = gqa::kMlaKernelDefault;
+  gqa::MlaTcMaps maps;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int rc = current_device(&dev, &st);
+    if (rc != GQA_OK) return rc;
+    const Tuning& t = g_tune;
+    mla_kind = t.mla_kernel;
+    // default: the tensor-memory kernel when a sequence's rows come in multiples of 32 (one pass over the
+    // latent rows serves 32 or 64 rows, where the mma.sync kernel reads them once per 16; measured faster
+    // from 32 rows up), mma.sync otherwise (faster at 16 rows)
+    mp.piece_rows = 16;
+    if (mla_kind == gqa::kMlaKernelDefault)
+      mla_kind = rows % 32 == 0 ? gqa::kMlaKernelTensorMemory : gqa::kMlaKernelMma3;
+    if (mla_kind == gqa::kMlaKernelTensorMemory) {
+      // where the block size allows it (and Q rows fit the 32-bit box coordinates); else the mma.sync kernel
+      mp.piece_rows = gqa::mla_tc_piece_rows(static_cast<int>(rows));
+      const bool tc = gqa::mla_tc_supported(page_size) && static_cast<int64_t>(batch) * rows < INT32_MAX &&
+                      gqa::mla_tc_encode(mp, &maps);
+      if (!tc) mp.piece_rows = 16;
+      mla_kind = tc ? gqa::kMlaKernelTensorMemory : gqa::kMlaKernelMma3;
+    }
+    cfg = mla_plan(*st, t, mla_kind);
+    at = mla_space(cfg, mla_kind, mp.piece_rows, batch, page_table_width, page_size);
+    if (own) {
+      rc = library_workspace(st, at.need, &ws);
+      if (rc != GQA_OK) return rc;
+    } else if (user_ws == nullptr || !aligned(user_ws, 256) || user_ws_bytes < at.need) {
+      return GQA_ERR_WORKSPACE;
+    }
+  }
+  char* wsb = static_cast<char*>(ws);
+  int* err_word = nullptr;
+  if (gqa::device_error_word(&err_word) != cudaSuccess) return GQA_ERR_LAUNCH;
+  mp.kv_indptr_mut = reinterpret_cast<int*>(wsb);
+  mp.kv_indptr = mp.kv_indptr_mut;
+  mp.slots_mut = reinterpret_cast<int*>(wsb + at.slots);
+  mp.slots = mp.slots_mut;
+  mp.out = out;
+  mp.lse = lse;
+  mp.part_o = reinterpret_cast<float*>(wsb + at.po);
+  mp.part_lse = reinterpret_cast<float*>(wsb + at.pl);
+  mp.split_rec = reinterpret_cast<int4*>(wsb + at.rec);
+  mp.cost_ptr = reinterpret_cast<int*>(wsb + at.cost);
+  mp.bounds = at.balanced ? reinterpret_cast<int64_t*>(wsb + at.bounds) : nullptr;
+  mp.piece_cost = kMlaTcPieceCost;
+  mp.err = err_word;
+  mp.plan = cfg;
+  mp.epoch = (g_epoch.fetch_add(1) % ((1ull << 40) - 1)) + 1;
+  mp.h_q = h_q;
+  mp.s_q = s_q;
+  mp.scale_log2 = softmax_scale * kLog2e;
+  return gqa::launch_mla(mp, cache_seqlens, mla_kind, &maps, stream) == cudaSuccess
+             ? GQA_OK
+             : GQA_ERR_LAUNCH;
+}
+
 bool valid_kernel(const KernelChoice& k) { return gqa::decode_smem_bytes(k) > 0; }
 
 }  // namespace
@@ -648,106 +778,29 @@ int gqa_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache
 int gqa_mla_decode(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* cache_seqlens,
                    float softmax_scale, void* out, float* lse, int batch, int s_q, int h_q, int page_size,
                    int num_blocks, int page_table_width, struct CUstream_st* stream) {
-  if (batch < 0) return GQA_ERR_INVALID_ARGUMENT;
-  if (batch == 0) return GQA_OK;
-  if (s_q <= 0 || h_q <= 0 || page_size <= 0 || num_blocks <= 0 || page_table_width <= 0)
-    return GQA_ERR_INVALID_ARGUMENT;
-  const int64_t rows = static_cast<int64_t>(s_q) * h_q;
-  if (rows % 16 != 0 || rows > (1 << 20)) return GQA_ERR_INVALID_ARGUMENT;
-  if (static_cast<int64_t>(num_blocks) * page_size > INT32_MAX) return GQA_ERR_INVALID_ARGUMENT;
-  const int64_t max_tokens = static_cast<int64_t>(batch) * page_table_width * page_size;  // bound on sum(seqlens)
-  if (max_tokens > INT32_MAX || max_tokens * (rows / 16) > (int64_t{1} << 40)) return GQA_ERR_INVALID_ARGUMENT;
-  if (q == nullptr || kv_cache == nullptr || block_table == nullptr || cache_seqlens == nullptr || out == nullptr)
-    return GQA_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(softmax_scale)) return GQA_ERR_INVALID_ARGUMENT;
-  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||
-      !aligned(cache_seqlens, 4) || (lse != nullptr && !aligned(lse, 4)))
-    return GQA_ERR_INVALID_ARGUMENT;
+  return mla_decode(q, kv_cache, block_table, cache_seqlens, softmax_scale, out, lse, batch, s_q, h_q, page_size, num_blocks,
+                    page_table_width, stream, true, nullptr, 0);
+}
 
-  DeviceState* st = nullptr;
+int gqa_mla_decode_ws(const void* q, const void* kv_cache, const int32_t* block_table, const int32_t* cache_seqlens,
+                      float softmax_scale, void* out, float* lse, int batch, int s_q, int h_q, int page_size,
+                      int num_blocks, int page_table_width, struct CUstream_st* stream, void* workspace,
+                      size_t workspace_bytes) {
+  return mla_decode(q, kv_cache, block_table, cache_seqlens, softmax_scale, out, lse, batch, s_q, h_q, page_size, num_blocks,
+                    page_table_width, stream, false, workspace, workspace_bytes);
+}
+
+size_t gqa_mla_decode_ws_size(int batch, int s_q, int h_q, int page_size, int num_blocks, int page_table_width) {
+  if (!mla_sizes_ok(batch, s_q, h_q, page_size, num_blocks, page_table_width)) return 0;
+  std::lock_guard<std::mutex> lock(g_mu);
   int dev = 0;
-  gqa::PlanConfig cfg;
-  void* ws = nullptr;
-  size_t off_indptr = 0, off_slots = 0, off_po = 0, off_pl = 0, off_rec = 0, off_cost = 0, off_bounds = 0;
-  bool balanced = false;
-  gqa::MlaParams mp{};
-  mp.q = q;
-  mp.kv = kv_cache;
-  mp.batch = batch;
-  mp.rows = static_cast<int>(rows);
-  mp.block_table = block_table;
-  mp.width = page_table_width;
-  mp.page_size = page_size;
-  mp.num_blocks = num_blocks;
-  int mla_kind = gqa::kMlaKernelDefault;
-  gqa::MlaTcMaps maps;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    int rc = current_device(&dev, &st);
-    if (rc != GQA_OK) return rc;
-    const Tuning& t = g_tune;
-    mla_kind = t.mla_kernel;
-    // default: the tensor-memory kernel when a sequence's rows come in multiples of 32 (one pass over the
-    // latent rows serves 32 or 64 rows, where the mma.sync kernel reads them once per 16; measured faster
-    // from 32 rows up), mma.sync otherwise (faster at 16 rows)
-    mp.piece_rows = 16;
-    if (mla_kind == gqa::kMlaKernelDefault)
-      mla_kind = rows % 32 == 0 ? gqa::kMlaKernelTensorMemory : gqa::kMlaKernelMma3;
-    if (mla_kind == gqa::kMlaKernelTensorMemory) {
-      // where the block size allows it (and Q rows fit the 32-bit box coordinates); else the mma.sync kernel
-      mp.piece_rows = gqa::mla_tc_piece_rows(static_cast<int>(rows));
-      const bool tc = gqa::mla_tc_supported(page_size) && static_cast<int64_t>(batch) * rows < INT32_MAX &&
-                      gqa::mla_tc_encode(mp, &maps);
-      if (!tc) mp.piece_rows = 16;
-      mla_kind = tc ? gqa::kMlaKernelTensorMemory : gqa::kMlaKernelMma3;
-    }
-    cfg.tier1_ctas = t.num_ctas > 0 ? t.num_ctas : st->sm_count * gqa::mla_ctas_per_sm(mla_kind);  // one wave
-    // one tier unless the tuning asks for tier 2: the MLA merge walks a sequence's pieces in turn
-    cfg.tier2_ctas = t.tier2_ctas > 0 ? t.tier2_ctas : 0;
-    cfg.min_units = t.min_units > 0 ? t.min_units : kDefaultMinUnits;
-    cfg.tier2_permille = t.tier2_permille;
-    cfg.tier2_min_units = t.tier2_min_units;
-    const size_t ctas = static_cast<size_t>(cfg.tier1_ctas) + cfg.tier2_ctas;
-    off_indptr = 0;
-    off_slots = round256(static_cast<size_t>(batch + 1) * 4);
-    off_po = off_slots + round256(static_cast<size_t>(max_tokens) * 4);
-    const size_t pr = static_cast<size_t>(mp.piece_rows);
-    off_pl = off_po + round256(2 * ctas * pr * 512 * sizeof(float));
-    off_rec = off_pl + round256(2 * ctas * pr * sizeof(float));
-    // the tensor-memory kernel with one tier: CTA ranges balanced by the scan for the cost of pieces
-    // (the scan's 32-bit cost prefix must hold every token plus the piece cost of every sequence)
-    balanced = mla_kind == gqa::kMlaKernelTensorMemory && cfg.tier2_ctas == 0 &&
-               max_tokens + static_cast<int64_t>(batch) * kMlaTcPieceCost <= INT32_MAX;
-    off_cost = off_rec + round256(2 * ctas * 16);
-    off_bounds = off_cost + round256(static_cast<size_t>(batch + 1) * 4);
-    const size_t need = off_bounds + round256((ctas + 1) * sizeof(int64_t));
-    rc = library_workspace(st, need, &ws);
-    if (rc != GQA_OK) return rc;
-  }
-  char* wsb = static_cast<char*>(ws);
-  int* err_word = nullptr;
-  if (gqa::device_error_word(&err_word) != cudaSuccess) return GQA_ERR_LAUNCH;
-  mp.kv_indptr_mut = reinterpret_cast<int*>(wsb + off_indptr);
-  mp.kv_indptr = mp.kv_indptr_mut;
-  mp.slots_mut = reinterpret_cast<int*>(wsb + off_slots);
-  mp.slots = mp.slots_mut;
-  mp.out = out;
-  mp.lse = lse;
-  mp.part_o = reinterpret_cast<float*>(wsb + off_po);
-  mp.part_lse = reinterpret_cast<float*>(wsb + off_pl);
-  mp.split_rec = reinterpret_cast<int4*>(wsb + off_rec);
-  mp.cost_ptr = reinterpret_cast<int*>(wsb + off_cost);
-  mp.bounds = balanced ? reinterpret_cast<int64_t*>(wsb + off_bounds) : nullptr;
-  mp.piece_cost = kMlaTcPieceCost;
-  mp.err = err_word;
-  mp.plan = cfg;
-  mp.epoch = (g_epoch.fetch_add(1) % ((1ull << 40) - 1)) + 1;
-  mp.h_q = h_q;
-  mp.s_q = s_q;
-  mp.scale_log2 = softmax_scale * kLog2e;
-  return gqa::launch_mla(mp, cache_seqlens, mla_kind, &maps, stream) == cudaSuccess
-             ? GQA_OK
-             : GQA_ERR_LAUNCH;
+  DeviceState* st = nullptr;
+  if (current_device(&dev, &st) != GQA_OK) return 0;
+  // whichever kernel the call takes
+  const int tc = gqa::kMlaKernelTensorMemory, mma = g_tune.mla_kernel == gqa::kMlaKernelMma4 ? gqa::kMlaKernelMma4 : gqa::kMlaKernelMma3;
+  const size_t a = mla_space(mla_plan(*st, g_tune, tc), tc, gqa::mla_tc_piece_rows(s_q * h_q), batch, page_table_width, page_size).need;
+  const size_t b = mla_space(mla_plan(*st, g_tune, mma), mma, 16, batch, page_table_width, page_size).need;
+  return a > b ? a : b;
 }
 
 int gqa_paged_decode_test_fail_allocs(int count) {

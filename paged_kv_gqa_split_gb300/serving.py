@@ -17,7 +17,7 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import (FP8_ROW_BYTES, GQA_OK, GqaError, HEAD_DIM, MLA_D_QK, MLA_D_V, NUM_KV_HEADS, NUM_QO_HEADS, load,
-                   mla_run)
+                   mla_run, mla_workspace_size)
 
 try:  # the allocation that compiled PyTorch programs call: no dispatch (3 us of a 14 us call on the GPU's host)
     from torch._C._dynamo.guards import _empty_strided_cuda
@@ -368,6 +368,7 @@ def mla_absorbed_run(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor
                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Latent attention for new tokens, absorbed form: ``mla_absorb_q``, ``mla_run`` and ``mla_expand_out`` in turn.
     q: [B, s_q, heads, 192] (s_q * heads a multiple of 16; not causal within the s_q tokens); positions: [B * s_q].
+    Each call allocates its workspace, so calls in several streams and captured ones do not share one.
     Returns (out [B, s_q, heads, 128] bf16, lse [B, heads, s_q] fp32 natural log, or None)."""
     if stream is not None:  # the intermediate tensors then belong to that stream
         with torch.cuda.stream(stream):
@@ -377,8 +378,24 @@ def mla_absorbed_run(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor
         raise ValueError(f"expected q [B, s_q, heads, {MLA_D_HEAD}]")
     b, s, h, d = q.shape
     flat = mla_absorb_q(q.reshape(b * s, h, d), w_kv, positions, inv_freq, scale, layout)
-    o, lse = mla_run(flat.view(b, s, h, MLA_D_QK), kv_cache, block_table, cache_seqlens,
-                     MLA_D_HEAD ** -0.5 if softmax_scale is None else softmax_scale, with_lse=with_lse)
+    flat, index = flat.view(b, s, h, MLA_D_QK), flat.get_device()
+    if not (_ready(index, kv_cache, torch.bfloat16) and _ready(index, block_table, torch.int32)):
+        _check(index, torch.bfloat16, True, kv_cache=kv_cache)
+        _check(index, torch.int32, True, block_table=block_table)
+    blocks, page = _latent_cache(kv_cache)
+    if block_table.dim() != 2:
+        raise ValueError("expected block_table [B, width]")
+    # a workspace of the call's own: other streams' calls and captured graphs do not share it
+    if index == torch._C._cuda_getDevice():  # without the switch of devices, 5 us
+        size = load().gqa_mla_decode_ws_size(b, s, h, page, blocks, block_table.shape[1])
+    else:
+        size = mla_workspace_size(flat, kv_cache, block_table)
+    if size == 0 and b > 0:
+        raise ValueError("the batch, the heads or the block table are out of range")
+    workspace = _new(index, (size,), torch.uint8, None)
+    o, lse = mla_run(flat, kv_cache, block_table, cache_seqlens,
+                     MLA_D_HEAD ** -0.5 if softmax_scale is None else softmax_scale, with_lse=with_lse,
+                     workspace=workspace)
     return mla_expand_out(o.view(b * s, h, MLA_D_V), w_kv).view(b, s, h, MLA_HEAD_V), lse
 
 

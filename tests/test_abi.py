@@ -200,3 +200,11 @@ def test_mla_cpu_tensors_raise():
     w = wl.make_mla_workload([5, 9], 16, 1, 4, seed=1)
     with pytest.raises(ValueError, match="no CPU path"):
         _lib.mla_run(w.q, w.kv_cache, w.block_table, w.cache_seqlens)
+
+
+def test_mla_workspace_size_refusals(lib):
+    ok = [4, 1, 16, 64, 100, 9]
+    for i, bad in ((0, 0), (0, -1), (1, 0), (2, 8), (2, 0), (3, 0), (4, 0), (5, 0), (4, 1 << 26), (5, 1 << 26), (2, 1 << 21)):
+        args = list(ok)
+        args[i] = bad
+        assert lib.gqa_mla_decode_ws_size(*args) == 0, (i, bad)

@@ -257,3 +257,25 @@ def test_slots_past_the_lengths_hold_anything(lens, h_q, s_q, ps, kernel, value)
     out, lse = _lib.mla_run(q, cache.to(torch.bfloat16).cuda(), *args)
     assert torch.equal(out, want) and torch.equal(lse, wl_) and out.isfinite().all()
     assert _lib.gqa_paged_decode_device_error() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 3, 4])
+def test_caller_workspace(kernel):
+    """The same bits on a workspace of the caller's that holds anything; one too small or misaligned is refused."""
+    for h_q, ps in ((64, 64), (32, 16), (16, 32)):
+        w = wl.make_mla_workload([3000, 0, 77, 1200], h_q, 1, ps, 81)
+        g = w.to("cuda")
+        assert _lib.gqa_mla_set_tuning(kernel) == 0
+        args = (g.q, g.kv_cache, g.block_table, g.cache_seqlens, w.softmax_scale)
+        want, lse = _lib.mla_run(*args)
+        size = _lib.mla_workspace_size(g.q, g.kv_cache, g.block_table)
+        for fill in (0, 0xFF, 1):
+            space = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+            out, l2 = _lib.mla_run(*args, workspace=space)
+            assert torch.equal(out, want) and torch.equal(lse, l2)
+        for bad in (torch.empty(100, dtype=torch.uint8, device="cuda"), torch.empty(size + 256, dtype=torch.uint8, device="cuda")[16:]):
+            with pytest.raises(_lib.GqaError):
+                _lib.mla_run(*args, workspace=bad)
+    with pytest.raises(ValueError):
+        _lib.mla_run(*args, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    assert _lib.gqa_paged_decode_device_error() == 0

@@ -653,3 +653,62 @@ def test_projections_in_streams_and_a_graph(n):
                 torch.empty(n, 128, h, dtype=BF, device="cuda").transpose(1, 2)):
         with pytest.raises(ValueError):
             pkg.mla_expand_out(o, w, out=bad)
+
+
+def test_absorbed_runs_share_no_workspace():
+    """Calls in two streams at once, two captured graphs replayed at once, and a graph replayed after a call that needs
+    far more room: each gives what it gives alone."""
+    page, freq = 64, pkg.rope_inv_freq(64)[0]
+    lens = [[3000, 40, 700, 1], [5, 2000, 2000, 64, 900]]
+    sets = []
+    for i, (ln, h) in enumerate(zip(lens, (32, 16))):
+        c = case([(1, n) for n in ln], h, page, 60 + i)
+        g, b = on_gpu(c), len(ln)
+        pos = torch.tensor(ln, dtype=torch.int32).cuda() - 1
+        sets.append((g["q"].view(b, 1, h, 192), g["w_kv"], g["kv_cache"], g["block_table"], g["cache_seqlens"], pos, freq))
+    want = [pkg.mla_absorbed_run(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [(i, pkg.mla_absorbed_run(*sets[i], stream=streams[i])) for _ in range(10) for i in (0, 1)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for i, (o, l) in got)
+    graphs, outs = [], []
+    for a in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(pkg.mla_absorbed_run(*a))
+        graphs.append(graph)
+    large = case([(1, 9000)] * 40, 64, page, 62)
+    g = on_gpu(large)
+    pkg.mla_absorbed_run(g["q"].view(40, 1, 64, 192), g["w_kv"], g["kv_cache"], g["block_table"], g["cache_seqlens"],
+                         g["cache_seqlens"] - 1, freq)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for (o, l), w in zip(outs, want))
+        for o, l in outs:
+            o.zero_()
+            l.zero_()
+        torch.cuda.synchronize()
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+def test_absorbed_run_refusals():
+    c = case([(1, 20), (1, 3)], 16, 16, 63)
+    g = on_gpu(c)
+    ok = dict(q=g["q"].view(2, 1, 16, 192), w_kv=g["w_kv"], kv_cache=g["kv_cache"], block_table=g["block_table"],
+              cache_seqlens=g["cache_seqlens"])
+    pkg.mla_absorbed_run(**ok)
+    for name in ok:
+        with pytest.raises((TypeError, ValueError)):
+            pkg.mla_absorbed_run(**dict(ok, **{name: None}))
+    for change in (dict(q=ok["q"][:, 0]), dict(kv_cache=ok["kv_cache"][:, :, 0]), dict(block_table=ok["block_table"][0]),
+                   dict(block_table=ok["block_table"].long()), dict(block_table=ok["block_table"][:, :0]),
+                   dict(cache_seqlens=ok["cache_seqlens"][:1]), dict(q=ok["q"][:, :, :8], w_kv=ok["w_kv"][:8])):
+        with pytest.raises(ValueError):
+            pkg.mla_absorbed_run(**dict(ok, **change))
+    out, lse = pkg.mla_absorbed_run(**dict(ok, q=ok["q"][:0], block_table=ok["block_table"][:0], cache_seqlens=ok["cache_seqlens"][:0]))
+    assert out.shape == (0, 1, 16, 128) and lse.shape == (0, 16, 1)
