@@ -552,7 +552,8 @@ int gqa_mla_expand_out(const void* o_latent, const void* w_kv, void* out, int nu
  * makes them 0 in out, with GQA_FILL_LSE -inf in lse. The expanded keys and values are fp16, scaled by powers of two, one
  * per sequence or, where its tokens differ by more than 2^8, one per token: a
  * token's values below about 2^-29 of 512 * max|its latent| * max|w_kv| lose bits
- * (2^-21 where the sequence has one), and no token's size costs another's.
+ * (2^-21 where the sequence has one), and no token's size costs another's. Keys
+ * and values past fp32's range count as its largest number.
  * Everything else accumulates in fp32. lse carries that rounding of the keys:
  * about 2^-12 of a score's size.
  * With few queries and many tokens a row's sums are split and joined in an order

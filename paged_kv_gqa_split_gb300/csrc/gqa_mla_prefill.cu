@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -376,6 +377,11 @@ __device__ __forceinline__ bool kv_exponents(const unsigned* amax, int b, int& e
   exponents(amax, t.x, t.y, ek, ev);
   return (t.x != 0 && (t.x >> 23) - (~t.z >> 23) > kWindow) || (t.y != 0 && (t.y >> 23) - (~t.w >> 23) > kWindow);
 }
+// Whether keys or values of a sequence may pass fp32's range as they accumulate.
+__device__ __forceinline__ bool may_overflow(const unsigned* amax, int b) {
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(amax));
+  return exponent_of(__ldcg(amax + 4 + 4 * b)) + exponent_of(max(w.x, w.y)) + 11 > 127;
+}
 // Those of a packed row of sequence b; a row of zeros has the sequence's.
 __device__ __forceinline__ bool row_exponents(const MlaPrefillParams& p, int b, int64_t row, int& ek, int& ev) {
   const bool wide = kv_exponents(p.amax, b, ek, ev);
@@ -590,15 +596,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const uint32_t of_bad = part == 0 ? 0x7fff7fffu : 0u;
     const uint32_t dfree = cluster_addr(bar(E_DFREE), 0);
     const uint32_t dst = base + kExOut + part * kExRegion;
-    bool bad = false;
+    bool bad = false, over = false;
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
       const int i = u - u0, m0 = tile_of(u) * 256 + 128 * half;  // this CTA's packed rows (may lie past the last one)
       const bool out = m0 < total;
       if (first_of_tile(u) && out) {  // 128 rows are one sequence's
         int ek, ev;
-        row_exponents(p, find_seq(p.kv_start, p.batch, m0), m0 + row, ek, ev);
+        const int b = find_seq(p.kv_start, p.batch, m0);
+        row_exponents(p, b, m0 + row, ek, ev);
         f = pow2(part == 0 ? -ek : -ev);
+        over = may_overflow(p.amax, b);
         bad = ((__ldcg(p.bad + (m0 >> 5) + wq) >> lane) & 1u) != 0;
       }
       const bool good = warp_wait(bar(E_DFULL + (i & 1)), (i >> 1) & 1, abort_s, err, kErrTimeoutFull);
@@ -617,6 +625,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
         tc_ld32(d + 64 * r, v);
         tc_ld32(d + 64 * r + 32, v + 32);
         tc_wait_ld();
+        if (over) {  // a weight of 0 times an infinity would be NaN in rows that do not see the token
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(fminf(fmaxf(__uint_as_float(v[e]), -FLT_MAX), FLT_MAX));
+        }
         if (r == 1) {
           tc_fence_before();
           __syncwarp();

@@ -534,6 +534,22 @@ def test_prefill_one_huge_token_in_several_passes_and_beside_others():
     assert torch.equal(out[:50], plain[:50]) and torch.equal(out[350:], plain[350:])
 
 
+@pytest.mark.parametrize("others", [1.0, 2.0 ** 118])
+def test_prefill_expansion_past_32_bits(others):
+    """A finite latent whose keys and values pass fp32's range leaves the rows that do not see it alone, whether the
+    tokens have their own exponents (the others 2^125 times smaller) or one (2^7 times)."""
+    c = case([(200, 200)], 2, 1, 44, w_std=1.0)
+    block, scale = int(c["block_table"][0, 150]), 192 ** -0.5 / others
+    row = c["kv_cache"][block].double()
+    c["kv_cache"] = (c["kv_cache"].double() * others).to(BF)
+    c["kv_cache"][block] = (row * 2.0 ** 125).to(BF)
+    assert c["kv_cache"][block].isfinite().all()
+    assert np.abs(sv.f64(c["w_kv"]) @ sv.f64(c["kv_cache"][block, 0, 0, :512])).max() > 2.0 ** 128
+    out, lse = pkg.mla_prefill(**on_gpu(c), softmax_scale=scale)
+    o, l, ob, lb = sv.mla_prefill_oracle(c["q"][:150], c["w_kv"], c["kv_cache"], c["block_table"], [150], [0, 150], scale)
+    assert np.all(np.abs(sv.f64(out)[:150] - o) <= ob) and np.all(np.abs(sv.f64(lse)[:, :150] - l) <= lb)
+
+
 def test_prefill_not_finite_and_huge_tokens_together():
     """Rows before either are as without both; rows that see the one that is not finite are NaN."""
     c = case([(200, 200)], 2, 1, 43)
