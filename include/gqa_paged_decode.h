@@ -452,8 +452,8 @@ int gqa_rope_inv_freq(int rot_dim, double base, int scaling, double factor, doub
  * Rotates x [num_tokens][num_heads][head_dim] (GQA_TYPE_*; token and head
  * strides in elements, a head's values contiguous) into out, laid out by its
  * own strides; elements outside the window are copied. out may be x itself
- * with the same strides, and must not overlap it otherwise; its rows must not
- * overlap one another. inverse != 0 turns by -a: it undoes a rotation (with
+ * with the same strides (others at the same address are refused), and must not
+ * overlap it otherwise; its rows must not overlap one another. inverse != 0 turns by -a: it undoes a rotation (with
  * scale 1 / scale), and is the gradient of one (with the same scale).
  * num_heads and head_dim up to 1024. Addresses need the type's alignment only;
  * 16-byte aligned rows and windows are fastest. num_tokens == 0 returns 0

@@ -92,6 +92,10 @@ int gqa_rope(const void* x, const int32_t* positions, const double* inv_freq, fl
   const bool head_major = (num_tokens == 1 || out_token_stride >= head_dim) &&
                           (num_heads == 1 || out_head_stride >= (num_tokens - 1) * out_token_stride + head_dim);
   if (!token_major && !head_major) return GQA_ERR_INVALID_ARGUMENT;
+  // in place the strides are the same: otherwise rows would be written before others have read them
+  if (x == out && ((num_tokens > 1 && x_token_stride != out_token_stride) ||
+                   (num_heads > 1 && x_head_stride != out_head_stride)))
+    return GQA_ERR_INVALID_ARGUMENT;
   int sms = 0;
   const int rc = gqa::current_device_sms(&sms);
   if (rc != GQA_OK) return rc;

@@ -154,3 +154,10 @@ def test_cpu_tensors_raise(lib):
     for call in calls:
         with pytest.raises(ValueError, match="no CPU path"):
             call()
+
+
+def test_rope_in_place_needs_the_same_strides(lib):
+    ok = dict(x=A, positions=A, inv_freq=A, scale=1.0, out=A, n=4, heads=3, dim=128, offset=0, rot=128, layout=0,
+              inverse=0, dtype=0, xt=384, xh=128, ot=384, oh=128, stream=None)
+    _refused(lib.gqa_rope, ok, [dict(ot=512, oh=128), dict(ot=128, oh=512), dict(xt=512), dict(n=1, xh=256),
+                                dict(heads=1, xt=512)])
