@@ -1102,7 +1102,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll 1
     for (int it = 0; good && enter_unit(it); ++it) {
       const int nt = unit_word(it, U_NT0 + a);
-      float row_fac = 1.f;
+      int row_exp = 0;
       if (nt > 0) {
         // this row's query, copied in as bf16, to fp16 with its largest value in [2^10, 2^11). Small loops: straight-line
         // code for the whole row took 6 to 8 us a CTA, most of it instruction fetch. Rows past the sequence's queries hold
@@ -1117,9 +1117,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ld_shared_u4(sw128(q_row + (k >> 3) * kQRegion, 32 * wq + lane, k & 7), v.x, v.y, v.z, v.w);
           top = finite_bits(v, top);
         }
-        const int e = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
-        row_fac = pow2(e);
-        const float f = p.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
+        row_exp = top != 0 ? max(exponent_of(top), -116) - 10 : 0;
+        const float f = p.scale_log2 < 0.f ? -pow2(-row_exp) : pow2(-row_exp);
         auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
 #pragma unroll 2
         for (int k = 0; k < 24; ++k) {
@@ -1132,7 +1131,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(q_bar);
       }
-      const float sc = fmaxf(row_fac * fabsf(p.scale_log2) * pow2(unit_word(it, U_EK)), 1e-37f);  // > 0: -inf * sc stays -inf
+      const int sc_exp = row_exp + unit_word(it, U_EK);  // in two factors, so that nothing between leaves the range
+      const float sc = fmaxf(fabsf(p.scale_log2) * pow2(sc_exp >> 1) * pow2(sc_exp - (sc_exp >> 1)), 1e-37f);  // > 0: -inf * sc stays -inf
       // the last key that the warp's first row and this row see
       const int row0 = unit_word(it, U_ROW) + 256 * a + 128 * half + 32 * wq;
       const int lim0 = p.causal ? unit_word(it, U_KEYS) - unit_word(it, U_NQ) + row0 : INT_MAX;

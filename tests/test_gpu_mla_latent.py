@@ -728,3 +728,31 @@ def test_absorbed_run_refusals():
             pkg.mla_absorbed_run(**dict(ok, **change))
     out, lse = pkg.mla_absorbed_run(**dict(ok, q=ok["q"][:0], block_table=ok["block_table"][:0], cache_seqlens=ok["cache_seqlens"][:0]))
     assert out.shape == (0, 1, 16, 128) and lse.shape == (0, 16, 1)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 2.0 ** -130])
+@pytest.mark.parametrize("huge", [False, True])
+def test_prefill_scales_of_any_sign(scale, huge):
+    """A negative scale turns the order round; 0 and one below what 32 bits hold give the mean of the values seen."""
+    c = case([(150, 170), (40, 40)], 2, 1, 64)
+    rows = torch.ones(190, dtype=torch.bool)
+    if huge:
+        block = int(c["block_table"][0, 120])
+        c["kv_cache"][block] = (c["kv_cache"][block].double() * 2.0 ** 50).to(BF)
+        rows[100:150] = False  # they see it
+    out, lse = pkg.mla_prefill(**on_gpu(c), softmax_scale=scale)
+    o, l, ob, lb = sv.mla_prefill_oracle(c["q"], c["w_kv"], c["kv_cache"], c["block_table"], c["cache_seqlens"],
+                                         c["cu_seqlens_q"], scale)
+    assert np.all((np.abs(sv.f64(out) - o) <= ob)[rows]) and np.all((np.abs(sv.f64(lse) - l) <= lb)[:, rows])
+
+
+def test_prefill_small_scale_of_small_queries_and_large_keys():
+    """The factors of a score pass the range of 32 bits only among themselves: bit for bit the outputs at ordinary size
+    (all powers of two; rotary keys 0, which another power would scale)."""
+    c = case([(40, 90)], 2, 16, 12)
+    c["kv_cache"][..., 512:] = 0
+    big = dict(c, q=(c["q"].double() * 2.0 ** -50).to(BF), kv_cache=(c["kv_cache"].double() * 2.0 ** 60).to(BF),
+               w_kv=(c["w_kv"].double() * 2.0 ** 58).to(BF))
+    want, wl = pkg.mla_prefill(**on_gpu(c), softmax_scale=2.0 ** -4)
+    out, lse = pkg.mla_prefill(**on_gpu(big), softmax_scale=2.0 ** (-4 + 50 - 60 - 58))
+    assert torch.equal((out.double() * 2.0 ** -118).to(BF), want) and torch.equal(lse, wl)
