@@ -246,7 +246,8 @@ int gqa_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache
  * layout). Not causal within the s_q query tokens (the page's dense kernel
  * supports causal masking only for s_q = 1, where it changes nothing). A
  * sequence with no cached token gives out = 0 and lse = -inf; a token whose
- * block-table entry lies outside [0, num_blocks) is left out.
+ * block-table entry lies outside [0, num_blocks) is left out. Slots past the
+ * lengths may hold anything.
  *
  * Layouts (caller-owned device memory, contiguous): q [batch][s_q][h_q][576]
  * bf16 and out [batch][s_q][h_q][512] bf16, 16-byte aligned; kv_cache

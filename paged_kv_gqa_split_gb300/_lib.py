@@ -449,7 +449,7 @@ MLA_D_QK, MLA_D_V = 576, 512
 
 
 def gqa_mla_set_tuning(kernel: int) -> int:
-    """MLA decode kernel: 0 default (the tensor-memory kernel for 64-row multiples and block sizes
+    """MLA decode kernel: 0 default (the tensor-memory kernel for 32-row multiples and block sizes
     that are a multiple of 32, else mma.sync with 3 stages), 1 the tensor-memory kernel (block
     sizes that are a multiple of 32), 3 or 4 the mma.sync kernel with that ring depth."""
     return load().gqa_mla_set_tuning(kernel)
@@ -468,9 +468,9 @@ def mla_run(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, 
             workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Dense MLA paged decode on the GPU (flash_mla_with_kvcache's dense path,
     one latent KV head of 576 values, d_v = 512). Returns (out [B, s_q, h_q, 512]
-    bf16, lse [B, h_q, s_q] fp32 natural log, or None). workspace: a call of its
-    own streams or graphs passes one of mla_workspace_size bytes; without, the
-    library's is used, which calls ordered on one stream share."""
+    bf16, lse [B, h_q, s_q] fp32 natural log, or None). workspace: of
+    mla_workspace_size bytes, for calls in several streams or captured ones;
+    without it the library's is used, which calls ordered on one stream share."""
     tensors = {"q": q, "kv_cache": kv_cache, "block_table": block_table, "cache_seqlens": cache_seqlens}
     for name, t in tensors.items():
         if not isinstance(t, torch.Tensor):

@@ -26,8 +26,8 @@
 // sums over the sequences), the gather (paged rows to packed rows, 128-aligned per
 // sequence and zero-filled, and the maxima), the expansion, the attention, and a join
 // where that was split. Bound by
-// the tensor cores: 8192 tokens x 16 heads 252 us in all (1500 TFLOP/s, 80 % of the
-// measured cuBLAS bf16 rate); five short prompts 33 us, the chain's latency.
+// the tensor cores: 8192 tokens x 16 heads 250 to 260 us in all (1460 to 1510 TFLOP/s, 78 to
+// 81 % of the measured cuBLAS bf16 rate); five short prompts 35 us, the chain's latency.
 #include <cuda_bf16.h>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -710,8 +710,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // Every wait is bounded: on a timeout the CTA flags
 // the device error word and leaves after draining its copies and MMAs.
 //
-// Measured: 8192 causal tokens x 16 heads 197 us (1740 TFLOP/s), 1024 tokens behind
+// Measured: 8192 causal tokens x 16 heads 198 us (1740 TFLOP/s), 1024 tokens behind
 // 16384 x 32 heads 193 us (1720 TFLOP/s, on 64 of the 76 pairs).
+//
+// A timeout frees what the CTA holds and leaves, after the drains of its own copies and MMAs. A pair's copies are counted
+// by the even CTA alone, so the odd one's last are only known to have landed because every wait lasts 2 s: this path is
+// not for shorter limits, and the test hook's does not reach it.
 constexpr int kKTile = 128, kSlots = 3;
 constexpr int kQRegion = 128 * 128, kQTileBytes = 3 * kQRegion;  // 128 rows x 64 values; a CTA's half of a query tile
 constexpr int kKRegion = 64 * 128, kKSlot = 3 * kKRegion;        // 64 keys x 64 values

@@ -380,7 +380,11 @@ cudaError_t launch(const MlaProjParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// 16 tokens: the most that the mma.sync tile takes in one pass over the weights.
+// 16 tokens: the most that the mma.sync tile takes in one pass over the weights. Both forms in us a call, weights cold,
+// absorb_q / expand_out (mma.sync; tensor memory). 128 heads: 16 tokens 5.9 / 5.5; 7.7 / 6.8, 32 tokens 7.8 / 8.3;
+// 8.0 / 6.8, 64 tokens 11.8 / 12.0; 9.6 / 6.8, 128 tokens 19.8 / 19.4; 10.3 / 7.0. With few heads the crossover lies
+// higher (16 heads: 16 tokens 2.5 / 3.8; 4.8 / 5.1, 64 tokens 3.0 / 3.8; 6.6 / 5.2, 128 tokens 4.5 / 4.3; 6.9 / 5.3),
+// which the rule does not use.
 cudaError_t launch_mla_absorb_q(const MlaProjParams& p, cudaStream_t stream) {
   return p.num_tokens <= 16 ? launch<1, 4, 1, 2, 3, true>(p, stream) : launch_tc<true>(p, stream);
 }

@@ -10,15 +10,17 @@
 // Bounded by HBM: every element is read and written once. A thread stays at one
 // vector of a head and one token and walks that token's heads (or, with few tokens,
 // a share of them), a few rows' loads in flight; it forms its pairs' (cos, sin) once
-// for all of them, while the first rows load. The frequencies' 64-bit arithmetic runs
-// once per CTA: the part has few FP64 lanes. (With a table of all pairs' (cos, sin) in
+// for all of them, while the first rows load; the frequencies' fixed-point fractions are
+// formed once per CTA. (With a table of all pairs' (cos, sin) in
 // shared memory the two barriers and the table's latency held HBM at 50 %.) With 16-byte
 // vectors (bf16 / fp16: 8 elements) a half-layout item holds the vectors of both
 // partners, so a rotation never crosses threads and in-place calls are safe. Windows,
 // strides or addresses that do not fit 16-byte vectors take the one-element form.
 // Rotation is in fp32; the one rounding is the store to the tensor's type.
-// Measured: 32768 tokens x 16 heads x 192 bf16, 64 values turned, 68 us (5.9 TB/s, 87 %
-// of the measured copy rate); 64 tokens x 36 heads x 128, 4.4 us.
+// Measured: 32768 tokens x 16 heads x 192 bf16, 64 values turned, 69 us (5.8 TB/s, 86 %
+// of the measured copy rate); x 36 heads x 128, whole heads, interleaved 97 us (6.2 TB/s), half
+// layout 118 us (5.1); 16 heads x 128 fp32, half layout, 83 us (6.5); 64 tokens x 36 heads x 128,
+// 4.4 us. The one-element form: 2.6 TB/s (rows off 16-byte boundaries, or 20 of 80 values turned).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -5,8 +5,10 @@ Rotary positions (``rope_inv_freq``, ``rope``), the cache's write and read
 latent attention's projections and prompt pass (``mla_absorb_q``,
 ``mla_expand_out``, ``mla_absorbed_run``, ``mla_prefill``). As in ``_lib``:
 argument checks and marshalling only, no CPU path; a call runs on the current
-stream of its tensors' device unless ``stream`` is given (what the call
-allocates then belongs to that stream).
+stream of its tensors' device unless ``stream`` is given. What the call
+allocates then belongs to that stream, as under ``torch.cuda.stream``: a result
+that another stream reads needs its ``record_stream``, beside the wait. (``run``,
+``run_fp8``, ``sparse_run`` and ``mla_run`` allocate from the current stream.)
 """
 from __future__ import annotations
 
@@ -147,7 +149,9 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = 
                   original_positions: float = 4096.0, slow_turns: float = 1.0, fast_turns: float = 32.0,
                   device="cuda") -> Tuple[torch.Tensor, float]:
     """(inv_freq float64 [rot_dim / 2] on `device`, scale): radians a position of each pair, and the factor
-    that goes with them (0.1 ln(factor) + 1 for "by_parts", else 1). scaling: None, "linear", "base" or "by_parts"."""
+    that goes with them (0.1 ln(factor) + 1 for "by_parts", else 1). scaling: None, "linear", "base" or "by_parts".
+    "by_parts" ramps linearly in a pair's turns over original_positions; a model trained with a ramp over the pairs'
+    index needs frequencies of its own (any float64 [pairs] tensor will do)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}")
     freq = torch.empty(max(int(rot_dim), 2) // 2, dtype=torch.float64)
@@ -407,9 +411,11 @@ def mla_prefill(q: torch.Tensor, w_kv: torch.Tensor, kv_cache: torch.Tensor, blo
     """Latent attention for prompts and prompt chunks, expanded form: packed queries q [total, heads, 192] (sequence
     b's rows from cu_seqlens_q[b] on, rotary part turned) over the cached tokens that block_table [B, width] and
     cache_seqlens [B] list, the new ones among them. max_kv_tokens: a bound on the sum of cache_seqlens, which sizes
-    the workspace (default: what the block table can list). Rows of no sequence are 0 (lse -inf) in outputs that the call
-    allocates, and left as they were in given ones. Returns (out [total, heads, 128] bf16, lse [heads, total]
-    fp32 natural log, or None)."""
+    the workspace and how many heads a pass takes (default: what the block table can list; with a table far wider
+    than the lengths that costs memory and up to several times the time). Sequences past a bound that is too small
+    come back as 0 and -inf; bit 64 of ``_lib.gqa_paged_decode_device_error`` is all that tells. Rows of no sequence
+    are 0 (lse -inf) in outputs that the call allocates, and left as they were in given ones. Returns (out
+    [total, heads, 128] bf16, lse [heads, total] fp32 natural log, or None)."""
     index = _index("q", q)
     n, h, ts, hs = _query(q)
     w = _weights(w_kv, h, index)
