@@ -7,7 +7,8 @@ loaded on first use, and every call fails loudly if it is missing.
 ``sparse_run(q, k_cache, v_cache, logical_indices, block_table, token_to_req)``
 is the selected-token variant over a block table of any page size,
 ``run_fp8`` reads an FP8 (e4m3, per-128 fp32 scale) cache, ``mla_run`` is
-the dense MLA decode over one 576-value latent KV head, and
+the dense MLA decode over one 576-value latent KV head (``mla_workspace_size``:
+the bytes of a workspace of the caller's for it), and
 ``kv_append`` stores new tokens' K/V rows into the page pool.
 
 What a serving step runs around them (``serving``): ``rope_inv_freq`` and
@@ -17,10 +18,11 @@ in a bf16 or FP8 cache), ``kv_append_fp8``, ``kv_read_fp8`` and
 ``mla_absorb_q``, ``mla_expand_out``, ``mla_absorbed_run`` (new tokens) and
 ``mla_prefill`` (prompts).
 """
-from ._lib import GqaError, kv_append, mla_run, run, run_checked, run_fp8, sparse_run  # noqa: F401
+from ._lib import (GqaError, kv_append, mla_run, mla_workspace_size, run, run_checked, run_fp8,  # noqa: F401
+                   sparse_run)
 from .serving import (kv_append_fp8, kv_read_fp8, mla_absorb_q, mla_absorbed_run, mla_expand_out,  # noqa: F401
                       mla_kv_append, mla_prefill, rope, rope_inv_freq, rope_kv_append)
 
 __all__ = ["GqaError", "kv_append", "kv_append_fp8", "kv_read_fp8", "mla_absorb_q", "mla_absorbed_run",
-           "mla_expand_out", "mla_kv_append", "mla_prefill", "mla_run", "rope", "rope_inv_freq", "rope_kv_append", "run",
-           "run_checked", "run_fp8", "sparse_run"]
+           "mla_expand_out", "mla_kv_append", "mla_prefill", "mla_run", "mla_workspace_size", "rope", "rope_inv_freq",
+           "rope_kv_append", "run", "run_checked", "run_fp8", "sparse_run"]
