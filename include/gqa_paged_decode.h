@@ -582,6 +582,129 @@ int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, 
                          int num_blocks, int page_table_width, int64_t max_kv_tokens, int64_t q_token_stride,
                          int64_t q_head_stride, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 
+/*
+ * ---- The decode over long and shared contexts: shared prefixes, selected blocks, accumulated weights, eviction.
+ *
+ * The calls of this section are asynchronous on `stream`, allocate nothing and
+ * keep nothing between calls; they can be captured into a graph. A workspace is
+ * device memory of the size that the call's _ws_size function gives (0:
+ * arguments out of range, or no supported device) under the present tuning,
+ * 256-byte aligned, one per call in flight, not initialised; a smaller one is
+ * GQA_ERR_WORKSPACE. Shapes are those of gqa_paged_decode (32 query heads over 4
+ * KV heads g of dimension 128). Offsets ([n + 1] int32, non-decreasing) are not
+ * checked; entries past the stated count of what they point into are cut to it.
+ * A page or block outside the pool is left out, wherever a table lists it.
+ * The tuning's CTA counts and tiers apply to the decode inside, not its kernel
+ * choice. The caches are bf16, or where cache_format is an argument also FP8
+ * (GQA_CACHE_*; as in gqa_paged_decode_fp8). lse is in base 2 as there.
+ */
+
+/*
+ * Decode of a batch whose sequences share prefixes. Sequence b of group g
+ * (group_indptr[g] <= b < group_indptr[g + 1]; the groups' ranges do not
+ * overlap) reads the pages prefix_indices[prefix_indptr[g] ..
+ * prefix_indptr[g + 1]), then its own kv_indices[kv_indptr[b] ..
+ * kv_indptr[b + 1]); a sequence of no group reads its own alone. The result is
+ * gqa_paged_decode's on the two lists joined; a prefix is read once for all
+ * sequences of its group. Prefixes, groups and own lists may be empty; a
+ * sequence that reads nothing gives 0 and -inf.
+ *
+ * q, out [batch][32][128] bf16, 16-byte aligned; lse [batch][32] fp32 or NULL;
+ * prefix_count and index_count: entries of prefix_indices and kv_indices.
+ * batch and groups up to 2^20; batch == 0 returns 0 without launching.
+ */
+size_t gqa_shared_paged_decode_ws_size(int batch, int cache_format);
+int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_indptr,
+                            const int32_t* prefix_indices, const int32_t* group_indptr, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, float sm_scale, void* out, float* lse, int batch, int groups,
+                            int prefix_count, int index_count, int num_pages, int cache_format, void* workspace,
+                            size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * Bounds of a block-table cache's blocks, for gqa_block_select. For request r
+ * and every block i of its table that holds a token t of first[r] <= t <
+ * lens[r] (first NULL: 0), with block = block_table[r][i]:
+ *   bounds[block][0][g][d] = max over the block's tokens t < lens[r] of k_cache[block][t % page_size][g][d],
+ *   bounds[block][1][g][d] = min of the same
+ * (exact; a NaN makes both NaN). Other blocks keep what they have. lens are cut
+ * to page_table_width * page_size. A block that several requests list must
+ * hold the same tokens for all that renew it in one call.
+ *
+ * k_cache [num_blocks][page_size][4][128] bf16, bounds [num_blocks][2][4][128]
+ * bf16, both 16-byte aligned; block_table [requests][page_table_width].
+ */
+int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_table, const int32_t* lens,
+                     const int32_t* first, int requests, int page_size, int num_blocks, int page_table_width,
+                     struct CUstream_st* stream);
+
+/*
+ * Chooses, for every query row and KV head g, `top` of the blocks that hold the
+ * row's tokens t < lens[row] of request token_to_req[row] (a row of no request
+ * has none): the first keep_first and the last keep_last of them, then those of
+ * the largest
+ *   score = max over the 8 query heads h of g of sum_d max(q[h][d], 0) bounds[block][0][g][d] + min(q[h][d], 0) bounds[block][1][g][d],
+ * which no query head's product with a key of the block passes. A score that is
+ * no finite fp32 number counts as the largest; equal scores go to the lower
+ * block. The scores decide as if formed with 2^-44 of their terms' size.
+ * blocks[row][g][0 .. top) are the chosen blocks' numbers in the table, ascending,
+ * then -1. keep_first + keep_last <= top.
+ *
+ * q [rows][32][128] bf16, 16-byte aligned; token_to_req, lens [rows]; blocks
+ * [rows][4][top] int32. rows == 0 returns 0 without launching.
+ */
+size_t gqa_block_select_ws_size(int rows, int page_table_width);
+int gqa_block_select(const void* q, const void* bounds, const int32_t* block_table, const int32_t* token_to_req,
+                     const int32_t* lens, int32_t* blocks, int rows, int requests, int page_size, int num_blocks,
+                     int page_table_width, int top, int keep_first, int keep_last, void* workspace, size_t workspace_bytes,
+                     struct CUstream_st* stream);
+
+/*
+ * Decode over chosen blocks: gqa_sparse_paged_decode with a list a KV head.
+ * Query row `row` attends, with the query heads of KV head g, to the tokens t <
+ * lens[row] of the blocks blocks[row][g][0 .. top) (numbers in the table of
+ * request token_to_req[row]; others, for example -1, are left out; one listed
+ * twice counts twice). A row and head with no token gives 0 and -inf.
+ *
+ * q, out [rows][32][128] bf16, k_cache, v_cache [num_blocks][page_size][4][128]
+ * bf16, 16-byte aligned; lse [rows][32] fp32 or NULL; rows * top * page_size
+ * below 2^31. rows == 0 returns 0 without launching.
+ */
+size_t gqa_block_sparse_decode_ws_size(int rows, int top, int page_size);
+int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* blocks,
+                            const int32_t* block_table, const int32_t* token_to_req, const int32_t* lens, float sm_scale,
+                            void* out, float* lse, int rows, int requests, int top, int page_size, int num_blocks,
+                            int page_table_width, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * gqa_paged_decode that also accumulates how much attention each token got:
+ *   weights_out[b][j] = decay * weights[b][j] + sum over the 32 query heads of exp(s_j) / sum_i exp(s_i)
+ * for the j-th token of sequence b, fp32 [batch][width]; a decay of 0 does not
+ * read weights there. Places past a sequence's length are copied; tokens past
+ * width count in the decode alone. weights_out may be weights itself, and must
+ * not overlap it otherwise. lse is required. index_count: entries of kv_indices.
+ */
+size_t gqa_paged_decode_weighted_ws_size(int index_count, int cache_format);
+int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_indptr,
+                              const int32_t* kv_indices, float sm_scale, const float* weights, float decay,
+                              float* weights_out, void* out, float* lse, int batch, int width, int index_count,
+                              int num_pages, int cache_format, void* workspace, size_t workspace_bytes,
+                              struct CUstream_st* stream);
+
+/*
+ * Cuts every sequence back to `budget` tokens. One of more than that keeps its
+ * first keep_first and last keep_last tokens and, of those between, the ones of
+ * the largest weights[b][j] (equal ones: the lower j; NaN above all; tokens past
+ * width have weight 0), in their order. keep_first + keep_last <= budget.
+ * new_indptr [batch + 1], new_indices [index_count]: the tokens kept, as a page
+ * table; freed_indptr, freed: the others' pages in the same form; entries of
+ * new_indices and freed behind the last sequence's are -1. weights_out
+ * [batch][width]: the kept tokens' weights at their new places, then zeros. No
+ * output may overlap an input or another output.
+ */
+int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* kv_indices, int budget, int keep_first,
+                 int keep_last, float* weights_out, int32_t* new_indptr, int32_t* new_indices, int32_t* freed_indptr,
+                 int32_t* freed, int batch, int width, int index_count, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,12 +17,20 @@ in a bf16 or FP8 cache), ``kv_append_fp8``, ``kv_read_fp8`` and
 ``mla_kv_append`` (the caches' write and read), and latent attention's
 ``mla_absorb_q``, ``mla_expand_out``, ``mla_absorbed_run`` (new tokens) and
 ``mla_prefill`` (prompts).
+
+The decode over long and shared contexts (``context``): ``shared_run`` (a batch
+that shares prefixes), ``block_bounds``, ``block_select`` and
+``block_sparse_run`` (attention over blocks that a cheap score selects),
+``run_weighted`` and ``kv_evict`` (attention weights accumulated, and the
+eviction by them).
 """
 from ._lib import (GqaError, kv_append, mla_run, mla_workspace_size, run, run_checked, run_fp8,  # noqa: F401
                    sparse_run)
+from .context import block_bounds, block_select, block_sparse_run, kv_evict, run_weighted, shared_run  # noqa: F401
 from .serving import (kv_append_fp8, kv_read_fp8, mla_absorb_q, mla_absorbed_run, mla_expand_out,  # noqa: F401
                       mla_kv_append, mla_prefill, rope, rope_inv_freq, rope_kv_append)
 
-__all__ = ["GqaError", "kv_append", "kv_append_fp8", "kv_read_fp8", "mla_absorb_q", "mla_absorbed_run",
+__all__ = ["GqaError", "block_bounds", "block_select", "block_sparse_run", "kv_append", "kv_append_fp8", "kv_evict",
+           "kv_read_fp8", "mla_absorb_q", "mla_absorbed_run",
            "mla_expand_out", "mla_kv_append", "mla_prefill", "mla_run", "mla_workspace_size", "rope", "rope_inv_freq",
-           "rope_kv_append", "run", "run_checked", "run_fp8", "sparse_run"]
+           "rope_kv_append", "run", "run_checked", "run_fp8", "run_weighted", "shared_run", "sparse_run"]

@@ -22,7 +22,8 @@ LIB_NAME = "libgqa_paged_decode.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["gqa_decode_lsu.cu", "gqa_decode_tma.cu", "gqa_merge.cu", "gqa_api.cu", "gqa_noalloc.cu", "gqa_kv_append.cu",
            "gqa_sparse.cu", "gqa_mla.cu", "gqa_mla_tc.cu", "gqa_rope.cu", "gqa_rope_append.cu", "gqa_mla_proj.cu",
-           "gqa_mla_prefill.cu", "gqa_serving_api.cu"]
+           "gqa_mla_prefill.cu", "gqa_serving_api.cu", "gqa_shared.cu", "gqa_blocks.cu", "gqa_weights.cu",
+           "gqa_context_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

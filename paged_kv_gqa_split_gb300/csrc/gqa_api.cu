@@ -508,6 +508,21 @@ int decode_in_scratch(const void* q, const void* k_cache, const void* v_cache, c
              false, 0, nullptr, true);
 }
 
+int decode_setup(bool fp8, DecodeSetup* setup) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0;
+  DeviceState* st = nullptr;
+  const int rc = current_device(&dev, &st);
+  if (rc != GQA_OK) return rc;
+  Tuning tune = g_tune;  // its CTA counts and tiers, with the one variant that the forms have
+  tune.kernel = fp8 ? KernelChoice{kGatherLsuF8, 4, 16, 2} : KernelChoice{kGatherLsu, 4, 16, 2};
+  setup->plan = plan_config(*st, tune);
+  setup->sm_count = st->sm_count;
+  setup->epoch = (g_epoch.fetch_add(1) % ((1ull << 40) - 1)) + 1;
+  setup->wait_limit_ns = g_wait_limit_ns > 0 ? g_wait_limit_ns : kDefaultWaitLimitNs;
+  return device_error_word(&setup->err) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+}
+
 int current_device_sms(int* sm_count, unsigned long long* wait_limit_ns) {
   std::lock_guard<std::mutex> lock(g_mu);
   int dev = 0;

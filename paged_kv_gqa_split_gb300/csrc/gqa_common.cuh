@@ -155,12 +155,20 @@ __device__ __forceinline__ void load_q_frags(uint32_t (&qf)[16], const __nv_bflo
   }
 }
 
+// Scores of tokens r and r + 8 of a sub-tile for heads 2c and 2c + 1.
+__device__ __forceinline__ void store_scores(float* scores, const float (&s)[4], int r, int c, int cnt) {
+  if (r < cnt) *reinterpret_cast<float2*>(scores + r * kGroup + 2 * c) = make_float2(s[0], s[1]);
+  if (r + 8 < cnt) *reinterpret_cast<float2*>(scores + (r + 8) * kGroup + 2 * c) = make_float2(s[2], s[3]);
+}
+
 // One 16-token sub-tile. k_addr / v_addr: this lane's ldmatrix row address for
 // dims 0..15 of the sub-tile's K and V rows (row pitch `pitch`, dims contiguous).
 // Tokens whose bit in `valid` is clear are masked out (their rows must hold
-// finite values); a sub-tile may have none valid.
+// finite values); a sub-tile may have none valid. STORE: the scores of the first
+// cnt tokens (base 2, -inf where masked out) go to scores[token][8 heads].
+template <bool STORE = false>
 __device__ __forceinline__ void attend_subtile(HeadState& st, uint32_t k_addr, uint32_t v_addr, unsigned valid,
-                                               float scale_log2, int lane) {
+                                               float scale_log2, int lane, float* scores = nullptr, int cnt = 0) {
   const int r = lane >> 2;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -174,6 +182,7 @@ __device__ __forceinline__ void attend_subtile(HeadState& st, uint32_t k_addr, u
   s[1] = v_lo ? s[1] * scale_log2 : -INFINITY;
   s[2] = v_hi ? s[2] * scale_log2 : -INFINITY;
   s[3] = v_hi ? s[3] * scale_log2 : -INFINITY;
+  if constexpr (STORE) store_scores(scores, s, r, lane & 3, cnt);
   float mx0 = fmaxf(s[0], s[2]);
   float mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
@@ -235,9 +244,11 @@ __device__ __forceinline__ float pow2_recip(float x) { return __uint_as_float((2
 // token's V scale over st.cv, a running power of two no smaller than any V
 // scale seen in the piece, so the f16 P operand stays in [0, 1]; acc then
 // holds O * l / cv, and l sums the plain probabilities.
+template <bool STORE = false>
 __device__ __forceinline__ void attend_subtile_f8(HeadState& st, uint32_t k_addr, uint32_t v_addr, unsigned valid,
                                                   float scale_log2, float sk_lo, float sk_hi, float sv_lo,
-                                                  float sv_hi, int lane, int k_pitch) {
+                                                  float sv_hi, int lane, int k_pitch, float* scores = nullptr,
+                                                  int cnt = 0) {
   const int r = lane >> 2;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -258,6 +269,7 @@ __device__ __forceinline__ void attend_subtile_f8(HeadState& st, uint32_t k_addr
   s[1] = v_lo ? s[1] * c_lo : -INFINITY;
   s[2] = v_hi ? s[2] * c_hi : -INFINITY;
   s[3] = v_hi ? s[3] * c_hi : -INFINITY;
+  if constexpr (STORE) store_scores(scores, s, r, lane & 3, cnt);
   float mx0 = fmaxf(s[0], s[2]);
   float mx1 = fmaxf(s[1], s[3]);
   float vm = fmaxf(v_lo ? fabsf(sv_lo) : 0.f, v_hi ? fabsf(sv_hi) : 0.f);

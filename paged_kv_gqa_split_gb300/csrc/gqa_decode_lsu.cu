@@ -439,7 +439,12 @@ __device__ __noinline__ void install_call_counters(const DecodeParams& p, int w,
 // the 4 KV heads, then their fp32 scales.
 // CC: the contractions on the CUDA cores (attend_subtile_cc) instead of
 // mma.sync, a variant kept for comparing the two.
-template <int NG, int D, bool SP, bool F8 = false, bool CC = false, int TT = 16>
+// FORM: what the operators for long and shared contexts ask of the decode besides (kForm* of gqa_kernels.h;
+// static grid, NG = 4). kFormParts: whole sequences leave a partial too (slot p.whole_base + sequence), for a
+// later kernel to join with others. kFormHeads (SP): every KV head has slots of its own, p.sparse_total apart.
+// kFormScores: the scaled scores are stored, [4][p.index_count][8] by position in kv_indices. kFormParts and
+// kFormScores leave tokens of pages outside [0, num_pages_check) out, and read no more than index_count indices.
+template <int NG, int D, bool SP, bool F8 = false, bool CC = false, int TT = 16, int FORM = kFormPlain>
 __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 / NG)
     gqa_decode_lsu_kernel(const DecodeParams p) {
   using C = LsuCfg<NG, D, F8, TT>;
@@ -467,7 +472,9 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
   // kv_indptr[B], the first round of the kv_indptr search and (one-wave mode)
   // this lane's empty-sequence check go out together: one round trip
   const int pre = (SP || F8) ? 0 : first_search_round(p.kv_indptr, B, lane);
-  const int T = SP ? p.sparse_total : __ldg(p.kv_indptr + B);
+  const int T = SP ? p.sparse_total : (FORM != kFormPlain ? max(0, min(__ldg(p.kv_indptr + B), p.index_count)) : __ldg(p.kv_indptr + B));
+  static_assert(FORM == kFormPlain || (NG == 4 && !CC && TT == 16 && SP == (FORM == kFormHeads)), "forms compiled in");
+  constexpr bool kLeaveOut = FORM == kFormParts || FORM == kFormScores;
   if (!SP && one_wave) {
     for (int b0 = (blockIdx.x * NG + w) * 32; b0 < B; b0 += gridDim.x * NG * 32) {
       const int b = b0 + lane;
@@ -497,7 +504,8 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
   int ib = 0;               // page-id ring holds tokens [ib, ib + 256)
 
   auto request_ids = [&](int pos) {  // page id of token pos into its ring slot (zero past the end)
-    cp_async_4(ids_base + (pos & (C::kIdsRing - 1)) * 4, p.kv_indices + min(pos, T - 1), pos < T ? 4u : 0u);
+    const int* ids_of = FORM == kFormHeads ? p.kv_indices + static_cast<int64_t>(w) * T : p.kv_indices;
+    cp_async_4(ids_base + (pos & (C::kIdsRing - 1)) * 4, ids_of + min(pos, T - 1), pos < T ? 4u : 0u);
   };
 
   // Opens the head-group segment at u_next of the current range. `first`:
@@ -638,14 +646,18 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
       const int pc = lane & 15;  // 16-byte column of the 256-byte head row
       // tokens that enter the softmax: the first cnt, less (sparse mode) masked columns
       unsigned mask = tl.cnt >= 32 ? 0xffffffffu : ((1u << tl.cnt) - 1u);
+      if constexpr (kLeaveOut) {
+        const int pg = ids[(tl.tt + lane) & (C::kIdsRing - 1)];
+        mask &= __ballot_sync(0xffffffffu, static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages_check));
+      }
       if constexpr (F8) {
         // kTile tokens x 8 16-byte chunks of the 128-byte e4m3 head row, for K and V
 #pragma unroll
         for (int i = 0; i < C::kTile / 4; ++i) {
           const int tok = 4 * i + (lane >> 3), ch = lane & 7;
-          bool valid = tok < tl.cnt;
+          bool valid = kLeaveOut ? (mask >> tok) & 1u : tok < tl.cnt;
           int pg = valid ? ids[(tl.tt + tok) & (C::kIdsRing - 1)] : 0;
-          if (valid && p.num_pages_check > 0 &&
+          if (!kLeaveOut && valid && p.num_pages_check > 0 &&
               static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages_check)) {
             atomicOr(p.err, kErrBadPage);
             valid = false;
@@ -658,9 +670,9 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
         }
         {  // the per-token scales of this KV head: 16 tokens: lanes 0-15 K, 16-31 V; 32: K and V of token lane
           const int tok = C::kTile == 16 ? (lane & 15) : lane;
-          bool valid = tok < tl.cnt;
+          bool valid = kLeaveOut ? (mask >> tok) & 1u : tok < tl.cnt;
           int pg = valid ? ids[(tl.tt + tok) & (C::kIdsRing - 1)] : 0;
-          if (valid && p.num_pages_check > 0 &&
+          if (!kLeaveOut && valid && p.num_pages_check > 0 &&
               static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages_check)) {
             valid = false;
             pg = 0;
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
 #pragma unroll
       for (int i = 0; i < (F8 ? 0 : 8); ++i) {
         const int tok = 2 * i + (lane >> 4);
-        bool valid = tok < tl.cnt;
+        bool valid = kLeaveOut ? (mask >> tok) & 1u : tok < tl.cnt;
         int pg = valid ? ids[(tl.tt + tok) & (C::kIdsRing - 1)] : 0;
         if (SP) {
           if (pg < 0) {
@@ -689,7 +701,7 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
           const unsigned bal = __ballot_sync(0xffffffffu, valid);  // lanes 0-15: token 2i, 16-31: 2i + 1
           mask = (mask & ~(3u << (2 * i))) | ((bal & 1u) << (2 * i)) | (((bal >> 16) & 1u) << (2 * i + 1));
         }
-        if (valid && p.num_pages_check > 0 && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages_check)) {
+        if (!kLeaveOut && valid && p.num_pages_check > 0 && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages_check)) {
           atomicOr(p.err, kErrBadPage);
           valid = false;
           pg = 0;
@@ -713,7 +725,8 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
         }
       }
       if (lane == 0) {
-        st_shared_v4(sb + C::kHdrOff, tl.b, tl.cnt, flags, tl.hg);
+        // one head group in all: the form that stores scores has the tile's first position there
+        st_shared_v4(sb + C::kHdrOff, tl.b, tl.cnt, flags, FORM == kFormScores ? tl.tt : tl.hg);
         if constexpr (F8)  // the FP8 variants run the static grid: the virtual CTA is the CTA
           st_shared_v4(sb + C::kHdrOff + 16, tl.si.S, tl.si.first_cta, tl.si.first_slot, static_cast<int>(mask));
         else
@@ -767,6 +780,11 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
       tok_mask &= 0xffff;
     }
     if (flags & F_DONE) break;
+    float* tile_scores = nullptr;
+    if constexpr (FORM == kFormScores) {
+      tile_scores = p.scores + (static_cast<int64_t>(w) * p.index_count + thg) * kGroup;
+      thg = 0;
+    }
     const int h0 = (thg * NG + w) * kGroup;
     if (flags & F_QLOAD) {
       if (flags & F_QREG) {
@@ -803,12 +821,18 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
       const int r = lane >> 2;
       const float sk_lo = ld_shared_f32(sb + C::kSkOff + r * 4), sk_hi = ld_shared_f32(sb + C::kSkOff + (r + 8) * 4);
       const float sv_lo = ld_shared_f32(sb + C::kSvOff + r * 4), sv_hi = ld_shared_f32(sb + C::kSvOff + (r + 8) * 4);
-      attend_subtile_f8(st, sb + k_lane, sb + v_lane, static_cast<unsigned>(tok_mask), p.scale_log2, sk_lo, sk_hi,
-                        sv_lo, sv_hi, lane, C::kK8Pitch);
+      attend_subtile_f8<FORM == kFormScores>(st, sb + k_lane, sb + v_lane, static_cast<unsigned>(tok_mask), p.scale_log2,
+                                             sk_lo, sk_hi, sv_lo, sv_hi, lane, C::kK8Pitch, tile_scores, cnt);
     } else {
-      attend_subtile(st, sb + k_lane, sb + v_lane, static_cast<unsigned>(tok_mask), p.scale_log2, lane);
+      attend_subtile<FORM == kFormScores>(st, sb + k_lane, sb + v_lane, static_cast<unsigned>(tok_mask), p.scale_log2, lane,
+                                          tile_scores, cnt);
     }
-    if (flags & F_END) {
+    if constexpr (FORM == kFormParts) {
+      if (flags & F_END) {
+        const int64_t sid = (flags & F_FINAL) ? p.whole_base + hb : slot_id(tile_cta, (flags & F_SLOT1) ? 1 : 0);
+        finish_piece<NG, F8>(st, false, hb, h0, sid, w, si, p, lane, F8 ? st.cv : 1.f);
+      }
+    } else if (flags & F_END) {
       bool owes;
       if constexpr (CC)
         owes = finish_piece_cc<NG>(cs, (flags & F_FINAL) != 0, hb, h0, slot_id(tile_cta, (flags & F_SLOT1) ? 1 : 0), w,
@@ -864,15 +888,15 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
 // launch: kLaunchPlain, kLaunchPdl (a programmatic dependent of the kernel
 // before it on the stream) or kLaunchCooperative (the one-wave mode: every CTA
 // resident at once, which the in-kernel merge's waits rely on).
-template <int NG, int D, bool SP, bool F8 = false, bool CC = false, int TT = 16>
+template <int NG, int D, bool SP, bool F8 = false, bool CC = false, int TT = 16, int FORM = kFormPlain>
 static cudaError_t launch_lsu(const DecodeParams& p, int num_ctas, cudaStream_t stream, int launch) {
   using C = LsuCfg<NG, D, F8, TT>;
   static std::atomic<int> configured[kMaxDevices];
   const cudaError_t e = set_smem_limit_once(
-      configured, reinterpret_cast<const void*>(gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT>), C::kSmemBytes);
+      configured, reinterpret_cast<const void*>(gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT, FORM>), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if (launch == kLaunchPlain) {
-    gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT><<<num_ctas, C::kThreads, C::kSmemBytes, stream>>>(p);
+    gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT, FORM><<<num_ctas, C::kThreads, C::kSmemBytes, stream>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -890,7 +914,7 @@ static cudaError_t launch_lsu(const DecodeParams& p, int num_ctas, cudaStream_t 
   }
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT>, p);
+  return cudaLaunchKernelEx(&cfg, gqa_decode_lsu_kernel<NG, D, SP, F8, CC, TT, FORM>, p);
 }
 
 // CTAs of a variant that the current device holds at once (0 if it cannot be
@@ -939,6 +963,17 @@ cudaError_t launch_decode_lsu(int ng, int stages, const DecodeParams& p, int num
 // Selected-token mode: one variant, 4 KV heads per CTA and a 2-deep ring.
 cudaError_t launch_decode_lsu_sparse(const DecodeParams& p, int num_ctas, cudaStream_t stream, int launch) {
   return launch_lsu<4, 2, true>(p, num_ctas, stream, launch);
+}
+
+cudaError_t launch_decode_lsu_form(int form, bool fp8, const DecodeParams& p, int num_ctas, cudaStream_t stream, int launch) {
+  if (form == kFormHeads && !fp8) return launch_lsu<4, 2, true, false, false, 16, kFormHeads>(p, num_ctas, stream, launch);
+  if (form == kFormParts)
+    return fp8 ? launch_lsu<4, 2, false, true, false, 16, kFormParts>(p, num_ctas, stream, launch)
+               : launch_lsu<4, 2, false, false, false, 16, kFormParts>(p, num_ctas, stream, launch);
+  if (form == kFormScores)
+    return fp8 ? launch_lsu<4, 2, false, true, false, 16, kFormScores>(p, num_ctas, stream, launch)
+               : launch_lsu<4, 2, false, false, false, 16, kFormScores>(p, num_ctas, stream, launch);
+  return cudaErrorInvalidValue;
 }
 
 // FP8-cache variants: 4 KV heads per CTA; 16-token stages in a ring of 2, 3

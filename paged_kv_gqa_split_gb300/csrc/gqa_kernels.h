@@ -47,7 +47,14 @@ struct DecodeParams {
   unsigned long long wait_limit_ns;  // give-up limit of a bounded wait (TMA variant; in-kernel merge)
   int inline_merge;             // one-wave mode: grid = tier-1 CTAs, tier 2 taken from `grab`, merge in-kernel
   unsigned long long* grab;     // [NG] one-wave mode: tier-2 range counters (epoch-tagged)
+  // forms for long and shared contexts (kForm*)
+  int index_count;              // entries of kv_indices
+  int64_t whole_base;           // kFormParts: partial slot of sequence 0 when it is whole
+  float* scores;                // kFormScores: [4][index_count][8], base 2
 };
+
+// Forms of the decode kernel (gqa_decode_lsu.cu, where they are described).
+enum : int { kFormPlain = 0, kFormParts = 1, kFormHeads = 2, kFormScores = 3 };
 
 // One-wave mode: a warp walks at most this many ranges (its tier-1 range and
 // tier-2 ranges); the host uses the mode only when P2 <= (this - 1) * P1.
@@ -91,6 +98,17 @@ struct MergeParams {
 int decode_in_scratch(const void* q, const void* k_cache, const void* v_cache, const int* kv_indptr,
                       const int* kv_indices, float sm_scale, void* out, float* lse, int batch, cudaStream_t stream,
                       void* scratch, size_t scratch_bytes);
+
+// What a call of a decode form needs besides its own arguments (gqa_api.cu): the plan of the default variant under the
+// present tuning, and the call's epoch. Returns a GQA_* code.
+struct DecodeSetup {
+  PlanConfig plan;
+  int sm_count;
+  unsigned long long epoch;
+  unsigned long long wait_limit_ns;
+  int* err;
+};
+int decode_setup(bool fp8, DecodeSetup* setup);
 
 // Dense MLA decode (gqa_mla.cu): one latent KV head of 576 values per token,
 // 512 of them also V; `rows` = s_q * h_q query rows per sequence, a multiple
@@ -163,6 +181,8 @@ cudaError_t launch_decode_lsu(int ng, int stages, const DecodeParams& p, int num
                               int launch);
 // The selected-token variant (p.sparse_topk > 0): 4 KV heads per CTA, 2 stages.
 cudaError_t launch_decode_lsu_sparse(const DecodeParams& p, int num_ctas, cudaStream_t stream, int launch);
+// A form other than kFormPlain: 4 KV heads per CTA, 2 stages (kFormHeads: bf16 caches only).
+cudaError_t launch_decode_lsu_form(int form, bool fp8, const DecodeParams& p, int num_ctas, cudaStream_t stream, int launch);
 // CTAs of a cp.async variant (sparse: the selected-token one) that the current
 // device holds at once; 0 for the TMA variant or if unknown.
 int decode_coresident_ctas(const KernelChoice& k, bool sparse);
@@ -311,6 +331,79 @@ struct MlaPrefillParams {
   int head_group;      // heads whose CTAs run together
   int split;           // units may be split over their keys
 };
+// ------------------------------- decode forms for long and shared contexts
+struct SharedParams {  // gqa_shared.cu
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int* prefix_indptr;   // [groups + 1]
+  const int* prefix_indices;  // [prefix_count]
+  const int* group_indptr;    // [groups + 1]
+  const int* kv_indptr;       // [batch + 1]
+  void* out;
+  float* lse;                 // or NULL
+  float* pre_o;               // parts of the prefixes: [batch][4][128 dims][8 heads], LSE [batch][4][8]
+  float* pre_lse;
+  const float* own_o;         // parts of the own tokens (DecodeParams::part_o, part_lse)
+  const float* own_lse;
+  int64_t whole_base;
+  PlanConfig plan;
+  float scale_log2;
+  int batch, groups, prefix_count, index_count, num_pages, fp8;
+  int* err;
+};
+cudaError_t launch_shared(const SharedParams& p, const DecodeParams& own, cudaStream_t stream);
+
+struct BoundsParams {  // gqa_blocks.cu
+  const void* k_cache;     // [num_blocks][page_size][4][128]
+  void* bounds;            // [num_blocks][2][4][128]
+  const int* block_table;  // [requests][width]
+  const int* lens;         // [requests]
+  const int* first;        // [requests] or NULL: 0
+  int requests, page_size, num_blocks, width;
+};
+cudaError_t launch_block_bounds(const BoundsParams& p, int sm_count, cudaStream_t stream);
+
+struct BlockParams {  // gqa_blocks.cu
+  const void* q;            // [rows][32][128]
+  const void* bounds;
+  const int* block_table;   // [requests][width]
+  const int* token_to_req;  // [rows]
+  const int* lens;          // [rows]
+  int* blocks;              // [rows][4][top]
+  float* scores;            // workspace: [rows][4][width] scores, their error bounds (-1: no block), scores formed again
+  float* errors;
+  float2* again;
+  int* slots;               // [4][rows * top * page_size]
+  int rows, requests, page_size, num_blocks, width, top, keep_first, keep_last;
+};
+cudaError_t launch_block_select(const BlockParams& p, cudaStream_t stream);
+cudaError_t launch_block_slots(const BlockParams& p, int sm_count, cudaStream_t stream);
+
+struct WeighParams {  // gqa_weights.cu
+  const float* scores;  // [4][index_count][8]
+  const float* lse;     // [batch][32]
+  const float* weights; // [batch][width]
+  float* out;           // the same, or `weights` itself
+  const int* kv_indptr;
+  float decay;
+  int batch, width, index_count;
+};
+cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream);
+
+struct EvictParams {  // gqa_weights.cu
+  const float* weights;  // [batch][width]
+  const int* kv_indptr;
+  const int* kv_indices;
+  float* weights_out;
+  int* new_indptr;   // [batch + 1]
+  int* new_indices;  // [index_count]
+  int* freed_indptr;
+  int* freed;
+  int budget, keep_first, keep_last, batch, width, index_count;
+};
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+
 // A tensor map of 2 or 3 dimensions (sizes and boxes from the contiguous one on, `pitch` bytes between steps of the
 // others, 128-byte swizzle). False if the driver call is missing or refuses.
 bool tc_encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const int64_t* size,
