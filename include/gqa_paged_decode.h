@@ -613,7 +613,7 @@ int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, 
  * prefix_count and index_count: entries of prefix_indices and kv_indices.
  * batch and groups up to 2^20; batch == 0 returns 0 without launching.
  */
-size_t gqa_shared_paged_decode_ws_size(int batch, int cache_format);
+size_t gqa_shared_paged_decode_ws_size(int batch, int groups, int cache_format);
 int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_indptr,
                             const int32_t* prefix_indices, const int32_t* group_indptr, const int32_t* kv_indptr,
                             const int32_t* kv_indices, float sm_scale, void* out, float* lse, int batch, int groups,

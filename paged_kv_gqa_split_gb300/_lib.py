@@ -73,7 +73,7 @@ _SIGNATURES = {
                         [ctypes.c_int64] * 3 + [_vp, ctypes.c_size_t, _vp]),
     "gqa_mla_prefill_fill": (ctypes.c_int, [_vp] * 6 + [ctypes.c_float] + [ctypes.c_int] * 2 + [_vp, _vp] +
                              [ctypes.c_int] * 6 + [ctypes.c_int64] * 3 + [_vp, ctypes.c_size_t, _vp]),
-    "gqa_shared_paged_decode_ws_size": (ctypes.c_size_t, [ctypes.c_int] * 2),
+    "gqa_shared_paged_decode_ws_size": (ctypes.c_size_t, [ctypes.c_int] * 3),
     "gqa_shared_paged_decode": (ctypes.c_int, [_vp] * 8 + [ctypes.c_float, _vp, _vp] + [ctypes.c_int] * 6 +
                                 [_vp, ctypes.c_size_t, _vp]),
     "gqa_block_bounds": (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 4 + [_vp]),

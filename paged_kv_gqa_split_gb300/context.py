@@ -98,7 +98,7 @@ def shared_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pr
     out, lse = _results(index, n, out, lse, True, stream)
     if n == 0:
         return out, lse
-    ws, size = _workspace(index, workspace, stream, "gqa_shared_paged_decode_ws_size", n, fmt)
+    ws, size = _workspace(index, workspace, stream, "gqa_shared_paged_decode_ws_size", n, groups, fmt)
     _call("gqa_shared_paged_decode", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           prefix_indptr.data_ptr(), prefix_indices.data_ptr(), group_indptr.data_ptr(), kv_indptr.data_ptr(),
           kv_indices.data_ptr(), HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), lse.data_ptr(), n,

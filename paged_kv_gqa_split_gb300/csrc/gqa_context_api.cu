@@ -70,11 +70,12 @@ gqa::MergeParams merge_params(const gqa::DecodeParams& d) {
 }
 
 struct SharedSpace {
-  size_t pre_o, pre_lse;
+  size_t start, pre_o, pre_lse;
   DecodeSpace own;
-  SharedSpace(const gqa::PlanConfig& plan, int batch)
-      : pre_o(0), pre_lse(round256(static_cast<size_t>(batch) * gqa::kKvHeads * kPartBytes)),
-        own(plan, batch, pre_lse + round256(static_cast<size_t>(batch) * gqa::kKvHeads * gqa::kGroup * sizeof(float))) {}
+  SharedSpace(const gqa::DecodeSetup& setup, int batch, int groups)
+      : start(0), pre_o(round256((static_cast<size_t>(groups) + 1) * sizeof(int64_t))),
+        pre_lse(pre_o + gqa::shared_prefix_blocks(batch, setup.sm_count) * kPartBytes),
+        own(setup.plan, batch, pre_lse + round256(gqa::shared_prefix_blocks(batch, setup.sm_count) * gqa::kGroup * sizeof(float))) {}
 };
 
 struct SelectSpaceLayout {
@@ -98,10 +99,10 @@ bool sparse_sizes_ok(int rows, int top, int page_size) {
 
 extern "C" {
 
-size_t gqa_shared_paged_decode_ws_size(int batch, int cache_format) {
+size_t gqa_shared_paged_decode_ws_size(int batch, int groups, int cache_format) {
   gqa::DecodeSetup setup;
-  if (batch <= 0 || batch > (1 << 20) || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
-  return SharedSpace(setup.plan, batch).own.end;
+  if (batch <= 0 || batch > (1 << 20) || groups < 0 || groups > (1 << 20) || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
+  return SharedSpace(setup, batch, groups).own.end;
 }
 
 int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_indptr,
@@ -128,7 +129,7 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   gqa::DecodeSetup setup;
   const int rc = gqa::decode_setup(fp8, &setup);
   if (rc != GQA_OK) return rc;
-  const SharedSpace at(setup.plan, batch);
+  const SharedSpace at(setup, batch, groups);
   if (workspace_bytes < at.own.end) return GQA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   gqa::DecodeParams d = decode_params(setup, at.own, ws, sm_scale);
@@ -153,6 +154,9 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   p.kv_indptr = kv_indptr;
   p.out = out;
   p.lse = lse;
+  p.group_start = reinterpret_cast<int64_t*>(ws + at.start);
+  p.pre_ctas = groups > 0 && prefix_count > 0 ? setup.sm_count : 0;
+  p.wait_limit_ns = setup.wait_limit_ns;
   p.pre_o = reinterpret_cast<float*>(ws + at.pre_o);
   p.pre_lse = reinterpret_cast<float*>(ws + at.pre_lse);
   p.own_o = d.part_o;

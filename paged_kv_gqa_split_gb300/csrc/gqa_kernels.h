@@ -342,7 +342,8 @@ struct SharedParams {  // gqa_shared.cu
   const int* kv_indptr;       // [batch + 1]
   void* out;
   float* lse;                 // or NULL
-  float* pre_o;               // parts of the prefixes: [batch][4][128 dims][8 heads], LSE [batch][4][8]
+  int64_t* group_start;       // [groups + 1] first step of each group's prefix (written by the prefix pass)
+  float* pre_o;               // parts of the prefixes, blocks of [128 dims][8 heads] and 8 LSEs: [batch][4], [pre_ctas][32]
   float* pre_lse;
   const float* own_o;         // parts of the own tokens (DecodeParams::part_o, part_lse)
   const float* own_lse;
@@ -350,8 +351,11 @@ struct SharedParams {  // gqa_shared.cu
   PlanConfig plan;
   float scale_log2;
   int batch, groups, prefix_count, index_count, num_pages, fp8;
+  int pre_ctas;               // 0: no prefix has a token
+  unsigned long long wait_limit_ns;
   int* err;
 };
+int shared_prefix_blocks(int batch, int ctas);
 cudaError_t launch_shared(const SharedParams& p, const DecodeParams& own, cudaStream_t stream);
 
 struct BoundsParams {  // gqa_blocks.cu

@@ -396,22 +396,8 @@ __device__ __forceinline__ bool row_exponents(const MlaPrefillParams& p, int b, 
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
 
-__device__ __forceinline__ uint32_t sw128(uint32_t base, int r, int c) { return base + r * 128 + ((c ^ (r & 7)) << 4); }
 
 // ------------------------------------------------------------------ waits
-constexpr uint64_t kWaitNs = 2000000000ull;
-
-// The value that all lanes hold, so that the compiler knows it to be one: operands of MMAs then need no move from a
-// lane's register (the attention's key tiles took a tenth longer with them in a loop over units).
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-
-// Bounded wait that ignores the abort flag (draining before exit).
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (global_timer_ns() - t0 > kWaitNs) break;
-}
-
 // Whole warp: every lane waits (bounded; no lane runs apart from the others), every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_s, int* err, int bit,
                                           uint64_t limit = kWaitNs) {
@@ -749,25 +735,6 @@ struct AttnMaps {  // boxes of 64 values x 64 rows (keys) and x 128 rows (values
   CUtensorMap kn, vv, kr, q;
 };
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Two scores to probabilities 2^(s sc + off): packed fp16, and their sum added to l.
 __device__ __forceinline__ uint32_t exp_pair(uint32_t s0, uint32_t s1, uint64_t sc2, uint64_t off2, uint64_t& l) {
   float x0, x1;
@@ -776,12 +743,6 @@ __device__ __forceinline__ uint32_t exp_pair(uint32_t s0, uint32_t s1, uint64_t 
   x1 = ex2(x1);
   l = add2(l, pack2(x0, x1));
   return pack_f16(x0, x1);
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // Bits c of a word whose key 32 k + c (of the key tile at t0) is at most lim.

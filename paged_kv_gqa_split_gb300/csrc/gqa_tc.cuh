@@ -58,6 +58,16 @@ __device__ __forceinline__ void tc_mma_bf16_warp(uint32_t d_tmem, uint64_t a_des
       : "memory");
 }
 
+// With A in tensor memory (row i in lane i, two 16-bit values a column).
+__device__ __forceinline__ void tc_mma_tmem_a_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // tc_commit from the lane that elect.sync picks (the one that issued tc_mma_bf16_warp).
 __device__ __forceinline__ void tc_commit_warp(uint32_t bar) {
   asm volatile(
@@ -300,6 +310,48 @@ __device__ __forceinline__ bool tc_wait_limited(uint32_t bar, uint32_t parity, v
       return false;
     }
   }
+}
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // of a wait that no limit of the call's own bounds
+
+// The value that all lanes hold, so that the compiler knows it to be one: operands of MMAs then need no move from a
+// lane's register (the prompt attention's key tiles took a tenth longer with them in a loop over units).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Bounded wait that ignores the abort flag (draining before exit).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitNs) break;
+}
+
+// Address of 16-byte column c of row r in a region of 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(uint32_t base, int r, int c) { return base + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// ---------------------------------------------------------- pairs of floats
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 }  // namespace gqa

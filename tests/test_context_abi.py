@@ -38,7 +38,7 @@ def test_shared_refusals(lib):
         dict(q=A + 8), dict(k=A + 8), dict(v=A + 2), dict(out=A + 8), dict(lse=A + 4), dict(pi=A + 1), dict(px=A + 2),
         dict(gi=A + 2), dict(ki=A + 2), dict(kx=A + 1)])
     refused(lib.gqa_shared_paged_decode, ok, [dict(ws=None), dict(ws=A + 128)], SPACE)
-    for bad in ((0, 0), (-1, 0), ((1 << 20) + 1, 0), (3, 2)):
+    for bad in ((0, 1, 0), (-1, 1, 0), ((1 << 20) + 1, 1, 0), (3, -1, 0), (3, 1, 2)):
         assert lib.gqa_shared_paged_decode_ws_size(*bad) == 0
 
 

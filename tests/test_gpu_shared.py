@@ -161,7 +161,7 @@ def test_repeats_streams_graphs_and_workspaces():
     got = pkg.shared_run(*args, stream=stream)
     stream.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    size = _lib.load().gqa_shared_paged_decode_ws_size(args[0].shape[0], 0)
+    size = _lib.load().gqa_shared_paged_decode_ws_size(args[0].shape[0], 2, 0)
     ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever it is read before it is written
     got = pkg.shared_run(*args, workspace=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
