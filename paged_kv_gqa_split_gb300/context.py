@@ -14,48 +14,70 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import HEAD_DIM, NUM_KV_HEADS, NUM_QO_HEADS, load
-from .serving import _INT_MAX, _cache_format, _call, _check, _index, _new, _ready
+from .serving import _INT_MAX, _cache_format, _call, _check, _empty_strided_cuda, _entries, _index, _new
 
 
-def _ints(index, **tensors):
-    """Raises unless all are contiguous int32 tensors of one dimension on GPU `index`."""
+_SCALE = HEAD_DIM ** -0.5
+_OUT_STRIDE, _LSE_STRIDE = (NUM_QO_HEADS * HEAD_DIM, HEAD_DIM, 1), (NUM_QO_HEADS, 1)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _plain(index, dtype, dim, *tensors):
+    """Whether all are contiguous tensors of `dtype` with `dim` dimensions on GPU `index`: the common case, in few steps."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != index or t.ndim != dim or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
+
+
+def _need(index, dtype, dim, **tensors):
+    """Raises unless all are contiguous tensors of `dtype` with `dim` dimensions on GPU `index`."""
     for name, t in tensors.items():
-        if not _ready(index, t, torch.int32):
-            _check(index, torch.int32, True, **{name: t})
-        if t.dim() != 1:
-            raise ValueError(f"{name} must have one dimension")
+        _check(index, dtype, True, **{name: t})
+        if t.dim() != dim:
+            raise ValueError(f"{name} must have {dim} dimension{'s' if dim > 1 else ''}, not {t.dim()}")
 
 
 def _queries(index, q):
-    if not _ready(index, q, torch.bfloat16):
-        _check(index, torch.bfloat16, True, q=q)
-    if q.dim() != 3 or q.shape[1] != NUM_QO_HEADS or q.shape[2] != HEAD_DIM:
+    if not _plain(index, _BF16, 3, q):
+        _need(index, _BF16, 3, q=q)
+    n, heads, dim = q.shape
+    if heads != NUM_QO_HEADS or dim != HEAD_DIM:
         raise ValueError("expected q [N, 32, 128]")
-    return q.shape[0]
+    return n
 
 
 def _paged(index, k_cache, v_cache):
     """(format, pages) of CSR-paged caches."""
-    if not (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and
-            k_cache.get_device() == v_cache.get_device() == index and k_cache.is_contiguous() and v_cache.is_contiguous()):
+    if not (_plain(index, _BF16, 4, k_cache, v_cache) or _plain(index, torch.uint8, 2, k_cache, v_cache)):
         _check(index, None, True, k_cache=k_cache, v_cache=v_cache)
     return _cache_format(k_cache, v_cache)
+
+
+def _alloc(index, shape, stride, dtype, stream):
+    """_new with the strides of a contiguous tensor of that shape, known to the caller."""
+    if stream is None and _empty_strided_cuda is not None and index == torch._C._cuda_getDevice():
+        return _empty_strided_cuda(shape, stride, dtype)
+    return _new(index, shape, dtype, stream)
 
 
 def _results(index, n, out, lse, with_lse, stream):
     """out [n, 32, 128] and lse [n, 32] (or None), allocated where they are not given."""
     if out is None:
-        out = _new(index, (n, NUM_QO_HEADS, HEAD_DIM), torch.bfloat16, stream)
+        out = _alloc(index, (n, NUM_QO_HEADS, HEAD_DIM), _OUT_STRIDE, _BF16, stream)
     else:
-        _check(index, torch.bfloat16, True, out=out)
+        _check(index, _BF16, True, out=out)
         if out.shape != (n, NUM_QO_HEADS, HEAD_DIM):
             raise ValueError(f"out must be {(n, NUM_QO_HEADS, HEAD_DIM)}")
     if lse is not None:
-        _check(index, torch.float32, True, lse=lse)
+        _check(index, _F32, True, lse=lse)
         if lse.shape != (n, NUM_QO_HEADS):
             raise ValueError(f"lse must be {(n, NUM_QO_HEADS)}")
     elif with_lse:
-        lse = _new(index, (n, NUM_QO_HEADS), torch.float32, stream)
+        lse = _alloc(index, (n, NUM_QO_HEADS), _LSE_STRIDE, _F32, stream)
     return out, lse
 
 
@@ -64,14 +86,17 @@ def _workspace(index, given, stream, what, *sizes):
     if given is not None:
         _check(index, None, True, workspace=given)
         return given, given.numel() * given.element_size()
+    size_of = _entries.get(what)
+    if size_of is None:
+        size_of = _entries[what] = getattr(load(), what)
     if index == torch._C._cuda_getDevice():
-        size = getattr(load(), what)(*sizes)
+        size = size_of(*sizes)
     else:
         with torch.cuda.device(index):
-            size = getattr(load(), what)(*sizes)
+            size = size_of(*sizes)
     if size == 0:
         raise ValueError(f"sizes {sizes} are out of range")
-    return _new(index, (size,), torch.uint8, stream), size
+    return _alloc(index, (size,), (1,), torch.uint8, stream), size
 
 
 def _pointer(t):
@@ -90,8 +115,9 @@ def shared_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pr
     index = _index("q", q)
     n = _queries(index, q)
     fmt, pages = _paged(index, k_cache, v_cache)
-    _ints(index, prefix_indptr=prefix_indptr, prefix_indices=prefix_indices, group_indptr=group_indptr,
-          kv_indptr=kv_indptr, kv_indices=kv_indices)
+    if not _plain(index, _I32, 1, prefix_indptr, prefix_indices, group_indptr, kv_indptr, kv_indices):
+        _need(index, _I32, 1, prefix_indptr=prefix_indptr, prefix_indices=prefix_indices, group_indptr=group_indptr,
+              kv_indptr=kv_indptr, kv_indices=kv_indices)
     groups = group_indptr.shape[0] - 1
     if groups < 0 or prefix_indptr.shape[0] != groups + 1 or kv_indptr.shape[0] != n + 1:
         raise ValueError(f"expected prefix_indptr and group_indptr [G + 1] and kv_indptr [{n + 1}]")
@@ -101,34 +127,34 @@ def shared_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pr
     ws, size = _workspace(index, workspace, stream, "gqa_shared_paged_decode_ws_size", n, groups, fmt)
     _call("gqa_shared_paged_decode", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           prefix_indptr.data_ptr(), prefix_indices.data_ptr(), group_indptr.data_ptr(), kv_indptr.data_ptr(),
-          kv_indices.data_ptr(), HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), lse.data_ptr(), n,
+          kv_indices.data_ptr(), _SCALE if sm_scale is None else sm_scale, out.data_ptr(), lse.data_ptr(), n,
           groups, prefix_indices.shape[0], kv_indices.shape[0], pages, fmt, ws.data_ptr(), size)
     return out, lse
 
 
 def _blocked(index, name, cache):
     """(blocks, page size) of a block-table cache [blocks, page, 4, 128]."""
-    if not _ready(index, cache, torch.bfloat16):
-        _check(index, torch.bfloat16, True, **{name: cache})
-    if cache.dim() != 4 or cache.shape[2] != NUM_KV_HEADS or cache.shape[3] != HEAD_DIM:
+    if not _plain(index, _BF16, 4, cache):
+        _need(index, _BF16, 4, **{name: cache})
+    blocks, page, heads, dim = cache.shape
+    if heads != NUM_KV_HEADS or dim != HEAD_DIM:
         raise ValueError(f"expected {name} [blocks, page_size, 4, 128]")
-    return cache.shape[0], cache.shape[1]
+    return blocks, page
 
 
 def _table(index, block_table):
-    if not _ready(index, block_table, torch.int32):
-        _check(index, torch.int32, True, block_table=block_table)
-    if block_table.dim() != 2:
-        raise ValueError("expected block_table [requests, width]")
+    if not _plain(index, _I32, 2, block_table):
+        _need(index, _I32, 2, block_table=block_table)
     return block_table.shape
 
 
 def _bounds(index, bounds):
-    if not _ready(index, bounds, torch.bfloat16):
-        _check(index, torch.bfloat16, True, bounds=bounds)
-    if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (2, NUM_KV_HEADS, HEAD_DIM):
+    if not _plain(index, _BF16, 4, bounds):
+        _need(index, _BF16, 4, bounds=bounds)
+    blocks, two, heads, dim = bounds.shape
+    if two != 2 or heads != NUM_KV_HEADS or dim != HEAD_DIM:
         raise ValueError("expected bounds [blocks, 2, 4, 128]")
-    return bounds.shape[0]
+    return blocks
 
 
 def block_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
@@ -140,9 +166,10 @@ def block_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch
     index = _index("k_cache", k_cache)
     blocks, page = _blocked(index, "k_cache", k_cache)
     requests, width = _table(index, block_table)
-    _ints(index, lens=lens)
-    if first is not None:
-        _ints(index, first=first)
+    if not _plain(index, _I32, 1, lens):
+        _need(index, _I32, 1, lens=lens)
+    if first is not None and not _plain(index, _I32, 1, first):
+        _need(index, _I32, 1, first=first)
     if _bounds(index, bounds) != blocks or lens.shape[0] != requests or (first is not None and first.shape[0] != requests):
         raise ValueError("expected bounds [blocks, 2, 4, 128], and lens and first [requests]")
     _call("gqa_block_bounds", index, stream, k_cache.data_ptr(), bounds.data_ptr(), block_table.data_ptr(),
@@ -162,16 +189,16 @@ def block_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     rows = _queries(index, q)
     held = _bounds(index, bounds)
     requests, width = _table(index, block_table)
-    _ints(index, token_to_req=token_to_req, lens=lens)
+    if not _plain(index, _I32, 1, token_to_req, lens):
+        _need(index, _I32, 1, token_to_req=token_to_req, lens=lens)
     if token_to_req.shape[0] != rows or lens.shape[0] != rows:
         raise ValueError(f"token_to_req and lens must be [{rows}]")
-    for name, x in (("top", top), ("page_size", page_size), ("keep_first", keep_first), ("keep_last", keep_last)):
-        if not 0 <= x <= _INT_MAX:
-            raise ValueError(f"{name} {x} is out of range")
+    if not (0 <= keep_first and 0 <= keep_last and 0 < top <= _INT_MAX and 0 < page_size <= _INT_MAX):
+        raise ValueError("top, page_size, keep_first or keep_last is out of range")
     if keep_first + keep_last > top:
         raise ValueError("keep_first and keep_last take more than top blocks")
     if blocks is None:
-        blocks = _new(index, (rows, NUM_KV_HEADS, top), torch.int32, stream)
+        blocks = _alloc(index, (rows, NUM_KV_HEADS, top), (NUM_KV_HEADS * top, top, 1), _I32, stream)
     else:
         _check(index, torch.int32, True, blocks=blocks)
         if blocks.shape != (rows, NUM_KV_HEADS, top):
@@ -200,21 +227,22 @@ def block_sparse_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if _blocked(index, "v_cache", v_cache) != (held, page):
         raise ValueError("k_cache and v_cache must have the same shape")
     requests, width = _table(index, block_table)
-    _ints(index, token_to_req=token_to_req, lens=lens)
-    if not _ready(index, blocks, torch.int32):
-        _check(index, torch.int32, True, blocks=blocks)
-    if blocks.dim() != 3 or blocks.shape[0] != rows or blocks.shape[1] != NUM_KV_HEADS:
+    if not _plain(index, _I32, 1, token_to_req, lens):
+        _need(index, _I32, 1, token_to_req=token_to_req, lens=lens)
+    if not _plain(index, _I32, 3, blocks):
+        _need(index, _I32, 3, blocks=blocks)
+    listed, heads, top = blocks.shape
+    if listed != rows or heads != NUM_KV_HEADS:
         raise ValueError(f"blocks must be [{rows}, 4, top]")
     if token_to_req.shape[0] != rows or lens.shape[0] != rows:
         raise ValueError(f"token_to_req and lens must be [{rows}]")
     out, lse = _results(index, rows, out, lse, with_lse, stream)
     if rows == 0:
         return out, lse
-    top = blocks.shape[2]
     ws, size = _workspace(index, workspace, stream, "gqa_block_sparse_decode_ws_size", rows, top, page)
     _call("gqa_block_sparse_decode", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           blocks.data_ptr(), block_table.data_ptr(), token_to_req.data_ptr(), lens.data_ptr(),
-          HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _pointer(lse), rows, requests, top, page,
+          _SCALE if sm_scale is None else sm_scale, out.data_ptr(), _pointer(lse), rows, requests, top, page,
           held, width, ws.data_ptr(), size)
     return out, lse
 
@@ -233,16 +261,16 @@ def run_weighted(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     index = _index("q", q)
     n = _queries(index, q)
     fmt, pages = _paged(index, k_cache, v_cache)
-    _ints(index, kv_indptr=kv_indptr, kv_indices=kv_indices)
-    if not _ready(index, weights, torch.float32):
-        _check(index, torch.float32, True, weights=weights)
-    if weights.dim() != 2 or weights.shape[0] != n or kv_indptr.shape[0] != n + 1:
+    if not (_plain(index, _I32, 1, kv_indptr, kv_indices) and _plain(index, _F32, 2, weights)):
+        _need(index, _I32, 1, kv_indptr=kv_indptr, kv_indices=kv_indices)
+        _need(index, _F32, 2, weights=weights)
+    rows, width = weights.shape
+    if rows != n or kv_indptr.shape[0] != n + 1:
         raise ValueError(f"expected weights [{n}, width] and kv_indptr [{n + 1}]")
     if not math.isfinite(decay):
         raise ValueError("decay must be finite")
-    width = weights.shape[1]
     if weights_out is None:
-        weights_out = _new(index, (n, width), torch.float32, stream)
+        weights_out = _alloc(index, (n, width), (max(width, 1), 1), _F32, stream)
     else:
         _check(index, torch.float32, True, weights_out=weights_out)
         if weights_out.shape != weights.shape:
@@ -252,7 +280,7 @@ def run_weighted(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         return out, lse, weights_out
     ws, size = _workspace(index, workspace, stream, "gqa_paged_decode_weighted_ws_size", kv_indices.shape[0], fmt)
     _call("gqa_paged_decode_weighted", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          kv_indptr.data_ptr(), kv_indices.data_ptr(), HEAD_DIM ** -0.5 if sm_scale is None else sm_scale,
+          kv_indptr.data_ptr(), kv_indices.data_ptr(), _SCALE if sm_scale is None else sm_scale,
           weights.data_ptr(), decay, weights_out.data_ptr(), out.data_ptr(), lse.data_ptr(), n, width,
           kv_indices.shape[0], pages, fmt, ws.data_ptr(), size)
     return out, lse, weights_out
@@ -266,20 +294,21 @@ def kv_evict(weights: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: torch.T
     as a page table, and the other tokens' pages in the same form. kv_indices and freed are as long as the given
     kv_indices, -1 behind the last sequence's."""
     index = _index("weights", weights)
-    if not _ready(index, weights, torch.float32):
-        _check(index, torch.float32, True, weights=weights)
-    _ints(index, kv_indptr=kv_indptr, kv_indices=kv_indices)
-    if weights.dim() != 2 or kv_indptr.shape[0] != weights.shape[0] + 1:
+    if not (_plain(index, _F32, 2, weights) and _plain(index, _I32, 1, kv_indptr, kv_indices)):
+        _need(index, _F32, 2, weights=weights)
+        _need(index, _I32, 1, kv_indptr=kv_indptr, kv_indices=kv_indices)
+    (n, width), total = weights.shape, kv_indices.shape[0]
+    if kv_indptr.shape[0] != n + 1:
         raise ValueError("expected weights [B, width] and kv_indptr [B + 1]")
-    for name, x in (("budget", budget), ("keep_first", keep_first), ("keep_last", keep_last)):
-        if not 0 <= x <= _INT_MAX:
-            raise ValueError(f"{name} {x} is out of range")
+    if not (0 <= keep_first and 0 <= keep_last and 0 <= budget <= _INT_MAX):
+        raise ValueError("budget, keep_first or keep_last is out of range")
     if keep_first + keep_last > budget:
         raise ValueError("keep_first and keep_last take more than the budget")
-    (n, width), total = weights.shape, kv_indices.shape[0]
-    got = _new(index, (n, width), torch.float32, stream)
-    indptr, freed_indptr = (_new(index, (n + 1,), torch.int32, stream) for _ in range(2))
-    indices, freed = (_new(index, (total,), torch.int32, stream) for _ in range(2))
+    got = _alloc(index, (n, width), (max(width, 1), 1), _F32, stream)
+    indptr = _alloc(index, (n + 1,), (1,), _I32, stream)
+    freed_indptr = _alloc(index, (n + 1,), (1,), _I32, stream)
+    indices = _alloc(index, (total,), (1,), _I32, stream)
+    freed = _alloc(index, (total,), (1,), _I32, stream)
     if n == 0:
         with torch.cuda.stream(stream):
             indptr.zero_(), freed_indptr.zero_(), indices.fill_(-1), freed.fill_(-1)

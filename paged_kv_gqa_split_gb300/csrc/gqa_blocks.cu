@@ -16,8 +16,11 @@ namespace gqa {
 constexpr int kRowValues = kKvHeads * kHeadDim;  // of a token, or of a block's upper or lower bounds
 
 // ----------------------------------------------------------------- bounds
-// A block of threads per cache block: 64 lanes of 16 bytes a token, four tokens at a time.
-constexpr int kBoundThreads = 256;
+// Teams of 64 lanes, 16 bytes a lane and token. The blocks to renew, request by request, are numbered by prefix sums that
+// every block of threads forms by itself, 256 requests at a time; a team takes every gridDim-th one. Where there are no
+// more of them than blocks of threads (a decode step's), the four teams of a block share one. Bound by the keys' bytes:
+// 131072 tokens in pages of 32 take BOUNDS_US.
+constexpr int kBoundThreads = 256, kBoundTeams = kBoundThreads / 64;
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -28,48 +31,107 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+struct MinMax {
+  uint4 hi, lo;
+  __device__ __forceinline__ void init() {
+    hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);
+  }
+  __device__ __forceinline__ void add(const uint4& a, const uint4& b) {
+    hi = make_uint4(max2(hi.x, a.x), max2(hi.y, a.y), max2(hi.z, a.z), max2(hi.w, a.w));
+    lo = make_uint4(min2(lo.x, b.x), min2(lo.y, b.y), min2(lo.z, b.z), min2(lo.w, b.w));
+  }
+};
+
 __global__ void __launch_bounds__(kBoundThreads) gqa_block_bounds_kernel(const BoundsParams p) {
-  __shared__ uint4 part[2][4][64];
-  const int lane = threadIdx.x & 63, team = threadIdx.x >> 6;
-  for (int r = blockIdx.y; r < p.requests; r += gridDim.y) {
-    const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(__ldg(p.lens + r)), static_cast<int64_t>(p.width) * p.page_size)));
-    const int first = p.first == nullptr ? 0 : max(0, __ldg(p.first + r));
-    if (first >= n) continue;
-    for (int i = first / p.page_size + blockIdx.x; i <= (n - 1) / p.page_size; i += gridDim.x) {
-      const int block = __ldg(p.block_table + static_cast<int64_t>(r) * p.width + i);
-      if (static_cast<unsigned>(block) >= static_cast<unsigned>(p.num_blocks)) continue;  // the same for all threads
-      const int tokens = min(p.page_size, n - i * p.page_size);
-      const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + static_cast<int64_t>(block) * p.page_size * kRowValues) + lane;
-      uint4 hi = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u), lo = make_uint4(0x7f807f80u, 0x7f807f80u, 0x7f807f80u, 0x7f807f80u);
-#pragma unroll 8
-      for (int t = team; t < tokens; t += 4) {
-        const uint4 x = __ldg(k + t * 64);
-        hi = make_uint4(max2(hi.x, x.x), max2(hi.y, x.y), max2(hi.z, x.z), max2(hi.w, x.w));
-        lo = make_uint4(min2(lo.x, x.x), min2(lo.y, x.y), min2(lo.z, x.z), min2(lo.w, x.w));
-      }
-      __syncthreads();  // the last block's parts have been read
-      part[0][team][lane] = hi;
-      part[1][team][lane] = lo;
-      __syncthreads();
-      if (team < 2) {
-        uint4 a = part[team][0][lane];
+  __shared__ MinMax part[kBoundTeams][64];
+  __shared__ int64_t start[kBoundThreads + 1], warp_sum[kBoundThreads / 32];
+  __shared__ int first_block[kBoundThreads], length[kBoundThreads];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 63, team = tid >> 6;
+  // tokens t0, t0 + step, ... of the i-th block of request r; false if its table names no block of the pool
+  auto walk = [&](int r, int i, int n, int t0, int step, MinMax& mm, int64_t& block) {
+    const int b = __ldcg(p.block_table + static_cast<int64_t>(r) * p.width + i);
+    if (static_cast<unsigned>(b) >= static_cast<unsigned>(p.num_blocks)) return false;
+    block = b;
+    const int tokens = min(p.page_size, n - i * p.page_size);
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + lane;
+    mm.init();
+    int t = t0;
+    for (; t + 7 * step < tokens; t += 8 * step) {
+      uint4 x[8];
 #pragma unroll
-        for (int j = 1; j < 4; ++j) {
-          const uint4 x = part[team][j][lane];
-          a = team == 0 ? make_uint4(max2(a.x, x.x), max2(a.y, x.y), max2(a.z, x.z), max2(a.w, x.w))
-                        : make_uint4(min2(a.x, x.x), min2(a.y, x.y), min2(a.z, x.z), min2(a.w, x.w));
-        }
-        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.bounds) + static_cast<int64_t>(block) * 2 * kRowValues)[team * 64 + lane] = a;
+      for (int u = 0; u < 8; ++u) x[u] = __ldcg(k + (t + u * step) * 64);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mm.add(x[u], x[u]);
+    }
+#pragma unroll 4
+    for (; t < tokens; t += step) {
+      const uint4 x = __ldcg(k + t * 64);
+      mm.add(x, x);
+    }
+    return true;
+  };
+  auto store = [&](int64_t block, const MinMax& mm) {
+    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.bounds) + block * 2 * kRowValues) + lane;
+    to[0] = mm.hi;
+    to[64] = mm.lo;
+  };
+  for (int r0 = 0; r0 < p.requests; r0 += kBoundThreads) {
+    const int r = r0 + tid;
+    int count = 0, at = 0, n = 0;
+    if (r < p.requests) {
+      n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(__ldcg(p.lens + r)), static_cast<int64_t>(p.width) * p.page_size)));
+      const int first = p.first == nullptr ? 0 : max(0, __ldcg(p.first + r));
+      at = first / p.page_size;
+      if (first < n) count = (n - 1) / p.page_size + 1 - at;
+    }
+    int64_t upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += up;
+    }
+    __syncthreads();  // the requests before have been walked
+    if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
+    first_block[tid] = at;
+    length[tid] = n;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w) upto += warp_sum[w];
+    start[tid + 1] = upto;
+    if (tid == 0) start[0] = 0;
+    __syncthreads();
+    const int64_t total = start[kBoundThreads];
+    const bool shared = total <= gridDim.x;
+    const int64_t teams = shared ? gridDim.x : gridDim.x * kBoundTeams;
+    for (int64_t x = shared ? blockIdx.x : blockIdx.x + team * gridDim.x; x < total; x += teams) {
+      int lo = 0, hi = kBoundThreads;  // the request: start[lo] <= x < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid; else hi = mid;
       }
+      MinMax mm;
+      int64_t block = 0;
+      const bool ok = walk(r0 + lo, first_block[lo] + static_cast<int>(x - start[lo]), length[lo], shared ? team : 0, shared ? kBoundTeams : 1, mm, block);
+      if (!ok) continue;  // the same for the team, and for the block of threads where it shares
+      if (shared) {
+        part[team][lane] = mm;
+        __syncthreads();
+        if (team == 0)
+#pragma unroll
+          for (int j = 1; j < kBoundTeams; ++j) mm.add(part[j][lane].hi, part[j][lane].lo);
+        __syncthreads();
+        if (team != 0) continue;
+      }
+      store(block, mm);
     }
   }
 }
 
 cudaError_t launch_block_bounds(const BoundsParams& p, int sm_count, cudaStream_t stream) {
-  const int y = p.requests < 65535 ? p.requests : 65535;
-  const int most = (8 * sm_count + y - 1) / y;
-  gqa_block_bounds_kernel<<<dim3(p.width < most ? p.width : most, y), kBoundThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int64_t most = static_cast<int64_t>(p.requests) * p.width;
+  return launch_chained(gqa_block_bounds_kernel, dim3(most < 8 * sm_count ? most : 8 * sm_count), kBoundThreads, 0, stream, 1, p);
 }
 
 // ------------------------------------------------------------------ score
@@ -79,8 +141,9 @@ cudaError_t launch_block_bounds(const BoundsParams& p, int sm_count, cudaStream_
 // Beside the score goes a bound of its error, kGamma * max_h |q_h|_1 * max |bounds|, for the choice: products of bf16 are
 // exact in fp32; an MMA sums 16 of them and the accumulator, each cut off at 2^-23 of the largest, and no partial sum
 // passes |q|_1 max|bounds|: 16 MMAs x 17 terms x 2^-23 < 2^-14.9.
-constexpr int kScoreBlocks = 64;  // of a row, a block of threads
+constexpr int kScoreBlocks = 16;  // of a row, a block of threads
 constexpr float kGamma = 0x1p-14f;
+constexpr uint32_t kNoBlock = 0xffffffffu;  // in a score's place where the table names no block of the pool
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -93,26 +156,41 @@ struct RowView {
 };
 __device__ __forceinline__ RowView row_view(const BlockParams& p, int row) {
   RowView v;
-  v.req = __ldg(p.token_to_req + row);
+  v.req = __ldcg(p.token_to_req + row);
   const bool ok = v.req >= 0 && v.req < p.requests;
-  v.n = ok ? static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(__ldg(p.lens + row)), static_cast<int64_t>(p.width) * p.page_size))) : 0;
+  v.n = ok ? static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(__ldcg(p.lens + row)), static_cast<int64_t>(p.width) * p.page_size))) : 0;
   v.count = (v.n + p.page_size - 1) / p.page_size;
   return v;
 }
 
 __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams p) {
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
   for (int row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(row) * kQoHeads + g * kGroup + r) * kHeadDim) + c;
+    uint4 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = __ldcg(qr + 4 * j);
     const RowView v = row_view(p, row);
     const int first = blockIdx.x * kScoreBlocks;
     if (first >= v.count) continue;
     const int* table = p.block_table + static_cast<int64_t>(v.req) * p.width;
-    const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(row) * kQoHeads + g * kGroup + r) * kHeadDim) + c;
-    uint4 q[4];
+    const int ia = first + r, ib = first + r + 8;
+    const int pa = ia < v.count ? __ldcg(table + ia) : -1, pb = ib < v.count ? __ldcg(table + ib) : -1;
+    const bool oka = static_cast<unsigned>(pa) < static_cast<unsigned>(p.num_blocks), okb = static_cast<unsigned>(pb) < static_cast<unsigned>(p.num_blocks);
+    const uint4* xa = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(oka ? pa : 0) * 2 * kKvHeads + g) * kHeadDim) + c;
+    const uint4* xb = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(okb ? pb : 0) * 2 * kKvHeads + g) * kHeadDim) + c;
+    uint4 a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // 0 .. 3 hi, 4 .. 7 lo
+      const int at = (j >> 2) * (kRowValues / 8) + 4 * (j & 3);
+      a[j] = oka ? __ldcg(xa + at) : make_uint4(0, 0, 0, 0);
+      b[j] = okb ? __ldcg(xb + at) : make_uint4(0, 0, 0, 0);
+    }
     float norm = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      q[j] = __ldg(qr + 4 * j);
       const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) norm += fabsf(bf16_lo(w[i])) + fabsf(bf16_hi(w[i]));
@@ -121,56 +199,50 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
     norm += __shfl_xor_sync(0xffffffffu, norm, 2);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) norm = max_nan(norm, __shfl_xor_sync(0xffffffffu, norm, o));
-    float* scores = p.scores + (static_cast<int64_t>(row) * kKvHeads + g) * p.width;
-    float* errors = p.errors + (static_cast<int64_t>(row) * kKvHeads + g) * p.width;
-    const int end = min(first + kScoreBlocks, v.count);
-#pragma unroll 1
-    for (int b0 = first; b0 < end; b0 += 16) {
-      const int ia = b0 + r, ib = b0 + r + 8;
-      const int pa = ia < end ? __ldg(table + ia) : -1, pb = ib < end ? __ldg(table + ib) : -1;
-      const bool oka = static_cast<unsigned>(pa) < static_cast<unsigned>(p.num_blocks), okb = static_cast<unsigned>(pb) < static_cast<unsigned>(p.num_blocks);
-      const uint4* xa = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(oka ? pa : 0) * 2 * kKvHeads + g) * kHeadDim) + c;
-      const uint4* xb = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(okb ? pb : 0) * 2 * kKvHeads + g) * kHeadDim) + c;
-      uint4 a[8], b[8];
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t ta = 0, tb = 0;  // largest |bound| so far, two at a time
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // 0 .. 3 hi, 4 .. 7 lo
-        const int at = (j >> 2) * (kRowValues / 8) + 4 * (j & 3);
-        a[j] = oka ? __ldg(xa + at) : make_uint4(0, 0, 0, 0);
-        b[j] = okb ? __ldg(xb + at) : make_uint4(0, 0, 0, 0);
-      }
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t ta = 0, tb = 0;  // largest |bound| so far, two at a time
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint4 qj = q[j & 3];
-        const bool up = j < 4;
-        auto part = [&](uint32_t x) { return up ? max2(x, 0u) : min2(x, 0u); };
-        mma_bf16_16816(s, a[j].x, b[j].x, a[j].y, b[j].y, part(qj.x), part(qj.y));
-        mma_bf16_16816(s, a[j].z, b[j].z, a[j].w, b[j].w, part(qj.z), part(qj.w));
-        ta = max2(max2(ta, a[j].x & 0x7fff7fffu), max2(max2(a[j].y & 0x7fff7fffu, a[j].z & 0x7fff7fffu), a[j].w & 0x7fff7fffu));
-        tb = max2(max2(tb, b[j].x & 0x7fff7fffu), max2(max2(b[j].y & 0x7fff7fffu, b[j].z & 0x7fff7fffu), b[j].w & 0x7fff7fffu));
-      }
-      float sa = max_nan(s[0], s[1]), sb = max_nan(s[2], s[3]);
-      float ea = max_nan(bf16_lo(ta), bf16_hi(ta)), eb = max_nan(bf16_lo(tb), bf16_hi(tb));
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        sa = max_nan(sa, __shfl_xor_sync(0xffffffffu, sa, o));
-        sb = max_nan(sb, __shfl_xor_sync(0xffffffffu, sb, o));
-        ea = max_nan(ea, __shfl_xor_sync(0xffffffffu, ea, o));
-        eb = max_nan(eb, __shfl_xor_sync(0xffffffffu, eb, o));
-      }
-      // a block outside the pool is no candidate: error -1
-      if (c == 0 && ia < end) scores[ia] = sa, errors[ia] = oka ? kGamma * norm * ea : -1.f;
-      if (c == 0 && ib < end) scores[ib] = sb, errors[ib] = okb ? kGamma * norm * eb : -1.f;
+    for (int j = 0; j < 8; ++j) {
+      const uint4 qj = q[j & 3];
+      const bool up = j < 4;
+      auto part = [&](uint32_t x) { return up ? max2(x, 0u) : min2(x, 0u); };
+      mma_bf16_16816(s, a[j].x, b[j].x, a[j].y, b[j].y, part(qj.x), part(qj.y));
+      mma_bf16_16816(s, a[j].z, b[j].z, a[j].w, b[j].w, part(qj.z), part(qj.w));
+      ta = max2(max2(ta, a[j].x & 0x7fff7fffu), max2(max2(a[j].y & 0x7fff7fffu, a[j].z & 0x7fff7fffu), a[j].w & 0x7fff7fffu));
+      tb = max2(max2(tb, b[j].x & 0x7fff7fffu), max2(max2(b[j].y & 0x7fff7fffu, b[j].z & 0x7fff7fffu), b[j].w & 0x7fff7fffu));
     }
+    float sa = max_nan(s[0], s[1]), sb = max_nan(s[2], s[3]);
+    float ea = kGamma * norm * max_nan(bf16_lo(ta), bf16_hi(ta)), eb = kGamma * norm * max_nan(bf16_lo(tb), bf16_hi(tb));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      sa = max_nan(sa, __shfl_xor_sync(0xffffffffu, sa, o));
+      sb = max_nan(sb, __shfl_xor_sync(0xffffffffu, sb, o));
+      ea = max_nan(ea, __shfl_xor_sync(0xffffffffu, ea, o));
+      eb = max_nan(eb, __shfl_xor_sync(0xffffffffu, eb, o));
+    }
+    // a score whose error has no bound is to be formed again, as one that is no number
+    if (!(ea < INFINITY)) sa = __uint_as_float(0x7fc00000u), ea = 0.f;
+    if (!(eb < INFINITY)) sb = __uint_as_float(0x7fc00000u), eb = 0.f;
+    float e = fmaxf(ea, eb);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
+    const int64_t unit = static_cast<int64_t>(row) * kKvHeads + g;
+    float* scores = p.scores + unit * p.width;
+    if (c == 0 && ia < v.count) scores[ia] = oka ? sa : __uint_as_float(kNoBlock);
+    if (c == 0 && ib < v.count) scores[ib] = okb ? sb : __uint_as_float(kNoBlock);
+    if (lane == 0) p.errors[unit * ((p.width + kScoreBlocks - 1) / kScoreBlocks) + blockIdx.x] = e;
   }
 }
 
 // ----------------------------------------------------------------- choice
 // A block of threads per row and KV head. The MMA's scores decide all blocks but those within the error of the k-th
 // largest; of these the score is formed again in two floats (products of bf16 are exact, sums are carried with their
-// rounding errors: 2^-44 of the terms), and the larger ones, then the lower ones, fill what is left.
-constexpr int kChooseThreads = 512;
+// rounding errors: 2^-44 of the terms), and the larger ones, then the lower ones, fill what is left. They are few unless
+// scores tie: up to kListed are compared with one another, more by a second radix select over both floats. Scores are held
+// in shared memory as ordered words, up to kHeldWords of them (else in their place in global memory).
+// Small blocks of threads for short rows: their barriers are cheap and all fit the GPU at once.
+constexpr int kHeldWords = 48 * 1024, kListed = 128;
+constexpr uint32_t kAbsent = 0, kChosen = 1;  // marks below any score's word
 
 // s + e += x, exactly but for e's own rounding.
 __device__ __forceinline__ void add_exact(float& s, float& e, float x) {
@@ -182,19 +254,29 @@ __device__ __forceinline__ void add_exact(float& s, float& e, float x) {
 // The score of block `at` for the 8 query heads at q, by one warp: as hi + lo, rounded into hi first; false if it is no
 // number. Lane (h = lane >> 2, c = lane & 3) sums 32 of the 128 dims of head h.
 __device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int lane, float& hi, float& lo) {
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + (lane >> 2) * kHeadDim) + 16 * (lane & 3);
-  const uint32_t* up = reinterpret_cast<const uint32_t*>(bounds) + 16 * (lane & 3);
-  const uint32_t* down = up + kRowValues / 2;
+  const uint4* qr = reinterpret_cast<const uint4*>(q + (lane >> 2) * kHeadDim) + 4 * (lane & 3);
+  const uint4* up = reinterpret_cast<const uint4*>(bounds) + 4 * (lane & 3);
+  const uint4* down = up + kRowValues / 8;
+  uint4 x4[4], a4[4], b4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x4[i] = __ldcg(qr + i);
+    a4[i] = __ldcg(up + i);
+    b4[i] = __ldcg(down + i);
+  }
   float s = 0.f, e = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t x = __ldg(qr + i), a = __ldg(up + i), b = __ldg(down + i);
-    const float x0 = bf16_lo(x), x1 = bf16_hi(x);
-    // of the two products one is 0 for any finite bounds; both count, so that 0 times an infinity shows
-    add_exact(s, e, __fmul_rn(x0 > 0.f ? x0 : x0 * 0.f, bf16_lo(a)));
-    add_exact(s, e, __fmul_rn(x0 < 0.f ? x0 : x0 * 0.f, bf16_lo(b)));
-    add_exact(s, e, __fmul_rn(x1 > 0.f ? x1 : x1 * 0.f, bf16_hi(a)));
-    add_exact(s, e, __fmul_rn(x1 < 0.f ? x1 : x1 * 0.f, bf16_hi(b)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t xs[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w}, as[4] = {a4[i].x, a4[i].y, a4[i].z, a4[i].w}, bs[4] = {b4[i].x, b4[i].y, b4[i].z, b4[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x0 = bf16_lo(xs[k]), x1 = bf16_hi(xs[k]);
+      // of the two products one is 0 for any finite bounds; both count, so that 0 times an infinity shows
+      add_exact(s, e, __fmul_rn(x0 > 0.f ? x0 : x0 * 0.f, bf16_lo(as[k])));
+      add_exact(s, e, __fmul_rn(x0 < 0.f ? x0 : x0 * 0.f, bf16_lo(bs[k])));
+      add_exact(s, e, __fmul_rn(x1 > 0.f ? x1 : x1 * 0.f, bf16_hi(as[k])));
+      add_exact(s, e, __fmul_rn(x1 < 0.f ? x1 : x1 * 0.f, bf16_hi(bs[k])));
+    }
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
@@ -217,155 +299,186 @@ __device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_b
   return number;
 }
 
-__global__ void __launch_bounds__(kChooseThreads) gqa_block_choose_kernel(const BlockParams p) {
-  __shared__ SelectSpace<kChooseThreads> sp;
-  __shared__ float widest[kChooseThreads / 32];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockParams p) {
+  extern __shared__ uint32_t held[];
+  __shared__ SelectSpace<THREADS> sp;
+  __shared__ float widest[THREADS / 32];
+  __shared__ int list[kListed], listed;
+  __shared__ uint64_t listed_key[kListed];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
   for (int64_t unit = blockIdx.x; unit < static_cast<int64_t>(p.rows) * kKvHeads; unit += gridDim.x) {
     const int row = static_cast<int>(unit / kKvHeads), g = static_cast<int>(unit % kKvHeads);
     const RowView v = row_view(p, row);
     const int* table = p.block_table + static_cast<int64_t>(max(v.req, 0)) * p.width;
-    float* scores = p.scores + unit * p.width;
-    float* errors = p.errors + unit * p.width;
-    auto forced = [&](int i) { return i < p.keep_first || i >= v.count - p.keep_last; };
-    // candidates; of those not forced the widest error
-    int mine = 0, held = 0;
+    const float* scores = p.scores + unit * p.width;
+    uint32_t* words = p.width <= kHeldWords ? held : reinterpret_cast<uint32_t*>(p.scores + unit * p.width);
+    // candidates and those of them that are kept in any case; the widest error
+    int2 mine = make_int2(0, 0);
     float wide = 0.f;
-    for (int i = tid; i < v.count; i += kChooseThreads) {
-      const float e = errors[i];
-      if (e == -1.f) continue;
-      ++mine;
-      if (forced(i)) ++held; else if (e < INFINITY) wide = fmaxf(wide, e);
+    const int tiles = (p.width + kScoreBlocks - 1) / kScoreBlocks;
+    for (int i = tid; i < (v.count + kScoreBlocks - 1) / kScoreBlocks; i += THREADS) wide = fmaxf(wide, __ldcg(p.errors + unit * tiles + i));
+#pragma unroll 4
+    for (int i = tid; i < v.count; i += THREADS) {
+      const float s = __ldcg(scores + i);
+      uint32_t x = kAbsent;
+      if (__float_as_uint(s) != kNoBlock) {
+        const bool fixed = i < p.keep_first || i >= v.count - p.keep_last;
+        x = fixed ? kChosen : ordered_bits(s);
+        ++mine.x;
+        mine.y += fixed;
+      }
+      words[i] = x;
     }
-    const int count = block_sum(sp, mine), fixed = block_sum(sp, held);
+    if (tid == 0) listed = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
     if (lane == 0) widest[warp] = wide;
-    __syncthreads();
+    mine = block_sum2<THREADS>(sp.sums, mine);  // (its barriers: the words and the widest errors are there too)
+    wide = widest[lane & (THREADS / 32 - 1)];  // (a power of two of warps)
 #pragma unroll
-    for (int w = 0; w < kChooseThreads / 32; ++w) wide = fmaxf(wide, widest[w]);
-    const int take = min(p.top, count) - fixed;  // of those not forced; fixed <= top
-    const bool all = count <= p.top;
-    float above_all = INFINITY, below_all = INFINITY;
-    int ties = 0;
+    for (int o = 16; o > 0; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
+    const int take = min(p.top, mine.x) - mine.y;  // of the others; mine.y <= top
+    const bool all = mine.x <= p.top;
+    // words above `above` are chosen, below `below` not; those between, and what is no finite number, are to be decided
+    uint32_t above = all ? kAbsent : 0xffffffffu, below = all ? kAbsent : 0xffffffffu;
+    bool settled = all, again = false;
     uint64_t least = 0;
-    bool settled = true;  // whether every block between the two limits is chosen
-    auto open = [&](int i) { return errors[i] != -1.f && !forced(i); };  // errors of scores formed again stay above -1
+    int ties = 0;
+    auto open = [&](uint32_t x) { return x > kChosen && (x >= kKeyInf || x == kKeyLeast || (x >= below && x <= above)); };
     if (!all && take > 0) {
-      int above = 0;
-      const uint32_t kth = block_kth<kChooseThreads, uint32_t>(sp, v.count, take, open, [&](int i) { return ordered_bits(scores[i]); }, above);
-      const float mark = __uint_as_float((kth & 0x80000000u) ? kth & 0x7fffffffu : ~kth);  // NaN if no number
-      above_all = __fadd_ru(mark, __fmul_ru(2.f, wide));
-      below_all = __fadd_rd(mark, __fmul_rd(-2.f, wide));
-      if (!isfinite(mark)) above_all = INFINITY, below_all = -INFINITY;  // decide all of them again
-    }
-    // 2: chosen, 1: to be decided, 0: not chosen
-    auto rough = [&](int i) {
-      if (errors[i] == -1.f) return 0;
-      if (all || forced(i)) return 2;
-      if (take <= 0) return 0;
-      const float s = scores[i];
-      if (!(fabsf(s) < INFINITY) || !(errors[i] < INFINITY)) return 1;
-      return s > above_all ? 2 : (s < below_all ? 0 : 1);
-    };
-    if (!all && take > 0) {
-      int sure = 0, maybe = 0;
-      for (int i = tid; i < v.count; i += kChooseThreads) {
-        const int c = rough(i);
-        sure += c == 2 && !forced(i);
-        maybe += c == 1;
+      int unused = 0;
+      const uint32_t kth = select_kth<THREADS, false, uint32_t>(sp, v.count, take, [&](int i) { return words[i]; }, unused);
+      const float mark = ordered_float(kth);
+      if (fabsf(mark) < INFINITY) {
+        above = ordered_bits(__fadd_ru(mark, __fmul_ru(2.f, wide)));
+        below = ordered_bits(__fadd_rd(mark, __fmul_rd(-2.f, wide)));
+      } else {
+        below = kKeyLeast;  // decide all of them again
       }
-      sure = block_sum(sp, sure);
-      maybe = block_sum(sp, maybe);
-      const int left = take - sure;
-      settled = left >= maybe;
-      if (!settled) {
-        // form their scores again, a warp each; marked by an error of -2 while both floats are kept
+      mine = make_int2(0, 0);  // chosen by their words, to be decided
+      for (int i = tid; i < v.count; i += THREADS) {
+        const uint32_t x = words[i];
+        if (open(x)) {
+          ++mine.y;
+          const int at = atomicAdd(&listed, 1);
+          if (at < kListed) list[at] = i;
+        } else if (x > above) {
+          ++mine.x;
+        }
+      }
+      mine = block_sum2<THREADS>(sp.sums, mine);
+      const int left = take - mine.x;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(row) * kQoHeads + g * kGroup) * kHeadDim;
+      auto formed = [&](int i) {  // block i's score, by a warp
+        float hi, lo;
+        const int64_t block = __ldcg(table + i);
+        const bool number = exact_score(q, static_cast<const __nv_bfloat16*>(p.bounds) + (block * 2 * kKvHeads + g) * kHeadDim, lane, hi, lo);
+        return number ? make_float2(hi, lo) : make_float2(INFINITY, 0.f);
+      };
+      auto key_of = [](float2 x) { return (static_cast<uint64_t>(ordered_bits(x.x)) << 32) | ordered_bits(x.y); };
+      if (left >= mine.y) {
+        settled = true;
+      } else if (mine.y <= kListed) {
+        for (int i = warp; i < mine.y; i += THREADS / 32) {
+          const uint64_t k = key_of(formed(list[i]));
+          if (lane == 0) listed_key[i] = k;
+        }
         __syncthreads();
-        for (int i0 = 32 * warp; i0 < v.count; i0 += kChooseThreads) {
+        if (tid < mine.y) {
+          const uint64_t k = listed_key[tid];
+          const int at = list[tid];
+          int better = 0;
+          for (int i = 0; i < mine.y; ++i) better += listed_key[i] > k || (listed_key[i] == k && list[i] < at);
+          words[at] = better < left ? kChosen : kAbsent;
+        }
+        __syncthreads();
+        settled = true;  // (none is left open)
+      } else {
+        again = true;
+        for (int i0 = 32 * warp; i0 < v.count; i0 += THREADS) {
           const int i = i0 + lane;
-          const int page = i < v.count && rough(i) == 1 ? __ldg(table + i) : -1;
-          for (unsigned m = __ballot_sync(0xffffffffu, page >= 0); m != 0; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int64_t block = __shfl_sync(0xffffffffu, page, src);
-            float hi, lo;
-            const bool number = exact_score(static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(row) * kQoHeads + g * kGroup) * kHeadDim,
-                                            static_cast<const __nv_bfloat16*>(p.bounds) + (block * 2 * kKvHeads + g) * kHeadDim, lane, hi, lo);
-            if (lane == 0) p.again[unit * p.width + i0 + src] = make_float2(number ? hi : INFINITY, number ? lo : 0.f);
+          for (unsigned m = __ballot_sync(0xffffffffu, i < v.count && open(words[i])); m != 0; m &= m - 1) {
+            const int at = i0 + __ffs(m) - 1;
+            const float2 x = formed(at);
+            if (lane == 0) p.again[unit * p.width + at] = x;
           }
         }
         __syncthreads();
-        int above = 0;
-        least = block_kth<kChooseThreads, uint64_t>(
-            sp, v.count, left, [&](int i) { return rough(i) == 1; },
-            [&](int i) {
-              const float2 x = p.again[unit * p.width + i];
-              return (static_cast<uint64_t>(ordered_bits(x.x)) << 32) | ordered_bits(x.y);
-            }, above);
-        ties = left - above;
+        least = select_kth<THREADS, false, uint64_t>(
+            sp, v.count, left, [&](int i) { return open(words[i]) ? key_of(p.again[unit * p.width + i]) : uint64_t{0}; }, ties);
       }
     }
     int* out = p.blocks + unit * p.top;
-    int at = 0;
-    for (int i0 = 0; i0 < v.count; i0 += kChooseThreads) {
-      const int i = i0 + tid;
-      const int c = i < v.count ? rough(i) : 0;
-      bool stay = c == 2 || (c == 1 && settled), tie = false;
-      if (c == 1 && !settled) {
-        const float2 x = p.again[unit * p.width + i];
-        const uint64_t k = (static_cast<uint64_t>(ordered_bits(x.x)) << 32) | ordered_bits(x.y);
-        tie = k == least;
-        stay = k > least;
-      }
-      int tied, kept;
-      const int tie_rank = block_rank(sp, tie, tied);
-      stay = stay || (tie && tie_rank < ties);
-      ties -= min(ties, tied);
-      const int rank = block_rank(sp, stay, kept);
-      if (stay && at + rank < p.top) out[at + rank] = i;
-      at += kept;
-    }
-    for (int i = min(at, p.top) + tid; i < p.top; i += kChooseThreads) out[i] = -1;
+    const int chosen = all ? mine.x : p.top;
+    select_in_order<THREADS, false, 1>(
+        sp, v.count, ties,
+        [&](int i) {
+          const uint32_t x = words[i];
+          if (x <= kChosen) return x == kChosen ? 2 : 0;
+          if (all) return 2;
+          if (!open(x)) return x > above ? 2 : 0;
+          if (!again) return settled ? 2 : 0;
+          const float2 y = p.again[unit * p.width + i];
+          const uint64_t k = (static_cast<uint64_t>(ordered_bits(y.x)) << 32) | ordered_bits(y.y);
+          return k > least ? 2 : (k == least ? 1 : 0);
+        },
+        [](int) { return 0; },
+        [&](int i, int, int at, bool stay) {
+          if (stay && at < p.top) out[at] = i;
+        });
+    for (int i = chosen + tid; i < p.top; i += THREADS) out[i] = -1;
     __syncthreads();
   }
+}
+
+template <int THREADS>
+static cudaError_t launch_choose(const BlockParams& p, cudaStream_t stream) {
+  static std::atomic<int> configured[kMaxDevices];
+  const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_block_choose_kernel<THREADS>), kHeldWords * 4);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(p.rows) * kKvHeads;
+  return launch_chained(gqa_block_choose_kernel<THREADS>, dim3(units < (1 << 20) ? units : (1 << 20)), THREADS,
+                        p.width <= kHeldWords ? p.width * 4 : 0, stream, 1, p);
 }
 
 cudaError_t launch_block_select(const BlockParams& p, cudaStream_t stream) {
   const dim3 grid((p.width + kScoreBlocks - 1) / kScoreBlocks, p.rows < 65535 ? p.rows : 65535);
-  gqa_block_score_kernel<<<grid, 128, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_chained(gqa_block_score_kernel, grid, 128, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
-  const int64_t units = static_cast<int64_t>(p.rows) * kKvHeads;
-  gqa_block_choose_kernel<<<static_cast<int>(units < (1 << 20) ? units : (1 << 20)), kChooseThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.width <= 1024 ? launch_choose<128>(p, stream) : launch_choose<512>(p, stream);
 }
 
 // ------------------------------------------------------------------ slots
+// A warp per listed block, a lane per token.
 __global__ void __launch_bounds__(256) gqa_block_slots_kernel(const BlockParams p) {
+  pdl_wait();
   pdl_launch_dependents();
-  const int64_t per_row = static_cast<int64_t>(p.top) * p.page_size, total = p.rows * per_row;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; x < kKvHeads * total; x += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int g = static_cast<int>(x / total);
-    const int64_t y = x - g * total;
-    const int row = static_cast<int>(y / per_row), z = static_cast<int>(y - row * per_row);
-    const int j = z / p.page_size, t = z - j * p.page_size;
+  const int lane = threadIdx.x & 31;
+  const int64_t per_row = static_cast<int64_t>(p.top) * p.page_size;
+  for (int64_t unit = blockIdx.x; unit < static_cast<int64_t>(p.rows) * kKvHeads; unit += gridDim.x) {
+    const int row = static_cast<int>(unit / kKvHeads), g = static_cast<int>(unit % kKvHeads);
     const RowView v = row_view(p, row);
-    const int i = __ldg(p.blocks + (static_cast<int64_t>(row) * kKvHeads + g) * p.top + j);
-    int slot = -1;
-    if (i >= 0 && i < v.count && static_cast<int64_t>(i) * p.page_size + t < v.n) {
-      const int block = __ldg(p.block_table + static_cast<int64_t>(v.req) * p.width + i);
-      if (static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks)) slot = block * p.page_size + t;
+    int* slots = p.slots + static_cast<int64_t>(g) * p.rows * per_row + row * per_row;
+    for (int j = (threadIdx.x >> 5) + 8 * blockIdx.y; j < p.top; j += 8 * gridDim.y) {
+      const int i = __ldcg(p.blocks + unit * p.top + j);
+      int block = -1, tokens = 0;
+      if (i >= 0 && i < v.count) {
+        block = __ldcg(p.block_table + static_cast<int64_t>(v.req) * p.width + i);
+        tokens = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks) ? min(p.page_size, v.n - i * p.page_size) : 0;
+      }
+      for (int t = lane; t < p.page_size; t += 32) slots[static_cast<int64_t>(j) * p.page_size + t] = t < tokens ? block * p.page_size + t : -1;
     }
-    p.slots[x] = slot;
   }
 }
 
 cudaError_t launch_block_slots(const BlockParams& p, int sm_count, cudaStream_t stream) {
-  const int64_t n = static_cast<int64_t>(kKvHeads) * p.rows * p.top * p.page_size;
-  int64_t grid = (n + 255) / 256;
-  if (grid > 8 * sm_count) grid = 8 * sm_count;
-  gqa_block_slots_kernel<<<static_cast<int>(grid), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int64_t units = static_cast<int64_t>(p.rows) * kKvHeads;
+  const int x = static_cast<int>(units < (1 << 20) ? units : (1 << 20)), most = (8 * sm_count + x - 1) / x;
+  const int y = (p.top + 7) / 8;
+  return launch_chained(gqa_block_slots_kernel, dim3(x, y < most ? y : most), 256, 0, stream, 1, p);
 }
 
 }  // namespace gqa

@@ -24,24 +24,23 @@ bool table_ok(int page_size, int num_blocks, int width) {
          static_cast<int64_t>(width) * page_size <= INT_MAX;
 }
 
-// The split decode's share of a workspace: outputs and LSEs of 2 parts a CTA and `whole` more, and the split records.
+// The split decode's share of a workspace: outputs and LSEs of 2 parts a CTA, and the split records.
 struct DecodeSpace {
   size_t o, lse, rec, end;
-  DecodeSpace(const gqa::PlanConfig& plan, int64_t whole, size_t at) {
-    const size_t ctas = static_cast<size_t>(plan.tier1_ctas) + plan.tier2_ctas;
-    const size_t parts = (2 * ctas + static_cast<size_t>(whole)) * gqa::kKvHeads;
+  DecodeSpace(const gqa::PlanConfig& plan, size_t at) {
+    const size_t ctas = static_cast<size_t>(plan.tier1_ctas) + plan.tier2_ctas, parts = 2 * ctas * gqa::kKvHeads;
     o = at;
-    lse = o + round256(parts * kPartBytes);
+    lse = o + parts * kPartBytes;
     rec = lse + round256(parts * gqa::kGroup * sizeof(float));
     end = rec + round256(ctas * 16);
   }
 };
 
-gqa::DecodeParams decode_params(const gqa::DecodeSetup& setup, const DecodeSpace& at, char* ws, float sm_scale) {
+gqa::DecodeParams decode_params(const gqa::DecodeSetup& setup, void* part_o, void* part_lse, void* split_rec, float sm_scale) {
   gqa::DecodeParams d{};
-  d.part_o = reinterpret_cast<float*>(ws + at.o);
-  d.part_lse = reinterpret_cast<float*>(ws + at.lse);
-  d.split_rec = reinterpret_cast<int4*>(ws + at.rec);
+  d.part_o = static_cast<float*>(part_o);
+  d.part_lse = static_cast<float*>(part_lse);
+  d.split_rec = static_cast<int4*>(split_rec);
   d.err = setup.err;
   d.epoch = setup.epoch;
   d.plan = setup.plan;
@@ -69,13 +68,21 @@ gqa::MergeParams merge_params(const gqa::DecodeParams& d) {
   return m;
 }
 
+// Parts of the prefixes, then of the own tokens: one array of outputs, one of LSEs.
 struct SharedSpace {
-  size_t start, pre_o, pre_lse;
-  DecodeSpace own;
-  SharedSpace(const gqa::DecodeSetup& setup, int batch, int groups)
-      : start(0), pre_o(round256((static_cast<size_t>(groups) + 1) * sizeof(int64_t))),
-        pre_lse(pre_o + gqa::shared_prefix_blocks(batch, setup.sm_count) * kPartBytes),
-        own(setup.plan, batch, pre_lse + round256(gqa::shared_prefix_blocks(batch, setup.sm_count) * gqa::kGroup * sizeof(float))) {}
+  int64_t own_base, whole_base;
+  size_t start, o, lse, rec, end;
+  SharedSpace(const gqa::DecodeSetup& setup, int batch, int groups) {
+    const int64_t ctas = static_cast<int64_t>(setup.plan.tier1_ctas) + setup.plan.tier2_ctas;
+    own_base = gqa::shared_prefix_blocks(batch, setup.sm_count);
+    whole_base = 2 * ctas;
+    const size_t parts = static_cast<size_t>(own_base + (whole_base + batch) * gqa::kKvHeads);
+    start = 0;
+    o = round256((static_cast<size_t>(groups) + 1) * sizeof(int64_t));
+    lse = o + parts * kPartBytes;
+    rec = lse + round256(parts * gqa::kGroup * sizeof(float));
+    end = rec + round256(static_cast<size_t>(ctas) * 16);
+  }
 };
 
 struct SelectSpaceLayout {
@@ -84,7 +91,7 @@ struct SelectSpaceLayout {
     const size_t n = static_cast<size_t>(rows) * gqa::kKvHeads * static_cast<size_t>(width);
     scores = 0;
     errors = round256(n * sizeof(float));
-    again = errors + round256(n * sizeof(float));
+    again = errors + round256(static_cast<size_t>(rows) * gqa::kKvHeads * ((static_cast<size_t>(width) + 15) / 16) * sizeof(float));
     end = again + round256(n * sizeof(float2));
   }
 };
@@ -102,7 +109,7 @@ extern "C" {
 size_t gqa_shared_paged_decode_ws_size(int batch, int groups, int cache_format) {
   gqa::DecodeSetup setup;
   if (batch <= 0 || batch > (1 << 20) || groups < 0 || groups > (1 << 20) || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
-  return SharedSpace(setup, batch, groups).own.end;
+  return SharedSpace(setup, batch, groups).end;
 }
 
 int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_indptr,
@@ -130,9 +137,12 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   const int rc = gqa::decode_setup(fp8, &setup);
   if (rc != GQA_OK) return rc;
   const SharedSpace at(setup, batch, groups);
-  if (workspace_bytes < at.own.end) return GQA_ERR_WORKSPACE;
+  if (workspace_bytes < at.end) return GQA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  gqa::DecodeParams d = decode_params(setup, at.own, ws, sm_scale);
+  float* part_o = reinterpret_cast<float*>(ws + at.o);
+  float* part_lse = reinterpret_cast<float*>(ws + at.lse);
+  gqa::DecodeParams d = decode_params(setup, part_o + at.own_base * (gqa::kHeadDim * gqa::kGroup),
+                                      part_lse + at.own_base * gqa::kGroup, ws + at.rec, sm_scale);
   d.q = q;
   d.k_cache = k_cache;
   d.v_cache = v_cache;
@@ -143,7 +153,7 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   d.batch = batch;
   d.num_pages_check = num_pages;
   d.index_count = index_count;
-  d.whole_base = 2 * (static_cast<int64_t>(setup.plan.tier1_ctas) + setup.plan.tier2_ctas);
+  d.whole_base = at.whole_base;
   gqa::SharedParams p{};
   p.q = q;
   p.k_cache = k_cache;
@@ -157,10 +167,9 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   p.group_start = reinterpret_cast<int64_t*>(ws + at.start);
   p.pre_ctas = groups > 0 && prefix_count > 0 ? setup.sm_count : 0;
   p.wait_limit_ns = setup.wait_limit_ns;
-  p.pre_o = reinterpret_cast<float*>(ws + at.pre_o);
-  p.pre_lse = reinterpret_cast<float*>(ws + at.pre_lse);
-  p.own_o = d.part_o;
-  p.own_lse = d.part_lse;
+  p.part_o = part_o;
+  p.part_lse = part_lse;
+  p.own_base = at.own_base;
   p.whole_base = d.whole_base;
   p.plan = setup.plan;
   p.scale_log2 = d.scale_log2;
@@ -240,7 +249,7 @@ int gqa_block_select(const void* q, const void* bounds, const int32_t* block_tab
 size_t gqa_block_sparse_decode_ws_size(int rows, int top, int page_size) {
   gqa::DecodeSetup setup;
   if (!sparse_sizes_ok(rows, top, page_size) || gqa::decode_setup(false, &setup) != GQA_OK) return 0;
-  return DecodeSpace(setup.plan, 0, round256(sizeof(int32_t) * gqa::kKvHeads * static_cast<size_t>(rows) * top * page_size)).end;
+  return DecodeSpace(setup.plan, round256(sizeof(int32_t) * gqa::kKvHeads * static_cast<size_t>(rows) * top * page_size)).end;
 }
 
 int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* blocks,
@@ -262,7 +271,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
   const int rc = gqa::decode_setup(false, &setup);
   if (rc != GQA_OK) return rc;
   const int total = rows * (top * page_size);
-  const DecodeSpace at(setup.plan, 0, round256(sizeof(int32_t) * gqa::kKvHeads * static_cast<size_t>(total)));
+  const DecodeSpace at(setup.plan, round256(sizeof(int32_t) * gqa::kKvHeads * static_cast<size_t>(total)));
   if (workspace_bytes < at.end) return GQA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   gqa::BlockParams p{};
@@ -278,7 +287,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
   p.width = page_table_width;
   p.top = top;
   if (gqa::launch_block_slots(p, setup.sm_count, stream) != cudaSuccess) return GQA_ERR_LAUNCH;
-  gqa::DecodeParams d = decode_params(setup, at, ws, sm_scale);
+  gqa::DecodeParams d = decode_params(setup, ws + at.o, ws + at.lse, ws + at.rec, sm_scale);
   d.q = q;
   d.k_cache = k_cache;
   d.v_cache = v_cache;
@@ -297,7 +306,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
 size_t gqa_paged_decode_weighted_ws_size(int index_count, int cache_format) {
   gqa::DecodeSetup setup;
   if (index_count < 0 || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
-  return DecodeSpace(setup.plan, 0, round256(static_cast<size_t>(index_count) * gqa::kQoHeads * sizeof(float))).end;
+  return DecodeSpace(setup.plan, round256(static_cast<size_t>(index_count) * gqa::kQoHeads * sizeof(float))).end;
 }
 
 int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_indptr,
@@ -321,10 +330,10 @@ int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_
   gqa::DecodeSetup setup;
   const int rc = gqa::decode_setup(fp8, &setup);
   if (rc != GQA_OK) return rc;
-  const DecodeSpace at(setup.plan, 0, round256(static_cast<size_t>(index_count) * gqa::kQoHeads * sizeof(float)));
+  const DecodeSpace at(setup.plan, round256(static_cast<size_t>(index_count) * gqa::kQoHeads * sizeof(float)));
   if (workspace_bytes < at.end) return GQA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  gqa::DecodeParams d = decode_params(setup, at, ws, sm_scale);
+  gqa::DecodeParams d = decode_params(setup, ws + at.o, ws + at.lse, ws + at.rec, sm_scale);
   d.q = q;
   d.k_cache = k_cache;
   d.v_cache = v_cache;
@@ -365,7 +374,7 @@ int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* 
   const int rc = gqa::current_device_sms(&sms);
   if (rc != GQA_OK) return rc;
   const gqa::EvictParams p{weights, kv_indptr, kv_indices, weights_out, new_indptr, new_indices, freed_indptr, freed,
-                           budget, keep_first, keep_last, batch, width, index_count};
+                           budget, keep_first, keep_last, batch, width, index_count, 1, 0};
   return launched(gqa::launch_evict(p, stream));
 }
 

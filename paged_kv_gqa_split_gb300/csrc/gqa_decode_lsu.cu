@@ -461,7 +461,9 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
   // Selected-token mode is launched as a dependent of the slot-resolving
   // kernel: nothing that kernel writes is read before this returns. Without a
   // programmatic dependency (every other launch) it returns at once.
-  pdl_wait();
+  // kFormParts runs beside the kernel that it depends on, reads nothing of its,
+  // and waits for it at the end: what waits for this grid then waits for both.
+  if constexpr (FORM != kFormParts) pdl_wait();
   if (p.skip_if_set != nullptr && *p.skip_if_set != 0) return;
 
   const uint8_t* __restrict__ kc = static_cast<const uint8_t*>(p.k_cache);
@@ -854,6 +856,9 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
   }
   cp_async_wait<0>();
   __syncwarp();
+  if constexpr (FORM == kFormParts) {
+    if (blockIdx.x + 1 == gridDim.x) pdl_wait();
+  }
   if (one_wave) {
     // count this warp's split pieces (one fence publishes all of their
     // partials), then merge the shares that fell to it; the stage and

@@ -343,10 +343,11 @@ struct SharedParams {  // gqa_shared.cu
   void* out;
   float* lse;                 // or NULL
   int64_t* group_start;       // [groups + 1] first step of each group's prefix (written by the prefix pass)
-  float* pre_o;               // parts of the prefixes, blocks of [128 dims][8 heads] and 8 LSEs: [batch][4], [pre_ctas][32]
-  float* pre_lse;
-  const float* own_o;         // parts of the own tokens (DecodeParams::part_o, part_lse)
-  const float* own_lse;
+  // parts, blocks of [128 dims][8 heads] and 8 LSEs: the prefixes' [batch][4] and [pre_ctas][32], from own_base on the own
+  // tokens' (DecodeParams::part_o, part_lse)
+  float* part_o;
+  float* part_lse;
+  int64_t own_base;
   int64_t whole_base;
   PlanConfig plan;
   float scale_log2;
@@ -375,9 +376,9 @@ struct BlockParams {  // gqa_blocks.cu
   const int* token_to_req;  // [rows]
   const int* lens;          // [rows]
   int* blocks;              // [rows][4][top]
-  float* scores;            // workspace: [rows][4][width] scores, their error bounds (-1: no block), scores formed again
-  float* errors;
-  float2* again;
+  float* scores;            // workspace: [rows][4][width] scores, NaN of bits kNoBlock where there is none
+  float* errors;            // [rows][4][ceil(width / 16)] error bounds of 16 scores
+  float2* again;            // [rows][4][width] scores formed again
   int* slots;               // [4][rows * top * page_size]
   int rows, requests, page_size, num_blocks, width, top, keep_first, keep_last;
 };
@@ -405,8 +406,30 @@ struct EvictParams {  // gqa_weights.cu
   int* freed_indptr;
   int* freed;
   int budget, keep_first, keep_last, batch, width, index_count;
+  int cluster, held;  // blocks a sequence, words that one holds in shared memory (set by the launch)
 };
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
+
+// Launches a kernel that begins with pdl_wait() so that it may start while the one before it on the stream ends, over
+// clusters of `cluster` blocks.
+template <typename Params>
+inline cudaError_t launch_chained(void (*kernel)(Params), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster,
+                                  const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // A tensor map of 2 or 3 dimensions (sizes and boxes from the contiguous one on, `pitch` bytes between steps of the
 // others, 128-byte swizzle). False if the driver call is missing or refuses.

@@ -1,7 +1,10 @@
 // Decode of a batch whose sequences share prefixes: what a sequence reads is its group's prefix, then its own tokens.
 //   out = (sum over prefix and own tokens of 2^(s - m) v) / (the same sum of 2^(s - m))
 // is formed from parts: the prefix's (computed here, once a group for all its sequences), the own tokens' (the split
-// decode, kFormParts) and their join by log-sum-exp weights.
+// decode, kFormParts, which fills the SMs as the prefix pass leaves them) and their join by log-sum-exp weights.
+//
+// These kernels start while the ones before them on the stream end, and what those wrote is read with ld.cg, behind the
+// wait: the non-coherent load is for words that no kernel under way writes.
 #include <cuda_runtime.h>
 
 #include "gqa_common.cuh"
@@ -15,15 +18,15 @@ __device__ __forceinline__ int group_of(const SharedParams& p, int b) {
   int lo = 0, hi = p.groups;  // group_indptr[lo] <= b wherever any entry is
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.group_indptr + mid) <= b) lo = mid; else hi = mid;
+    if (__ldcg(p.group_indptr + mid) <= b) lo = mid; else hi = mid;
   }
-  return p.groups > 0 && __ldg(p.group_indptr + lo) <= b && b < __ldg(p.group_indptr + lo + 1) ? lo : -1;
+  return p.groups > 0 && __ldcg(p.group_indptr + lo) <= b && b < __ldcg(p.group_indptr + lo + 1) ? lo : -1;
 }
 
 // First prefix token of group g and their count, cut to the table.
 __device__ __forceinline__ int prefix_range(const SharedParams& p, int g, int& first) {
-  first = max(0, min(__ldg(p.prefix_indptr + g), p.prefix_count));
-  return max(0, min(__ldg(p.prefix_indptr + g + 1), p.prefix_count) - first);
+  first = max(0, min(__ldcg(p.prefix_indptr + g), p.prefix_count));
+  return max(0, min(__ldcg(p.prefix_indptr + g + 1), p.prefix_count) - first);
 }
 
 // ----------------------------------------------------------------- prefix
@@ -79,8 +82,8 @@ struct PrefixCfg {
 __device__ __forceinline__ int64_t group_steps(const SharedParams& p, int g, int& tiles, int& seq0, int& members) {
   int first;
   tiles = (prefix_range(p, g, first) + kStep - 1) / kStep;
-  seq0 = max(0, min(__ldg(p.group_indptr + g), p.batch));
-  members = max(0, min(__ldg(p.group_indptr + g + 1), p.batch) - seq0);
+  seq0 = max(0, min(__ldcg(p.group_indptr + g), p.batch));
+  members = max(0, min(__ldcg(p.group_indptr + g + 1), p.batch) - seq0);
   return static_cast<int64_t>((members + kUnitSeqs - 1) / kUnitSeqs) * kKvHeads * tiles;
 }
 
@@ -131,6 +134,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
   auto bar = [&](int i) { return base + C::kBarOff + 8u * static_cast<uint32_t>(i); };
   __shared__ int64_t warp_steps[kPreThreads / 32], begin_s;
   __shared__ int begin_g;
+  pdl_wait();
+  pdl_launch_dependents();  // the own tokens' decode: by now all that it reads is there
 
   // total steps, then where this CTA's run begins
   Walk walk;
@@ -211,14 +216,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
         const uint32_t to = (c >> 3) * kHalfTile;
         while (good && walk.next(p)) {
           int t = walk.step0 * kStep + 32 * warp + lane;
-          int id = t < walk.n ? __ldg(p.prefix_indices + walk.first + t) : -1;
+          int id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;
 #pragma unroll 1
           for (int j = 0; j < walk.steps && good; ++j) {
             const bool live = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
             const unsigned mask = __ballot_sync(0xffffffffu, live);
             const int page = live ? id : 0;
             t += kStep;
-            id = t < walk.n ? __ldg(p.prefix_indices + walk.first + t) : -1;  // of the next step, behind this one's copies
+            id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;  // of the next step, behind this one's copies
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
               if (filled >= C::kSlots) good = wait(C::kFree + s, ph, kErrTimeoutEmpty);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
           if (more) {
             if (akv == 0) {
               const int t = (ahead.step0 + aj) * kStep + 32 * warp + lane;
-              const int id = t < ahead.n ? __ldg(p.prefix_indices + ahead.first + t) : -1;
+              const int id = t < ahead.n ? __ldcg(p.prefix_indices + ahead.first + t) : -1;
               const bool live = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
               mask = __ballot_sync(0xffffffffu, live);
               page = live ? id : 0;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 if (lane == 0) reinterpret_cast<volatile float*>(sm + C::kTopOff)[4 * info + warp] = top;
                 const int t = (walk.step0 + j) * kStep + 32 * warp + lane;
-                const int id = t < walk.n ? __ldg(p.prefix_indices + walk.first + t) : -1;
+                const int id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;
                 const unsigned mk = __ballot_sync(0xffffffffu, static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages));
                 if (lane == 0) reinterpret_cast<volatile unsigned*>(sm + C::kMaskOff)[4 * info + warp] = mk;
               }
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
 #pragma unroll 4
       for (int i = 0; i < kSeqTile; ++i) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (i < seqs) x = __ldg(from + i * (kQoHeads * kHeadDim / 8));
+        if (i < seqs) x = __ldcg(from + i * (kQoHeads * kHeadDim / 8));
         x = make_uint4(x.x ^ sign, x.y ^ sign, x.z ^ sign, x.w ^ sign);
         if constexpr (F8) {
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       const bool begins = walk.step0 == 0;
       const int64_t block = begins ? static_cast<int64_t>(seq + i) * kKvHeads + walk.head
                                    : static_cast<int64_t>(p.batch) * kKvHeads + static_cast<int64_t>(blockIdx.x) * kUnitSeqs + a * kSeqTile + i;
-      float* po = p.pre_o + block * (kHeadDim * kGroup) + h;
+      float* po = p.part_o + block * (kHeadDim * kGroup) + h;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
 #pragma unroll
           for (int k = 0; k < 32; ++k) po[(32 * c + k) * kGroup] = __uint_as_float(o[k]) * inv;
       }
-      if (i < seqs) p.pre_lse[block * kGroup + h] = l == 0.f ? -INFINITY : m - C::kShift + log2f(l);
+      if (i < seqs) p.part_lse[block * kGroup + h] = l == 0.f ? -INFINITY : m - C::kShift + log2f(l);
       tc_fence_before();
     }
   }
@@ -607,67 +612,125 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
 }
 
 // ------------------------------------------------------------------- join
-// A block per sequence and KV head, a thread per dim: the parts' running join by 2^(LSE - max).
-struct Join {
-  float m[8], den[8], acc[8];
-  __device__ __forceinline__ void init() {
-#pragma unroll
-    for (int h = 0; h < 8; ++h) m[h] = -INFINITY, den[h] = acc[h] = 0.f;
-  }
-  __device__ __forceinline__ void add(const float* o, const float* lse) {  // a part's row of this dim, its LSEs
-    const float4 la = __ldcg(reinterpret_cast<const float4*>(lse)), lb = __ldcg(reinterpret_cast<const float4*>(lse) + 1);
-    const float4 oa = __ldcg(reinterpret_cast<const float4*>(o)), ob = __ldcg(reinterpret_cast<const float4*>(o) + 1);
-    const float l8[8] = {la.x, la.y, la.z, la.w, lb.x, lb.y, lb.z, lb.w}, o8[8] = {oa.x, oa.y, oa.z, oa.w, ob.x, ob.y, ob.z, ob.w};
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      const float mn = fmaxf(m[h], l8[h]), sh = mn == -INFINITY ? 0.f : mn, sc = ex2(m[h] - sh), wt = ex2(l8[h] - sh);
-      den[h] = den[h] * sc + wt;
-      acc[h] = acc[h] * sc + wt * o8[h];
-      m[h] = mn;
-    }
-  }
-};
+// A block per sequence and KV head, a thread per dim. The parts are taken 16 at a time: a thread per part and head finds
+// the part and its LSE, their largest gives the weights 2^(LSE - max), and every thread sums its dim of the parts, whose
+// loads do not depend on one another. Bound by two round trips of loads, and by 4 KB a part.
+constexpr int kJoinParts = 16;
 
 __global__ void __launch_bounds__(kHeadDim) gqa_shared_join_kernel(const SharedParams p) {
-  const int d = threadIdx.x, g = blockIdx.x % kKvHeads;
-  constexpr int kBlock = kHeadDim * kGroup;
-  const int total = max(0, min(__ldg(p.kv_indptr + p.batch), p.index_count));
-  for (int b = blockIdx.x / kKvHeads; b < p.batch; b += gridDim.x / kKvHeads) {
-    Join j;
-    j.init();
-    const int group = p.pre_ctas > 0 ? group_of(p, b) : -1;
-    int tiles = 0, seq0, members;
-    if (group >= 0) group_steps(p, group, tiles, seq0, members);
-    if (tiles > 0) {  // the prefix's pieces: the first in the sequence's block, the others in their CTA's
-      const int64_t run = steps_per_cta(__ldcg(p.group_start + p.groups), p.pre_ctas);
-      const int64_t first = __ldcg(p.group_start + group) + (static_cast<int64_t>((b - seq0) / kUnitSeqs) * kKvHeads + g) * tiles;
-      const int64_t cta0 = first / run, pieces = min((first + tiles - 1) / run, static_cast<int64_t>(p.pre_ctas - 1)) - cta0 + 1;
-      for (int i = 0; i < pieces; ++i) {
-        const int64_t part = i == 0 ? static_cast<int64_t>(b) * kKvHeads + g
-                                    : static_cast<int64_t>(p.batch) * kKvHeads + (cta0 + i) * kUnitSeqs + (b - seq0) % kUnitSeqs;
-        j.add(p.pre_o + part * kBlock + d * kGroup, p.pre_lse + part * kGroup);
-      }
-    }
-    const int lo = max(0, min(__ldg(p.kv_indptr + b), total)), hi = min(__ldg(p.kv_indptr + b + 1), total);
-    if (hi > lo) {
-      const Plan pl = make_plan(total, p.plan);
-      const SeqSplit sp = seq_split(pl, lo, hi);
-      const int n = static_cast<int>(sp.last_cta - sp.first_cta) + 1;
-      for (int i = 0; i < n; ++i) {
-        const int64_t sid = n == 1 ? p.whole_base + b : slot_id(sp.first_cta + i, i == 0 ? sp.first_slot : 0);
-        const int64_t at = sid * kKvHeads + g;
-        j.add(p.own_o + at * kBlock + d * kGroup, p.own_lse + at * kGroup);
-      }
-    }
-    __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(p.out) + (static_cast<int64_t>(b) * kQoHeads + g * kGroup) * kHeadDim + d;
+  __shared__ float lse_s[kJoinParts][kGroup];
+  __shared__ __align__(16) float weight_s[kJoinParts][kGroup];
+  __shared__ int64_t part_s[kJoinParts];
+  constexpr int kPart = kHeadDim * kGroup;
+  const int tid = threadIdx.x, g = blockIdx.x % kKvHeads;
+  // What the call's inputs tell is read ahead of the wait: the kernels before this one do not write it. Steps before
+  // each group and in all, where a thread a group can count them; else the prefix pass has left them.
+  const bool few = p.groups <= kHeadDim;
+  __shared__ int64_t start_s[kHeadDim + 1];
+  if (few && p.pre_ctas > 0) {
+    int t, s0, m;
+    int64_t upto = tid < p.groups ? group_steps(p, tid, t, s0, m) : 0;
 #pragma unroll
-    for (int h = 0; h < 8; ++h) ob[h * kHeadDim] = __float2bfloat16_rn(j.den[h] == 0.f ? 0.f : j.acc[h] / j.den[h]);
-    if (p.lse != nullptr && d < kGroup) {
-      float mm = j.m[0], dd = j.den[0];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += up;
+    }
+    if ((tid & 31) == 31) part_s[tid >> 5] = upto;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w) upto += part_s[w];
+    start_s[tid + 1] = upto;
+    if (tid == 0) start_s[0] = 0;
+    __syncthreads();
+  } else if (!few) {
+    pdl_wait();
+  }
+  const int total = max(0, min(__ldcg(p.kv_indptr + p.batch), p.index_count));
+  bool waited = false;
+  for (int b = blockIdx.x / kKvHeads; b < p.batch; b += gridDim.x / kKvHeads) {
+    // pieces of the prefix: the first in the sequence's block, the others in their CTA's
+    int pre = 0, own = 0, cta0 = 0, local = 0;
+    const int lo = max(0, min(__ldcg(p.kv_indptr + b), total)), hi = min(__ldcg(p.kv_indptr + b + 1), total);
+    const int group = p.pre_ctas > 0 ? group_of(p, b) : -1;
+    if (group >= 0) {
+      int tiles, seq0, members;
+      group_steps(p, group, tiles, seq0, members);
+      if (tiles > 0) {
+        const int64_t run = steps_per_cta(few ? start_s[p.groups] : __ldcg(p.group_start + p.groups), p.pre_ctas);
+        const int64_t first = (few ? start_s[group] : __ldcg(p.group_start + group)) + (static_cast<int64_t>((b - seq0) / kUnitSeqs) * kKvHeads + g) * tiles;
+        cta0 = static_cast<int>(first / run);
+        pre = min(static_cast<int>((first + tiles - 1) / run), p.pre_ctas - 1) - cta0 + 1;
+        local = (b - seq0) % kUnitSeqs;
+      }
+    }
+    SeqSplit sp{0, 0, 0};
+    if (hi > lo) {
+      sp = seq_split(make_plan(total, p.plan), lo, hi);
+      own = static_cast<int>(sp.last_cta - sp.first_cta) + 1;
+    }
+    if (!waited) pdl_wait();
+    waited = true;
+    auto part_of = [&](int i) -> int64_t {
+      if (i < pre) return i == 0 ? static_cast<int64_t>(b) * kKvHeads + g : static_cast<int64_t>(p.batch) * kKvHeads + (cta0 + i) * kUnitSeqs + local;
+      i -= pre;
+      const int64_t sid = own == 1 ? p.whole_base + b : slot_id(sp.first_cta + i, i == 0 ? sp.first_slot : 0);
+      return p.own_base + sid * kKvHeads + g;
+    };
+    float m[8], den[8], acc[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) m[h] = -INFINITY, den[h] = acc[h] = 0.f;
+    for (int i0 = 0; i0 < pre + own; i0 += kJoinParts) {
+      const int n = min(kJoinParts, pre + own - i0);
+      const int i = tid >> 3, h = tid & 7;
+      __syncthreads();  // the parts before have been read
+      float l = -INFINITY;
+      if (i < n) {
+        const int64_t part = part_of(i0 + i);
+        l = __ldcg(p.part_lse + part * kGroup + h);
+        if (h == 0) part_s[i] = part;
+      }
+      lse_s[i][h] = l;
+      __syncthreads();
+      float top = -INFINITY;  // of head h over these parts (NaN aside: it goes into its own part's weight)
+#pragma unroll
+      for (int k = 0; k < kJoinParts; ++k) top = fmaxf(top, lse_s[k][h]);
+      // head h's running maximum is the same in every thread that holds it
+      float mh = m[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) mh = h == k ? m[k] : mh;
+      const float mn = fmaxf(mh, top);
+      weight_s[i][h] = ex2(l - (mn == -INFINITY ? 0.f : mn));
+      // every thread: all heads' new maxima, and what was summed under the old ones
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float t = fmaxf(m[k], __shfl_sync(0xffffffffu, top, k));
+        const float sc = ex2(m[k] - (t == -INFINITY ? 0.f : t));
+        m[k] = t;
+        den[k] *= sc;
+        acc[k] *= sc;
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float4* o = reinterpret_cast<const float4*>(p.part_o + part_s[k] * kPart + tid * kGroup);
+        const float4 oa = __ldcg(o), ob = __ldcg(o + 1);
+        const float4 wa = *reinterpret_cast<const float4*>(weight_s[k]), wb = *reinterpret_cast<const float4*>(weight_s[k] + 4);
+        const float o8[8] = {oa.x, oa.y, oa.z, oa.w, ob.x, ob.y, ob.z, ob.w}, w8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          den[e] += w8[e];
+          acc[e] += w8[e] * o8[e];
+        }
+      }
+    }
+    __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(p.out) + (static_cast<int64_t>(b) * kQoHeads + g * kGroup) * kHeadDim + tid;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) ob[h * kHeadDim] = __float2bfloat16_rn(den[h] == 0.f ? 0.f : acc[h] / den[h]);
+    if (p.lse != nullptr && tid < kGroup) {
+      float mm = m[0], dd = den[0];
 #pragma unroll
       for (int h = 1; h < 8; ++h)
-        if (d == h) mm = j.m[h], dd = j.den[h];
-      p.lse[static_cast<int64_t>(b) * kQoHeads + g * kGroup + d] = dd == 0.f ? -INFINITY : mm + log2f(dd);
+        if (tid == h) mm = m[h], dd = den[h];
+      p.lse[static_cast<int64_t>(b) * kQoHeads + g * kGroup + tid] = dd == 0.f ? -INFINITY : mm + log2f(dd);
     }
   }
 }
@@ -677,8 +740,7 @@ static cudaError_t launch_prefix(const SharedParams& p, cudaStream_t stream) {
   static std::atomic<int> configured[kMaxDevices];
   const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_shared_prefix_kernel<F8>), PrefixCfg<F8>::kBytes);
   if (e != cudaSuccess) return e;
-  gqa_shared_prefix_kernel<F8><<<p.pre_ctas, kPreThreads, PrefixCfg<F8>::kBytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(gqa_shared_prefix_kernel<F8>, dim3(p.pre_ctas), kPreThreads, PrefixCfg<F8>::kBytes, stream, 1, p);
 }
 
 int shared_prefix_blocks(int batch, int ctas) { return batch * kKvHeads + ctas * kUnitSeqs; }
@@ -687,11 +749,11 @@ cudaError_t launch_shared(const SharedParams& p, const DecodeParams& own, cudaSt
   cudaError_t e = cudaSuccess;
   if (p.pre_ctas > 0) e = p.fp8 ? launch_prefix<true>(p, stream) : launch_prefix<false>(p, stream);
   if (e != cudaSuccess) return e;
-  e = launch_decode_lsu_form(kFormParts, p.fp8 != 0, own, own.plan.tier1_ctas + own.plan.tier2_ctas, stream, kLaunchPlain);
+  e = launch_decode_lsu_form(kFormParts, p.fp8 != 0, own, own.plan.tier1_ctas + own.plan.tier2_ctas, stream,
+                             p.pre_ctas > 0 ? kLaunchPdl : kLaunchPlain);
   if (e != cudaSuccess) return e;
   const int grid = p.batch < (1 << 16) ? p.batch : (1 << 16);
-  gqa_shared_join_kernel<<<grid * kKvHeads, kHeadDim, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(gqa_shared_join_kernel, dim3(grid * kKvHeads), kHeadDim, 0, stream, 1, p);
 }
 
 }  // namespace gqa

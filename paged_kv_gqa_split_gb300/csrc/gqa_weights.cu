@@ -13,12 +13,14 @@ constexpr int kWeighThreads = 256;
 
 __global__ void __launch_bounds__(kWeighThreads) gqa_weigh_kernel(const WeighParams p) {
   __shared__ float lse[kQoHeads];
+  pdl_wait();
+  pdl_launch_dependents();
   for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
     __syncthreads();
     if (threadIdx.x < kQoHeads) lse[threadIdx.x] = __ldcg(p.lse + static_cast<int64_t>(b) * kQoHeads + threadIdx.x);
     __syncthreads();
-    const int total = max(0, min(__ldg(p.kv_indptr + p.batch), p.index_count));
-    const int lo = max(0, min(__ldg(p.kv_indptr + b), total)), n = min(__ldg(p.kv_indptr + b + 1), total) - lo;
+    const int total = max(0, min(__ldcg(p.kv_indptr + p.batch), p.index_count));
+    const int lo = max(0, min(__ldcg(p.kv_indptr + b), total)), n = min(__ldcg(p.kv_indptr + b + 1), total) - lo;
     const int j = blockIdx.x * kWeighThreads + threadIdx.x;
     if (j >= p.width || (j >= n && p.weights == p.out)) continue;
     const int64_t at = static_cast<int64_t>(b) * p.width + j;
@@ -45,35 +47,45 @@ __global__ void __launch_bounds__(kWeighThreads) gqa_weigh_kernel(const WeighPar
 cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream) {
   if (p.width == 0) return cudaSuccess;
   const dim3 grid((p.width + kWeighThreads - 1) / kWeighThreads, p.batch < 65535 ? p.batch : 65535);
-  gqa_weigh_kernel<<<grid, kWeighThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(gqa_weigh_kernel, grid, kWeighThreads, 0, stream, 1, p);
 }
 
 // --------------------------------------------------------------- eviction
-// A block per sequence. Of more than `budget` tokens the first keep_first and the last keep_last stay, and of those
-// between them the heaviest; the sequence's share of the new lists begins where the sequences before it end, which every
-// block sums up by itself.
-constexpr int kEvictThreads = 1024;
+// A cluster of blocks per sequence, each with an equal run of its tokens. Of more than `budget` tokens the first
+// keep_first and the last keep_last stay, and of those between them the heaviest; the sequence's share of the new lists
+// begins where the sequences before it end, which every block sums up by itself. The weights are read once into shared
+// memory as ordered words (from global memory each time where a run does not fit).
+constexpr int kEvictThreads = 512;
+constexpr int kEvictHeld = 48 * 1024;   // words of shared memory at most
+constexpr int kEvictRun = 8 * 1024;     // tokens a block, before a cluster of twice as many is taken
+constexpr int kEvictBlocks = 8;         // blocks of a cluster at most (the portable size)
+constexpr uint32_t kStays = 1, kGoes = 0;  // marks below any key
 
+template <bool CLUSTERED>
 __global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictParams p) {
+  extern __shared__ uint32_t held[];
   __shared__ SelectSpace<kEvictThreads> sp;
+  pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
+  const int blocks = p.cluster, rank = CLUSTERED ? static_cast<int>(blockIdx.x) % blocks : 0;
   auto length = [&](int b, int& lo) {
-    lo = max(0, min(__ldg(p.kv_indptr + b), p.index_count));
-    return max(0, min(__ldg(p.kv_indptr + b + 1), p.index_count) - lo);
+    lo = max(0, min(__ldcg(p.kv_indptr + b), p.index_count));
+    return max(0, min(__ldcg(p.kv_indptr + b + 1), p.index_count) - lo);
   };
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    int before = 0, before_all = 0, lo = 0;
-    for (int i = tid; i < b; i += kEvictThreads) {
+  for (int b = blockIdx.x / blocks; b < p.batch; b += gridDim.x / blocks) {
+    int2 ahead = make_int2(0, 0), all = make_int2(0, 0);  // tokens kept and tokens: of the sequences before this one, of all
+    int lo = 0;
+    for (int i = tid; i < p.batch; i += kEvictThreads) {
       const int n = length(i, lo);
-      before += min(n, p.budget);
-      before_all += n;
+      all.x += min(n, p.budget);
+      all.y += n;
+      if (i < b) ahead.x += min(n, p.budget), ahead.y += n;
     }
-    before = block_sum(sp, before);
-    before_all = block_sum(sp, before_all);
-    const int n = length(b, lo), keep = min(n, p.budget);
-    int gone = before_all - before;
-    if (tid == 0) {
+    ahead = block_sum2<kEvictThreads>(sp.sums, ahead);
+    all = block_sum2<kEvictThreads>(sp.sums, all);
+    const int n = length(b, lo), keep = min(n, p.budget), before = ahead.x, gone = ahead.y - ahead.x;
+    if (tid == 0 && rank == 0) {
       if (b == 0) p.new_indptr[0] = p.freed_indptr[0] = 0;
       p.new_indptr[b + 1] = before + keep;
       p.freed_indptr[b + 1] = gone + n - keep;
@@ -81,53 +93,72 @@ __global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictPar
     const float* w = p.weights + static_cast<int64_t>(b) * p.width;
     float* wo = p.weights_out + static_cast<int64_t>(b) * p.width;
     const int mid_lo = min(p.keep_first, n), mid_hi = max(n - p.keep_last, mid_lo);
-    auto weight = [&](int j) { return j < p.width ? w[j] : 0.f; };
-    auto key = [&](int j) { return ordered_bits(weight(j)); };
     const int take = keep - (n - (mid_hi - mid_lo));  // of the middle
-    uint32_t least = 0;
+    const int run = (n + blocks - 1) / blocks, first = min(rank * run, n), mine = min(run, n - first);
+    const bool cut = n > p.budget, hold = mine <= p.held;
+    auto word = [&](int i) -> uint32_t {  // of token first + i
+      const int j = first + i;
+      if (j < mid_lo || j >= mid_hi) return kStays;
+      return take > 0 ? ordered_bits(j < p.width ? __ldcg(w + j) : 0.f) : kGoes;
+    };
+    uint32_t least = kKeyLeast;
     int ties = 0;
-    if (n > p.budget && take > 0) {
-      int above = 0;
-      least = block_kth<kEvictThreads, uint32_t>(sp, mid_hi - mid_lo, take, [](int) { return true; },
-                                                 [&](int i) { return key(mid_lo + i); }, above);
-      ties = take - above;
-    }
-    int at = 0;  // kept so far
-    for (int j0 = 0; j0 < n; j0 += kEvictThreads) {
-      const int j = j0 + tid;
-      bool stay = j < n, tie = false;
-      if (j < n && n > p.budget && j >= mid_lo && j < mid_hi) {
-        const uint32_t x = key(j);
-        tie = take > 0 && x == least;
-        stay = take > 0 && x > least;
+    if (cut) {
+      if (hold) {
+        __syncthreads();  // (the words of the sequence before)
+#pragma unroll 8
+        for (int i = tid; i < mine; i += kEvictThreads) held[i] = word(i);
+        __syncthreads();
       }
-      int tied, kept;
-      const int tie_rank = block_rank(sp, tie, tied);
-      stay = stay || (tie && tie_rank < ties);
-      ties -= min(ties, tied);
-      const int rank = block_rank(sp, stay, kept);
-      if (j < n) {
-        const int page = __ldg(p.kv_indices + lo + j);
-        if (stay) {
-          if (before + at + rank < p.index_count) p.new_indices[before + at + rank] = page;  // offsets that decrease
-          if (at + rank < p.width) wo[at + rank] = weight(j);
-        } else {
-          if (gone + j - (at + rank) < p.index_count) p.freed[gone + j - (at + rank)] = page;
-        }
+      if (take > 0) {
+        least = hold ? select_kth<kEvictThreads, CLUSTERED, uint32_t>(sp, mine, take, [&](int i) { return held[i]; }, ties)
+                     : select_kth<kEvictThreads, CLUSTERED, uint32_t>(sp, mine, take, word, ties);
       }
-      at += kept;
     }
-    for (int j = keep + tid; j < p.width; j += kEvictThreads) wo[j] = 0.f;
-    if (b == p.batch - 1) {  // behind the last sequence's
-      for (int i = before + keep + tid; i < p.index_count; i += kEvictThreads) p.new_indices[i] = -1;
-      for (int i = gone + n - keep + tid; i < p.index_count; i += kEvictThreads) p.freed[i] = -1;
-    }
+    struct Token {
+      int page;
+      float weight;
+    };
+    select_in_order<kEvictThreads, CLUSTERED, 8>(
+        sp, mine, ties,
+        [&](int i) {
+          if (!cut) return 2;
+          const uint32_t x = hold ? held[i] : word(i);
+          return x == kStays || x > least ? 2 : (x == least ? 1 : 0);
+        },
+        [&](int i) {
+          const int j = first + i;
+          return Token{__ldcg(p.kv_indices + lo + j), j < p.width ? __ldcg(w + j) : 0.f};
+        },
+        [&](int i, const Token& t, int at, bool stay) {
+          const int to = stay ? before + at : gone + first + i - at;
+          if (to < p.index_count) (stay ? p.new_indices : p.freed)[to] = t.page;  // (offsets that decrease could pass it)
+          if (stay && at < p.width) wo[at] = t.weight;
+        });
+    for (int j = keep + rank * kEvictThreads + tid; j < p.width; j += blocks * kEvictThreads) wo[j] = 0.f;
+    // behind the last sequence's, a share a block
+    const int share = (p.index_count + p.batch * blocks - 1) / (p.batch * blocks), from = (b * blocks + rank) * share;
+    const int to = static_cast<int>(min(static_cast<int64_t>(from) + share, static_cast<int64_t>(p.index_count)));
+    for (int i = max(from, all.x) + tid; i < to; i += kEvictThreads) p.new_indices[i] = -1;
+    for (int i = max(from, all.y - all.x) + tid; i < to; i += kEvictThreads) p.freed[i] = -1;
   }
 }
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-  gqa_evict_kernel<<<p.batch < (1 << 16) ? p.batch : (1 << 16), kEvictThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+template <bool CLUSTERED>
+static cudaError_t launch_evict_form(const EvictParams& p, cudaStream_t stream) {
+  static std::atomic<int> configured[kMaxDevices];
+  const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED>), kEvictHeld * 4);
+  if (e != cudaSuccess) return e;
+  const int64_t units = p.batch < (1 << 16) ? p.batch : (1 << 16);
+  return launch_chained(gqa_evict_kernel<CLUSTERED>, dim3(static_cast<unsigned>(units * p.cluster)), kEvictThreads, p.held * 4, stream, p.cluster, p);
+}
+
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
+  p.cluster = 1;
+  while (p.cluster < kEvictBlocks && p.width > p.cluster * kEvictRun) p.cluster *= 2;
+  const int run = (p.width + p.cluster - 1) / p.cluster;
+  p.held = run < kEvictHeld ? run : kEvictHeld;
+  return p.cluster > 1 ? launch_evict_form<true>(p, stream) : launch_evict_form<false>(p, stream);
 }
 
 }  // namespace gqa
