@@ -96,6 +96,24 @@ struct SelectSpaceLayout {
   }
 };
 
+// CTAs of the prefix pass, an even number, one an SM: the others are left to the own tokens' decode, which runs beside it.
+// Both are given SMs by the time of an SM that they take, as far as the sizes tell (groups alike, offsets that use all of
+// the indices): a step of 128 tokens and 64 sequences takes a pair 1.6 us (FP8 2.4), an own token an SM 0.03 us (FP8 0.02).
+// At most 9 SMs of 10, so that the decode's short runs begin at once, and at least two steps a pair. All SMs for the pass and
+// then all for the decode took: 16384 tokens x 128 sequences with 64 to 1024 own tokens 80 us, this way 69; with up to 64
+// own tokens 57 and 47; 2048 x 8 with up to 256 own tokens 26 and 20.
+int prefix_ctas(int sms, int batch, int groups, int prefix_count, int index_count, bool fp8) {
+  const int pairs = sms / 2;
+  if (groups <= 0 || prefix_count <= 0 || pairs == 0) return 0;
+  const double units = gqa::kKvHeads * std::ceil(std::ceil(static_cast<double>(batch) / groups) / 64.0);
+  const double steps = units * std::ceil(prefix_count / 128.0 + 0.5 * (groups - 1));
+  const double pass = steps * 2 * (fp8 ? 2.4 : 1.6), own = index_count * (fp8 ? 0.02 : 0.03);
+  double n = std::fmin(pairs * pass / (pass + own), 0.9 * pairs);
+  const double run = std::fmax(std::ceil(steps / std::fmax(n, 1.0)), 2.0);
+  n = std::ceil(steps / run);  // as few pairs as make the same runs
+  return 2 * static_cast<int>(std::fmin(std::fmax(n, 1.0), pairs));
+}
+
 bool select_sizes_ok(int rows, int width) { return rows > 0 && width > 0 && static_cast<int64_t>(rows) * width <= (int64_t{1} << 34); }
 bool sparse_sizes_ok(int rows, int top, int page_size) {
   return rows > 0 && top > 0 && page_size > 0 && static_cast<int64_t>(top) * page_size <= INT_MAX &&
@@ -165,7 +183,7 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   p.out = out;
   p.lse = lse;
   p.group_start = reinterpret_cast<int64_t*>(ws + at.start);
-  p.pre_ctas = groups > 0 && prefix_count > 0 ? setup.sm_count : 0;
+  p.pre_ctas = prefix_ctas(setup.sm_count, batch, groups, prefix_count, index_count, fp8);
   p.wait_limit_ns = setup.wait_limit_ns;
   p.part_o = part_o;
   p.part_lse = part_lse;

@@ -343,8 +343,8 @@ struct SharedParams {  // gqa_shared.cu
   void* out;
   float* lse;                 // or NULL
   int64_t* group_start;       // [groups + 1] first step of each group's prefix (written by the prefix pass)
-  // parts, blocks of [128 dims][8 heads] and 8 LSEs: the prefixes' [batch][4] and [pre_ctas][32], from own_base on the own
-  // tokens' (DecodeParams::part_o, part_lse)
+  // parts of 1024 outputs and 8 LSEs: the prefixes' [batch][4] and [pre_ctas / 2][64], [8 heads][128 dims] each; from
+  // own_base on the own tokens' (DecodeParams::part_o, part_lse), [128 dims][8 heads]
   float* part_o;
   float* part_lse;
   int64_t own_base;
@@ -352,7 +352,7 @@ struct SharedParams {  // gqa_shared.cu
   PlanConfig plan;
   float scale_log2;
   int batch, groups, prefix_count, index_count, num_pages, fp8;
-  int pre_ctas;               // 0: no prefix has a token
+  int pre_ctas;               // an even number; 0: no prefix has a token
   unsigned long long wait_limit_ns;
   int* err;
 };

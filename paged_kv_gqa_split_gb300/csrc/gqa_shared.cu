@@ -30,133 +30,198 @@ __device__ __forceinline__ int prefix_range(const SharedParams& p, int g, int& f
 }
 
 // ----------------------------------------------------------------- prefix
-// Query rows of one KV head are its 8 query heads of up to 32 sequences of a group: two tiles of 128 rows, a row a lane
-// of tensor memory. A unit is these rows and the group's prefix, walked in steps of 128 tokens: S = Q K^T (M = 128,
-// N = 128 tokens, 8 MMAs of K = 16) lands in tensor memory, a thread per row turns it into probabilities that overwrite
-// it there, and O += P V (8 MMAs, P read from tensor memory) accumulates beside it; while one tile is in its softmax the
-// tensor cores do the other's MMAs. Rows without a sequence are zeros; with 16 sequences or fewer there is one tile.
+// Query rows of one KV head are its 8 query heads of up to 64 sequences of a group. A pair of CTAs takes them as two tiles
+// of 256 rows (128 a CTA, 16 sequences, a row a lane of tensor memory) and walks the group's prefix in steps of 128 tokens:
+// S = Q K^T (M = 256, N = 128 tokens, 8 MMAs of K = 16) lands in tensor memory, a thread per row turns it into
+// probabilities that overwrite it there, and O += P V (8 MMAs, P read from tensor memory) accumulates beside it. The two
+// tiles alternate: while one is in its softmax the tensor cores do the other's MMAs. Rows without a sequence are zeros;
+// with 32 sequences or fewer there is one tile.
 //
-// The steps of all units (groups, then row tiles, then KV heads) are one line, cut into equal runs, one a CTA, one CTA
-// an SM: prefixes of any number and length fill the GPU. What a CTA has of a unit is a piece. Its outputs and LSE go out
-// in fp32, as blocks of [128 dims][8 heads] a sequence: the piece that begins the unit to the sequence's own block, one
-// that goes on with it to the CTA's (a CTA has one such piece at most, its first).
+// A unit is these rows and the prefix. The steps of all units (groups, then 64 sequences at a time, then KV heads) are one
+// line, cut into equal runs, one a pair, one CTA an SM: prefixes of any number and length fill the GPU. What a pair has of
+// a unit is a piece. Its outputs and LSE go out in fp32, as blocks of [8 heads][128 dims] a sequence: the piece that begins
+// the unit to the sequence's own block, one that goes on with it to the pair's (a pair has one such piece at most, its
+// first).
 //
-// Pages are single tokens in any order, so a token's 256 bytes of a KV head are gathered by 16-byte cp.async, written
-// where the 128-byte swizzle wants them; four warps keep five 32 KB slots (128 tokens of K or V) in flight. An FP8
-// cache's codes go through a ring of their own and become fp16 (exact) on the way to three such slots; a token's K
-// scale is taken on its score, its V scale on its probability (over a running power of two), Q is fp16 times a power of
-// two a row, as in the decode.
+// Why pairs: a CTA alone reads 64 KB a step of 256 rows, and its copies took 2500 of the step's 4050 clocks. In a pair
+// each CTA copies and keeps half (K of 64 of the tokens, V of 64 of the 128 dims).
+//
+// Pages are single tokens in any order, so their rows are gathered by 16-byte cp.async, written where the 128-byte swizzle
+// wants them; four warps keep four steps (32 KB a CTA) in flight. The odd CTA's copies are counted there, and its MMA warp
+// tells the even CTA, which issues for both. An FP8 cache's codes go through a ring of their own and become fp16 (exact) on
+// the way to three such stages; a token's K scale is taken on its score, its V scale on its probability (over a running power of
+// two), Q is fp16 times a power of two a row, as in the decode.
 //
 // The running maximum moves only when a row's scores pass it by 2^8, so O is seldom rescaled; fp16 probabilities are held
 // times 2^7. Every wait is bounded: on a timeout the CTA flags the device error word, waits for its copies and MMAs in
 // flight, frees tensor memory and leaves.
-constexpr int kStep = 128, kSeqTile = 16, kUnitSeqs = 2 * kSeqTile;
+constexpr int kStep = 128, kSeqTile = 16, kUnitSeqs = 4 * kSeqTile;
 constexpr int kPreThreads = 512, kCopyWarps = 4, kMmaWarp = 4, kRowWarp = 8;  // two MMA warps; from 8 on two warpgroups of rows
 constexpr int kRowRegs = 200, kOtherRegs = 56;
 static_assert(256 * kRowRegs + 256 * kOtherRegs <= 65536, "register split");
-constexpr int kHalfTile = 128 * 128, kSlotBytes = 2 * kHalfTile;  // 128 rows of 64 values; of 128
-constexpr int kInfo = 4;  // steps whose masks and scales are held: the copies are at most three ahead of the softmax
+constexpr int kQRegion = 128 * 128, kQTile = 2 * kQRegion;  // 128 rows of 64 values; of 128
+constexpr int kKRegion = 64 * 128, kVOff = 2 * kKRegion;   // 64 tokens x 128 values of K in two regions, then 128 x 64 of V
+constexpr int kStageBytes = kVOff + 128 * 128;
+constexpr int kInfo = 8;  // steps whose masks and scales are held: the copies are at most six ahead of the softmax
 constexpr float kMoveBy = 8.f;
+
+// A role's walk over the pieces of its pair, kept in shared memory.
+struct Walk {
+  int64_t x, end, group_end;         // next step, the run's end, the end of group g's steps
+  int g, tiles, seq0, members, first, n;  // the group: steps a unit, sequences, prefix tokens
+};
+struct Piece {
+  int head, row0, step0, steps;  // KV head, first sequence (within the group), steps
+  int seq0, members, first, n;
+  // sequences of tile a; those of one CTA's half of it
+  __device__ __forceinline__ int seqs(int a) const { return max(0, min(members - row0 - a * 2 * kSeqTile, 2 * kSeqTile)); }
+  __device__ __forceinline__ int seqs(int a, int half) const { return max(0, min(seqs(a) - half * kSeqTile, kSeqTile)); }
+};
 
 template <bool F8>
 struct PrefixCfg {
-  static constexpr int kSlots = F8 ? 3 : 5;
-  static constexpr int kRaw = F8 ? 3 : 0;  // slots of codes, 16 KB each
+  static constexpr int kStages = F8 ? 3 : 4;
+  static constexpr int kRaw = F8 ? 3 : 0;  // stages of codes
   static constexpr float kShift = F8 ? 7.f : 0.f;
-  static constexpr int kSlotOff = 2 * kSlotBytes;  // behind the two query tiles
-  static constexpr int kRawOff = kSlotOff + kSlots * kSlotBytes;
-  static constexpr int kRawBytes = kStep * kHeadDim + 2 * kStep * 4;  // codes; with K's the scales of K and V
+  static constexpr int kStageOff = 2 * kQTile;
+  static constexpr int kRawOff = kStageOff + kStages * kStageBytes;
+  static constexpr int kRawV = kVOff / 2, kRawScales = kStageBytes / 2, kRawBytes = kRawScales + 2 * kStep * 4;  // codes of K, of V; scales of K, of V
   static constexpr int kMaskOff = kRawOff + kRaw * kRawBytes;
-  static constexpr int kScaleOff = kMaskOff + kInfo * 16;                   // K, then V scales of a step; their largest, a warp's each
+  static constexpr int kScaleOff = kMaskOff + kInfo * 16;           // K, then V scales of a step; V's largest, a warp's each
   static constexpr int kTopOff = kScaleOff + (F8 ? kInfo * 2 * kStep * 4 : 0);
-  static constexpr int kRowOff = kTopOff + (F8 ? kInfo * 16 : 0);           // the queries' factors
-  static constexpr int kBarOff = kRowOff + (F8 ? 256 * 4 : 0);
-  // barriers: slots full and free; queries written, S and O there, the halves of P written, a tile each; all done
-  static constexpr int kFull = 0, kFree = kSlots, kQ = 2 * kSlots, kS = kQ + 2, kO = kS + 2, kP = kO + 2, kDone = kP + 4, kBars = kDone + 1;
+  static constexpr int kRowOff = kTopOff + (F8 ? kInfo * 16 : 0);   // the queries' factors
+  static constexpr int kWalkOff = kRowOff + (F8 ? 256 * 4 : 0);
+  static constexpr int kBarOff = kWalkOff + kPreThreads / 32 * static_cast<int>(sizeof(Walk));
+  // Barriers. Both CTAs': stages full (the even one's counts the odd one's too) and free, S and O there (MMA commits), all
+  // done. The even CTA's: queries written, the halves of P written (4 warps of each CTA), whose turn it is to issue.
+  static constexpr int kFull = 0, kFree = kStages, kQ = 2 * kStages, kS = kQ + 2, kO = kS + 2, kP = kO + 2, kTurn = kP + 4,
+                       kDone = kTurn + 2, kBars = kDone + 1;
   static constexpr int kWordOff = kBarOff + kBars * 8;
   static constexpr int kBytes = kWordOff + 16 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
-  static_assert(kBytes <= 227 * 1024, "prefix pass exceeds shared memory");
+  static_assert(kBytes <= 226 * 1024 && sizeof(Walk) % 8 == 0, "prefix pass exceeds shared memory");
 };
 
-// Steps of group g's units together.
-__device__ __forceinline__ int64_t group_steps(const SharedParams& p, int g, int& tiles, int& seq0, int& members) {
-  int first;
-  tiles = (prefix_range(p, g, first) + kStep - 1) / kStep;
+// Steps of group g's units together; its steps a unit, first sequence, sequences, first prefix token and their count.
+__device__ __forceinline__ int64_t group_steps(const SharedParams& p, int g, int& tiles, int& seq0, int& members, int& first, int& n) {
+  n = prefix_range(p, g, first);
+  tiles = (n + kStep - 1) / kStep;
   seq0 = max(0, min(__ldcg(p.group_indptr + g), p.batch));
   members = max(0, min(__ldcg(p.group_indptr + g + 1), p.batch) - seq0);
   return static_cast<int64_t>((members + kUnitSeqs - 1) / kUnitSeqs) * kKvHeads * tiles;
 }
 
-__host__ __device__ __forceinline__ int64_t steps_per_cta(int64_t total, int ctas) {
-  return total > ctas ? (total + ctas - 1) / ctas : 1;
+__device__ __forceinline__ int64_t steps_per_pair(int64_t total, int pairs) {
+  return total > pairs ? (total + pairs - 1) / pairs : 1;
 }
 
-// A role's walk over the pieces of its CTA.
-struct Walk {
-  int64_t x, end, group_end;  // next step, the run's end, the end of group g's steps
-  int g, tiles, seq0, members, first, n;  // the group: steps a unit, sequences, prefix tokens
-  int head, row0, step0, steps;           // the piece: KV head, first sequence (within the group), steps
-
-  __device__ __forceinline__ bool next(const SharedParams& p) {
-    if (x >= end) return false;
-    while (x >= group_end) {
-      ++g;
-      group_end += group_steps(p, g, tiles, seq0, members);
-    }
-    n = prefix_range(p, g, first);
-    const int64_t per_group = static_cast<int64_t>((members + kUnitSeqs - 1) / kUnitSeqs) * kKvHeads * tiles;
-    const int64_t at = x - (group_end - per_group);
-    const int unit = static_cast<int>(at / tiles);
-    step0 = static_cast<int>(at - static_cast<int64_t>(unit) * tiles);
-    steps = static_cast<int>(min(static_cast<int64_t>(tiles - step0), end - x));
-    head = unit % kKvHeads;
-    row0 = unit / kKvHeads * kUnitSeqs;
-    x += steps;
-    return true;
+// The next piece of the warp's walk; false at the run's end. Every lane gets it.
+__device__ __forceinline__ bool next_piece(const SharedParams& p, volatile Walk* w, int lane, Piece& pc) {
+  __syncwarp();
+  int64_t x = w->x, group_end = w->group_end;
+  const int64_t end = w->end;
+  if (x >= end) return false;
+  int g = w->g, tiles = w->tiles;
+  pc.seq0 = w->seq0;
+  pc.members = w->members;
+  pc.first = w->first;
+  pc.n = w->n;
+  while (x >= group_end) {
+    ++g;
+    group_end += group_steps(p, g, tiles, pc.seq0, pc.members, pc.first, pc.n);
   }
-  __device__ __forceinline__ int seqs(int a) const { return max(0, min(members - row0 - a * kSeqTile, kSeqTile)); }
-};
+  const int64_t per_group = static_cast<int64_t>((pc.members + kUnitSeqs - 1) / kUnitSeqs) * kKvHeads * tiles;
+  const int64_t at = x - (group_end - per_group);
+  const int unit = at < INT32_MAX ? static_cast<int>(at) / tiles : static_cast<int>(at / tiles);
+  pc.step0 = static_cast<int>(at - static_cast<int64_t>(unit) * tiles);
+  pc.steps = static_cast<int>(min(static_cast<int64_t>(tiles - pc.step0), end - x));
+  pc.head = unit % kKvHeads;
+  pc.row0 = unit / kKvHeads * kUnitSeqs;
+  __syncwarp();
+  if (lane == 0) {
+    w->x = x + pc.steps;
+    w->group_end = group_end;
+    w->g = g;
+    w->tiles = tiles;
+    w->seq0 = pc.seq0;
+    w->members = pc.members;
+    w->first = pc.first;
+    w->n = pc.n;
+  }
+  return true;
+}
 
 template <bool F8>
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   return F8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
 }
 
+// Two scores to weights x = 2^(s sc + off), their sum added to l: packed operands x, or x (w iv) with an FP8 cache.
+template <bool F8>
+__device__ __forceinline__ uint32_t weigh_pair(uint32_t s0, uint32_t s1, uint64_t sc2, uint64_t off2, float w0, float w1, uint64_t iv2, uint64_t& l) {
+  float x0, x1;
+  unpack2(fma2(pack2(__uint_as_float(s0), __uint_as_float(s1)), sc2, off2), x0, x1);
+  x0 = ex2(x0);
+  x1 = ex2(x1);
+  const uint64_t x = pack2(x0, x1);
+  l = add2(l, x);
+  if constexpr (F8) unpack2(mul2(x, mul2(pack2(w0, w1), iv2)), x0, x1);
+  return pack_p<F8>(x0, x1);
+}
+
+// 16 consecutive floats of shared memory, their loads together.
+__device__ __forceinline__ void load16(uint32_t addr, float (&x)[16]) {
+  uint32_t u[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ld_shared_u4(addr + 16 * i, u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void store_f8(float* to, const uint32_t* x, float f) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(__uint_as_float(x[0]) * f),
+               "f"(__uint_as_float(x[1]) * f), "f"(__uint_as_float(x[2]) * f), "f"(__uint_as_float(x[3]) * f),
+               "f"(__uint_as_float(x[4]) * f), "f"(__uint_as_float(x[5]) * f), "f"(__uint_as_float(x[6]) * f),
+               "f"(__uint_as_float(x[7]) * f)
+               : "memory");
+}
+
 template <bool F8>
 __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const SharedParams p) {
   using C = PrefixCfg<F8>;
   extern __shared__ uint8_t smem_raw[];
+  const int half = static_cast<int>(cluster_rank());
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort_s = reinterpret_cast<volatile int*>(sm + C::kWordOff + 4);
   auto bar = [&](int i) { return base + C::kBarOff + 8u * static_cast<uint32_t>(i); };
-  __shared__ int64_t warp_steps[kPreThreads / 32], begin_s;
-  __shared__ int begin_g;
+  __shared__ int64_t warp_steps[kPreThreads / 32];
+  Walk* walks = reinterpret_cast<Walk*>(sm + C::kWalkOff);
+  if (tid == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      int count = 1;  // S, O, turns
+      if (i < C::kFree) count = (F8 ? kCopyWarps : kCopyWarps * 32 + kCopyWarps) + (half == 0 ? 1 : 0);
+      else if (i < C::kQ || i == C::kDone) count = 2;  // a commit of each MMA warp
+      else if (i < C::kS || (i >= C::kP && i < C::kTurn)) count = 8;
+      mbar_init(bar(i), count);
+    }
+    *abort_s = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
   pdl_wait();
   pdl_launch_dependents();  // the own tokens' decode: by now all that it reads is there
 
-  // total steps, then where this CTA's run begins
-  Walk walk;
+  // total steps, then where this pair's run begins; groups 512 at a time
   {
-    int64_t mine = 0;
-    int t, s0, m;
-    for (int g = tid; g < p.groups; g += kPreThreads) mine += group_steps(p, g, t, s0, m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) warp_steps[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kPreThreads / 32; ++w) total += warp_steps[w];
-    const int64_t run = steps_per_cta(total, gridDim.x);
-    walk.x = run * blockIdx.x;
-    walk.end = min(walk.x + run, total);
-    int64_t carry = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += kPreThreads) {
-      const int g = g0 + tid;
-      const int64_t steps = g < p.groups ? group_steps(p, g, t, s0, m) : 0;
-      int64_t upto = steps;
+    int t = 0, s0 = 0, m = 0, f = 0, n = 0;
+    int64_t total = 0, carry = 0, steps = 0, upto = 0;
+    const bool once = p.groups <= kPreThreads;
+    auto scan = [&](int g0) {  // steps of group g0 + tid, and up to its end within these 512
+      steps = g0 + tid < p.groups ? group_steps(p, g0 + tid, t, s0, m, f, n) : 0;
+      upto = steps;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
@@ -165,269 +230,295 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       __syncthreads();
       if (lane == 31) warp_steps[warp] = upto;
       __syncthreads();
-      for (int w = 0; w < warp; ++w) upto += warp_steps[w];
-      upto += carry;
-      if (g < p.groups) {
-        if (blockIdx.x == 0) p.group_start[g + 1] = upto;
-        if (upto - steps <= walk.x && walk.x < upto) begin_g = g, begin_s = upto;
+      int64_t all = 0;
+#pragma unroll 1
+      for (int w = 0; w < kPreThreads / 32 && (g0 + 32 * w < p.groups); ++w) {
+        if (w == warp) upto += all;
+        all += warp_steps[w];
       }
-      for (int w = 0; w < kPreThreads / 32; ++w) carry += warp_steps[w];
+      return all;
+    };
+    for (int g0 = 0; g0 < p.groups; g0 += kPreThreads) total += scan(g0);
+    const int64_t run = steps_per_pair(total, pairs), begin = run * pair;
+    for (int g0 = 0; g0 < p.groups; g0 += kPreThreads) {
+      const int64_t all = once ? total : scan(g0);
+      upto += carry;
+      if (g0 + tid < p.groups) {
+        if (blockIdx.x == 0) p.group_start[g0 + tid + 1] = upto;
+        if (upto - steps <= begin && begin < upto)
+          for (int w = 0; w < kPreThreads / 32; ++w) walks[w] = Walk{begin, min(begin + run, total), upto, g0 + tid, t, s0, m, f, n};
+      }
+      carry += all;
     }
     if (blockIdx.x == 0 && tid == 0) p.group_start[0] = 0;
-    __syncthreads();
-    if (walk.x >= total) return;
-    walk.g = begin_g;
-    walk.group_end = begin_s;
-    group_steps(p, walk.g, walk.tiles, walk.seq0, walk.members);
+    if (begin >= total) return;  // both CTAs of the pair
   }
-
-  if (tid == 0) {
-    for (int i = 0; i < C::kBars; ++i) {
-      int count = 1;  // S, O: a commit
-      if (i < C::kFree) count = F8 ? kCopyWarps : kCopyWarps * 32 + kCopyWarps;
-      else if (i < C::kQ || i == C::kDone) count = 2;  // a commit of each MMA warp
-      else if (i < C::kS || (i >= C::kP && i < C::kDone)) count = 4;  // warps of a tile's rows
-      mbar_init(bar(i), count);
-    }
-    *abort_s = 0;
-    fence_mbar_init();
-    fence_proxy_async_smem();
-  }
-  if (warp == kMmaWarp) tc_alloc(base + C::kWordOff, 512);
+  if (warp == kMmaWarp) tc2_alloc(base + C::kWordOff, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the barriers and the tensor memory of both CTAs are ready
+  volatile Walk* walk = walks + warp;
+  Piece pc;
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kWordOff);
   auto wait = [&](int i, uint32_t parity, int bit) {
     return __all_sync(0xffffffffu, tc_wait_limited(bar(i), parity, abort_s, p.err, bit, p.wait_limit_ns)) != 0;
+  };
+  // for barriers that releases of the other CTA's threads complete
+  auto wait_pair = [&](int i, uint32_t parity, int bit) {
+    return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar(i), parity) ||
+                                       (tc_wait_limited(bar(i), parity, abort_s, p.err, bit, p.wait_limit_ns) &&
+                                        mbar_try_wait_cluster(bar(i), parity))) != 0;
   };
 
   if (warp < kRowWarp) {
     setmaxnreg_dec<kOtherRegs>();
     if (warp < kCopyWarps) {
       // ------------------------------------------------------------- copies
+      // Warp w: K of tokens 16 w .. of this CTA's 64, V of tokens 32 w .. of the 128.
       const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
       const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
       int s = 0, info = 0, filled = 0;
-      uint32_t ph = 1;  // parity of the slot's previous release
+      uint32_t ph = 1;  // parity of the stage's previous release
       bool good = true;
+      const int k_token = 64 * half + 16 * warp + (lane & 15), v_token = 32 * warp + lane;
+      auto id_of = [&](const Piece& w, int t) { return t < w.n ? __ldcg(p.prefix_indices + w.first + t) : -1; };
+      auto live = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages); };
       if constexpr (!F8) {
-        const int c = lane & 15;  // 16-byte column of a token's 256 bytes
-        const uint32_t to = (c >> 3) * kHalfTile;
-        while (good && walk.next(p)) {
-          int t = walk.step0 * kStep + 32 * warp + lane;
-          int id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;
+        const uint8_t* k_from = kc + 16 * (lane & 15);
+        const uint8_t* v_from = vc + 128 * half + 16 * (lane & 7);
+        // rows 2 i + lane / 16 of K (8 apart: every fourth i), 4 i + lane / 8 of V: the swizzle of i and i + 4, or i + 2, is one
+        const uint32_t k_to = ((lane & 15) >> 3) * kKRegion;
+        while (good && next_piece(p, walk, lane, pc)) {
+          int t0 = pc.step0 * kStep;
+          int kid = id_of(pc, t0 + k_token), vid = id_of(pc, t0 + v_token);
+          const int64_t head_off = pc.head * (kHeadDim * 2);
 #pragma unroll 1
-          for (int j = 0; j < walk.steps && good; ++j) {
-            const bool live = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
-            const unsigned mask = __ballot_sync(0xffffffffu, live);
-            const int page = live ? id : 0;
-            t += kStep;
-            id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;  // of the next step, behind this one's copies
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-              if (filled >= C::kSlots) good = wait(C::kFree + s, ph, kErrTimeoutEmpty);
-              if (!good) break;
-              ++filled;
-              const uint8_t* from = (kv == 0 ? kc : vc) + walk.head * (kHeadDim * 2) + 16 * c;
-              const uint32_t slot = base + C::kSlotOff + s * kSlotBytes + to;
+          for (int j = 0; j < pc.steps; ++j) {
+            const unsigned k_mask = __ballot_sync(0xffffffffu, live(kid)), v_mask = __ballot_sync(0xffffffffu, live(vid));
+            const int k_page = live(kid) ? kid : 0, v_page = live(vid) ? vid : 0;
+            t0 += kStep;
+            kid = id_of(pc, t0 + k_token);  // of the next step, behind this one's copies
+            vid = id_of(pc, t0 + v_token);
+            if (filled >= C::kStages) good = wait(C::kFree + s, ph, kErrTimeoutEmpty);
+            if (!good) break;
+            ++filled;
+            const uint32_t stage = base + C::kStageOff + s * kStageBytes;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int r = 2 * i + (lane >> 4);
-                const int64_t pg = __shfl_sync(0xffffffffu, page, r);
-                cp_async_16(sw128(slot, 32 * warp + r, c & 7), from + pg * kPageBytes, (mask >> r) & 1u ? 16u : 0u);
-              }
-              cp_async_arrive(bar(C::kFull + s));
-              if (lane == 0) {
-                if (kv == 0) reinterpret_cast<volatile unsigned*>(sm + C::kMaskOff)[4 * info + warp] = mask;
-                mbar_arrive(bar(C::kFull + s));
-              }
-              if (++s == C::kSlots) {
-                s = 0;
-                ph ^= 1;
-              }
+            for (int i = 0; i < 8; ++i) {
+              const int r = 2 * i + (lane >> 4);
+              const int64_t pg = __shfl_sync(0xffffffffu, k_page, r);
+              cp_async_16(sw128(stage + k_to, 16 * warp + r, lane & 7), k_from + head_off + pg * kPageBytes, (k_mask >> r) & 1u ? 16u : 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              const int64_t pg = __shfl_sync(0xffffffffu, v_page, r);
+              cp_async_16(sw128(stage + kVOff, 32 * warp + r, lane & 7), v_from + head_off + pg * kPageBytes, (v_mask >> r) & 1u ? 16u : 0u);
+            }
+            cp_async_arrive(bar(C::kFull + s));
+            if (lane == 0) {
+              reinterpret_cast<volatile unsigned*>(sm + C::kMaskOff)[4 * info + warp] = v_mask;
+              mbar_arrive(bar(C::kFull + s));
+            }
+            if (++s == C::kStages) {
+              s = 0;
+              ph ^= 1;
             }
             info = (info + 1) % kInfo;
           }
         }
       } else {
-        // A thread converts the chunks that it copied itself: row r = 4 i + lane / 8 of the warp's 32, 16 codes at lane % 8.
-        const int c = lane & 7;
+        // A thread converts the chunks that it copied itself: 16 codes of rows 4 i + lane / 8 of K, 8 i + lane / 4 of V. The
+        // copies run kRaw - 1 steps ahead of the conversion; the conversions are counted by the copies' walk.
         constexpr int kRow = kKvHeads * kHeadDim + 4 * kKvHeads;
-        Walk ahead = walk;  // the copies' walk, kRaw - 1 slots ahead of the conversion's
-        bool more = ahead.next(p);
-        int aj = 0, akv = 0, as = 0, page = 0;
-        unsigned mask = 0;
+        bool more = next_piece(p, walk, lane, pc);
+        int aj = 0, as = 0, ainfo = 0, copied = 0, kid = -1, vid = -1;
+        auto ids = [&]() {
+          if (more) {
+            const int t0 = (pc.step0 + aj) * kStep;
+            kid = id_of(pc, t0 + k_token);
+            vid = id_of(pc, t0 + v_token);
+          }
+        };
+        ids();
         auto copy = [&]() {
           if (more) {
-            if (akv == 0) {
-              const int t = (ahead.step0 + aj) * kStep + 32 * warp + lane;
-              const int id = t < ahead.n ? __ldcg(p.prefix_indices + ahead.first + t) : -1;
-              const bool live = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
-              mask = __ballot_sync(0xffffffffu, live);
-              page = live ? id : 0;
-            }
-            const uint8_t* from = akv == 0 ? kc : vc;
-            const uint32_t slot = base + C::kRawOff + as * C::kRawBytes;
+            const uint32_t stage = base + C::kRawOff + as * C::kRawBytes;
+            const int64_t head_off = pc.head * kHeadDim;
+            const unsigned k_mask = __ballot_sync(0xffffffffu, live(kid)), v_mask = __ballot_sync(0xffffffffu, live(vid));
+            const int k_page = live(kid) ? kid : 0, v_page = live(vid) ? vid : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int r = 4 * i + (lane >> 3);
-              const int64_t pg = __shfl_sync(0xffffffffu, page, r);
-              cp_async_16(slot + (32 * warp + r) * kHeadDim + 16 * c, from + pg * kRow + ahead.head * kHeadDim + 16 * c,
-                          (mask >> r) & 1u ? 16u : 0u);
+              const int64_t pg = __shfl_sync(0xffffffffu, k_page, r);
+              cp_async_16(stage + (16 * warp + r) * kHeadDim + 16 * (lane & 7), kc + pg * kRow + head_off + 16 * (lane & 7),
+                          (k_mask >> r) & 1u ? 16u : 0u);
             }
-            if (akv == 0) {  // V's scales with K's: the softmax reads both when the scores are there
-              const int64_t at = static_cast<int64_t>(page) * kRow + kKvHeads * kHeadDim + 4 * ahead.head;
-              const uint32_t to = slot + kStep * kHeadDim + 4 * (32 * warp + lane);
-              cp_async_4(to, kc + at, (mask >> lane) & 1u ? 4u : 0u);
-              cp_async_4(to + 4 * kStep, vc + at, (mask >> lane) & 1u ? 4u : 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2);
+              const int64_t pg = __shfl_sync(0xffffffffu, v_page, r);
+              cp_async_16(stage + C::kRawV + (32 * warp + r) * 64 + 16 * (lane & 3), vc + pg * kRow + head_off + 64 * half + 16 * (lane & 3),
+                          (v_mask >> r) & 1u ? 16u : 0u);
             }
+            const int64_t at = static_cast<int64_t>(v_page) * kRow + kKvHeads * kHeadDim + 4 * pc.head;
+            const uint32_t to = stage + C::kRawScales + 4 * v_token;
+            cp_async_4(to, kc + at, (v_mask >> lane) & 1u ? 4u : 0u);
+            cp_async_4(to + 4 * kStep, vc + at, (v_mask >> lane) & 1u ? 4u : 0u);
+            if (lane == 0) reinterpret_cast<volatile unsigned*>(sm + C::kMaskOff)[4 * ainfo + warp] = v_mask;
             as = as + 1 == C::kRaw ? 0 : as + 1;
-            akv ^= 1;
-            if (akv == 0 && ++aj == ahead.steps) {
+            ainfo = (ainfo + 1) % kInfo;
+            ++copied;
+            if (++aj == pc.steps) {
               aj = 0;
-              more = ahead.next(p);
+              more = next_piece(p, walk, lane, pc);
             }
+            ids();  // of the next step, behind this one's copies
           }
           cp_async_commit();  // one group a call, even when empty
+        };
+        auto convert = [&](uint32_t from, uint32_t region, int r, int c) {  // 16 codes to columns c and c + 1 of row r
+          uint32_t x[4], y[8];
+          ld_shared_u4(from, x[0], x[1], x[2], x[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[2 * k] = cvt_e4m3x2_f16x2(x[k]);
+            y[2 * k + 1] = cvt_e4m3x2_f16x2(x[k] >> 16);
+          }
+          st_shared_u4(sw128(region, r, c), y[0], y[1], y[2], y[3]);
+          st_shared_u4(sw128(region, r, c + 1), y[4], y[5], y[6], y[7]);
         };
 #pragma unroll 1
         for (int i = 0; i < C::kRaw - 1; ++i) copy();
         int rs = 0;
-        while (good && walk.next(p)) {
 #pragma unroll 1
-          for (int j = 0; j < walk.steps && good; ++j) {
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-              __syncwarp();
-              copy();
-              cp_async_wait<C::kRaw - 1>();
-              if (filled >= C::kSlots) good = wait(C::kFree + s, ph, kErrTimeoutEmpty);
-              if (!good) break;
-              ++filled;
-              const uint32_t slot = base + C::kSlotOff + s * kSlotBytes + (c >> 2) * kHalfTile;
-              const uint32_t codes = base + C::kRawOff + rs * C::kRawBytes;
-#pragma unroll 4
-              for (int i = 0; i < 8; ++i) {
-                const int r = 32 * warp + 4 * i + (lane >> 3);
-                uint32_t x[4], y[8];
-                ld_shared_u4(codes + r * kHeadDim + 16 * c, x[0], x[1], x[2], x[3]);
+        while (filled < copied || more) {
+          __syncwarp();
+          copy();
+          cp_async_wait<C::kRaw - 1>();
+          if (filled >= C::kStages) good = wait(C::kFree + s, ph, kErrTimeoutEmpty);
+          if (!good) break;
+          ++filled;
+          const uint32_t stage = base + C::kStageOff + s * kStageBytes;
+          const uint32_t codes = base + C::kRawOff + rs * C::kRawBytes;
+          const uint32_t at = codes + C::kRawScales + 4 * v_token;
+          const float sk = ld_shared_f32(at), sv = ld_shared_f32(at + 4 * kStep);
+          volatile float* scales = reinterpret_cast<volatile float*>(sm + C::kScaleOff) + 2 * info * kStep + v_token;
+          scales[0] = sk;
+          scales[kStep] = sv;
+          const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, fabsf(sv) < INFINITY ? __float_as_uint(fabsf(sv)) : 0u));
+          if (lane == 0) reinterpret_cast<volatile float*>(sm + C::kTopOff)[4 * info + warp] = top;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  y[2 * k] = cvt_e4m3x2_f16x2(x[k]);
-                  y[2 * k + 1] = cvt_e4m3x2_f16x2(x[k] >> 16);
-                }
-                st_shared_u4(sw128(slot, r, 2 * (c & 3)), y[0], y[1], y[2], y[3]);
-                st_shared_u4(sw128(slot, r, 2 * (c & 3) + 1), y[4], y[5], y[6], y[7]);
-              }
-              if (kv == 0) {
-                const uint32_t at = codes + kStep * kHeadDim + 4 * (32 * warp + lane);
-                const float sk = ld_shared_f32(at), sv = ld_shared_f32(at + 4 * kStep);
-                volatile float* scales = reinterpret_cast<volatile float*>(sm + C::kScaleOff) + 2 * info * kStep + 32 * warp + lane;
-                scales[0] = sk;
-                scales[kStep] = sv;
-                float top = fabsf(sv) < INFINITY ? fabsf(sv) : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            const int c = lane & 7, r = 16 * warp + 4 * i + (lane >> 3);
+            convert(codes + r * kHeadDim + 16 * c, stage + (c >> 2) * kKRegion, r, 2 * (c & 3));
+          }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                if (lane == 0) reinterpret_cast<volatile float*>(sm + C::kTopOff)[4 * info + warp] = top;
-                const int t = (walk.step0 + j) * kStep + 32 * warp + lane;
-                const int id = t < walk.n ? __ldcg(p.prefix_indices + walk.first + t) : -1;
-                const unsigned mk = __ballot_sync(0xffffffffu, static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages));
-                if (lane == 0) reinterpret_cast<volatile unsigned*>(sm + C::kMaskOff)[4 * info + warp] = mk;
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(C::kFull + s));
-              rs = rs + 1 == C::kRaw ? 0 : rs + 1;
-              if (++s == C::kSlots) {
-                s = 0;
-                ph ^= 1;
-              }
-            }
-            info = (info + 1) % kInfo;
+          for (int i = 0; i < 4; ++i) {
+            const int r = 32 * warp + 8 * i + (lane >> 2);
+            convert(codes + C::kRawV + r * 64 + 16 * (lane & 3), stage + kVOff, r, 2 * (lane & 3));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kFull + s));
+          rs = rs + 1 == C::kRaw ? 0 : rs + 1;
+          info = (info + 1) % kInfo;
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
           }
         }
       }
       cp_async_commit();
       cp_async_wait<0>();  // no copy may still be writing when the CTA leaves
-    } else if (warp < kMmaWarp + 2) {
+    } else if (warp == kMmaWarp && half == 1) {
+      // the odd CTA's stages, told to the even one as they are full
+      const uint32_t peer = cluster_addr(bar(C::kFull), 0);
+      int s = 0;
+      uint32_t ph = 0;
+      bool good = true;
+      while (good && next_piece(p, walk, lane, pc)) {
+#pragma unroll 1
+        for (int j = 0; j < pc.steps; ++j) {
+          good = wait(C::kFull + s, ph, kErrTimeoutFull);
+          if (!good) break;
+          fence_proxy_async_smem();  // the copies' writes, seen behind the barrier, for the MMAs
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(peer + 8 * s);
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp < kMmaWarp + 2 && half == 0) {
       // --------------------------------------------------------------- MMAs
       // tile a: the whole warp walks (warp-uniform operands), one elected lane issues
       const int a = static_cast<int>(uniform(warp - kMmaWarp));
       const uint32_t ub = uniform(base), ut = uniform(tmem);
-      constexpr uint32_t idesc_s = F8 ? tc_idesc_f16(128, kStep, false, false) : tc_idesc_bf16(128, kStep, false, false);
-      constexpr uint32_t idesc_o = F8 ? tc_idesc_f16(128, kHeadDim, false, true) : tc_idesc_bf16(128, kHeadDim, false, true);
-      const uint64_t dq0 = tc_sdesc(ub + a * kSlotBytes, 16, 1024, kSwizzle128B);
-      const uint64_t dk0 = tc_sdesc(ub + C::kSlotOff, 16, 1024, kSwizzle128B);
-      // V as B: N = 128 dims in two regions (LBO), K = tokens in 8-row groups (SBO)
-      const uint64_t dv0 = tc_sdesc(ub + C::kSlotOff, kHalfTile, 1024, kSwizzle128B);
+      constexpr uint32_t idesc_s = F8 ? tc_idesc_f16(256, kStep, false, false) : tc_idesc_bf16(256, kStep, false, false);
+      constexpr uint32_t idesc_o = F8 ? tc_idesc_f16(256, kHeadDim, false, true) : tc_idesc_bf16(256, kHeadDim, false, true);
+      const uint64_t dq0 = tc_sdesc(ub + a * kQTile, 16, 1024, kSwizzle128B);
+      const uint64_t dk0 = tc_sdesc(ub + C::kStageOff, 16, 1024, kSwizzle128B);
+      // V as B: N = 64 dims a CTA (one swizzle atom), K = tokens in 8-row groups (SBO)
+      const uint64_t dv0 = tc_sdesc(ub + C::kStageOff + kVOff, 128 * 128, 1024, kSwizzle128B);
       const uint32_t s_col = ut + 128 * a, o_col = ut + 256 + 128 * a;
       auto ubar = [&](int i) { return ub + C::kBarOff + 8u * static_cast<uint32_t>(i); };
-      int s = 0;
-      uint32_t ph = 0, np = 0, nq = 0;
+      int s = 0;  // stage and parity of step j
+      uint32_t ph = 0, np = 0, nq = 0, turn = 0;
       bool good = true;
-      auto advance = [&]() {
-        if (++s == C::kSlots) {
-          s = 0;
-          ph ^= 1;
-        }
-      };
-      while (good && walk.next(p)) {
-        const int steps = static_cast<int>(uniform(walk.steps));
-        const bool mine = uniform(walk.seqs(a)) > 0;
-        if (mine) good = wait(C::kQ + a, nq++ & 1, kErrTimeoutFull);
-        int vs = 0;
+      while (good && next_piece(p, walk, lane, pc)) {
+        const int steps = static_cast<int>(uniform(pc.steps));
+        const bool mine = uniform(pc.seqs(a)) > 0;
+        if (mine) good = wait_pair(C::kQ + a, nq++ & 1, kErrTimeoutFull);
 #pragma unroll 1
-        for (int j = 0; j <= steps && good; ++j) {
-          // O += P(j - 1) V(j - 1) behind S(j) = Q K(j) in the slots' order K(0) V(0) K(1) ..., so V's slot is the last one
-          int v_slot = vs;
-          const bool have_v = j > 0;
-          if (have_v) {
-            good = wait(C::kFull + s, ph, kErrTimeoutFull);
-            v_slot = s;
-            if (!good) break;
-            advance();
-          }
-          const int k_slot = s;
-          if (j < steps) {
-            good = wait(C::kFull + s, ph, kErrTimeoutFull);
-            if (!good) break;
-          }
+        for (int j = 0; j <= steps; ++j, ++turn) {
+          // O += P(j - 1) V(j - 1), then S(j) = Q K(j), in turn with the other tile's warp
+          const int vs = s == 0 ? C::kStages - 1 : s - 1;
+          if (j < steps) good = good && wait_pair(C::kFull + s, ph, kErrTimeoutFull);
+          if (a == 1 || turn > 0) good = good && wait(C::kTurn + a, (a == 1 ? turn : turn - 1) & 1, kErrTimeoutFull);
+          const bool pv = j > 0 && mine, qk = j < steps && mine;
+          if (pv) good = good && wait(C::kP + 2 * a, np & 1, kErrTimeoutFull);
+          if (!good) break;
           if (!F8) fence_proxy_async_smem();  // the copies' writes, seen behind the barrier, for the MMAs
-          if (have_v && mine) {
-            good = wait(C::kP + 2 * a, np & 1, kErrTimeoutFull);
-            if (!good) break;
-            tc_fence_after();
-            const uint64_t dv = dv0 + v_slot * (kSlotBytes >> 4);
+          tc_fence_after();
+          if (pv) {
+            const uint64_t dv = dv0 + vs * (kStageBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : (j > 1 ? 1u : 0u));
+              tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, kk ? 1u : (j > 1 ? 1u : 0u));
             good = wait(C::kP + 2 * a + 1, np & 1, kErrTimeoutFull);
             if (!good) break;
             ++np;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 4; kk < 8; ++kk) tc_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1u);
+            for (int kk = 4; kk < 8; ++kk) tc2_mma_tmem_a_warp(o_col, s_col + 8 * kk, dv + ((kk * 2048) >> 4), idesc_o, 1u);
           }
-          if (j < steps && mine) {
-            const uint64_t dk = dk0 + k_slot * (kSlotBytes >> 4);
+          const uint64_t dk = dk0 + s * (kStageBytes >> 4);
+          auto scores = [&](int r) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_bf16_warp(s_col, dq0 + (((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4),
-                               dk + (((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4), idesc_s, kk ? 1u : 0u);
-            tc_commit_warp(ubar(C::kS + a));
+            for (int kk = 0; kk < 4; ++kk)
+              tc2_mma_warp(s_col, dq0 + ((r * kQRegion + kk * 32) >> 4), dk + ((r * kKRegion + kk * 32) >> 4), idesc_s, (r | kk) ? 1u : 0u);
+          };
+          if (qk) scores(0);
+          if (lane == 0) mbar_arrive(bar(C::kTurn + 1 - a));  // early: the rest is issued before the other warp gets going
+          __syncwarp();
+          if (qk) {
+            scores(1);
+            tc2_commit_warp(ubar(C::kS + a));
           }
-          if (have_v) {
-            tc_commit_warp(ubar(C::kFree + v_slot));
-            if (mine && j == steps) tc_commit_warp(ubar(C::kO + a));
+          if (j > 0) {
+            tc2_commit_warp(ubar(C::kFree + vs));
+            if (mine && j == steps) tc2_commit_warp(ubar(C::kO + a));
           }
-          if (j < steps) {
-            tc_commit_warp(ubar(C::kFree + k_slot));
-            advance();
+          if (j < steps && ++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
           }
         }
       }
-      tc_commit_warp(ubar(C::kDone));  // every MMA done before tensor memory is freed
+      tc2_commit_warp(ubar(C::kDone));  // every MMA done before tensor memory is freed
       __syncwarp();
     }
     __syncwarp();
@@ -437,20 +528,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
     const int a = (warp - kRowWarp) >> 2, wq = warp & 3, t = 32 * wq + lane;
     const uint32_t quarter = static_cast<uint32_t>(32 * wq) << 16;
     const uint32_t s_col = tmem + quarter + 128 * a, o_col = tmem + quarter + 256 + 128 * a;
+    const uint32_t q_bar = cluster_addr(bar(C::kQ + a), 0), p_bar = cluster_addr(bar(C::kP + 2 * a), 0);
     const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes to the queries
     uint32_t scored = 0, units = 0, info = 0;
     bool good = true;
-    while (good && walk.next(p)) {
-      const int seqs = walk.seqs(a);
-      if (seqs == 0) {
-        info = (info + walk.steps) % kInfo;
+    while (good && next_piece(p, walk, lane, pc)) {
+      if (pc.seqs(a) == 0) {
+        info = (info + pc.steps) % kInfo;
         continue;
       }
       // the queries: sequence i's 8 rows are 2 KB in a row, 16 bytes a thread
-      const int seq = walk.seq0 + walk.row0 + a * kSeqTile;
+      const int seqs = pc.seqs(a, half), seq = pc.seq0 + pc.row0 + (2 * a + half) * kSeqTile;
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         (static_cast<int64_t>(seq) * kQoHeads + walk.head * kGroup) * kHeadDim) + t;
-      const uint32_t to = base + a * kSlotBytes + ((t & 15) >> 3) * kHalfTile;
+                                                         (static_cast<int64_t>(seq) * kQoHeads + pc.head * kGroup) * kHeadDim) + t;
+      const uint32_t to = base + a * kQTile + ((t & 15) >> 3) * kQRegion;
 #pragma unroll 4
       for (int i = 0; i < kSeqTile; ++i) {
         uint4 x = make_uint4(0, 0, 0, 0);
@@ -478,42 +569,68 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kQ + a));
+      if (lane == 0) mbar_arrive_cluster(q_bar);
       float sc = fabsf(p.scale_log2);
       if constexpr (F8) {
         asm volatile("bar.sync %0, 128;" ::"r"(1 + a) : "memory");
         sc *= reinterpret_cast<volatile float*>(sm + C::kRowOff)[128 * a + t];
       }
       sc = fmaxf(sc, 1e-37f);  // > 0: -inf * sc stays -inf
+      const uint64_t sc2 = pack2(sc, sc);
       float m = -INFINITY, cv = 0.f;
       uint64_t l2 = 0;
 #pragma unroll 1
-      for (int j = 0; j < walk.steps; ++j) {
+      for (int j = 0; j < pc.steps; ++j) {
         good = wait(C::kS + a, scored & 1, kErrTimeoutFull);
         if (!good) break;
         ++scored;
         tc_fence_after();
+        const uint32_t k_scales = base + C::kScaleOff + info * 2 * kStep * 4, v_scales = k_scales + kStep * 4;
+        uint32_t w[4];
+        ld_shared_u4(base + C::kMaskOff + 16 * info, w[0], w[1], w[2], w[3]);
         uint32_t s[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc_ld32(s_col + 32 * c, s + 32 * c);
         tc_wait_ld();
         if constexpr (F8) {
-          const uint32_t scales = base + C::kScaleOff + info * 2 * kStep * 4;
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            uint32_t x[4];
-            ld_shared_u4(scales + 4 * c, x[0], x[1], x[2], x[3]);
+          for (int c = 0; c < 128; c += 16) {
+            float x[16];
+            load16(k_scales + 4 * c, x);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[c + k] = __float_as_uint(__uint_as_float(s[c + k]) * __uint_as_float(x[k]));
+            for (int e = 0; e < 16; ++e) s[c + e] = __float_as_uint(__uint_as_float(s[c + e]) * x[e]);
           }
         }
-        uint32_t w[4];
-        ld_shared_u4(base + C::kMaskOff + 16 * info, w[0], w[1], w[2], w[3]);
         if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (((w[c >> 5] >> (c & 31)) & 1u) == 0) s[c] = 0xff800000u;  // -inf
         }
+        float iv = 1.f, cv_new = cv;
+        uint64_t iv2 = 0;
+        if constexpr (F8) {
+          uint32_t x[4];
+          ld_shared_u4(base + C::kTopOff + 16 * info, x[0], x[1], x[2], x[3]);
+          const float vm = fminf(fmaxf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]))), 0x1p126f);
+          cv_new = fmaxf(cv, vm > 0.f ? pow2_ceil(fmaxf(vm, 0x1p-126f)) : 0.f);
+          iv = cv_new > 0.f ? pow2_recip(cv_new) : 0.f;
+          iv2 = pack2(iv, iv);
+        }
+        auto weigh = [&](int c, uint64_t off2, uint32_t* pk, uint64_t& l) {  // of tokens 64 c .. 64 c + 63
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float v[16];
+            if constexpr (F8) load16(v_scales + 256 * c + 8 * k, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              pk[k + e] = weigh_pair<F8>(s[64 * c + 2 * (k + e)], s[64 * c + 2 * (k + e) + 1], sc2, off2, v[2 * e], v[2 * e + 1], iv2, l);
+          }
+        };
+        // Optimistic: the first half's weights are formed with the running maximum as it stands, beside the search for this
+        // step's; only if a row passed it by 2^8 (the first step, and seldom after) are they formed again.
+        uint32_t pk[32];
+        uint64_t l_new = 0, off2 = pack2(C::kShift - m, C::kShift - m);
+        weigh(0, off2, pk, l_new);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int k = 0; k < 32; ++k)
@@ -521,15 +638,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
                            __uint_as_float(s[4 * k + 3]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
         const bool move = top > m + kMoveBy;
-        float cv_new = cv, iv = 1.f;
-        if constexpr (F8) {
-          uint32_t x[4];
-          ld_shared_u4(base + C::kTopOff + 16 * info, x[0], x[1], x[2], x[3]);
-          const float vm = fminf(fmaxf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]))), 0x1p126f);
-          cv_new = fmaxf(cv, vm > 0.f ? pow2_ceil(fmaxf(vm, 0x1p-126f)) : 0.f);
-          iv = cv_new > 0.f ? pow2_recip(cv_new) : 0.f;
-        }
-        if (__any_sync(0xffffffffu, move || cv_new != cv)) {
+        if (__any_sync(0xffffffffu, move || m == -INFINITY || cv_new != cv)) {
           const float alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2(m - top));
           if (move) m = top;
           float lo, hi;
@@ -548,32 +657,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
             }
           }
           cv = cv_new;
+          const float off = m == -INFINITY ? 0.f : C::kShift - m;
+          off2 = pack2(off, off);
+          l_new = 0;
+          weigh(0, off2, pk, l_new);
         }
-        const float off = m == -INFINITY ? 0.f : C::kShift - m;
-        const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-          const uint32_t vscales = base + C::kScaleOff + (info * 2 + 1) * kStep * 4 + 256 * half;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float x0, x1;
-            unpack2(fma2(pack2(__uint_as_float(s[64 * half + 2 * k]), __uint_as_float(s[64 * half + 2 * k + 1])), sc2, off2), x0, x1);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            l2 = add2(l2, pack2(x0, x1));
-            if constexpr (F8) {
-              x0 *= ld_shared_f32(vscales + 8 * k) * iv;
-              x1 *= ld_shared_f32(vscales + 8 * k + 4) * iv;
-            }
-            pk[k] = pack_p<F8>(x0, x1);
-          }
-          tc_st32(s_col + 32 * half, pk);  // over scores that have been read
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kP + 2 * a + half));  // half of the tokens: the MMAs may start on it
-        }
+        tc_st32(s_col, pk);  // over scores that have been read
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(p_bar);  // half of the tokens: the MMAs may start on it
+        weigh(1, off2, pk, l_new);
+        l2 = add2(l2, l_new);
+        tc_st32(s_col + 32, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(p_bar + 8);
         info = (info + 1) % kInfo;
       }
       if (!good) break;
@@ -585,10 +685,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       l += hi;
       const float inv = l == 0.f ? 0.f : (F8 ? cv : 1.f) / l;
       const int i = t >> 3, h = t & 7;
-      const bool begins = walk.step0 == 0;
-      const int64_t block = begins ? static_cast<int64_t>(seq + i) * kKvHeads + walk.head
-                                   : static_cast<int64_t>(p.batch) * kKvHeads + static_cast<int64_t>(blockIdx.x) * kUnitSeqs + a * kSeqTile + i;
-      float* po = p.part_o + block * (kHeadDim * kGroup) + h;
+      const int64_t block = pc.step0 == 0 ? static_cast<int64_t>(seq + i) * kKvHeads + pc.head
+                                            : static_cast<int64_t>(p.batch) * kKvHeads + static_cast<int64_t>(pair) * kUnitSeqs + (2 * a + half) * kSeqTile + i;
+      float* po = p.part_o + block * (kHeadDim * kGroup) + h * kHeadDim;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -596,7 +695,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
         tc_wait_ld();
         if (i < seqs)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) po[(32 * c + k) * kGroup] = __uint_as_float(o[k]) * inv;
+          for (int k = 0; k < 32; k += 8) store_f8(po + 32 * c + k, o + k, inv);
       }
       if (i < seqs) p.part_lse[block * kGroup + h] = l == 0.f ? -INFINITY : m - C::kShift + log2f(l);
       tc_fence_before();
@@ -608,7 +707,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tc_dealloc(tmem, 512);
+  cluster_sync();  // the other CTA's arrivals and MMAs are done too
+  if (warp == kMmaWarp) tc2_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------- join
@@ -628,8 +728,8 @@ __global__ void __launch_bounds__(kHeadDim) gqa_shared_join_kernel(const SharedP
   const bool few = p.groups <= kHeadDim;
   __shared__ int64_t start_s[kHeadDim + 1];
   if (few && p.pre_ctas > 0) {
-    int t, s0, m;
-    int64_t upto = tid < p.groups ? group_steps(p, tid, t, s0, m) : 0;
+    int t, s0, m, f, n;
+    int64_t upto = tid < p.groups ? group_steps(p, tid, t, s0, m, f, n) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
@@ -647,18 +747,18 @@ __global__ void __launch_bounds__(kHeadDim) gqa_shared_join_kernel(const SharedP
   const int total = max(0, min(__ldcg(p.kv_indptr + p.batch), p.index_count));
   bool waited = false;
   for (int b = blockIdx.x / kKvHeads; b < p.batch; b += gridDim.x / kKvHeads) {
-    // pieces of the prefix: the first in the sequence's block, the others in their CTA's
+    // pieces of the prefix: the first in the sequence's block, the others in their pair's
     int pre = 0, own = 0, cta0 = 0, local = 0;
     const int lo = max(0, min(__ldcg(p.kv_indptr + b), total)), hi = min(__ldcg(p.kv_indptr + b + 1), total);
     const int group = p.pre_ctas > 0 ? group_of(p, b) : -1;
     if (group >= 0) {
-      int tiles, seq0, members;
-      group_steps(p, group, tiles, seq0, members);
+      int tiles, seq0, members, first_token, n;
+      group_steps(p, group, tiles, seq0, members, first_token, n);
       if (tiles > 0) {
-        const int64_t run = steps_per_cta(few ? start_s[p.groups] : __ldcg(p.group_start + p.groups), p.pre_ctas);
+        const int64_t run = steps_per_pair(few ? start_s[p.groups] : __ldcg(p.group_start + p.groups), p.pre_ctas / 2);
         const int64_t first = (few ? start_s[group] : __ldcg(p.group_start + group)) + (static_cast<int64_t>((b - seq0) / kUnitSeqs) * kKvHeads + g) * tiles;
         cta0 = static_cast<int>(first / run);
-        pre = min(static_cast<int>((first + tiles - 1) / run), p.pre_ctas - 1) - cta0 + 1;
+        pre = min(static_cast<int>((first + tiles - 1) / run), p.pre_ctas / 2 - 1) - cta0 + 1;
         local = (b - seq0) % kUnitSeqs;
       }
     }
@@ -709,10 +809,18 @@ __global__ void __launch_bounds__(kHeadDim) gqa_shared_join_kernel(const SharedP
         acc[k] *= sc;
       }
       __syncthreads();
-#pragma unroll 8
+#pragma unroll 4
       for (int k = 0; k < n; ++k) {
-        const float4* o = reinterpret_cast<const float4*>(p.part_o + part_s[k] * kPart + tid * kGroup);
-        const float4 oa = __ldcg(o), ob = __ldcg(o + 1);
+        const float* o = p.part_o + part_s[k] * kPart;
+        float4 oa, ob;
+        if (i0 + k < pre) {  // [8 heads][128 dims]
+          o += tid;
+          oa = make_float4(__ldcg(o), __ldcg(o + kHeadDim), __ldcg(o + 2 * kHeadDim), __ldcg(o + 3 * kHeadDim));
+          ob = make_float4(__ldcg(o + 4 * kHeadDim), __ldcg(o + 5 * kHeadDim), __ldcg(o + 6 * kHeadDim), __ldcg(o + 7 * kHeadDim));
+        } else {             // [128 dims][8 heads]
+          oa = __ldcg(reinterpret_cast<const float4*>(o + tid * kGroup));
+          ob = __ldcg(reinterpret_cast<const float4*>(o + tid * kGroup) + 1);
+        }
         const float4 wa = *reinterpret_cast<const float4*>(weight_s[k]), wb = *reinterpret_cast<const float4*>(weight_s[k] + 4);
         const float o8[8] = {oa.x, oa.y, oa.z, oa.w, ob.x, ob.y, ob.z, ob.w}, w8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
@@ -740,10 +848,10 @@ static cudaError_t launch_prefix(const SharedParams& p, cudaStream_t stream) {
   static std::atomic<int> configured[kMaxDevices];
   const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_shared_prefix_kernel<F8>), PrefixCfg<F8>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_chained(gqa_shared_prefix_kernel<F8>, dim3(p.pre_ctas), kPreThreads, PrefixCfg<F8>::kBytes, stream, 1, p);
+  return launch_chained(gqa_shared_prefix_kernel<F8>, dim3(p.pre_ctas), kPreThreads, PrefixCfg<F8>::kBytes, stream, 2, p);
 }
 
-int shared_prefix_blocks(int batch, int ctas) { return batch * kKvHeads + ctas * kUnitSeqs; }
+int shared_prefix_blocks(int batch, int ctas) { return batch * kKvHeads + ctas / 2 * kUnitSeqs; }
 
 cudaError_t launch_shared(const SharedParams& p, const DecodeParams& own, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
