@@ -307,11 +307,13 @@ __global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockPa
   __shared__ int list[kListed], listed;
   __shared__ uint64_t listed_key[kListed];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the call's inputs are there: the score kernel let this one start behind its own wait
+  RowView v = row_view(p, static_cast<int>(blockIdx.x / kKvHeads));
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t unit = blockIdx.x; unit < static_cast<int64_t>(p.rows) * kKvHeads; unit += gridDim.x) {
     const int row = static_cast<int>(unit / kKvHeads), g = static_cast<int>(unit % kKvHeads);
-    const RowView v = row_view(p, row);
+    if (unit != blockIdx.x) v = row_view(p, row);
     const int* table = p.block_table + static_cast<int64_t>(max(v.req, 0)) * p.width;
     const float* scores = p.scores + unit * p.width;
     uint32_t* words = p.width <= kHeldWords ? held : reinterpret_cast<uint32_t*>(p.scores + unit * p.width);

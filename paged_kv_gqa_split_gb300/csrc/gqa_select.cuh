@@ -34,6 +34,8 @@ __device__ __forceinline__ int2 block_sum2(int2* sums, int2 x) {
   return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
 }
 
+constexpr int kMostBlocks = 8;  // of a cluster
+
 template <int THREADS>
 struct SelectSpace {
   alignas(16) int hist[3][256];  // of this block, in turns
@@ -64,28 +66,32 @@ __device__ __forceinline__ Key select_kth(SelectSpace<THREADS>& sp, int n, int k
     turn = turn == 2 ? 0 : turn + 1;
     for (int i = threadIdx.x; i < 256; i += THREADS) sp.hist[turn][i] = 0;  // the next pass's: read last two passes ago
     const Key mask = shift == kBits - 8 ? Key(0) : (~Key(0)) << (shift + 8);
-#pragma unroll 2
-    for (int i0 = 0; i0 < n; i0 += THREADS) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      int d = 256;
-      if (i < n) {
-        const Key x = key(i);
-        if ((x & mask) == prefix) d = static_cast<int>((x >> shift) & 255);
-      }
-      // keys of one size share their top digits: one addition where all lanes have the same
-      const int d0 = __shfl_sync(0xffffffffu, d, 0);
-      if (__all_sync(0xffffffffu, d == d0)) {
-        if (d0 < 256 && lane == 0) atomicAdd(&hist[d0], 32);
-      } else if (d < 256) {
-        atomicAdd(&hist[d], 1);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 4 * THREADS) {  // four keys a thread, their loads together
+      Key x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = key(min(i0 + u * THREADS + static_cast<int>(threadIdx.x), n - 1));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int d = i0 + u * THREADS + static_cast<int>(threadIdx.x) < n && (x[u] & mask) == prefix ? static_cast<int>((x[u] >> shift) & 255) : 256;
+        // keys of one size share their top digits: one addition where all lanes have the same
+        const int d0 = __shfl_sync(0xffffffffu, d, 0);
+        if (__all_sync(0xffffffffu, d == d0)) {
+          if (d0 < 256 && lane == 0) atomicAdd(&hist[d0], 32);
+        } else if (d < 256) {
+          atomicAdd(&hist[d], 1);
+        }
       }
     }
     if constexpr (CLUSTERED) {
       auto cluster = cooperative_groups::this_cluster();
       cluster.sync();  // (others read this turn's counts until the next pass's, and they are cleared after that)
       for (int i = threadIdx.x; i < 256; i += THREADS) {
-        int sum = 0;
-        for (unsigned r = 0; r < cluster.num_blocks(); ++r) sum += cluster.map_shared_rank(hist, r)[i];
+        int x[kMostBlocks], sum = 0;  // (their loads together)
+#pragma unroll
+        for (int r = 0; r < kMostBlocks; ++r) x[r] = r < static_cast<int>(cluster.num_blocks()) ? cluster.map_shared_rank(hist, r)[i] : 0;
+#pragma unroll
+        for (int r = 0; r < kMostBlocks; ++r) sum += x[r];
         sp.all[i] = sum;
       }
       hist = sp.all;
@@ -160,10 +166,15 @@ __device__ __forceinline__ void select_in_order(SelectSpace<THREADS>& sp, int n,
   const int run = ((n + THREADS - 1) / THREADS) * 32, first = warp * run, end = min(first + run, n);
   int2 mine = make_int2(0, 0);  // chosen outright, ties
 #pragma unroll 1
-  for (int i0 = first; i0 < end; i0 += 32) {
-    const int c = i0 + lane < end ? cls(i0 + lane) : 0;
-    mine.x += __popc(__ballot_sync(0xffffffffu, c == 2));
-    mine.y += __popc(__ballot_sync(0xffffffffu, c == 1));
+  for (int i0 = first; i0 < end; i0 += 128) {
+    int c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) c[u] = i0 + 32 * u + lane < end ? cls(i0 + 32 * u + lane) : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      mine.x += __popc(__ballot_sync(0xffffffffu, c[u] == 2));
+      mine.y += __popc(__ballot_sync(0xffffffffu, c[u] == 1));
+    }
   }
   __syncthreads();
   if (lane == 0) sp.sums[warp] = mine;

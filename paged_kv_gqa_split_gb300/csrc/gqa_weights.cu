@@ -55,16 +55,15 @@ cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream) {
 // keep_first and the last keep_last stay, and of those between them the heaviest; the sequence's share of the new lists
 // begins where the sequences before it end, which every block sums up by itself. The weights are read once into shared
 // memory as ordered words (from global memory each time where a run does not fit).
-constexpr int kEvictThreads = 512;
 constexpr int kEvictHeld = 48 * 1024;   // words of shared memory at most
 constexpr int kEvictRun = 8 * 1024;     // tokens a block, before a cluster of twice as many is taken
 constexpr int kEvictBlocks = 8;         // blocks of a cluster at most (the portable size)
 constexpr uint32_t kStays = 1, kGoes = 0;  // marks below any key
 
-template <bool CLUSTERED>
-__global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictParams p) {
+template <bool CLUSTERED, int THREADS>
+__global__ void __launch_bounds__(THREADS) gqa_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t held[];
-  __shared__ SelectSpace<kEvictThreads> sp;
+  __shared__ SelectSpace<THREADS> sp;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x;
@@ -76,14 +75,14 @@ __global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictPar
   for (int b = blockIdx.x / blocks; b < p.batch; b += gridDim.x / blocks) {
     int2 ahead = make_int2(0, 0), all = make_int2(0, 0);  // tokens kept and tokens: of the sequences before this one, of all
     int lo = 0;
-    for (int i = tid; i < p.batch; i += kEvictThreads) {
+    for (int i = tid; i < p.batch; i += THREADS) {
       const int n = length(i, lo);
       all.x += min(n, p.budget);
       all.y += n;
       if (i < b) ahead.x += min(n, p.budget), ahead.y += n;
     }
-    ahead = block_sum2<kEvictThreads>(sp.sums, ahead);
-    all = block_sum2<kEvictThreads>(sp.sums, all);
+    ahead = block_sum2<THREADS>(sp.sums, ahead);
+    all = block_sum2<THREADS>(sp.sums, all);
     const int n = length(b, lo), keep = min(n, p.budget), before = ahead.x, gone = ahead.y - ahead.x;
     if (tid == 0 && rank == 0) {
       if (b == 0) p.new_indptr[0] = p.freed_indptr[0] = 0;
@@ -96,30 +95,35 @@ __global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictPar
     const int take = keep - (n - (mid_hi - mid_lo));  // of the middle
     const int run = (n + blocks - 1) / blocks, first = min(rank * run, n), mine = min(run, n - first);
     const bool cut = n > p.budget, hold = mine <= p.held;
-    auto word = [&](int i) -> uint32_t {  // of token first + i
-      const int j = first + i;
-      if (j < mid_lo || j >= mid_hi) return kStays;
-      return take > 0 ? ordered_bits(j < p.width ? __ldcg(w + j) : 0.f) : kGoes;
-    };
+    auto weight = [&](int j) { return p.width > 0 && j < p.width ? __ldcg(w + j) : 0.f; };
+    auto word_of = [&](int j, float x) -> uint32_t { return j < mid_lo || j >= mid_hi ? kStays : (take > 0 ? ordered_bits(x) : kGoes); };
+    auto word = [&](int i) { return word_of(first + i, weight(first + i)); };
     uint32_t least = kKeyLeast;
     int ties = 0;
     if (cut) {
       if (hold) {
         __syncthreads();  // (the words of the sequence before)
-#pragma unroll 8
-        for (int i = tid; i < mine; i += kEvictThreads) held[i] = word(i);
+#pragma unroll 1
+        for (int i0 = tid; i0 < mine; i0 += 8 * THREADS) {  // eight words a thread, their loads together
+          float x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x[u] = weight(first + min(i0 + u * THREADS, mine - 1));
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (i0 + u * THREADS < mine) held[i0 + u * THREADS] = word_of(first + i0 + u * THREADS, x[u]);
+        }
         __syncthreads();
       }
       if (take > 0) {
-        least = hold ? select_kth<kEvictThreads, CLUSTERED, uint32_t>(sp, mine, take, [&](int i) { return held[i]; }, ties)
-                     : select_kth<kEvictThreads, CLUSTERED, uint32_t>(sp, mine, take, word, ties);
+        least = hold ? select_kth<THREADS, CLUSTERED, uint32_t>(sp, mine, take, [&](int i) { return held[i]; }, ties)
+                     : select_kth<THREADS, CLUSTERED, uint32_t>(sp, mine, take, word, ties);
       }
     }
     struct Token {
       int page;
       float weight;
     };
-    select_in_order<kEvictThreads, CLUSTERED, 8>(
+    select_in_order<THREADS, CLUSTERED, 8>(
         sp, mine, ties,
         [&](int i) {
           if (!cut) return 2;
@@ -128,29 +132,29 @@ __global__ void __launch_bounds__(kEvictThreads) gqa_evict_kernel(const EvictPar
         },
         [&](int i) {
           const int j = first + i;
-          return Token{__ldcg(p.kv_indices + lo + j), j < p.width ? __ldcg(w + j) : 0.f};
+          return Token{__ldcg(p.kv_indices + lo + j), weight(j)};
         },
         [&](int i, const Token& t, int at, bool stay) {
           const int to = stay ? before + at : gone + first + i - at;
           if (to < p.index_count) (stay ? p.new_indices : p.freed)[to] = t.page;  // (offsets that decrease could pass it)
           if (stay && at < p.width) wo[at] = t.weight;
         });
-    for (int j = keep + rank * kEvictThreads + tid; j < p.width; j += blocks * kEvictThreads) wo[j] = 0.f;
+    for (int j = keep + rank * THREADS + tid; j < p.width; j += blocks * THREADS) wo[j] = 0.f;
     // behind the last sequence's, a share a block
     const int share = (p.index_count + p.batch * blocks - 1) / (p.batch * blocks), from = (b * blocks + rank) * share;
     const int to = static_cast<int>(min(static_cast<int64_t>(from) + share, static_cast<int64_t>(p.index_count)));
-    for (int i = max(from, all.x) + tid; i < to; i += kEvictThreads) p.new_indices[i] = -1;
-    for (int i = max(from, all.y - all.x) + tid; i < to; i += kEvictThreads) p.freed[i] = -1;
+    for (int i = max(from, all.x) + tid; i < to; i += THREADS) p.new_indices[i] = -1;
+    for (int i = max(from, all.y - all.x) + tid; i < to; i += THREADS) p.freed[i] = -1;
   }
 }
 
-template <bool CLUSTERED>
+template <bool CLUSTERED, int THREADS>
 static cudaError_t launch_evict_form(const EvictParams& p, cudaStream_t stream) {
   static std::atomic<int> configured[kMaxDevices];
-  const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED>), kEvictHeld * 4);
+  const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), kEvictHeld * 4);
   if (e != cudaSuccess) return e;
   const int64_t units = p.batch < (1 << 16) ? p.batch : (1 << 16);
-  return launch_chained(gqa_evict_kernel<CLUSTERED>, dim3(static_cast<unsigned>(units * p.cluster)), kEvictThreads, p.held * 4, stream, p.cluster, p);
+  return launch_chained(gqa_evict_kernel<CLUSTERED, THREADS>, dim3(static_cast<unsigned>(units * p.cluster)), THREADS, p.held * 4, stream, p.cluster, p);
 }
 
 cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
@@ -158,7 +162,7 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
   while (p.cluster < kEvictBlocks && p.width > p.cluster * kEvictRun) p.cluster *= 2;
   const int run = (p.width + p.cluster - 1) / p.cluster;
   p.held = run < kEvictHeld ? run : kEvictHeld;
-  return p.cluster > 1 ? launch_evict_form<true>(p, stream) : launch_evict_form<false>(p, stream);
+  return p.cluster > 1 ? launch_evict_form<true, 1024>(p, stream) : launch_evict_form<false, 512>(p, stream);
 }
 
 }  // namespace gqa
