@@ -14,11 +14,12 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import HEAD_DIM, NUM_KV_HEADS, NUM_QO_HEADS, load
-from .serving import _INT_MAX, _cache_format, _call, _check, _empty_strided_cuda, _entries, _index, _new
+from .serving import CACHE_BF16, _INT_MAX, _cache_format, _call, _check, _empty_strided_cuda, _entries, _index, _new
 
 
 _SCALE = HEAD_DIM ** -0.5
 _OUT_STRIDE, _LSE_STRIDE = (NUM_QO_HEADS * HEAD_DIM, HEAD_DIM, 1), (NUM_QO_HEADS, 1)
+_BF16_PAGE = (1, NUM_KV_HEADS, HEAD_DIM)
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
@@ -52,14 +53,20 @@ def _queries(index, q):
 
 def _paged(index, k_cache, v_cache):
     """(format, pages) of CSR-paged caches."""
-    if not (_plain(index, _BF16, 4, k_cache, v_cache) or _plain(index, torch.uint8, 2, k_cache, v_cache)):
-        _check(index, None, True, k_cache=k_cache, v_cache=v_cache)
+    if _plain(index, _BF16, 4, k_cache, v_cache):
+        shape = k_cache.shape
+        if shape[1:] == _BF16_PAGE and v_cache.shape == shape:
+            return CACHE_BF16, shape[0]
+    _check(index, None, True, k_cache=k_cache, v_cache=v_cache)
     return _cache_format(k_cache, v_cache)
+
+
+_current = torch._C._cuda_getDevice
 
 
 def _alloc(index, shape, stride, dtype, stream):
     """_new with the strides of a contiguous tensor of that shape, known to the caller."""
-    if stream is None and _empty_strided_cuda is not None and index == torch._C._cuda_getDevice():
+    if stream is None and _empty_strided_cuda is not None and index == _current():
         return _empty_strided_cuda(shape, stride, dtype)
     return _new(index, shape, dtype, stream)
 
@@ -89,7 +96,7 @@ def _workspace(index, given, stream, what, *sizes):
     size_of = _entries.get(what)
     if size_of is None:
         size_of = _entries[what] = getattr(load(), what)
-    if index == torch._C._cuda_getDevice():
+    if index == _current():
         size = size_of(*sizes)
     else:
         with torch.cuda.device(index):

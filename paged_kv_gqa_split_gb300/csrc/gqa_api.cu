@@ -359,6 +359,7 @@ int run(const void* q, const void* k, const void* v, const int32_t* indptr, cons
   mp.epoch = epoch;
   mp.use_pdl = profile ? 0 : 1;
   mp.fuse_max_splits = tune.fuse_max_splits;
+  mp.index_cap = -1;
   if (gqa::launch_merge(ng, mp, stream) != cudaSuccess) return GQA_ERR_LAUNCH;
   t_last_launches = before + 2;
   return GQA_OK;

@@ -19,7 +19,7 @@ constexpr int kRowValues = kKvHeads * kHeadDim;  // of a token, or of a block's 
 // Teams of 64 lanes, 16 bytes a lane and token. The blocks to renew, request by request, are numbered by prefix sums that
 // every block of threads forms by itself, 256 requests at a time; a team takes every gridDim-th one. Where there are no
 // more of them than blocks of threads (a decode step's), the four teams of a block share one. Bound by the keys' bytes:
-// 131072 tokens in pages of 32 take BOUNDS_US.
+// 131072 tokens in pages of 32 take 31 us (4.4 TB/s), one token each of 64 requests 5 us (two dependent loads and the launch).
 constexpr int kBoundThreads = 256, kBoundTeams = kBoundThreads / 64;
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {

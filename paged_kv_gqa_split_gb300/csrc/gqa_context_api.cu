@@ -65,6 +65,7 @@ gqa::MergeParams merge_params(const gqa::DecodeParams& d) {
   m.sparse_total = d.sparse_total;
   m.use_pdl = 1;
   m.fuse_max_splits = 1;
+  m.index_cap = d.sparse_topk > 0 ? -1 : d.index_count;
   return m;
 }
 

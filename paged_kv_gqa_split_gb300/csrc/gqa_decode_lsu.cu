@@ -570,6 +570,7 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
             pb = wb + k;
             seq_lo = __shfl_sync(0xffffffffu, win, k);
             seq_hi = __shfl_sync(0xffffffffu, win, k + 1);
+            if constexpr (kLeaveOut) seq_hi = min(seq_hi, T);
           }
           p_hi = min(seq_hi, t_stop);
           p_flags = F_QLOAD | ((tt == seq_lo && p_hi == seq_hi) ? F_FINAL : 0) |

@@ -90,6 +90,7 @@ struct MergeParams {
   int sparse_total;
   int use_pdl;
   int fuse_max_splits;  // sequences of at most this many pieces were merged by the decode kernel
+  int index_cap;        // kFormScores: offsets are cut to it; -1: they are not
 };
 
 // Decode with the split partials in a fixed caller scratch (gqa_api.cu): a plan

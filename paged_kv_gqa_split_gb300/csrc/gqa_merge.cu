@@ -92,10 +92,11 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
   // their round trip overlaps it; nothing waits on them until after it.
   // sparse rows (sparse_topk > 0) are never empty and have no kv_indptr
   const bool sparse = p.sparse_topk > 0;
-  const int T = sparse ? p.sparse_total : __ldg(p.kv_indptr + B);
+  const auto offset = [&](int b) { const int x = __ldg(p.kv_indptr + b); return p.index_cap < 0 ? x : min(x, p.index_cap); };
+  const int T = sparse ? p.sparse_total : offset(B);
   const bool check_empty = !sparse && j < B;
-  const int e_lo = check_empty ? __ldg(p.kv_indptr + j) : 0;
-  const int e_hi = check_empty ? __ldg(p.kv_indptr + j + 1) : 0;
+  const int e_lo = check_empty ? offset(j) : 0;
+  const int e_hi = check_empty ? offset(j + 1) : 0;
 
   // Everything below reads what the decode grid wrote.
   pdl_wait();
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
 
   // Empty sequences: O = 0, LSE = -inf (no decode CTA touches them).
   for (int b = j; !sparse && b < B; b += gridDim.x) {
-    if (b == j ? e_lo == e_hi : __ldg(p.kv_indptr + b) == __ldg(p.kv_indptr + b + 1)) {
+    if (b == j ? e_lo == e_hi : offset(b) == offset(b + 1)) {
       uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(b) * kQoHeads * kHeadDim);
       for (int i = tid; i < kQoHeads * kHeadDim * 2 / 16; i += kMergeThreads) ob[i] = make_uint4(0, 0, 0, 0);
       if (tid < kQoHeads && p.lse != nullptr) p.lse[static_cast<int64_t>(b) * kQoHeads + tid] = -INFINITY;

@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(THREADS) gqa_evict_kernel(const EvictParams p)
         });
     for (int j = keep + rank * THREADS + tid; j < p.width; j += blocks * THREADS) wo[j] = 0.f;
     // behind the last sequence's, a share a block
-    const int share = (p.index_count + p.batch * blocks - 1) / (p.batch * blocks), from = (b * blocks + rank) * share;
-    const int to = static_cast<int>(min(static_cast<int64_t>(from) + share, static_cast<int64_t>(p.index_count)));
-    for (int i = max(from, all.x) + tid; i < to; i += THREADS) p.new_indices[i] = -1;
-    for (int i = max(from, all.y - all.x) + tid; i < to; i += THREADS) p.freed[i] = -1;
+    const int64_t shares = static_cast<int64_t>(p.batch) * blocks, share = (p.index_count + shares - 1) / shares;
+    const int64_t from = (static_cast<int64_t>(b) * blocks + rank) * share, to = min(from + share, static_cast<int64_t>(p.index_count));
+    for (int64_t i = max(from, static_cast<int64_t>(all.x)) + tid; i < to; i += THREADS) p.new_indices[i] = -1;
+    for (int64_t i = max(from, static_cast<int64_t>(all.y) - all.x) + tid; i < to; i += THREADS) p.freed[i] = -1;
   }
 }
 

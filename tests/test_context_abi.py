@@ -166,3 +166,17 @@ def test_oracle_eviction_by_hand():
     assert got[0].tolist() == [[5, 1, 9, 7, 0, 0], [1, 2, 0, 0, 0, 0]]
     assert got[1].tolist() == [0, 4, 6] and got[2].tolist() == [10, 11, 12, 15, 20, 21, -1, -1]
     assert got[3].tolist() == [0, 2, 2] and got[4].tolist() == [13, 14] + [-1] * 6
+
+
+def test_chained_kernels_use_no_noncoherent_load():
+    """Kernels that start before the ones ahead of them end read with ld.cg or plain loads (source check): the
+    non-coherent load may be moved ahead of the wait."""
+    import os
+    import re
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_gqa_split_gb300", "csrc")
+    for name in ("gqa_shared.cu", "gqa_blocks.cu", "gqa_weights.cu", "gqa_select.cuh"):
+        with open(os.path.join(src, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        assert "__ldg(" not in text and "__restrict__" not in text, name
+        for body in re.split(r"__global__", text)[1:]:
+            assert "pdl_wait();" in body.split("launch_chained")[0], name

@@ -256,3 +256,19 @@ def test_streams_graphs_and_workspaces():
           for n in (lib.gqa_block_select_ws_size(rows, width), lib.gqa_block_sparse_decode_ws_size(rows, 20, 16))]
     blocks = select(w, 20, workspace=ws[0])
     assert torch.equal(blocks, want[0]) and torch.equal(attend(w, blocks, workspace=ws[1])[0], want[1])
+
+
+def test_choice_among_more_blocks_than_are_held():
+    w = make([50_000], 1, 10)
+    pkg.block_bounds(w["k"], w["bounds"], w["table"], w["lens"])
+    assert np.array_equal(select(w, 700, 1, 2).cpu().numpy(), chosen(w, 700, 1, 2))
+
+
+def test_bounds_of_many_requests():
+    """More requests than are numbered at once; few blocks to renew, and more than there are blocks of threads."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 60, (700,), generator=g).tolist()
+    w = make(lens, 8, 11)
+    for first in (None, i32([max(0, n - 1) for n in lens])):
+        want = cx.bounds_oracle(w["k"], w["bounds"], w["table"], w["lens"], first)
+        assert same_values(pkg.block_bounds(w["k"], w["bounds"], w["table"], w["lens"], first), want)

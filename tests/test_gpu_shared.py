@@ -191,3 +191,66 @@ def test_offsets_past_the_tables_are_cut():
     args[6] = torch.tensor([0, 10, 500], dtype=torch.int32).cuda()
     out, lse = pkg.shared_run(*args)
     assert torch.isfinite(out.float()[0]).all()
+
+
+def test_many_groups():
+    """More groups than a block of threads counts at once, most of them of one sequence, empty ones among them."""
+    g = torch.Generator().manual_seed(11)
+    members = torch.randint(0, 3, (1300,), generator=g).tolist()
+    prefixes = torch.randint(0, 40, (1300,), generator=g).tolist()
+    members[700], prefixes[700] = 70, 300
+    args = make(prefixes, members, 2, [0, 1, 2], seed=12)
+    out, lse = pkg.shared_run(*args)
+    check(args, out, lse)
+
+
+def test_fp8_scales_of_zero_and_far_apart():
+    args = list(make([400], [20], 0, [5, 0], True, seed=13))
+    k, v = args[1], args[2]
+    scales = v[:, 512:].view(torch.float32)
+    scales[::3] = 0.0
+    scales[1::7] *= 2.0 ** 20
+    scales[2::7] *= 2.0 ** -30
+    k[:, 512:].view(torch.float32)[::5] = 0.0
+    out, lse = pkg.shared_run(*args)
+    check(args, out, lse)
+    scales.zero_()
+    out, lse = pkg.shared_run(*args)
+    check(args, out, lse)
+    assert torch.equal(out, torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wait_that_gives_up_and_the_next_call(fp8):
+    """With a limit of a few nanoseconds the waits of the prefix pass run out: the call completes, the device error word
+    carries a timeout bit and no other, and the next call gives what the one before gave."""
+    args = make([3000], [40], 0, [20], fp8, seed=14)
+    want = pkg.shared_run(*args)
+    assert _lib.gqa_paged_decode_device_error() == 0
+    try:
+        assert _lib.gqa_paged_decode_test_wait_limit_ns(5) == 0
+        for _ in range(3):
+            pkg.shared_run(*args)
+        torch.cuda.synchronize()
+        flags = _lib.gqa_paged_decode_device_error()
+        assert flags & 3 and not flags & ~3, flags
+    finally:
+        _lib.gqa_paged_decode_test_wait_limit_ns(0)
+    for _ in range(3):
+        got = pkg.shared_run(*args)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+def test_two_streams_at_once():
+    a, b = make([2000], [33], 0, [100], seed=15), make([50, 900], [2, 20], 1, [7, 300], True, seed=16)
+    want = pkg.shared_run(*a), pkg.shared_run(*b)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append([pkg.shared_run(*x, stream=s) for x, s in zip((a, b), streams)])
+    torch.cuda.synchronize()
+    for pair in got:
+        for x, y in zip(pair, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])

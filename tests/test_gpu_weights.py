@@ -156,3 +156,20 @@ def test_steps_with_eviction(fp8):
     side = pkg.kv_evict(side[2], args[3], args[4], 128, keep_first=4, keep_last=32, stream=stream)
     stream.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(side, (w2, indptr, ids, freed_at, freed)))
+
+
+def test_offsets_past_the_indices_are_cut():
+    args = list(make([30, 20], 64, False, 8))
+    whole = pkg.run_weighted(*args)
+    args[3] = torch.tensor([0, 30, 5000], dtype=torch.int32).cuda()
+    got = pkg.run_weighted(*args)
+    assert all(torch.equal(a, b) for a, b in zip(got, whole))
+    args[3] = torch.tensor([0, 50, 5000], dtype=torch.int32).cuda()  # the second begins where the indices end
+    out, lse, w = pkg.run_weighted(*args)
+    assert torch.equal(out[1], torch.zeros_like(out[1])) and torch.isneginf(lse[1]).all() and torch.equal(w[1], args[5][1])
+
+
+@pytest.mark.parametrize("n", [500_000])
+def test_evict_more_than_the_blocks_hold(n):
+    w, indptr, ids = listed([n, 3], n, 3, "few")
+    evict_check((w, indptr, ids, n // 3, 10, 1000), pkg.kv_evict(w, indptr, ids, n // 3, 10, 1000))
