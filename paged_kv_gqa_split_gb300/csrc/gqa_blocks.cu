@@ -351,8 +351,13 @@ __global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockPa
     int ties = 0;
     auto open = [&](uint32_t x) { return x > kChosen && (x >= kKeyInf || x == kKeyLeast || (x >= below && x <= above)); };
     if (!all && take > 0) {
-      int unused = 0;
-      const uint32_t kth = select_kth<THREADS, false, uint32_t>(sp, v.count, take, [&](int i) { return words[i]; }, unused);
+      uint32_t kth;
+      if (THREADS == 128 && v.count <= 256) {
+        kth = warp_kth<8>(words, v.count, take);
+      } else {
+        int unused = 0;
+        kth = select_kth<THREADS, false, uint32_t>(sp, v.count, take, [&](int i) { return words[i]; }, unused);
+      }
       const float mark = ordered_float(kth);
       if (fabsf(mark) < INFINITY) {
         above = ordered_bits(__fadd_ru(mark, __fmul_ru(2.f, wide)));
@@ -454,33 +459,39 @@ cudaError_t launch_block_select(const BlockParams& p, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ slots
-// A warp per listed block, a lane per token.
-__global__ void __launch_bounds__(256) gqa_block_slots_kernel(const BlockParams p) {
+// A warp per kSlotBlocks listed blocks: a lane looks a block up, then the warp writes the blocks' slots in a row.
+constexpr int kSlotThreads = 128, kSlotBlocks = 8;
+
+__global__ void __launch_bounds__(kSlotThreads) gqa_block_slots_kernel(const BlockParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t per_row = static_cast<int64_t>(p.top) * p.page_size;
-  for (int64_t unit = blockIdx.x; unit < static_cast<int64_t>(p.rows) * kKvHeads; unit += gridDim.x) {
-    const int row = static_cast<int>(unit / kKvHeads), g = static_cast<int>(unit % kKvHeads);
+  const int64_t per_row = static_cast<int64_t>(p.top) * p.page_size, parts = (p.top + kSlotBlocks - 1) / kSlotBlocks;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kSlotThreads / 32);
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * (kSlotThreads / 32) + (threadIdx.x >> 5); x < p.rows * kKvHeads * parts; x += warps) {
+    const int64_t unit = x / parts;
+    const int j0 = static_cast<int>(x - unit * parts) * kSlotBlocks, row = static_cast<int>(unit / kKvHeads), g = static_cast<int>(unit % kKvHeads);
+    const int i = lane < kSlotBlocks && j0 + lane < p.top ? __ldcg(p.blocks + unit * p.top + j0 + lane) : -1;
     const RowView v = row_view(p, row);
-    int* slots = p.slots + static_cast<int64_t>(g) * p.rows * per_row + row * per_row;
-    for (int j = (threadIdx.x >> 5) + 8 * blockIdx.y; j < p.top; j += 8 * gridDim.y) {
-      const int i = __ldcg(p.blocks + unit * p.top + j);
-      int block = -1, tokens = 0;
-      if (i >= 0 && i < v.count) {
-        block = __ldcg(p.block_table + static_cast<int64_t>(v.req) * p.width + i);
-        tokens = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks) ? min(p.page_size, v.n - i * p.page_size) : 0;
-      }
-      for (int t = lane; t < p.page_size; t += 32) slots[static_cast<int64_t>(j) * p.page_size + t] = t < tokens ? block * p.page_size + t : -1;
+    int block = -1, tokens = 0;
+    if (i >= 0 && i < v.count) {
+      block = __ldcg(p.block_table + static_cast<int64_t>(v.req) * p.width + i);
+      tokens = static_cast<unsigned>(block) < static_cast<unsigned>(p.num_blocks) ? min(p.page_size, v.n - i * p.page_size) : 0;
+    }
+    int* slots = p.slots + (static_cast<int64_t>(g) * p.rows + row) * per_row + static_cast<int64_t>(j0) * p.page_size;
+    const int count = min(kSlotBlocks, p.top - j0) * p.page_size;  // at most 2^31 - 1: rows * top * page_size is
+    for (int z0 = 0; z0 < count; z0 += 32) {
+      const int z = min(z0 + lane, count - 1), j = z / p.page_size, t = z - j * p.page_size;
+      const int b = __shfl_sync(0xffffffffu, block, j), n = __shfl_sync(0xffffffffu, tokens, j);
+      if (z0 + lane < count) slots[z] = t < n ? b * p.page_size + t : -1;
     }
   }
 }
 
 cudaError_t launch_block_slots(const BlockParams& p, int sm_count, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.rows) * kKvHeads;
-  const int x = static_cast<int>(units < (1 << 20) ? units : (1 << 20)), most = (8 * sm_count + x - 1) / x;
-  const int y = (p.top + 7) / 8;
-  return launch_chained(gqa_block_slots_kernel, dim3(x, y < most ? y : most), 256, 0, stream, 1, p);
+  const int64_t warps = static_cast<int64_t>(p.rows) * kKvHeads * ((p.top + kSlotBlocks - 1) / kSlotBlocks);
+  const int64_t blocks = (warps + kSlotThreads / 32 - 1) / (kSlotThreads / 32), most = 16 * static_cast<int64_t>(sm_count);
+  return launch_chained(gqa_block_slots_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kSlotThreads, 0, stream, 1, p);
 }
 
 }  // namespace gqa

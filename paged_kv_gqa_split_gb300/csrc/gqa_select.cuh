@@ -156,6 +156,33 @@ __device__ __forceinline__ Key select_kth(SelectSpace<THREADS>& sp, int n, int k
   return prefix;
 }
 
+// The k-th largest of up to 32 * OWN words, by one warp and without a barrier: bit by bit the largest word that k words
+// reach, until exactly k do. For short rows (choosing among 144 blocks for 128 rows: 22.9 us with select_kth, 21.6 with this,
+// where counting by ballots, under a condition each, took 35).
+template <int OWN>
+__device__ __forceinline__ uint32_t warp_kth(const uint32_t* words, int n, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x[OWN];
+#pragma unroll
+  for (int u = 0; u < OWN; ++u) x[u] = 32 * u + lane < n ? words[32 * u + lane] : 0;
+  uint32_t t = 0;
+  bool exact = false;
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit != 0 && !exact; bit >>= 1) {
+    int reach = 0;
+#pragma unroll
+    for (int u = 0; u < OWN; ++u) reach += x[u] >= (t | bit) ? 1 : 0;
+    reach = __reduce_add_sync(0xffffffffu, reach);
+    if (reach >= k) t |= bit;
+    exact = reach == k;
+  }
+  uint32_t least = 0xffffffffu;  // of those that reach it
+#pragma unroll
+  for (int u = 0; u < OWN; ++u)
+    if (x[u] >= t && x[u] < least) least = x[u];
+  return __reduce_min_sync(0xffffffffu, least);
+}
+
 // Walks this block's items 0 .. n in index order: cls(i) is 2 for a chosen item, 1 for one that ties with the last chosen
 // (the first `ties` of the cluster's are chosen too), 0 for others; put(i, x, rank, chosen) is called for every item, rank
 // being the number of chosen items before it in the cluster and x what get(i) returned: those are called AHEAD at a time,
