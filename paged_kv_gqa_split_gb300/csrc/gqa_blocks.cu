@@ -17,10 +17,11 @@ constexpr int kRowValues = kKvHeads * kHeadDim;  // of a token, or of a block's 
 
 // ----------------------------------------------------------------- bounds
 // Teams of 64 lanes, 16 bytes a lane and token. The blocks to renew, request by request, are numbered by prefix sums that
-// every block of threads forms by itself, 256 requests at a time; a team takes every gridDim-th one. Where there are no
-// more of them than blocks of threads (a decode step's), the four teams of a block share one. Bound by the keys' bytes:
-// 131072 tokens in pages of 32 take 31 us (4.4 TB/s), one token each of 64 requests 5 us (two dependent loads and the launch).
-constexpr int kBoundThreads = 256, kBoundTeams = kBoundThreads / 64;
+// every block of threads forms by itself, 256 requests at a time, and taken in turns: by a block of threads, its four teams
+// sharing one, or by a team where they are many and of few tokens (131072 tokens in pages of 16: 31 us by teams, 34 shared;
+// of 32: 29 and 27; of 64: 37 and 31). Bound by the keys' bytes (524288 tokens: 5.6 TB/s) and, below that, by how many
+// loads a block's tokens give a team at once; one new token each of 64 requests takes 5 us, the launch and four dependent loads.
+constexpr int kBoundThreads = 256, kBoundTeams = kBoundThreads / 64, kSharedPage = 32;
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -59,12 +60,12 @@ __global__ void __launch_bounds__(kBoundThreads) gqa_block_bounds_kernel(const B
     const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + lane;
     mm.init();
     int t = t0;
-    for (; t + 7 * step < tokens; t += 8 * step) {
-      uint4 x[8];
+    for (; t + 15 * step < tokens; t += 16 * step) {
+      uint4 x[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = __ldcg(k + (t + u * step) * 64);
+      for (int u = 0; u < 16; ++u) x[u] = __ldcg(k + (t + u * step) * 64);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) mm.add(x[u], x[u]);
+      for (int u = 0; u < 16; ++u) mm.add(x[u], x[u]);
     }
 #pragma unroll 4
     for (; t < tokens; t += step) {
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kBoundThreads) gqa_block_bounds_kernel(const B
     if (tid == 0) start[0] = 0;
     __syncthreads();
     const int64_t total = start[kBoundThreads];
-    const bool shared = total <= gridDim.x;
+    const bool shared = total <= gridDim.x || p.page_size >= kSharedPage;
     const int64_t teams = shared ? gridDim.x : gridDim.x * kBoundTeams;
     for (int64_t x = shared ? blockIdx.x : blockIdx.x + team * gridDim.x; x < total; x += teams) {
       int lo = 0, hi = kBoundThreads;  // the request: start[lo] <= x < start[hi]
