@@ -591,9 +591,11 @@ int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, 
  * arguments out of range, or no supported device) under the present tuning,
  * 256-byte aligned, one per call in flight, not initialised; a smaller one is
  * GQA_ERR_WORKSPACE. Shapes are those of gqa_paged_decode (32 query heads over 4
- * KV heads g of dimension 128). Offsets ([n + 1] int32, non-decreasing) are not
- * checked; entries past the stated count of what they point into are cut to it.
+ * KV heads g of dimension 128). Offsets ([n + 1] int32, non-decreasing; kv_indptr
+ * from 0) are not checked; entries past the stated count of what they point into
+ * are cut to it.
  * A page or block outside the pool is left out, wherever a table lists it.
+ * Counts and widths go up to 2^30.
  * The tuning's CTA counts and tiers apply to the decode inside, not its kernel
  * choice. The caches are bf16, or where cache_format is an argument also FP8
  * (GQA_CACHE_*; as in gqa_paged_decode_fp8). lse is in base 2 as there.
@@ -645,7 +647,8 @@ int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_tab
  *   score = max over the 8 query heads h of g of sum_d max(q[h][d], 0) bounds[block][0][g][d] + min(q[h][d], 0) bounds[block][1][g][d],
  * which no query head's product with a key of the block passes. A score that is
  * no finite fp32 number counts as the largest; equal scores go to the lower
- * block. The scores decide as if formed with 2^-44 of their terms' size.
+ * block. The scores decide as if formed with 2^-44 of their terms' size (terms
+ * below fp32's normal range: with what an fp32 product leaves of them).
  * blocks[row][g][0 .. top) are the chosen blocks' numbers in the table, ascending,
  * then -1. keep_first + keep_last <= top.
  *

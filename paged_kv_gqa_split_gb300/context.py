@@ -106,6 +106,12 @@ def _workspace(index, given, stream, what, *sizes):
     return _alloc(index, (size,), (1,), torch.uint8, stream), size
 
 
+def _fit(*counts):
+    """Raises for counts that a C int would cut."""
+    if max(counts) > _INT_MAX:
+        raise ValueError(f"more than {_INT_MAX} entries")
+
+
 def _pointer(t):
     return None if t is None else t.data_ptr()
 
@@ -126,6 +132,7 @@ def shared_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pr
         _need(index, _I32, 1, prefix_indptr=prefix_indptr, prefix_indices=prefix_indices, group_indptr=group_indptr,
               kv_indptr=kv_indptr, kv_indices=kv_indices)
     groups = group_indptr.shape[0] - 1
+    _fit(n, groups, prefix_indices.shape[0], kv_indices.shape[0], pages)
     if groups < 0 or prefix_indptr.shape[0] != groups + 1 or kv_indptr.shape[0] != n + 1:
         raise ValueError(f"expected prefix_indptr and group_indptr [G + 1] and kv_indptr [{n + 1}]")
     out, lse = _results(index, n, out, lse, True, stream)
@@ -177,6 +184,7 @@ def block_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch
         _need(index, _I32, 1, lens=lens)
     if first is not None and not _plain(index, _I32, 1, first):
         _need(index, _I32, 1, first=first)
+    _fit(requests, width, blocks, page)
     if _bounds(index, bounds) != blocks or lens.shape[0] != requests or (first is not None and first.shape[0] != requests):
         raise ValueError("expected bounds [blocks, 2, 4, 128], and lens and first [requests]")
     _call("gqa_block_bounds", index, stream, k_cache.data_ptr(), bounds.data_ptr(), block_table.data_ptr(),
@@ -196,6 +204,7 @@ def block_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     rows = _queries(index, q)
     held = _bounds(index, bounds)
     requests, width = _table(index, block_table)
+    _fit(rows, requests, width, held)
     if not _plain(index, _I32, 1, token_to_req, lens):
         _need(index, _I32, 1, token_to_req=token_to_req, lens=lens)
     if token_to_req.shape[0] != rows or lens.shape[0] != rows:
@@ -239,6 +248,7 @@ def block_sparse_run(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if not _plain(index, _I32, 3, blocks):
         _need(index, _I32, 3, blocks=blocks)
     listed, heads, top = blocks.shape
+    _fit(rows, requests, width, held, page, top)
     if listed != rows or heads != NUM_KV_HEADS:
         raise ValueError(f"blocks must be [{rows}, 4, top]")
     if token_to_req.shape[0] != rows or lens.shape[0] != rows:
@@ -272,6 +282,7 @@ def run_weighted(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         _need(index, _I32, 1, kv_indptr=kv_indptr, kv_indices=kv_indices)
         _need(index, _F32, 2, weights=weights)
     rows, width = weights.shape
+    _fit(n, width, kv_indices.shape[0], pages)
     if rows != n or kv_indptr.shape[0] != n + 1:
         raise ValueError(f"expected weights [{n}, width] and kv_indptr [{n + 1}]")
     if not math.isfinite(decay):
@@ -307,6 +318,7 @@ def kv_evict(weights: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: torch.T
     (n, width), total = weights.shape, kv_indices.shape[0]
     if kv_indptr.shape[0] != n + 1:
         raise ValueError("expected weights [B, width] and kv_indptr [B + 1]")
+    _fit(n, width, total)
     if not (0 <= keep_first and 0 <= keep_last and 0 <= budget <= _INT_MAX):
         raise ValueError("budget, keep_first or keep_last is out of range")
     if keep_first + keep_last > budget:

@@ -160,7 +160,7 @@ __device__ __forceinline__ RowView row_view(const BlockParams& p, int row) {
   v.req = __ldcg(p.token_to_req + row);
   const bool ok = v.req >= 0 && v.req < p.requests;
   v.n = ok ? static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(__ldcg(p.lens + row)), static_cast<int64_t>(p.width) * p.page_size))) : 0;
-  v.count = (v.n + p.page_size - 1) / p.page_size;
+  v.count = v.n > 0 ? (v.n - 1) / p.page_size + 1 : 0;
   return v;
 }
 

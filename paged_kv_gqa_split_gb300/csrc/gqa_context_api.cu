@@ -19,8 +19,11 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 int launched(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH; }
 bool scale_ok(float s) { return std::isfinite(s) && std::isfinite(s * kLog2e); }
 bool format_ok(int f) { return f == GQA_CACHE_BF16 || f == GQA_CACHE_FP8; }
+// Sizes that kernels walk in steps of up to 8192: no index of theirs passes 31 bits.
+constexpr int kMostItems = 1 << 30;
+bool items_ok(int n) { return n >= 0 && n <= kMostItems; }
 bool table_ok(int page_size, int num_blocks, int width) {
-  return page_size > 0 && num_blocks > 0 && width > 0 && static_cast<int64_t>(num_blocks) * page_size <= INT_MAX &&
+  return page_size > 0 && num_blocks > 0 && width > 0 && width <= kMostItems && static_cast<int64_t>(num_blocks) * page_size <= INT_MAX &&
          static_cast<int64_t>(width) * page_size <= INT_MAX;
 }
 
@@ -115,7 +118,7 @@ int prefix_ctas(int sms, int batch, int groups, int prefix_count, int index_coun
   return 2 * static_cast<int>(std::fmin(std::fmax(n, 1.0), pairs));
 }
 
-bool select_sizes_ok(int rows, int width) { return rows > 0 && width > 0 && static_cast<int64_t>(rows) * width <= (int64_t{1} << 34); }
+bool select_sizes_ok(int rows, int width) { return rows > 0 && width > 0 && width <= kMostItems && static_cast<int64_t>(rows) * width <= (int64_t{1} << 34); }
 bool sparse_sizes_ok(int rows, int top, int page_size) {
   return rows > 0 && top > 0 && page_size > 0 && static_cast<int64_t>(top) * page_size <= INT_MAX &&
          static_cast<int64_t>(rows) * (static_cast<int64_t>(top) * page_size) <= INT_MAX;
@@ -138,7 +141,7 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
                             size_t workspace_bytes, struct CUstream_st* stream) {
   if (batch < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (batch == 0) return GQA_OK;
-  if (batch > (1 << 20) || groups < 0 || groups > (1 << 20) || prefix_count < 0 || index_count < 0 || num_pages < 0 ||
+  if (batch > (1 << 20) || groups < 0 || groups > (1 << 20) || !items_ok(prefix_count) || !items_ok(index_count) || num_pages < 0 ||
       !format_ok(cache_format) || !scale_ok(sm_scale))
     return GQA_ERR_INVALID_ARGUMENT;
   if (q == nullptr || kv_indptr == nullptr || out == nullptr) return GQA_ERR_INVALID_ARGUMENT;
@@ -207,7 +210,7 @@ int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_tab
                      struct CUstream_st* stream) {
   if (requests < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (requests == 0) return GQA_OK;
-  if (!table_ok(page_size, num_blocks, page_table_width)) return GQA_ERR_INVALID_ARGUMENT;
+  if (!items_ok(requests) || !table_ok(page_size, num_blocks, page_table_width)) return GQA_ERR_INVALID_ARGUMENT;
   if (k_cache == nullptr || bounds == nullptr || block_table == nullptr || lens == nullptr) return GQA_ERR_INVALID_ARGUMENT;
   if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(first, 4))
     return GQA_ERR_INVALID_ARGUMENT;
@@ -324,7 +327,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
 
 size_t gqa_paged_decode_weighted_ws_size(int index_count, int cache_format) {
   gqa::DecodeSetup setup;
-  if (index_count < 0 || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
+  if (!items_ok(index_count) || !format_ok(cache_format) || gqa::decode_setup(cache_format == GQA_CACHE_FP8, &setup) != GQA_OK) return 0;
   return DecodeSpace(setup.plan, round256(static_cast<size_t>(index_count) * gqa::kQoHeads * sizeof(float))).end;
 }
 
@@ -335,7 +338,7 @@ int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_
                               struct CUstream_st* stream) {
   if (batch < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (batch == 0) return GQA_OK;
-  if (width < 0 || index_count < 0 || num_pages < 0 || !format_ok(cache_format) || !scale_ok(sm_scale) || !std::isfinite(decay))
+  if (!items_ok(batch) || !items_ok(width) || !items_ok(index_count) || num_pages < 0 || !format_ok(cache_format) || !scale_ok(sm_scale) || !std::isfinite(decay))
     return GQA_ERR_INVALID_ARGUMENT;
   if (q == nullptr || kv_indptr == nullptr || out == nullptr || lse == nullptr) return GQA_ERR_INVALID_ARGUMENT;
   if (width > 0 && (weights == nullptr || weights_out == nullptr)) return GQA_ERR_INVALID_ARGUMENT;
@@ -377,7 +380,7 @@ int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* 
                  int32_t* freed, int batch, int width, int index_count, struct CUstream_st* stream) {
   if (batch < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (batch == 0) return GQA_OK;
-  if (width < 0 || index_count < 0 || budget < 0 || keep_first < 0 || keep_last < 0 || keep_first > budget ||
+  if (!items_ok(batch) || !items_ok(width) || !items_ok(index_count) || budget < 0 || keep_first < 0 || keep_last < 0 || keep_first > budget ||
       keep_last > budget - keep_first)
     return GQA_ERR_INVALID_ARGUMENT;
   if (kv_indptr == nullptr || new_indptr == nullptr || freed_indptr == nullptr) return GQA_ERR_INVALID_ARGUMENT;

@@ -58,16 +58,6 @@ __device__ __forceinline__ void tc_mma_bf16_warp(uint32_t d_tmem, uint64_t a_des
       : "memory");
 }
 
-// With A in tensor memory (row i in lane i, two 16-bit values a column).
-__device__ __forceinline__ void tc_mma_tmem_a_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                   uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // tc_commit from the lane that elect.sync picks (the one that issued tc_mma_bf16_warp).
 __device__ __forceinline__ void tc_commit_warp(uint32_t bar) {
   asm volatile(

@@ -7,7 +7,7 @@ import torch
 
 import oracle.context as cx
 import paged_kv_gqa_split_gb300 as pkg
-from paged_kv_gqa_split_gb300 import _lib
+from paged_kv_gqa_split_gb300 import _lib, context
 from paged_kv_gqa_split_gb300.build import build
 
 A = 1 << 20  # a 256-byte aligned dummy address; no call below reaches the device
@@ -107,6 +107,25 @@ def test_evict_refusals(lib):
         dict(first=5, last=5), dict(first=BIG, last=BIG, budget=BIG), dict(w=None), dict(ki=None), dict(kx=None), dict(wo=None),
         dict(ni=None), dict(nx=None), dict(fi=None), dict(fx=None), dict(wo=A), dict(nx=A + 8192), dict(fx=A + 8192),
         dict(fx=A + 12), dict(ni=A + 4096), dict(fi=A + 4096), dict(fi=A + 8), dict(w=A + 2), dict(kx=A + 8193), dict(ni=A + 9)])
+
+
+def test_counts_past_what_the_kernels_walk_are_refused(lib):
+    most = 1 << 30
+    ok = dict(q=A, k=A, v=A, pi=A, px=A, gi=A, ki=A, kx=A, scale=0.1, out=A, lse=A, batch=3, groups=2, pn=9, n=5, pages=20,
+              fmt=0, ws=A, size=0, stream=None)
+    refused(lib.gqa_shared_paged_decode, ok, [dict(pn=most + 1), dict(n=most + 1), dict(n=BIG)])
+    ok = dict(k=A, bounds=A, table=A, lens=A, first=A, requests=3, page=1, blocks=9, width=4, stream=None)
+    refused(lib.gqa_block_bounds, ok, [dict(requests=most + 1), dict(width=most + 1), dict(width=BIG)])
+    ok = dict(q=A, k=A, v=A, ki=A, kx=A, scale=0.1, w=A, decay=1.0, wo=A, out=A, lse=A, batch=3, width=7, n=5, pages=20, fmt=1,
+              ws=A, size=0, stream=None)
+    refused(lib.gqa_paged_decode_weighted, ok, [dict(width=BIG), dict(width=most + 1), dict(n=most + 1), dict(batch=most + 1)])
+    assert lib.gqa_paged_decode_weighted_ws_size(most + 1, 0) == 0 and lib.gqa_block_select_ws_size(1, most + 1) == 0
+    ok = dict(w=A, ki=A + 4096, kx=A + 8192, budget=9, first=2, last=3, wo=A + 4, ni=A + 8, nx=A + 12, fi=A + 16, fx=A + 20,
+              batch=3, width=7, n=5, stream=None)
+    refused(lib.gqa_kv_evict, ok, [dict(width=BIG), dict(n=most + 1), dict(batch=most + 1)])
+    context._fit(BIG, 0)
+    with pytest.raises(ValueError, match="entries"):
+        context._fit(3, BIG + 1)
 
 
 def test_cpu_tensors_raise(lib):

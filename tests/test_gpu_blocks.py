@@ -272,3 +272,15 @@ def test_bounds_of_many_requests():
     for first in (None, i32([max(0, n - 1) for n in lens])):
         want = cx.bounds_oracle(w["k"], w["bounds"], w["table"], w["lens"], first)
         assert same_values(pkg.block_bounds(w["k"], w["bounds"], w["table"], w["lens"], first), want)
+
+
+@pytest.mark.parametrize("page", [2 ** 31 - 1, 2 ** 30 + 1])
+def test_choice_of_the_longest_pages(page):
+    """One block as long as a table's product with its width may be: lengths and block counts stay within 31 bits."""
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(4, 32, 128, generator=g).to(BF).cuda()
+    bounds = torch.randn(1, 2, 4, 128, generator=g).to(BF).cuda()
+    table, req = i32([[0]]), i32([0, 0, 0, 0])
+    lens = i32([2 ** 31 - 1, 2 ** 30 + 1, 1, 0])
+    got = pkg.block_select(q, bounds, table, req, lens, 3, page)
+    assert got[:3].cpu().tolist() == [[[0, -1, -1]] * 4] * 3 and (got[3] == -1).all()
