@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
 
   // Everything below reads what the decode grid wrote.
   pdl_wait();
+  if (p.index_cap >= 0) pdl_launch_dependents();  // what the decode stored besides, the kernel behind may read from here on
   // The sequence holding decode CTA j's last unit, as that CTA recorded it
   // (read before checking that CTA j had work, to save a round trip).
   const int4 rec = boundary ? __ldcg(p.split_rec + j) : make_int4(0, 0, 0, 0);

@@ -13,34 +13,47 @@ constexpr int kWeighThreads = 256;
 
 __global__ void __launch_bounds__(kWeighThreads) gqa_weigh_kernel(const WeighParams p) {
   __shared__ float lse[kQoHeads];
-  pdl_wait();
-  pdl_launch_dependents();
+  bool waited = false;
   for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    __syncthreads();
-    if (threadIdx.x < kQoHeads) lse[threadIdx.x] = __ldcg(p.lse + static_cast<int64_t>(b) * kQoHeads + threadIdx.x);
-    __syncthreads();
+    // ahead of the wait: the call's inputs, and the scores, which the merge let this kernel start behind
     const int total = max(0, min(__ldcg(p.kv_indptr + p.batch), p.index_count));
     const int lo = max(0, min(__ldcg(p.kv_indptr + b), total)), n = min(__ldcg(p.kv_indptr + b + 1), total) - lo;
     const int j = blockIdx.x * kWeighThreads + threadIdx.x;
-    if (j >= p.width || (j >= n && p.weights == p.out)) continue;
     const int64_t at = static_cast<int64_t>(b) * p.width + j;
-    if (j >= n) {
-      p.out[at] = p.weights[at];
-      continue;
-    }
-    float sum = 0.f;
+    const bool in = j < p.width, add = in && j < n;
+    float4 s[2 * kKvHeads];
+    if (add) {
 #pragma unroll
-    for (int g = 0; g < kKvHeads; ++g) {
-      const float4* s = reinterpret_cast<const float4*>(p.scores + (static_cast<int64_t>(g) * p.index_count + lo + j) * kGroup);
-      const float4 x = __ldcg(s), y = __ldcg(s + 1);
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int h = 0; h < kGroup; ++h) {
-        const float l = lse[g * kGroup + h];
-        sum += l == -INFINITY ? 0.f : ex2(v[h] - l);
+      for (int g = 0; g < kKvHeads; ++g) {
+        const float4* from = reinterpret_cast<const float4*>(p.scores + (static_cast<int64_t>(g) * p.index_count + lo + j) * kGroup);
+        s[2 * g] = __ldcg(from);
+        s[2 * g + 1] = __ldcg(from + 1);
       }
     }
-    p.out[at] = p.decay == 0.f ? sum : p.decay * p.weights[at] + sum;
+    const float old = in && !(add && p.decay == 0.f) ? __ldcg(p.weights + at) : 0.f;
+    if (!waited) {
+      pdl_wait();
+      pdl_launch_dependents();
+      waited = true;
+    }
+    __syncthreads();
+    if (threadIdx.x < kQoHeads) lse[threadIdx.x] = __ldcg(p.lse + static_cast<int64_t>(b) * kQoHeads + threadIdx.x);
+    __syncthreads();
+    if (add) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * kKvHeads; ++k) {
+        const float v[4] = {s[k].x, s[k].y, s[k].z, s[k].w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float l = lse[4 * k + h];
+          sum += l == -INFINITY ? 0.f : ex2(v[h] - l);
+        }
+      }
+      p.out[at] = p.decay == 0.f ? sum : p.decay * old + sum;
+    } else if (in && p.weights != p.out) {
+      p.out[at] = old;
+    }
   }
 }
 
