@@ -397,7 +397,7 @@ int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* 
   if (rc != GQA_OK) return rc;
   const gqa::EvictParams p{weights, kv_indptr, kv_indices, weights_out, new_indptr, new_indices, freed_indptr, freed,
                            budget, keep_first, keep_last, batch, width, index_count, 1, 0};
-  return launched(gqa::launch_evict(p, stream));
+  return launched(gqa::launch_evict(p, sms, stream));
 }
 
 }  // extern "C"

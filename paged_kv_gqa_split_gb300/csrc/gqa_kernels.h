@@ -409,7 +409,7 @@ struct EvictParams {  // gqa_weights.cu
   int budget, keep_first, keep_last, batch, width, index_count;
   int cluster, held;  // blocks a sequence, words that one holds in shared memory (set by the launch)
 };
-cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream);
 
 // Launches a kernel that begins with pdl_wait() so that it may start while the one before it on the stream ends, over
 // clusters of `cluster` blocks.
@@ -454,15 +454,18 @@ int current_device_sms(int* sm_count, unsigned long long* wait_limit_ns = nullpt
 // idempotent and the flags are atomic. Devices past the table set it on
 // every call.
 constexpr int kMaxDevices = 64;
-inline cudaError_t set_smem_limit_once(std::atomic<int> (&done)[kMaxDevices], const void* fn, int bytes) {
+inline cudaError_t set_attribute_once(std::atomic<int> (&done)[kMaxDevices], const void* fn, cudaFuncAttribute what, int value) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool tracked = dev >= 0 && dev < kMaxDevices;
   if (tracked && done[dev].load(std::memory_order_acquire) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(fn, what, value);
   if (e == cudaSuccess && tracked) done[dev].store(1, std::memory_order_release);
   return e;
+}
+inline cudaError_t set_smem_limit_once(std::atomic<int> (&done)[kMaxDevices], const void* fn, int bytes) {
+  return set_attribute_once(done, fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace gqa

@@ -34,7 +34,7 @@ __device__ __forceinline__ int2 block_sum2(int2* sums, int2 x) {
   return make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
 }
 
-constexpr int kMostBlocks = 8;  // of a cluster
+constexpr int kMostBlocks = 16;  // of a cluster
 
 template <int THREADS>
 struct SelectSpace {

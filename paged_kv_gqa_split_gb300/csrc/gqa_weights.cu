@@ -1,6 +1,8 @@
 // Attention weights accumulated beside the decode, and the eviction by them.
 //   weights[b][j] = decay * weights[b][j] + sum over the 32 query heads of 2^(s[j] - lse)
-// from the scores that the decode stored (kFormScores) and the LSE that it returned.
+// from the scores that the decode stored (kFormScores) and the LSE that it returned. Bound by the launch and the round trips
+// of loads; the scores (128 bytes a token) come from L2 and are read while the merge runs (6019 tokens of 16 sequences, the
+// whole call: 20.8 us; behind the merge: 22.8).
 #include <cuda_runtime.h>
 
 #include "gqa_common.cuh"
@@ -69,8 +71,8 @@ cudaError_t launch_weigh(const WeighParams& p, cudaStream_t stream) {
 // begins where the sequences before it end, which every block sums up by itself. The weights are read once into shared
 // memory as ordered words (from global memory each time where a run does not fit).
 constexpr int kEvictHeld = 48 * 1024;   // words of shared memory at most
-constexpr int kEvictRun = 8 * 1024;     // tokens a block, before a cluster of twice as many is taken
-constexpr int kEvictBlocks = 8;         // blocks of a cluster at most (the portable size)
+constexpr int kEvictRun = 4 * 1024;     // tokens a block of a cluster at least
+static_assert(kMostBlocks == 16, "evict_us goes up to 16 blocks a cluster");
 constexpr uint32_t kStays = 1, kGoes = 0;  // marks below any key
 
 template <bool CLUSTERED, int THREADS>
@@ -166,14 +168,33 @@ static cudaError_t launch_evict_form(const EvictParams& p, cudaStream_t stream) 
   static std::atomic<int> configured[kMaxDevices];
   const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), kEvictHeld * 4);
   if (e != cudaSuccess) return e;
+  if (p.cluster > 8) {
+    static std::atomic<int> allowed[kMaxDevices];
+    const cudaError_t a = set_attribute_once(allowed, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (a != cudaSuccess) return a;
+  }
   const int64_t units = p.batch < (1 << 16) ? p.batch : (1 << 16);
   return launch_chained(gqa_evict_kernel<CLUSTERED, THREADS>, dim3(static_cast<unsigned>(units * p.cluster)), THREADS, p.held * 4, stream, p.cluster, p);
 }
 
-cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
+// What an eviction takes with clusters of `blocks`, in us: a line in the tokens a block for each kernel, twice where they are
+// not held, times the rounds (a cluster stays within a part of the GPU, so that of larger ones fewer fit at once). Measured,
+// for 1, 2, 4, 8, 16 blocks: 1 sequence of 16384 tokens 27, 19, 16, 16, 16; 48 of 16384 29, 21, 33, 33, 33; 128 of 16384 31, 40,
+// 64, 64, 64; 2 of 131072 -, -, -, 30, 24; 8 of 131072 -, 126, 49, 32, 48; 64 of 131072 412, 137, 100, 151, 235.
+static double evict_us(int batch, int width, int blocks, int sms) {
+  const int run = (width - 1) / blocks + 1;
+  const int at_once = blocks == 1 ? 2 * sms : (blocks <= 4 ? sms : (blocks == 8 ? sms * 2 / 3 : sms * 5 / 9)) / blocks;
+  if (at_once == 0) return 1e30;
+  const int rounds = (batch - 1) / at_once + 1;
+  return rounds * (blocks == 1 ? 5.0 + run * (1.4 / 1024) : 11.5 + run * (1.05 / 1024)) * (run > kEvictHeld ? 2 : 1);
+}
+
+cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream) {
+  const int width = p.width > 0 ? p.width : 1;
   p.cluster = 1;
-  while (p.cluster < kEvictBlocks && p.width > p.cluster * kEvictRun) p.cluster *= 2;
-  const int run = (p.width + p.cluster - 1) / p.cluster;
+  for (int blocks = 2; blocks <= kMostBlocks && width >= blocks * kEvictRun; blocks *= 2)
+    if (evict_us(p.batch, width, blocks, sm_count) < evict_us(p.batch, width, p.cluster, sm_count)) p.cluster = blocks;
+  const int run = (width - 1) / p.cluster + 1;
   p.held = run < kEvictHeld ? run : kEvictHeld;
   return p.cluster > 1 ? launch_evict_form<true, 1024>(p, stream) : launch_evict_form<false, 512>(p, stream);
 }

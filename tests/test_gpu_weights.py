@@ -173,3 +173,10 @@ def test_offsets_past_the_indices_are_cut():
 def test_evict_more_than_the_blocks_hold(n):
     w, indptr, ids = listed([n, 3], n, 3, "few")
     evict_check((w, indptr, ids, n // 3, 10, 1000), pkg.kv_evict(w, indptr, ids, n // 3, 10, 1000))
+
+
+@pytest.mark.parametrize("lens,budget", [([70000, 1, 0, 4096, 65536], 5000), ([33000], 33000 - 1), ([20000, 16384], 1), ([300] * 200 + [9000], 256)])
+def test_evict_by_clusters_of_each_size(lens, budget):
+    first, last = min(2, budget), min(40, budget - min(2, budget))
+    w, indptr, ids = listed(lens, max(lens), 5, "few")
+    evict_check((w, indptr, ids, budget, first, last), pkg.kv_evict(w, indptr, ids, budget, first, last))
