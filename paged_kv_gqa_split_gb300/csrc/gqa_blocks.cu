@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
 // Small blocks of threads for short rows: their barriers are cheap and all fit the GPU at once.
 constexpr int kHeldWords = 48 * 1024, kListed = 128;
 constexpr uint32_t kAbsent = 0, kChosen = 1;  // marks below any score's word
+constexpr uint32_t kUnknown = 0xffffffffu;    // of a score that is no finite number: it is formed again in any case
 
 // s + e += x, exactly but for e's own rounding.
 __device__ __forceinline__ void add_exact(float& s, float& e, float x) {
@@ -265,19 +266,26 @@ __device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_b
     a4[i] = __ldcg(up + i);
     b4[i] = __ldcg(down + i);
   }
-  float s = 0.f, e = 0.f;
+  float sum[4], rest_of[4], other = 0.f;  // four sums at once: each term waits for the one before
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    sum[i] = rest_of[i] = 0.f;
     const uint32_t xs[4] = {x4[i].x, x4[i].y, x4[i].z, x4[i].w}, as[4] = {a4[i].x, a4[i].y, a4[i].z, a4[i].w}, bs[4] = {b4[i].x, b4[i].y, b4[i].z, b4[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float x0 = bf16_lo(xs[k]), x1 = bf16_hi(xs[k]);
-      // of the two products one is 0 for any finite bounds; both count, so that 0 times an infinity shows
-      add_exact(s, e, __fmul_rn(x0 > 0.f ? x0 : x0 * 0.f, bf16_lo(as[k])));
-      add_exact(s, e, __fmul_rn(x0 < 0.f ? x0 : x0 * 0.f, bf16_lo(bs[k])));
-      add_exact(s, e, __fmul_rn(x1 > 0.f ? x1 : x1 * 0.f, bf16_hi(as[k])));
-      add_exact(s, e, __fmul_rn(x1 < 0.f ? x1 : x1 * 0.f, bf16_hi(bs[k])));
+      const bool up0 = x0 > 0.f, up1 = x1 > 0.f;
+      add_exact(sum[i], rest_of[i], __fmul_rn(x0, up0 ? bf16_lo(as[k]) : bf16_lo(bs[k])));
+      add_exact(sum[i], rest_of[i], __fmul_rn(x1, up1 ? bf16_hi(as[k]) : bf16_hi(bs[k])));
+      other = fmaf(up0 ? bf16_lo(bs[k]) : bf16_lo(as[k]), 0.f, other);  // the products of 0: nothing, or NaN
+      other = fmaf(up1 ? bf16_hi(bs[k]) : bf16_hi(as[k]), 0.f, other);
     }
+  }
+  float s = sum[0] + other, e = rest_of[0];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    add_exact(s, e, sum[i]);
+    e = __fadd_rn(e, rest_of[i]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
@@ -305,6 +313,7 @@ __global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockPa
   extern __shared__ uint32_t held[];
   __shared__ SelectSpace<THREADS> sp;
   __shared__ float widest[THREADS / 32];
+  __shared__ int unknown_s[THREADS / 32];
   __shared__ int list[kListed], listed;
   __shared__ uint64_t listed_key[kListed];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -320,6 +329,7 @@ __global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockPa
     uint32_t* words = p.width <= kHeldWords ? held : reinterpret_cast<uint32_t*>(p.scores + unit * p.width);
     // candidates and those of them that are kept in any case; the widest error
     int2 mine = make_int2(0, 0);
+    int unknown = 0;
     float wide = 0.f;
     const int tiles = (p.width + kScoreBlocks - 1) / kScoreBlocks;
     for (int i = tid; i < (v.count + kScoreBlocks - 1) / kScoreBlocks; i += THREADS) wide = fmaxf(wide, __ldcg(p.errors + unit * tiles + i));
@@ -329,43 +339,44 @@ __global__ void __launch_bounds__(THREADS) gqa_block_choose_kernel(const BlockPa
       uint32_t x = kAbsent;
       if (__float_as_uint(s) != kNoBlock) {
         const bool fixed = i < p.keep_first || i >= v.count - p.keep_last;
-        x = fixed ? kChosen : ordered_bits(s);
+        const bool number = fabsf(s) < INFINITY;
+        x = fixed ? kChosen : (number ? ordered_bits(s) : kUnknown);
         ++mine.x;
         mine.y += fixed;
+        unknown += !fixed && !number;
       }
       words[i] = x;
     }
     if (tid == 0) listed = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
-    if (lane == 0) widest[warp] = wide;
+    unknown = __reduce_add_sync(0xffffffffu, unknown);
+    if (lane == 0) widest[warp] = wide, unknown_s[warp] = unknown;
     mine = block_sum2<THREADS>(sp.sums, mine);  // (its barriers: the words and the widest errors are there too)
     wide = widest[lane & (THREADS / 32 - 1)];  // (a power of two of warps)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
+    unknown = __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? unknown_s[lane] : 0);
     const int take = min(p.top, mine.x) - mine.y;  // of the others; mine.y <= top
+    const int others = mine.x - mine.y;
     const bool all = mine.x <= p.top;
-    // words above `above` are chosen, below `below` not; those between, and what is no finite number, are to be decided
+    // words above `above` are chosen, below `below` not; those between, and the unknown, are to be decided
     uint32_t above = all ? kAbsent : 0xffffffffu, below = all ? kAbsent : 0xffffffffu;
     bool settled = all, again = false;
     uint64_t least = 0;
     int ties = 0;
-    auto open = [&](uint32_t x) { return x > kChosen && (x >= kKeyInf || x == kKeyLeast || (x >= below && x <= above)); };
+    auto open = [&](uint32_t x) { return x > kChosen && (x == kUnknown || (x >= below && x <= above)); };
     if (!all && take > 0) {
-      uint32_t kth;
-      if (THREADS == 128 && v.count <= 256) {
-        kth = warp_kth<8>(words, v.count, take);
-      } else {
+      auto rank = [&](int k) {  // the k-th largest word
+        if (THREADS == 128 && v.count <= 256) return warp_kth<8>(words, v.count, k);
         int unused = 0;
-        kth = select_kth<THREADS, false, uint32_t>(sp, v.count, take, [&](int i) { return words[i]; }, unused);
-      }
-      const float mark = ordered_float(kth);
-      if (fabsf(mark) < INFINITY) {
-        above = ordered_bits(__fadd_ru(mark, __fmul_ru(2.f, wide)));
-        below = ordered_bits(__fadd_rd(mark, __fmul_rd(-2.f, wide)));
-      } else {
-        below = kKeyLeast;  // decide all of them again
-      }
+        return select_kth<THREADS, false, uint32_t>(sp, v.count, k, [&](int i) { return words[i]; }, unused);
+      };
+      // the unknown may come out above all others or below them: chosen for sure is what passes the (take - unknown)-th of
+      // the others (the take-th with the unknown on top), and what their take-th passes is not
+      const uint32_t kth = rank(take), kth_low = unknown == 0 ? kth : (take + unknown <= others ? rank(take + unknown) : kAbsent);
+      if (kth != kUnknown) above = ordered_bits(__fadd_ru(ordered_float(kth), __fmul_ru(2.f, wide)));
+      below = kth_low == kAbsent ? kKeyLeast : ordered_bits(__fadd_rd(ordered_float(kth_low), __fmul_rd(-2.f, wide)));
       mine = make_int2(0, 0);  // chosen by their words, to be decided
       for (int i = tid; i < v.count; i += THREADS) {
         const uint32_t x = words[i];

@@ -284,3 +284,19 @@ def test_choice_of_the_longest_pages(page):
     lens = i32([2 ** 31 - 1, 2 ** 30 + 1, 1, 0])
     got = pkg.block_select(q, bounds, table, req, lens, 3, page)
     assert got[:3].cpu().tolist() == [[[0, -1, -1]] * 4] * 3 and (got[3] == -1).all()
+
+
+@pytest.mark.parametrize("top,first,last", [(4, 0, 0), (9, 1, 1), (40, 2, 3)])
+@pytest.mark.parametrize("bad", [1, 5, 60])
+def test_choice_where_errors_have_no_bound(top, first, last, bad):
+    """Bounds so large where the queries are 0 that the scores' error has no finite bound: the scores themselves are the
+    lowest, and whole numbers of blocks before them are to be chosen."""
+    w = make([600, 8000], 8, 6)
+    pkg.block_bounds(w["k"], w["bounds"], w["table"], w["lens"])
+    w["q"].mul_(10000.0)
+    w["q"][:, :, 5] = 0
+    for r in range(2):
+        blocks = w["table"][r, 7:7 + bad].long()
+        w["bounds"][blocks] = -20.0
+        w["bounds"][blocks, :, :, 5] = 3e38
+    assert np.array_equal(select(w, top, first, last).cpu().numpy(), chosen(w, top, first, last))
