@@ -598,7 +598,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
             float x[16];
             load16(k_scales + 4 * c, x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[c + e] = __float_as_uint(__uint_as_float(s[c + e]) * x[e]);
+            for (int e = 0; e < 16; e += 2) {
+              float lo, hi;
+              unpack2(mul2(pack2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), pack2(x[e], x[e + 1])), lo, hi);
+              s[c + e] = __float_as_uint(lo);
+              s[c + e + 1] = __float_as_uint(hi);
+            }
           }
         }
         if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
