@@ -46,8 +46,14 @@ __device__ __forceinline__ int prefix_range(const SharedParams& p, int g, int& f
 // Why pairs: a CTA alone reads 64 KB a step of 256 rows, and its copies took 2500 of the step's 4050 clocks. In a pair
 // each CTA copies and keeps half (K of 64 of the tokens, V of 64 of the 128 dims).
 //
+// What bounds it: a step of both tiles takes 3330 clocks, 2048 of them MMAs; a tile's chain is its softmax (1880 clocks from
+// scores to the second half of P), its MMAs (1024 at least) and the barriers between them. 16384 tokens for 128 sequences on 43
+// pairs: 54 us, 53 % of the tensor pipe's cycles (the own tokens' decode has the other SMs). With an FP8 cache a step takes 4800
+// clocks: twice the operations a score, and warps that convert beside them. Two threads a row (64 tokens each, 768 threads) took
+// 1270 clocks for the softmax, but 79 us for the whole call instead of 68 (FP8 103, not 81): more warps for the same issue slots.
+//
 // Pages are single tokens in any order, so their rows are gathered by 16-byte cp.async, written where the 128-byte swizzle
-// wants them; four warps keep four steps (32 KB a CTA) in flight. The odd CTA's copies are counted there, and its MMA warp
+// wants them; four warps keep up to four steps (32 KB each, a CTA) in flight. The odd CTA's copies are counted there, and its MMA warp
 // tells the even CTA, which issues for both. An FP8 cache's codes go through a ring of their own and become fp16 (exact) on
 // the way to three such stages; a token's K scale is taken on its score, its V scale on its probability (over a running power of
 // two), Q is fp16 times a power of two a row, as in the decode.
@@ -93,9 +99,10 @@ struct PrefixCfg {
   static constexpr int kWalkOff = kRowOff + (F8 ? 256 * 4 : 0);
   static constexpr int kBarOff = kWalkOff + kPreThreads / 32 * static_cast<int>(sizeof(Walk));
   // Barriers. Both CTAs': stages full (the even one's counts the odd one's too) and free, S and O there (MMA commits), all
-  // done. The even CTA's: queries written, the halves of P written (4 warps of each CTA), whose turn it is to issue.
+  // done; for an FP8 cache, the factors of a tile's rows written. The even CTA's: queries written, the halves of P written
+  // (4 warps of each CTA), whose turn it is to issue.
   static constexpr int kFull = 0, kFree = kStages, kQ = 2 * kStages, kS = kQ + 2, kO = kS + 2, kP = kO + 2, kTurn = kP + 4,
-                       kDone = kTurn + 2, kBars = kDone + 1;
+                       kRows = kTurn + 2, kDone = kRows + 2, kBars = kDone + 1;
   static constexpr int kWordOff = kBarOff + kBars * 8;
   static constexpr int kBytes = kWordOff + 16 + 1024;  // the base is rounded up to 1024 bytes (swizzle atoms)
   static_assert(kBytes <= 226 * 1024 && sizeof(Walk) % 8 == 0, "prefix pass exceeds shared memory");
@@ -205,6 +212,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       if (i < C::kFree) count = (F8 ? kCopyWarps : kCopyWarps * 32 + kCopyWarps) + (half == 0 ? 1 : 0);
       else if (i < C::kQ || i == C::kDone) count = 2;  // a commit of each MMA warp
       else if (i < C::kS || (i >= C::kP && i < C::kTurn)) count = 8;
+      else if (i >= C::kRows && i < C::kDone) count = 4;
       mbar_init(bar(i), count);
     }
     *abort_s = 0;
@@ -572,7 +580,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
       if (lane == 0) mbar_arrive_cluster(q_bar);
       float sc = fabsf(p.scale_log2);
       if constexpr (F8) {
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + a) : "memory");
+        if (lane == 0) mbar_arrive(bar(C::kRows + a));
+        good = wait(C::kRows + a, units & 1, kErrTimeoutFull);
+        if (!good) break;
         sc *= reinterpret_cast<volatile float*>(sm + C::kRowOff)[128 * a + t];
       }
       sc = fmaxf(sc, 1e-37f);  // > 0: -inf * sc stays -inf
