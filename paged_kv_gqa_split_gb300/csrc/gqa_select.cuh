@@ -48,7 +48,7 @@ struct SelectSpace {
 // The k-th largest (k >= 1) of this cluster's keys, of which this block has keys[0 .. n), and in `ties` at least how many
 // of the keys equal to it are among the k largest. Every block of the cluster calls it (CLUSTERED), or a block alone.
 // A pass counts the keys of a prefix by their next 8 bits; every warp finds the digit by itself, so that a pass needs one
-// barrier. As soon as all keys of the digit are among the k largest, the smallest of them is the k-th.
+// barrier (a cluster one of its own more). As soon as all keys of the digit are among the k largest, the smallest of them is the k-th.
 template <int THREADS, bool CLUSTERED, typename Key, typename Get>
 __device__ __forceinline__ Key select_kth(SelectSpace<THREADS>& sp, int n, int k, Get key, int& ties) {
   constexpr int kBits = 8 * sizeof(Key);
