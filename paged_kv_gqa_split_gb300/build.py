@@ -2,7 +2,8 @@
 
 ``python -m paged_kv_gqa_split_gb300.build`` (or ``build()``) compiles the CUDA
 translation units in parallel and links ``libgqa_paged_decode.so`` next to this
-file. Objects go to ``_build/`` inside the package; both are git-ignored.
+file. Objects go to ``_build/`` inside the package; both are git-ignored. Beside it the host compiler makes
+``_context_host.so``, a Python module against the installed PyTorch's headers that ``context`` uses where it is there.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from typing import List
 
@@ -24,6 +26,7 @@ SOURCES = ["gqa_decode_lsu.cu", "gqa_decode_tma.cu", "gqa_merge.cu", "gqa_api.cu
            "gqa_sparse.cu", "gqa_mla.cu", "gqa_mla_tc.cu", "gqa_rope.cu", "gqa_rope_append.cu", "gqa_mla_proj.cu",
            "gqa_mla_prefill.cu", "gqa_serving_api.cu", "gqa_shared.cu", "gqa_blocks.cu", "gqa_weights.cu",
            "gqa_context_api.cu"]
+HOST_PATH = os.path.join(PKG, "_context_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -50,6 +53,21 @@ def _run(cmd: List[str], verbose: bool) -> str:
     return res.stdout
 
 
+def _build_host(verbose: bool) -> None:
+    """The Python module; without it (no headers, another compiler) `context` does its work in Python."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    tmp = HOST_PATH + ".tmp"
+    try:
+        _run(["g++", "-O2", "-fPIC", "-std=c++17", "-shared", "-I", os.path.join(at, "include"), "-I",
+              os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+              os.path.join(CSRC, "context_host.cpp"), "-o", tmp, "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu",
+              "-lc10"], verbose)
+        os.replace(tmp, HOST_PATH)
+    except (OSError, RuntimeError) as e:
+        print(f"{os.path.basename(HOST_PATH)} was not built: {e}", file=sys.stderr)
+
+
 def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
@@ -74,8 +92,10 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
             print(out)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = ex.submit(_build_host, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        host.result()
     tmp = LIB_PATH + ".tmp"
     _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB_PATH)
