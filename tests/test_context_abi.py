@@ -142,6 +142,16 @@ def test_cpu_tensors_raise(lib):
             call()
 
 
+def test_the_look_at_tensors_in_one_step(lib):
+    host = pytest.importorskip("paged_kv_gqa_split_gb300._context_host")
+    assert host.gather(b"f1", torch.zeros(3)) is None and host.gather(b"x1", torch.zeros(3)) is None
+    assert host.gather(b"f1", [0.0]) is None
+    for bad in ((), (b"f1",), (b"f", torch.zeros(3)), (b"f1f1", torch.zeros(3)), ("f1", torch.zeros(3)), (b"f1" * 17, *[torch.zeros(1)] * 17)):
+        with pytest.raises(TypeError):
+            host.gather(*bad)
+    assert host.torch_version == torch.__version__.split("+")[0]
+
+
 def test_names_are_exported():
     for name in ("shared_run", "block_bounds", "block_select", "block_sparse_run", "run_weighted", "kv_evict"):
         assert name in pkg.__all__ and callable(getattr(pkg, name))

@@ -169,3 +169,35 @@ def test_empty_batches():
     assert CALLS["weighted"](none)[2].shape == (0, 8)
     got = CALLS["evict"](none)
     assert torch.equal(got[2], torch.full((5,), -1, dtype=I32, device="cuda")) and torch.equal(got[4], got[2])
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_without_the_look_in_one_step(name, monkeypatch):
+    """The same results and refusals where the C++ step is not there."""
+    from paged_kv_gqa_split_gb300 import context
+
+    g, a = torch.Generator().manual_seed(9), tensors()
+    for key in ("q", "k", "v", "kb", "vb", "b", "w"):
+        a[key].copy_(torch.randn(a[key].shape, generator=g).to(a[key].dtype))
+    for key, values in dict(pi=[0, 4], px=[1, 2, 3, 4], gi=[0, 2], ki=[0, 2, 5], kx=[5, 6, 7, 8, 0], l=[5, 12]).items():
+        a[key].copy_(torch.tensor(values, dtype=I32))
+    a["t"].copy_(torch.tensor([[0, 1, 2], [2, 1, 0]], dtype=I32))
+    fast = CALLS[name](a)
+    fast = [x.clone() for x in (fast if isinstance(fast, tuple) else (fast,))]
+    monkeypatch.setattr(context, "_gather", context._no_gather)
+    slow = CALLS[name](a)
+    for x, y in zip(fast, slow if isinstance(slow, tuple) else (slow,)):
+        assert torch.equal(x, y)
+    for key in USES[name].split():
+        for bad in (a[key].cpu(), a[key][None]):
+            with pytest.raises(ValueError):
+                CALLS[name](dict(a, **{key: bad}))
+
+
+def test_fp8_rows_of_more_dimensions():
+    """FP8 caches [P, 1, 528] as the plain decode takes them."""
+    a, f = tensors(), torch.zeros(9, 1, 528, dtype=torch.uint8, device="cuda")
+    flat = dict(a, k=f.view(9, 528), v=f.view(9, 528))
+    for name in ("shared", "weighted"):
+        for x, y in zip(CALLS[name](dict(a, k=f, v=f)), CALLS[name](flat)):
+            assert torch.equal(x, y)
