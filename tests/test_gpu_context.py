@@ -179,7 +179,7 @@ def test_without_the_look_in_one_step(name, monkeypatch):
     g, a = torch.Generator().manual_seed(9), tensors()
     for key in ("q", "k", "v", "kb", "vb", "b", "w"):
         a[key].copy_(torch.randn(a[key].shape, generator=g).to(a[key].dtype))
-    for key, values in dict(pi=[0, 4], px=[1, 2, 3, 4], gi=[0, 2], ki=[0, 2, 5], kx=[5, 6, 7, 8, 0], l=[5, 12]).items():
+    for key, values in dict(pi=[0, 4], px=[1, 2, 3, 4], gi=[0, 2], ki=[0, 2, 5], kx=[5, 6, 7, 8, 0], l=[4, 12]).items():
         a[key].copy_(torch.tensor(values, dtype=I32))
     a["t"].copy_(torch.tensor([[0, 1, 2], [2, 1, 0]], dtype=I32))
     fast = CALLS[name](a)
