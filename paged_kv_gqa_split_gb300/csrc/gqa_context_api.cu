@@ -39,6 +39,16 @@ struct DecodeSpace {
   }
 };
 
+// The plan for `tokens` at most. The second tier evens out long ranges; where a CTA of the first has few tokens, its ranges of 64
+// tokens begin when the first's, as short, are done. Two tiers and one, us a call, by tokens a CTA: blocks of bf16 caches 9: 15.5
+// and 16.7, 21: 17.6 both, 36: 28 and 20, 72: 34 and 25, 287: 61 and 55, 449: 84 and 82, 575: 101 and 105; accumulated weights, FP8
+// caches 35: 24 and 19, 283: 52 and 47, 555: 84 and 77, 1169: 157 and 153, 2278: 289 and 307.
+gqa::PlanConfig plan_for(const gqa::DecodeSetup& setup, int64_t tokens, bool fp8) {
+  gqa::PlanConfig plan = setup.plan;
+  if (setup.default_tiers && tokens >= int64_t{20} * plan.tier1_ctas && tokens < int64_t{fp8 ? 1536 : 512} * plan.tier1_ctas) plan.tier2_ctas = 0;
+  return plan;
+}
+
 gqa::DecodeParams decode_params(const gqa::DecodeSetup& setup, void* part_o, void* part_lse, void* split_rec, float sm_scale) {
   gqa::DecodeParams d{};
   d.part_o = static_cast<float*>(part_o);
@@ -193,7 +203,8 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   p.part_lse = part_lse;
   p.own_base = at.own_base;
   p.whole_base = d.whole_base;
-  p.plan = setup.plan;
+  if (p.pre_ctas == 0) d.plan = plan_for(setup, index_count, fp8);
+  p.plan = d.plan;
   p.scale_log2 = d.scale_log2;
   p.batch = batch;
   p.groups = groups;
@@ -319,7 +330,8 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
   d.batch = rows;
   d.sparse_topk = top * page_size;
   d.sparse_total = total;
-  if (gqa::launch_decode_lsu_form(gqa::kFormHeads, false, d, setup.plan.tier1_ctas + setup.plan.tier2_ctas, stream,
+  d.plan = plan_for(setup, total, false);
+  if (gqa::launch_decode_lsu_form(gqa::kFormHeads, false, d, d.plan.tier1_ctas + d.plan.tier2_ctas, stream,
                                   gqa::kLaunchPdl) != cudaSuccess)
     return GQA_ERR_LAUNCH;
   return launched(gqa::launch_merge(gqa::kKvHeads, merge_params(d), stream));
@@ -367,7 +379,8 @@ int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_
   d.num_pages_check = num_pages;
   d.index_count = index_count;
   d.scores = reinterpret_cast<float*>(ws);
-  if (gqa::launch_decode_lsu_form(gqa::kFormScores, fp8, d, setup.plan.tier1_ctas + setup.plan.tier2_ctas, stream,
+  d.plan = plan_for(setup, index_count, fp8);
+  if (gqa::launch_decode_lsu_form(gqa::kFormScores, fp8, d, d.plan.tier1_ctas + d.plan.tier2_ctas, stream,
                                   gqa::kLaunchPlain) != cudaSuccess)
     return GQA_ERR_LAUNCH;
   if (gqa::launch_merge(gqa::kKvHeads, merge_params(d), stream) != cudaSuccess) return GQA_ERR_LAUNCH;
