@@ -43,9 +43,20 @@ struct DecodeSpace {
 // tokens begin when the first's, as short, are done. Two tiers and one, us a call, by tokens a CTA: blocks of bf16 caches 9: 15.5
 // and 16.7, 21: 17.6 both, 36: 28 and 20, 72: 34 and 25, 287: 61 and 55, 449: 84 and 82, 575: 101 and 105; accumulated weights, FP8
 // caches 35: 24 and 19, 283: 52 and 47, 555: 84 and 77, 1169: 157 and 153, 2278: 289 and 307.
-gqa::PlanConfig plan_for(const gqa::DecodeSetup& setup, int64_t tokens, bool fp8) {
+// Short sequences: a CTA takes them one after another (2 us each), so its smallest share is two of them where they are shorter than
+// 16 tokens, and no second tier (100 sequences of a token each: 78 us with shares of 32 tokens, 13 of 2).
+void share_for(gqa::PlanConfig& plan, int64_t tokens, int64_t sequences) {
+  const int64_t two = 2 * tokens / sequences;
+  if (two >= plan.min_units) return;
+  plan.min_units = static_cast<int>(two < 2 ? 2 : two);
+  plan.tier2_ctas = 0;
+}
+
+gqa::PlanConfig plan_for(const gqa::DecodeSetup& setup, int64_t tokens, int64_t sequences, bool fp8) {
   gqa::PlanConfig plan = setup.plan;
-  if (setup.default_tiers && tokens >= int64_t{20} * plan.tier1_ctas && tokens < int64_t{fp8 ? 1536 : 512} * plan.tier1_ctas) plan.tier2_ctas = 0;
+  if (!setup.default_plan) return plan;
+  share_for(plan, tokens, sequences);
+  if (tokens >= int64_t{20} * plan.tier1_ctas && tokens < int64_t{fp8 ? 1536 : 512} * plan.tier1_ctas) plan.tier2_ctas = 0;
   return plan;
 }
 
@@ -110,22 +121,47 @@ struct SelectSpaceLayout {
   }
 };
 
-// CTAs of the prefix pass, an even number, one an SM: the others are left to the own tokens' decode, which runs beside it.
-// Both are given SMs by the time of an SM that they take, as far as the sizes tell (groups alike, offsets that use all of
-// the indices): a step of 128 tokens and 64 sequences takes a pair 1.6 us (FP8 2.4), an own token an SM 0.03 us (FP8 0.02).
-// At most 9 SMs of 10, so that the decode's short runs begin at once, and at least two steps a pair. All SMs for the pass and
-// then all for the decode took: 16384 tokens x 128 sequences with 64 to 1024 own tokens 80 us, this way 69; with up to 64
-// own tokens 57 and 47; 2048 x 8 with up to 256 own tokens 26 and 20.
-int prefix_ctas(int sms, int batch, int groups, int prefix_count, int index_count, bool fp8) {
+// How the SMs are shared between the prefix pass, a pair of CTAs on two, and the own tokens' decode, which runs beside it on the
+// others: the number of pairs whose estimate, as far as the sizes tell (groups alike, offsets that use all of the indices), has
+// both done soonest. In us, measured with 4 to 72 pairs of 76: the pass 20 and 1.6 a step of its run (FP8 2.6; 1.3 and 2.1 where
+// the sequences of a group fill one tile), 0.3 a part that is joined, and 7 where a run ends inside a unit, or for each unit more that it holds; the decode 16
+// and 0.031 a token and SM, at least what HBM takes. Against shares in proportion and the decode's whole grid: 16384 tokens x 128
+// sequences with 64 to 1024 own tokens 68 -> 62, 4000 x 64 with 500 to 4000 87 -> 60, 500 x 64 with 2000 to 8000 170 -> 115, four
+// groups of 1000 x 32 with 100 to 1500 66 -> 47.
+int prefix_pairs(int sms, int batch, int groups, int prefix_count, int index_count, bool fp8) {
   const int pairs = sms / 2;
   if (groups <= 0 || prefix_count <= 0 || pairs == 0) return 0;
-  const double units = gqa::kKvHeads * std::ceil(std::ceil(static_cast<double>(batch) / groups) / 64.0);
-  const double steps = units * std::ceil(prefix_count / 128.0 + 0.5 * (groups - 1));
-  const double pass = steps * 2 * (fp8 ? 2.4 : 1.6), own = index_count * (fp8 ? 0.02 : 0.03);
-  double n = std::fmin(pairs * pass / (pass + own), 0.9 * pairs);
-  const double run = std::fmax(std::ceil(steps / std::fmax(n, 1.0)), 2.0);
-  n = std::ceil(steps / run);  // as few pairs as make the same runs
-  return 2 * static_cast<int>(std::fmin(std::fmax(n, 1.0), pairs));
+  const int64_t members = (batch - 1) / groups + 1, units = gqa::kKvHeads * ((members - 1) / 64 + 1) * groups;
+  const int64_t tiles = (prefix_count - 1) / (int64_t{128} * groups) + 1, steps = units * tiles;
+  const double step = members <= 32 ? (fp8 ? 2.1 : 1.3) : (fp8 ? 2.6 : 1.6), least = index_count * (fp8 ? 1056 / 6.3e6 : 2048 / 6.3e6);
+  int best = 1;
+  double best_us = 1e30;
+  int64_t last = 0;
+  for (int n = 1; n <= pairs - (index_count > 0 && pairs > 1); ++n) {
+    const int64_t run = (steps - 1) / n + 1;
+    if (run == last) continue;  // more pairs, none of them done sooner
+    last = run;
+    const double pass = 20 + step * run + 0.3 * tiles / run + (run > tiles ? 7.0 * ((run - 1) / tiles) : (tiles % run != 0 ? 7.0 : 0.0));
+    const double alone = index_count * 0.031 / (sms - 2 * n), r = std::fmin(alone, least) / std::fmax(std::fmax(alone, least), 1e-9), r3 = r * r * r;
+    const double own = 16 + std::fmax(alone, least) * (1 + 0.15 * r3 * r3);  // both near the end of what they have
+    const double us = std::fmax(pass, own) + 0.1 * std::fmin(pass, own);
+    if (us < best_us) best_us = us, best = n;
+  }
+  return best;
+}
+
+// The decode's plan beside `pairs` pairs: one tier that fills the other SMs, three CTAs each, or two where they have few tokens
+// (2048 tokens x 64 sequences with 200 to 1000 own tokens 28 us with two, 32 with three; groups of 1000 x 32 with 100 to 1500
+// 50 and 47; FP8 caches always three: 61 and 54 for 4000 x 64).
+gqa::PlanConfig plan_beside(const gqa::DecodeSetup& setup, int pairs, int index_count, int batch, bool fp8) {
+  gqa::PlanConfig plan = setup.plan;
+  const int left = setup.sm_count - 2 * pairs;
+  if (!setup.default_plan || left <= 0) return plan;
+  share_for(plan, index_count, batch);
+  const int ctas = left * (!fp8 && index_count < 512 * left ? 2 : 3);
+  if (ctas < plan.tier1_ctas) plan.tier1_ctas = ctas;
+  plan.tier2_ctas = 0;
+  return plan;
 }
 
 bool select_sizes_ok(int rows, int width) { return rows > 0 && width > 0 && width <= kMostItems && static_cast<int64_t>(rows) * width <= (int64_t{1} << 34); }
@@ -197,13 +233,14 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
   p.out = out;
   p.lse = lse;
   p.group_start = reinterpret_cast<int64_t*>(ws + at.start);
-  p.pre_ctas = prefix_ctas(setup.sm_count, batch, groups, prefix_count, index_count, fp8);
+  const int pairs = prefix_pairs(setup.sm_count, batch, groups, prefix_count, index_count, fp8);
+  p.pre_ctas = 2 * pairs;
   p.wait_limit_ns = setup.wait_limit_ns;
   p.part_o = part_o;
   p.part_lse = part_lse;
   p.own_base = at.own_base;
   p.whole_base = d.whole_base;
-  if (p.pre_ctas == 0) d.plan = plan_for(setup, index_count, fp8);
+  d.plan = pairs > 0 ? plan_beside(setup, pairs, index_count, batch, fp8) : plan_for(setup, index_count, batch, fp8);
   p.plan = d.plan;
   p.scale_log2 = d.scale_log2;
   p.batch = batch;
@@ -330,7 +367,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
   d.batch = rows;
   d.sparse_topk = top * page_size;
   d.sparse_total = total;
-  d.plan = plan_for(setup, total, false);
+  d.plan = plan_for(setup, total, rows, false);
   if (gqa::launch_decode_lsu_form(gqa::kFormHeads, false, d, d.plan.tier1_ctas + d.plan.tier2_ctas, stream,
                                   gqa::kLaunchPdl) != cudaSuccess)
     return GQA_ERR_LAUNCH;
@@ -379,7 +416,7 @@ int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_
   d.num_pages_check = num_pages;
   d.index_count = index_count;
   d.scores = reinterpret_cast<float*>(ws);
-  d.plan = plan_for(setup, index_count, fp8);
+  d.plan = plan_for(setup, index_count, batch, fp8);
   if (gqa::launch_decode_lsu_form(gqa::kFormScores, fp8, d, d.plan.tier1_ctas + d.plan.tier2_ctas, stream,
                                   gqa::kLaunchPlain) != cudaSuccess)
     return GQA_ERR_LAUNCH;
