@@ -300,3 +300,12 @@ def test_choice_where_errors_have_no_bound(top, first, last, bad):
         w["bounds"][blocks] = -20.0
         w["bounds"][blocks, :, :, 5] = 3e38
     assert np.array_equal(select(w, top, first, last).cpu().numpy(), chosen(w, top, first, last))
+
+
+@pytest.mark.parametrize("lens,page,rows,top", [([40] * 200, 1, 1, 1), ([500] * 50, 4, 2, 3), ([3000] * 8, 16, 2, 100)])
+def test_attention_over_the_plans(lens, page, rows, top):
+    """Rows of a token or a few (small shares), and as many tokens as one tier takes."""
+    w = make(lens, page, sum(lens), rows)
+    pkg.block_bounds(w["k"], w["bounds"], w["table"], w["lens"])
+    blocks = select(w, top, 0, 1)
+    check(w, blocks, *attend(w, blocks))

@@ -254,3 +254,11 @@ def test_two_streams_at_once():
     for pair in got:
         for x, y in zip(pair, want):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefixes,members,own", [([1000], [100], [1]), ([300, 40], [70, 50], [0, 1, 2]), ([40], [60], [300, 500]), ([3000], [40], [2, 900])])
+def test_parity_over_the_plans(prefixes, members, own, fp8):
+    """Own tokens few, short and many beside the prefix: every share of the SMs."""
+    args = make(prefixes, members, 1, own, fp8, seed=sum(prefixes) + sum(own))
+    check(args, *pkg.shared_run(*args))

@@ -180,3 +180,11 @@ def test_evict_by_clusters_of_each_size(lens, budget):
     first, last = min(2, budget), min(40, budget - min(2, budget))
     w, indptr, ids = listed(lens, max(lens), 5, "few")
     evict_check((w, indptr, ids, budget, first, last), pkg.kv_evict(w, indptr, ids, budget, first, last))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[1] * 300, [0, 1, 2, 3] * 100, [15, 17, 0] * 40, [400] * 30, [300, 3] * 60])
+def test_parity_over_the_plans(lens, fp8):
+    """Sequences of a token or two (small shares), and as many tokens as one tier takes."""
+    args = make(lens, max(lens), fp8, sum(lens) + 1)
+    check(args, 0.5, pkg.run_weighted(*args, decay=0.5))
