@@ -48,9 +48,9 @@ __device__ __forceinline__ int prefix_range(const SharedParams& p, int g, int& f
 //
 // What bounds it: a step of both tiles takes 3330 clocks, 2048 of them MMAs; a tile's chain is its softmax (1880 clocks from
 // scores to the second half of P), its MMAs (1024 at least) and the barriers between them. 16384 tokens for 128 sequences on 43
-// pairs: 54 us, 53 % of the tensor pipe's cycles (the own tokens' decode has the other SMs). With an FP8 cache a step takes 4800
+// pairs: 54 us, 53 % of the tensor pipe's cycles (the own tokens' decode has the other SMs; on 47 pairs 49.5 us). With an FP8 cache a step takes 4800
 // clocks: twice the operations a score, and warps that convert beside them. Two threads a row (64 tokens each, 768 threads) took
-// 1270 clocks for the softmax, but 79 us for the whole call instead of 68 (FP8 103, not 81): more warps for the same issue slots.
+// 1270 clocks for the softmax, but 79 us for the whole call where this form took 68 (FP8 103 and 81): more warps for the same issue slots.
 //
 // Pages are single tokens in any order, so their rows are gathered by 16-byte cp.async, written where the 128-byte swizzle
 // wants them; four warps keep up to four steps (32 KB each, a CTA) in flight. The odd CTA's copies are counted there, and its MMA warp
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) gqa_shared_prefix_kernel(const
 // ------------------------------------------------------------------- join
 // A block per sequence and KV head, a thread per dim. The parts are taken 16 at a time: a thread per part and head finds
 // the part and its LSE, their largest gives the weights 2^(LSE - max), and every thread sums its dim of the parts, whose
-// loads do not depend on one another. Bound by two round trips of loads, and by 4 KB a part (64 sequences 11 us, 128 14).
+// loads do not depend on one another. Bound by two round trips of loads, and by 4 KB a part (8 sequences 11 us, 128 10 to 14).
 constexpr int kJoinParts = 16;
 
 __global__ void __launch_bounds__(kHeadDim) gqa_shared_join_kernel(const SharedParams p) {
