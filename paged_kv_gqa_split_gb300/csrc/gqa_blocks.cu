@@ -57,19 +57,20 @@ __global__ void __launch_bounds__(kBoundThreads) gqa_block_bounds_kernel(const B
     if (static_cast<unsigned>(b) >= static_cast<unsigned>(p.num_blocks)) return false;
     block = b;
     const int tokens = min(p.page_size, n - i * p.page_size);
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + lane;
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + t0 * 64 + lane;
     mm.init();
-    int t = t0;
-    for (; t + 15 * step < tokens; t += 16 * step) {
+    // a block may have more than 2^25 tokens: what is left is counted, and the offset grows in the pointer's 64 bits
+    int left = tokens > t0 ? (tokens - t0 - 1) / step + 1 : 0;
+    for (; left >= 16; left -= 16, k += 16 * step * 64) {
       uint4 x[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) x[u] = __ldcg(k + (t + u * step) * 64);
+      for (int u = 0; u < 16; ++u) x[u] = __ldcg(k + u * step * 64);
 #pragma unroll
       for (int u = 0; u < 16; ++u) mm.add(x[u], x[u]);
     }
 #pragma unroll 4
-    for (; t < tokens; t += step) {
-      const uint4 x = __ldcg(k + t * 64);
+    for (; left > 0; --left, k += step * 64) {
+      const uint4 x = __ldcg(k);
       mm.add(x, x);
     }
     return true;
