@@ -496,10 +496,10 @@ __global__ void __launch_bounds__(kSlotThreads) gqa_block_slots_kernel(const Blo
     }
     int* slots = p.slots + (static_cast<int64_t>(g) * p.rows + row) * per_row + static_cast<int64_t>(j0) * p.page_size;
     const int count = min(kSlotBlocks, p.top - j0) * p.page_size;  // at most 2^31 - 1: rows * top * page_size is
-    for (int z0 = 0; z0 < count; z0 += 32) {
-      const int z = min(z0 + lane, count - 1), j = z / p.page_size, t = z - j * p.page_size;
+    for (unsigned z0 = 0; z0 < static_cast<unsigned>(count); z0 += 32) {
+      const int z = static_cast<int>(min(z0 + lane, static_cast<unsigned>(count) - 1)), j = z / p.page_size, t = z - j * p.page_size;
       const int b = __shfl_sync(0xffffffffu, block, j), n = __shfl_sync(0xffffffffu, tokens, j);
-      if (z0 + lane < count) slots[z] = t < n ? b * p.page_size + t : -1;
+      if (z0 + lane < static_cast<unsigned>(count)) slots[z] = t < n ? b * p.page_size + t : -1;
     }
   }
 }

@@ -505,9 +505,11 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
   int wb = 0, win = 0;      // kv_indptr[wb + lane]
   int ib = 0;               // page-id ring holds tokens [ib, ib + 256)
 
-  auto request_ids = [&](int pos) {  // page id of token pos into its ring slot (zero past the end)
+  // page id of token pos into its ring slot (zero past the end; unsigned, since a position past the end may pass 31 bits)
+  auto request_ids = [&](unsigned pos) {
+    const unsigned n = static_cast<unsigned>(T);
     const int* ids_of = FORM == kFormHeads ? p.kv_indices + static_cast<int64_t>(w) * T : p.kv_indices;
-    cp_async_4(ids_base + (pos & (C::kIdsRing - 1)) * 4, ids_of + min(pos, T - 1), pos < T ? 4u : 0u);
+    cp_async_4(ids_base + (pos & (C::kIdsRing - 1)) * 4, ids_of + min(pos, n - 1), pos < n ? 4u : 0u);
   };
 
   // Opens the head-group segment at u_next of the current range. `first`:
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
     // round trip overlaps the search of kv_indptr
     ib = tt & ~31;
 #pragma unroll
-    for (int c = 0; c < C::kIdsRing / 32; ++c) request_ids(ib + 32 * c + lane);
+    for (int c = 0; c < C::kIdsRing / 32; ++c) request_ids(static_cast<unsigned>(ib) + 32 * c + lane);
     cp_async_commit();
     if (!SP) wb = warp_find_window(p.kv_indptr, B, tt, lane, first, pre, win);
     cp_async_wait<0>();
@@ -640,8 +642,8 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
     if (more && next_tile(tl)) {
       // keep the ring at [ib, ib + 256) with tl.tt < ib + 32: the ids this tile
       // reads were requested >= 12 tiles ago and have completed
-      while (tl.tt >= ib + 32) {
-        request_ids(ib + C::kIdsRing + lane);
+      while (tl.tt - ib >= 32) {
+        request_ids(static_cast<unsigned>(ib) + C::kIdsRing + lane);
         ib += 32;
       }
       int flags = tl.flags;
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(NG * 32, (F8 || CC) ? (TT == 32 ? 2 : 3) : 16 
       // tokens that enter the softmax: the first cnt, less (sparse mode) masked columns
       unsigned mask = tl.cnt >= 32 ? 0xffffffffu : ((1u << tl.cnt) - 1u);
       if constexpr (kLeaveOut) {
-        const int pg = ids[(tl.tt + lane) & (C::kIdsRing - 1)];
+        const int pg = ids[(static_cast<unsigned>(tl.tt) + lane) & (C::kIdsRing - 1)];
         mask &= __ballot_sync(0xffffffffu, static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages_check));
       }
       if constexpr (F8) {

@@ -68,8 +68,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
-__device__ __forceinline__ int load_index(const int* __restrict__ idx, int total, int pos) {
-  return pos < total ? __ldg(idx + pos) : 0;
+// (unsigned: a position past the end may pass 31 bits)
+__device__ __forceinline__ int load_index(const int* __restrict__ idx, int total, unsigned pos) {
+  return pos < static_cast<unsigned>(total) ? __ldg(idx + pos) : 0;
 }
 
 // ------------------------------------------------------------------ producer
@@ -167,10 +168,10 @@ __device__ __forceinline__ void tma_producer(const DecodeParams& p, uint32_t sba
 
     // ring of four 32-entry windows of kv_indices, starting at the 32-aligned block holding t
     int ib = t & ~31;
-    int ix0 = load_index(p.kv_indices, T, ib + lane);
-    int ix1 = load_index(p.kv_indices, T, ib + 32 + lane);
-    int ix2 = load_index(p.kv_indices, T, ib + 64 + lane);
-    int ix3 = load_index(p.kv_indices, T, ib + 96 + lane);
+    int ix0 = load_index(p.kv_indices, T, static_cast<unsigned>(ib) + lane);
+    int ix1 = load_index(p.kv_indices, T, static_cast<unsigned>(ib) + 32 + lane);
+    int ix2 = load_index(p.kv_indices, T, static_cast<unsigned>(ib) + 64 + lane);
+    int ix3 = load_index(p.kv_indices, T, static_cast<unsigned>(ib) + 96 + lane);
 
     while (ok && t < t_stop) {
       unsigned m;
@@ -200,15 +201,15 @@ __device__ __forceinline__ void tma_producer(const DecodeParams& p, uint32_t sba
       last_hg = hg;
       last_si = si;
 
-      for (int tt = t; tt < p_hi; tt += TILE) {
+      for (int tt = t; tt < p_hi; tt += min(TILE, p_hi - tt)) {
         const int cnt = min(TILE, p_hi - tt);
         const int flags = pflags | (tt == t ? F_QLOAD : 0) | (tt + cnt == p_hi ? F_END : 0);
-        while (tt >= ib + 32) {
+        while (tt - ib >= 32) {
           ix0 = ix1;
           ix1 = ix2;
           ix2 = ix3;
           ib += 32;
-          ix3 = load_index(p.kv_indices, T, ib + 96 + lane);
+          ix3 = load_index(p.kv_indices, T, static_cast<unsigned>(ib) + 96 + lane);
         }
         // page of token tt + lane (tt - ib < 32, so tt + lane - ib < 64)
         const int off = tt + lane - ib;

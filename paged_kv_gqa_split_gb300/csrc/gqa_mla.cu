@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
   int p_hi = 0, p_flags = 0, pb = 0;
   SplitInfo p_si = {1, 0, 0};
   int wb = 0, win = 0, ib = 0;
-  auto request_ids = [&](int pos) {
-    cp_async_4(ids_base + (pos & (kMlaIdsRing - 1)) * 4, p.slots + min(pos, T - 1), pos < T ? 4u : 0u);
+  auto request_ids = [&](unsigned pos) {  // (a position past the end may pass 31 bits)
+    const unsigned n = static_cast<unsigned>(T);
+    cp_async_4(ids_base + (pos & (kMlaIdsRing - 1)) * 4, p.slots + min(pos, n - 1), pos < n ? 4u : 0u);
   };
   struct MTile {
     int b, cnt, flags, hg, tt;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
       p_hi = tt;
       ib = tt & ~31;
 #pragma unroll
-      for (int cc = 0; cc < kMlaIdsRing / 32; ++cc) request_ids(ib + 32 * cc + lane);
+      for (int cc = 0; cc < kMlaIdsRing / 32; ++cc) request_ids(static_cast<unsigned>(ib) + 32 * cc + lane);
       cp_async_commit();
       wb = warp_find_seq<true>(p.kv_indptr, B, tt, lane);
       if (wb >= 0) win = load_indptr_window<true>(p.kv_indptr, B, wb, lane);
@@ -324,8 +325,8 @@ __global__ void __launch_bounds__(kMlaThreads, CPS) gqa_mla_decode_kernel(const 
     const uint32_t sb = sbase + stage * L::kStageBytes;
     MTile tl;
     if (more && next_tile(tl)) {
-      while (tl.tt >= ib + 32) {
-        request_ids(ib + kMlaIdsRing + lane);
+      while (tl.tt - ib >= 32) {
+        request_ids(static_cast<unsigned>(ib) + kMlaIdsRing + lane);
         ib += 32;
       }
       // 16 rows x 72 chunks: 8 threads per row, each copying chunks (tid & 7) + 8 k

@@ -46,3 +46,46 @@ def test_bounds_of_a_block_of_more_than_2_25_tokens(ahead):
     bounds = torch.full((1, 2, 4, 128), 9.0, dtype=BF, device="cuda")
     pkg.block_bounds(k, bounds, i32([[0]]), i32([page - ahead]), i32([page - ahead - 1]))
     assert np.array_equal(cx.f64(bounds), want)
+
+
+def test_chosen_blocks_of_nearly_2_31_tokens():
+    """One row whose listed blocks make 2^31 - 128 places: the reads ahead of the last ones end where the list ends. All
+    places but those of the last 4 listed blocks are -1, so the result is that of these blocks alone."""
+    room(48)
+    page, top = 128, 2 ** 24 - 1
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(4, page, 4, 128, generator=g).to(BF).cuda() for _ in range(2))
+    q = torch.randn(1, 32, 128, generator=g).to(BF).cuda()
+    table, req, lens = i32([[2, 0, 3, 1]]), i32([0]), i32([3 * page + 77])
+    few = i32([[[0, 1, 2, 3]] * 4])
+    blocks = torch.full((1, 4, top), -1, dtype=I32, device="cuda")
+    blocks[..., -4:] = few
+    out, lse = pkg.block_sparse_run(q, k, v, blocks, table, req, lens)
+    (want,) = cx.block_sparse_oracle(q, k, v, few, table, req, lens, 128 ** -0.5)
+    assert np.all(np.abs(cx.f64(out)[0] - want.out) <= want.out_bound(False))
+    assert np.all(np.abs(cx.f64(lse)[0] - want.lse) <= want.lse_bound())
+    assert _lib.gqa_paged_decode_device_error() == 0
+
+
+@pytest.mark.parametrize("tuning", [(0, 0, 0, 0, 0, 0), (0, 0, 4, 16, 5, 1)])
+def test_decode_of_nearly_2_31_tokens(tuning):
+    """The plain decode by copies and by tensor copies, every token the same page: all probabilities are 2^-31, the sums of
+    values that are powers of two are exact, and so is the result; the LSE is the score and 31."""
+    room(16)
+    n = 2 ** 31 - 1
+    g = torch.Generator().manual_seed(2)
+    k = torch.randn(3, 1, 4, 128, generator=g).to(BF).cuda()
+    v = torch.exp2(torch.randint(-3, 4, (3, 1, 4, 128), generator=g).float()).to(BF).cuda()
+    q = torch.randn(1, 32, 128, generator=g).to(BF).cuda()
+    pages = torch.ones(n, dtype=I32, device="cuda")
+    try:
+        assert _lib.gqa_paged_decode_set_tuning(*tuning) == 0
+        out, lse = pkg.run(q, k, v, i32([0, n]), pages, 128 ** -0.5)
+    finally:
+        _lib.gqa_paged_decode_set_tuning(0, 0, 0, 0, 0, 0)
+    assert torch.equal(out[0].view(4, 8, 128), v[1, 0][:, None].expand(4, 8, 128))
+    s = (cx.f64(q)[0].reshape(4, 8, 128) * cx.f64(k)[1, 0][:, None]).sum(-1).reshape(32) * 128 ** -0.5 / np.log(2)
+    a = cx.Attended(q[0], cx.f64(k)[1], cx.f64(v)[1], 128 ** -0.5)
+    # the pieces' own LSEs are rounded to 2^-24 of about 31, and 2^-19 of weight: 2^-18 in all
+    assert np.all(np.abs(cx.f64(lse)[0] - s - 31) <= a.lse_bound() + 2.0 ** -18)
+    assert _lib.gqa_paged_decode_device_error() == 0
