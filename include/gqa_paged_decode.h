@@ -598,7 +598,9 @@ int gqa_mla_prefill_fill(const void* q, const void* w_kv, const void* kv_cache, 
  * Counts and widths go up to 2^30.
  * The tuning's CTA counts and tiers apply to the decode inside, not its kernel
  * choice. The caches are bf16, or where cache_format is an argument also FP8
- * (GQA_CACHE_*; as in gqa_paged_decode_fp8). lse is in base 2 as there.
+ * (GQA_CACHE_*; as in gqa_paged_decode_fp8). lse is in base 2 as there. A query
+ * head that meets a score of NaN or +inf has NaN for its outputs and its lse,
+ * as in gqa_paged_decode; other heads and rows are as without it.
  */
 
 /*

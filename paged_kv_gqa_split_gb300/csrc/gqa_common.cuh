@@ -705,7 +705,7 @@ __device__ __forceinline__ void merge_split_warp(const float* part_o, const floa
   __nv_bfloat16* ob = out + (b * kQoHeads + h0) * kHeadDim;
 #pragma unroll
   for (int h = 0; h < 8; ++h) {
-    const float inv = den[h] > 0.f ? 1.f / den[h] : 0.f;  // no valid token in any piece: O = 0
+    const float inv = den[h] != 0.f ? 1.f / den[h] : 0.f;  // no valid token in any piece: O = 0
 #pragma unroll
     for (int j = 0; j < 4; ++j) ob[h * kHeadDim + lane + 32 * j] = __float2bfloat16_rn(acc[j][h] * inv);
   }
@@ -784,7 +784,7 @@ __device__ __forceinline__ void merge_split_warp_staged(const float* part_o, con
   __nv_bfloat16* ob = out + (b * kQoHeads + h0) * kHeadDim;
 #pragma unroll
   for (int h = 0; h < 8; ++h) {
-    const float inv = den[h] > 0.f ? 1.f / den[h] : 0.f;  // no valid token in any piece: O = 0
+    const float inv = den[h] != 0.f ? 1.f / den[h] : 0.f;  // no valid token in any piece: O = 0
 #pragma unroll
     for (int j = 0; j < 4; ++j) ob[h * kHeadDim + lane + 32 * j] = __float2bfloat16_rn(acc[j][h] * inv);
   }
@@ -821,12 +821,13 @@ __device__ __forceinline__ bool finish_piece(const HeadState& st, bool final_pie
     lt0 += __shfl_xor_sync(0xffffffffu, lt0, o);
     lt1 += __shfl_xor_sync(0xffffffffu, lt1, o);
   }
-  // a piece whose tokens were all masked out has l = 0: O = 0, LSE = -inf
+  // a piece whose tokens were all masked out has l = 0: O = 0, LSE = -inf; one with a score of NaN or +inf has NaN
+  // for both, which the joins of pieces pass on
   // oscale: the FP8 path's acc holds O * l / cv, so its oscale is cv
-  const float i0 = lt0 > 0.f ? oscale / lt0 : 0.f;
-  const float i1 = lt1 > 0.f ? oscale / lt1 : 0.f;
-  const float lse0 = lt0 > 0.f ? st.m0 + log2f(lt0) : -INFINITY;
-  const float lse1 = lt1 > 0.f ? st.m1 + log2f(lt1) : -INFINITY;
+  const float i0 = lt0 != 0.f ? oscale / lt0 : 0.f;
+  const float i1 = lt1 != 0.f ? oscale / lt1 : 0.f;
+  const float lse0 = lt0 != 0.f ? st.m0 + log2f(lt0) : -INFINITY;
+  const float lse1 = lt1 != 0.f ? st.m1 + log2f(lt1) : -INFINITY;
   if (final_piece) {
     __nv_bfloat16* ob = out + (b * kQoHeads + h0) * kHeadDim;
 #pragma unroll
@@ -862,8 +863,8 @@ template <int NG>
 __device__ __forceinline__ bool finish_piece_cc(const CcState& cs, bool final_piece, int64_t b, int h0, int64_t sid,
                                                 int w, const SplitInfo& si, const DecodeParams& p, int lane) {
   const int h = lane & 7, g = lane >> 3;
-  const float inv = cs.l > 0.f ? 1.f / cs.l : 0.f;
-  const float lse_v = cs.l > 0.f ? cs.m + log2f(cs.l) : -INFINITY;
+  const float inv = cs.l != 0.f ? 1.f / cs.l : 0.f;
+  const float lse_v = cs.l != 0.f ? cs.m + log2f(cs.l) : -INFINITY;
   if (final_piece) {
     uint4* ob = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (b * kQoHeads + h0 + h) * kHeadDim +
                                          32 * g);

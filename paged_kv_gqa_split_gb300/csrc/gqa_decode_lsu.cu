@@ -156,21 +156,9 @@ __device__ __forceinline__ void stage_partials(const DecodeParams& p, int first_
   staged_wait();
 }
 
-// Running LSE-weighted fold of one staged piece into (m, den, acc) for head q:
-// m = max LSE so far, den = sum 2^(LSE_i - m), acc = sum 2^(LSE_i - m) O_i.
-// A piece with LSE -inf (no token) adds nothing.
-__device__ __forceinline__ bool fold_weights(float& m, float& den, float lse_i, float& sc, float& wt) {
-  const float mn = fmaxf(m, lse_i);
-  if (mn == -INFINITY) return false;
-  sc = ex2(m - mn);
-  wt = ex2(lse_i - mn);
-  den = den * sc + wt;
-  m = mn;
-  return true;
-}
-
 // Running LSE-weighted fold of four heads: (m, den, acc) take piece i's LSEs
-// `l` and O values `o` (one dim) with the weights 2^(LSE_i - m).
+// `l` and O values `o` (one dim) with the weights 2^(LSE_i - m); m = max LSE so
+// far, den = sum 2^(LSE_i - m), acc = sum 2^(LSE_i - m) O_i.
 struct Fold4 {
   float m[4], den[4], acc[4];
   __device__ __forceinline__ void init() {
@@ -186,7 +174,7 @@ struct Fold4 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float mn = fmaxf(m[j], lv[j]);
-      if (mn == -INFINITY) continue;  // nothing yet and a piece with no token
+      if (mn == -INFINITY && lv[j] == -INFINITY) continue;  // nothing yet and a piece with no token (NaN is passed on)
       const float sc = ex2(m[j] - mn), wt = ex2(lv[j] - mn);
       den[j] = den[j] * sc + wt;
       acc[j] = acc[j] * sc + wt * ov[j];
@@ -201,7 +189,7 @@ struct Fold4 {
       const float d2 = __shfl_xor_sync(0xffffffffu, den[j], o);
       const float a2 = __shfl_xor_sync(0xffffffffu, acc[j], o);
       const float mn = fmaxf(m[j], m2);
-      if (mn == -INFINITY) continue;
+      if (mn == -INFINITY && d2 == 0.f) continue;
       const float s1 = ex2(m[j] - mn), s2 = ex2(m2 - mn);
       den[j] = den[j] * s1 + d2 * s2;
       acc[j] = acc[j] * s1 + a2 * s2;
@@ -261,12 +249,12 @@ __device__ __forceinline__ void merge_share(const DecodeParams& p, int b, int h0
       const Fold4& f = r == 0 ? f0 : f1;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        out[j * kHeadDim + d_lo + r] = __float2bfloat16_rn(f.den[j] > 0.f ? f.acc[j] / f.den[j] : 0.f);
+        out[j * kHeadDim + d_lo + r] = __float2bfloat16_rn(f.den[j] != 0.f ? f.acc[j] / f.den[j] : 0.f);
     }
     if (r == 0 && d_lo == 0 && p.lse != nullptr) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        p.lse[static_cast<int64_t>(b) * kQoHeads + h0 + 4 * hh + j] = f0.den[j] > 0.f ? f0.m[j] + log2f(f0.den[j])
+        p.lse[static_cast<int64_t>(b) * kQoHeads + h0 + 4 * hh + j] = f0.den[j] != 0.f ? f0.m[j] + log2f(f0.den[j])
                                                                                     : -INFINITY;
     }
     return;
@@ -290,12 +278,12 @@ __device__ __forceinline__ void merge_share(const DecodeParams& p, int b, int h0
     if (d < nd) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        out[j * kHeadDim + d_lo + d] = __float2bfloat16_rn(f.den[j] > 0.f ? f.acc[j] / f.den[j] : 0.f);
+        out[j * kHeadDim + d_lo + d] = __float2bfloat16_rn(f.den[j] != 0.f ? f.acc[j] / f.den[j] : 0.f);
     }
     if (d == 0 && d_lo == 0 && p.lse != nullptr) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        p.lse[static_cast<int64_t>(b) * kQoHeads + h0 + 4 * hh + j] = f.den[j] > 0.f ? f.m[j] + log2f(f.den[j])
+        p.lse[static_cast<int64_t>(b) * kQoHeads + h0 + 4 * hh + j] = f.den[j] != 0.f ? f.m[j] + log2f(f.den[j])
                                                                                   : -INFINITY;
     }
   }

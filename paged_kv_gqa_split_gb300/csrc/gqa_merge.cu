@@ -148,12 +148,12 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
       }
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        const float o = ma.den[h] > 0.f ? ma.acc[h] / ma.den[h] : 0.f;  // no valid token anywhere: O = 0
+        const float o = ma.den[h] != 0.f ? ma.acc[h] / ma.den[h] : 0.f;  // no valid token anywhere: O = 0
         ob[(g * kGroup + h) * kHeadDim + d] = __float2bfloat16_rn(o);
       }
       if ((it & 3) == 0 && lane == 0 && lo != nullptr) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) lo[g * kGroup + h] = ma.den[h] > 0.f ? ma.m[h] + log2f(ma.den[h]) : -INFINITY;
+        for (int h = 0; h < 8; ++h) lo[g * kGroup + h] = ma.den[h] != 0.f ? ma.m[h] + log2f(ma.den[h]) : -INFINITY;
       }
     }
   } else {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float mn = fmaxf(m[i], l4[i]);
-            if (mn == -INFINITY) continue;  // nothing added yet and a padding split
+            if (mn == -INFINITY && l4[i] == -INFINITY) continue;  // nothing added yet and a padding split (NaN is passed on)
             const float sc = ex2(m[i] - mn), wt = ex2(l4[i] - mn);
             den[i] = den[i] * sc + wt;
             acc[i] = acc[i] * sc + wt * o4[i];
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
           const float d2 = __shfl_xor_sync(0xffffffffu, den[i], o);
           const float a2 = __shfl_xor_sync(0xffffffffu, acc[i], o);
           const float mn = fmaxf(m[i], m2);
-          if (mn == -INFINITY) continue;
+          if (mn == -INFINITY && d2 == 0.f) continue;
           const float s1 = ex2(m[i] - mn), s2 = ex2(m2 - mn);
           den[i] = den[i] * s1 + d2 * s2;
           acc[i] = acc[i] * s1 + a2 * s2;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
           for (int i = 0; i < 4; ++i) {
             const float m2 = xw[gi * cols + col][i];
             const float mn = fmaxf(m[i], m2);
-            if (mn == -INFINITY) continue;
+            if (mn == -INFINITY && xw[gi * cols + col][4 + i] == 0.f) continue;
             const float s1 = ex2(m[i] - mn), s2 = ex2(m2 - mn);
             den[i] = den[i] * s1 + xw[gi * cols + col][4 + i] * s2;
             acc[i] = acc[i] * s1 + xw[gi * cols + col][8 + i] * s2;
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const MergePar
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int h = g * kGroup + hq * 4 + i;
-          ob[h * kHeadDim + d] = __float2bfloat16_rn(den[i] > 0.f ? acc[i] / den[i] : 0.f);
-          if (d == 0 && lo != nullptr) lo[h] = den[i] > 0.f ? m[i] + log2f(den[i]) : -INFINITY;
+          ob[h * kHeadDim + d] = __float2bfloat16_rn(den[i] != 0.f ? acc[i] / den[i] : 0.f);
+          if (d == 0 && lo != nullptr) lo[h] = den[i] != 0.f ? m[i] + log2f(den[i]) : -INFINITY;
         }
       }
     }

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kWeighThreads) gqa_weigh_kernel(const WeighPar
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const float l = lse[4 * k + h];
-          sum += l == -INFINITY ? 0.f : ex2(v[h] - l);
+          sum += v[h] == -INFINITY ? 0.f : ex2(v[h] - l);  // 0: left out, where l may be -inf or NaN
         }
       }
       p.out[at] = p.decay == 0.f ? sum : p.decay * old + sum;
