@@ -647,9 +647,10 @@ int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_tab
  * has none): the first keep_first and the last keep_last of them, then those of
  * the largest
  *   score = max over the 8 query heads h of g of sum_d max(q[h][d], 0) bounds[block][0][g][d] + min(q[h][d], 0) bounds[block][1][g][d],
- * which no query head's product with a key of the block passes. A score that is
- * no finite fp32 number counts as the largest; equal scores go to the lower
- * block. The scores decide as if formed with 2^-44 of their terms' size (terms
+ * which no query head's product with a key of the block passes. A score that
+ * rounds to no finite fp32 number, or of which a head's sum is NaN, counts as
+ * the largest; equal scores go to the lower block. The scores decide as if
+ * formed with 2^-40 of their terms' size, whatever partial sums may reach (terms
  * below fp32's normal range: with what an fp32 product leaves of them).
  * blocks[row][g][0 .. top) are the chosen blocks' numbers in the table, ascending,
  * then -1. keep_first + keep_last <= top.

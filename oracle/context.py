@@ -120,10 +120,8 @@ def select_oracle(q, bounds, block_table, token_to_req, lens, top, page, keep_fi
             qg = q[r, g * GQA_GROUP:(g + 1) * GQA_GROUP]
             with np.errstate(invalid="ignore", over="ignore"):
                 each = (np.maximum(qg, 0)[None] * x[:, 0, g][:, None] + np.minimum(qg, 0)[None] * x[:, 1, g][:, None])
-                size = np.maximum(np.abs(qg)[None] * np.abs(x[:, :, g]).max(1)[:, None], 0).sum(-1)
-                s = each.sum(-1)
-            ok = np.isfinite(s).all(1) & (size < 3.0e38).all(1)
-            score = np.where(ok, s.max(1), np.inf)
+                s = each.sum(-1).max(1)  # NaN if a head's is
+                score = np.where(np.isfinite(s.astype(np.float32)), s, np.inf)
             order = sorted(range(len(cand)),
                            key=lambda c: (not (cand[c] < keep_first or cand[c] >= count - keep_last), -score[c], cand[c]))
             pick = sorted(cand[c] for c in order[:top])

@@ -146,6 +146,7 @@ cudaError_t launch_block_bounds(const BoundsParams& p, int sm_count, cudaStream_
 // blocks 4.3 us), with many rows by the bounds' bytes (128 rows of 32 to 256 blocks 9 us).
 constexpr int kScoreBlocks = 16;  // of a row, a block of threads
 constexpr float kGamma = 0x1p-14f;
+constexpr float kBounded = kGamma * 0x1p126f;  // an error below it: no partial sum of the MMAs can pass fp32's range
 constexpr uint32_t kNoBlock = 0xffffffffu;  // in a score's place where the table names no block of the pool
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -223,9 +224,9 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
       ea = max_nan(ea, __shfl_xor_sync(0xffffffffu, ea, o));
       eb = max_nan(eb, __shfl_xor_sync(0xffffffffu, eb, o));
     }
-    // a score whose error has no bound is to be formed again, as one that is no number
-    if (!(ea < INFINITY)) sa = __uint_as_float(0x7fc00000u), ea = 0.f;
-    if (!(eb < INFINITY)) sb = __uint_as_float(0x7fc00000u), eb = 0.f;
+    // a score whose sums may have passed fp32's range on the way is to be formed again, as one that is no number
+    if (!(ea < kBounded)) sa = __uint_as_float(0x7fc00000u), ea = 0.f;
+    if (!(eb < kBounded)) sb = __uint_as_float(0x7fc00000u), eb = 0.f;
     float e = fmaxf(ea, eb);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
 // ----------------------------------------------------------------- choice
 // A block of threads per row and KV head. The MMA's scores decide all blocks but those within the error of the k-th
 // largest; of these the score is formed again in two floats (products of bf16 are exact, sums are carried with their
-// rounding errors: 2^-44 of the terms), and the larger ones, then the lower ones, fill what is left. They are few unless
+// rounding errors: 2^-40 of the terms), and the larger ones, then the lower ones, fill what is left. They are few unless
 // scores tie: up to kListed are compared with one another, more by a second radix select over both floats. Scores are held
 // in shared memory as ordered words, up to kHeldWords of them (else in their place in global memory).
 // Small blocks of threads for short rows: their barriers are cheap and all fit the GPU at once. Bound by barriers and round
@@ -256,19 +257,14 @@ __device__ __forceinline__ void add_exact(float& s, float& e, float x) {
   s = t;
 }
 
-// The score of block `at` for the 8 query heads at q, by one warp: as hi + lo, rounded into hi first; false if it is no
-// number. Lane (h = lane >> 2, c = lane & 3) sums 32 of the 128 dims of head h.
-__device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int lane, float& hi, float& lo) {
-  const uint4* qr = reinterpret_cast<const uint4*>(q + (lane >> 2) * kHeadDim) + 4 * (lane & 3);
-  const uint4* up = reinterpret_cast<const uint4*>(bounds) + 4 * (lane & 3);
-  const uint4* down = up + kRowValues / 8;
-  uint4 x4[4], a4[4], b4[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x4[i] = __ldcg(qr + i);
-    a4[i] = __ldcg(up + i);
-    b4[i] = __ldcg(down + i);
-  }
+// Lane (h = lane >> 2, c = lane & 3): the score of head h from its four lanes' 32 dims each, as t + rest, rounded into t
+// first; t is NaN if a term is. With u = 2^-24 and S the sum of the terms' sizes a lane's four sums leave 36 u^2 S (eight
+// terms' errors are added up in fp32), their join 66, the two joins of lanes 52 and the last rounding 2: 2^-40 S in all.
+// SCALED: products of both factors times 2^-70, whose sums of 128 stay in range (2^256 becomes 2^116; what underflows is
+// below 2^-70 of terms whose sum passed the range unscaled). Only the score itself then decides whether it is past fp32's.
+template <bool SCALED>
+__device__ __forceinline__ void exact_sum(const uint4 (&x4)[4], const uint4 (&a4)[4], const uint4 (&b4)[4], float& t, float& rest) {
+  constexpr float kDown = SCALED ? 0x1p-70f : 1.f;
   float sum[4], rest_of[4], other = 0.f;  // four sums at once: each term waits for the one before
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -278,8 +274,8 @@ __device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_b
     for (int k = 0; k < 4; ++k) {
       const float x0 = bf16_lo(xs[k]), x1 = bf16_hi(xs[k]);
       const bool up0 = x0 > 0.f, up1 = x1 > 0.f;
-      add_exact(sum[i], rest_of[i], __fmul_rn(x0, up0 ? bf16_lo(as[k]) : bf16_lo(bs[k])));
-      add_exact(sum[i], rest_of[i], __fmul_rn(x1, up1 ? bf16_hi(as[k]) : bf16_hi(bs[k])));
+      add_exact(sum[i], rest_of[i], __fmul_rn(kDown * x0, kDown * (up0 ? bf16_lo(as[k]) : bf16_lo(bs[k]))));
+      add_exact(sum[i], rest_of[i], __fmul_rn(kDown * x1, kDown * (up1 ? bf16_hi(as[k]) : bf16_hi(bs[k]))));
       other = fmaf(up0 ? bf16_lo(bs[k]) : bf16_lo(as[k]), 0.f, other);  // the products of 0: nothing, or NaN
       other = fmaf(up1 ? bf16_hi(bs[k]) : bf16_hi(as[k]), 0.f, other);
     }
@@ -296,19 +292,46 @@ __device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_b
     add_exact(s, e, s2);
     e = __fadd_rn(e, e2);
   }
-  float t = __fadd_rn(s, e), z = __fsub_rn(t, s);
-  float rest = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(e, z));
-  bool number = isfinite(t);  // a sum that overflows counts as none
-  if (!number) rest = 0.f;
+  t = __fadd_rn(s, e);
+  rest = __fadd_rn(__fsub_rn(s, __fsub_rn(t, __fsub_rn(t, s))), __fsub_rn(e, __fsub_rn(t, s)));
+  if (!isfinite(s)) t = s;  // (s is the plain sum, infinite or NaN as the terms make it; its error is no number)
+  if constexpr (SCALED) {
+    t = t * 0x1p70f * 0x1p70f;
+    rest = rest * 0x1p70f * 0x1p70f;
+  }
+  if (!isfinite(t)) rest = 0.f;
+}
+
+// A block's score for the 8 query heads at q, the largest of theirs, by one warp, as hi + lo; false if it is no finite
+// fp32 number, or a head's is none at all.
+__device__ __forceinline__ bool exact_score(const __nv_bfloat16* q, const __nv_bfloat16* bounds, int lane, float& hi, float& lo) {
+  const uint4* qr = reinterpret_cast<const uint4*>(q + (lane >> 2) * kHeadDim) + 4 * (lane & 3);
+  const uint4* up = reinterpret_cast<const uint4*>(bounds) + 4 * (lane & 3);
+  const uint4* down = up + kRowValues / 8;
+  uint4 x4[4], a4[4], b4[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x4[i] = __ldcg(qr + i);
+    a4[i] = __ldcg(up + i);
+    b4[i] = __ldcg(down + i);
+  }
+  float t, rest;
+  exact_sum<false>(x4, a4, b4, t, rest);
+  if (!__all_sync(0xffffffffu, isfinite(t))) {  // a sum passed the range, at its end or on the way
+    float t2, rest2;
+    exact_sum<true>(x4, a4, b4, t2, rest2);
+    if (!isfinite(t)) t = t2, rest = rest2;  // (the other heads' terms may be too small for the scaled form)
+  }
+  bool nan = t != t;
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) {  // the largest of the heads
     const float t2 = __shfl_xor_sync(0xffffffffu, t, o), r2 = __shfl_xor_sync(0xffffffffu, rest, o);
-    number = __shfl_xor_sync(0xffffffffu, number ? 1 : 0, o) != 0 && number;
+    nan = __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, o) != 0 || nan;
     if (t2 > t || (t2 == t && r2 > rest)) t = t2, rest = r2;
   }
   hi = t;
   lo = rest;
-  return number;
+  return !nan && isfinite(t);
 }
 
 template <int THREADS>
