@@ -518,7 +518,8 @@ int decode_setup(bool fp8, DecodeSetup* setup) {
   Tuning tune = g_tune;  // its CTA counts and tiers, with the one variant that the forms have
   tune.kernel = fp8 ? KernelChoice{kGatherLsuF8, 4, 16, 2} : KernelChoice{kGatherLsu, 4, 16, 2};
   setup->plan = plan_config(*st, tune);
-  setup->default_plan = tune.tier2_ctas == 0 && tune.min_units == 0;
+  setup->default_plan = tune.num_ctas == 0 && tune.min_units == 0 && tune.tier2_ctas == 0 &&
+                        tune.tier2_permille == kDefaultTier2Permille && tune.tier2_min_units == kDefaultTier2MinUnits;
   setup->sm_count = st->sm_count;
   setup->epoch = (g_epoch.fetch_add(1) % ((1ull << 40) - 1)) + 1;
   setup->wait_limit_ns = g_wait_limit_ns > 0 ? g_wait_limit_ns : kDefaultWaitLimitNs;

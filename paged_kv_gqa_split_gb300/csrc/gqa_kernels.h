@@ -104,7 +104,7 @@ int decode_in_scratch(const void* q, const void* k_cache, const void* v_cache, c
 // present tuning, and the call's epoch. Returns a GQA_* code.
 struct DecodeSetup {
   PlanConfig plan;
-  bool default_plan;  // no tuning of tiers or smallest shares
+  bool default_plan;  // no tuning of CTA counts, tiers or smallest shares: the forms' own rules apply
   int sm_count;
   unsigned long long epoch;
   unsigned long long wait_limit_ns;
