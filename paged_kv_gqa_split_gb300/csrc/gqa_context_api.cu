@@ -447,7 +447,7 @@ int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* 
   const int rc = gqa::current_device_sms(&sms);
   if (rc != GQA_OK) return rc;
   const gqa::EvictParams p{weights, kv_indptr, kv_indices, weights_out, new_indptr, new_indices, freed_indptr, freed,
-                           budget, keep_first, keep_last, batch, width, index_count, 1, 0};
+                           budget, keep_first, keep_last, batch, width, index_count, 1, 0, 0};
   return launched(gqa::launch_evict(p, sms, stream));
 }
 

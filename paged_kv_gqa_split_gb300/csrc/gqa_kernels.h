@@ -409,6 +409,7 @@ struct EvictParams {  // gqa_weights.cu
   int* freed;
   int budget, keep_first, keep_last, batch, width, index_count;
   int cluster, held;  // blocks a sequence, words that one holds in shared memory (set by the launch)
+  int sums;           // a kernel ahead forms new_indptr and freed_indptr (set by the launch)
 };
 cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream);
 
