@@ -368,9 +368,15 @@ int gqa_paged_decode_device_error(int* flags);
  * copies and MMAs in flight have ended (that drain keeps the 2 s limit), a
  * merging warp skips that merge. A call made with a tiny limit therefore completes, with outputs that
  * are not valid.
+ *
+ * gqa_paged_decode_test_cluster_limit(blocks): gqa_kv_evict takes clusters of at
+ * most so many thread blocks (a power of two up to 16), as on a device that
+ * holds no larger ones. 0 turns it off. Returns GQA_ERR_INVALID_ARGUMENT for
+ * another value.
  */
 int gqa_paged_decode_test_fail_allocs(int count);
 int gqa_paged_decode_test_wait_limit_ns(uint64_t ns);
+int gqa_paged_decode_test_cluster_limit(int blocks);
 
 /*
  * The pages this library follows have no counterpart to this entry point: it

@@ -56,6 +56,7 @@ _SIGNATURES = {
     "gqa_paged_decode_last_launch_count": (ctypes.c_int, []),
     "gqa_paged_decode_test_fail_allocs": (ctypes.c_int, [ctypes.c_int]),
     "gqa_paged_decode_test_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
+    "gqa_paged_decode_test_cluster_limit": (ctypes.c_int, [ctypes.c_int]),
     "gqa_rope_inv_freq": (ctypes.c_int, [ctypes.c_int, _d, ctypes.c_int, _d, _d, _d, _d, _vp,
                                          ctypes.POINTER(ctypes.c_float)]),
     "gqa_rope": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_float, _vp] + [ctypes.c_int] * 8 + [ctypes.c_int64] * 4 + [_vp]),
@@ -202,6 +203,10 @@ def gqa_paged_decode_test_fail_allocs(count: int) -> int:
 
 def gqa_paged_decode_test_wait_limit_ns(ns: int) -> int:
     return load().gqa_paged_decode_test_wait_limit_ns(ns)
+
+
+def gqa_paged_decode_test_cluster_limit(blocks: int) -> int:
+    return load().gqa_paged_decode_test_cluster_limit(blocks)
 
 
 def gqa_paged_kv_append(k_new, v_new, slots, k_cache, v_cache, num_tokens, num_pages, stream) -> int:

@@ -451,4 +451,10 @@ int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* 
   return launched(gqa::launch_evict(p, sms, stream));
 }
 
+int gqa_paged_decode_test_cluster_limit(int blocks) {
+  if (blocks < 0 || blocks > 16 || (blocks & (blocks - 1)) != 0) return GQA_ERR_INVALID_ARGUMENT;
+  gqa::set_evict_cluster_limit(blocks);
+  return GQA_OK;
+}
+
 }  // extern "C"

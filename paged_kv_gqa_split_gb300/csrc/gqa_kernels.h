@@ -412,6 +412,7 @@ struct EvictParams {  // gqa_weights.cu
   int sums;           // a kernel ahead forms new_indptr and freed_indptr (set by the launch)
 };
 cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream);
+void set_evict_cluster_limit(int blocks);  // test hook; 0: none
 
 // Launches a kernel that begins with pdl_wait() so that it may start while the one before it on the stream ends, over
 // clusters of `cluster` blocks.

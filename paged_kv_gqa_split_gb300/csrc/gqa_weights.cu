@@ -225,15 +225,56 @@ __global__ void __launch_bounds__(THREADS) gqa_evict_kernel(const EvictParams p)
   }
 }
 
+constexpr int kClusterThreads = 1024;
+static std::atomic<int> g_cluster_limit{0};
+void set_evict_cluster_limit(int blocks) { g_cluster_limit.store(blocks); }
+
+// The largest cluster of the eviction that the current device can hold: those of 16 blocks need a part of the GPU with that
+// many SMs, which not every one has. Asked for once a device.
+static cudaError_t evict_cluster_limit(int* most) {
+  static std::atomic<int> known[kMaxDevices], configured[kMaxDevices], allowed[kMaxDevices];
+  const void* fn = reinterpret_cast<const void*>(gqa_evict_kernel<true, kClusterThreads>);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = set_smem_limit_once(configured, fn, kEvictHeld * 4);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < kMaxDevices;
+  *most = tracked ? known[dev].load(std::memory_order_acquire) : 0;
+  if (*most == 0) {
+    *most = 1;
+    for (int blocks = kMostBlocks; blocks > 1 && *most == 1; blocks /= 2) {
+      int fit = 0;
+      if (blocks > 8 && set_attribute_once(allowed, fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();
+        continue;
+      }
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(blocks);
+      cfg.blockDim = dim3(kClusterThreads);
+      cfg.dynamicSmemBytes = kEvictHeld * 4;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = blocks;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) != cudaSuccess) cudaGetLastError();
+      else if (fit > 0) *most = blocks;
+    }
+    if (tracked) known[dev].store(*most, std::memory_order_release);
+  }
+  const int limit = g_cluster_limit.load();
+  if (limit > 0 && limit < *most) *most = limit;
+  return cudaSuccess;
+}
+
 template <bool CLUSTERED, int THREADS>
 static cudaError_t launch_evict_form(const EvictParams& p, cudaStream_t stream) {
-  static std::atomic<int> configured[kMaxDevices];
-  const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), kEvictHeld * 4);
-  if (e != cudaSuccess) return e;
-  if (p.cluster > 8) {
-    static std::atomic<int> allowed[kMaxDevices];
-    const cudaError_t a = set_attribute_once(allowed, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (a != cudaSuccess) return a;
+  if (!CLUSTERED) {
+    static std::atomic<int> configured[kMaxDevices];
+    const cudaError_t e = set_smem_limit_once(configured, reinterpret_cast<const void*>(gqa_evict_kernel<CLUSTERED, THREADS>), kEvictHeld * 4);
+    if (e != cudaSuccess) return e;
   }
   const int64_t units = p.batch < (1 << 16) ? p.batch : (1 << 16);
   return launch_chained(gqa_evict_kernel<CLUSTERED, THREADS>, dim3(static_cast<unsigned>(units * p.cluster)), THREADS, p.held * 4, stream, p.cluster, p);
@@ -254,7 +295,12 @@ static double evict_us(int batch, int width, int blocks, int sms) {
 cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream) {
   const int width = p.width > 0 ? p.width : 1;
   p.cluster = 1;
-  for (int blocks = 2; blocks <= kMostBlocks && width >= blocks * kEvictRun; blocks *= 2)
+  int most = 1;
+  if (width >= 2 * kEvictRun) {
+    const cudaError_t e = evict_cluster_limit(&most);
+    if (e != cudaSuccess) return e;
+  }
+  for (int blocks = 2; blocks <= most && width >= blocks * kEvictRun; blocks *= 2)
     if (evict_us(p.batch, width, blocks, sm_count) < evict_us(p.batch, width, p.cluster, sm_count)) p.cluster = blocks;
   const int run = (width - 1) / p.cluster + 1;
   p.held = run < kEvictHeld ? run : kEvictHeld;
@@ -263,7 +309,7 @@ cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream) {
     const cudaError_t e = launch_chained(gqa_evict_sums_kernel, dim3(1), kSumThreads, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
   }
-  return p.cluster > 1 ? launch_evict_form<true, 1024>(p, stream) : launch_evict_form<false, 512>(p, stream);
+  return p.cluster > 1 ? launch_evict_form<true, kClusterThreads>(p, stream) : launch_evict_form<false, 512>(p, stream);
 }
 
 }  // namespace gqa
