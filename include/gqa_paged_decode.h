@@ -361,10 +361,11 @@ int gqa_paged_decode_device_error(int* flags);
  * gqa_paged_decode_test_wait_limit_ns(ns): the give-up limit, in
  * nanoseconds, of the bounded waits of the decode kernels: the mbarrier waits
  * of the TMA-gather variant (gather = 1 in gqa_paged_decode_set_tuning), those
- * of the latent projections above 16 tokens and, in the one-wave mode, a
- * warp's wait for the pieces of a sequence it merges.
+ * of the latent projections above 16 tokens and of gqa_shared_paged_decode's
+ * prefixes and, in the one-wave mode, a warp's wait for the pieces of a sequence
+ * it merges.
  * 0 restores the default of 2 s. A wait that runs out sets bit 1, 2 or 32 of
- * the device error word; a TMA-variant or projection CTA returns after its
+ * the device error word; a TMA-variant, projection or prefix CTA returns after its
  * copies and MMAs in flight have ended (that drain keeps the 2 s limit), a
  * merging warp skips that merge. A call made with a tiny limit therefore completes, with outputs that
  * are not valid.
@@ -640,8 +641,9 @@ int gqa_shared_paged_decode(const void* q, const void* k_cache, const void* v_ca
  * to page_table_width * page_size. A block that several requests list must
  * hold the same tokens for all that renew it in one call.
  *
- * k_cache [num_blocks][page_size][4][128] bf16, bounds [num_blocks][2][4][128]
- * bf16, both 16-byte aligned; block_table [requests][page_table_width].
+ * k_cache [num_blocks][page_size][4][128] bf16, page_size up to 2^30, bounds
+ * [num_blocks][2][4][128] bf16, both 16-byte aligned; block_table
+ * [requests][page_table_width].
  */
 int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_table, const int32_t* lens,
                      const int32_t* first, int requests, int page_size, int num_blocks, int page_table_width,
@@ -694,6 +696,7 @@ int gqa_block_sparse_decode(const void* q, const void* k_cache, const void* v_ca
  * read weights there. Places past a sequence's length are copied; tokens past
  * width count in the decode alone. weights_out may be weights itself, and must
  * not overlap it otherwise. lse is required. index_count: entries of kv_indices.
+ * batch == 0 returns 0 without launching.
  */
 size_t gqa_paged_decode_weighted_ws_size(int index_count, int cache_format);
 int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_indptr,
@@ -711,7 +714,8 @@ int gqa_paged_decode_weighted(const void* q, const void* k_cache, const void* v_
  * table; freed_indptr, freed: the others' pages in the same form; entries of
  * new_indices and freed behind the last sequence's are -1. weights_out
  * [batch][width]: the kept tokens' weights at their new places, then zeros. No
- * output may overlap an input or another output.
+ * output may overlap an input or another output. batch == 0 returns 0 without
+ * launching, and leaves the outputs as they are.
  */
 int gqa_kv_evict(const float* weights, const int32_t* kv_indptr, const int32_t* kv_indices, int budget, int keep_first,
                  int keep_last, float* weights_out, int32_t* new_indptr, int32_t* new_indices, int32_t* freed_indptr,

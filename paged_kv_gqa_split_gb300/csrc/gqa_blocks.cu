@@ -57,20 +57,19 @@ __global__ void __launch_bounds__(kBoundThreads) gqa_block_bounds_kernel(const B
     if (static_cast<unsigned>(b) >= static_cast<unsigned>(p.num_blocks)) return false;
     block = b;
     const int tokens = min(p.page_size, n - i * p.page_size);
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + t0 * 64 + lane;
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) + block * p.page_size * kRowValues) + lane;
     mm.init();
-    // a block may have more than 2^25 tokens: what is left is counted, and the offset grows in the pointer's 64 bits
-    int left = tokens > t0 ? (tokens - t0 - 1) / step + 1 : 0;
-    for (; left >= 16; left -= 16, k += 16 * step * 64) {
+    int t = t0;  // (up to 2^30 tokens a block: their numbers have 31 bits, the offsets of those from 2^25 on have not)
+    for (; t + 15 * step < tokens; t += 16 * step) {
       uint4 x[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) x[u] = __ldcg(k + u * step * 64);
+      for (int u = 0; u < 16; ++u) x[u] = __ldcg(k + static_cast<int64_t>(t + u * step) * 64);
 #pragma unroll
       for (int u = 0; u < 16; ++u) mm.add(x[u], x[u]);
     }
 #pragma unroll 4
-    for (; left > 0; --left, k += step * 64) {
-      const uint4 x = __ldcg(k);
+    for (; t < tokens; t += step) {
+      const uint4 x = __ldcg(k + static_cast<int64_t>(t) * 64);
       mm.add(x, x);
     }
     return true;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
 // trips: one row of 2048 blocks 15 us, of which the k-th largest takes 3.4 and the exact scores 2; 128 rows of 32 to 256 14.
 constexpr int kHeldWords = 48 * 1024, kListed = 128;
 constexpr uint32_t kAbsent = 0, kChosen = 1;  // marks below any score's word
-constexpr uint32_t kUnknown = 0xffffffffu;    // of a score that is no finite number: it is formed again in any case
+constexpr uint32_t kUnknown = 0xffffffffu;    // of a score whose sums may have left fp32's range: it is formed again in any case
 
 // s + e += x, exactly but for e's own rounding.
 __device__ __forceinline__ void add_exact(float& s, float& e, float x) {

@@ -259,7 +259,7 @@ int gqa_block_bounds(const void* k_cache, void* bounds, const int32_t* block_tab
                      struct CUstream_st* stream) {
   if (requests < 0) return GQA_ERR_INVALID_ARGUMENT;
   if (requests == 0) return GQA_OK;
-  if (!items_ok(requests) || !table_ok(page_size, num_blocks, page_table_width)) return GQA_ERR_INVALID_ARGUMENT;
+  if (!items_ok(requests) || !items_ok(page_size) || !table_ok(page_size, num_blocks, page_table_width)) return GQA_ERR_INVALID_ARGUMENT;
   if (k_cache == nullptr || bounds == nullptr || block_table == nullptr || lens == nullptr) return GQA_ERR_INVALID_ARGUMENT;
   if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(first, 4))
     return GQA_ERR_INVALID_ARGUMENT;
