@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(128) gqa_block_score_kernel(const BlockParams 
 // scores tie: up to kListed are compared with one another, more by a second radix select over both floats. Scores are held
 // in shared memory as ordered words, up to kHeldWords of them (else in their place in global memory).
 // Small blocks of threads for short rows: their barriers are cheap and all fit the GPU at once. Bound by barriers and round
-// trips: one row of 2048 blocks 15 us, of which the k-th largest takes 3.4 and the exact scores 2; 128 rows of 32 to 256 14.
+// trips: one row of 2048 blocks 15 us, of which the k-th largest takes 3.4 and the exact scores 2; 128 rows of 32 to 256 13.
 constexpr int kHeldWords = 48 * 1024, kListed = 128;
 constexpr uint32_t kAbsent = 0, kChosen = 1;  // marks below any score's word
 constexpr uint32_t kUnknown = 0xffffffffu;    // of a score whose sums may have left fp32's range: it is formed again in any case
