@@ -69,15 +69,15 @@ def test_chosen_blocks_of_nearly_2_31_tokens():
 
 @pytest.mark.parametrize("tuning", [(0, 0, 0, 0, 0, 0), (0, 0, 4, 16, 5, 1)])
 def test_decode_of_nearly_2_31_tokens(tuning):
-    """The plain decode by copies and by tensor copies, every token the same page: all probabilities are 2^-31, the sums of
+    """The plain decode by copies and by tensor copies, every token's page alike: all probabilities are 2^-31, the sums of
     values that are powers of two are exact, and so is the result; the LSE is the score and 31."""
     room(16)
     n = 2 ** 31 - 1
     g = torch.Generator().manual_seed(2)
-    k = torch.randn(3, 1, 4, 128, generator=g).to(BF).cuda()
-    v = torch.exp2(torch.randint(-3, 4, (3, 1, 4, 128), generator=g).float()).to(BF).cuda()
+    k = torch.randn(1, 1, 4, 128, generator=g).to(BF).cuda().expand(8192, 1, 4, 128).contiguous()
+    v = torch.exp2(torch.randint(-3, 4, (1, 1, 4, 128), generator=g).float()).to(BF).cuda().expand_as(k).contiguous()
     q = torch.randn(1, 32, 128, generator=g).to(BF).cuda()
-    pages = torch.ones(n, dtype=I32, device="cuda")
+    pages = torch.arange(n, dtype=I32, device="cuda").bitwise_and_(8191)
     try:
         assert _lib.gqa_paged_decode_set_tuning(*tuning) == 0
         out, lse = pkg.run(q, k, v, i32([0, n]), pages, 128 ** -0.5)
